@@ -8,11 +8,20 @@ The operator lives in the C-ABI library ``libdiffattn.so`` (``include/diffattn.h
 from .binding import (  # noqa: F401
     DiffAttnError,
     diffattn_get_device_status,
+    diffattn_kv4_append,
+    diffattn_kv4_read,
+    diffattn_kv4_record_bytes,
+    diffattn_kv_evict,
+    diffattn_kv_evict_workspace_size,
     diffattn_lambda_init,
     diffattn_v1_bwd,
     diffattn_v1_fwd,
     diffattn_v2_decode,
+    diffattn_v2_decode_kv4,
+    diffattn_v2_decode_kv4_workspace_size,
     diffattn_v2_decode_num_splits,
+    diffattn_v2_decode_weighted,
+    diffattn_v2_decode_weighted_workspace_size,
     diffattn_v2_decode_workspace_size,
     diffattn_v2_fwd,
     diffattn_v2_gate,

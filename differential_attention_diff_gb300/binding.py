@@ -48,6 +48,15 @@ EXPORTS = (
     "diffattn_v2_decode_noalloc",
     "diffattn_v2_decode_num_splits",
     "diffattn_v2_decode_workspace_size",
+    "diffattn_kv4_record_bytes",
+    "diffattn_kv4_append",
+    "diffattn_kv4_read",
+    "diffattn_v2_decode_kv4",
+    "diffattn_v2_decode_kv4_workspace_size",
+    "diffattn_v2_decode_weighted",
+    "diffattn_v2_decode_weighted_workspace_size",
+    "diffattn_kv_evict",
+    "diffattn_kv_evict_workspace_size",
     "diffattn_get_device_status",
     "diffattn_debug_inject_fault",
     "diffattn_get_device_status_detail",
@@ -152,6 +161,44 @@ class da_v2_decode_params(C.Structure):
                 ("workspace_bytes", C.c_size_t)]
 
 
+class da_kv4_append_params(C.Structure):
+    _fields_ = [("B", C.c_int), ("N", C.c_int), ("h_kv", C.c_int), ("d", C.c_int), ("L_max", C.c_int),
+                ("k", da_t4), ("v", da_t4), ("cache", da_t4), ("start", C.c_void_p), ("counts", C.c_void_p),
+                ("key_weights", C.c_void_p), ("positions", C.c_void_p), ("first_position", C.c_void_p)]
+
+
+class da_kv4_read_params(C.Structure):
+    _fields_ = [("B", C.c_int), ("N", C.c_int), ("h_kv", C.c_int), ("d", C.c_int), ("L_max", C.c_int),
+                ("cache", da_t4), ("start", C.c_void_p), ("counts", C.c_void_p), ("k_out", da_t4),
+                ("v_out", da_t4)]
+
+
+class da_v2_decode_kv4_params(C.Structure):
+    _fields_ = [("B", C.c_int), ("h", C.c_int), ("h_kv", C.c_int), ("d", C.c_int),
+                ("L_max", C.c_int), ("d_model", C.c_int), ("softmax_scale", C.c_float),
+                ("q", C.c_void_p), ("cache", da_t4), ("seqlens", C.c_void_p),
+                ("gate", C.c_void_p), ("x", C.c_void_p), ("w_lambda", C.c_void_p),
+                ("weights_in", C.c_void_p), ("weights_out", C.c_void_p), ("out", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+class da_v2_decode_weighted_params(C.Structure):
+    _fields_ = [("decode", da_v2_decode_params), ("weights_in", C.c_void_p), ("weights_out", C.c_void_p)]
+
+
+DIFFATTN_EVICT_MAX_ROWS = 3
+
+
+class da_kv_evict_params(C.Structure):
+    _fields_ = [("B", C.c_int), ("h_kv", C.c_int), ("L_max", C.c_int), ("keep", C.c_int),
+                ("sinks", C.c_int), ("recent", C.c_int), ("seqlens", C.c_void_p),
+                ("seqlens_out", C.c_void_p), ("weights_in", C.c_void_p), ("weights_out", C.c_void_p),
+                ("positions_in", C.c_void_p), ("positions_out", C.c_void_p), ("next_position", C.c_void_p),
+                ("n_rows", C.c_int), ("row_bytes", C.c_int * DIFFATTN_EVICT_MAX_ROWS),
+                ("rows", da_t4 * DIFFATTN_EVICT_MAX_ROWS), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -178,7 +225,12 @@ def load(path: str = LIB_PATH):
                          ("diffattn_grouped_fwd", da_grouped_fwd_params),
                          ("diffattn_grouped_bwd", da_grouped_bwd_params),
                          ("diffattn_v2_decode", da_v2_decode_params),
-                         ("diffattn_v2_decode_noalloc", da_v2_decode_params)):
+                         ("diffattn_v2_decode_noalloc", da_v2_decode_params),
+                         ("diffattn_kv4_append", da_kv4_append_params),
+                         ("diffattn_kv4_read", da_kv4_read_params),
+                         ("diffattn_v2_decode_kv4", da_v2_decode_kv4_params),
+                         ("diffattn_v2_decode_weighted", da_v2_decode_weighted_params),
+                         ("diffattn_kv_evict", da_kv_evict_params)):
             f = getattr(lib, name)
             f.restype = C.c_int
             f.argtypes = [C.POINTER(st), vp]
@@ -202,6 +254,14 @@ def load(path: str = LIB_PATH):
         lib.diffattn_v2_decode_num_splits.argtypes = [C.c_int] * 3
         lib.diffattn_v2_decode_workspace_size.restype = C.c_size_t
         lib.diffattn_v2_decode_workspace_size.argtypes = [C.c_int] * 7
+        lib.diffattn_kv4_record_bytes.restype = C.c_int
+        lib.diffattn_kv4_record_bytes.argtypes = [C.c_int]
+        for name, n in (("diffattn_v2_decode_kv4_workspace_size", 7),
+                        ("diffattn_v2_decode_weighted_workspace_size", 7),
+                        ("diffattn_kv_evict_workspace_size", 4)):
+            f = getattr(lib, name)
+            f.restype = C.c_size_t
+            f.argtypes = [C.c_int] * n
         lib.diffattn_debug_inject_fault.restype = C.c_int
         lib.diffattn_debug_inject_fault.argtypes = [C.c_int]
         lib.diffattn_get_device_status.restype = C.c_int
@@ -541,6 +601,178 @@ def diffattn_v2_decode_noalloc(q, k_cache, v_cache, *, seqlens=None, gate=None, 
         int(num_splits), None, 0)
     _check(lib.diffattn_v2_decode_noalloc(C.byref(p), _stream(stream)), "diffattn_v2_decode_noalloc")
     return out
+
+
+# ---- 4-bit KV cache, gathered key weights, eviction -------------------------
+
+def _array(t, shape, dtype, name, optional=True):
+    """The data pointer of a contiguous device array of the given shape and type."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: contiguous CUDA {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows4(t, shape, dtype, name):
+    """da_t4 of a device tensor of the given shape and type (strides in its elements)."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda:
+        raise ValueError(f"{name}: CUDA {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+    return _t4(t)
+
+
+def _bytes(t):
+    return t.numel() * t.element_size()
+
+
+def diffattn_kv4_record_bytes(d) -> int:
+    """Bytes of one 4-bit record (a key and a value row): d + 16, 0 if d is unsupported."""
+    return int(load().diffattn_kv4_record_bytes(int(d)))
+
+
+def diffattn_kv4_append(k, v, cache, *, start=None, counts=None, key_weights=None, positions=None,
+                        first_position=None, stream=None):
+    """Quantise k, v [B, N, h_kv, d] (bf16) into the 4-bit cache, uint8 [B,
+    L_max, h_kv, d + 16] in any stride order: row i < counts[b] goes to
+    position start[b] + i.  key_weights / positions [B, h_kv, L_max] are reset
+    for the written positions."""
+    B, N, hkv, d = k.shape
+    L_max, bf16, i32 = cache.shape[1], torch.bfloat16, torch.int32
+    p = da_kv4_append_params(
+        B, N, hkv, d, L_max, _rows4(k, (B, N, hkv, d), bf16, "k"), _rows4(v, (B, N, hkv, d), bf16, "v"),
+        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, "cache"), _array(start, (B,), i32, "start"),
+        _array(counts, (B,), i32, "counts"), _array(key_weights, (B, hkv, L_max), torch.float32, "key_weights"),
+        _array(positions, (B, hkv, L_max), i32, "positions"), _array(first_position, (B,), i32, "first_position"))
+    _check(load().diffattn_kv4_append(C.byref(p), _stream(stream)), "diffattn_kv4_append")
+    return cache
+
+
+def diffattn_kv4_read(cache, N, *, start=None, counts=None, k_out=None, v_out=None, stream=None):
+    """Positions start[b] .. start[b] + counts[b] - 1 of the 4-bit cache as
+    bf16 rows: (k, v) [B, N, h_kv, d].  Rows i >= counts[b] are left as they
+    were (zeros where the outputs are allocated here)."""
+    B, L_max, hkv, rec = cache.shape
+    d, bf16 = rec - 16, torch.bfloat16
+    if k_out is None:
+        k_out = torch.zeros((B, N, hkv, d), dtype=bf16, device=cache.device)
+    if v_out is None:
+        v_out = torch.zeros((B, N, hkv, d), dtype=bf16, device=cache.device)
+    p = da_kv4_read_params(
+        B, N, hkv, d, L_max, _rows4(cache, (B, L_max, hkv, rec), torch.uint8, "cache"),
+        _array(start, (B,), torch.int32, "start"), _array(counts, (B,), torch.int32, "counts"),
+        _rows4(k_out, (B, N, hkv, d), bf16, "k_out"), _rows4(v_out, (B, N, hkv, d), bf16, "v_out"))
+    _check(load().diffattn_kv4_read(C.byref(p), _stream(stream)), "diffattn_kv4_read")
+    return k_out, v_out
+
+
+def _decode_operands(q, seqlens, gate, x, w_lambda, out, B, H2, d):
+    """What the two decodes below check and allocate alike: (q, seqlens, gate, x, w_lambda, out, d_model)."""
+    bf16, h = torch.bfloat16, H2 // 2
+    if out is None:
+        out = torch.empty((B, h, d), dtype=bf16, device=q.device)
+    d_model = 0 if x is None else x.shape[-1]
+    return (_array(q, (B, H2, d), bf16, "q"), _array(seqlens, (B,), torch.int32, "seqlens"),
+            _array(gate, (B, h), torch.float32, "gate"), _array(x, (B, d_model), bf16, "x"),
+            _array(w_lambda, (d_model, h), bf16, "w_lambda"), out, d_model)
+
+
+def diffattn_v2_decode_kv4_workspace_size(B, h, h_kv, d, L_max, gate_given=False, weights=False) -> int:
+    return int(load().diffattn_v2_decode_kv4_workspace_size(B, h, h_kv, d, L_max, int(gate_given), int(weights)))
+
+
+def diffattn_v2_decode_kv4(q, cache, *, seqlens=None, gate=None, x=None, w_lambda=None, weights_in=None,
+                           weights_out=None, out=None, softmax_scale=0.0, workspace=None, stream=None):
+    """V2 decode over a 4-bit cache (uint8 [B, L_max, h_kv, d + 16]): out [B,
+    h, d].  weights_out [B, h_kv, L_max]: weights_in (None = 0, may be the same
+    tensor) plus what each key contributes to this step's differential maps."""
+    B, H2, d = q.shape
+    L_max, hkv = cache.shape[1], cache.shape[2]
+    h = H2 // 2
+    q_, lens, gate_, x_, w_, out, d_model = _decode_operands(q, seqlens, gate, x, w_lambda, out, B, H2, d)
+    if workspace is None:
+        need = diffattn_v2_decode_kv4_workspace_size(B, h, hkv, d, L_max, gate is not None, weights_out is not None)
+        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+    p = da_v2_decode_kv4_params(
+        B, h, hkv, d, L_max, d_model, float(softmax_scale), q_,
+        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, "cache"), lens, gate_, x_, w_,
+        _array(weights_in, (B, hkv, L_max), torch.float32, "weights_in"),
+        _array(weights_out, (B, hkv, L_max), torch.float32, "weights_out"),
+        _array(out, (B, h, d), torch.bfloat16, "out"), workspace.data_ptr(), _bytes(workspace))
+    _check(load().diffattn_v2_decode_kv4(C.byref(p), _stream(stream)), "diffattn_v2_decode_kv4")
+    return out
+
+
+def diffattn_v2_decode_weighted_workspace_size(B, h, h_kv, d, L_max, num_splits=0, gate_given=False) -> int:
+    return int(load().diffattn_v2_decode_weighted_workspace_size(B, h, h_kv, d, L_max, num_splits,
+                                                                 int(gate_given)))
+
+
+def diffattn_v2_decode_weighted(q, k_cache, v_cache, *, weights_out, weights_in=None, seqlens=None, gate=None,
+                                x=None, w_lambda=None, out=None, num_splits=0, softmax_scale=0.0,
+                                workspace=None, stream=None):
+    """diffattn_v2_decode that also gathers the keys' weights into weights_out
+    [B, h_kv, L_max] (see diffattn_v2_decode_kv4)."""
+    B, H2, d = q.shape
+    L_max, hkv = k_cache.shape[1], k_cache.shape[2]
+    h = H2 // 2
+    q_, lens, gate_, x_, w_, out, d_model = _decode_operands(q, seqlens, gate, x, w_lambda, out, B, H2, d)
+    if workspace is None:
+        need = diffattn_v2_decode_weighted_workspace_size(B, h, hkv, d, L_max, num_splits, gate is not None)
+        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+    shape = (B, L_max, hkv, d)
+    dec = da_v2_decode_params(
+        B, h, hkv, d, L_max, d_model, float(softmax_scale), q_, _rows4(k_cache, shape, torch.bfloat16, "k_cache"),
+        _rows4(v_cache, shape, torch.bfloat16, "v_cache"), lens, gate_, x_, w_,
+        _array(out, (B, h, d), torch.bfloat16, "out"), int(num_splits), workspace.data_ptr(), _bytes(workspace))
+    p = da_v2_decode_weighted_params(
+        dec, _array(weights_in, (B, hkv, L_max), torch.float32, "weights_in"),
+        _array(weights_out, (B, hkv, L_max), torch.float32, "weights_out", optional=False))
+    _check(load().diffattn_v2_decode_weighted(C.byref(p), _stream(stream)), "diffattn_v2_decode_weighted")
+    return out
+
+
+def diffattn_kv_evict_workspace_size(B, h_kv, L_max, keep) -> int:
+    return int(load().diffattn_kv_evict_workspace_size(B, h_kv, L_max, keep))
+
+
+def diffattn_kv_evict(rows, key_weights, keep, *, sinks=0, recent=0, seqlens=None, positions=None,
+                      next_position=None, weights_out=None, positions_out=None, seqlens_out=None,
+                      workspace=None, stream=None):
+    """Cut the caches in `rows` (up to three tensors [B, L_max, h_kv, width],
+    compacted in place) down to the `keep` slots per sequence and KV head that
+    gathered the most weight; the first `sinks` and the newest `recent` token
+    positions always stay.  Returns dict(key_weights, positions, seqlens) after
+    the cut.  Without the _out arguments the given key_weights, positions and
+    seqlens are updated in place (a seqlens of None gives a new tensor)."""
+    B, hkv, L_max = key_weights.shape
+    i32, f32 = torch.int32, torch.float32
+    if not 1 <= len(rows) <= DIFFATTN_EVICT_MAX_ROWS:
+        raise ValueError(f"1 to {DIFFATTN_EVICT_MAX_ROWS} caches expected, got {len(rows)}")
+    weights_out = key_weights if weights_out is None else weights_out
+    positions_out = positions if positions_out is None else positions_out
+    if seqlens_out is None:
+        seqlens_out = torch.empty((B,), dtype=i32, device=key_weights.device) if seqlens is None else seqlens
+    p = da_kv_evict_params(
+        B, hkv, L_max, int(keep), int(sinks), int(recent), _array(seqlens, (B,), i32, "seqlens"),
+        _array(seqlens_out, (B,), i32, "seqlens_out"), _array(key_weights, (B, hkv, L_max), f32, "key_weights"),
+        _array(weights_out, (B, hkv, L_max), f32, "weights_out"),
+        _array(positions, (B, hkv, L_max), i32, "positions"),
+        _array(positions_out, (B, hkv, L_max), i32, "positions_out"),
+        _array(next_position, (B,), i32, "next_position"), len(rows))
+    for i, r in enumerate(rows):
+        if tuple(r.shape[:3]) != (B, L_max, hkv) or not r.is_cuda:
+            raise ValueError(f"rows[{i}]: CUDA [{B}, {L_max}, {hkv}, width] expected, got {tuple(r.shape)}")
+        t, n = _t4(r), r.element_size()
+        p.rows[i] = da_t4(t.ptr, t.sb * n, t.sn * n, t.sh * n)
+        p.row_bytes[i] = r.shape[3] * n
+    if workspace is None:
+        need = diffattn_kv_evict_workspace_size(B, hkv, L_max, int(keep))
+        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=key_weights.device)
+    p.workspace, p.workspace_bytes = workspace.data_ptr(), _bytes(workspace)
+    _check(load().diffattn_kv_evict(C.byref(p), _stream(stream)), "diffattn_kv_evict")
+    return dict(key_weights=weights_out, positions=positions_out, seqlens=seqlens_out)
 
 
 DA_FAULT_NONE, DA_FAULT_V2_FWD_SKIP_LOAD = 0, 1

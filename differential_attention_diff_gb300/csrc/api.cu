@@ -76,6 +76,13 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+bool da::device_handles(uint32_t** status, int* num_sms) {
+  const DevInfo d = device_info();
+  *status = d.status;
+  *num_sms = d.num_sms;
+  return d.ok;
+}
+
 extern "C" {
 
 float diffattn_lambda_init(int layer) {
@@ -190,14 +197,28 @@ da_status da::check_v2_decode_args(const da_v2_decode_params* p) {
 
 extern "C" {
 
-da_status diffattn_v2_decode(const da_v2_decode_params* p, void* stream) {
-  const da_status chk = da::check_v2_decode_args(p);
-  if (chk != DA_OK) return chk;
+size_t diffattn_v2_decode_weighted_workspace_size(int B, int h, int h_kv, int d, int L_max, int num_splits,
+                                                  int gate_given) {
+  if (B <= 0 || h <= 0 || h_kv <= 0 || d <= 0 || L_max <= 0) return 0;
+  return diffattn_v2_decode_workspace_size(B, h, h_kv, d, L_max, num_splits, gate_given) +
+         align256(static_cast<size_t>(B) * 2 * h * L_max * sizeof(float));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The V2 decode, with the keys' weights gathered where weights_out is given:
+// its workspace then ends with the scores [B, h_kv, L_max, G].
+da_status run_v2_decode(const da_v2_decode_params* p, const float* weights_in, float* weights_out, void* stream) {
   const int splits = p->num_splits > 0 ? p->num_splits
                                        : diffattn_v2_decode_num_splits(p->B, p->h_kv, p->L_max);
   if (splits > da::kMaxDecodeSplits) return DA_ERR_INVALID_ARG;
-  const size_t need = diffattn_v2_decode_workspace_size(p->B, p->h, p->h_kv, p->d, p->L_max,
-                                                        splits, p->gate != nullptr);
+  const size_t plain = diffattn_v2_decode_workspace_size(p->B, p->h, p->h_kv, p->d, p->L_max,
+                                                         splits, p->gate != nullptr);
+  const size_t need = weights_out ? diffattn_v2_decode_weighted_workspace_size(p->B, p->h, p->h_kv, p->d, p->L_max,
+                                                                               splits, p->gate != nullptr)
+                                  : plain;
   if (p->workspace == nullptr || p->workspace_bytes < need || !aligned(p->workspace, 256))
     return DA_ERR_WORKSPACE;
   DevInfo d = device_info();
@@ -209,6 +230,7 @@ da_status diffattn_v2_decode(const da_v2_decode_params* p, void* stream) {
   const size_t pml = static_cast<size_t>(splits) * p->B * 2 * p->h * 2 * sizeof(float);
   float* part_o = reinterpret_cast<float*>(ws);
   float* part_ml = reinterpret_cast<float*>(ws + align256(po));
+  float* scores = weights_out ? reinterpret_cast<float*>(ws + plain) : nullptr;
   const float* gate = p->gate;
   if (gate == nullptr) {
     float* g = reinterpret_cast<float*>(ws + align256(po) + align256(pml));
@@ -220,8 +242,35 @@ da_status diffattn_v2_decode(const da_v2_decode_params* p, void* stream) {
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.f / std::sqrt(static_cast<float>(p->d));
   da::DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, splits, scale * kLog2e,
                    p->q, p->k_cache, p->v_cache, p->seqlens, gate, p->out,
-                   part_o, part_ml, d.status};
-  return cuda_status(da::launch_decode(a, s));
+                   part_o, part_ml, d.status, scores};
+  cudaError_t e = da::launch_decode(a, s);
+  if (e == cudaSuccess && weights_out) {
+    const da::KeyWeightsArgs w{p->B, p->h, p->h_kv, p->L_max, splits, p->seqlens, gate, part_ml, scores,
+                               weights_in, weights_out};
+    e = da::launch_key_weights(w, s);
+  }
+  return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+da_status diffattn_v2_decode(const da_v2_decode_params* p, void* stream) {
+  const da_status chk = da::check_v2_decode_args(p);
+  if (chk != DA_OK) return chk;
+  return run_v2_decode(p, nullptr, nullptr, stream);
+}
+
+da_status diffattn_v2_decode_weighted(const da_v2_decode_weighted_params* p, void* stream) {
+  if (p == nullptr) return DA_ERR_INVALID_ARG;
+  const da_status chk = da::check_v2_decode_args(&p->decode);
+  if (chk != DA_OK) return chk;
+  if (!p->weights_out || !aligned(p->weights_out, 4) || !aligned(p->weights_in, 4) || !aligned(p->decode.seqlens, 4))
+    return DA_ERR_INVALID_ARG;
+  if (p->decode.gate == nullptr && (!aligned(p->decode.x, 16) || !aligned(p->decode.w_lambda, 16)))
+    return DA_ERR_INVALID_ARG;
+  return run_v2_decode(&p->decode, p->weights_in, p->weights_out, stream);
 }
 
 // ----------------------------------------------------------- V1 fwd --------

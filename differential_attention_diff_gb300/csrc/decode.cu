@@ -44,7 +44,9 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return static_cast<uint32_t>(r * Cfg<D>::kRowBytes + ((c ^ (r & 7)) << 4));
 }
 
-template <int D>
+// kScores: also store every key's scaled scores (log2 units, fp32) for the
+// keys' gathered weights (key_weights.cu).
+template <int D, bool kScores>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 decode_split_kernel(DecodeArgs a) {
   constexpr int kD = D;
@@ -159,6 +161,11 @@ decode_split_kernel(DecodeArgs a) {
       for (int e = 0; e < 4; ++e) {
         const int key = key_base + nt * 8 + 2 * tq + (e & 1);
         s[nt][e] = key < k_end ? s[nt][e] * a.scale_log2 : -INFINITY;
+        if constexpr (kScores) {
+          const int row = gr + (e >> 1) * 8;
+          if (key < k_end && row < G)
+            a.scores[((static_cast<int64_t>(b) * a.h_kv + g) * a.L_max + key) * G + row] = s[nt][e];
+        }
       }
     }
     // online softmax per row (rows gr and gr + 8)
@@ -288,22 +295,26 @@ decode_merge_kernel(DecodeArgs a) {
       __float2bfloat16_rn(y);
 }
 
-template <int D>
+template <int D, bool kScores>
 cudaError_t launch_split(const DecodeArgs& a, cudaStream_t s) {
   // set on every launch: the attribute is per device, and the call is cheap
-  cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 g1(a.num_splits, a.h_kv, a.B);
-  decode_split_kernel<D><<<g1, kWarps * 32, kSmemBytes, s>>>(a);
+  decode_split_kernel<D, kScores><<<g1, kWarps * 32, kSmemBytes, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
-  cudaError_t e = a.d == 128 ? launch_split<128>(a, s) : a.d == 64 ? launch_split<64>(a, s)
-                                                                    : cudaErrorInvalidValue;
+  if (a.d != 128 && a.d != 64) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if (a.scores)
+    e = a.d == 128 ? launch_split<128, true>(a, s) : launch_split<64, true>(a, s);
+  else
+    e = a.d == 128 ? launch_split<128, false>(a, s) : launch_split<64, false>(a, s);
   if (e != cudaSuccess) return e;
   dim3 g2(a.h, a.B);
   decode_merge_kernel<<<g2, a.d, 0, s>>>(a);

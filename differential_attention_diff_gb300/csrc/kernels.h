@@ -44,6 +44,7 @@ struct DecodeArgs {
   float* part_o;      // [splits, B, 2h, d]
   float* part_ml;     // [splits, B, 2h, 2]  (running max in log2 units, sum)
   uint32_t* status;
+  float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 // The split count is a grid dimension (at most 65535).
@@ -51,6 +52,67 @@ constexpr int kMaxDecodeSplits = 65535;
 // Every argument check of diffattn_v2_decode except the split count chosen
 // by the library and the workspace; DA_OK or the status the call returns.
 da_status check_v2_decode_args(const da_v2_decode_params* p);
+
+// ---- device handles shared by the entry points ------------------------------
+// The current device's status word and SM count; false if they cannot be had.
+bool device_handles(uint32_t** status, int* num_sms);
+
+// ---- 4-bit KV cache: append and read back -----------------------------------
+struct Kv4RowsArgs {
+  int B, N, h_kv, d, L_max;
+  da_t4 k, v;      // bf16 [B, N, h_kv, d]: read by append, written by read
+  da_t4 cache;     // records [B, L_max, h_kv], byte strides
+  const int* start;
+  const int* counts;
+  float* key_weights;
+  int* positions;
+  const int* first_position;
+  uint32_t* status;
+};
+cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s);
+
+// ---- V2 decode over a 4-bit KV cache ----------------------------------------
+struct Kv4DecodeArgs {
+  int B, h, h_kv, d, L_max, num_splits;
+  float scale_log2;
+  const void* q;
+  da_t4 cache;        // records [B, L_max, h_kv], byte strides
+  const int* seqlens;
+  const float* gate;  // [B, h]
+  void* out;          // bf16 [B, h, d]
+  float* part_o;      // [splits, B, 2h, d]
+  float* part_ml;     // [splits, B, 2h, 2]
+  float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
+  const float* weights_in;
+  float* weights_out;
+  uint32_t* status;
+};
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
+
+// ---- gathered key weights from the scores of a decode -------------------------
+struct KeyWeightsArgs {
+  int B, h, h_kv, L_max, num_splits;
+  const int* seqlens;
+  const float* gate;
+  const float* part_ml;  // [splits, B, 2h, 2]
+  const float* scores;   // [B, h_kv, L_max, G]
+  const float* weights_in;
+  float* weights_out;
+};
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t s);
+
+// ---- eviction from a cache -----------------------------------------------------
+struct EvictArgs {
+  da_kv_evict_params p;
+  int* n_moves;  // [B * h_kv]
+  int* new_len;  // [B]
+  int* dst;      // [B * h_kv, max_moves]
+  int* src;      // [B * h_kv, max_moves]
+  int max_moves;
+  uint32_t* status;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
 
 // ---- V1 decode: split-KV partials of both streams, then merge + RMSNorm ----
 struct V1DecodeArgs {

@@ -1,0 +1,204 @@
+// kv_api.cu — the extern "C" entry points of the 4-bit KV cache (append, read
+// back, V2 decode) and of eviction: argument checks, workspace carving and the
+// launches.  As in api.cu, nothing here allocates, frees or synchronises.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "diffattn.h"
+#include "kernels.h"
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+da_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ERR_CUDA; }
+
+// Pointer and strides of a 16-byte-granular array: `unit` elements per 16 bytes.
+bool ok_t4(const da_t4& t, int unit) {
+  return t.ptr != nullptr && aligned(t.ptr, 16) && t.sb >= 0 && t.sn >= 0 && t.sh >= 0 && t.sb % unit == 0 &&
+         t.sn % unit == 0 && t.sh % unit == 0;
+}
+
+// The checks that append and read share; DA_OK with *empty set for no rows.
+da_status check_rows(int B, int N, int h_kv, int d, int L_max, const da_t4& k, const da_t4& v, const da_t4& cache,
+                     const int* start, const int* counts, bool* empty) {
+  *empty = false;
+  if (B < 0 || N < 0 || h_kv <= 0 || d <= 0 || L_max <= 0) return DA_ERR_INVALID_ARG;
+  if (diffattn_kv4_record_bytes(d) == 0) return DA_ERR_UNSUPPORTED;
+  if (!aligned(start, 4) || !aligned(counts, 4)) return DA_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) {
+    *empty = true;
+    return DA_OK;
+  }
+  if (!ok_t4(k, 8) || !ok_t4(v, 8) || !ok_t4(cache, 16)) return DA_ERR_INVALID_ARG;
+  // one launch covers at most 2^31 - 1 blocks of 16 key/value rows
+  if (static_cast<double>(B) * N * h_kv >= 8.0 * 2147483647.0) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+// Key-range splits per (sequence, KV head).
+int decode_splits(int B, int h_kv, int L_max) {
+  uint32_t* status;
+  int sms = 152;
+  if (!da::device_handles(&status, &sms)) sms = 152;
+  const long units = static_cast<long>(B) * h_kv;
+  long s = (12L * sms + units - 1) / units;
+  const long most = (L_max + 511) / 512;
+  if (s > most) s = most;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+struct DecodeSpace {
+  size_t ml, scores, gate, total;  // offsets; the partial O rows are at 0
+};
+DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
+  const size_t rows = static_cast<size_t>(decode_splits(B, h_kv, L_max)) * B * 2 * h;
+  DecodeSpace w;
+  w.ml = align256(rows * d * sizeof(float));
+  w.scores = w.ml + align256(rows * 2 * sizeof(float));
+  w.gate = w.scores + (weights ? align256(static_cast<size_t>(B) * 2 * h * L_max * sizeof(float)) : 0);
+  w.total = w.gate + (gate_given ? 0 : align256(static_cast<size_t>(B) * h * sizeof(float)));
+  return w;
+}
+
+struct EvictSpace {
+  size_t len, dst, src, total;  // offsets; the move counts are at 0
+  int max_moves;
+};
+EvictSpace evict_space(int B, int h_kv, int L_max, int keep) {
+  const size_t units = static_cast<size_t>(B) * h_kv;
+  EvictSpace w;
+  // a head moves one row per slot below m that goes: at most min(m, L - m)
+  w.max_moves = keep >= L_max ? 0 : (keep < L_max - keep ? keep : L_max - keep);
+  w.len = align256(units * sizeof(int));
+  w.dst = w.len + align256(static_cast<size_t>(B) * sizeof(int));
+  w.src = w.dst + align256(units * w.max_moves * sizeof(int));
+  w.total = w.src + align256(units * w.max_moves * sizeof(int));
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int diffattn_kv4_record_bytes(int d) { return d == 64 || d == 128 ? d + 16 : 0; }
+
+da_status diffattn_kv4_append(const da_kv4_append_params* p, void* stream) {
+  if (p == nullptr) return DA_ERR_INVALID_ARG;
+  bool empty;
+  const da_status chk =
+      check_rows(p->B, p->N, p->h_kv, p->d, p->L_max, p->k, p->v, p->cache, p->start, p->counts, &empty);
+  if (chk != DA_OK) return chk;
+  if (!aligned(p->key_weights, 4) || !aligned(p->positions, 4) || !aligned(p->first_position, 4))
+    return DA_ERR_INVALID_ARG;
+  if (empty) return DA_OK;
+  uint32_t* status;
+  int sms;
+  if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
+  const da::Kv4RowsArgs a{p->B, p->N, p->h_kv, p->d, p->L_max, p->k, p->v, p->cache, p->start, p->counts,
+                          p->key_weights, p->positions, p->first_position, status};
+  return cuda_status(da::launch_kv4_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+da_status diffattn_kv4_read(const da_kv4_read_params* p, void* stream) {
+  if (p == nullptr) return DA_ERR_INVALID_ARG;
+  bool empty;
+  const da_status chk =
+      check_rows(p->B, p->N, p->h_kv, p->d, p->L_max, p->k_out, p->v_out, p->cache, p->start, p->counts, &empty);
+  if (chk != DA_OK || empty) return chk;
+  uint32_t* status;
+  int sms;
+  if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
+  const da::Kv4RowsArgs a{p->B, p->N, p->h_kv, p->d, p->L_max, p->k_out, p->v_out, p->cache, p->start, p->counts,
+                          nullptr, nullptr, nullptr, status};
+  return cuda_status(da::launch_kv4_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t diffattn_v2_decode_kv4_workspace_size(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
+  if (B <= 0 || h <= 0 || h_kv <= 0 || d <= 0 || L_max <= 0) return 0;
+  return decode_space(B, h, h_kv, d, L_max, gate_given, weights).total;
+}
+
+da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream) {
+  if (p == nullptr) return DA_ERR_INVALID_ARG;
+  // the checks of diffattn_v2_decode on what both take; the cache's own below
+  da_v2_decode_params q{};
+  q.B = p->B;
+  q.h = p->h;
+  q.h_kv = p->h_kv;
+  q.d = p->d;
+  q.L_max = p->L_max;
+  q.d_model = p->d_model;
+  q.q = p->q;
+  q.k_cache = q.v_cache = p->cache;
+  q.gate = p->gate;
+  q.x = p->x;
+  q.w_lambda = p->w_lambda;
+  q.out = p->out;
+  const da_status chk = da::check_v2_decode_args(&q);
+  if (chk != DA_OK) return chk;
+  if (!ok_t4(p->cache, 16) || !aligned(p->seqlens, 4)) return DA_ERR_INVALID_ARG;
+  if (!aligned(p->weights_in, 4) || !aligned(p->weights_out, 4) || (p->weights_in && !p->weights_out))
+    return DA_ERR_INVALID_ARG;
+  if (p->gate == nullptr && (!aligned(p->x, 16) || !aligned(p->w_lambda, 16))) return DA_ERR_INVALID_ARG;
+  if (p->B > 65535 || p->h_kv > 65535) return DA_ERR_UNSUPPORTED;
+  const DecodeSpace w = decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr);
+  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
+  uint32_t* status;
+  int sms;
+  if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+  const float* gate = p->gate;
+  if (gate == nullptr) {
+    float* g = reinterpret_cast<float*>(ws + w.gate);
+    const da::GateArgs ga{p->B, p->d_model, p->h, p->x, p->d_model, p->w_lambda, g, status};
+    if (da::launch_gate(ga, s) != cudaSuccess) return DA_ERR_CUDA;
+    gate = g;
+  }
+  const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.f / std::sqrt(static_cast<float>(p->d));
+  const da::Kv4DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, decode_splits(p->B, p->h_kv, p->L_max),
+                            scale * kLog2e, p->q, p->cache, p->seqlens, gate, p->out,
+                            reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.ml),
+                            p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
+                            p->weights_in, p->weights_out, status};
+  return cuda_status(da::launch_kv4_decode(a, s));
+}
+
+size_t diffattn_kv_evict_workspace_size(int B, int h_kv, int L_max, int keep) {
+  if (B <= 0 || h_kv <= 0 || L_max <= 0 || keep <= 0) return 0;
+  return evict_space(B, h_kv, L_max, keep).total;
+}
+
+da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
+  if (p == nullptr) return DA_ERR_INVALID_ARG;
+  if (p->B < 0 || p->h_kv <= 0 || p->L_max <= 0) return DA_ERR_INVALID_ARG;
+  if (p->keep < 1 || p->sinks < 0 || p->recent < 0 || p->sinks > p->keep - p->recent) return DA_ERR_INVALID_ARG;
+  if (p->n_rows < 1 || p->n_rows > DIFFATTN_EVICT_MAX_ROWS) return DA_ERR_INVALID_ARG;
+  if (p->B == 0) return DA_OK;
+  if (!p->weights_in || !p->weights_out || !p->seqlens_out || (p->positions_in && !p->positions_out))
+    return DA_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(p->weights_in), static_cast<const void*>(p->weights_out),
+                        static_cast<const void*>(p->positions_in), static_cast<const void*>(p->positions_out),
+                        static_cast<const void*>(p->seqlens), static_cast<const void*>(p->seqlens_out),
+                        static_cast<const void*>(p->next_position)})
+    if (!aligned(q, 4)) return DA_ERR_INVALID_ARG;
+  for (int k = 0; k < p->n_rows; ++k)
+    if (!ok_t4(p->rows[k], 16) || p->row_bytes[k] <= 0 || p->row_bytes[k] % 16) return DA_ERR_INVALID_ARG;
+  // one CTA per head to select, up to 64 to move its rows
+  if (static_cast<int64_t>(p->B) * p->h_kv > 2147483647 / 64) return DA_ERR_UNSUPPORTED;
+  const EvictSpace w = evict_space(p->B, p->h_kv, p->L_max, p->keep);
+  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
+  uint32_t* status;
+  int sms;
+  if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+  const da::EvictArgs a{*p, reinterpret_cast<int*>(ws), reinterpret_cast<int*>(ws + w.len),
+                        reinterpret_cast<int*>(ws + w.dst), reinterpret_cast<int*>(ws + w.src), w.max_moves, status};
+  return cuda_status(da::launch_kv_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

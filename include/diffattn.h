@@ -453,6 +453,164 @@ da_status diffattn_v2_decode(const da_v2_decode_params* p, void* cuda_stream);
 da_status diffattn_v2_decode_noalloc(const da_v2_decode_params* p, void* cuda_stream);
 
 /* ------------------------------------------------------------------------ */
+/* 4-bit KV cache.  The pages have no counterpart; [P1] "V2로의 진화" and [P2]
+ * §2 say why a user wants one: a decode step is bound by reading the cache.
+ * A cache is one array of records, one record per sequence, position and KV
+ * head, holding the key and the value row in diffattn_kv4_record_bytes(d) =
+ * d + 16 bytes (d = 64 or 128):
+ *   bytes 0 .. d/2-1        key codes: byte i holds the codes of feature 2i
+ *                           (low four bits) and 2i + 1 (high four bits)
+ *   bytes d/2 .. d-1        value codes, likewise
+ *   bytes d .. d+7          key parameters s0 s1 m0 m1, bf16
+ *   bytes d+8 .. d+15       value parameters, likewise
+ * A row has two groups of d/2 features, each with a scale s and a minimum m:
+ *   m = min x,  s = bf16((max x - min x) / 15)   (round to nearest even)
+ *   code = rint((x - m) / s) limited to 0..15,   value = s * code + m
+ * computed in fp32.  A group with s = 0 has codes 0.  A group whose s is not
+ * finite (it holds a NaN or an infinity, or its range overflows fp32) is
+ * stored as s = m = NaN, codes 0, so what reads it gives NaN.
+ * A cache is given as a da_t4 over bytes: record (b, n, g) lives at
+ * ptr + b*sb + n*sn + g*sh, strides in BYTES, pointer and strides multiples
+ * of 16.  Any order of the three dimensions will do; with sn = d + 16 (each
+ * head's records contiguous) the decode reads it fastest. */
+int diffattn_kv4_record_bytes(int d); /* d + 16, or 0 for an unsupported d */
+
+/* Quantise N new rows per sequence into the cache.  Row (b, i, g), i <
+ * counts[b], goes to record (b, start[b] + i, g).
+ * k, v: bf16 [B, N, h_kv, d]; cache: records [B, L_max, h_kv]; start, counts:
+ * int32 [B] device (start NULL = all 0, counts NULL = all N).  Optional, fp32
+ * / int32 [B, h_kv, L_max] contiguous: key_weights (the gathered weights of
+ * diffattn_v2_decode_kv4: the written positions are set to 0) and positions
+ * (set to the row's token position, first_position[b] + i; first_position
+ * NULL = start).  Records that no row goes to are left as they were.
+ * A sequence with start < 0, counts outside [0, N] or start + counts > L_max
+ * is recorded as DA_ERR_BOUNDS in the device status word and not written. */
+typedef struct {
+  int B, N, h_kv, d, L_max;
+  da_t4 k, v;
+  da_t4 cache;
+  const int* start;
+  const int* counts;
+  float* key_weights;
+  int* positions;
+  const int* first_position;
+} da_kv4_append_params;
+
+da_status diffattn_kv4_append(const da_kv4_append_params* p, void* cuda_stream);
+
+/* Read records back as bf16 rows (value = s * code + m, rounded once), for an
+ * attention over bf16 rows such as diffattn_v2_fwd on a cached prefix: record
+ * (b, start[b] + i, g), i < counts[b], goes to k_out, v_out (b, i, g); the
+ * other rows are left as they were.  Arguments and errors as in
+ * diffattn_kv4_append; k_out, v_out: bf16 [B, N, h_kv, d]. */
+typedef struct {
+  int B, N, h_kv, d, L_max;
+  da_t4 cache;
+  const int* start;
+  const int* counts;
+  da_t4 k_out, v_out;
+} da_kv4_read_params;
+
+da_status diffattn_kv4_read(const da_kv4_read_params* p, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
+/* V2 decode over a 4-bit cache: diffattn_v2_decode's result, with the keys
+ * and values that the records stand for.  q, seqlens, gate, x, w_lambda, out,
+ * the supported shapes and the treatment of bad sequence lengths are those of
+ * diffattn_v2_decode.
+ * Gathered weights (optional, weights_out NULL = not computed): what each key
+ * contributes to the differential maps of its KV head, summed over the head's
+ * output pairs p,
+ *   weights_out[b, g, j] = weights_in[b, g, j]
+ *                          + sum_p |A_2p[j] - gate[b, p] A_2p+1[j]|,
+ * for j < seqlens[b]; the other positions are left as they were.  Both fp32
+ * [B, h_kv, L_max] contiguous; weights_in NULL = 0, and it may be the same
+ * array as weights_out (it may not overlap it otherwise).
+ * workspace: diffattn_v2_decode_kv4_workspace_size bytes, 256-byte aligned,
+ * contents on entry irrelevant; calls that run at the same time need
+ * workspaces of their own.  Results are bitwise reproducible. */
+typedef struct {
+  int B, h, h_kv, d, L_max, d_model;
+  float softmax_scale;   /* <= 0 selects 1/sqrt(d) */
+  const void* q;
+  da_t4 cache;
+  const int* seqlens;
+  const float* gate;
+  const void* x;
+  const void* w_lambda;
+  const float* weights_in;
+  float* weights_out;
+  void* out;
+  void* workspace;
+  size_t workspace_bytes;
+} da_v2_decode_kv4_params;
+
+size_t diffattn_v2_decode_kv4_workspace_size(int B, int h, int h_kv, int d, int L_max,
+                                             int gate_given, int weights);
+da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* cuda_stream);
+
+/* diffattn_v2_decode over bf16 caches that also gathers the keys' weights, as
+ * diffattn_v2_decode_kv4 does: `decode` as for diffattn_v2_decode, with a
+ * workspace of diffattn_v2_decode_weighted_workspace_size bytes; weights_out
+ * is required. */
+typedef struct {
+  da_v2_decode_params decode;
+  const float* weights_in;
+  float* weights_out;
+} da_v2_decode_weighted_params;
+
+size_t diffattn_v2_decode_weighted_workspace_size(int B, int h, int h_kv, int d, int L_max,
+                                                  int num_splits, int gate_given);
+da_status diffattn_v2_decode_weighted(const da_v2_decode_weighted_params* p, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Eviction by gathered weight: cut every sequence's cache down to `keep`
+ * positions, per KV head.  Of the L = seqlens[b] filled slots of (b, g) the
+ * m = min(L, keep) highest stay: first those whose token position is below
+ * `sinks` or at least next_position[b] - recent, then the others by
+ * weights_in (a NaN above every number), ties to the lowest slot.  Slots
+ * below m that stay are not moved; the i-th slot below m that does not stay
+ * takes the i-th slot at or above m that does (both in ascending order), so
+ * the cache is compacted in place and as little as possible is moved.  An
+ * attention over the cache does not depend on the slots' order.
+ * rows[0 .. n_rows-1]: the caches to compact, [B, L_max, h_kv] rows of
+ * row_bytes[i] bytes each (K and V, or K1, K2 and V, or 4-bit records), with
+ * strides in BYTES; pointers, strides and row_bytes multiples of 16; no two
+ * rows overlap.  Slots at or above m are left as they were.
+ * weights_in / weights_out: fp32 [B, h_kv, L_max] contiguous; positions_in /
+ * positions_out: int32, likewise (positions_in NULL: slot j holds token
+ * position j; positions_out NULL: not written, allowed where positions_in is
+ * NULL); seqlens / seqlens_out: int32 [B] (seqlens NULL = all L_max).  Slots
+ * below m of the outputs are written with what moved there, the others left.
+ * Each _out may be the same array as its _in (and may not overlap it
+ * otherwise).  next_position: int32 [B], one past the newest token's position
+ * (NULL = seqlens).  1 <= keep, 0 <= sinks, 0 <= recent, sinks + recent <=
+ * keep; keep may exceed L_max.
+ * A length outside [0, L_max] is recorded as DA_ERR_BOUNDS in the device
+ * status word; that sequence is left as it was, with its length copied.
+ * workspace: diffattn_kv_evict_workspace_size bytes, 256-byte aligned. */
+#define DIFFATTN_EVICT_MAX_ROWS 3
+typedef struct {
+  int B, h_kv, L_max;
+  int keep, sinks, recent;
+  const int* seqlens;
+  int* seqlens_out;
+  const float* weights_in;
+  float* weights_out;
+  const int* positions_in;
+  int* positions_out;
+  const int* next_position;
+  int n_rows;
+  int row_bytes[DIFFATTN_EVICT_MAX_ROWS];
+  da_t4 rows[DIFFATTN_EVICT_MAX_ROWS];
+  void* workspace;
+  size_t workspace_bytes;
+} da_kv_evict_params;
+
+size_t diffattn_kv_evict_workspace_size(int B, int h_kv, int L_max, int keep);
+da_status diffattn_kv_evict(const da_kv_evict_params* p, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
 /* Device status word.  Kernels record the first error they detect (a bounded
  * wait that expired, a failed index check) in a per-device word instead of
  * trapping.  diffattn_get_device_status synchronises `cuda_stream`, returns
