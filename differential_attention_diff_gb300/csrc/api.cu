@@ -245,7 +245,7 @@ da_status run_v2_decode(const da_v2_decode_params* p, const float* weights_in, f
                    part_o, part_ml, d.status, scores};
   cudaError_t e = da::launch_decode(a, s);
   if (e == cudaSuccess && weights_out) {
-    const da::KeyWeightsArgs w{p->B, p->h, p->h_kv, p->L_max, splits, p->seqlens, gate, part_ml, scores,
+    const da::KeyWeightsArgs w{p->B, p->h, p->h_kv, p->L_max, splits, nullptr, p->seqlens, gate, part_ml, scores,
                                weights_in, weights_out};
     e = da::launch_key_weights(w, s);
   }

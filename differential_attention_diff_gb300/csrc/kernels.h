@@ -74,15 +74,17 @@ cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s);
 
 // ---- V2 decode over a 4-bit KV cache ----------------------------------------
 struct Kv4DecodeArgs {
-  int B, h, h_kv, d, L_max, num_splits;
+  int B, h, h_kv, d, L_max;
+  int grid;           // CTAs that share the work
   float scale_log2;
   const void* q;
   da_t4 cache;        // records [B, L_max, h_kv], byte strides
   const int* seqlens;
   const float* gate;  // [B, h]
   void* out;          // bf16 [B, h, d]
-  float* part_o;      // [splits, B, 2h, d]
-  float* part_ml;     // [splits, B, 2h, 2]
+  float* part_o;      // [grid + B * h_kv, G, d] (numbered as in kv4.cuh)
+  float* part_ml;     // [grid + B * h_kv, G, 2]
+  int64_t* prefix;    // [B + 1] chunks of one head before each sequence
   float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
   const float* weights_in;
   float* weights_out;
@@ -92,10 +94,12 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 
 // ---- gathered key weights from the scores of a decode -------------------------
 struct KeyWeightsArgs {
-  int B, h, h_kv, L_max, num_splits;
+  int B, h, h_kv, L_max;
+  int splits;             // key-range splits, or the 4-bit decode's grid where prefix is given
+  const int64_t* prefix;  // the 4-bit decode's table, or null
   const int* seqlens;
   const float* gate;
-  const float* part_ml;  // [splits, B, 2h, 2]
+  const float* part_ml;  // [splits, B, 2h, 2], or the 4-bit decode's
   const float* scores;   // [B, h_kv, L_max, G]
   const float* weights_in;
   float* weights_out;

@@ -8,6 +8,7 @@
 // would not do: an error e in t is an error of 0.7 e in the weight.
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace da {
 namespace {
@@ -24,12 +25,20 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a)
   __shared__ float sm[kMaxG], sc[kMaxG];
   if (threadIdx.x < G) {
     const int j = g * G + threadIdx.x;
+    // this head's partials: one per split, or the parts of a line of chunks
+    int64_t first = static_cast<int64_t>(b) * a.h_kv + g, step = static_cast<int64_t>(a.B) * a.h_kv;
+    int count = a.splits;
+    if (a.prefix) {
+      const Kv4Parts s = kv4_head_parts(a.prefix, a.B, a.h_kv, b, g, a.splits);
+      first = s.first;
+      count = s.count;
+      step = 1;
+    }
     float mt = -INFINITY, lt = 0.f;
-    for (int s = 0; s < a.num_splits; ++s)
-      mt = fmaxf(mt, a.part_ml[((static_cast<int64_t>(s) * a.B + b) * H2 + j) * 2]);
+    for (int i = 0; i < count; ++i) mt = fmaxf(mt, a.part_ml[((first + i * step) * G + threadIdx.x) * 2]);
     const float base = mt == -INFINITY ? 0.f : mt;
-    for (int s = 0; s < a.num_splits; ++s) {
-      const float* ml = a.part_ml + ((static_cast<int64_t>(s) * a.B + b) * H2 + j) * 2;
+    for (int i = 0; i < count; ++i) {
+      const float* ml = a.part_ml + ((first + i * step) * G + threadIdx.x) * 2;
       lt += ml[1] * exp2f(ml[0] - base);
     }
     float c = lt == 0.f ? 0.f : 1.f / lt;

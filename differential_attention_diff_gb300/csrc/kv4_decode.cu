@@ -1,123 +1,632 @@
 // kv4_decode.cu — V2 decode over a 4-bit KV cache (records of kv4.cu).
 //
-// Split-KV as in decode.cu: grid (splits, h_kv, B), partial (max, sum, O) per
-// split and query head, then the same merge.  Each warp takes every eighth
-// key of the split: its lanes hold D/32 features of the record's two rows,
-// scores are reduced by shuffles, and the online softmax runs per warp.
+// out_p = (A_2p - gate_p A_2p+1) V with A_j = softmax(scale q_j K^T), K and V
+// the values s n + m that the records stand for (n a 4-bit code; s, m per
+// half row).  A record is 144 bytes for 512 bytes of bf16 rows, so at the
+// memory's rate an SM gets 23 bytes, 47 codes, a cycle: there are about 2.7
+// lane-instructions per code.  Turning every code into s n + m first would
+// spend twice that.  The kernel therefore multiplies the codes themselves:
+//   score_j  = sum_groups s (q . n) + m (sum of q),
+//   output_f = sum_j (p_j s_j) n_jf + sum_j p_j m_j,
+// with s and m applied to a group's 32 or 64 products at once.  A code masked
+// out of its word IS an fp16 number, the subnormal n 2^-24 (or 16 n 2^-24 for
+// the upper code of a byte), which the tensor cores take exactly, so a pair
+// of codes costs one AND (and a shift per two pairs); 2^24 and 1/16 are
+// powers of two that move into q and the final factor.
+//
+// Scores are taken transposed, S^T[16 keys x 8 heads] = K Q^T, so that the
+// codes are the A operand and the heads (2h/h_kv of them, up to 16) fill the
+// small side of m16n8k16; the products p s go through movmatrix into the B
+// operand of O^T[16 features x 8 heads] += V^T P^T, whose pairs of keys are
+// put side by side by two byte permutes per four pairs.
+//
+// P is fp16 (11 bits, against 8 of a bf16 P).  Its range is kept by a power
+// of two per head, vs, beside the running maximum m of the scores: both are
+// references that only move when a value would pass 2^8 (p) or 2^14 (p s vs),
+// by a warp vote, so the common path has no reductions.  vs follows p s and
+// not s, so a large value row of a key with no weight costs no precision.
+// Sums of p, of p m and the score corrections are fp32.
+//
+// Schedule: the batch's work is one line of 32-key chunks in (sequence, KV
+// head) order, cut into equal parts, one per CTA (one CTA per SM), so ragged
+// lengths balance exactly; a CTA's warps take chunks in turn, each from a
+// ring of its own that it fills with bulk copies (one per chunk where a
+// head's records are contiguous, else one per record) and its own barriers.
+// The warps meet only where a head ends: each puts its partial O into the
+// ring slot it last read and all sum them.  A second kernel merges the parts
+// of each head and applies the gate.
 #include "common.cuh"
+#include <cuda_fp16.h>
+
 #include "kernels.h"
+#include "kv4.cuh"
+#include "tma.cuh"
 
 namespace da {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxG = 16;
+constexpr int kChunk = kKv4ChunkKeys;  // keys per ring slot
 
-__device__ __forceinline__ float bf16_at(uint2 par, int i) {
-  const uint32_t w = i < 2 ? par.x : par.y;
-  return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+template <int D, int NT>
+struct Cfg {
+  // 128 registers a thread allow 16 warps; two head tiles need more
+  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRec = D + 16;
+  static constexpr int kSlot = kChunk * kRec;  // bytes
+  static constexpr int kStages = NT == 1 ? 3 : 5;
+  static constexpr int kRing = kWarps * kStages * kSlot;  // 221,184 (D 128, 16 warps) or less
+  static constexpr int kWords = D / 64;     // 4-byte code words per lane, group and key row (K side)
+  static constexpr int kTiles = D / 16;     // 16-feature tiles of O^T
+  static constexpr int kGroupTiles = kTiles / 2;
+  static constexpr int kRegPitch = 36;      // floats between O registers in a slot: spreads the banks
+};
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// D = A(16x16, row) * B(16x8, col) + D, fp16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of 16-bit values across the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Untiled bulk copy, both addresses and the size multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float exponent_scale(float x, int target) {
+  // the power of two that brings x > 0 into [2^target, 2^(target+1)), limited to 2^-126 .. 2^100
+  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 0xffu) - 127;
+  int k = target - e;
+  k = k > 100 ? 100 : k < -126 ? -126 : k;
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv4_split_kernel(Kv4DecodeArgs a) {
-  constexpr int F = D / 32;  // features per lane, contiguous
-  const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int H2 = 2 * a.h, G = H2 / a.h_kv, qh0 = g * G;
-  int L = a.seqlens ? a.seqlens[b] : a.L_max;
-  if (L < 1 || L > a.L_max) {
-    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
-    L = 0;
-  }
-  const int chunk = (L + a.num_splits - 1) / a.num_splits;
-  const int k0 = min(L, split * chunk), k1 = min(L, k0 + chunk);
+// Chunks of one head of sequence b: 0 for a bad length.
+__device__ __forceinline__ int seq_chunks(const Kv4DecodeArgs& a, int b) {
+  const int L = a.seqlens ? a.seqlens[b] : a.L_max;
+  return L < 1 || L > a.L_max ? 0 : (L + kChunk - 1) / kChunk;
+}
 
-  float q[kMaxG][F], o[kMaxG][F], m[kMaxG], l[kMaxG];
+// A position on the line of chunks: the head u = b * h_kv + g, and this
+// warp's next chunk of it within [chunk, end).
+struct Cursor {
+  int b, g, chunk, end;
+  int L;         // the sequence's length
+  int64_t left;  // chunks of this CTA's part behind this head
+};
+
+template <int D, int NT, bool kScores>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4DecodeArgs a) {
+  using C = Cfg<D, NT>;
+  constexpr int kW = C::kWarps, kS = C::kStages, kRec = C::kRec, kWords = C::kWords, kGT = C::kGroupTiles;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kW * kS];
+  __shared__ int64_t scan[kW];
+  __shared__ int64_t found[4];
+  __shared__ float sm_m[kW][8 * NT], sm_l[kW][8 * NT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gr = lane >> 2, tq = lane & 3;
+  const int H2 = 2 * a.h, G = H2 / a.h_kv;
+
+  if (tid < kW * kS) mbar_init(smem_u32(&bars[tid]), 1);
+  fence_mbar_init();
+
+  // ---- this CTA's part of the line ----
+  // prefix[b] = chunks of one head over the sequences before b; every CTA
+  // sums the lengths itself, the first also leaves the table for the merge
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+    const int b = b0 + tid;
+    const int n = b < a.B ? seq_chunks(a, b) : 0;
+    if (blockIdx.x == 0 && b < a.B && n == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
+    int64_t x = n;
 #pragma unroll
-  for (int r = 0; r < kMaxG; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      o[r][f] = 0.f;
-      q[r][f] = r < G ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[(static_cast<int64_t>(b) * H2 + qh0 + r) * D +
-                                                                                lane * F + f])
-                      : 0.f;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t before = carry;
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += scan[w];
+      carry += scan[w];
+    }
+    if (b < a.B) {
+      if (blockIdx.x == 0) a.prefix[b] = before + x - n;
+    }
+    __syncthreads();
   }
-  const uint8_t* base = static_cast<const uint8_t*>(a.cache.ptr) + b * a.cache.sb + g * a.cache.sh;
-  for (int key = k0 + warp; key < k1; key += kWarps) {
-    const uint8_t* rec = base + key * a.cache.sn;
-    float kv[2][F];
+  const int64_t total = carry * a.h_kv;
+  if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = carry;
+  const int64_t parts = kv4_parts(total, gridDim.x);
+  if (blockIdx.x >= parts || total == 0) return;
+  const int64_t first = blockIdx.x * total / parts, last = (blockIdx.x + 1) * total / parts;
+  // the sequence that holds chunk `first`
+  carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+    const int b = b0 + tid;
+    const int n = b < a.B ? seq_chunks(a, b) : 0;
+    int64_t x = n;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint2 par = *reinterpret_cast<const uint2*>(rec + D + 8 * w);
-      const float s = bf16_at(par, lane >> 4), mn = bf16_at(par, 2 + (lane >> 4));
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t before = carry;
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += scan[w];
+      carry += scan[w];
+    }
+    const int64_t from = (before + x - n) * a.h_kv;
+    if (n > 0 && first >= from && first < from + static_cast<int64_t>(n) * a.h_kv) {
+      found[0] = b;
+      found[1] = (first - from) / n;
+      found[2] = (first - from) % n;
+    }
+    __syncthreads();
+    if (carry * a.h_kv > first) break;  // uniform: found in this tile
+  }
+
+  Cursor at;
+  auto enter = [&](Cursor& c, int begin) {  // chunks [begin, ..) of head (c.b, c.g), as far as the part goes
+    c.L = a.seqlens ? a.seqlens[c.b] : a.L_max;
+    const int n = (c.L + kChunk - 1) / kChunk;
+    const int64_t take = min(static_cast<int64_t>(n - begin), c.left);
+    c.end = begin + static_cast<int>(take);
+    c.left -= take;
+    c.chunk = begin + warp;
+  };
+  auto next_head = [&](Cursor& c) {  // c.left > 0: another head with chunks follows
+    do {
+      if (++c.g == a.h_kv) c.g = 0, ++c.b;
+    } while (seq_chunks(a, c.b) == 0);
+    enter(c, 0);
+  };
+  at.b = static_cast<int>(found[0]);
+  at.g = static_cast<int>(found[1]);
+  at.left = last - first;
+  enter(at, static_cast<int>(found[2]));
+
+  const uint32_t ring = smem_u32(smem) + warp * kS * C::kSlot;
+  const uint32_t bar0 = smem_u32(&bars[warp * kS]);
+  const uint8_t* cache = static_cast<const uint8_t*>(a.cache.ptr);
+  const bool dense = a.cache.sn == kRec;
+  bool dead = false;  // a wait ran out: nothing more is issued or read
+
+  // fill the ring's next slot with the chunk that `ahead` is at
+  Cursor ahead = at;
+  int issued = 0, taken = 0;
+  auto issue = [&]() {
+    while (ahead.chunk >= ahead.end) {
+      if (ahead.left == 0) return;
+      next_head(ahead);
+    }
+    if (dead) return;
+    const int key0 = ahead.chunk * kChunk, n = min(kChunk, ahead.L - key0);
+    const int slot = issued % kS;
+    const uint32_t dst = ring + slot * C::kSlot, bar = bar0 + slot * 8;
+    const uint8_t* src = cache + ahead.b * a.cache.sb + ahead.g * a.cache.sh + key0 * a.cache.sn;
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * kRec);
+    if (dense) {
+      if (lane == 0) bulk_load(dst, src, n * kRec, bar);
+    } else {
+      __syncwarp();
+      if (lane < n) bulk_load(dst + lane * kRec, src + lane * a.cache.sn, kRec, bar);
+    }
+    ++issued;
+    ahead.chunk += kW;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kS - 1; ++i) issue();
+
+  // row gr of a 16-key tile is key row_key, row gr + 8 the key after it: an
+  // order that keeps both the K and the V loads off each other's banks
+  const int b2 = gr >> 2, b1 = (gr >> 1) & 1, b0 = gr & 1;
+  const int row_key = 8 * b2 + 2 * b1 + 4 * (b0 ^ b2);
+  auto key_of = [](int r) { return 8 * (r >> 2) + 2 * ((r >> 1) & 1) + 4 * ((r & 1) ^ (r >> 2)); };
+  const int vkey0 = key_of(2 * tq), vkey1 = key_of(2 * tq + 1);
+
+  while (true) {
+    // ---- a head: its queries ----
+    const int64_t unit = static_cast<int64_t>(at.b) * a.h_kv + at.g;
+    uint32_t qf[NT][4 * kWords][2];  // B fragments: [2 groups x kWords x 2 MMAs]
+    float qs0[NT][2], qs1[NT][2], fac[NT][2];  // of heads 2 tq, 2 tq + 1: group sums of q, score factor
 #pragma unroll
-      for (int f = 0; f < F; f += 2) {
-        const uint32_t c = rec[w * (D / 2) + (lane * F + f) / 2];
-        kv[w][f] = fmaf(s, static_cast<float>(c & 15u), mn);
-        kv[w][f + 1] = fmaf(s, static_cast<float>(c >> 4), mn);
+    for (int t = 0; t < NT; ++t) {
+      const int head = t * 8 + gr;
+      float q[2][8 * kWords];
+      float mx = 0.f;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (head < G)
+            v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                (static_cast<int64_t>(at.b) * H2 + at.g * G + head) * D + p * (D / 2) +
+                                                tq * (D / 8) + w * 8);
+          const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            q[p][w * 8 + 2 * e] = lo_bf16(ws[e]);
+            q[p][w * 8 + 2 * e + 1] = hi_bf16(ws[e]);
+            mx = fmaxf(mx, fmaxf(fabsf(lo_bf16(ws[e])), fabsf(hi_bf16(ws[e]))));
+          }
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // largest query feature in [2^14, 2^15): exact in fp16 down to 2^-29 of it
+      const float up = mx > 0.f ? exponent_scale(mx, 14) : 1.f;
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int i = 0; i < 8 * kWords; ++i) {
+          q[p][i] *= up;
+          sum[p] += q[p][i];
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const float* x = &q[p][w * 8 + 2 * m];
+            qf[t][(p * kWords + w) * 2 + m][0] = pack_f16x2(x[0], x[4]);
+            qf[t][(p * kWords + w) * 2 + m][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
+          }
+        sum[p] += __shfl_xor_sync(0xffffffffu, sum[p], 1);
+        sum[p] += __shfl_xor_sync(0xffffffffu, sum[p], 2);
+        sum[p] *= 0x1p-24f;
+      }
+      const float f = 0x1p24f / up * a.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qs0[t][e] = __shfl_sync(0xffffffffu, sum[0], (2 * tq + e) * 4);
+        qs1[t][e] = __shfl_sync(0xffffffffu, sum[1], (2 * tq + e) * 4);
+        fac[t][e] = __shfl_sync(0xffffffffu, f, (2 * tq + e) * 4);
       }
     }
+    float o[NT][C::kTiles][4];
+    float mx[NT][2], vs[NT][2], l[NT][2], mn[NT][2][2];  // reference max, value factor, sums of p and p m (per group)
 #pragma unroll
-    for (int r = 0; r < kMaxG; ++r) {
-      if (r >= G) break;
-      float t = 0.f;
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int f = 0; f < F; ++f) t = fmaf(q[r][f], kv[0][f], t);
+      for (int i = 0; i < C::kTiles; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 #pragma unroll
-      for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-      t *= a.scale_log2;
-      if (a.scores && lane == 0)
-        a.scores[((static_cast<int64_t>(b) * a.h_kv + g) * a.L_max + key) * G + r] = t;
-      const float mn = fmaxf(m[r], t);
-      const float base_m = mn == -INFINITY ? 0.f : mn;
-      const float al = exp2f(m[r] - base_m), p = exp2f(t - base_m);
-      m[r] = mn;
-      l[r] = l[r] * al + p;
-#pragma unroll
-      for (int f = 0; f < F; ++f) o[r][f] = fmaf(p, kv[1][f], o[r][f] * al);
+      for (int e = 0; e < 2; ++e) {
+        mx[t][e] = -INFINITY;
+        vs[t][e] = 0x1p100f;
+        l[t][e] = mn[t][0][e] = mn[t][1][e] = 0.f;
+      }
     }
-  }
-  __shared__ float so[kWarps][kMaxG][D];
-  __shared__ float sm[kWarps][kMaxG], sl[kWarps][kMaxG];
+
+    for (; at.chunk < at.end; at.chunk += kW) {
+      issue();  // into the slot read last
+      const int slot = taken % kS;
+      if (!dead && !mbar_wait(bar0 + slot * 8, (taken / kS) & 1, a.status, 0x4B04)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      ++taken;
+      if (dead) continue;
+      const uint32_t base = ring + slot * C::kSlot;
+      const int key0 = at.chunk * kChunk;
+      const int valid = at.L - key0;  // keys of this chunk
+
+      // ---- scores, two 16-key tiles ----
+      uint4 par[2][2];  // [tile][row half]: K s0 s1 | K m0 m1 | V s0 s1 | V m0 m1
+      float s[2][NT][4];
 #pragma unroll
-  for (int r = 0; r < kMaxG; ++r) {
-    if (r >= G) break;
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t ra = base + (u * 16 + row_key) * kRec;
+        par[u][0] = lds128(ra + D);
+        par[u][1] = lds128(ra + kRec + D);
+        if (valid < kChunk) {  // what lies behind the last key may be anything: give it zero parameters
+          if (u * 16 + row_key >= valid) par[u][0] = make_uint4(0, 0, 0, 0);
+          if (u * 16 + row_key + 1 >= valid) par[u][1] = make_uint4(0, 0, 0, 0);
+        }
+        float acc[2][NT][4];
 #pragma unroll
-    for (int f = 0; f < F; ++f) so[warp][r][lane * F + f] = o[r][f];
-    if (lane == 0) sm[warp][r] = m[r], sl[warp][r] = l[r];
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < G * D; idx += kWarps * 32) {
-    const int r = idx / D, f = idx % D;
-    float mt = -INFINITY, lt = 0.f, ot = 0.f;
-    for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm[w][r]);
-    const float base_m = mt == -INFINITY ? 0.f : mt;
-    for (int w = 0; w < kWarps; ++w) {
-      const float e = exp2f(sm[w][r] - base_m);
-      lt += sl[w][r] * e;
-      ot += so[w][r][f] * e;
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[p][t][0] = acc[p][t][1] = acc[p][t][2] = acc[p][t][3] = 0.f;
+          uint32_t wa[kWords], wb[kWords];
+          const uint32_t off = p * (D / 4) + tq * (D / 16);
+          if constexpr (kWords == 2) {
+            const uint2 x = lds64(ra + off), y = lds64(ra + kRec + off);
+            wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
+          } else {
+            wa[0] = lds32(ra + off);
+            wb[0] = lds32(ra + kRec + off);
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const uint32_t x = wa[w] >> (8 * m), y = wb[w] >> (8 * m);
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                mma_f16_16816(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
+                              qf[t][(p * kWords + w) * 2 + m][0], qf[t][(p * kWords + w) * 2 + m][1]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4& r = par[u][e >> 1];
+            const int c = e & 1;
+            float x = hi_bf16(r.y) * qs1[t][c];
+            x = fmaf(lo_bf16(r.y), qs0[t][c], x);
+            x = fmaf(lo_bf16(r.x), acc[0][t][e], x);
+            x = fmaf(hi_bf16(r.x), acc[1][t][e], x);
+            s[u][t][e] = x * fac[t][c];
+            if (valid < kChunk && u * 16 + row_key + (e >> 1) >= valid) s[u][t][e] = -INFINITY;
+          }
+        if constexpr (kScores) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int k = u * 16 + row_key + r;
+              if (k < valid && t * 8 + 2 * tq < G)
+                *reinterpret_cast<float2*>(a.scores + (unit * a.L_max + key0 + k) * G + t * 8 + 2 * tq) =
+                    make_float2(s[u][t][2 * r], s[u][t][2 * r + 1]);
+            }
+        }
+      }
+
+      // ---- softmax against the references ----
+      float p[2][NT][4], lsum[NT][2];
+      uint32_t pf[2][NT][2][2];  // [tile][head tile][group][row half], fp16 pairs of heads
+      auto weigh = [&]() {
+        bool over = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float m0 = mx[t][0] == -INFINITY ? 0.f : mx[t][0], m1 = mx[t][1] == -INFINITY ? 0.f : mx[t][1];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float x = fast_exp2(s[u][t][2 * r] - m0), y = fast_exp2(s[u][t][2 * r + 1] - m1);
+              p[u][t][2 * r] = x;
+              p[u][t][2 * r + 1] = y;
+              const float xv = x * vs[t][0], yv = y * vs[t][1];
+              const float s0 = lo_bf16(par[u][r].z), s1 = hi_bf16(par[u][r].z);
+              pf[u][t][0][r] = pack_f16x2(xv * s0, yv * s0);
+              pf[u][t][1][r] = pack_f16x2(xv * s1, yv * s1);
+            }
+          lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
+          lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
+          over |= lsum[t][0] > 256.f || lsum[t][1] > 256.f;
+          __half2 top = *reinterpret_cast<__half2*>(&pf[0][t][0][0]);
+#pragma unroll
+          for (int i = 1; i < 8; ++i)
+            top = __hmax2(top, *reinterpret_cast<__half2*>(&pf[i >> 2][t][(i >> 1) & 1][i & 1]));
+          over |= __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(16384.f));
+        }
+        return over;
+      };
+      bool first_tile = mx[0][0] == -INFINITY;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) first_tile |= mx[t][0] == -INFINITY || mx[t][1] == -INFINITY;
+      const bool over = weigh();
+      if (__any_sync(0xffffffffu, over || first_tile)) {
+        // new references from this chunk's keys: the score maximum, then the
+        // largest p s under it
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float old = mx[t][e], now = fmaxf(old, top);
+            const float nb = now == -INFINITY ? 0.f : now;
+            float big = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                big = fmaxf(big, fast_exp2(s[u][t][2 * r + e] - nb) *
+                                     fmaxf(lo_bf16(par[u][r].z), hi_bf16(par[u][r].z)));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+            const float down = old == -INFINITY ? 0.f : exp2f(old - nb);
+            l[t][e] *= down;
+            mn[t][0][e] *= down;
+            mn[t][1][e] *= down;
+            mx[t][e] = now;
+            // O stands for O / vs: a higher maximum raises vs and leaves O alone
+            const float keep = old == -INFINITY ? vs[t][e] : vs[t][e] * exp2f(nb - old);
+            float v = fminf(keep, 0x1p100f);
+            if (big > 0.f) v = fminf(v, exponent_scale(big, 8));
+            const float by = keep == v ? 1.f : v / keep;
+            vs[t][e] = v;
+#pragma unroll
+            for (int i = 0; i < C::kTiles; ++i) {
+              o[t][i][e] *= by;
+              o[t][i][2 + e] *= by;
+            }
+          }
+        weigh();
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[t][e] += lsum[t][e];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              mn[t][0][e] = fmaf(p[u][t][2 * r + e], lo_bf16(par[u][r].w), mn[t][0][e]);
+              mn[t][1][e] = fmaf(p[u][t][2 * r + e], hi_bf16(par[u][r].w), mn[t][1][e]);
+            }
+        }
+
+      // ---- O^T += V^T P^T ----
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t va = base + (u * 16 + vkey0) * kRec + D / 2, vb = base + (u * 16 + vkey1) * kRec + D / 2;
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2) {
+          uint32_t bf[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            bf[t][0] = movmatrix(pf[u][t][g2][0]);
+            bf[t][1] = movmatrix(pf[u][t][g2][1]);
+          }
+          uint32_t w0, w1, w2, w3;  // keys (vkey0, vkey1) and the ones after them
+          if constexpr (D == 128) {
+            const uint32_t off = g2 * 32 + gr * 4;
+            w0 = lds32(va + off), w1 = lds32(vb + off), w2 = lds32(va + kRec + off), w3 = lds32(vb + kRec + off);
+          } else {
+            const uint32_t off = g2 * 16 + gr * 2;
+            w0 = lds16(va + off), w1 = lds16(vb + off), w2 = lds16(va + kRec + off), w3 = lds16(vb + kRec + off);
+          }
+#pragma unroll
+          for (int hw = 0; hw < kWords; ++hw) {  // four features of both keys side by side
+            const uint32_t x = __byte_perm(w0, w1, hw ? 0x7632 : 0x5410), y = __byte_perm(w2, w3, hw ? 0x7632 : 0x5410);
+            const uint32_t xs = x >> 8, ys = y >> 8;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma_f16_16816(o[t][g2 * kGT + hw * 2], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu,
+                            ys & 0x000f000fu, bf[t][0], bf[t][1]);
+              mma_f16_16816(o[t][g2 * kGT + hw * 2 + 1], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u,
+                            ys & 0x00f000f0u, bf[t][0], bf[t][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the slot is read before it is filled again
     }
-    const int64_t at = (static_cast<int64_t>(split) * a.B + b) * H2 + qh0 + r;
-    a.part_o[at * D + f] = ot;
-    if (f == 0) a.part_ml[at * 2] = mt, a.part_ml[at * 2 + 1] = lt;
+
+    // ---- the head's end: sum the warps' partials ----
+    // O register i of lane l goes to word i * kRegPitch + l of the slot read
+    // last; the copies in flight go to the others
+    const int64_t row = (static_cast<int64_t>(blockIdx.x) + unit) * G;
+    float* park = reinterpret_cast<float*>(smem + (warp * kS + (taken + kS - 1) % kS) * C::kSlot);
+    __shared__ int park_slot[kW];
+    if (lane == 0) park_slot[warp] = (taken + kS - 1) % kS;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float lt = l[t][e], m0 = mn[t][0][e], m1 = mn[t][1][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          lt += __shfl_xor_sync(0xffffffffu, lt, x);
+          m0 += __shfl_xor_sync(0xffffffffu, m0, x);
+          m1 += __shfl_xor_sync(0xffffffffu, m1, x);
+        }
+        const float f = 1.f / vs[t][e];
+#pragma unroll
+        for (int i = 0; i < C::kTiles; ++i) {
+          const float fi = (i & 1) ? 0x1p20f : 0x1p24f;  // apart from f: their product may overflow
+          const float mi = i < kGT ? m0 : m1;
+          park[(i * 4 + e) * C::kRegPitch + lane] = fmaf(o[t][i][e] * fi, f, mi);
+          park[(i * 4 + 2 + e) * C::kRegPitch + lane] = fmaf(o[t][i][2 + e] * fi, f, mi);
+        }
+        if (gr == 0) {
+          sm_m[warp][t * 8 + 2 * tq + e] = mx[t][e];
+          sm_l[warp][t * 8 + 2 * tq + e] = lt;
+        }
+      }
+      __syncthreads();
+      // item (lane, head parity, pair of neighbouring features)
+      constexpr int kItems = 32 * 2 * (D / 16);
+      for (int x = tid; x < kItems; x += C::kThreads) {
+        const int fp = x % (D / 16);             // pair of features within the lane's D/8
+        const int ln = (x / (D / 16)) & 31, e = x / (D / 16) / 32;
+        const int head = 2 * (ln & 3) + e;
+        if (t * 8 + head >= G) continue;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) top = fmaxf(top, sm_m[w][t * 8 + head]);
+        const float nb = top == -INFINITY ? 0.f : top;
+        // features 2 fp, 2 fp + 1 of the lane's: tile pair, row half
+        constexpr int kPairs = D / 32;  // pairs per group and lane
+        const int g2 = fp / kPairs, q2 = fp % kPairs;
+        const int reg = (g2 * kGT + (q2 >> 1) * 2) * 4 + (q2 & 1) * 2 + e;
+        float lt = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          const float c = fast_exp2(sm_m[w][t * 8 + head] - nb);
+          const float* pk = reinterpret_cast<const float*>(smem + (w * kS + park_slot[w]) * C::kSlot);
+          lt = fmaf(sm_l[w][t * 8 + head], c, lt);
+          x0 = fmaf(pk[reg * C::kRegPitch + ln], c, x0);
+          x1 = fmaf(pk[(reg + 4) * C::kRegPitch + ln], c, x1);
+        }
+        const int64_t at_row = row + t * 8 + head;
+        const int f = g2 * (D / 2) + (ln >> 2) * (D / 16) + q2 * 2;
+        *reinterpret_cast<float2*>(a.part_o + at_row * D + f) = make_float2(x0, x1);
+        if (fp == 0 && (ln >> 2) == 0) {
+          a.part_ml[at_row * 2] = top;
+          a.part_ml[at_row * 2 + 1] = lt;
+        }
+      }
+      fence_proxy_async_smem();  // the next bulk copy into these slots comes after
+      __syncthreads();
+    }
+    if (at.left == 0) break;
+    next_head(at);
   }
+  // a warp that gave up waits (bounded) for what it still has in flight
+  if (dead)
+    for (; taken < issued; ++taken) mbar_wait(bar0 + (taken % kS) * 8, (taken / kS) & 1, nullptr, 0);
 }
 
-// One output head's splits merged, even - gate * odd.
-__global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4DecodeArgs a) {
-  const int p = blockIdx.x, b = blockIdx.y, f = threadIdx.x, H2 = 2 * a.h;
+// One output head's parts merged, even - gate * odd.  Grid (h, B).
+__global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4DecodeArgs a, int grid) {
+  const int p = blockIdx.x, b = blockIdx.y, f = threadIdx.x;
+  const int G = 2 * a.h / a.h_kv, g = 2 * p / G, r = 2 * p % G;
+  const Kv4Parts s = kv4_head_parts(a.prefix, a.B, a.h_kv, b, g, grid);
   float res[2];
   for (int e = 0; e < 2; ++e) {
     float mt = -INFINITY, lt = 0.f, ot = 0.f;
-    for (int s = 0; s < a.num_splits; ++s)
-      mt = fmaxf(mt, a.part_ml[((static_cast<int64_t>(s) * a.B + b) * H2 + 2 * p + e) * 2]);
-    const float base_m = mt == -INFINITY ? 0.f : mt;
-    for (int s = 0; s < a.num_splits; ++s) {
-      const int64_t at = (static_cast<int64_t>(s) * a.B + b) * H2 + 2 * p + e;
-      const float c = exp2f(a.part_ml[at * 2] - base_m);
+    for (int i = 0; i < s.count; ++i) mt = fmaxf(mt, a.part_ml[((s.first + i) * G + r + e) * 2]);
+    const float base = mt == -INFINITY ? 0.f : mt;
+    for (int i = 0; i < s.count; ++i) {
+      const int64_t at = (s.first + i) * G + r + e;
+      const float c = exp2f(a.part_ml[at * 2] - base);
       lt += a.part_ml[at * 2 + 1] * c;
       ot += a.part_o[at * a.d + f] * c;
     }
@@ -129,20 +638,35 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4DecodeArgs a) {
       __float2bfloat16_rn(__fsub_rn(res[0], __fmul_rn(a.gate[at], res[1])));
 }
 
+template <int D, int NT, bool kScores>
+cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  static_assert(C::kRing <= 225 * 1024, "the ring and the static arrays fit an SM");
+  static_assert(C::kTiles * 4 * C::kRegPitch * 4 <= C::kSlot, "a head tile's partial fits a slot");
+  auto* kernel = kv4_split_kernel<D, NT, kScores>;
+  // set on every launch: the attribute is per device, and the call is cheap
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.grid, C::kThreads, C::kRing, s>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
-  const dim3 grid(a.num_splits, a.h_kv, a.B);
+  const bool two = 2 * a.h / a.h_kv > 8, sc = a.scores != nullptr;
+  cudaError_t e;
   if (a.d == 128)
-    kv4_split_kernel<128><<<grid, kWarps * 32, 0, s>>>(a);
+    e = two ? (sc ? launch_split<128, 2, true>(a, s) : launch_split<128, 2, false>(a, s))
+            : (sc ? launch_split<128, 1, true>(a, s) : launch_split<128, 1, false>(a, s));
   else
-    kv4_split_kernel<64><<<grid, kWarps * 32, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+    e = two ? (sc ? launch_split<64, 2, true>(a, s) : launch_split<64, 2, false>(a, s))
+            : (sc ? launch_split<64, 1, true>(a, s) : launch_split<64, 1, false>(a, s));
   if (e != cudaSuccess) return e;
-  kv4_merge_kernel<<<dim3(a.h, a.B), a.d, 0, s>>>(a);
+  kv4_merge_kernel<<<dim3(a.h, a.B), a.d, 0, s>>>(a, a.grid);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
-  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, a.num_splits, a.seqlens, a.gate, a.part_ml, a.scores,
+  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, a.grid, a.prefix, a.seqlens, a.gate, a.part_ml, a.scores,
                          a.weights_in, a.weights_out};
   return launch_key_weights(w, s);
 }

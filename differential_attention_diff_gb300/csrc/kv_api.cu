@@ -7,6 +7,7 @@
 
 #include "diffattn.h"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace {
 
@@ -39,26 +40,25 @@ da_status check_rows(int B, int N, int h_kv, int d, int L_max, const da_t4& k, c
   return DA_OK;
 }
 
-// Key-range splits per (sequence, KV head).
-int decode_splits(int B, int h_kv, int L_max) {
+// CTAs of the 4-bit decode: one per SM, or as many as the fullest batch has
+// parts.  The lengths are on the device, so this is an upper bound.
+int decode_grid(int B, int h_kv, int L_max) {
   uint32_t* status;
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
-  const long units = static_cast<long>(B) * h_kv;
-  long s = (12L * sms + units - 1) / units;
-  const long most = (L_max + 511) / 512;
-  if (s > most) s = most;
-  return s < 1 ? 1 : static_cast<int>(s);
+  const int64_t chunks = (static_cast<int64_t>(L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys;
+  return static_cast<int>(da::kv4_parts(chunks * h_kv * B, sms));
 }
 
 struct DecodeSpace {
-  size_t ml, scores, gate, total;  // offsets; the partial O rows are at 0
+  size_t ml, prefix, scores, gate, total;  // offsets; the partial O rows are at 0
 };
 DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
-  const size_t rows = static_cast<size_t>(decode_splits(B, h_kv, L_max)) * B * 2 * h;
+  const size_t rows = (decode_grid(B, h_kv, L_max) + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
   DecodeSpace w;
   w.ml = align256(rows * d * sizeof(float));
-  w.scores = w.ml + align256(rows * 2 * sizeof(float));
+  w.prefix = w.ml + align256(rows * 2 * sizeof(float));
+  w.scores = w.prefix + align256((static_cast<size_t>(B) + 1) * sizeof(int64_t));
   w.gate = w.scores + (weights ? align256(static_cast<size_t>(B) * 2 * h * L_max * sizeof(float)) : 0);
   w.total = w.gate + (gate_given ? 0 : align256(static_cast<size_t>(B) * h * sizeof(float)));
   return w;
@@ -160,9 +160,10 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
     gate = g;
   }
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.f / std::sqrt(static_cast<float>(p->d));
-  const da::Kv4DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, decode_splits(p->B, p->h_kv, p->L_max),
+  const da::Kv4DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, decode_grid(p->B, p->h_kv, p->L_max),
                             scale * kLog2e, p->q, p->cache, p->seqlens, gate, p->out,
                             reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.ml),
+                            reinterpret_cast<int64_t*>(ws + w.prefix),
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
                             p->weights_in, p->weights_out, status};
   return cuda_status(da::launch_kv4_decode(a, s));
