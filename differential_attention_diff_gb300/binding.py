@@ -605,26 +605,56 @@ def diffattn_v2_decode_noalloc(q, k_cache, v_cache, *, seqlens=None, gate=None, 
 
 # ---- 4-bit KV cache, gathered key weights, eviction -------------------------
 
-def _array(t, shape, dtype, name, optional=True):
-    """The data pointer of a contiguous device array of the given shape and type."""
+def _device(t, stream):
+    """The device of t, which has to be the current one (the library launches
+    there), and the raw stream to launch on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on the current CUDA device expected, got {t.device}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"a stream of {t.device} expected, got one of {stream.device}")
+    return dev, stream.cuda_stream
+
+
+def _array(t, shape, dtype, dev, name):
+    """The data pointer of a contiguous array of the given shape and type on device dev (None: no array)."""
     if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is required")
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: contiguous CUDA {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: contiguous {dtype} {shape} on device {dev} expected, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows4(t, shape, dtype, name):
-    """da_t4 of a device tensor of the given shape and type (strides in its elements)."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda:
-        raise ValueError(f"{name}: CUDA {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
-    return _t4(t)
+def _rows4(t, shape, dtype, dev, name):
+    """da_t4 of a tensor of the given shape and type on device dev (strides in its elements)."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name}: {dtype} {shape} on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+    sb, sn, sh, sx = t.stride()
+    if sx != 1:
+        raise ValueError(f"{name}: a contiguous last dimension expected")
+    return da_t4(t.data_ptr(), sb, sn, sh)
 
 
-def _bytes(t):
-    return t.numel() * t.element_size()
+def _new(make, shape, dtype, dev, stream):
+    """A tensor made on the stream that the call launches on, so that its
+    memory (and its zeros) are ordered with the launch."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+
+
+def _space(workspace, need, dev, stream):
+    """(tensor, pointer, bytes) of a workspace: the given one, or a new one."""
+    if workspace is None:
+        workspace = _new(torch.empty, (max(need(), 1),), torch.uint8, dev, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on device {dev} expected")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def diffattn_kv4_record_bytes(d) -> int:
@@ -638,14 +668,17 @@ def diffattn_kv4_append(k, v, cache, *, start=None, counts=None, key_weights=Non
     L_max, h_kv, d + 16] in any stride order: row i < counts[b] goes to
     position start[b] + i.  key_weights / positions [B, h_kv, L_max] are reset
     for the written positions."""
-    B, N, hkv, d = k.shape
+    dev, raw = _device(k, stream)
+    B, N, hkv, d = shape = k.shape
     L_max, bf16, i32 = cache.shape[1], torch.bfloat16, torch.int32
     p = da_kv4_append_params(
-        B, N, hkv, d, L_max, _rows4(k, (B, N, hkv, d), bf16, "k"), _rows4(v, (B, N, hkv, d), bf16, "v"),
-        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, "cache"), _array(start, (B,), i32, "start"),
-        _array(counts, (B,), i32, "counts"), _array(key_weights, (B, hkv, L_max), torch.float32, "key_weights"),
-        _array(positions, (B, hkv, L_max), i32, "positions"), _array(first_position, (B,), i32, "first_position"))
-    _check(load().diffattn_kv4_append(C.byref(p), _stream(stream)), "diffattn_kv4_append")
+        B, N, hkv, d, L_max, _rows4(k, shape, bf16, dev, "k"), _rows4(v, shape, bf16, dev, "v"),
+        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, dev, "cache"), _array(start, (B,), i32, dev, "start"),
+        _array(counts, (B,), i32, dev, "counts"),
+        _array(key_weights, (B, hkv, L_max), torch.float32, dev, "key_weights"),
+        _array(positions, (B, hkv, L_max), i32, dev, "positions"),
+        _array(first_position, (B,), i32, dev, "first_position"))
+    _check((_lib or load()).diffattn_kv4_append(C.byref(p), raw), "diffattn_kv4_append")
     return cache
 
 
@@ -653,29 +686,31 @@ def diffattn_kv4_read(cache, N, *, start=None, counts=None, k_out=None, v_out=No
     """Positions start[b] .. start[b] + counts[b] - 1 of the 4-bit cache as
     bf16 rows: (k, v) [B, N, h_kv, d].  Rows i >= counts[b] are left as they
     were (zeros where the outputs are allocated here)."""
+    dev, raw = _device(cache, stream)
     B, L_max, hkv, rec = cache.shape
     d, bf16 = rec - 16, torch.bfloat16
+    shape = (B, N, hkv, d)
     if k_out is None:
-        k_out = torch.zeros((B, N, hkv, d), dtype=bf16, device=cache.device)
+        k_out = _new(torch.zeros, shape, bf16, dev, stream)
     if v_out is None:
-        v_out = torch.zeros((B, N, hkv, d), dtype=bf16, device=cache.device)
+        v_out = _new(torch.zeros, shape, bf16, dev, stream)
     p = da_kv4_read_params(
-        B, N, hkv, d, L_max, _rows4(cache, (B, L_max, hkv, rec), torch.uint8, "cache"),
-        _array(start, (B,), torch.int32, "start"), _array(counts, (B,), torch.int32, "counts"),
-        _rows4(k_out, (B, N, hkv, d), bf16, "k_out"), _rows4(v_out, (B, N, hkv, d), bf16, "v_out"))
-    _check(load().diffattn_kv4_read(C.byref(p), _stream(stream)), "diffattn_kv4_read")
+        B, N, hkv, d, L_max, _rows4(cache, (B, L_max, hkv, rec), torch.uint8, dev, "cache"),
+        _array(start, (B,), torch.int32, dev, "start"), _array(counts, (B,), torch.int32, dev, "counts"),
+        _rows4(k_out, shape, bf16, dev, "k_out"), _rows4(v_out, shape, bf16, dev, "v_out"))
+    _check((_lib or load()).diffattn_kv4_read(C.byref(p), raw), "diffattn_kv4_read")
     return k_out, v_out
 
 
-def _decode_operands(q, seqlens, gate, x, w_lambda, out, B, H2, d):
-    """What the two decodes below check and allocate alike: (q, seqlens, gate, x, w_lambda, out, d_model)."""
-    bf16, h = torch.bfloat16, H2 // 2
-    if out is None:
-        out = torch.empty((B, h, d), dtype=bf16, device=q.device)
-    d_model = 0 if x is None else x.shape[-1]
-    return (_array(q, (B, H2, d), bf16, "q"), _array(seqlens, (B,), torch.int32, "seqlens"),
-            _array(gate, (B, h), torch.float32, "gate"), _array(x, (B, d_model), bf16, "x"),
-            _array(w_lambda, (d_model, h), bf16, "w_lambda"), out, d_model)
+def _gate_source(gate, x, w_lambda, B, h, dev):
+    """The checked gate or (x, w_lambda) of a decode step: (gate, x, w_lambda, d_model)."""
+    if gate is not None:
+        return _array(gate, (B, h), torch.float32, dev, "gate"), None, None, 0
+    if x is None or w_lambda is None:
+        return None, None, None, 0  # refused by the library
+    d_model = x.shape[-1]
+    return (None, _array(x, (B, d_model), torch.bfloat16, dev, "x"),
+            _array(w_lambda, (d_model, h), torch.bfloat16, dev, "w_lambda"), d_model)
 
 
 def diffattn_v2_decode_kv4_workspace_size(B, h, h_kv, d, L_max, gate_given=False, weights=False) -> int:
@@ -687,20 +722,23 @@ def diffattn_v2_decode_kv4(q, cache, *, seqlens=None, gate=None, x=None, w_lambd
     """V2 decode over a 4-bit cache (uint8 [B, L_max, h_kv, d + 16]): out [B,
     h, d].  weights_out [B, h_kv, L_max]: weights_in (None = 0, may be the same
     tensor) plus what each key contributes to this step's differential maps."""
+    dev, raw = _device(q, stream)
     B, H2, d = q.shape
     L_max, hkv = cache.shape[1], cache.shape[2]
-    h = H2 // 2
-    q_, lens, gate_, x_, w_, out, d_model = _decode_operands(q, seqlens, gate, x, w_lambda, out, B, H2, d)
-    if workspace is None:
-        need = diffattn_v2_decode_kv4_workspace_size(B, h, hkv, d, L_max, gate is not None, weights_out is not None)
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+    h, bf16, f32 = H2 // 2, torch.bfloat16, torch.float32
+    if out is None:
+        out = _new(torch.empty, (B, h, d), bf16, dev, stream)
+    ws, ws_ptr, ws_bytes = _space(workspace, lambda: diffattn_v2_decode_kv4_workspace_size(
+        B, h, hkv, d, L_max, gate is not None, weights_out is not None), dev, stream)
+    gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
     p = da_v2_decode_kv4_params(
-        B, h, hkv, d, L_max, d_model, float(softmax_scale), q_,
-        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, "cache"), lens, gate_, x_, w_,
-        _array(weights_in, (B, hkv, L_max), torch.float32, "weights_in"),
-        _array(weights_out, (B, hkv, L_max), torch.float32, "weights_out"),
-        _array(out, (B, h, d), torch.bfloat16, "out"), workspace.data_ptr(), _bytes(workspace))
-    _check(load().diffattn_v2_decode_kv4(C.byref(p), _stream(stream)), "diffattn_v2_decode_kv4")
+        B, h, hkv, d, L_max, d_model, softmax_scale, _array(q, (B, 2 * h, d), bf16, dev, "q"),
+        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, dev, "cache"),
+        _array(seqlens, (B,), torch.int32, dev, "seqlens"), gate_, x_, w_,
+        _array(weights_in, (B, hkv, L_max), f32, dev, "weights_in"),
+        _array(weights_out, (B, hkv, L_max), f32, dev, "weights_out"), _array(out, (B, h, d), bf16, dev, "out"),
+        ws_ptr, ws_bytes)
+    _check((_lib or load()).diffattn_v2_decode_kv4(C.byref(p), raw), "diffattn_v2_decode_kv4")
     return out
 
 
@@ -714,22 +752,24 @@ def diffattn_v2_decode_weighted(q, k_cache, v_cache, *, weights_out, weights_in=
                                 workspace=None, stream=None):
     """diffattn_v2_decode that also gathers the keys' weights into weights_out
     [B, h_kv, L_max] (see diffattn_v2_decode_kv4)."""
+    dev, raw = _device(q, stream)
     B, H2, d = q.shape
-    L_max, hkv = k_cache.shape[1], k_cache.shape[2]
-    h = H2 // 2
-    q_, lens, gate_, x_, w_, out, d_model = _decode_operands(q, seqlens, gate, x, w_lambda, out, B, H2, d)
-    if workspace is None:
-        need = diffattn_v2_decode_weighted_workspace_size(B, h, hkv, d, L_max, num_splits, gate is not None)
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
-    shape = (B, L_max, hkv, d)
+    shape = k_cache.shape
+    L_max, hkv = shape[1], shape[2]
+    h, bf16, f32 = H2 // 2, torch.bfloat16, torch.float32
+    if out is None:
+        out = _new(torch.empty, (B, h, d), bf16, dev, stream)
+    ws, ws_ptr, ws_bytes = _space(workspace, lambda: diffattn_v2_decode_weighted_workspace_size(
+        B, h, hkv, d, L_max, num_splits, gate is not None), dev, stream)
+    gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
     dec = da_v2_decode_params(
-        B, h, hkv, d, L_max, d_model, float(softmax_scale), q_, _rows4(k_cache, shape, torch.bfloat16, "k_cache"),
-        _rows4(v_cache, shape, torch.bfloat16, "v_cache"), lens, gate_, x_, w_,
-        _array(out, (B, h, d), torch.bfloat16, "out"), int(num_splits), workspace.data_ptr(), _bytes(workspace))
-    p = da_v2_decode_weighted_params(
-        dec, _array(weights_in, (B, hkv, L_max), torch.float32, "weights_in"),
-        _array(weights_out, (B, hkv, L_max), torch.float32, "weights_out", optional=False))
-    _check(load().diffattn_v2_decode_weighted(C.byref(p), _stream(stream)), "diffattn_v2_decode_weighted")
+        B, h, hkv, d, L_max, d_model, softmax_scale, _array(q, (B, 2 * h, d), bf16, dev, "q"),
+        _rows4(k_cache, (B, L_max, hkv, d), bf16, dev, "k_cache"), _rows4(v_cache, shape, bf16, dev, "v_cache"),
+        _array(seqlens, (B,), torch.int32, dev, "seqlens"), gate_, x_, w_, _array(out, (B, h, d), bf16, dev, "out"),
+        num_splits, ws_ptr, ws_bytes)
+    p = da_v2_decode_weighted_params(dec, _array(weights_in, (B, hkv, L_max), f32, dev, "weights_in"),
+                                     _array(weights_out, (B, hkv, L_max), f32, dev, "weights_out"))
+    _check((_lib or load()).diffattn_v2_decode_weighted(C.byref(p), raw), "diffattn_v2_decode_weighted")
     return out
 
 
@@ -746,32 +786,31 @@ def diffattn_kv_evict(rows, key_weights, keep, *, sinks=0, recent=0, seqlens=Non
     positions always stay.  Returns dict(key_weights, positions, seqlens) after
     the cut.  Without the _out arguments the given key_weights, positions and
     seqlens are updated in place (a seqlens of None gives a new tensor)."""
-    B, hkv, L_max = key_weights.shape
+    dev, raw = _device(key_weights, stream)
+    B, hkv, L_max = shape = key_weights.shape
     i32, f32 = torch.int32, torch.float32
     if not 1 <= len(rows) <= DIFFATTN_EVICT_MAX_ROWS:
         raise ValueError(f"1 to {DIFFATTN_EVICT_MAX_ROWS} caches expected, got {len(rows)}")
-    weights_out = key_weights if weights_out is None else weights_out
-    positions_out = positions if positions_out is None else positions_out
+    if weights_out is None:
+        weights_out = key_weights
+    if positions_out is None:
+        positions_out = positions
     if seqlens_out is None:
-        seqlens_out = torch.empty((B,), dtype=i32, device=key_weights.device) if seqlens is None else seqlens
+        seqlens_out = _new(torch.empty, (B,), i32, dev, stream) if seqlens is None else seqlens
+    ws, ws_ptr, ws_bytes = _space(workspace, lambda: diffattn_kv_evict_workspace_size(B, hkv, L_max, keep), dev, stream)
     p = da_kv_evict_params(
-        B, hkv, L_max, int(keep), int(sinks), int(recent), _array(seqlens, (B,), i32, "seqlens"),
-        _array(seqlens_out, (B,), i32, "seqlens_out"), _array(key_weights, (B, hkv, L_max), f32, "key_weights"),
-        _array(weights_out, (B, hkv, L_max), f32, "weights_out"),
-        _array(positions, (B, hkv, L_max), i32, "positions"),
-        _array(positions_out, (B, hkv, L_max), i32, "positions_out"),
-        _array(next_position, (B,), i32, "next_position"), len(rows))
+        B, hkv, L_max, keep, sinks, recent, _array(seqlens, (B,), i32, dev, "seqlens"),
+        _array(seqlens_out, (B,), i32, dev, "seqlens_out"), _array(key_weights, shape, f32, dev, "key_weights"),
+        _array(weights_out, shape, f32, dev, "weights_out"), _array(positions, shape, i32, dev, "positions"),
+        _array(positions_out, shape, i32, dev, "positions_out"),
+        _array(next_position, (B,), i32, dev, "next_position"), len(rows))
     for i, r in enumerate(rows):
-        if tuple(r.shape[:3]) != (B, L_max, hkv) or not r.is_cuda:
-            raise ValueError(f"rows[{i}]: CUDA [{B}, {L_max}, {hkv}, width] expected, got {tuple(r.shape)}")
-        t, n = _t4(r), r.element_size()
+        n, width = r.element_size(), r.shape[-1]
+        t = _rows4(r, (B, L_max, hkv, width), r.dtype, dev, f"rows[{i}]")
+        p.row_bytes[i] = width * n
         p.rows[i] = da_t4(t.ptr, t.sb * n, t.sn * n, t.sh * n)
-        p.row_bytes[i] = r.shape[3] * n
-    if workspace is None:
-        need = diffattn_kv_evict_workspace_size(B, hkv, L_max, int(keep))
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=key_weights.device)
-    p.workspace, p.workspace_bytes = workspace.data_ptr(), _bytes(workspace)
-    _check(load().diffattn_kv_evict(C.byref(p), _stream(stream)), "diffattn_kv_evict")
+    p.workspace, p.workspace_bytes = ws_ptr, ws_bytes
+    _check((_lib or load()).diffattn_kv_evict(C.byref(p), raw), "diffattn_kv_evict")
     return dict(key_weights=weights_out, positions=positions_out, seqlens=seqlens_out)
 
 

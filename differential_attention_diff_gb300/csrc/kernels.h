@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "diffattn.h"
+#include "kv4.cuh"
 
 namespace da {
 
@@ -84,7 +85,7 @@ struct Kv4DecodeArgs {
   void* out;          // bf16 [B, h, d]
   float* part_o;      // [grid + B * h_kv, G, d] (numbered as in kv4.cuh)
   float* part_ml;     // [grid + B * h_kv, G, 2]
-  int64_t* prefix;    // [B + 1] chunks of one head before each sequence
+  Kv4Parts* parts;    // [B * h_kv]
   float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
   const float* weights_in;
   float* weights_out;
@@ -95,8 +96,8 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 // ---- gathered key weights from the scores of a decode -------------------------
 struct KeyWeightsArgs {
   int B, h, h_kv, L_max;
-  int splits;             // key-range splits, or the 4-bit decode's grid where prefix is given
-  const int64_t* prefix;  // the 4-bit decode's table, or null
+  int splits;             // key-range splits, where parts is null
+  const Kv4Parts* parts;  // [B * h_kv] of the 4-bit decode, or null
   const int* seqlens;
   const float* gate;
   const float* part_ml;  // [splits, B, 2h, 2], or the 4-bit decode's
@@ -115,6 +116,7 @@ struct EvictArgs {
   int* src;      // [B * h_kv, max_moves]
   int max_moves;
   uint32_t* status;
+  int num_sms;
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
 

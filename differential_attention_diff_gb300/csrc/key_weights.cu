@@ -3,67 +3,128 @@
 //
 // A key's weight needs both maps' normalisers, which exist only after the
 // whole sequence was read.  The decode's split kernel therefore stores its
-// scaled scores t (log2 units, fp32); this kernel merges the splits' maxima
+// scaled scores t (log2 units, fp32); this kernel merges the partials' maxima
 // and sums and takes A = exp2(t - max) / sum from them.  Scores in fewer bits
-// would not do: an error e in t is an error of 0.7 e in the weight.
+// would not do: an error e in t is an error of 0.7 e in the weight.  4 G bytes
+// of scores per key are fewer than its K row's 2 d of bf16, so keeping them
+// beats a second pass over K.
 #include "common.cuh"
 #include "kernels.h"
-#include "kv4.cuh"
 
 namespace da {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxG = 16;
+constexpr int kKeys = 4;  // per thread, all loaded before the first is used
 
+// P pairs of heads; block (1024 keys, KV head, sequence).
+template <int P>
 __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a) {
+  constexpr int G = 2 * P;
+  __shared__ float sm[G], sc[G];
+  cudaGridDependencySynchronize();  // scores and partials
   const int g = blockIdx.y, b = blockIdx.z;
-  const int H2 = 2 * a.h, G = H2 / a.h_kv;
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
   if (L < 1 || L > a.L_max) return;  // recorded by the split kernel
-  if (static_cast<int64_t>(blockIdx.x) * kThreads >= L) return;
-  __shared__ float sm[kMaxG], sc[kMaxG];
-  if (threadIdx.x < G) {
-    const int j = g * G + threadIdx.x;
-    // this head's partials: one per split, or the parts of a line of chunks
-    int64_t first = static_cast<int64_t>(b) * a.h_kv + g, step = static_cast<int64_t>(a.B) * a.h_kv;
+  const int key0 = blockIdx.x * (kThreads * kKeys);
+  if (key0 >= L) return;
+  const int64_t unit = static_cast<int64_t>(b) * a.h_kv + g;
+  const int64_t base = unit * a.L_max;
+  // loads first: they do not wait for the normalisers
+  float2 t[kKeys][P];
+  float w[kKeys];
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const int key = key0 + k * kThreads + threadIdx.x;
+    if (key < L) {
+      const float* s = a.scores + (base + key) * G;
+      if constexpr (P % 2 == 0) {
+#pragma unroll
+        for (int p = 0; p < P; p += 2) {
+          const float4 v = reinterpret_cast<const float4*>(s)[p / 2];
+          t[k][p] = make_float2(v.x, v.y);
+          t[k][p + 1] = make_float2(v.z, v.w);
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) t[k][p] = reinterpret_cast<const float2*>(s)[p];
+      }
+      w[k] = a.weights_in ? a.weights_in[base + key] : 0.f;
+    }
+  }
+  // a warp per head, a lane per partial
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < G; r += kThreads / 32) {
+    int64_t first = unit, step = static_cast<int64_t>(a.B) * a.h_kv;
     int count = a.splits;
-    if (a.prefix) {
-      const Kv4Parts s = kv4_head_parts(a.prefix, a.B, a.h_kv, b, g, a.splits);
-      first = s.first;
-      count = s.count;
+    if (a.parts) {
+      first = a.parts[unit].first;
+      count = a.parts[unit].last - a.parts[unit].first + 1;
       step = 1;
     }
     float mt = -INFINITY, lt = 0.f;
-    for (int i = 0; i < count; ++i) mt = fmaxf(mt, a.part_ml[((first + i * step) * G + threadIdx.x) * 2]);
-    const float base = mt == -INFINITY ? 0.f : mt;
-    for (int i = 0; i < count; ++i) {
-      const float* ml = a.part_ml + ((first + i * step) * G + threadIdx.x) * 2;
-      lt += ml[1] * exp2f(ml[0] - base);
+    for (int i = lane; i < count; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + ((first + i * step) * G + r) * 2);
+      const float top = fmaxf(mt, ml.x), nb = top == -INFINITY ? 0.f : top;
+      lt = lt * exp2f(mt - nb) + ml.y * exp2f(ml.x - nb);
+      mt = top;
     }
-    float c = lt == 0.f ? 0.f : 1.f / lt;
-    if (threadIdx.x & 1) c *= a.gate[static_cast<int64_t>(b) * a.h + j / 2];
-    sm[threadIdx.x] = base;
-    sc[threadIdx.x] = c;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, mt, o), l2 = __shfl_xor_sync(0xffffffffu, lt, o);
+      const float top = fmaxf(mt, m2), nb = top == -INFINITY ? 0.f : top;
+      lt = lt * exp2f(mt - nb) + l2 * exp2f(m2 - nb);
+      mt = top;
+    }
+    if (lane == 0) {
+      float c = lt == 0.f ? 0.f : 1.f / lt;
+      if (r & 1) c *= a.gate[static_cast<int64_t>(b) * a.h + (g * G + r) / 2];
+      sm[r] = mt == -INFINITY ? 0.f : mt;
+      sc[r] = c;
+    }
   }
   __syncthreads();
-  const int key = blockIdx.x * kThreads + threadIdx.x;
-  if (key >= L) return;
-  const int64_t at = (static_cast<int64_t>(b) * a.h_kv + g) * a.L_max + key;
-  const float* t = a.scores + at * G;
-  float w = a.weights_in ? a.weights_in[at] : 0.f;
-  // products rounded before they are subtracted: equal maps cancel to zero
-  for (int r = 0; r < G; r += 2)
-    w += fabsf(__fsub_rn(__fmul_rn(exp2f(t[r] - sm[r]), sc[r]), __fmul_rn(exp2f(t[r + 1] - sm[r + 1]), sc[r + 1])));
-  a.weights_out[at] = w;
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const int key = key0 + k * kThreads + threadIdx.x;
+    if (key >= L) continue;
+    // products rounded before they are subtracted: equal maps cancel to zero
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      w[k] += fabsf(__fsub_rn(__fmul_rn(exp2f(t[k][p].x - sm[2 * p]), sc[2 * p]),
+                              __fmul_rn(exp2f(t[k][p].y - sm[2 * p + 1]), sc[2 * p + 1])));
+    a.weights_out[base + key] = w[k];
+  }
+}
+
+template <int P>
+cudaError_t launch_pairs(const KeyWeightsArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3((a.L_max + kThreads * kKeys - 1) / (kThreads * kKeys), a.h_kv, a.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<P>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t s) {
-  const dim3 grid((a.L_max + kThreads - 1) / kThreads, a.h_kv, a.B);
-  key_weights_kernel<<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  switch (a.h / a.h_kv) {  // pairs per KV head
+    case 1: return launch_pairs<1>(a, s);
+    case 2: return launch_pairs<2>(a, s);
+    case 3: return launch_pairs<3>(a, s);
+    case 4: return launch_pairs<4>(a, s);
+    case 5: return launch_pairs<5>(a, s);
+    case 6: return launch_pairs<6>(a, s);
+    case 7: return launch_pairs<7>(a, s);
+    case 8: return launch_pairs<8>(a, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace da

@@ -16,25 +16,18 @@ constexpr int kKv4ChunkKeys = 32;
 // A CTA takes at least this many chunks: below it the parts cost more to
 // merge than they save.
 constexpr int kKv4MinPart = 8;
+// CTAs at most (one per SM), and so partials of one head.
+constexpr int kKv4MaxGrid = 512;
 
 __host__ __device__ inline int64_t kv4_parts(int64_t total, int64_t grid) {
   const int64_t most = (total + kKv4MinPart - 1) / kKv4MinPart;
   return most < grid ? most : grid;
 }
 
-// The partials of head (b, g): numbers first .. first + count - 1.
+// The numbers of a head's first and last partial, left by the CTAs that take
+// its first and its last chunk (a head without chunks has no entry).
 struct Kv4Parts {
-  int64_t first;
-  int count;
+  int first, last;
 };
-__device__ inline Kv4Parts kv4_head_parts(const int64_t* prefix, int B, int h_kv, int b, int g, int grid) {
-  const int64_t total = prefix[B] * h_kv, n = prefix[b + 1] - prefix[b];
-  if (n == 0) return {0, 0};
-  const int64_t parts = kv4_parts(total, grid);
-  const int64_t from = prefix[b] * h_kv + g * n;
-  // chunk x is in the last part that starts at or before it
-  const int64_t c0 = ((from + 1) * parts - 1) / total, c1 = ((from + n) * parts - 1) / total;
-  return {c0 + static_cast<int64_t>(b) * h_kv + g, static_cast<int>(c1 - c0 + 1)};
-}
 
 }  // namespace da

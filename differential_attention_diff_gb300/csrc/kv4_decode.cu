@@ -39,7 +39,6 @@
 #include <cuda_fp16.h>
 
 #include "kernels.h"
-#include "kv4.cuh"
 #include "tma.cuh"
 
 namespace da {
@@ -127,7 +126,7 @@ __device__ __forceinline__ int seq_chunks(const Kv4DecodeArgs& a, int b) {
 // A position on the line of chunks: the head u = b * h_kv + g, and this
 // warp's next chunk of it within [chunk, end).
 struct Cursor {
-  int b, g, chunk, end;
+  int b, g, begin, chunk, end;
   int L;         // the sequence's length
   int64_t left;  // chunks of this CTA's part behind this head
 };
@@ -145,12 +144,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   const int gr = lane >> 2, tq = lane & 3;
   const int H2 = 2 * a.h, G = H2 / a.h_kv;
 
+  cudaTriggerProgrammaticLaunchCompletion();  // the merge may take its place; it waits for this kernel's end
   if (tid < kW * kS) mbar_init(smem_u32(&bars[tid]), 1);
   fence_mbar_init();
 
   // ---- this CTA's part of the line ----
-  // prefix[b] = chunks of one head over the sequences before b; every CTA
-  // sums the lengths itself, the first also leaves the table for the merge
+  // every CTA sums the lengths itself
   int64_t carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
     const int b = b0 + tid;
@@ -158,24 +157,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     if (blockIdx.x == 0 && b < a.B && n == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
     int64_t x = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) scan[warp] = x;
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) scan[warp] = x;
     __syncthreads();
-    int64_t before = carry;
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += scan[w];
-      carry += scan[w];
-    }
-    if (b < a.B) {
-      if (blockIdx.x == 0) a.prefix[b] = before + x - n;
-    }
+    for (int w = 0; w < kW; ++w) carry += scan[w];
     __syncthreads();
   }
   const int64_t total = carry * a.h_kv;
-  if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = carry;
   const int64_t parts = kv4_parts(total, gridDim.x);
   if (blockIdx.x >= parts || total == 0) return;
   const int64_t first = blockIdx.x * total / parts, last = (blockIdx.x + 1) * total / parts;
@@ -214,6 +202,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     const int64_t take = min(static_cast<int64_t>(n - begin), c.left);
     c.end = begin + static_cast<int>(take);
     c.left -= take;
+    c.begin = begin;
     c.chunk = begin + warp;
   };
   auto next_head = [&](Cursor& c) {  // c.left > 0: another head with chunks follows
@@ -542,7 +531,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     // ---- the head's end: sum the warps' partials ----
     // O register i of lane l goes to word i * kRegPitch + l of the slot read
     // last; the copies in flight go to the others
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) + unit) * G;
+    const int number = static_cast<int>(blockIdx.x + unit);
+    const int64_t row = static_cast<int64_t>(number) * G;
+    if (tid == 0) {
+      if (at.begin == 0) a.parts[unit].first = number;
+      if (at.end * kChunk >= at.L) a.parts[unit].last = number;
+    }
     float* park = reinterpret_cast<float*>(smem + (warp * kS + (taken + kS - 1) % kS) * C::kSlot);
     __shared__ int park_slot[kW];
     if (lane == 0) park_slot[warp] = (taken + kS - 1) % kS;
@@ -614,28 +608,79 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     for (; taken < issued; ++taken) mbar_wait(bar0 + (taken % kS) * 8, (taken / kS) & 1, nullptr, 0);
 }
 
-// One output head's parts merged, even - gate * odd.  Grid (h, B).
-__global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4DecodeArgs a, int grid) {
-  const int p = blockIdx.x, b = blockIdx.y, f = threadIdx.x;
+constexpr int kMergeThreads = 512;
+
+// One output head's parts merged, even - gate * odd.  Grid (h, B).  A warp
+// per head takes the maximum and the sum over the parts and leaves a factor
+// per part; then 256 threads per head add up the parts, 256 / D at a time.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeArgs a) {
+  constexpr int kWays = kMergeThreads / 2 / D;
+  __shared__ float factor[2][kKv4MaxGrid];
+  __shared__ float sums[2][kWays][D];
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();  // the parts
+  const int p = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = 2 * a.h / a.h_kv, g = 2 * p / G, r = 2 * p % G;
-  const Kv4Parts s = kv4_head_parts(a.prefix, a.B, a.h_kv, b, g, grid);
-  float res[2];
-  for (int e = 0; e < 2; ++e) {
-    float mt = -INFINITY, lt = 0.f, ot = 0.f;
-    for (int i = 0; i < s.count; ++i) mt = fmaxf(mt, a.part_ml[((s.first + i) * G + r + e) * 2]);
-    const float base = mt == -INFINITY ? 0.f : mt;
-    for (int i = 0; i < s.count; ++i) {
-      const int64_t at = (s.first + i) * G + r + e;
-      const float c = exp2f(a.part_ml[at * 2] - base);
-      lt += a.part_ml[at * 2 + 1] * c;
-      ot += a.part_o[at * a.d + f] * c;
-    }
-    // a sum of 0 is an empty sequence or keys that are all -inf: zeros, as in decode.cu; NaN stays
-    res[e] = lt == 0.f ? 0.f : ot / lt;
+  const int L = a.seqlens ? a.seqlens[b] : a.L_max;
+  const bool bad = L < 1 || L > a.L_max;  // recorded by the split kernel
+  int first = 0, count = 0;
+  if (!bad) {
+    const Kv4Parts s = a.parts[static_cast<int64_t>(b) * a.h_kv + g];
+    first = s.first;
+    count = s.last - s.first + 1;
   }
-  const int64_t at = static_cast<int64_t>(b) * a.h + p;
-  static_cast<__nv_bfloat16*>(a.out)[at * a.d + f] =
-      __float2bfloat16_rn(__fsub_rn(res[0], __fmul_rn(a.gate[at], res[1])));
+  if (warp < 2) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + static_cast<int64_t>(first) * G + r + warp;
+    float mt = -INFINITY, lt = 0.f;
+    for (int i = lane; i < count; i += 32) mt = fmaxf(mt, ml[static_cast<int64_t>(i) * G].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    const float base = mt == -INFINITY ? 0.f : mt;
+    for (int i = lane; i < count; i += 32) {
+      const float2 v = ml[static_cast<int64_t>(i) * G];
+      const float c = exp2f(v.x - base);
+      lt += v.y * c;
+      factor[warp][i] = c;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    // a sum of 0 is an empty sequence or keys that are all -inf: zeros, as in decode.cu; NaN stays
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    for (int i = lane; i < count; i += 32) factor[warp][i] *= inv;
+  }
+  __syncthreads();
+  const int e = tid / (kWays * D), way = tid / D % kWays, f = tid % D;
+  const float* po = a.part_o + (static_cast<int64_t>(first) * G + r + e) * D + f;
+  float x = 0.f;
+#pragma unroll 4
+  for (int i = way; i < count; i += kWays) x = fmaf(po[static_cast<int64_t>(i) * G * D], factor[e][i], x);
+  sums[e][way][f] = x;
+  __syncthreads();
+  if (tid < D) {
+    float res[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int w = 0; w < kWays; ++w) res[k] += sums[k][w][tid];
+    const int64_t at = static_cast<int64_t>(b) * a.h + p;
+    static_cast<__nv_bfloat16*>(a.out)[at * D + tid] =
+        __float2bfloat16_rn(__fsub_rn(res[0], __fmul_rn(a.gate[at], res[1])));
+  }
+}
+
+template <int D>
+cudaError_t launch_merge(const Kv4DecodeArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(a.h, a.B);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D>, a);
 }
 
 template <int D, int NT, bool kScores>
@@ -663,10 +708,9 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
     e = two ? (sc ? launch_split<64, 2, true>(a, s) : launch_split<64, 2, false>(a, s))
             : (sc ? launch_split<64, 1, true>(a, s) : launch_split<64, 1, false>(a, s));
   if (e != cudaSuccess) return e;
-  kv4_merge_kernel<<<dim3(a.h, a.B), a.d, 0, s>>>(a, a.grid);
-  e = cudaGetLastError();
+  e = a.d == 128 ? launch_merge<128>(a, s) : launch_merge<64>(a, s);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
-  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, a.grid, a.prefix, a.seqlens, a.gate, a.part_ml, a.scores,
+  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, 0, a.parts, a.seqlens, a.gate, a.part_ml, a.scores,
                          a.weights_in, a.weights_out};
   return launch_key_weights(w, s);
 }

@@ -7,7 +7,6 @@
 
 #include "diffattn.h"
 #include "kernels.h"
-#include "kv4.cuh"
 
 namespace {
 
@@ -35,8 +34,8 @@ da_status check_rows(int B, int N, int h_kv, int d, int L_max, const da_t4& k, c
     return DA_OK;
   }
   if (!ok_t4(k, 8) || !ok_t4(v, 8) || !ok_t4(cache, 16)) return DA_ERR_INVALID_ARG;
-  // one launch covers at most 2^31 - 1 blocks of 16 key/value rows
-  if (static_cast<double>(B) * N * h_kv >= 8.0 * 2147483647.0) return DA_ERR_UNSUPPORTED;
+  // a sequence's rows are counted in 32 bits
+  if (static_cast<int64_t>(N) * h_kv > (1 << 29)) return DA_ERR_UNSUPPORTED;
   return DA_OK;
 }
 
@@ -47,18 +46,18 @@ int decode_grid(int B, int h_kv, int L_max) {
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
   const int64_t chunks = (static_cast<int64_t>(L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys;
-  return static_cast<int>(da::kv4_parts(chunks * h_kv * B, sms));
+  return static_cast<int>(da::kv4_parts(chunks * h_kv * B, sms < da::kKv4MaxGrid ? sms : da::kKv4MaxGrid));
 }
 
 struct DecodeSpace {
-  size_t ml, prefix, scores, gate, total;  // offsets; the partial O rows are at 0
+  size_t ml, parts, scores, gate, total;  // offsets; the partial O rows are at 0
 };
 DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
   const size_t rows = (decode_grid(B, h_kv, L_max) + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
   DecodeSpace w;
   w.ml = align256(rows * d * sizeof(float));
-  w.prefix = w.ml + align256(rows * 2 * sizeof(float));
-  w.scores = w.prefix + align256((static_cast<size_t>(B) + 1) * sizeof(int64_t));
+  w.parts = w.ml + align256(rows * 2 * sizeof(float));
+  w.scores = w.parts + align256(static_cast<size_t>(B) * h_kv * sizeof(da::Kv4Parts));
   w.gate = w.scores + (weights ? align256(static_cast<size_t>(B) * 2 * h * L_max * sizeof(float)) : 0);
   w.total = w.gate + (gate_given ? 0 : align256(static_cast<size_t>(B) * h * sizeof(float)));
   return w;
@@ -163,7 +162,7 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
   const da::Kv4DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, decode_grid(p->B, p->h_kv, p->L_max),
                             scale * kLog2e, p->q, p->cache, p->seqlens, gate, p->out,
                             reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.ml),
-                            reinterpret_cast<int64_t*>(ws + w.prefix),
+                            reinterpret_cast<da::Kv4Parts*>(ws + w.parts),
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
                             p->weights_in, p->weights_out, status};
   return cuda_status(da::launch_kv4_decode(a, s));
@@ -189,8 +188,10 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
     if (!aligned(q, 4)) return DA_ERR_INVALID_ARG;
   for (int k = 0; k < p->n_rows; ++k)
     if (!ok_t4(p->rows[k], 16) || p->row_bytes[k] <= 0 || p->row_bytes[k] % 16) return DA_ERR_INVALID_ARG;
-  // one CTA per head to select, up to 64 to move its rows
-  if (static_cast<int64_t>(p->B) * p->h_kv > 2147483647 / 64) return DA_ERR_UNSUPPORTED;
+  // heads are a grid dimension, up to 8 CTAs each; a head's 16-byte pieces are counted in 32 bits
+  if (static_cast<int64_t>(p->B) * p->h_kv > (1 << 28)) return DA_ERR_UNSUPPORTED;
+  for (int k = 0; k < p->n_rows; ++k)
+    if (static_cast<int64_t>(p->L_max) * (p->row_bytes[k] / 16) > (1 << 30)) return DA_ERR_UNSUPPORTED;
   const EvictSpace w = evict_space(p->B, p->h_kv, p->L_max, p->keep);
   if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   uint32_t* status;
@@ -198,7 +199,7 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
   if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   const da::EvictArgs a{*p, reinterpret_cast<int*>(ws), reinterpret_cast<int*>(ws + w.len),
-                        reinterpret_cast<int*>(ws + w.dst), reinterpret_cast<int*>(ws + w.src), w.max_moves, status};
+                        reinterpret_cast<int*>(ws + w.dst), reinterpret_cast<int*>(ws + w.src), w.max_moves, status, sms};
   return cuda_status(da::launch_kv_evict(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -122,7 +122,7 @@ def test_append_and_read_argument_checks(lib):
             assert f(_with(p, **{n: bd.da_t4(FAKE, 64, 60, 64)}), None) == bd.DA_ERR_INVALID_ARG
             assert f(_with(p, **{n: bd.da_t4(FAKE + 2, 64, 64, 64)}), None) == bd.DA_ERR_INVALID_ARG
         assert f(_with(p, d=96), None) == bd.DA_ERR_UNSUPPORTED
-        assert f(_with(p, B=1 << 20, N=1 << 20), None) == bd.DA_ERR_UNSUPPORTED  # more blocks than a launch has
+        assert f(_with(p, N=1 << 28), None) == bd.DA_ERR_UNSUPPORTED  # more rows than 32 bits count
         assert f(_with(p, B=0), None) == bd.DA_OK
         assert f(_with(p, N=0), None) == bd.DA_OK
     for n in ("key_weights", "positions", "first_position"):
