@@ -83,8 +83,8 @@ struct Kv4DecodeArgs {
   const int* seqlens;
   const float* gate;  // [B, h]
   void* out;          // bf16 [B, h, d]
-  float* part_o;      // [grid + B * h_kv, G, d] (numbered as in kv4.cuh)
-  float* part_ml;     // [grid + B * h_kv, G, 2]
+  float* part_o;      // [grid * warps + B * h_kv, G, d] (numbered as in kv4.cuh)
+  float* part_ml;     // [grid * warps + B * h_kv, G, 2]
   Kv4Parts* parts;    // [B * h_kv]
   float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
   const float* weights_in;

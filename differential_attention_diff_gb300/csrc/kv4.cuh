@@ -2,9 +2,9 @@
 // merge the parts.
 //
 // The work is a line of 32-key chunks, head after head (u = b * h_kv + g; a
-// head of sequence b has ceil(L_b / 32) of them).  CTA c of `parts` takes
-// chunks [floor(c T / parts), floor((c + 1) T / parts)) of the T in all, and
-// writes its part of head u to partial c + u: heads and CTAs both only go up
+// head of sequence b has ceil(L_b / 32) of them).  Warp w of `parts` takes
+// chunks [floor(w T / parts), floor((w + 1) T / parts)) of the T in all, and
+// writes its part of head u to partial w + u: heads and warps both only go up
 // along the line, so no two parts share a number.
 #pragma once
 
@@ -13,18 +13,19 @@
 namespace da {
 
 constexpr int kKv4ChunkKeys = 32;
-// A CTA takes at least this many chunks: below it the parts cost more to
+// A warp takes at least this many chunks: below it the parts cost more to
 // merge than they save.
-constexpr int kKv4MinPart = 8;
-// CTAs at most (one per SM), and so partials of one head.
-constexpr int kKv4MaxGrid = 512;
+constexpr int kKv4MinPart = 2;
+constexpr int kKv4MaxGrid = 256;   // CTAs at most (one per SM)
+constexpr int kKv4MaxWarps = 16;   // of each
+constexpr int kKv4MaxParts = kKv4MaxGrid * kKv4MaxWarps;  // and so partials of one head
 
-__host__ __device__ inline int64_t kv4_parts(int64_t total, int64_t grid) {
+__host__ __device__ inline int64_t kv4_parts(int64_t total, int64_t warps) {
   const int64_t most = (total + kKv4MinPart - 1) / kKv4MinPart;
-  return most < grid ? most : grid;
+  return most < warps ? most : warps;
 }
 
-// The numbers of a head's first and last partial, left by the CTAs that take
+// The numbers of a head's first and last partial, left by the warps that take
 // its first and its last chunk (a head without chunks has no entry).
 struct Kv4Parts {
   int first, last;

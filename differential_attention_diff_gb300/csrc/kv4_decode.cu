@@ -28,13 +28,14 @@
 // Sums of p, of p m and the score corrections are fp32.
 //
 // Schedule: the batch's work is one line of 32-key chunks in (sequence, KV
-// head) order, cut into equal parts, one per CTA (one CTA per SM), so ragged
-// lengths balance exactly; a CTA's warps take chunks in turn, each from a
-// ring of its own that it fills with bulk copies (one per chunk where a
-// head's records are contiguous, else one per record) and its own barriers.
-// The warps meet only where a head ends: each puts its partial O into the
-// ring slot it last read and all sum them.  A second kernel merges the parts
-// of each head and applies the gate.
+// head) order, cut into equal parts, one per warp (16 warps on each SM, 8
+// where two head tiles need the registers), so ragged lengths balance
+// exactly.  A warp streams its part through a ring of its own and shares
+// nothing with the others: where a head ends it writes its partial (max, sum,
+// O) and goes on to the next, and no block-wide barrier stops the loads.
+// (Warps that shared a head and summed their partials in shared memory took
+// 63 us for 64 x 2048 keys, see the note at the launch.)  A second kernel
+// merges the parts of each head and applies the gate.
 #include "common.cuh"
 #include <cuda_fp16.h>
 
@@ -58,7 +59,6 @@ struct Cfg {
   static constexpr int kWords = D / 64;     // 4-byte code words per lane, group and key row (K side)
   static constexpr int kTiles = D / 16;     // 16-feature tiles of O^T
   static constexpr int kGroupTiles = kTiles / 2;
-  static constexpr int kRegPitch = 36;      // floats between O registers in a slot: spreads the banks
 };
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -117,18 +117,23 @@ __device__ __forceinline__ float exponent_scale(float x, int target) {
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
+// 16-byte copies that a barrier counts: each lane's arrival comes when its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Chunks of one head of sequence b: 0 for a bad length.
 __device__ __forceinline__ int seq_chunks(const Kv4DecodeArgs& a, int b) {
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
   return L < 1 || L > a.L_max ? 0 : (L + kChunk - 1) / kChunk;
 }
 
-// A position on the line of chunks: the head u = b * h_kv + g, and this
-// warp's next chunk of it within [chunk, end).
+// A warp's place on the line of chunks: the next chunk of head b * h_kv + g,
+// and where its part of that head ends.
 struct Cursor {
-  int b, g, begin, chunk, end;
+  int b, g, chunk, end;
   int L;         // the sequence's length
-  int64_t left;  // chunks of this CTA's part behind this head
+  int left;      // chunks of this warp's part behind this head (its records fit the memory: 32 bits do)
 };
 
 template <int D, int NT, bool kScores>
@@ -137,73 +142,81 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   constexpr int kW = C::kWarps, kS = C::kStages, kRec = C::kRec, kWords = C::kWords, kGT = C::kGroupTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kW * kS];
-  __shared__ int64_t scan[kW];
-  __shared__ int64_t found[4];
-  __shared__ float sm_m[kW][8 * NT], sm_l[kW][8 * NT];
+  __shared__ int64_t warp_sum[kW];
+  __shared__ int64_t ends[C::kThreads];  // of a tile of sequences: chunks of one head up to each one's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tq = lane & 3;
   const int H2 = 2 * a.h, G = H2 / a.h_kv;
+  const bool dense = a.cache.sn == kRec;
 
   cudaTriggerProgrammaticLaunchCompletion();  // the merge may take its place; it waits for this kernel's end
-  if (tid < kW * kS) mbar_init(smem_u32(&bars[tid]), 1);
+  if (tid < kW * kS) mbar_init(smem_u32(&bars[tid]), dense ? 1 : 32);
   fence_mbar_init();
 
-  // ---- this CTA's part of the line ----
-  // every CTA sums the lengths itself
-  int64_t carry = 0;
-  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+  // ---- this warp's part of the line ----
+  // sequences b0 .. b0 + kThreads - 1 into `ends`; returns the sum up to their end
+  auto sum_tile = [&](int b0, int64_t carry) {
     const int b = b0 + tid;
-    const int n = b < a.B ? seq_chunks(a, b) : 0;
-    if (blockIdx.x == 0 && b < a.B && n == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
-    int64_t x = n;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) scan[warp] = x;
-    __syncthreads();
-    for (int w = 0; w < kW; ++w) carry += scan[w];
-    __syncthreads();
-  }
-  const int64_t total = carry * a.h_kv;
-  const int64_t parts = kv4_parts(total, gridDim.x);
-  if (blockIdx.x >= parts || total == 0) return;
-  const int64_t first = blockIdx.x * total / parts, last = (blockIdx.x + 1) * total / parts;
-  // the sequence that holds chunk `first`
-  carry = 0;
-  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    const int b = b0 + tid;
-    const int n = b < a.B ? seq_chunks(a, b) : 0;
-    int64_t x = n;
+    int64_t x = b < a.B ? seq_chunks(a, b) : 0;
+    if (blockIdx.x == 0 && b < a.B && x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) scan[warp] = x;
+    if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    int64_t before = carry;
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += scan[w];
-      carry += scan[w];
-    }
-    const int64_t from = (before + x - n) * a.h_kv;
-    if (n > 0 && first >= from && first < from + static_cast<int64_t>(n) * a.h_kv) {
-      found[0] = b;
-      found[1] = (first - from) / n;
-      found[2] = (first - from) % n;
-    }
+    for (int w = 0; w < warp; ++w) x += warp_sum[w];
+    x += carry;
+    ends[tid] = x;
     __syncthreads();
-    if (carry * a.h_kv > first) break;  // uniform: found in this tile
+    return ends[C::kThreads - 1];
+  };
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+    if (b0) __syncthreads();
+    sum = sum_tile(b0, sum);
   }
-
+  const int64_t total = sum * a.h_kv;
+  const int64_t parts = kv4_parts(total, static_cast<int64_t>(gridDim.x) * kW);
+  // neighbouring parts on different SMs: few parts then have an SM each
+  const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const bool works = me < parts;
+  const int64_t first = works ? me * total / parts : 0, last = works ? (me + 1) * total / parts : 0;
   Cursor at;
-  auto enter = [&](Cursor& c, int begin) {  // chunks [begin, ..) of head (c.b, c.g), as far as the part goes
+  at.b = -1;
+  int64_t from = 0;  // chunks before the tile, of one head
+  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+    if (a.B > C::kThreads) {  // more than one tile: the last one is in `ends` now
+      __syncthreads();
+      sum_tile(b0, from);
+    }
+    if (works && at.b < 0 && first < ends[C::kThreads - 1] * a.h_kv) {
+      // the sequence whose end is the first above `first`
+      for (int i = 0; at.b < 0; i += 32) {
+        const unsigned hit = __ballot_sync(0xffffffffu, ends[i + lane] * a.h_kv > first);
+        if (hit) {
+          const int k = i + __ffs(hit) - 1;
+          at.b = b0 + k;
+          const int64_t before = k ? ends[k - 1] : from;
+          const int n = static_cast<int>(ends[k] - before);
+          const int64_t in = first - before * a.h_kv;
+          at.g = static_cast<int>(in / n);
+          at.chunk = static_cast<int>(in - static_cast<int64_t>(at.g) * n);
+        }
+      }
+    }
+    from = ends[C::kThreads - 1];
+  }
+  if (!works) return;
+
+  auto enter = [&](Cursor& c, int begin) {  // chunks begin .. of head (c.b, c.g), as far as the part goes
     c.L = a.seqlens ? a.seqlens[c.b] : a.L_max;
     const int n = (c.L + kChunk - 1) / kChunk;
-    const int64_t take = min(static_cast<int64_t>(n - begin), c.left);
-    c.end = begin + static_cast<int>(take);
+    const int take = min(n - begin, c.left);
+    c.end = begin + take;
     c.left -= take;
-    c.begin = begin;
-    c.chunk = begin + warp;
+    c.chunk = begin;
   };
   auto next_head = [&](Cursor& c) {  // c.left > 0: another head with chunks follows
     do {
@@ -211,22 +224,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     } while (seq_chunks(a, c.b) == 0);
     enter(c, 0);
   };
-  at.b = static_cast<int>(found[0]);
-  at.g = static_cast<int>(found[1]);
-  at.left = last - first;
-  enter(at, static_cast<int>(found[2]));
+  at.left = static_cast<int>(last - first);
+  enter(at, at.chunk);
 
   const uint32_t ring = smem_u32(smem) + warp * kS * C::kSlot;
   const uint32_t bar0 = smem_u32(&bars[warp * kS]);
   const uint8_t* cache = static_cast<const uint8_t*>(a.cache.ptr);
-  const bool dense = a.cache.sn == kRec;
   bool dead = false;  // a wait ran out: nothing more is issued or read
 
   // fill the ring's next slot with the chunk that `ahead` is at
   Cursor ahead = at;
   int issued = 0, taken = 0;
   auto issue = [&]() {
-    while (ahead.chunk >= ahead.end) {
+    if (ahead.chunk >= ahead.end) {
       if (ahead.left == 0) return;
       next_head(ahead);
     }
@@ -235,15 +245,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     const int slot = issued % kS;
     const uint32_t dst = ring + slot * C::kSlot, bar = bar0 + slot * 8;
     const uint8_t* src = cache + ahead.b * a.cache.sb + ahead.g * a.cache.sh + key0 * a.cache.sn;
-    if (lane == 0) mbar_arrive_expect_tx(bar, n * kRec);
-    if (dense) {
-      if (lane == 0) bulk_load(dst, src, n * kRec, bar);
-    } else {
-      __syncwarp();
-      if (lane < n) bulk_load(dst + lane * kRec, src + lane * a.cache.sn, kRec, bar);
+    if (dense) {  // one bulk copy
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, n * kRec);
+        bulk_load(dst, src, n * kRec, bar);
+      }
+    } else {  // records apart: a bulk copy each measured slower than 16 bytes per lane
+      constexpr int kPieces = kRec / 16;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int x = i * 32 + lane, r = x / kPieces, c = x % kPieces;
+        if (r < n) cp_async_16(dst + x * 16, src + r * a.cache.sn + c * 16, 16);
+      }
+      cp_async_arrive(bar);
     }
     ++issued;
-    ahead.chunk += kW;
+    ++ahead.chunk;
   };
 #pragma unroll 1
   for (int i = 0; i < kS - 1; ++i) issue();
@@ -328,7 +345,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       }
     }
 
-    for (; at.chunk < at.end; at.chunk += kW) {
+    const int begin = at.chunk;
+    for (; at.chunk < at.end; ++at.chunk) {
       issue();  // into the slot read last
       const int slot = taken % kS;
       if (!dead && !mbar_wait(bar0 + slot * 8, (taken / kS) & 1, a.status, 0x4B04)) dead = true;
@@ -528,20 +546,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       __syncwarp();  // the slot is read before it is filled again
     }
 
-    // ---- the head's end: sum the warps' partials ----
-    // O register i of lane l goes to word i * kRegPitch + l of the slot read
-    // last; the copies in flight go to the others
-    const int number = static_cast<int>(blockIdx.x + unit);
-    const int64_t row = static_cast<int64_t>(number) * G;
-    if (tid == 0) {
-      if (at.begin == 0) a.parts[unit].first = number;
-      if (at.end * kChunk >= at.L) a.parts[unit].last = number;
+    // ---- the head's end: this warp's partial ----
+    const int64_t number = me + unit, row = number * G;
+    if (lane == 0) {
+      if (begin == 0) a.parts[unit].first = static_cast<int>(number);
+      if (at.end * kChunk >= at.L) a.parts[unit].last = static_cast<int>(number);
     }
-    float* park = reinterpret_cast<float*>(smem + (warp * kS + (taken + kS - 1) % kS) * C::kSlot);
-    __shared__ int park_slot[kW];
-    if (lane == 0) park_slot[warp] = (taken + kS - 1) % kS;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float lt = l[t][e], m0 = mn[t][0][e], m1 = mn[t][1][e];
@@ -551,55 +563,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
           m0 += __shfl_xor_sync(0xffffffffu, m0, x);
           m1 += __shfl_xor_sync(0xffffffffu, m1, x);
         }
+        const int head = t * 8 + 2 * tq + e;
+        if (head >= G) continue;
         const float f = 1.f / vs[t][e];
+        float* po = a.part_o + (row + head) * D;
+        if (gr == 0) *reinterpret_cast<float2*>(a.part_ml + (row + head) * 2) = make_float2(mx[t][e], lt);
+        // four neighbouring features: rows gr and gr + 8 of two tiles.  2^24
+        // and f are applied apart: their product may overflow
 #pragma unroll
-        for (int i = 0; i < C::kTiles; ++i) {
-          const float fi = (i & 1) ? 0x1p20f : 0x1p24f;  // apart from f: their product may overflow
-          const float mi = i < kGT ? m0 : m1;
-          park[(i * 4 + e) * C::kRegPitch + lane] = fmaf(o[t][i][e] * fi, f, mi);
-          park[(i * 4 + 2 + e) * C::kRegPitch + lane] = fmaf(o[t][i][2 + e] * fi, f, mi);
-        }
-        if (gr == 0) {
-          sm_m[warp][t * 8 + 2 * tq + e] = mx[t][e];
-          sm_l[warp][t * 8 + 2 * tq + e] = lt;
-        }
+        for (int g2 = 0; g2 < 2; ++g2)
+#pragma unroll
+          for (int hw = 0; hw < kWords; ++hw) {
+            const float* x = o[t][g2 * kGT + hw * 2];
+            const float* y = o[t][g2 * kGT + hw * 2 + 1];
+            const float m = g2 ? m1 : m0;
+            *reinterpret_cast<float4*>(po + g2 * (D / 2) + gr * (D / 16) + hw * 4) =
+                make_float4(fmaf(x[e] * 0x1p24f, f, m), fmaf(y[e] * 0x1p20f, f, m),
+                            fmaf(x[2 + e] * 0x1p24f, f, m), fmaf(y[2 + e] * 0x1p20f, f, m));
+          }
       }
-      __syncthreads();
-      // item (lane, head parity, pair of neighbouring features)
-      constexpr int kItems = 32 * 2 * (D / 16);
-      for (int x = tid; x < kItems; x += C::kThreads) {
-        const int fp = x % (D / 16);             // pair of features within the lane's D/8
-        const int ln = (x / (D / 16)) & 31, e = x / (D / 16) / 32;
-        const int head = 2 * (ln & 3) + e;
-        if (t * 8 + head >= G) continue;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) top = fmaxf(top, sm_m[w][t * 8 + head]);
-        const float nb = top == -INFINITY ? 0.f : top;
-        // features 2 fp, 2 fp + 1 of the lane's: tile pair, row half
-        constexpr int kPairs = D / 32;  // pairs per group and lane
-        const int g2 = fp / kPairs, q2 = fp % kPairs;
-        const int reg = (g2 * kGT + (q2 >> 1) * 2) * 4 + (q2 & 1) * 2 + e;
-        float lt = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-          const float c = fast_exp2(sm_m[w][t * 8 + head] - nb);
-          const float* pk = reinterpret_cast<const float*>(smem + (w * kS + park_slot[w]) * C::kSlot);
-          lt = fmaf(sm_l[w][t * 8 + head], c, lt);
-          x0 = fmaf(pk[reg * C::kRegPitch + ln], c, x0);
-          x1 = fmaf(pk[(reg + 4) * C::kRegPitch + ln], c, x1);
-        }
-        const int64_t at_row = row + t * 8 + head;
-        const int f = g2 * (D / 2) + (ln >> 2) * (D / 16) + q2 * 2;
-        *reinterpret_cast<float2*>(a.part_o + at_row * D + f) = make_float2(x0, x1);
-        if (fp == 0 && (ln >> 2) == 0) {
-          a.part_ml[at_row * 2] = top;
-          a.part_ml[at_row * 2 + 1] = lt;
-        }
-      }
-      fence_proxy_async_smem();  // the next bulk copy into these slots comes after
-      __syncthreads();
-    }
     if (at.left == 0) break;
     next_head(at);
   }
@@ -616,7 +598,7 @@ constexpr int kMergeThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeArgs a) {
   constexpr int kWays = kMergeThreads / 2 / D;
-  __shared__ float factor[2][kKv4MaxGrid];
+  __shared__ float factor[2][kKv4MaxParts];
   __shared__ float sums[2][kWays][D];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();  // the parts
@@ -686,8 +668,8 @@ cudaError_t launch_merge(const Kv4DecodeArgs& a, cudaStream_t s) {
 template <int D, int NT, bool kScores>
 cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
   using C = Cfg<D, NT>;
-  static_assert(C::kRing <= 225 * 1024, "the ring and the static arrays fit an SM");
-  static_assert(C::kTiles * 4 * C::kRegPitch * 4 <= C::kSlot, "a head tile's partial fits a slot");
+  static_assert(C::kRing <= 220 * 1024, "the ring and the static arrays fit an SM");
+  static_assert(C::kWarps <= kKv4MaxWarps, "the workspace has room for every warp's parts");
   auto* kernel = kv4_split_kernel<D, NT, kScores>;
   // set on every launch: the attribute is per device, and the call is cheap
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);

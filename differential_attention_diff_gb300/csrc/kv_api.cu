@@ -53,7 +53,8 @@ struct DecodeSpace {
   size_t ml, parts, scores, gate, total;  // offsets; the partial O rows are at 0
 };
 DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
-  const size_t rows = (decode_grid(B, h_kv, L_max) + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
+  const size_t rows =
+      (static_cast<size_t>(decode_grid(B, h_kv, L_max)) * da::kKv4MaxWarps + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
   DecodeSpace w;
   w.ml = align256(rows * d * sizeof(float));
   w.parts = w.ml + align256(rows * 2 * sizeof(float));
@@ -143,7 +144,8 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
   if (!aligned(p->weights_in, 4) || !aligned(p->weights_out, 4) || (p->weights_in && !p->weights_out))
     return DA_ERR_INVALID_ARG;
   if (p->gate == nullptr && (!aligned(p->x, 16) || !aligned(p->w_lambda, 16))) return DA_ERR_INVALID_ARG;
-  if (p->B > 65535 || p->h_kv > 65535) return DA_ERR_UNSUPPORTED;
+  // sequences are a grid dimension; partials are numbered in 32 bits
+  if (p->B > 65535 || static_cast<int64_t>(p->B) * p->h_kv > (1 << 28)) return DA_ERR_UNSUPPORTED;
   const DecodeSpace w = decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr);
   if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   uint32_t* status;

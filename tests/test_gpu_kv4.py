@@ -281,7 +281,10 @@ def test_decode_kv4_gate_from_x_and_strided_views():
     assert torch.equal(a, b)
     half = big[:, :, 1:3]  # KV heads 1 and 2
     c = bd.diffattn_v2_decode_kv4(q[:, 2:6].contiguous(), half, seqlens=sl, gate=gate[:, 1:3].contiguous())
-    assert torch.equal(c, b[:, 1:3])
+    # other heads beside them cut the work elsewhere: equal up to the order of fp32 sums
+    kf, vf, rk, rv = ranges(clean(half, lens))
+    check_decode(q[:, 2:6], kf, vf, rk, rv, lens, f64(gate[:, 1:3]), c)
+    check_decode(q[:, 2:6], kf, vf, rk, rv, lens, f64(gate[:, 1:3]), b[:, 1:3])
 
 
 def test_decode_kv4_exact_cancellation_and_repeats():
