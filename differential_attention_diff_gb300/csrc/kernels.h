@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "diffattn.h"
 #include "kv4.cuh"
 
@@ -58,6 +60,26 @@ da_status check_v2_decode_args(const da_v2_decode_params* p);
 // The current device's status word and SM count; false if they cannot be had.
 bool device_handles(uint32_t** status, int* num_sms);
 
+// Runs a set-up call (a kernel attribute, say) once on each device: with its
+// result on the first call there, cudaSuccess on later ones.
+class OncePerDevice {
+ public:
+  template <class F>
+  cudaError_t run(F&& f) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t r = f();
+    if (r == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
+    return r;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
 // ---- 4-bit KV cache: append and read back -----------------------------------
 struct Kv4RowsArgs {
   int B, N, h_kv, d, L_max;
@@ -86,6 +108,7 @@ struct Kv4DecodeArgs {
   float* part_o;      // [grid * warps + B * h_kv, G, d] (numbered as in kv4.cuh)
   float* part_ml;     // [grid * warps + B * h_kv, G, 2]
   Kv4Parts* parts;    // [B * h_kv]
+  float2* norm;       // [B, 2h] each head's maximum and 1 / sum, or null
   float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
   const float* weights_in;
   float* weights_out;
@@ -96,11 +119,11 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 // ---- gathered key weights from the scores of a decode -------------------------
 struct KeyWeightsArgs {
   int B, h, h_kv, L_max;
-  int splits;             // key-range splits, where parts is null
-  const Kv4Parts* parts;  // [B * h_kv] of the 4-bit decode, or null
+  int splits;          // key-range splits, where norm is null
+  const float2* norm;  // [B, 2h] each head's maximum and 1 / sum, or null: taken from part_ml
   const int* seqlens;
   const float* gate;
-  const float* part_ml;  // [splits, B, 2h, 2], or the 4-bit decode's
+  const float* part_ml;  // [splits, B, 2h, 2]
   const float* scores;   // [B, h_kv, L_max, G]
   const float* weights_in;
   float* weights_out;
@@ -108,6 +131,7 @@ struct KeyWeightsArgs {
 cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t s);
 
 // ---- eviction from a cache -----------------------------------------------------
+constexpr int kEvictMaxSlots = 1 << 20;  // of a head: 8 slices whose masks fit shared memory beside their ranks
 struct EvictArgs {
   da_kv_evict_params p;
   int* n_moves;  // [B * h_kv]

@@ -55,16 +55,18 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a)
   // a warp per head, a lane per partial
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = warp; r < G; r += kThreads / 32) {
-    int64_t first = unit, step = static_cast<int64_t>(a.B) * a.h_kv;
-    int count = a.splits;
-    if (a.parts) {
-      first = a.parts[unit].first;
-      count = a.parts[unit].last - a.parts[unit].first + 1;
-      step = 1;
+    const int64_t head = static_cast<int64_t>(b) * 2 * a.h + g * G + r;
+    if (a.norm) {
+      if (lane == 0) {
+        const float2 n = a.norm[head];
+        sm[r] = n.x;
+        sc[r] = (r & 1) ? n.y * a.gate[head / 2] : n.y;
+      }
+      continue;
     }
     float mt = -INFINITY, lt = 0.f;
-    for (int i = lane; i < count; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + ((first + i * step) * G + r) * 2);
+    for (int i = lane; i < a.splits; i += 32) {
+      const float2 ml = reinterpret_cast<const float2*>(a.part_ml)[i * static_cast<int64_t>(a.B) * 2 * a.h + head];
       const float top = fmaxf(mt, ml.x), nb = top == -INFINITY ? 0.f : top;
       lt = lt * exp2f(mt - nb) + ml.y * exp2f(ml.x - nb);
       mt = top;
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a)
     }
     if (lane == 0) {
       float c = lt == 0.f ? 0.f : 1.f / lt;
-      if (r & 1) c *= a.gate[static_cast<int64_t>(b) * a.h + (g * G + r) / 2];
+      if (r & 1) c *= a.gate[head / 2];
       sm[r] = mt == -INFINITY ? 0.f : mt;
       sc[r] = c;
     }

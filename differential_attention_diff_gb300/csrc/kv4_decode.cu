@@ -132,9 +132,11 @@ __device__ __forceinline__ int seq_chunks(const Kv4DecodeArgs& a, int b) {
 // and where its part of that head ends.
 struct Cursor {
   int b, g, chunk, end;
-  int L;         // the sequence's length
-  int left;      // chunks of this warp's part behind this head (its records fit the memory: 32 bits do)
+  int L;     // the sequence's length
+  int left;  // chunks of this warp's part behind this head (its records fit the memory: 32 bits do)
 };
+// The reference of a head that has seen no key: any score sends p past 2^8.
+constexpr float kNoMax = -3e38f;
 
 template <int D, int NT, bool kScores>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4DecodeArgs a) {
@@ -234,17 +236,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 
   // fill the ring's next slot with the chunk that `ahead` is at
   Cursor ahead = at;
-  int issued = 0, taken = 0;
+  const int64_t chunk_bytes = kChunk * a.cache.sn;
+  auto source = [&]() { return cache + ahead.b * a.cache.sb + ahead.g * a.cache.sh + ahead.chunk * chunk_bytes; };
+  const uint8_t* src = source();
+  int in_flight = 0, fill = 0;    // chunks, and the slot that the next one goes to
+  int slot = 0;                   // the slot to read next
+  uint32_t parity = 0;            // of each slot's barrier, one bit each
   auto issue = [&]() {
     if (ahead.chunk >= ahead.end) {
       if (ahead.left == 0) return;
       next_head(ahead);
+      src = source();
     }
     if (dead) return;
-    const int key0 = ahead.chunk * kChunk, n = min(kChunk, ahead.L - key0);
-    const int slot = issued % kS;
-    const uint32_t dst = ring + slot * C::kSlot, bar = bar0 + slot * 8;
-    const uint8_t* src = cache + ahead.b * a.cache.sb + ahead.g * a.cache.sh + key0 * a.cache.sn;
+    const int n = min(kChunk, ahead.L - ahead.chunk * kChunk);
+    const uint32_t dst = ring + fill * C::kSlot, bar = bar0 + fill * 8;
     if (dense) {  // one bulk copy
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, n * kRec);
@@ -259,8 +265,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       }
       cp_async_arrive(bar);
     }
-    ++issued;
+    ++in_flight;
+    fill = fill == kS - 1 ? 0 : fill + 1;
     ++ahead.chunk;
+    src += chunk_bytes;
   };
 #pragma unroll 1
   for (int i = 0; i < kS - 1; ++i) issue();
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       for (int i = 0; i < C::kTiles; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[t][e] = -INFINITY;
+        mx[t][e] = kNoMax;
         vs[t][e] = 0x1p100f;
         l[t][e] = mn[t][0][e] = mn[t][1][e] = 0.f;
       }
@@ -348,16 +356,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     const int begin = at.chunk;
     for (; at.chunk < at.end; ++at.chunk) {
       issue();  // into the slot read last
-      const int slot = taken % kS;
-      if (!dead && !mbar_wait(bar0 + slot * 8, (taken / kS) & 1, a.status, 0x4B04)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      ++taken;
       if (dead) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar0 + slot * 8, (parity >> slot) & 1, a.status, 0x4B04))) {
+        dead = true;
+        continue;
+      }
+      --in_flight;
+      parity ^= 1u << slot;
       const uint32_t base = ring + slot * C::kSlot;
-      const int key0 = at.chunk * kChunk;
-      const int valid = at.L - key0;  // keys of this chunk
+      slot = slot == kS - 1 ? 0 : slot + 1;
+      const int valid = at.L - at.chunk * kChunk;  // keys of this chunk
 
-      // ---- scores, two 16-key tiles ----
+      // ---- scores (of fac log2 units), two 16-key tiles ----
       uint4 par[2][2];  // [tile][row half]: K s0 s1 | K m0 m1 | V s0 s1 | V m0 m1
       float s[2][NT][4];
 #pragma unroll
@@ -365,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         const uint32_t ra = base + (u * 16 + row_key) * kRec;
         par[u][0] = lds128(ra + D);
         par[u][1] = lds128(ra + kRec + D);
-        if (valid < kChunk) {  // what lies behind the last key may be anything: give it zero parameters
+        if (__builtin_expect(valid < kChunk, 0)) {  // what lies behind the last key may be anything: zero parameters
           if (u * 16 + row_key >= valid) par[u][0] = make_uint4(0, 0, 0, 0);
           if (u * 16 + row_key + 1 >= valid) par[u][1] = make_uint4(0, 0, 0, 0);
         }
@@ -404,9 +414,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             x = fmaf(lo_bf16(r.y), qs0[t][c], x);
             x = fmaf(lo_bf16(r.x), acc[0][t][e], x);
             x = fmaf(hi_bf16(r.x), acc[1][t][e], x);
-            s[u][t][e] = x * fac[t][c];
-            if (valid < kChunk && u * 16 + row_key + (e >> 1) >= valid) s[u][t][e] = -INFINITY;
+            s[u][t][e] = x;
           }
+        if (__builtin_expect(valid < kChunk, 0)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (u * 16 + row_key + (e >> 1) >= valid) s[u][t][e] = -INFINITY;
+        }
         if constexpr (kScores) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -414,8 +430,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             for (int r = 0; r < 2; ++r) {
               const int k = u * 16 + row_key + r;
               if (k < valid && t * 8 + 2 * tq < G)
-                *reinterpret_cast<float2*>(a.scores + (unit * a.L_max + key0 + k) * G + t * 8 + 2 * tq) =
-                    make_float2(s[u][t][2 * r], s[u][t][2 * r + 1]);
+                *reinterpret_cast<float2*>(a.scores + (unit * a.L_max + at.chunk * kChunk + k) * G + t * 8 + 2 * tq) =
+                    make_float2(s[u][t][2 * r] * fac[t][0], s[u][t][2 * r + 1] * fac[t][1]);
             }
         }
       }
@@ -427,12 +443,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         bool over = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float m0 = mx[t][0] == -INFINITY ? 0.f : mx[t][0], m1 = mx[t][1] == -INFINITY ? 0.f : mx[t][1];
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float x = fast_exp2(s[u][t][2 * r] - m0), y = fast_exp2(s[u][t][2 * r + 1] - m1);
+              const float x = fast_exp2(fmaf(s[u][t][2 * r], fac[t][0], -mx[t][0]));
+              const float y = fast_exp2(fmaf(s[u][t][2 * r + 1], fac[t][1], -mx[t][1]));
               p[u][t][2 * r] = x;
               p[u][t][2 * r + 1] = y;
               const float xv = x * vs[t][0], yv = y * vs[t][1];
@@ -443,46 +459,42 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
           lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
           lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
           over |= lsum[t][0] > 256.f || lsum[t][1] > 256.f;
+          // none of them is negative: their sum bounds each (and its adds do
+          // not take the pipe that the code masks fill)
           __half2 top = *reinterpret_cast<__half2*>(&pf[0][t][0][0]);
 #pragma unroll
-          for (int i = 1; i < 8; ++i)
-            top = __hmax2(top, *reinterpret_cast<__half2*>(&pf[i >> 2][t][(i >> 1) & 1][i & 1]));
-          over |= __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(16384.f));
+          for (int i = 1; i < 8; ++i) top = __hadd2(top, *reinterpret_cast<__half2*>(&pf[i >> 2][t][(i >> 1) & 1][i & 1]));
+          over |= __hgt(__hadd(__low2half(top), __high2half(top)), __float2half(16384.f));
         }
         return over;
       };
-      bool first_tile = mx[0][0] == -INFINITY;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) first_tile |= mx[t][0] == -INFINITY || mx[t][1] == -INFINITY;
-      const bool over = weigh();
-      if (__any_sync(0xffffffffu, over || first_tile)) {
+      if (__any_sync(0xffffffffu, weigh())) {
         // new references from this chunk's keys: the score maximum, then the
         // largest p s under it
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
+            float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fac[t][e];
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             const float old = mx[t][e], now = fmaxf(old, top);
-            const float nb = now == -INFINITY ? 0.f : now;
             float big = 0.f;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                big = fmaxf(big, fast_exp2(s[u][t][2 * r + e] - nb) *
+                big = fmaxf(big, fast_exp2(fmaf(s[u][t][2 * r + e], fac[t][e], -now)) *
                                      fmaxf(lo_bf16(par[u][r].z), hi_bf16(par[u][r].z)));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            const float down = old == -INFINITY ? 0.f : exp2f(old - nb);
+            const float down = exp2f(old - now);
             l[t][e] *= down;
             mn[t][0][e] *= down;
             mn[t][1][e] *= down;
             mx[t][e] = now;
             // O stands for O / vs: a higher maximum raises vs and leaves O alone
-            const float keep = old == -INFINITY ? vs[t][e] : vs[t][e] * exp2f(nb - old);
+            const float keep = vs[t][e] * exp2f(now - old);
             float v = fminf(keep, 0x1p100f);
             if (big > 0.f) v = fminf(v, exponent_scale(big, 8));
             const float by = keep == v ? 1.f : v / keep;
@@ -587,82 +599,96 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   }
   // a warp that gave up waits (bounded) for what it still has in flight
   if (dead)
-    for (; taken < issued; ++taken) mbar_wait(bar0 + (taken % kS) * 8, (taken / kS) & 1, nullptr, 0);
+    for (; in_flight > 0; --in_flight) {
+      mbar_wait(bar0 + slot * 8, (parity >> slot) & 1, nullptr, 0);
+      slot = slot == kS - 1 ? 0 : slot + 1;
+    }
 }
 
-constexpr int kMergeThreads = 512;
-
-// One output head's parts merged, even - gate * odd.  Grid (h, B).  A warp
-// per head takes the maximum and the sum over the parts and leaves a factor
-// per part; then 256 threads per head add up the parts, 256 / D at a time.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeArgs a) {
-  constexpr int kWays = kMergeThreads / 2 / D;
-  __shared__ float factor[2][kKv4MaxParts];
-  __shared__ float sums[2][kWays][D];
+// One output head's parts merged, even - gate * odd; also the two heads'
+// normalisers for the keys' weights.  Grid (h, B).  Threads are (way, head of
+// the pair, four features); the ways share out the parts.
+template <int D, int WAYS>
+__global__ void __launch_bounds__(WAYS * D / 2) kv4_merge_kernel(Kv4DecodeArgs a) {
+  constexpr int kWarps = WAYS * D / 2 / 32;
+  __shared__ float top[2], inv[2];
+  __shared__ float4 sums[WAYS][2][D / 4];
   cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();  // the parts
   const int p = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = 2 * a.h / a.h_kv, g = 2 * p / G, r = 2 * p % G;
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
   const bool bad = L < 1 || L > a.L_max;  // recorded by the split kernel
-  int first = 0, count = 0;
+  cudaGridDependencySynchronize();        // the parts
+  int64_t first = 0;
+  int count = 0;
   if (!bad) {
     const Kv4Parts s = a.parts[static_cast<int64_t>(b) * a.h_kv + g];
     first = s.first;
     count = s.last - s.first + 1;
   }
-  if (warp < 2) {
-    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + static_cast<int64_t>(first) * G + r + warp;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + first * G + r;
+  for (int e = warp; e < 2; e += kWarps) {
     float mt = -INFINITY, lt = 0.f;
-    for (int i = lane; i < count; i += 32) mt = fmaxf(mt, ml[static_cast<int64_t>(i) * G].x);
+    for (int i = lane; i < count; i += 32) mt = fmaxf(mt, ml[static_cast<int64_t>(i) * G + e].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    const float base = mt == -INFINITY ? 0.f : mt;
     for (int i = lane; i < count; i += 32) {
-      const float2 v = ml[static_cast<int64_t>(i) * G];
-      const float c = exp2f(v.x - base);
-      lt += v.y * c;
-      factor[warp][i] = c;
+      const float2 v = ml[static_cast<int64_t>(i) * G + e];
+      lt += v.y * exp2f(v.x - mt);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-    // a sum of 0 is an empty sequence or keys that are all -inf: zeros, as in decode.cu; NaN stays
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    for (int i = lane; i < count; i += 32) factor[warp][i] *= inv;
+    if (lane == 0) {
+      // a sum of 0 is an empty sequence or keys that are all -inf: zeros, as in decode.cu; NaN stays
+      const float c = lt == 0.f ? 0.f : 1.f / lt;
+      top[e] = mt;
+      inv[e] = c;
+      if (a.norm) a.norm[static_cast<int64_t>(b) * 2 * a.h + 2 * p + e] = make_float2(mt, c);
+    }
   }
   __syncthreads();
-  const int e = tid / (kWays * D), way = tid / D % kWays, f = tid % D;
-  const float* po = a.part_o + (static_cast<int64_t>(first) * G + r + e) * D + f;
-  float x = 0.f;
+  const int f = tid % (D / 4), e = tid / (D / 4) % 2, way = tid / (D / 2);
+  const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * G + r + e) * (D / 4) + f;
+  const float mt = top[e];
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = way; i < count; i += kWays) x = fmaf(po[static_cast<int64_t>(i) * G * D], factor[e][i], x);
-  sums[e][way][f] = x;
+  for (int i = way; i < count; i += WAYS) {
+    const float c = exp2f(ml[static_cast<int64_t>(i) * G + e].x - mt);
+    const float4 v = po[static_cast<int64_t>(i) * G * (D / 4)];
+    x.x = fmaf(v.x, c, x.x);
+    x.y = fmaf(v.y, c, x.y);
+    x.z = fmaf(v.z, c, x.z);
+    x.w = fmaf(v.w, c, x.w);
+  }
+  sums[way][e][f] = x;
   __syncthreads();
   if (tid < D) {
     float res[2] = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int w = 0; w < kWays; ++w) res[k] += sums[k][w][tid];
+      for (int w = 0; w < WAYS; ++w) res[k] += reinterpret_cast<const float*>(&sums[w][k][0])[tid];
+      res[k] *= inv[k];
+    }
     const int64_t at = static_cast<int64_t>(b) * a.h + p;
     static_cast<__nv_bfloat16*>(a.out)[at * D + tid] =
         __float2bfloat16_rn(__fsub_rn(res[0], __fmul_rn(a.gate[at], res[1])));
   }
 }
 
-template <int D>
+template <int D, int WAYS>
 cudaError_t launch_merge(const Kv4DecodeArgs& a, cudaStream_t s) {
+  static_assert(WAYS * D / 2 >= D, "a thread per feature of the output");
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3(a.h, a.B);
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.blockDim = dim3(WAYS * D / 2);
   cfg.stream = s;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, WAYS>, a);
 }
 
 template <int D, int NT, bool kScores>
@@ -671,8 +697,10 @@ cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
   static_assert(C::kRing <= 220 * 1024, "the ring and the static arrays fit an SM");
   static_assert(C::kWarps <= kKv4MaxWarps, "the workspace has room for every warp's parts");
   auto* kernel = kv4_split_kernel<D, NT, kScores>;
-  // set on every launch: the attribute is per device, and the call is cheap
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
+  static OncePerDevice once;
+  const cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
+  });
   if (e != cudaSuccess) return e;
   kernel<<<a.grid, C::kThreads, C::kRing, s>>>(a);
   return cudaGetLastError();
@@ -690,9 +718,14 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
     e = two ? (sc ? launch_split<64, 2, true>(a, s) : launch_split<64, 2, false>(a, s))
             : (sc ? launch_split<64, 1, true>(a, s) : launch_split<64, 1, false>(a, s));
   if (e != cudaSuccess) return e;
-  e = a.d == 128 ? launch_merge<128>(a, s) : launch_merge<64>(a, s);
+  // A head has about warps / heads parts; 4 parts per way where they are many
+  const bool many = static_cast<int64_t>(a.grid) * 16 > 16 * static_cast<int64_t>(a.B) * a.h_kv;
+  if (a.d == 128)
+    e = many ? launch_merge<128, 16>(a, s) : launch_merge<128, 2>(a, s);
+  else
+    e = many ? launch_merge<64, 16>(a, s) : launch_merge<64, 2>(a, s);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
-  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, 0, a.parts, a.seqlens, a.gate, a.part_ml, a.scores,
+  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, 0, a.norm, a.seqlens, a.gate, a.part_ml, a.scores,
                          a.weights_in, a.weights_out};
   return launch_key_weights(w, s);
 }

@@ -50,7 +50,7 @@ int decode_grid(int B, int h_kv, int L_max) {
 }
 
 struct DecodeSpace {
-  size_t ml, parts, scores, gate, total;  // offsets; the partial O rows are at 0
+  size_t ml, parts, norm, scores, gate, total;  // offsets; the partial O rows are at 0
 };
 DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
   const size_t rows =
@@ -58,7 +58,8 @@ DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_give
   DecodeSpace w;
   w.ml = align256(rows * d * sizeof(float));
   w.parts = w.ml + align256(rows * 2 * sizeof(float));
-  w.scores = w.parts + align256(static_cast<size_t>(B) * h_kv * sizeof(da::Kv4Parts));
+  w.norm = w.parts + align256(static_cast<size_t>(B) * h_kv * sizeof(da::Kv4Parts));
+  w.scores = w.norm + align256(static_cast<size_t>(B) * 2 * h * sizeof(float2));
   w.gate = w.scores + (weights ? align256(static_cast<size_t>(B) * 2 * h * L_max * sizeof(float)) : 0);
   w.total = w.gate + (gate_given ? 0 : align256(static_cast<size_t>(B) * h * sizeof(float)));
   return w;
@@ -165,6 +166,7 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
                             scale * kLog2e, p->q, p->cache, p->seqlens, gate, p->out,
                             reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.ml),
                             reinterpret_cast<da::Kv4Parts*>(ws + w.parts),
+                            p->weights_out ? reinterpret_cast<float2*>(ws + w.norm) : nullptr,
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
                             p->weights_in, p->weights_out, status};
   return cuda_status(da::launch_kv4_decode(a, s));
@@ -191,7 +193,7 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
   for (int k = 0; k < p->n_rows; ++k)
     if (!ok_t4(p->rows[k], 16) || p->row_bytes[k] <= 0 || p->row_bytes[k] % 16) return DA_ERR_INVALID_ARG;
   // heads are a grid dimension, up to 8 CTAs each; a head's 16-byte pieces are counted in 32 bits
-  if (static_cast<int64_t>(p->B) * p->h_kv > (1 << 28)) return DA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->B) * p->h_kv > (1 << 28) || p->L_max > da::kEvictMaxSlots) return DA_ERR_UNSUPPORTED;
   for (int k = 0; k < p->n_rows; ++k)
     if (static_cast<int64_t>(p->L_max) * (p->row_bytes[k] / 16) > (1 << 30)) return DA_ERR_UNSUPPORTED;
   const EvictSpace w = evict_space(p->B, p->h_kv, p->L_max, p->keep);

@@ -3,12 +3,14 @@
 //
 // Every slot has a 32-bit rank: all ones for a protected slot, else an
 // order-preserving image of its weight.  Select finds the rank of the m-th
-// highest slot by its digits, eight bits at a time from the top: a histogram
+// highest slot by its digits, eleven bits at a time from the top: a histogram
 // of the digit over the slots that match the digits so far, and the bin that
-// the m-th falls into.  Slots above that rank stay, and of those at it the
-// lowest ones until m stay.  A pass in slot order then lists the slots below m
-// that go (destinations) and the slots at or above m that stay (sources),
-// paired in ascending order.
+// the m-th falls into.  Two digits (sign, exponent and 13 bits of mantissa)
+// mostly leave one slot in that bin, and the search ends there.  Slots above
+// that rank stay, and of those at it the lowest ones until m stay.  Each
+// 32-slot word's answer is kept as a mask; the slots below m that go
+// (destinations) and the slots at or above m that stay (sources) are listed
+// from the masks, a word per lane, and paired in ascending order.
 //
 // A head's slots are spread over a cluster of CTAs, each holding its slice's
 // ranks in shared memory, so weights and positions are read once; histograms
@@ -32,8 +34,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kCopies = 8;        // of the histogram, by lane: weights crowd into few bins
+constexpr int kDigit = 11;        // bits looked at together
+constexpr int kBins = 1 << kDigit;
 constexpr int kMaxRanks = 49152;  // of a slice kept in shared memory (192 KB); those behind are read again
+constexpr int kMaxSelectSmem = 208 * 1024;  // ranks and masks: slices up to 131,072 slots, kEvictMaxSlots in all
 constexpr int kMoveThreads = 256;
 
 // Rank of slot j: protected, then NaN, then weights in ascending order (-0 as 0).
@@ -46,15 +50,14 @@ __device__ __forceinline__ uint32_t rank_of(float w, int pos, int sinks, int64_t
 }
 
 struct Shared {
-  uint32_t hist[256 * kCopies];
-  int sums[2][256];  // this slice's histogram, for the cluster; two, so that one barrier a digit suffices
-  int counts[3];     // this slice's ties, destinations, sources
+  uint32_t hist[2][kBins];  // this slice's histogram, read by the cluster; two, so that one barrier a digit suffices
+  int counts[3];            // this slice's ties, destinations, sources
   int warp_counts[3][kWarps];
-  int digit, above;
+  int digit, above, in_bin;
 };
 
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int cached) {
-  extern __shared__ uint32_t ranks[];
+  extern __shared__ uint32_t ranks[];  // and behind them the masks
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
@@ -109,27 +112,38 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   int shift = 32;       // bits not looked at yet
   bool all = false;     // every slot that matches stays
   for (int round = 0; shift > 0 && !all; ++round) {
-    shift -= 8;
-    for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[i] = 0;
+    const int bits = min(shift, kDigit), above_shift = shift;
+    shift -= bits;
+    uint32_t* hist = sh.hist[round & 1];
+    for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     for (int j = j0 + tid; j < j1; j += kThreads) {
       const uint32_t r = rank(j);
-      if (shift == 24 || (r >> (shift + 8)) == prefix) atomicAdd(&sh.hist[((r >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+      if (round == 0 || (r >> above_shift) == prefix) atomicAdd(&hist[(r >> shift) & ((1u << bits) - 1)], 1u);
     }
-    __syncthreads();
-    static_assert(kThreads == 256, "one thread per bin");
-    int mine = 0;
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) mine += sh.hist[tid * kCopies + k];
-    if (cs > 1) {
-      sh.sums[round & 1][tid] = mine;
+    if (cs > 1)
       cluster.sync();
-      mine = 0;
-      for (int c = 0; c < cs; ++c) mine += cluster.map_shared_rank(&sh.sums[round & 1][0], c)[tid];
+    else
+      __syncthreads();
+    constexpr int kMine = kBins / kThreads;  // neighbouring bins per thread
+    int bin[kMine], up = 0;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) bin[k] = 0;
+    for (int c = 0; c < cs; ++c) {
+      const uint4* h = reinterpret_cast<const uint4*>(cs > 1 ? cluster.map_shared_rank(hist, c) : hist) + tid * (kMine / 4);
+#pragma unroll
+      for (int k = 0; k < kMine / 4; ++k) {
+        const uint4 v = h[k];
+        bin[4 * k] += v.x;
+        bin[4 * k + 1] += v.y;
+        bin[4 * k + 2] += v.z;
+        bin[4 * k + 3] += v.w;
+      }
     }
-    // slots in the bins above this thread's: sums from the top
-    const int bin_count = mine;
-    int up = bin_count;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) up += bin[k];
+    const int own = up;
+    // slots in this thread's bins and those above: sums from the top
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_down_sync(0xffffffffu, up, o);
@@ -138,28 +152,28 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     if (lane == 0) sh.warp_counts[0][warp] = up;
     __syncthreads();
     for (int w = warp + 1; w < kWarps; ++w) up += sh.warp_counts[0][w];
-    if (up >= need && up - bin_count < need) {  // one bin
-      sh.digit = tid;
-      sh.above = up - bin_count;
-      sh.counts[0] = bin_count;
+    if (up >= need && up - own < need) {  // one thread, and one of its bins
+      int above = up - own;
+#pragma unroll
+      for (int k = kMine - 1; k >= 0; --k) {
+        if (above < need && above + bin[k] >= need) {
+          sh.digit = tid * kMine + k;
+          sh.above = above;
+          sh.in_bin = bin[k];
+        }
+        above += bin[k];
+      }
     }
     __syncthreads();
-    prefix = (prefix << 8) | static_cast<uint32_t>(sh.digit);
+    prefix = (prefix << bits) | static_cast<uint32_t>(sh.digit);
     need -= sh.above;
-    all = sh.counts[0] == need;
-    __syncthreads();
+    all = sh.in_bin == need;
   }
 
-  // ---- who stays, in slot order: each warp takes a run of 32-slot words ----
+  // ---- who stays, a mask per 32-slot word; each warp takes a run of words ----
+  __syncthreads();
+  uint32_t* masks = ranks + cached;
   const int words = (j1 - j0 + 31) / 32, w0 = words * warp / kWarps, w1 = words * (warp + 1) / kWarps;
-  auto state = [&](int word, int ties_before, bool& stays, unsigned& tie) {
-    const int j = j0 + word * 32 + lane;
-    const uint32_t r = j < j1 ? rank(j) >> shift : 0u;
-    const bool t = j < j1 && r == prefix;
-    tie = __ballot_sync(0xffffffffu, t);
-    stays = j < j1 && (r > prefix || (t && (all || ties_before + __popc(tie & ((1u << lane) - 1)) < need)));
-    return j;
-  };
   // numbers before this warp's run, from per-warp counts and the slices before
   auto before = [&](int k, int n) {
     if (lane == 0) sh.warp_counts[k][warp] = n;
@@ -178,26 +192,54 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     for (int c = 0; c < part; ++c) s += cluster.map_shared_rank(&sh.counts[0], c)[k];
     return s;
   };
-  int ties = 0;
-  bool stays;
-  unsigned tie;
+  int ties = 0;  // before this warp's run
   if (!all) {
     int n = 0;
     for (int w = w0; w < w1; ++w) {
-      state(w, 0, stays, tie);
-      n += __popc(tie);
+      const int j = j0 + w * 32 + lane;
+      n += __popc(__ballot_sync(0xffffffffu, j < j1 && (rank(j) >> shift) == prefix));
     }
     ties = before(0, n);
     cluster.sync();
     ties += slices_before(0);
   }
-  int n_dst = 0, n_src = 0, seen = ties;
+  int n_dst = 0, n_src = 0;
   for (int w = w0; w < w1; ++w) {
-    const int j = state(w, seen, stays, tie);
-    seen += __popc(tie);
-    n_dst += __popc(__ballot_sync(0xffffffffu, j < j1 && j < m && !stays));
-    n_src += __popc(__ballot_sync(0xffffffffu, j >= m && stays));
+    const int j = j0 + w * 32 + lane;
+    const uint32_t r = j < j1 ? rank(j) >> shift : 0u;
+    bool stays = j < j1 && r >= prefix;
+    if (!all) {
+      const bool tie = stays && r == prefix;
+      const unsigned t = __ballot_sync(0xffffffffu, tie);
+      if (tie) stays = ties + __popc(t & ((1u << lane) - 1)) < need;
+      ties += __popc(t);
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, stays);
+    if (lane == 0) masks[w] = mask;
+    if (j < m && stays) {
+      if (copy_w) w_out[j] = w_in[j];
+      if (copy_p) p_out[j] = p_in ? p_in[j] : j;
+    }
   }
+  __syncwarp();
+  // a word per lane: its slots that go below m, and those that stay from m on
+  auto split = [&](int w, uint32_t& d, uint32_t& s) {
+    d = s = 0;
+    if (w >= w1) return;
+    const int first = j0 + w * 32;  // the word's slots below m, and those that exist
+    const uint32_t low = m >= first + 32 ? ~0u : m > first ? (1u << (m - first)) - 1 : 0u;
+    const uint32_t live = j1 >= first + 32 ? ~0u : (1u << (j1 - first)) - 1;
+    d = ~masks[w] & low & live;
+    s = masks[w] & ~low;
+  };
+  for (int w = w0 + lane; w - lane < w1; w += 32) {
+    uint32_t d, s;
+    split(w, d, s);
+    n_dst += __popc(d);
+    n_src += __popc(s);
+  }
+  n_dst = __reduce_add_sync(0xffffffffu, n_dst);
+  n_src = __reduce_add_sync(0xffffffffu, n_src);
   n_dst = before(1, n_dst);
   n_src = before(2, n_src);
   cluster.sync();
@@ -205,21 +247,23 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   n_src += slices_before(2);
   int* dst = a.dst + static_cast<int64_t>(unit) * a.max_moves;
   int* src = a.src + static_cast<int64_t>(unit) * a.max_moves;
-  seen = ties;
-  for (int w = w0; w < w1; ++w) {
-    const int j = state(w, seen, stays, tie);
-    seen += __popc(tie);
-    const bool is_dst = j < j1 && j < m && !stays, is_src = j >= m && stays;
-    const unsigned db = __ballot_sync(0xffffffffu, is_dst), sb = __ballot_sync(0xffffffffu, is_src);
-    const unsigned low = (1u << lane) - 1;
-    if (is_dst) dst[n_dst + __popc(db & low)] = j;
-    if (is_src) src[n_src + __popc(sb & low)] = j;
-    n_dst += __popc(db);
-    n_src += __popc(sb);
-    if (j < m && stays) {
-      if (copy_w) w_out[j] = w_in[j];
-      if (copy_p) p_out[j] = p_in ? p_in[j] : j;
+  for (int w = w0 + lane; w - lane < w1; w += 32) {
+    uint32_t d, s;
+    split(w, d, s);
+    int di = __popc(d), si = __popc(s);  // up to and with this lane's word
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, di, o), y = __shfl_up_sync(0xffffffffu, si, o);
+      if (lane >= o) di += x, si += y;
     }
+    const int td = __shfl_sync(0xffffffffu, di, 31), ts = __shfl_sync(0xffffffffu, si, 31);
+    di += n_dst - __popc(d);
+    si += n_src - __popc(s);
+    n_dst += td;
+    n_src += ts;
+    const int first = j0 + w * 32;
+    for (; d; d &= d - 1) dst[di++] = first + __ffs(d) - 1;
+    for (; s; s &= s - 1) src[si++] = first + __ffs(s) - 1;
   }
   if (part == 0 && tid == 0) {
     int s = 0;
@@ -282,9 +326,13 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
     cs *= 2;
   const int per = ((a.p.L_max + cs - 1) / cs + 31) / 32 * 32;
   const int cached = per < kMaxRanks ? per : kMaxRanks;
-  const size_t smem = static_cast<size_t>(cached) * sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxRanks * static_cast<int>(sizeof(uint32_t)));
+  const size_t smem = (static_cast<size_t>(cached) + per / 32) * sizeof(uint32_t);
+  if (smem > kMaxSelectSmem) return cudaErrorInvalidValue;  // refused by the entry point before
+  static OncePerDevice once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMaxSelectSmem);
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];

@@ -195,6 +195,14 @@ def test_evict_many_heads():
     run_evict(B, hkv, L, 60, lens, sinks=2, recent=20, weights=spread((B, hkv, L), 760), widths=((80, torch.uint8),))
 
 
+def test_evict_more_slots_than_shared_memory_holds():
+    """Half a million slots of one head: each CTA of the cluster keeps the
+    first 49152 ranks of its slice and reads the others again."""
+    L = 500_001
+    for keep, ties in ((200_000, True), (499_000, False)):
+        run_evict(1, 1, L, keep, [L], sinks=4, recent=1000, weights=spread((1, 1, L), 780, ties), widths=((8, BF16),))
+
+
 def test_evict_does_not_change_what_a_decode_over_the_kept_keys_gives():
     """A decode over the compacted cache equals one over the kept keys in their
     own order, up to the order of fp32 sums."""

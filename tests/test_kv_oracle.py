@@ -198,6 +198,8 @@ def test_evict_argument_checks(lib):
     assert need >= 2 * 4 * 32 * 2 * 4
     assert f(_with(p, workspace=FAKE, workspace_bytes=need - 1), None) == bd.DA_ERR_WORKSPACE
     assert f(_with(p, B=0), None) == bd.DA_OK
+    for bad in (dict(L_max=(1 << 20) + 1), dict(B=1 << 28)):  # more slots, or more heads, than are counted
+        assert f(_with(p, **bad), None) == bd.DA_ERR_UNSUPPORTED, bad
     # keeping everything needs no lists
     assert lib.diffattn_kv_evict_workspace_size(2, 4, 64, 64) < need
 
