@@ -23,6 +23,8 @@
 // many rows move as there are holes, fewer than a compaction in order moves.
 #include <cooperative_groups.h>
 
+#include <climits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -31,8 +33,6 @@ namespace cg = cooperative_groups;
 namespace da {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kDigit = 11;        // bits looked at together
 constexpr int kBins = 1 << kDigit;
@@ -41,7 +41,7 @@ constexpr int kMaxSelectSmem = 208 * 1024;  // ranks and masks: slices up to 131
 constexpr int kMoveThreads = 256;
 
 // Rank of slot j: protected, then NaN, then weights in ascending order (-0 as 0).
-__device__ __forceinline__ uint32_t rank_of(float w, int pos, int sinks, int64_t recent_from) {
+__device__ __forceinline__ uint32_t rank_of(float w, int pos, int sinks, int recent_from) {
   if (pos < sinks || pos >= recent_from) return 0xffffffffu;
   w += 0.f;
   if (w != w) return 0xfffffffeu;
@@ -49,16 +49,20 @@ __device__ __forceinline__ uint32_t rank_of(float w, int pos, int sinks, int64_t
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <int T>
 struct Shared {
   uint32_t hist[2][kBins];  // this slice's histogram, read by the cluster; two, so that one barrier a digit suffices
   int counts[3];            // this slice's ties, destinations, sources
-  int warp_counts[3][kWarps];
+  int warp_counts[3][T / 32];
   int digit, above, in_bin;
 };
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int cached) {
+// T threads; kAll: every slice fits in `cached` ranks.
+template <int T, bool kAll>
+__global__ void __launch_bounds__(T, 2048 / T) evict_select_kernel(EvictArgs a, int cached) {
+  constexpr int kThreads = T, kWarps = T / 32;
   extern __shared__ uint32_t ranks[];  // and behind them the masks
-  __shared__ Shared sh;
+  __shared__ Shared<T> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / cs, b = unit / a.p.h_kv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -84,25 +88,43 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
       }
     return;
   }
-  const int64_t recent_from = (a.p.next_position ? a.p.next_position[b] : L) - static_cast<int64_t>(a.p.recent);
+  const int end = a.p.next_position ? a.p.next_position[b] : L;
+  const int recent_from = end >= INT_MIN + a.p.recent ? end - a.p.recent : INT_MIN;
+  const bool alone = cs == 1;
+  auto sync_all = [&]() {
+    if (alone)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
   const int slice = ((L + cs - 1) / cs + 31) / 32 * 32;
   const int j0 = min(L, part * slice), j1 = min(L, j0 + slice);
   auto read_rank = [&](int j) { return rank_of(w_in[j], p_in ? p_in[j] : j, a.p.sinks, recent_from); };
-  auto rank = [&](int j) { return j - j0 < cached ? ranks[j - j0] : read_rank(j); };
-  {
-    const int n = min(j1 - j0, cached);
-    for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {  // four reads in flight
-      float w[4];
-      int p[4];
+  auto rank = [&](int j) { return kAll || j - j0 < cached ? ranks[j - j0] : read_rank(j); };
+  for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist[0])[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  // Read the slots, four in flight; their first digit is counted on the way,
+  // and what lies below m is copied whether it stays or not: the slots that
+  // go are written again when their successors move in.
+  for (int i0 = j0 + tid; i0 < j1; i0 += 4 * kThreads) {
+    float w[4];
+    int p[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kThreads;
-        w[k] = i < n ? w_in[j0 + i] : 0.f;
-        p[k] = i < n && p_in ? p_in[j0 + i] : j0 + i;
+    for (int k = 0; k < 4; ++k) {
+      const int j = i0 + k * kThreads;
+      w[k] = j < j1 ? w_in[j] : 0.f;
+      p[k] = j < j1 && p_in ? p_in[j] : j;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = i0 + k * kThreads;
+      if (j < j1) {
+        const uint32_t r = rank_of(w[k], p[k], a.p.sinks, recent_from);
+        if (kAll || j - j0 < cached) ranks[j - j0] = r;
+        atomicAdd(&sh.hist[0][r >> (32 - kDigit)], 1u);
+        if (copy_w && j < m) w_out[j] = w[k];
+        if (copy_p && j < m) p_out[j] = p[k];
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * kThreads < n) ranks[i0 + k * kThreads] = rank_of(w[k], p[k], a.p.sinks, recent_from);
     }
   }
 
@@ -115,29 +137,27 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     const int bits = min(shift, kDigit), above_shift = shift;
     shift -= bits;
     uint32_t* hist = sh.hist[round & 1];
-    for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    for (int j = j0 + tid; j < j1; j += kThreads) {
-      const uint32_t r = rank(j);
-      if (round == 0 || (r >> above_shift) == prefix) atomicAdd(&hist[(r >> shift) & ((1u << bits) - 1)], 1u);
-    }
-    if (cs > 1)
-      cluster.sync();
-    else
+    if (round) {
+      for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
+#pragma unroll 4
+      for (int j = j0 + tid; j < j1; j += kThreads) {
+        const uint32_t r = rank(j);
+        if ((r >> above_shift) == prefix) atomicAdd(&hist[(r >> shift) & ((1u << bits) - 1)], 1u);
+      }
+    }
+    sync_all();
     constexpr int kMine = kBins / kThreads;  // neighbouring bins per thread
     int bin[kMine], up = 0;
 #pragma unroll
     for (int k = 0; k < kMine; ++k) bin[k] = 0;
     for (int c = 0; c < cs; ++c) {
-      const uint4* h = reinterpret_cast<const uint4*>(cs > 1 ? cluster.map_shared_rank(hist, c) : hist) + tid * (kMine / 4);
+      const uint2* h = reinterpret_cast<const uint2*>(alone ? hist : cluster.map_shared_rank(hist, c)) + tid * (kMine / 2);
 #pragma unroll
-      for (int k = 0; k < kMine / 4; ++k) {
-        const uint4 v = h[k];
-        bin[4 * k] += v.x;
-        bin[4 * k + 1] += v.y;
-        bin[4 * k + 2] += v.z;
-        bin[4 * k + 3] += v.w;
+      for (int k = 0; k < kMine / 2; ++k) {
+        const uint2 v = h[k];
+        bin[2 * k] += v.x;
+        bin[2 * k + 1] += v.y;
       }
     }
 #pragma unroll
@@ -151,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     }
     if (lane == 0) sh.warp_counts[0][warp] = up;
     __syncthreads();
-    for (int w = warp + 1; w < kWarps; ++w) up += sh.warp_counts[0][w];
+    up += __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? sh.warp_counts[0][lane] : 0);
     if (up >= need && up - own < need) {  // one thread, and one of its bins
       int above = up - own;
 #pragma unroll
@@ -178,32 +198,33 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   auto before = [&](int k, int n) {
     if (lane == 0) sh.warp_counts[k][warp] = n;
     __syncthreads();
-    if (tid == 0) {
-      int s = 0;
-      for (int w = 0; w < kWarps; ++w) s += sh.warp_counts[k][w];
-      sh.counts[k] = s;
+    const int c = lane < kWarps ? sh.warp_counts[k][lane] : 0;
+    if (warp == 0) {
+      const int all_warps = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) sh.counts[k] = all_warps;
     }
-    int s = 0;
-    for (int w = 0; w < warp; ++w) s += sh.warp_counts[k][w];
-    return s;
+    return __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
   };
-  auto slices_before = [&](int k) {
+  auto slices = [&](int k, int n) {  // over the first n slices
+    if (alone) return n ? sh.counts[k] : 0;
     int s = 0;
-    for (int c = 0; c < part; ++c) s += cluster.map_shared_rank(&sh.counts[0], c)[k];
+    for (int c = 0; c < n; ++c) s += cluster.map_shared_rank(&sh.counts[0], c)[k];
     return s;
   };
   int ties = 0;  // before this warp's run
   if (!all) {
     int n = 0;
+#pragma unroll 4
     for (int w = w0; w < w1; ++w) {
       const int j = j0 + w * 32 + lane;
       n += __popc(__ballot_sync(0xffffffffu, j < j1 && (rank(j) >> shift) == prefix));
     }
     ties = before(0, n);
-    cluster.sync();
-    ties += slices_before(0);
+    sync_all();
+    ties += slices(0, part);
   }
   int n_dst = 0, n_src = 0;
+#pragma unroll 4
   for (int w = w0; w < w1; ++w) {
     const int j = j0 + w * 32 + lane;
     const uint32_t r = j < j1 ? rank(j) >> shift : 0u;
@@ -216,10 +237,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     }
     const unsigned mask = __ballot_sync(0xffffffffu, stays);
     if (lane == 0) masks[w] = mask;
-    if (j < m && stays) {
-      if (copy_w) w_out[j] = w_in[j];
-      if (copy_p) p_out[j] = p_in ? p_in[j] : j;
-    }
   }
   __syncwarp();
   // a word per lane: its slots that go below m, and those that stay from m on
@@ -242,9 +259,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   n_src = __reduce_add_sync(0xffffffffu, n_src);
   n_dst = before(1, n_dst);
   n_src = before(2, n_src);
-  cluster.sync();
-  n_dst += slices_before(1);
-  n_src += slices_before(2);
+  sync_all();
+  n_dst += slices(1, part);
+  n_src += slices(2, part);
   int* dst = a.dst + static_cast<int64_t>(unit) * a.max_moves;
   int* src = a.src + static_cast<int64_t>(unit) * a.max_moves;
   for (int w = w0 + lane; w - lane < w1; w += 32) {
@@ -265,12 +282,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     for (; d; d &= d - 1) dst[di++] = first + __ffs(d) - 1;
     for (; s; s &= s - 1) src[si++] = first + __ffs(s) - 1;
   }
-  if (part == 0 && tid == 0) {
-    int s = 0;
-    for (int c = 0; c < cs; ++c) s += cluster.map_shared_rank(&sh.counts[0], c)[1];
-    a.n_moves[unit] = s;
-  }
-  cluster.sync();  // no CTA leaves while another may still read its counts
+  if (part == 0 && tid == 0) a.n_moves[unit] = slices(1, cs);
+  if (!alone) cluster.sync();  // no CTA leaves while another may still read its counts
 }
 
 // Block (part of a head's moves, head): 16 bytes per thread and step, four
@@ -316,28 +329,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, i
 
 }  // namespace
 
-cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
-  const int units = a.p.B * a.p.h_kv;
-  // Double the cluster while the CTAs are fewer than four per SM and each has
-  // more than 2048 slots; a slice that would pass kMaxRanks asks for more too.
-  int cs = 1;
-  while (cs < kMaxCluster && ((static_cast<int64_t>(units) * cs * 2 <= 4 * a.num_sms && a.p.L_max / cs > 2048) ||
-                              a.p.L_max / cs > kMaxRanks))
-    cs *= 2;
-  const int per = ((a.p.L_max + cs - 1) / cs + 31) / 32 * 32;
-  const int cached = per < kMaxRanks ? per : kMaxRanks;
-  const size_t smem = (static_cast<size_t>(cached) + per / 32) * sizeof(uint32_t);
-  if (smem > kMaxSelectSmem) return cudaErrorInvalidValue;  // refused by the entry point before
+namespace {
+
+template <int T, bool kAll>
+cudaError_t launch_select(const EvictArgs& a, int cs, int cached, size_t smem, cudaStream_t s) {
+  auto* kernel = evict_select_kernel<T, kAll>;
   static OncePerDevice once;
-  cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kMaxSelectSmem);
-  });
+  const cudaError_t e = once.run(
+      [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSelectSmem); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3(units * cs);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(a.p.B * a.p.h_kv * cs);
+  cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -345,15 +349,41 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cached);
+  return cudaLaunchKernelEx(&cfg, kernel, a, cached);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
+  const int units = a.p.B * a.p.h_kv;
+  // Spread a head over a cluster while that leaves no SM two CTAs and each
+  // still has 8192 slots (64 heads of 33000: 1, 2, 4, 8 CTAs took 32, 27, 33,
+  // 68 us; 8 heads of 131072: 231, 112, 35, 31; 8 of 4097: 11.5 and, with 2,
+  // 14.0); a slice that would pass kMaxRanks asks for more too.
+  int cs = 1;
+  while (cs < kMaxCluster &&
+         ((static_cast<int64_t>(units) * cs * 2 <= a.num_sms && a.p.L_max / cs > 8192) || a.p.L_max / cs > kMaxRanks))
+    cs *= 2;
+  const int per = ((a.p.L_max + cs - 1) / cs + 31) / 32 * 32;
+  const int cached = per < kMaxRanks ? per : kMaxRanks;
+  const size_t smem = (static_cast<size_t>(cached) + per / 32) * sizeof(uint32_t);
+  if (smem > kMaxSelectSmem) return cudaErrorInvalidValue;  // refused by the entry point before
+  // 1024 threads, but 256 for short heads that are many: their CTAs then share
+  // an SM six or more at a time (512 heads of 4352: 32 us, 34 with 512 threads,
+  // 41 with 1024; 128 of 8192: 46, 43, 41)
+  const bool small = per <= 1024 || (per <= 6144 && static_cast<int64_t>(units) * cs > 2 * a.num_sms);
+  cudaError_t e = per > kMaxRanks ? launch_select<1024, false>(a, cs, cached, smem, s)
+                  : small         ? launch_select<256, true>(a, cs, cached, smem, s)
+                                  : launch_select<1024, true>(a, cs, cached, smem, s);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
   // enough blocks for the most rows that can move, 4 steps of a block each
   int64_t chunks = 0;
   for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
   int64_t per_unit = a.max_moves * chunks / (4 * kMoveThreads);
   const int64_t most = (16 * a.num_sms + units - 1) / units;  // and no more than fill the GPU twice
   per_unit = per_unit < 1 ? 1 : per_unit > most ? most : per_unit;
-  cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * per_unit));
   cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = s;
