@@ -91,6 +91,7 @@ struct Kv4RowsArgs {
   int* positions;
   const int* first_position;
   uint32_t* status;
+  int step_i, step_g;  // a pass of rows onward, in tokens and heads (set by the launchers)
 };
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s);

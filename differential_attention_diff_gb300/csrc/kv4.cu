@@ -3,10 +3,11 @@
 //
 // A record (layout in diffattn.h) holds a key and a value row; each row has
 // two groups of d/2 features with value = s * code + m, m the group's
-// minimum and s = bf16(range / 15).  Both kernels give a row to d/8 lanes of
-// 8 features each: one 16-byte access on the bf16 side and one 4-byte word of
-// codes on the other, so a warp touches whole contiguous rows.  A group's
-// minimum and maximum come from shuffles over its d/16 lanes.
+// minimum and s = bf16(range / 15).  Both kernels give a row to d/16 lanes of
+// 16 features each: two 16-byte accesses on the bf16 side and 8 bytes of codes
+// on the other, so a warp touches whole contiguous rows.  Neither is bound by
+// memory alone: with 656 bytes moved per record, an SM has about 28 cycles for
+// one, so what counts is the instructions per feature.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -28,177 +29,245 @@ __device__ __forceinline__ bool sequence_rows(const Kv4RowsArgs& a, int b, bool 
   return false;
 }
 
-// A block's rows: kRows passes of kThreads / (D/8) rows each, out of the
-// sequence's N * h_kv * 2 (row = (i * h_kv + g) * 2 + is_value).  Loading
-// kRows rows before the first is used keeps enough bytes in flight.
-constexpr int kRows = 4;
+// A block's rows: kBatches x kRows passes of kThreads / (D/16) rows each, out
+// of the sequence's N * h_kv * 2 (row = (i * h_kv + g) * 2 + is_value; a pass
+// is an even number of rows, so a thread has keys only or values only).
+// Loading kRows rows before the first is used keeps enough bytes in flight;
+// the batches spread the set-up.
+constexpr int kRows = 2;
+constexpr int kBatches = 4;
 
-struct RowAt {
-  bool live;
-  bool is_v;
+// Byte offset of a thread's row in a [N, h_kv] array, and its token and head,
+// walked from pass to pass with additions only: 64-bit products per row would
+// be half of the kernels' instructions.
+struct RowWalk {
+  int64_t at;
   int i, g;
+  __device__ RowWalk(unsigned r, int h_kv, int64_t sn, int64_t sh) {
+    const unsigned u = r >> 1, h = static_cast<unsigned>(h_kv);
+    i = static_cast<int>(u / h);
+    g = static_cast<int>(u - i * h);
+    at = i * sn + g * sh;
+  }
+  __device__ __forceinline__ void next(const Kv4RowsArgs& a, int64_t step, int64_t wrap) {
+    i += a.step_i;
+    g += a.step_g;
+    at += step;
+    if (g >= a.h_kv) {
+      g -= a.h_kv;
+      ++i;
+      at += wrap;
+    }
+  }
 };
-__device__ __forceinline__ RowAt row_at(const Kv4RowsArgs& a, unsigned r, unsigned rows) {
-  RowAt x;
-  const unsigned u = r >> 1;
-  x.is_v = r & 1;
-  x.i = static_cast<int>(u / static_cast<unsigned>(a.h_kv));
-  x.g = static_cast<int>(u % static_cast<unsigned>(a.h_kv));
-  x.live = r < rows;
-  return x;
-}
 
-// Quantisation needs the exactly rounded quotient only where it is near a tie
-// between two codes; elsewhere a product with the reciprocal, off by at most
-// 2^-21 of 15, rounds to the same code.
-__device__ __forceinline__ uint32_t code_of(float t, float s, float inv) {
-  float q = t * inv, n = rintf(q);
-  if (!(fabsf(q - n) < 0.4999f)) n = rintf(__fdiv_rn(t, s));  // also where inv overflowed
-  return static_cast<uint32_t>(fminf(n, 15.f));
+// Eight codes of bf16 pairs w: rint((x - lo) / s) for (x - lo) in
+// [0, 15.03 s], exactly, without a division.  f is the quotient less a half,
+// rounded, so that the code is f or f + 1 whatever the reciprocal's error, and
+// c = (f + 1/2) s, which fp32 holds exactly (f has 4 bits and s 8), decides; a
+// tie goes to the even one, so for an odd f the comparison is against the
+// number just below c.  f stays in the low bits of 1.5 2^23 + f and the codes
+// are summed with those bits; what the eight constants add to is taken off.
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, float s, float inv) {
+  constexpr float kMagic = 12582912.f;  // 0x4b400000
+  const float half_s = 0.5f * s;
+  uint32_t sum = 0;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    const float t = __fsub_rn((e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]), lo);
+    const float r = fmaf(t, inv, -0.5f) + kMagic;
+    const uint32_t bits = __float_as_uint(r);
+    const float c = fmaf(r - kMagic, s, half_s);
+    sum = sum * 16u + bits;
+    if (t > __uint_as_float(__float_as_uint(c) - (bits & 1u))) ++sum;
+  }
+  return sum - 0x4b400000u * 0x11111111u;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4RowsArgs a) {
-  constexpr int kLanes = D / 8;        // of a row
-  constexpr int kGroupLanes = D / 16;  // of a group
+  constexpr int kLanes = D / 16;       // of a row
+  constexpr int kGroupLanes = D / 32;  // of a group
   constexpr int kPass = kThreads / kLanes;
   const int l = threadIdx.x % kLanes;
-  const unsigned r0 = blockIdx.x * (kRows * kPass) + threadIdx.x / kLanes;
+  const unsigned r0 = blockIdx.x * (kBatches * kRows * kPass) + threadIdx.x / kLanes;
+  const bool is_v = r0 & 1;
+  const int64_t sn = 2 * (is_v ? a.v.sn : a.k.sn), sh = 2 * (is_v ? a.v.sh : a.k.sh), sb = 2 * (is_v ? a.v.sb : a.k.sb);
+  const int64_t step = a.step_i * sn + a.step_g * sh, wrap = sn - a.h_kv * sh;
+  const int64_t step_c = a.step_i * a.cache.sn + a.step_g * a.cache.sh, wrap_c = a.cache.sn - a.h_kv * a.cache.sh;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     int start, count;
     if (!sequence_rows(a, b, blockIdx.x == 0 && threadIdx.x == 0, start, count)) continue;
     const unsigned rows = static_cast<unsigned>(count) * a.h_kv * 2;
-    if (blockIdx.x * (kRows * kPass) >= rows) continue;
-    uint4 in[kRows];
+    if (blockIdx.x * (kBatches * kRows * kPass) >= rows) continue;
+    const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v.ptr : a.k.ptr) + b * sb + l * 32;
+    uint8_t* to = static_cast<uint8_t*>(a.cache.ptr) + b * a.cache.sb + start * a.cache.sn;
+    RowWalk wi(r0, a.h_kv, sn, sh), wo(r0, a.h_kv, a.cache.sn, a.cache.sh);
+    unsigned r = r0;
+#pragma unroll 1
+    for (int batch = 0; batch < kBatches; ++batch) {
+      if (r - threadIdx.x / kLanes >= rows) break;  // the whole block's
+      uint4 in[kRows][2];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const RowAt x = row_at(a, r0 + j * kPass, rows);
-      const da_t4& src = x.is_v ? a.v : a.k;
-      in[j] = make_uint4(0, 0, 0, 0);
-      if (x.live)
-        in[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src.ptr) + b * src.sb +
-                                                      x.i * src.sn + x.g * src.sh + l * 8));
-    }
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const RowAt r = row_at(a, r0 + j * kPass, rows);
-      const uint32_t ws[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = bf16_lo(ws[e]);
-        x[2 * e + 1] = bf16_hi(ws[e]);
-      }
-      float lo = x[0], hi = x[0];
-      bool nan = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo = fminf(lo, x[e]);
-        hi = fmaxf(hi, x[e]);
-        nan |= x[e] != x[e];
-      }
-      // a NaN is ignored by fminf / fmaxf: carry it as an infinite maximum
-      if (nan) hi = INFINITY;
-#pragma unroll
-      for (int o = 1; o < kGroupLanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      }
-      float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
-      const bool bad = !(fabsf(s) < INFINITY);
-      uint32_t codes = 0;
-      if (!bad && s > 0.f) {
-        const float inv = __frcp_rn(s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) codes |= code_of(__fsub_rn(x[e], lo), s, inv) << (4 * e);
-      }
-      if (bad) s = lo = NAN;
-      // both groups' parameters at the row's first lane
-      const uint32_t mine = pack_bf16x2(s, lo);
-      const uint32_t other = __shfl_down_sync(0xffffffffu, mine, kGroupLanes);
-      if (!r.live) continue;
-      uint8_t* rec = static_cast<uint8_t*>(a.cache.ptr) + b * a.cache.sb +
-                     (static_cast<int64_t>(start) + r.i) * a.cache.sn + r.g * a.cache.sh;
-      *reinterpret_cast<uint32_t*>(rec + (r.is_v ? D / 2 : 0) + l * 4) = codes;
-      if (l == 0) {
-        *reinterpret_cast<uint2*>(rec + D + (r.is_v ? 8 : 0)) =
-            make_uint2(__byte_perm(mine, other, 0x5410), __byte_perm(mine, other, 0x7632));
-        if (!r.is_v) {
-          const int64_t at = (static_cast<int64_t>(b) * a.h_kv + r.g) * a.L_max + start + r.i;
-          if (a.key_weights) a.key_weights[at] = 0.f;
-          if (a.positions) a.positions[at] = (a.first_position ? a.first_position[b] : start) + r.i;
+      for (int j = 0; j < kRows; ++j) {
+        in[j][0] = in[j][1] = make_uint4(0, 0, 0, 0);
+        if (r + j * kPass < rows) {
+          in[j][0] = __ldcs(reinterpret_cast<const uint4*>(from + wi.at));
+          in[j][1] = __ldcs(reinterpret_cast<const uint4*>(from + wi.at) + 1);
         }
+        wi.next(a, step, wrap);
       }
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const uint32_t w0[4] = {in[j][0].x, in[j][0].y, in[j][0].z, in[j][0].w};
+        const uint32_t w1[4] = {in[j][1].x, in[j][1].y, in[j][1].z, in[j][1].w};
+        const __nv_bfloat162 *x0 = reinterpret_cast<const __nv_bfloat162*>(w0), *x1 = reinterpret_cast<const __nv_bfloat162*>(w1);
+        // both halves' minimum and maximum at once; NaN stays
+        __nv_bfloat162 lo2 = __hmin2_nan(x0[0], x1[0]), hi2 = __hmax2_nan(x0[0], x1[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) {
+          lo2 = __hmin2_nan(lo2, __hmin2_nan(x0[e], x1[e]));
+          hi2 = __hmax2_nan(hi2, __hmax2_nan(x0[e], x1[e]));
+        }
+#pragma unroll
+        for (int o = 1; o < kGroupLanes; o <<= 1) {
+          lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+          hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+        }
+        float lo = __bfloat162float(__hmin_nan(lo2.x, lo2.y));
+        const float hi = __bfloat162float(__hmax_nan(hi2.x, hi2.y));
+        float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
+        const bool bad = !(fabsf(s) < INFINITY);
+        uint2 codes = make_uint2(0, 0);
+        if (s >= 0x1p-100f && !bad) {
+          const float inv = __frcp_rn(s);
+          codes = make_uint2(codes_of(w0, lo, s, inv), codes_of(w1, lo, s, inv));
+        } else if (s > 0.f && !bad) {  // the reciprocal or the half step may not be normal numbers
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t w = (e & 8) ? w1[(e & 7) >> 1] : w0[e >> 1];
+            const float x = (e & 1) ? bf16_hi(w) : bf16_lo(w);
+            const uint32_t n = static_cast<uint32_t>(fminf(rintf(__fdiv_rn(__fsub_rn(x, lo), s)), 15.f));
+            if (e & 8)
+              codes.y |= n << (4 * (e & 7));
+            else
+              codes.x |= n << (4 * e);
+          }
+        }
+        if (bad) s = lo = NAN;
+        // both groups' parameters at the row's first lane
+        const uint32_t mine = pack_bf16x2(s, lo);
+        const uint32_t other = __shfl_down_sync(0xffffffffu, mine, kGroupLanes);
+        if (r + j * kPass < rows) {
+          uint8_t* rec = to + wo.at;
+          *reinterpret_cast<uint2*>(rec + (is_v ? D / 2 : 0) + l * 8) = codes;
+          if (l == 0) {
+            *reinterpret_cast<uint2*>(rec + D + (is_v ? 8 : 0)) =
+                make_uint2(__byte_perm(mine, other, 0x5410), __byte_perm(mine, other, 0x7632));
+            if (!is_v && (a.key_weights || a.positions)) {
+              const int64_t at = (static_cast<int64_t>(b) * a.h_kv + wo.g) * a.L_max + start + wo.i;
+              if (a.key_weights) a.key_weights[at] = 0.f;
+              if (a.positions) a.positions[at] = (a.first_position ? a.first_position[b] : start) + wo.i;
+            }
+          }
+        }
+        wo.next(a, step_c, wrap_c);
+      }
+      r += kRows * kPass;
     }
   }
 }
 
+// Four output words of eight codes.  A code byte times 0x1001 has its lower
+// code at bit 0 and its upper one at bit 16; set into the mantissa of bf16 128
+// each is 128 plus the code, and the fused multiply-add of s, code and m, all
+// exact in bf16, rounds once.
+__device__ __forceinline__ uint4 values_of(uint32_t codes, uint32_t s_twice, uint32_t m_twice) {
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s_twice);
+  const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&m_twice);
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t y = __byte_perm(codes, 0u, 0x4440u + e) * 0x1001u;
+    const uint32_t n = (y & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hfma2(s, __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&n), __nv_bfloat162(128.f, 128.f)), m);
+    out[e] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(Kv4RowsArgs a) {
-  constexpr int kLanes = D / 8;
+__global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(Kv4RowsArgs a) {
+  constexpr int kLanes = D / 16;
   constexpr int kPass = kThreads / kLanes;
   const int l = threadIdx.x % kLanes;
-  const unsigned r0 = blockIdx.x * (kRows * kPass) + threadIdx.x / kLanes;
+  const unsigned r0 = blockIdx.x * (kBatches * kRows * kPass) + threadIdx.x / kLanes;
+  const bool is_v = r0 & 1;
+  const int64_t sn = 2 * (is_v ? a.v.sn : a.k.sn), sh = 2 * (is_v ? a.v.sh : a.k.sh), sb = 2 * (is_v ? a.v.sb : a.k.sb);
+  const int64_t step = a.step_i * sn + a.step_g * sh, wrap = sn - a.h_kv * sh;
+  const int64_t step_c = a.step_i * a.cache.sn + a.step_g * a.cache.sh, wrap_c = a.cache.sn - a.h_kv * a.cache.sh;
+  // a lane takes 8 features of each group, so that the lanes' stores lie side by side
+  const int code_at = (is_v ? D / 2 : 0) + l * 4, par_at = D + (is_v ? 8 : 0);
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     int start, count;
     if (!sequence_rows(a, b, blockIdx.x == 0 && threadIdx.x == 0, start, count)) continue;
     const unsigned rows = static_cast<unsigned>(count) * a.h_kv * 2;
-    if (blockIdx.x * (kRows * kPass) >= rows) continue;
-    uint32_t codes[kRows];
-    uint2 par[kRows];
+    if (blockIdx.x * (kBatches * kRows * kPass) >= rows) continue;
+    const uint8_t* from = static_cast<const uint8_t*>(a.cache.ptr) + b * a.cache.sb + start * a.cache.sn;
+    uint8_t* to = static_cast<uint8_t*>(is_v ? a.v.ptr : a.k.ptr) + b * sb + l * 16;
+    RowWalk wi(r0, a.h_kv, a.cache.sn, a.cache.sh), wo(r0, a.h_kv, sn, sh);
+    unsigned r = r0;
+    constexpr int kAhead = kRows * 2;
+#pragma unroll 1
+    for (int batch = 0; batch < kBatches / 2; ++batch) {
+      uint2 codes[kAhead], par[kAhead];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const RowAt r = row_at(a, r0 + j * kPass, rows);
-      codes[j] = 0;
-      par[j] = make_uint2(0, 0);
-      if (!r.live) continue;
-      const uint8_t* rec = static_cast<const uint8_t*>(a.cache.ptr) + b * a.cache.sb +
-                           (static_cast<int64_t>(start) + r.i) * a.cache.sn + r.g * a.cache.sh;
-      codes[j] = *reinterpret_cast<const uint32_t*>(rec + (r.is_v ? D / 2 : 0) + l * 4);
-      par[j] = *reinterpret_cast<const uint2*>(rec + D + (r.is_v ? 8 : 0));
-    }
+      for (int j = 0; j < kAhead; ++j) {
+        codes[j] = par[j] = make_uint2(0, 0);
+        if (r + j * kPass < rows) {
+          codes[j].x = *reinterpret_cast<const uint32_t*>(from + wi.at + code_at);
+          codes[j].y = *reinterpret_cast<const uint32_t*>(from + wi.at + code_at + D / 4);
+          par[j] = *reinterpret_cast<const uint2*>(from + wi.at + par_at);
+        }
+        wi.next(a, step_c, wrap_c);
+      }
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const RowAt r = row_at(a, r0 + j * kPass, rows);
-      if (!r.live) continue;
-      const bool second = l >= kLanes / 2;
-      const float s = second ? bf16_hi(par[j].x) : bf16_lo(par[j].x);
-      const float m = second ? bf16_hi(par[j].y) : bf16_lo(par[j].y);
-      uint32_t out[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        out[e] = pack_bf16x2(fmaf(s, static_cast<float>((codes[j] >> (8 * e)) & 15u), m),
-                             fmaf(s, static_cast<float>((codes[j] >> (8 * e + 4)) & 15u), m));
-      const da_t4& dst = r.is_v ? a.v : a.k;
-      __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst.ptr) + b * dst.sb + r.i * dst.sn +
-                                      r.g * dst.sh + l * 8),
-             make_uint4(out[0], out[1], out[2], out[3]));
+      for (int j = 0; j < kAhead; ++j) {
+        if (r + j * kPass < rows) {
+          const uint32_t s0 = __byte_perm(par[j].x, 0u, 0x1010), m0 = __byte_perm(par[j].y, 0u, 0x1010);
+          const uint32_t s1 = __byte_perm(par[j].x, 0u, 0x3232), m1 = __byte_perm(par[j].y, 0u, 0x3232);
+          __stcs(reinterpret_cast<uint4*>(to + wo.at), values_of(codes[j].x, s0, m0));
+          __stcs(reinterpret_cast<uint4*>(to + wo.at + D), values_of(codes[j].y, s1, m1));
+        }
+        wo.next(a, step, wrap);
+      }
+      r += kAhead * kPass;
     }
   }
 }
 
 // Blocks of rows of one sequence along x, sequences along y.
 dim3 grid_for(const Kv4RowsArgs& a) {
-  const unsigned rows = static_cast<unsigned>(a.N) * a.h_kv * 2, per = kRows * kThreads / (a.d / 8);
+  const unsigned rows = static_cast<unsigned>(a.N) * a.h_kv * 2, per = kBatches * kRows * kThreads / (a.d / 16);
   return dim3((rows + per - 1) / per, a.B < 65535 ? a.B : 65535);
+}
+
+template <class F>
+cudaError_t launch_rows(F kernel, Kv4RowsArgs a, cudaStream_t s) {
+  const int records = kThreads / (a.d / 16) / 2;  // of a pass
+  a.step_i = records / a.h_kv;
+  a.step_g = records % a.h_kv;
+  kernel<<<grid_for(a), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s) {
-  if (a.d == 128)
-    kv4_append_kernel<128><<<grid_for(a), kThreads, 0, s>>>(a);
-  else
-    kv4_append_kernel<64><<<grid_for(a), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.d == 128 ? launch_rows(kv4_append_kernel<128>, a, s) : launch_rows(kv4_append_kernel<64>, a, s);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s) {
-  if (a.d == 128)
-    kv4_read_kernel<128><<<grid_for(a), kThreads, 0, s>>>(a);
-  else
-    kv4_read_kernel<64><<<grid_for(a), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.d == 128 ? launch_rows(kv4_read_kernel<128>, a, s) : launch_rows(kv4_read_kernel<64>, a, s);
 }
 
 }  // namespace da

@@ -100,7 +100,7 @@ da_status diffattn_kv4_append(const da_kv4_append_params* p, void* stream) {
   int sms;
   if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
   const da::Kv4RowsArgs a{p->B, p->N, p->h_kv, p->d, p->L_max, p->k, p->v, p->cache, p->start, p->counts,
-                          p->key_weights, p->positions, p->first_position, status};
+                          p->key_weights, p->positions, p->first_position, status, 0, 0};
   return cuda_status(da::launch_kv4_append(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -114,7 +114,7 @@ da_status diffattn_kv4_read(const da_kv4_read_params* p, void* stream) {
   int sms;
   if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
   const da::Kv4RowsArgs a{p->B, p->N, p->h_kv, p->d, p->L_max, p->k_out, p->v_out, p->cache, p->start, p->counts,
-                          nullptr, nullptr, nullptr, status};
+                          nullptr, nullptr, nullptr, status, 0, 0};
   return cuda_status(da::launch_kv4_read(a, static_cast<cudaStream_t>(stream)));
 }
 
