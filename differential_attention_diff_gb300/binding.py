@@ -639,22 +639,21 @@ def _rows4(t, shape, dtype, dev, name):
     return da_t4(t.data_ptr(), sb, sn, sh)
 
 
-def _new(make, shape, dtype, dev, stream):
-    """A tensor made on the stream that the call launches on, so that its
-    memory (and its zeros) are ordered with the launch."""
+def _new(make, like, shape, dtype, stream):
+    """make (torch.empty or torch.zeros) on the device of `like`, on the stream
+    that the call launches on, so that its memory (and its zeros) are ordered
+    with the launch."""
     if stream is None:
-        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+        return make(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+        return make(shape, dtype=dtype, device=like.device)
 
 
-def _space(workspace, need, dev, stream):
-    """(tensor, pointer, bytes) of a workspace: the given one, or a new one."""
-    if workspace is None:
-        workspace = _new(torch.empty, (max(need(), 1),), torch.uint8, dev, stream)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
+def _space(workspace, dev):
+    """(pointer, bytes) of a workspace."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on device {dev} expected")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def diffattn_kv4_record_bytes(d) -> int:
@@ -691,9 +690,9 @@ def diffattn_kv4_read(cache, N, *, start=None, counts=None, k_out=None, v_out=No
     d, bf16 = rec - 16, torch.bfloat16
     shape = (B, N, hkv, d)
     if k_out is None:
-        k_out = _new(torch.zeros, shape, bf16, dev, stream)
+        k_out = _new(torch.zeros, cache, shape, bf16, stream)
     if v_out is None:
-        v_out = _new(torch.zeros, shape, bf16, dev, stream)
+        v_out = _new(torch.zeros, cache, shape, bf16, stream)
     p = da_kv4_read_params(
         B, N, hkv, d, L_max, _rows4(cache, (B, L_max, hkv, rec), torch.uint8, dev, "cache"),
         _array(start, (B,), torch.int32, dev, "start"), _array(counts, (B,), torch.int32, dev, "counts"),
@@ -727,9 +726,11 @@ def diffattn_v2_decode_kv4(q, cache, *, seqlens=None, gate=None, x=None, w_lambd
     L_max, hkv = cache.shape[1], cache.shape[2]
     h, bf16, f32 = H2 // 2, torch.bfloat16, torch.float32
     if out is None:
-        out = _new(torch.empty, (B, h, d), bf16, dev, stream)
-    ws, ws_ptr, ws_bytes = _space(workspace, lambda: diffattn_v2_decode_kv4_workspace_size(
-        B, h, hkv, d, L_max, gate is not None, weights_out is not None), dev, stream)
+        out = _new(torch.empty, q, (B, h, d), bf16, stream)
+    if workspace is None:
+        need = diffattn_v2_decode_kv4_workspace_size(B, h, hkv, d, L_max, gate is not None, weights_out is not None)
+        workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
+    ws_ptr, ws_bytes = _space(workspace, dev)
     gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
     p = da_v2_decode_kv4_params(
         B, h, hkv, d, L_max, d_model, softmax_scale, _array(q, (B, 2 * h, d), bf16, dev, "q"),
@@ -758,9 +759,11 @@ def diffattn_v2_decode_weighted(q, k_cache, v_cache, *, weights_out, weights_in=
     L_max, hkv = shape[1], shape[2]
     h, bf16, f32 = H2 // 2, torch.bfloat16, torch.float32
     if out is None:
-        out = _new(torch.empty, (B, h, d), bf16, dev, stream)
-    ws, ws_ptr, ws_bytes = _space(workspace, lambda: diffattn_v2_decode_weighted_workspace_size(
-        B, h, hkv, d, L_max, num_splits, gate is not None), dev, stream)
+        out = _new(torch.empty, q, (B, h, d), bf16, stream)
+    if workspace is None:
+        need = diffattn_v2_decode_weighted_workspace_size(B, h, hkv, d, L_max, num_splits, gate is not None)
+        workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
+    ws_ptr, ws_bytes = _space(workspace, dev)
     gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
     dec = da_v2_decode_params(
         B, h, hkv, d, L_max, d_model, softmax_scale, _array(q, (B, 2 * h, d), bf16, dev, "q"),
@@ -796,8 +799,11 @@ def diffattn_kv_evict(rows, key_weights, keep, *, sinks=0, recent=0, seqlens=Non
     if positions_out is None:
         positions_out = positions
     if seqlens_out is None:
-        seqlens_out = _new(torch.empty, (B,), i32, dev, stream) if seqlens is None else seqlens
-    ws, ws_ptr, ws_bytes = _space(workspace, lambda: diffattn_kv_evict_workspace_size(B, hkv, L_max, keep), dev, stream)
+        seqlens_out = _new(torch.empty, key_weights, (B,), i32, stream) if seqlens is None else seqlens
+    if workspace is None:
+        need = diffattn_kv_evict_workspace_size(B, hkv, L_max, keep)
+        workspace = _new(torch.empty, key_weights, (max(need, 1),), torch.uint8, stream)
+    ws_ptr, ws_bytes = _space(workspace, dev)
     p = da_kv_evict_params(
         B, hkv, L_max, keep, sinks, recent, _array(seqlens, (B,), i32, dev, "seqlens"),
         _array(seqlens_out, (B,), i32, dev, "seqlens_out"), _array(key_weights, shape, f32, dev, "key_weights"),

@@ -242,7 +242,7 @@ da_status run_v2_decode(const da_v2_decode_params* p, const float* weights_in, f
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.f / std::sqrt(static_cast<float>(p->d));
   da::DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, splits, scale * kLog2e,
                    p->q, p->k_cache, p->v_cache, p->seqlens, gate, p->out,
-                   part_o, part_ml, d.status, scores};
+                   part_o, part_ml, d.status, scores, p->gate == nullptr};
   cudaError_t e = da::launch_decode(a, s);
   if (e == cudaSuccess && weights_out) {
     const da::KeyWeightsArgs w{p->B, p->h, p->h_kv, p->L_max, splits, nullptr, p->seqlens, gate, part_ml, scores,

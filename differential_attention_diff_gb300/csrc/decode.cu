@@ -264,12 +264,16 @@ decode_split_kernel(DecodeArgs a) {
       a.part_ml[pidx * 2 + 1] = lt;
     }
   }
+  // the gate, where it runs beside this kernel: the merge counts on its end
+  if constexpr (kScores) cudaGridDependencySynchronize();
 }
 
 // Merge the splits of one pair and apply the gate.  Block = d threads, one
-// feature each; grid (h, B).
+// feature each; grid (h, B).  kAhead: launched before the split kernel's end.
+template <bool kAhead>
 __global__ void __launch_bounds__(128)
 decode_merge_kernel(DecodeArgs a) {
+  if constexpr (kAhead) cudaGridDependencySynchronize();
   const int p = blockIdx.x, b = blockIdx.y, col = threadIdx.x;
   const int H2 = 2 * a.h;
   float res[2];
@@ -302,6 +306,8 @@ cudaError_t launch_split(const DecodeArgs& a, cudaStream_t s) {
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 g1(a.num_splits, a.h_kv, a.B);
+  if constexpr (kScores)
+    return launch_ahead(decode_split_kernel<D, true>, g1, dim3(kWarps * 32), kSmemBytes, s, a.after_gate, a);
   decode_split_kernel<D, kScores><<<g1, kWarps * 32, kSmemBytes, s>>>(a);
   return cudaGetLastError();
 }
@@ -317,7 +323,8 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
     e = a.d == 128 ? launch_split<128, false>(a, s) : launch_split<64, false>(a, s);
   if (e != cudaSuccess) return e;
   dim3 g2(a.h, a.B);
-  decode_merge_kernel<<<g2, a.d, 0, s>>>(a);
+  if (a.scores) return launch_ahead(decode_merge_kernel<true>, g2, dim3(a.d), 0, s, true, a);
+  decode_merge_kernel<false><<<g2, a.d, 0, s>>>(a);
   return cudaGetLastError();
 }
 

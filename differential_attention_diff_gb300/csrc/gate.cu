@@ -73,6 +73,9 @@ template <int kStages>
 __global__ void __launch_bounds__(128)
 gate_kernel(GateArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
+  // a decode launched to overlap this kernel may start (it does not read the
+  // gate before its own end); no effect on other launches
+  cudaTriggerProgrammaticLaunchCompletion();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * kTok;
   const int S = static_cast<int>(gridDim.y);

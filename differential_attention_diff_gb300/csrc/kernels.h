@@ -48,6 +48,7 @@ struct DecodeArgs {
   float* part_ml;     // [splits, B, 2h, 2]  (running max in log2 units, sum)
   uint32_t* status;
   float* scores;      // [B, h_kv, L_max, G] scaled scores in log2 units, or null
+  bool after_gate;    // the kernel launched just before is this call's gate (used with scores)
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 // The split count is a grid dimension (at most 65535).
@@ -59,6 +60,25 @@ da_status check_v2_decode_args(const da_v2_decode_params* p);
 // ---- device handles shared by the entry points ------------------------------
 // The current device's status word and SM count; false if they cannot be had.
 bool device_handles(uint32_t** status, int* num_sms);
+
+// Launches a kernel that may start before the one launched just before it has
+// ended (programmatic stream serialization): it waits for that one's end itself
+// (cudaGridDependencySynchronize) before it reads what that one writes, or
+// before its own end.
+template <class... P, class... A>
+cudaError_t launch_ahead(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool ahead, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = ahead ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 // Runs a set-up call (a kernel attribute, say) once on each device: with its
 // result on the first call there, cudaSuccess on later ones.
@@ -114,6 +134,7 @@ struct Kv4DecodeArgs {
   const float* weights_in;
   float* weights_out;
   uint32_t* status;
+  bool after_gate;    // the kernel launched just before is this call's gate
 };
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 

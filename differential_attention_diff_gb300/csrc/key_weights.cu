@@ -101,16 +101,8 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a)
 
 template <int P>
 cudaError_t launch_pairs(const KeyWeightsArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((a.L_max + kThreads * kKeys - 1) / (kThreads * kKeys), a.h_kv, a.B);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<P>, a);
+  const dim3 grid((a.L_max + kThreads * kKeys - 1) / (kThreads * kKeys), a.h_kv, a.B);
+  return launch_ahead(key_weights_kernel<P>, grid, dim3(kThreads), 0, s, true, a);
 }
 
 }  // namespace

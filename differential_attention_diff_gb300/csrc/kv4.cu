@@ -35,7 +35,7 @@ __device__ __forceinline__ bool sequence_rows(const Kv4RowsArgs& a, int b, bool 
 // Loading kRows rows before the first is used keeps enough bytes in flight;
 // the batches spread the set-up.
 constexpr int kRows = 2;
-constexpr int kBatches = 4;
+constexpr int kBatches = 4;  // 1 where the rows are too few to fill the GPU with that many each
 
 // Byte offset of a thread's row in a [N, h_kv] array, and its token and head,
 // walked from pass to pass with additions only: 64-bit products per row would
@@ -85,12 +85,12 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, f
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4RowsArgs a) {
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4RowsArgs a, int batches) {
   constexpr int kLanes = D / 16;       // of a row
   constexpr int kGroupLanes = D / 32;  // of a group
   constexpr int kPass = kThreads / kLanes;
   const int l = threadIdx.x % kLanes;
-  const unsigned r0 = blockIdx.x * (kBatches * kRows * kPass) + threadIdx.x / kLanes;
+  const unsigned r0 = blockIdx.x * (batches * kRows * kPass) + threadIdx.x / kLanes;
   const bool is_v = r0 & 1;
   const int64_t sn = 2 * (is_v ? a.v.sn : a.k.sn), sh = 2 * (is_v ? a.v.sh : a.k.sh), sb = 2 * (is_v ? a.v.sb : a.k.sb);
   const int64_t step = a.step_i * sn + a.step_g * sh, wrap = sn - a.h_kv * sh;
@@ -99,13 +99,13 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4RowsArgs a) {
     int start, count;
     if (!sequence_rows(a, b, blockIdx.x == 0 && threadIdx.x == 0, start, count)) continue;
     const unsigned rows = static_cast<unsigned>(count) * a.h_kv * 2;
-    if (blockIdx.x * (kBatches * kRows * kPass) >= rows) continue;
+    if (blockIdx.x * (batches * kRows * kPass) >= rows) continue;
     const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v.ptr : a.k.ptr) + b * sb + l * 32;
     uint8_t* to = static_cast<uint8_t*>(a.cache.ptr) + b * a.cache.sb + start * a.cache.sn;
     RowWalk wi(r0, a.h_kv, sn, sh), wo(r0, a.h_kv, a.cache.sn, a.cache.sh);
     unsigned r = r0;
 #pragma unroll 1
-    for (int batch = 0; batch < kBatches; ++batch) {
+    for (int batch = 0; batch < batches; ++batch) {
       if (r - threadIdx.x / kLanes >= rows) break;  // the whole block's
       uint4 in[kRows][2];
 #pragma unroll
@@ -195,12 +195,15 @@ __device__ __forceinline__ uint4 values_of(uint32_t codes, uint32_t s_twice, uin
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// A read holds less per row than an append does: twice the rows at once.
+constexpr int kReadRows = 2 * kRows;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(Kv4RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(Kv4RowsArgs a, int batches) {
   constexpr int kLanes = D / 16;
   constexpr int kPass = kThreads / kLanes;
   const int l = threadIdx.x % kLanes;
-  const unsigned r0 = blockIdx.x * (kBatches * kRows * kPass) + threadIdx.x / kLanes;
+  const unsigned r0 = blockIdx.x * (batches * kReadRows * kPass) + threadIdx.x / kLanes;
   const bool is_v = r0 & 1;
   const int64_t sn = 2 * (is_v ? a.v.sn : a.k.sn), sh = 2 * (is_v ? a.v.sh : a.k.sh), sb = 2 * (is_v ? a.v.sb : a.k.sb);
   const int64_t step = a.step_i * sn + a.step_g * sh, wrap = sn - a.h_kv * sh;
@@ -211,17 +214,17 @@ __global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(Kv4RowsArgs a) {
     int start, count;
     if (!sequence_rows(a, b, blockIdx.x == 0 && threadIdx.x == 0, start, count)) continue;
     const unsigned rows = static_cast<unsigned>(count) * a.h_kv * 2;
-    if (blockIdx.x * (kBatches * kRows * kPass) >= rows) continue;
+    if (blockIdx.x * (batches * kReadRows * kPass) >= rows) continue;
     const uint8_t* from = static_cast<const uint8_t*>(a.cache.ptr) + b * a.cache.sb + start * a.cache.sn;
     uint8_t* to = static_cast<uint8_t*>(is_v ? a.v.ptr : a.k.ptr) + b * sb + l * 16;
     RowWalk wi(r0, a.h_kv, a.cache.sn, a.cache.sh), wo(r0, a.h_kv, sn, sh);
     unsigned r = r0;
-    constexpr int kAhead = kRows * 2;
 #pragma unroll 1
-    for (int batch = 0; batch < kBatches / 2; ++batch) {
-      uint2 codes[kAhead], par[kAhead];
+    for (int batch = 0; batch < batches; ++batch) {
+      if (r - threadIdx.x / kLanes >= rows) break;  // the whole block's
+      uint2 codes[kReadRows], par[kReadRows];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+      for (int j = 0; j < kReadRows; ++j) {
         codes[j] = par[j] = make_uint2(0, 0);
         if (r + j * kPass < rows) {
           codes[j].x = *reinterpret_cast<const uint32_t*>(from + wi.at + code_at);
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(Kv4RowsArgs a) {
         wi.next(a, step_c, wrap_c);
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+      for (int j = 0; j < kReadRows; ++j) {
         if (r + j * kPass < rows) {
           const uint32_t s0 = __byte_perm(par[j].x, 0u, 0x1010), m0 = __byte_perm(par[j].y, 0u, 0x1010);
           const uint32_t s1 = __byte_perm(par[j].x, 0u, 0x3232), m1 = __byte_perm(par[j].y, 0u, 0x3232);
@@ -240,34 +243,33 @@ __global__ void __launch_bounds__(kThreads, 6) kv4_read_kernel(Kv4RowsArgs a) {
         }
         wo.next(a, step, wrap);
       }
-      r += kAhead * kPass;
+      r += kReadRows * kPass;
     }
   }
 }
 
 // Blocks of rows of one sequence along x, sequences along y.
-dim3 grid_for(const Kv4RowsArgs& a) {
-  const unsigned rows = static_cast<unsigned>(a.N) * a.h_kv * 2, per = kBatches * kRows * kThreads / (a.d / 16);
-  return dim3((rows + per - 1) / per, a.B < 65535 ? a.B : 65535);
-}
-
 template <class F>
-cudaError_t launch_rows(F kernel, Kv4RowsArgs a, cudaStream_t s) {
-  const int records = kThreads / (a.d / 16) / 2;  // of a pass
-  a.step_i = records / a.h_kv;
-  a.step_g = records % a.h_kv;
-  kernel<<<grid_for(a), kThreads, 0, s>>>(a);
+cudaError_t launch_rows(F kernel, Kv4RowsArgs a, int rows_at_once, cudaStream_t s) {
+  const int pass = kThreads / (a.d / 16);  // rows
+  a.step_i = pass / 2 / a.h_kv;
+  a.step_g = pass / 2 % a.h_kv;
+  const unsigned rows = static_cast<unsigned>(a.N) * a.h_kv * 2, per = rows_at_once * pass;
+  const unsigned y = a.B < 65535 ? a.B : 65535;
+  const int most = kBatches * kRows / rows_at_once;
+  const int batches = static_cast<int64_t>(rows) * y / (static_cast<int64_t>(per) * most) >= 1024 ? most : 1;
+  kernel<<<dim3((rows + per * batches - 1) / (per * batches), y), kThreads, 0, s>>>(a, batches);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s) {
-  return a.d == 128 ? launch_rows(kv4_append_kernel<128>, a, s) : launch_rows(kv4_append_kernel<64>, a, s);
+  return a.d == 128 ? launch_rows(kv4_append_kernel<128>, a, kRows, s) : launch_rows(kv4_append_kernel<64>, a, kRows, s);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, cudaStream_t s) {
-  return a.d == 128 ? launch_rows(kv4_read_kernel<128>, a, s) : launch_rows(kv4_read_kernel<64>, a, s);
+  return a.d == 128 ? launch_rows(kv4_read_kernel<128>, a, kReadRows, s) : launch_rows(kv4_read_kernel<64>, a, kReadRows, s);
 }
 
 }  // namespace da

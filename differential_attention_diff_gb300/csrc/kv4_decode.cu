@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   const int H2 = 2 * a.h, G = H2 / a.h_kv;
   const bool dense = a.cache.sn == kRec;
 
-  cudaTriggerProgrammaticLaunchCompletion();  // the merge may take its place; it waits for this kernel's end
   if (tid < kW * kS) mbar_init(smem_u32(&bars[tid]), dense ? 1 : 32);
   fence_mbar_init();
 
@@ -181,8 +180,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   }
   const int64_t total = sum * a.h_kv;
   const int64_t parts = kv4_parts(total, static_cast<int64_t>(gridDim.x) * kW);
-  // neighbouring parts on different SMs: few parts then have an SM each
-  const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  // Few parts go to an SM each; as many as there are warps go to each SM side
+  // by side, where they touch fewer pages.
+  const int64_t me = parts < static_cast<int64_t>(gridDim.x) * kW ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
+                                                                  : static_cast<int64_t>(blockIdx.x) * kW + warp;
   const bool works = me < parts;
   const int64_t first = works ? me * total / parts : 0, last = works ? (me + 1) * total / parts : 0;
   Cursor at;
@@ -210,7 +211,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     }
     from = ends[C::kThreads - 1];
   }
-  if (!works) return;
+  if (!works) {
+    cudaGridDependencySynchronize();  // the gate, where it runs beside this kernel: the merge counts on its end
+    return;
+  }
 
   auto enter = [&](Cursor& c, int begin) {  // chunks begin .. of head (c.b, c.g), as far as the part goes
     c.L = a.seqlens ? a.seqlens[c.b] : a.L_max;
@@ -603,6 +607,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       mbar_wait(bar0 + slot * 8, (parity >> slot) & 1, nullptr, 0);
       slot = slot == kS - 1 ? 0 : slot + 1;
     }
+  cudaGridDependencySynchronize();
 }
 
 // One output head's parts merged, even - gate * odd; also the two heads'
@@ -613,7 +618,6 @@ __global__ void __launch_bounds__(WAYS * D / 2) kv4_merge_kernel(Kv4DecodeArgs a
   constexpr int kWarps = WAYS * D / 2 / 32;
   __shared__ float top[2], inv[2];
   __shared__ float4 sums[WAYS][2][D / 4];
-  cudaTriggerProgrammaticLaunchCompletion();
   const int p = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = 2 * a.h / a.h_kv, g = 2 * p / G, r = 2 * p % G;
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
@@ -679,16 +683,7 @@ __global__ void __launch_bounds__(WAYS * D / 2) kv4_merge_kernel(Kv4DecodeArgs a
 template <int D, int WAYS>
 cudaError_t launch_merge(const Kv4DecodeArgs& a, cudaStream_t s) {
   static_assert(WAYS * D / 2 >= D, "a thread per feature of the output");
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3(a.h, a.B);
-  cfg.blockDim = dim3(WAYS * D / 2);
-  cfg.stream = s;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, WAYS>, a);
+  return launch_ahead(kv4_merge_kernel<D, WAYS>, dim3(a.h, a.B), dim3(WAYS * D / 2), 0, s, true, a);
 }
 
 template <int D, int NT, bool kScores>
@@ -702,8 +697,7 @@ cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
   });
   if (e != cudaSuccess) return e;
-  kernel<<<a.grid, C::kThreads, C::kRing, s>>>(a);
-  return cudaGetLastError();
+  return launch_ahead(kernel, dim3(a.grid), dim3(C::kThreads), C::kRing, s, a.after_gate, a);
 }
 
 }  // namespace

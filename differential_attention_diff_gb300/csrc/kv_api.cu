@@ -168,7 +168,7 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
                             reinterpret_cast<da::Kv4Parts*>(ws + w.parts),
                             p->weights_out ? reinterpret_cast<float2*>(ws + w.norm) : nullptr,
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
-                            p->weights_in, p->weights_out, status};
+                            p->weights_in, p->weights_out, status, p->gate == nullptr};
   return cuda_status(da::launch_kv4_decode(a, s));
 }
 

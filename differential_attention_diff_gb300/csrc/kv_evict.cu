@@ -376,22 +376,14 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
                   : small         ? launch_select<256, true>(a, cs, cached, smem, s)
                                   : launch_select<1024, true>(a, cs, cached, smem, s);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
   // enough blocks for the most rows that can move, 4 steps of a block each
   int64_t chunks = 0;
   for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
   int64_t per_unit = a.max_moves * chunks / (4 * kMoveThreads);
   const int64_t most = (16 * a.num_sms + units - 1) / units;  // and no more than fill the GPU twice
   per_unit = per_unit < 1 ? 1 : per_unit > most ? most : per_unit;
-  cfg.gridDim = dim3(static_cast<unsigned>(units * per_unit));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = s;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, static_cast<int>(per_unit));
+  return launch_ahead(evict_move_kernel, dim3(static_cast<unsigned>(units * per_unit)), dim3(kMoveThreads), 0, s, true, a,
+                      static_cast<int>(per_unit));
 }
 
 }  // namespace da
