@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 import torch
@@ -604,6 +605,40 @@ def diffattn_v2_decode_noalloc(q, k_cache, v_cache, *, seqlens=None, gate=None, 
 
 
 # ---- 4-bit KV cache, gathered key weights, eviction -------------------------
+#
+# A decode step of a small batch takes a few microseconds on the GPU, so these
+# calls pack their parameter structures with struct (a third of the time that
+# filling ctypes structures takes); the layout comes from the ctypes classes.
+
+def _codes(t):
+    if issubclass(t, C.Structure):
+        return "".join(_codes(f) for _, f in t._fields_)
+    if issubclass(t, C.Array):
+        return _codes(t._type_) * t._length_
+    return {C.c_int: "i", C.c_float: "f", C.c_int64: "q", C.c_size_t: "N", C.c_void_p: "P"}[t]
+
+
+def _packer(t):
+    s = struct.Struct("@" + _codes(t) + "0P")  # the trailing 0P pads to the pointers' alignment
+    assert s.size == C.sizeof(t), t
+    return s.pack
+
+
+_pack_append, _pack_read = _packer(da_kv4_append_params), _packer(da_kv4_read_params)
+_pack_decode_kv4, _pack_weighted = _packer(da_v2_decode_kv4_params), _packer(da_v2_decode_weighted_params)
+_pack_evict = _packer(da_kv_evict_params)
+_packed_calls = {}
+
+
+def _call(name, params, stream):
+    """Call the entry point `name` with packed parameters on a raw stream."""
+    f = _packed_calls.get(name)
+    if f is None:
+        f = _packed_calls[name] = C.CFUNCTYPE(C.c_int, C.c_char_p, C.c_void_p)((name, load()))
+    status = f(params, stream)
+    if status:
+        _check(status, name)
+
 
 def _device(t, stream):
     """The device of t, which has to be the current one (the library launches
@@ -621,22 +656,22 @@ def _device(t, stream):
 def _array(t, shape, dtype, dev, name):
     """The data pointer of a contiguous array of the given shape and type on device dev (None: no array)."""
     if t is None:
-        return None
+        return 0
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: contiguous {dtype} {shape} on device {dev} expected, got {t.dtype} "
+        raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on device {dev} expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _rows4(t, shape, dtype, dev, name):
-    """da_t4 of a tensor of the given shape and type on device dev (strides in its elements)."""
+    """The da_t4 fields of a tensor of the given shape and type on device dev (strides in its elements)."""
     if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name}: {dtype} {shape} on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
     sb, sn, sh, sx = t.stride()
     if sx != 1:
         raise ValueError(f"{name}: a contiguous last dimension expected")
-    return da_t4(t.data_ptr(), sb, sn, sh)
+    return t.data_ptr(), sb, sn, sh
 
 
 def _new(make, like, shape, dtype, stream):
@@ -653,7 +688,7 @@ def _space(workspace, dev):
     """(pointer, bytes) of a workspace."""
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on device {dev} expected")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def diffattn_kv4_record_bytes(d) -> int:
@@ -670,14 +705,13 @@ def diffattn_kv4_append(k, v, cache, *, start=None, counts=None, key_weights=Non
     dev, raw = _device(k, stream)
     B, N, hkv, d = shape = k.shape
     L_max, bf16, i32 = cache.shape[1], torch.bfloat16, torch.int32
-    p = da_kv4_append_params(
-        B, N, hkv, d, L_max, _rows4(k, shape, bf16, dev, "k"), _rows4(v, shape, bf16, dev, "v"),
-        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, dev, "cache"), _array(start, (B,), i32, dev, "start"),
-        _array(counts, (B,), i32, dev, "counts"),
-        _array(key_weights, (B, hkv, L_max), torch.float32, dev, "key_weights"),
-        _array(positions, (B, hkv, L_max), i32, dev, "positions"),
-        _array(first_position, (B,), i32, dev, "first_position"))
-    _check((_lib or load()).diffattn_kv4_append(C.byref(p), raw), "diffattn_kv4_append")
+    per_slot = (B, hkv, L_max)
+    _call("diffattn_kv4_append", _pack_append(
+        B, N, hkv, d, L_max, *_rows4(k, shape, bf16, dev, "k"), *_rows4(v, shape, bf16, dev, "v"),
+        *_rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, dev, "cache"), _array(start, (B,), i32, dev, "start"),
+        _array(counts, (B,), i32, dev, "counts"), _array(key_weights, per_slot, torch.float32, dev, "key_weights"),
+        _array(positions, per_slot, i32, dev, "positions"),
+        _array(first_position, (B,), i32, dev, "first_position")), raw)
     return cache
 
 
@@ -693,22 +727,21 @@ def diffattn_kv4_read(cache, N, *, start=None, counts=None, k_out=None, v_out=No
         k_out = _new(torch.zeros, cache, shape, bf16, stream)
     if v_out is None:
         v_out = _new(torch.zeros, cache, shape, bf16, stream)
-    p = da_kv4_read_params(
-        B, N, hkv, d, L_max, _rows4(cache, (B, L_max, hkv, rec), torch.uint8, dev, "cache"),
+    _call("diffattn_kv4_read", _pack_read(
+        B, N, hkv, d, L_max, *_rows4(cache, (B, L_max, hkv, rec), torch.uint8, dev, "cache"),
         _array(start, (B,), torch.int32, dev, "start"), _array(counts, (B,), torch.int32, dev, "counts"),
-        _rows4(k_out, shape, bf16, dev, "k_out"), _rows4(v_out, shape, bf16, dev, "v_out"))
-    _check((_lib or load()).diffattn_kv4_read(C.byref(p), raw), "diffattn_kv4_read")
+        *_rows4(k_out, shape, bf16, dev, "k_out"), *_rows4(v_out, shape, bf16, dev, "v_out")), raw)
     return k_out, v_out
 
 
 def _gate_source(gate, x, w_lambda, B, h, dev):
     """The checked gate or (x, w_lambda) of a decode step: (gate, x, w_lambda, d_model)."""
     if gate is not None:
-        return _array(gate, (B, h), torch.float32, dev, "gate"), None, None, 0
+        return _array(gate, (B, h), torch.float32, dev, "gate"), 0, 0, 0
     if x is None or w_lambda is None:
-        return None, None, None, 0  # refused by the library
+        return 0, 0, 0, 0  # refused by the library
     d_model = x.shape[-1]
-    return (None, _array(x, (B, d_model), torch.bfloat16, dev, "x"),
+    return (0, _array(x, (B, d_model), torch.bfloat16, dev, "x"),
             _array(w_lambda, (d_model, h), torch.bfloat16, dev, "w_lambda"), d_model)
 
 
@@ -730,16 +763,14 @@ def diffattn_v2_decode_kv4(q, cache, *, seqlens=None, gate=None, x=None, w_lambd
     if workspace is None:
         need = diffattn_v2_decode_kv4_workspace_size(B, h, hkv, d, L_max, gate is not None, weights_out is not None)
         workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
-    ws_ptr, ws_bytes = _space(workspace, dev)
     gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
-    p = da_v2_decode_kv4_params(
+    per_slot = (B, hkv, L_max)
+    _call("diffattn_v2_decode_kv4", _pack_decode_kv4(
         B, h, hkv, d, L_max, d_model, softmax_scale, _array(q, (B, 2 * h, d), bf16, dev, "q"),
-        _rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, dev, "cache"),
+        *_rows4(cache, (B, L_max, hkv, d + 16), torch.uint8, dev, "cache"),
         _array(seqlens, (B,), torch.int32, dev, "seqlens"), gate_, x_, w_,
-        _array(weights_in, (B, hkv, L_max), f32, dev, "weights_in"),
-        _array(weights_out, (B, hkv, L_max), f32, dev, "weights_out"), _array(out, (B, h, d), bf16, dev, "out"),
-        ws_ptr, ws_bytes)
-    _check((_lib or load()).diffattn_v2_decode_kv4(C.byref(p), raw), "diffattn_v2_decode_kv4")
+        _array(weights_in, per_slot, f32, dev, "weights_in"), _array(weights_out, per_slot, f32, dev, "weights_out"),
+        _array(out, (B, h, d), bf16, dev, "out"), *_space(workspace, dev)), raw)
     return out
 
 
@@ -755,24 +786,21 @@ def diffattn_v2_decode_weighted(q, k_cache, v_cache, *, weights_out, weights_in=
     [B, h_kv, L_max] (see diffattn_v2_decode_kv4)."""
     dev, raw = _device(q, stream)
     B, H2, d = q.shape
-    shape = k_cache.shape
-    L_max, hkv = shape[1], shape[2]
+    L_max, hkv = k_cache.shape[1], k_cache.shape[2]
     h, bf16, f32 = H2 // 2, torch.bfloat16, torch.float32
     if out is None:
         out = _new(torch.empty, q, (B, h, d), bf16, stream)
     if workspace is None:
         need = diffattn_v2_decode_weighted_workspace_size(B, h, hkv, d, L_max, num_splits, gate is not None)
         workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
-    ws_ptr, ws_bytes = _space(workspace, dev)
     gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
-    dec = da_v2_decode_params(
+    rows, per_slot = (B, L_max, hkv, d), (B, hkv, L_max)
+    _call("diffattn_v2_decode_weighted", _pack_weighted(
         B, h, hkv, d, L_max, d_model, softmax_scale, _array(q, (B, 2 * h, d), bf16, dev, "q"),
-        _rows4(k_cache, (B, L_max, hkv, d), bf16, dev, "k_cache"), _rows4(v_cache, shape, bf16, dev, "v_cache"),
+        *_rows4(k_cache, rows, bf16, dev, "k_cache"), *_rows4(v_cache, rows, bf16, dev, "v_cache"),
         _array(seqlens, (B,), torch.int32, dev, "seqlens"), gate_, x_, w_, _array(out, (B, h, d), bf16, dev, "out"),
-        num_splits, ws_ptr, ws_bytes)
-    p = da_v2_decode_weighted_params(dec, _array(weights_in, (B, hkv, L_max), f32, dev, "weights_in"),
-                                     _array(weights_out, (B, hkv, L_max), f32, dev, "weights_out"))
-    _check((_lib or load()).diffattn_v2_decode_weighted(C.byref(p), raw), "diffattn_v2_decode_weighted")
+        num_splits, *_space(workspace, dev), _array(weights_in, per_slot, f32, dev, "weights_in"),
+        _array(weights_out, per_slot, f32, dev, "weights_out")), raw)
     return out
 
 
@@ -803,20 +831,19 @@ def diffattn_kv_evict(rows, key_weights, keep, *, sinks=0, recent=0, seqlens=Non
     if workspace is None:
         need = diffattn_kv_evict_workspace_size(B, hkv, L_max, keep)
         workspace = _new(torch.empty, key_weights, (max(need, 1),), torch.uint8, stream)
-    ws_ptr, ws_bytes = _space(workspace, dev)
-    p = da_kv_evict_params(
+    row_bytes, views = [0] * DIFFATTN_EVICT_MAX_ROWS, [0] * (4 * DIFFATTN_EVICT_MAX_ROWS)
+    for i, r in enumerate(rows):
+        n, width = r.element_size(), r.shape[-1]
+        ptr, sb, sn, sh = _rows4(r, (B, L_max, hkv, width), r.dtype, dev, f"rows[{i}]")
+        row_bytes[i] = width * n
+        views[4 * i:4 * i + 4] = ptr, sb * n, sn * n, sh * n
+    _call("diffattn_kv_evict", _pack_evict(
         B, hkv, L_max, keep, sinks, recent, _array(seqlens, (B,), i32, dev, "seqlens"),
         _array(seqlens_out, (B,), i32, dev, "seqlens_out"), _array(key_weights, shape, f32, dev, "key_weights"),
         _array(weights_out, shape, f32, dev, "weights_out"), _array(positions, shape, i32, dev, "positions"),
         _array(positions_out, shape, i32, dev, "positions_out"),
-        _array(next_position, (B,), i32, dev, "next_position"), len(rows))
-    for i, r in enumerate(rows):
-        n, width = r.element_size(), r.shape[-1]
-        t = _rows4(r, (B, L_max, hkv, width), r.dtype, dev, f"rows[{i}]")
-        p.row_bytes[i] = width * n
-        p.rows[i] = da_t4(t.ptr, t.sb * n, t.sn * n, t.sh * n)
-    p.workspace, p.workspace_bytes = ws_ptr, ws_bytes
-    _check((_lib or load()).diffattn_kv_evict(C.byref(p), raw), "diffattn_kv_evict")
+        _array(next_position, (B,), i32, dev, "next_position"), len(rows), *row_bytes, *views,
+        *_space(workspace, dev)), raw)
     return dict(key_weights=weights_out, positions=positions_out, seqlens=seqlens_out)
 
 
