@@ -611,13 +611,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 }
 
 // One output head's parts merged, even - gate * odd; also the two heads'
-// normalisers for the keys' weights.  Grid (h, B).  Threads are (way, head of
-// the pair, four features); the ways share out the parts.
-template <int D, int WAYS>
-__global__ void __launch_bounds__(WAYS * D / 2) kv4_merge_kernel(Kv4DecodeArgs a) {
-  constexpr int kWarps = WAYS * D / 2 / 32;
-  __shared__ float top[2], inv[2];
-  __shared__ float4 sums[WAYS][2][D / 4];
+// normalisers for the keys' weights.  Grid (h, B, SLICES of the features).
+// First the maximum and the sum over each head's parts: by a warp per head, or
+// where the parts may be many (kMany) by the whole block; then threads are
+// (way, head, four features) and the ways share out the parts.
+template <int D, int SLICES, int WAYS, bool kMany>
+__global__ void __launch_bounds__(WAYS * D / SLICES / 2) kv4_merge_kernel(Kv4DecodeArgs a) {
+  constexpr int kCols = D / SLICES / 4, kThreads = WAYS * 2 * kCols, kWarps = kThreads / 32;
+  __shared__ float2 part[kWarps][2];
+  __shared__ float4 sums[WAYS][2][kCols];
   const int p = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = 2 * a.h / a.h_kv, g = 2 * p / G, r = 2 * p % G;
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
@@ -631,29 +633,63 @@ __global__ void __launch_bounds__(WAYS * D / 2) kv4_merge_kernel(Kv4DecodeArgs a
     count = s.last - s.first + 1;
   }
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + first * G + r;
-  for (int e = warp; e < 2; e += kWarps) {
-    float mt = -INFINITY, lt = 0.f;
-    for (int i = lane; i < count; i += 32) mt = fmaxf(mt, ml[static_cast<int64_t>(i) * G + e].x);
+  // of each head: maximum and 1 / sum.  A sum of 0 is an empty sequence or
+  // keys that are all -inf: zeros, as in decode.cu; NaN stays
+  float2 both[2];
+  auto norm_of = [](float m, float l) { return make_float2(m, l == 0.f ? 0.f : 1.f / l); };
+  if constexpr (kMany) {
+    auto join = [](float2& x, float2 y) {  // (maximum, sum) of both
+      const float m = fmaxf(x.x, y.x), nb = m == -INFINITY ? 0.f : m;
+      x.y = x.y * exp2f(x.x - nb) + y.y * exp2f(y.x - nb);
+      x.x = m;
+    };
+    float2 tot = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+    for (int i = tid >> 1; i < count; i += kThreads / 2) join(tot, ml[static_cast<int64_t>(i) * G + (tid & 1)]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    for (int i = lane; i < count; i += 32) {
-      const float2 v = ml[static_cast<int64_t>(i) * G + e];
-      lt += v.y * exp2f(v.x - mt);
-    }
+    for (int o = 2; o < 32; o <<= 1)
+      join(tot, make_float2(__shfl_xor_sync(0xffffffffu, tot.x, o), __shfl_xor_sync(0xffffffffu, tot.y, o)));
+    if (lane < 2) part[warp][lane] = tot;
+    __syncthreads();
 #pragma unroll
-    for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-    if (lane == 0) {
-      // a sum of 0 is an empty sequence or keys that are all -inf: zeros, as in decode.cu; NaN stays
-      const float c = lt == 0.f ? 0.f : 1.f / lt;
-      top[e] = mt;
-      inv[e] = c;
-      if (a.norm) a.norm[static_cast<int64_t>(b) * 2 * a.h + 2 * p + e] = make_float2(mt, c);
+    for (int e = 0; e < 2; ++e) {
+      tot = lane < kWarps ? part[lane][e] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1)
+        join(tot, make_float2(__shfl_xor_sync(0xffffffffu, tot.x, o), __shfl_xor_sync(0xffffffffu, tot.y, o)));
+      both[e] = norm_of(tot.x, tot.y);
     }
+  } else {
+    for (int e = warp; e < 2; e += kWarps) {
+      float2 v[4];  // the first 128 parts at once, one wait for all
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = lane + 32 * k;
+        v[k] = i < count ? ml[static_cast<int64_t>(i) * G + e] : make_float2(-INFINITY, 0.f);
+      }
+      float mt = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), lt = 0.f;
+      for (int i = lane + 128; i < count; i += 32) mt = fmaxf(mt, ml[static_cast<int64_t>(i) * G + e].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+      const float nb = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lt += v[k].y * exp2f(v[k].x - nb);
+      for (int i = lane + 128; i < count; i += 32) {
+        const float2 w = ml[static_cast<int64_t>(i) * G + e];
+        lt += w.y * exp2f(w.x - nb);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+      if (lane == 0) part[0][e] = norm_of(mt, lt);
+    }
+    __syncthreads();
+    both[0] = part[0][0];
+    both[1] = part[0][1];
   }
-  __syncthreads();
-  const int f = tid % (D / 4), e = tid / (D / 4) % 2, way = tid / (D / 2);
-  const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * G + r + e) * (D / 4) + f;
-  const float mt = top[e];
+  if (tid < 2 && blockIdx.z == 0 && a.norm) a.norm[static_cast<int64_t>(b) * 2 * a.h + 2 * p + tid] = both[tid & 1];
+  const int f = tid % kCols, e = tid / kCols % 2, way = tid / (2 * kCols);
+  const float4* po = reinterpret_cast<const float4*>(a.part_o) + (first * G + r + e) * (D / 4) + blockIdx.z * kCols + f;
+  const float mt = e ? both[1].x : both[0].x;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = way; i < count; i += WAYS) {
@@ -666,24 +702,38 @@ __global__ void __launch_bounds__(WAYS * D / 2) kv4_merge_kernel(Kv4DecodeArgs a
   }
   sums[way][e][f] = x;
   __syncthreads();
-  if (tid < D) {
+  if (tid < 4 * kCols) {
     float res[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-#pragma unroll
+#pragma unroll 8
       for (int w = 0; w < WAYS; ++w) res[k] += reinterpret_cast<const float*>(&sums[w][k][0])[tid];
-      res[k] *= inv[k];
+      res[k] *= both[k].y;
     }
     const int64_t at = static_cast<int64_t>(b) * a.h + p;
-    static_cast<__nv_bfloat16*>(a.out)[at * D + tid] =
+    static_cast<__nv_bfloat16*>(a.out)[at * D + blockIdx.z * 4 * kCols + tid] =
         __float2bfloat16_rn(__fsub_rn(res[0], __fmul_rn(a.gate[at], res[1])));
   }
 }
 
-template <int D, int WAYS>
+template <int D, int SLICES, int WAYS, bool kMany>
 cudaError_t launch_merge(const Kv4DecodeArgs& a, cudaStream_t s) {
-  static_assert(WAYS * D / 2 >= D, "a thread per feature of the output");
-  return launch_ahead(kv4_merge_kernel<D, WAYS>, dim3(a.h, a.B), dim3(WAYS * D / 2), 0, s, true, a);
+  constexpr int kThreads = WAYS * D / SLICES / 2;
+  static_assert(kThreads >= D / SLICES && kThreads % 32 == 0 && kThreads <= 1024, "a thread per feature of the slice");
+  return launch_ahead(kv4_merge_kernel<D, SLICES, WAYS, kMany>, dim3(a.h, a.B, SLICES), dim3(kThreads), 0, s, true, a);
+}
+
+// Ways by the parts that a head can have (as many as its chunks, or its share
+// of the warps) and by the blocks that there are to fill the SMs with.
+template <int D>
+cudaError_t launch_merge_for(const Kv4DecodeArgs& a, cudaStream_t s) {
+  const int64_t heads = static_cast<int64_t>(a.B) * a.h_kv, chunks = (static_cast<int64_t>(a.L_max) + kChunk - 1) / kChunk;
+  const int64_t share = static_cast<int64_t>(a.grid) * kKv4MaxWarps / heads + 2, most = chunks < share ? chunks : share;
+  const int64_t blocks = static_cast<int64_t>(a.h) * a.B;
+  constexpr int kThin = D / 32;  // slices of 32 features
+  if (most <= 16) return launch_merge<D, 1, 2, false>(a, s);
+  if (most <= 128) return blocks > a.grid ? launch_merge<D, 1, 8, false>(a, s) : launch_merge<D, 1, 16, false>(a, s);
+  return blocks * kThin > a.grid ? launch_merge<D, kThin / 2, 32, true>(a, s) : launch_merge<D, kThin, 64, true>(a, s);
 }
 
 template <int D, int NT, bool kScores>
@@ -712,12 +762,7 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
     e = two ? (sc ? launch_split<64, 2, true>(a, s) : launch_split<64, 2, false>(a, s))
             : (sc ? launch_split<64, 1, true>(a, s) : launch_split<64, 1, false>(a, s));
   if (e != cudaSuccess) return e;
-  // A head has about warps / heads parts; 4 parts per way where they are many
-  const bool many = static_cast<int64_t>(a.grid) * 16 > 16 * static_cast<int64_t>(a.B) * a.h_kv;
-  if (a.d == 128)
-    e = many ? launch_merge<128, 16>(a, s) : launch_merge<128, 2>(a, s);
-  else
-    e = many ? launch_merge<64, 16>(a, s) : launch_merge<64, 2>(a, s);
+  e = a.d == 128 ? launch_merge_for<128>(a, s) : launch_merge_for<64>(a, s);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
   const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, 0, a.norm, a.seqlens, a.gate, a.part_ml, a.scores,
                          a.weights_in, a.weights_out};

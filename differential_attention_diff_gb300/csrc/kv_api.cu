@@ -46,7 +46,8 @@ int decode_grid(int B, int h_kv, int L_max) {
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
   const int64_t chunks = (static_cast<int64_t>(L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys;
-  return static_cast<int>(da::kv4_parts(chunks * h_kv * B, sms < da::kKv4MaxGrid ? sms : da::kKv4MaxGrid));
+  const int64_t most = sms < da::kKv4MaxGrid ? sms : da::kKv4MaxGrid;
+  return static_cast<int>(chunks * h_kv * B < most ? chunks * h_kv * B : most);
 }
 
 struct DecodeSpace {
