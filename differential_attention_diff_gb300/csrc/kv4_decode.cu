@@ -20,6 +20,14 @@
 // operand of O^T[16 features x 8 heads] += V^T P^T, whose pairs of keys are
 // put side by side by two byte permutes per four pairs.
 //
+// A chunk's value product starts from zero and is then added to O.  Codes are
+// not negative, so over thousands of keys their sum outgrows what is left
+// once the minima are added, by a factor of hundreds; chained through the
+// tensor cores, whose accumulators are truncated at each step, it lost 2.2e-3
+// of the output (B64 L32768), more than the output's own rounding.  Sums of 32
+// keys, added with rounding, lose nothing that shows, for an addition per
+// accumulator and chunk.
+//
 // P is fp16 (11 bits, against 8 of a bf16 P).  Its range is kept by a power
 // of two per head, vs, beside the running maximum m of the scores: both are
 // references that only move when a value would pass 2^8 (p) or 2^14 (p s vs),
@@ -71,11 +79,19 @@ __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w 
 // D = A(16x16, row) * B(16x8, col) + D, fp16 inputs, fp32 accumulators.
 __device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+  // not volatile: the compiler may move products past each other to hide their latency
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from zero accumulators.
+__device__ __forceinline__ void mma_f16_16816_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // 8x8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -89,25 +105,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
 }
 __device__ __forceinline__ float exponent_scale(float x, int target) {
   // the power of two that brings x > 0 into [2^target, 2^(target+1)), limited to 2^-126 .. 2^100
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       }
       --in_flight;
       parity ^= 1u << slot;
-      const uint32_t base = ring + slot * C::kSlot;
+      const uint8_t* base = smem + (warp * kS + slot) * C::kSlot;
       slot = slot == kS - 1 ? 0 : slot + 1;
       const int valid = at.L - at.chunk * kChunk;  // keys of this chunk
 
@@ -376,9 +376,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       float s[2][NT][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t ra = base + (u * 16 + row_key) * kRec;
-        par[u][0] = lds128(ra + D);
-        par[u][1] = lds128(ra + kRec + D);
+        const uint8_t* ra = base + (u * 16 + row_key) * kRec;
+        par[u][0] = lds<uint4>(ra + D);
+        par[u][1] = lds<uint4>(ra + kRec + D);
         if (__builtin_expect(valid < kChunk, 0)) {  // what lies behind the last key may be anything: zero parameters
           if (u * 16 + row_key >= valid) par[u][0] = make_uint4(0, 0, 0, 0);
           if (u * 16 + row_key + 1 >= valid) par[u][1] = make_uint4(0, 0, 0, 0);
@@ -386,16 +386,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         float acc[2][NT][4];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) acc[p][t][0] = acc[p][t][1] = acc[p][t][2] = acc[p][t][3] = 0.f;
           uint32_t wa[kWords], wb[kWords];
           const uint32_t off = p * (D / 4) + tq * (D / 16);
           if constexpr (kWords == 2) {
-            const uint2 x = lds64(ra + off), y = lds64(ra + kRec + off);
+            const uint2 x = lds<uint2>(ra + off), y = lds<uint2>(ra + kRec + off);
             wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
           } else {
-            wa[0] = lds32(ra + off);
-            wb[0] = lds32(ra + kRec + off);
+            wa[0] = lds<uint32_t>(ra + off);
+            wb[0] = lds<uint32_t>(ra + kRec + off);
           }
 #pragma unroll
           for (int w = 0; w < kWords; ++w)
@@ -403,9 +401,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             for (int m = 0; m < 2; ++m) {
               const uint32_t x = wa[w] >> (8 * m), y = wb[w] >> (8 * m);
 #pragma unroll
-              for (int t = 0; t < NT; ++t)
-                mma_f16_16816(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
-                              qf[t][(p * kWords + w) * 2 + m][0], qf[t][(p * kWords + w) * 2 + m][1]);
+              for (int t = 0; t < NT; ++t) {
+                const uint32_t* b = qf[t][(p * kWords + w) * 2 + m];
+                if (w == 0 && m == 0)
+                  mma_f16_16816_first(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0],
+                                      b[1]);
+                else
+                  mma_f16_16816(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0], b[1]);
+              }
             }
         }
 #pragma unroll
@@ -525,38 +528,58 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             }
         }
 
-      // ---- O^T += V^T P^T ----
+      // ---- O^T += V^T P^T, a chunk's product first, then its sum in fp32 ----
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t va = base + (u * 16 + vkey0) * kRec + D / 2, vb = base + (u * 16 + vkey1) * kRec + D / 2;
+      for (int g2 = 0; g2 < 2; ++g2) {
+        uint32_t bf[2][NT][2], w[2][4];  // [tile]; codes of keys (vkey0, vkey1) and the ones after them
 #pragma unroll
-        for (int g2 = 0; g2 < 2; ++g2) {
-          uint32_t bf[NT][2];
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t *va = base + (u * 16 + vkey0) * kRec + D / 2, *vb = base + (u * 16 + vkey1) * kRec + D / 2;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            bf[t][0] = movmatrix(pf[u][t][g2][0]);
-            bf[t][1] = movmatrix(pf[u][t][g2][1]);
+            bf[u][t][0] = movmatrix(pf[u][t][g2][0]);
+            bf[u][t][1] = movmatrix(pf[u][t][g2][1]);
           }
-          uint32_t w0, w1, w2, w3;  // keys (vkey0, vkey1) and the ones after them
           if constexpr (D == 128) {
             const uint32_t off = g2 * 32 + gr * 4;
-            w0 = lds32(va + off), w1 = lds32(vb + off), w2 = lds32(va + kRec + off), w3 = lds32(vb + kRec + off);
+            w[u][0] = lds<uint32_t>(va + off), w[u][1] = lds<uint32_t>(vb + off);
+            w[u][2] = lds<uint32_t>(va + kRec + off), w[u][3] = lds<uint32_t>(vb + kRec + off);
           } else {
             const uint32_t off = g2 * 16 + gr * 2;
-            w0 = lds16(va + off), w1 = lds16(vb + off), w2 = lds16(va + kRec + off), w3 = lds16(vb + kRec + off);
+            w[u][0] = lds<uint16_t>(va + off), w[u][1] = lds<uint16_t>(vb + off);
+            w[u][2] = lds<uint16_t>(va + kRec + off), w[u][3] = lds<uint16_t>(vb + kRec + off);
           }
+        }
 #pragma unroll
-          for (int hw = 0; hw < kWords; ++hw) {  // four features of both keys side by side
-            const uint32_t x = __byte_perm(w0, w1, hw ? 0x7632 : 0x5410), y = __byte_perm(w2, w3, hw ? 0x7632 : 0x5410);
+        for (int hw = 0; hw < kWords; ++hw) {
+          float even[NT][4], odd[NT][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {  // four features of both keys side by side
+            const uint32_t sel = hw ? 0x7632 : 0x5410;
+            const uint32_t x = __byte_perm(w[u][0], w[u][1], sel), y = __byte_perm(w[u][2], w[u][3], sel);
             const uint32_t xs = x >> 8, ys = y >> 8;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              mma_f16_16816(o[t][g2 * kGT + hw * 2], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu,
-                            ys & 0x000f000fu, bf[t][0], bf[t][1]);
-              mma_f16_16816(o[t][g2 * kGT + hw * 2 + 1], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u,
-                            ys & 0x00f000f0u, bf[t][0], bf[t][1]);
+              if (u == 0) {
+                mma_f16_16816_first(even[t], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu, ys & 0x000f000fu,
+                                    bf[u][t][0], bf[u][t][1]);
+                mma_f16_16816_first(odd[t], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u, ys & 0x00f000f0u,
+                                    bf[u][t][0], bf[u][t][1]);
+              } else {
+                mma_f16_16816(even[t], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu, ys & 0x000f000fu,
+                              bf[u][t][0], bf[u][t][1]);
+                mma_f16_16816(odd[t], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u, ys & 0x00f000f0u,
+                              bf[u][t][0], bf[u][t][1]);
+              }
             }
           }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[t][g2 * kGT + hw * 2][i] += even[t][i];
+              o[t][g2 * kGT + hw * 2 + 1][i] += odd[t][i];
+            }
         }
       }
       __syncwarp();  // the slot is read before it is filled again
