@@ -61,7 +61,7 @@ struct Shared {
 template <int T, bool kAll>
 __global__ void __launch_bounds__(T, 2048 / T) evict_select_kernel(EvictArgs a, int cached) {
   constexpr int kThreads = T, kWarps = T / 32;
-  extern __shared__ uint32_t ranks[];  // and behind them the masks
+  extern __shared__ __align__(16) uint32_t ranks[];  // and behind them the masks
   __shared__ Shared<T> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
@@ -103,10 +103,40 @@ __global__ void __launch_bounds__(T, 2048 / T) evict_select_kernel(EvictArgs a, 
   auto rank = [&](int j) { return kAll || j - j0 < cached ? ranks[j - j0] : read_rank(j); };
   for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist[0])[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  // Read the slots, four in flight; their first digit is counted on the way,
-  // and what lies below m is copied whether it stays or not: the slots that
-  // go are written again when their successors move in.
-  for (int i0 = j0 + tid; i0 < j1; i0 += 4 * kThreads) {
+  // Read the slots; their first digit is counted on the way, and what lies
+  // below m is copied whether it stays or not: the slots that go are written
+  // again when their successors move in.  Four neighbouring slots per access
+  // where the arrays allow it (L_max a multiple of 4): a quarter of the address
+  // arithmetic, which is most of this pass.
+  auto count_digit = [&](uint32_t r) { atomicAdd(&sh.hist[0][r >> (32 - kDigit)], 1u); };
+  auto quad_ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool quads = kAll && quad_ok(w_in) && quad_ok(w_out) && quad_ok(p_in) && quad_ok(p_out);
+  const int full = quads ? j0 + (j1 - j0) / 4 * 4 : j0;  // slots up to here go by fours
+#pragma unroll 2
+  for (int j = j0 + 4 * tid; j < full; j += 4 * kThreads) {
+    const float4 w = *reinterpret_cast<const float4*>(w_in + j);
+    const int4 p = p_in ? *reinterpret_cast<const int4*>(p_in + j) : make_int4(j, j + 1, j + 2, j + 3);
+    const uint4 r = make_uint4(rank_of(w.x, p.x, a.p.sinks, recent_from), rank_of(w.y, p.y, a.p.sinks, recent_from),
+                               rank_of(w.z, p.z, a.p.sinks, recent_from), rank_of(w.w, p.w, a.p.sinks, recent_from));
+    *reinterpret_cast<uint4*>(ranks + (j - j0)) = r;
+    count_digit(r.x);
+    count_digit(r.y);
+    count_digit(r.z);
+    count_digit(r.w);
+    if (j + 3 < m) {
+      if (copy_w) *reinterpret_cast<float4*>(w_out + j) = w;
+      if (copy_p) *reinterpret_cast<int4*>(p_out + j) = p;
+    } else {
+      const float ws[4] = {w.x, w.y, w.z, w.w};
+      const int ps[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (copy_w && j + k < m) w_out[j + k] = ws[k];
+        if (copy_p && j + k < m) p_out[j + k] = ps[k];
+      }
+    }
+  }
+  for (int i0 = full + tid; i0 < j1; i0 += 4 * kThreads) {
     float w[4];
     int p[4];
 #pragma unroll
@@ -121,7 +151,7 @@ __global__ void __launch_bounds__(T, 2048 / T) evict_select_kernel(EvictArgs a, 
       if (j < j1) {
         const uint32_t r = rank_of(w[k], p[k], a.p.sinks, recent_from);
         if (kAll || j - j0 < cached) ranks[j - j0] = r;
-        atomicAdd(&sh.hist[0][r >> (32 - kDigit)], 1u);
+        count_digit(r);
         if (copy_w && j < m) w_out[j] = w[k];
         if (copy_p && j < m) p_out[j] = p[k];
       }
@@ -140,11 +170,19 @@ __global__ void __launch_bounds__(T, 2048 / T) evict_select_kernel(EvictArgs a, 
     if (round) {
       for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
-#pragma unroll 4
-      for (int j = j0 + tid; j < j1; j += kThreads) {
-        const uint32_t r = rank(j);
+      auto count = [&](uint32_t r) {
         if ((r >> above_shift) == prefix) atomicAdd(&hist[(r >> shift) & ((1u << bits) - 1)], 1u);
+      };
+      const int by_four = kAll ? j0 + (j1 - j0) / 4 * 4 : j0;
+#pragma unroll 2
+      for (int j = j0 + 4 * tid; j < by_four; j += 4 * kThreads) {
+        const uint4 r = *reinterpret_cast<const uint4*>(ranks + (j - j0));
+        count(r.x);
+        count(r.y);
+        count(r.z);
+        count(r.w);
       }
+      for (int j = by_four + tid; j < j1; j += kThreads) count(rank(j));
     }
     sync_all();
     constexpr int kMine = kBins / kThreads;  // neighbouring bins per thread
@@ -379,7 +417,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
   // enough blocks for the most rows that can move, 4 steps of a block each
   int64_t chunks = 0;
   for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
-  int64_t per_unit = a.max_moves * chunks / (4 * kMoveThreads);
+  int64_t per_unit = (a.max_moves * chunks + 4 * kMoveThreads - 1) / (4 * kMoveThreads);
   const int64_t most = (16 * a.num_sms + units - 1) / units;  // and no more than fill the GPU twice
   per_unit = per_unit < 1 ? 1 : per_unit > most ? most : per_unit;
   return launch_ahead(evict_move_kernel, dim3(static_cast<unsigned>(units * per_unit)), dim3(kMoveThreads), 0, s, true, a,
