@@ -47,6 +47,8 @@
 #include "common.cuh"
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "tma.cuh"
 
@@ -371,217 +373,224 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       slot = slot == kS - 1 ? 0 : slot + 1;
       const int valid = at.L - at.chunk * kChunk;  // keys of this chunk
 
-      // ---- scores (of fac log2 units), two 16-key tiles ----
-      uint4 par[2][2];  // [tile][row half]: K s0 s1 | K m0 m1 | V s0 s1 | V m0 m1
-      float s[2][NT][4];
+      auto take_chunk = [&](auto partial) {
+        constexpr bool kPartial = decltype(partial)::value;
+        // ---- scores (of fac log2 units), two 16-key tiles ----
+        uint4 par[2][2];  // [tile][row half]: K s0 s1 | K m0 m1 | V s0 s1 | V m0 m1
+        float s[2][NT][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint8_t* ra = base + (u * 16 + row_key) * kRec;
-        par[u][0] = lds<uint4>(ra + D);
-        par[u][1] = lds<uint4>(ra + kRec + D);
-        if (__builtin_expect(valid < kChunk, 0)) {  // what lies behind the last key may be anything: zero parameters
-          if (u * 16 + row_key >= valid) par[u][0] = make_uint4(0, 0, 0, 0);
-          if (u * 16 + row_key + 1 >= valid) par[u][1] = make_uint4(0, 0, 0, 0);
-        }
-        float acc[2][NT][4];
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* ra = base + (u * 16 + row_key) * kRec;
+          par[u][0] = lds<uint4>(ra + D);
+          par[u][1] = lds<uint4>(ra + kRec + D);
+          if constexpr (kPartial) {  // what lies behind the last key may be anything: zero parameters
+            if (u * 16 + row_key >= valid) par[u][0] = make_uint4(0, 0, 0, 0);
+            if (u * 16 + row_key + 1 >= valid) par[u][1] = make_uint4(0, 0, 0, 0);
+          }
+          float acc[2][NT][4];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t wa[kWords], wb[kWords];
-          const uint32_t off = p * (D / 4) + tq * (D / 16);
-          if constexpr (kWords == 2) {
-            const uint2 x = lds<uint2>(ra + off), y = lds<uint2>(ra + kRec + off);
-            wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
-          } else {
-            wa[0] = lds<uint32_t>(ra + off);
-            wb[0] = lds<uint32_t>(ra + kRec + off);
+          for (int p = 0; p < 2; ++p) {
+            uint32_t wa[kWords], wb[kWords];
+            const uint32_t off = p * (D / 4) + tq * (D / 16);
+            if constexpr (kWords == 2) {
+              const uint2 x = lds<uint2>(ra + off), y = lds<uint2>(ra + kRec + off);
+              wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
+            } else {
+              wa[0] = lds<uint32_t>(ra + off);
+              wb[0] = lds<uint32_t>(ra + kRec + off);
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                const uint32_t x = wa[w] >> (8 * m), y = wb[w] >> (8 * m);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  const uint32_t* b = qf[t][(p * kWords + w) * 2 + m];
+                  if (w == 0 && m == 0)
+                    mma_f16_16816_first(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0],
+                                        b[1]);
+                  else
+                    mma_f16_16816(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0], b[1]);
+                }
+              }
           }
 #pragma unroll
-          for (int w = 0; w < kWords; ++w)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const uint32_t x = wa[w] >> (8 * m), y = wb[w] >> (8 * m);
+            for (int e = 0; e < 4; ++e) {
+              const uint4& r = par[u][e >> 1];
+              const int c = e & 1;
+              float x = hi_bf16(r.y) * qs1[t][c];
+              x = fmaf(lo_bf16(r.y), qs0[t][c], x);
+              x = fmaf(lo_bf16(r.x), acc[0][t][e], x);
+              x = fmaf(hi_bf16(r.x), acc[1][t][e], x);
+              s[u][t][e] = x;
+            }
+          if constexpr (kPartial) {
 #pragma unroll
-              for (int t = 0; t < NT; ++t) {
-                const uint32_t* b = qf[t][(p * kWords + w) * 2 + m];
-                if (w == 0 && m == 0)
-                  mma_f16_16816_first(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0],
-                                      b[1]);
-                else
-                  mma_f16_16816(acc[p][t], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0], b[1]);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (u * 16 + row_key + (e >> 1) >= valid) s[u][t][e] = -INFINITY;
+          }
+          if constexpr (kScores) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const int k = u * 16 + row_key + r;
+                if ((!kPartial || k < valid) && t * 8 + 2 * tq < G)
+                  *reinterpret_cast<float2*>(a.scores + (unit * a.L_max + at.chunk * kChunk + k) * G + t * 8 + 2 * tq) =
+                      make_float2(s[u][t][2 * r] * fac[t][0], s[u][t][2 * r + 1] * fac[t][1]);
+              }
+          }
+        }
+
+        // ---- softmax against the references ----
+        float p[2][NT][4], lsum[NT][2];
+        uint32_t pf[2][NT][2][2];  // [tile][head tile][group][row half], fp16 pairs of heads
+        auto weigh = [&]() {
+          bool over = false;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float x = fast_exp2(fmaf(s[u][t][2 * r], fac[t][0], -mx[t][0]));
+                const float y = fast_exp2(fmaf(s[u][t][2 * r + 1], fac[t][1], -mx[t][1]));
+                p[u][t][2 * r] = x;
+                p[u][t][2 * r + 1] = y;
+                const float xv = x * vs[t][0], yv = y * vs[t][1];
+                const float s0 = lo_bf16(par[u][r].z), s1 = hi_bf16(par[u][r].z);
+                pf[u][t][0][r] = pack_f16x2(xv * s0, yv * s0);
+                pf[u][t][1][r] = pack_f16x2(xv * s1, yv * s1);
+              }
+            lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
+            lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
+            over |= lsum[t][0] > 256.f || lsum[t][1] > 256.f;
+            // none of them is negative: their sum bounds each (and its adds do
+            // not take the pipe that the code masks fill)
+            __half2 top = *reinterpret_cast<__half2*>(&pf[0][t][0][0]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = __hadd2(top, *reinterpret_cast<__half2*>(&pf[i >> 2][t][(i >> 1) & 1][i & 1]));
+            over |= __hgt(__hadd(__low2half(top), __high2half(top)), __float2half(16384.f));
+          }
+          return over;
+        };
+        if (__any_sync(0xffffffffu, weigh())) {
+          // new references from this chunk's keys: the score maximum, then the
+          // largest p s under it
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fac[t][e];
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              const float old = mx[t][e], now = fmaxf(old, top);
+              float big = 0.f;
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  big = fmaxf(big, fast_exp2(fmaf(s[u][t][2 * r + e], fac[t][e], -now)) *
+                                       fmaxf(lo_bf16(par[u][r].z), hi_bf16(par[u][r].z)));
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+              const float down = exp2f(old - now);
+              l[t][e] *= down;
+              mn[t][0][e] *= down;
+              mn[t][1][e] *= down;
+              mx[t][e] = now;
+              // O stands for O / vs: a higher maximum raises vs and leaves O alone
+              const float keep = vs[t][e] * exp2f(now - old);
+              float v = fminf(keep, 0x1p100f);
+              if (big > 0.f) v = fminf(v, exponent_scale(big, 8));
+              const float by = keep == v ? 1.f : v / keep;
+              vs[t][e] = v;
+#pragma unroll
+              for (int i = 0; i < C::kTiles; ++i) {
+                o[t][i][e] *= by;
+                o[t][i][2 + e] *= by;
               }
             }
+          weigh();
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4& r = par[u][e >> 1];
-            const int c = e & 1;
-            float x = hi_bf16(r.y) * qs1[t][c];
-            x = fmaf(lo_bf16(r.y), qs0[t][c], x);
-            x = fmaf(lo_bf16(r.x), acc[0][t][e], x);
-            x = fmaf(hi_bf16(r.x), acc[1][t][e], x);
-            s[u][t][e] = x;
-          }
-        if (__builtin_expect(valid < kChunk, 0)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (u * 16 + row_key + (e >> 1) >= valid) s[u][t][e] = -INFINITY;
-        }
-        if constexpr (kScores) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int k = u * 16 + row_key + r;
-              if (k < valid && t * 8 + 2 * tq < G)
-                *reinterpret_cast<float2*>(a.scores + (unit * a.L_max + at.chunk * kChunk + k) * G + t * 8 + 2 * tq) =
-                    make_float2(s[u][t][2 * r] * fac[t][0], s[u][t][2 * r + 1] * fac[t][1]);
-            }
-        }
-      }
-
-      // ---- softmax against the references ----
-      float p[2][NT][4], lsum[NT][2];
-      uint32_t pf[2][NT][2][2];  // [tile][head tile][group][row half], fp16 pairs of heads
-      auto weigh = [&]() {
-        bool over = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float x = fast_exp2(fmaf(s[u][t][2 * r], fac[t][0], -mx[t][0]));
-              const float y = fast_exp2(fmaf(s[u][t][2 * r + 1], fac[t][1], -mx[t][1]));
-              p[u][t][2 * r] = x;
-              p[u][t][2 * r + 1] = y;
-              const float xv = x * vs[t][0], yv = y * vs[t][1];
-              const float s0 = lo_bf16(par[u][r].z), s1 = hi_bf16(par[u][r].z);
-              pf[u][t][0][r] = pack_f16x2(xv * s0, yv * s0);
-              pf[u][t][1][r] = pack_f16x2(xv * s1, yv * s1);
-            }
-          lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
-          lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
-          over |= lsum[t][0] > 256.f || lsum[t][1] > 256.f;
-          // none of them is negative: their sum bounds each (and its adds do
-          // not take the pipe that the code masks fill)
-          __half2 top = *reinterpret_cast<__half2*>(&pf[0][t][0][0]);
-#pragma unroll
-          for (int i = 1; i < 8; ++i) top = __hadd2(top, *reinterpret_cast<__half2*>(&pf[i >> 2][t][(i >> 1) & 1][i & 1]));
-          over |= __hgt(__hadd(__low2half(top), __high2half(top)), __float2half(16384.f));
-        }
-        return over;
-      };
-      if (__any_sync(0xffffffffu, weigh())) {
-        // new references from this chunk's keys: the score maximum, then the
-        // largest p s under it
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fac[t][e];
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float old = mx[t][e], now = fmaxf(old, top);
-            float big = 0.f;
+            l[t][e] += lsum[t][e];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int r = 0; r < 2; ++r)
-                big = fmaxf(big, fast_exp2(fmaf(s[u][t][2 * r + e], fac[t][e], -now)) *
-                                     fmaxf(lo_bf16(par[u][r].z), hi_bf16(par[u][r].z)));
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            const float down = exp2f(old - now);
-            l[t][e] *= down;
-            mn[t][0][e] *= down;
-            mn[t][1][e] *= down;
-            mx[t][e] = now;
-            // O stands for O / vs: a higher maximum raises vs and leaves O alone
-            const float keep = vs[t][e] * exp2f(now - old);
-            float v = fminf(keep, 0x1p100f);
-            if (big > 0.f) v = fminf(v, exponent_scale(big, 8));
-            const float by = keep == v ? 1.f : v / keep;
-            vs[t][e] = v;
-#pragma unroll
-            for (int i = 0; i < C::kTiles; ++i) {
-              o[t][i][e] *= by;
-              o[t][i][2 + e] *= by;
-            }
+              for (int r = 0; r < 2; ++r) {
+                mn[t][0][e] = fmaf(p[u][t][2 * r + e], lo_bf16(par[u][r].w), mn[t][0][e]);
+                mn[t][1][e] = fmaf(p[u][t][2 * r + e], hi_bf16(par[u][r].w), mn[t][1][e]);
+              }
           }
-        weigh();
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[t][e] += lsum[t][e];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              mn[t][0][e] = fmaf(p[u][t][2 * r + e], lo_bf16(par[u][r].w), mn[t][0][e]);
-              mn[t][1][e] = fmaf(p[u][t][2 * r + e], hi_bf16(par[u][r].w), mn[t][1][e]);
-            }
-        }
 
-      // ---- O^T += V^T P^T, a chunk's product first, then its sum in fp32 ----
+        // ---- O^T += V^T P^T, a chunk's product first, then its sum in fp32 ----
 #pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2) {
-        uint32_t bf[2][NT][2], w[2][4];  // [tile]; codes of keys (vkey0, vkey1) and the ones after them
+        for (int g2 = 0; g2 < 2; ++g2) {
+          uint32_t bf[2][NT][2], w[2][4];  // [tile]; codes of keys (vkey0, vkey1) and the ones after them
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint8_t *va = base + (u * 16 + vkey0) * kRec + D / 2, *vb = base + (u * 16 + vkey1) * kRec + D / 2;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            bf[u][t][0] = movmatrix(pf[u][t][g2][0]);
-            bf[u][t][1] = movmatrix(pf[u][t][g2][1]);
-          }
-          if constexpr (D == 128) {
-            const uint32_t off = g2 * 32 + gr * 4;
-            w[u][0] = lds<uint32_t>(va + off), w[u][1] = lds<uint32_t>(vb + off);
-            w[u][2] = lds<uint32_t>(va + kRec + off), w[u][3] = lds<uint32_t>(vb + kRec + off);
-          } else {
-            const uint32_t off = g2 * 16 + gr * 2;
-            w[u][0] = lds<uint16_t>(va + off), w[u][1] = lds<uint16_t>(vb + off);
-            w[u][2] = lds<uint16_t>(va + kRec + off), w[u][3] = lds<uint16_t>(vb + kRec + off);
-          }
-        }
-#pragma unroll
-        for (int hw = 0; hw < kWords; ++hw) {
-          float even[NT][4], odd[NT][4];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {  // four features of both keys side by side
-            const uint32_t sel = hw ? 0x7632 : 0x5410;
-            const uint32_t x = __byte_perm(w[u][0], w[u][1], sel), y = __byte_perm(w[u][2], w[u][3], sel);
-            const uint32_t xs = x >> 8, ys = y >> 8;
+          for (int u = 0; u < 2; ++u) {
+            const uint8_t *va = base + (u * 16 + vkey0) * kRec + D / 2, *vb = base + (u * 16 + vkey1) * kRec + D / 2;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              if (u == 0) {
-                mma_f16_16816_first(even[t], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu, ys & 0x000f000fu,
-                                    bf[u][t][0], bf[u][t][1]);
-                mma_f16_16816_first(odd[t], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u, ys & 0x00f000f0u,
-                                    bf[u][t][0], bf[u][t][1]);
-              } else {
-                mma_f16_16816(even[t], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu, ys & 0x000f000fu,
-                              bf[u][t][0], bf[u][t][1]);
-                mma_f16_16816(odd[t], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u, ys & 0x00f000f0u,
-                              bf[u][t][0], bf[u][t][1]);
-              }
+              bf[u][t][0] = movmatrix(pf[u][t][g2][0]);
+              bf[u][t][1] = movmatrix(pf[u][t][g2][1]);
+            }
+            if constexpr (D == 128) {
+              const uint32_t off = g2 * 32 + gr * 4;
+              w[u][0] = lds<uint32_t>(va + off), w[u][1] = lds<uint32_t>(vb + off);
+              w[u][2] = lds<uint32_t>(va + kRec + off), w[u][3] = lds<uint32_t>(vb + kRec + off);
+            } else {
+              const uint32_t off = g2 * 16 + gr * 2;
+              w[u][0] = lds<uint16_t>(va + off), w[u][1] = lds<uint16_t>(vb + off);
+              w[u][2] = lds<uint16_t>(va + kRec + off), w[u][3] = lds<uint16_t>(vb + kRec + off);
             }
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int hw = 0; hw < kWords; ++hw) {
+            float even[NT][4], odd[NT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[t][g2 * kGT + hw * 2][i] += even[t][i];
-              o[t][g2 * kGT + hw * 2 + 1][i] += odd[t][i];
+            for (int u = 0; u < 2; ++u) {  // four features of both keys side by side
+              const uint32_t sel = hw ? 0x7632 : 0x5410;
+              const uint32_t x = __byte_perm(w[u][0], w[u][1], sel), y = __byte_perm(w[u][2], w[u][3], sel);
+              const uint32_t xs = x >> 8, ys = y >> 8;
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                if (u == 0) {
+                  mma_f16_16816_first(even[t], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu, ys & 0x000f000fu,
+                                      bf[u][t][0], bf[u][t][1]);
+                  mma_f16_16816_first(odd[t], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u, ys & 0x00f000f0u,
+                                      bf[u][t][0], bf[u][t][1]);
+                } else {
+                  mma_f16_16816(even[t], x & 0x000f000fu, xs & 0x000f000fu, y & 0x000f000fu, ys & 0x000f000fu,
+                                bf[u][t][0], bf[u][t][1]);
+                  mma_f16_16816(odd[t], x & 0x00f000f0u, xs & 0x00f000f0u, y & 0x00f000f0u, ys & 0x00f000f0u,
+                                bf[u][t][0], bf[u][t][1]);
+                }
+              }
             }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[t][g2 * kGT + hw * 2][i] += even[t][i];
+                o[t][g2 * kGT + hw * 2 + 1][i] += odd[t][i];
+              }
+          }
         }
-      }
+      };
+      if (valid >= kChunk)
+        take_chunk(std::false_type{});
+      else
+        take_chunk(std::true_type{});
       __syncwarp();  // the slot is read before it is filled again
     }
 

@@ -146,8 +146,8 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
   if (!aligned(p->weights_in, 4) || !aligned(p->weights_out, 4) || (p->weights_in && !p->weights_out))
     return DA_ERR_INVALID_ARG;
   if (p->gate == nullptr && (!aligned(p->x, 16) || !aligned(p->w_lambda, 16))) return DA_ERR_INVALID_ARG;
-  // sequences are a grid dimension; partials are numbered in 32 bits
-  if (p->B > 65535 || static_cast<int64_t>(p->B) * p->h_kv > (1 << 28)) return DA_ERR_UNSUPPORTED;
+  // sequences and KV heads are grid dimensions; partials are numbered in 32 bits
+  if (p->B > 65535 || p->h_kv > 65535 || static_cast<int64_t>(p->B) * p->h_kv > (1 << 28)) return DA_ERR_UNSUPPORTED;
   const DecodeSpace w = decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr);
   if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   uint32_t* status;
@@ -201,7 +201,7 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
   for (int k = 0; k < p->n_rows; ++k)
     if (!ok_t4(p->rows[k], 16) || p->row_bytes[k] <= 0 || p->row_bytes[k] % 16) return DA_ERR_INVALID_ARG;
   // heads are a grid dimension, up to 8 CTAs each; a head's 16-byte pieces are counted in 32 bits
-  if (static_cast<int64_t>(p->B) * p->h_kv > (1 << 28) || p->L_max > da::kEvictMaxSlots) return DA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->B) * p->h_kv > (1 << 24) || p->L_max > da::kEvictMaxSlots) return DA_ERR_UNSUPPORTED;
   for (int k = 0; k < p->n_rows; ++k)
     if (static_cast<int64_t>(p->L_max) * (p->row_bytes[k] / 16) > (1 << 30)) return DA_ERR_UNSUPPORTED;
   const EvictSpace w = evict_space(p->B, p->h_kv, p->L_max, p->keep);

@@ -465,8 +465,10 @@ da_status diffattn_v2_decode_noalloc(const da_v2_decode_params* p, void* cuda_st
  *   bytes d+8 .. d+15       value parameters, likewise
  * A row has two groups of d/2 features, each with a scale s and a minimum m:
  *   m = min x,  s = bf16((max x - min x) / 15)   (round to nearest even)
- *   code = rint((x - m) / s) limited to 0..15,   value = s * code + m
- * computed in fp32.  A group with s = 0 has codes 0.  A group whose s is not
+ *   code = rint((x - m) / s) limited to 0..15 (ties to the even code)
+ *   value = s * code + m
+ * with max x - min x and x - m computed in fp32.  Where a group holds zeros of
+ * both signs as its minimum, m is either of them.  A group with s = 0 has codes 0.  A group whose s is not
  * finite (it holds a NaN or an infinity, or its range overflows fp32) is
  * stored as s = m = NaN, codes 0, so what reads it gives NaN.
  * A cache is given as a da_t4 over bytes: record (b, n, g) lives at
@@ -551,8 +553,8 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* cuda_st
 
 /* diffattn_v2_decode over bf16 caches that also gathers the keys' weights, as
  * diffattn_v2_decode_kv4 does: `decode` as for diffattn_v2_decode, with a
- * workspace of diffattn_v2_decode_weighted_workspace_size bytes; weights_out
- * is required. */
+ * workspace of diffattn_v2_decode_weighted_workspace_size bytes (of its own
+ * for each of two calls that run at the same time); weights_out is required. */
 typedef struct {
   da_v2_decode_params decode;
   const float* weights_in;
@@ -588,7 +590,9 @@ da_status diffattn_v2_decode_weighted(const da_v2_decode_weighted_params* p, voi
  * keep; keep may exceed L_max; L_max at most 2^20.
  * A length outside [0, L_max] is recorded as DA_ERR_BOUNDS in the device
  * status word; that sequence is left as it was, with its length copied.
- * workspace: diffattn_kv_evict_workspace_size bytes, 256-byte aligned. */
+ * workspace: diffattn_kv_evict_workspace_size bytes, 256-byte aligned,
+ * contents on entry irrelevant; calls that run at the same time need
+ * workspaces of their own. */
 #define DIFFATTN_EVICT_MAX_ROWS 3
 typedef struct {
   int B, h_kv, L_max;

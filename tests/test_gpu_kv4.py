@@ -348,6 +348,106 @@ def test_decode_kv4_many_sequences():
     check_decode(q, kf, vf, rk, rv, lens, f64(gate), out, w, None, torch.zeros_like(w))
 
 
+@pytest.mark.parametrize("d,G,layout", [(64, 2, "head"), (64, 12, "token"), (128, 4, "padded")])
+def test_decode_kv4_more_sequences_than_threads(d, G, layout):
+    """1300 sequences of 0 to 45 keys: every block sums the lengths in tiles of
+    its 512 or 256 threads and finds its part in one of them.  Lengths of 0 are
+    recorded and their rows zero; the others are right."""
+    B, L = 1300, 45
+    lens = [int(x) for x in np.random.default_rng(d + G).integers(0, L + 1, B)]
+    g, cache, q, gate, sl = make(B, L, G // 2, 1, d, lens, 552, layout)
+    w = torch.zeros((B, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_out=w)
+    assert bd.diffattn_get_device_status() == bd.DA_ERR_BOUNDS
+    zero = [b for b in range(B) if lens[b] == 0]
+    full = [b for b in range(B) if lens[b]]
+    assert zero and torch.count_nonzero(out[zero]).item() == 0 and torch.count_nonzero(w[zero]).item() == 0
+    some = full[::7] + full[-3:]
+    kf, vf, rk, rv = ranges(clean(cache[some], [lens[b] for b in some]))
+    check_decode(q[some], kf, vf, rk, rv, [lens[b] for b in some], f64(gate[some]), out[some], w[some], None,
+                 torch.zeros_like(w[some]))
+
+
+def test_append_more_sequences_than_a_grid_dimension():
+    """70000 sequences, a row each: blocks walk the sequences behind the first 65535."""
+    B, d = 70_000, 64
+    k, v = randn((B, 1, 1, d), gen(7)), randn((B, 1, 1, d), gen(8))
+    cache = new_cache(B, 1, 1, d)
+    bd.diffattn_kv4_append(k, v, cache)
+    for part in (slice(0, 300), slice(65_400, 65_700), slice(69_900, B)):
+        assert np.array_equal(cache[part].cpu().numpy(), kvo.kv4_pack(f64(k[part]), f64(v[part])))
+    kb, _ = bd.diffattn_kv4_read(cache, 1)
+    err = (kb.double() - k.double()).abs().amax(-1)
+    assert float(err.max()) < 1.0  # every row came back
+
+
+def test_decode_kv4_two_streams_at_once():
+    """Two calls in flight on two streams, each with a workspace of its own."""
+    made = [make(2, 4000, 4, 2, 128, [4000, 2500], 590 + i) for i in range(2)]
+    want = [bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate) for _, cache, q, gate, sl in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, (_, cache, q, gate, sl) in enumerate(made):
+            got[i].append(bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_decode_kv4_shared_prefix_and_views():
+    """One cache read by every sequence of a batch (batch stride 0), and a
+    contiguous run of positions of a longer cache."""
+    g, cache, q, gate, _ = make(1, 300, 4, 2, 64, [300], 595)
+    qs, gates = randn((3, 8, 64), g), torch.rand((3, 4), generator=g, device="cuda")
+    both = bd.diffattn_v2_decode_kv4(qs, cache.expand(3, 300, 2, 80), gate=gates)
+    same = bd.diffattn_v2_decode_kv4(qs, cache.repeat(3, 1, 1, 1).contiguous(), gate=gates)
+    kf, vf, rk, rv = ranges(cache.expand(3, 300, 2, 80).cpu().numpy())
+    for out in (both, same):
+        check_decode(qs, kf, vf, rk, rv, [300] * 3, f64(gates), out)
+    part = cache[:, 100:250]
+    out = bd.diffattn_v2_decode_kv4(q, part, gate=gate)
+    kf, vf, rk, rv = ranges(part.cpu().numpy())
+    check_decode(q, kf, vf, rk, rv, [150], f64(gate), out)
+
+
+def test_decode_kv4_long_sums_lose_nothing():
+    """Over 16.8 million records (some 220 chunks of 32 keys per warp) the
+    output's RMS error against 64 bits stays at its own rounding.  A bf16 value
+    x in [1, 2) is off by 2^-8 / sqrt(3) in the mean square, 1.63e-3 of x after
+    the mean of 1 / x^2 = 1/2 over values spread evenly in a binade (1.66e-3
+    where their logarithm is).  P s in 16 bits is off by 2^-11 / sqrt(3) at
+    most, and a code's mean square, 8.7 s, is 2.6 to 2.9 of the values' own:
+    8e-4 of the output.  Together 1.9e-3; fp32 steps add 1e-5 of it.  Sums that
+    lose bits at every step add what grows with the length (chained through the
+    tensor cores' accumulators they gave 2.8e-3)."""
+    B, L, hkv, d = 32, 32768, 16, 64
+    g = gen(565)
+    cache = new_cache(B, L, hkv, d)
+    for b in range(B):
+        bd.diffattn_kv4_append(randn((1, L, hkv, d), g), randn((1, L, hkv, d), g), cache[b:b + 1])
+    q, gate = randn((B, 2 * hkv, d), g), torch.rand((B, hkv), generator=g, device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate)
+    num = den = 0.0
+    for b in (0, 13, 31):
+        rec = cache[b].transpose(0, 1).contiguous()  # [hkv, L, d + 16]
+        rows = []
+        for i in (0, 1):
+            c = rec[..., i * (d // 2):(i + 1) * (d // 2)]
+            n = torch.stack((c & 15, c >> 4), -1).flatten(-2).double().unflatten(-1, (2, -1))
+            p = rec[..., d + 8 * i:d + 8 * i + 8].contiguous().view(BF16).double()
+            rows.append((n * p[..., 0:2, None] + p[..., 2:4, None]).flatten(-2))
+        a = torch.softmax(q[b].double().reshape(hkv, 2, d) @ rows[0].transpose(1, 2) * d ** -0.5, -1)
+        ref = (a @ rows[1])[:, 0] - gate[b].double()[:, None] * (a @ rows[1])[:, 1]
+        num += float((out[b].double() - ref).square().sum())
+        den += float(ref.square().sum())
+    record({"rms": (num / den) ** 0.5 / 2e-3})
+    assert (num / den) ** 0.5 <= 2e-3
+    del cache
+    torch.cuda.empty_cache()
+
+
 def test_decode_kv4_long_cache_offsets():
     """A cache whose byte offsets pass 2^32: two sequences 4.5 GB apart."""
     L, hkv, d = 5000, 2, 128
