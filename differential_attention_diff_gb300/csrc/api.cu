@@ -270,6 +270,7 @@ da_status diffattn_v2_decode_weighted(const da_v2_decode_weighted_params* p, voi
     return DA_ERR_INVALID_ARG;
   if (p->decode.gate == nullptr && (!aligned(p->decode.x, 16) || !aligned(p->decode.w_lambda, 16)))
     return DA_ERR_INVALID_ARG;
+  if (p->decode.L_max > (1 << 30)) return DA_ERR_UNSUPPORTED;  // slots are counted in 32 bits
   return run_v2_decode(&p->decode, p->weights_in, p->weights_out, stream);
 }
 

@@ -147,7 +147,8 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
     return DA_ERR_INVALID_ARG;
   if (p->gate == nullptr && (!aligned(p->x, 16) || !aligned(p->w_lambda, 16))) return DA_ERR_INVALID_ARG;
   // sequences and KV heads are grid dimensions; partials are numbered in 32 bits
-  if (p->B > 65535 || p->h_kv > 65535 || static_cast<int64_t>(p->B) * p->h_kv > (1 << 28)) return DA_ERR_UNSUPPORTED;
+  if (p->B > 65535 || p->h_kv > 65535 || static_cast<int64_t>(p->B) * p->h_kv > (1 << 28) || p->L_max > (1 << 30))
+    return DA_ERR_UNSUPPORTED;
   const DecodeSpace w = decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr);
   if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   uint32_t* status;

@@ -530,7 +530,8 @@ da_status diffattn_kv4_read(const da_kv4_read_params* p, void* cuda_stream);
  * array as weights_out (it may not overlap it otherwise).
  * workspace: diffattn_v2_decode_kv4_workspace_size bytes, 256-byte aligned,
  * contents on entry irrelevant; calls that run at the same time need
- * workspaces of their own.  Results are bitwise reproducible. */
+ * workspaces of their own.  Results are bitwise reproducible from call to
+ * call.  B, h_kv at most 65535, B * h_kv at most 2^28, L_max at most 2^30. */
 typedef struct {
   int B, h, h_kv, d, L_max, d_model;
   float softmax_scale;   /* <= 0 selects 1/sqrt(d) */

@@ -337,6 +337,30 @@ def test_decode_kv4_nan_record_gives_nan():
     assert bool(torch.isnan(w[0, 0]).all()) and bool(torch.isfinite(w[0, 1]).all())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_kv4_nan_beside_growing_values(d):
+    """A NaN in one half of a value row leaves the other half's features right,
+    also where the value scales grow by orders of magnitude in the same keys."""
+    B, L, h, hkv = 1, 96, 2, 1
+    g = gen(545)
+    k, v, q = randn((B, L, hkv, d), g, 0.1), randn((B, L, hkv, d), g), randn((B, 2 * h, d), g)
+    v[:, 40:] *= 1000.0
+    v[0, 40:64:3, 0, 3] = float("nan")  # keys of the first group only
+    cache = new_cache(B, L, hkv, d)
+    bd.diffattn_kv4_append(k, v, cache)
+    gate = torch.rand((B, h), generator=g, device="cuda")
+    w = torch.zeros((B, hkv, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate, weights_out=w)
+    assert bool(torch.isnan(out[..., :d // 2]).all()) and bool(torch.isfinite(w).all())
+    kf, vf, rk, rv = ranges(cache.cpu().numpy())
+    half = slice(d // 2, d)
+    ref = orc.v2_decode(f64(q), kf, np.nan_to_num(vf), [L], f64(gate))["out"][0][:, half]
+    got = f64(out)[0][:, half]
+    # as check_decode: the output's rounding, and 2^-11 of the values' range
+    v_range = 15 * np.abs(kvo.kv4_quantise(f64(v)[..., half].repeat(2, -1))[1]).max()
+    assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2 * 2.0 ** -11 * v_range + 1e-4 * np.abs(vf[..., half]).max())
+
+
 def test_decode_kv4_many_sequences():
     """More (sequence, head) units than SMs, short and ragged."""
     B = 70

@@ -140,7 +140,8 @@ def test_decode_kv4_argument_checks(lib):
                 dict(weights_in=FAKE + 2, weights_out=FAKE),
                 dict(gate=None, x=FAKE + 2, w_lambda=FAKE, d_model=64)):
         assert f(_with(p, **bad), None) == bd.DA_ERR_INVALID_ARG, bad
-    for bad in (dict(d=96), dict(h=128), dict(gate=None, x=FAKE, w_lambda=FAKE, d_model=100)):
+    for bad in (dict(d=96), dict(h=128), dict(gate=None, x=FAKE, w_lambda=FAKE, d_model=100), dict(B=65536),
+                dict(L_max=(1 << 30) + 1)):
         assert f(_with(p, **bad), None) == bd.DA_ERR_UNSUPPORTED, bad
     need = lib.diffattn_v2_decode_kv4_workspace_size(2, 32, 8, 128, 1024, 1, 0)
     assert f(_with(p), None) == bd.DA_ERR_WORKSPACE
@@ -167,7 +168,9 @@ def test_decode_weighted_argument_checks(lib):
     assert f(_with(p), None) == bd.DA_ERR_UNSUPPORTED
     p.decode.d, p.decode.num_splits = 128, 70000
     assert f(_with(p), None) == bd.DA_ERR_INVALID_ARG
-    p.decode.num_splits = 4
+    p.decode.num_splits, p.decode.L_max = 4, (1 << 30) + 1
+    assert f(_with(p), None) == bd.DA_ERR_UNSUPPORTED
+    p.decode.L_max = 1024
     plain = lib.diffattn_v2_decode_workspace_size(2, 32, 8, 128, 1024, 4, 1)
     need = lib.diffattn_v2_decode_weighted_workspace_size(2, 32, 8, 128, 1024, 4, 1)
     assert need - plain >= 2 * 64 * 1024 * 4
