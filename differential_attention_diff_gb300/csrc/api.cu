@@ -245,9 +245,9 @@ da_status run_v2_decode(const da_v2_decode_params* p, const float* weights_in, f
                    part_o, part_ml, d.status, scores, p->gate == nullptr};
   cudaError_t e = da::launch_decode(a, s);
   if (e == cudaSuccess && weights_out) {
-    const da::KeyWeightsArgs w{p->B, p->h, p->h_kv, p->L_max, splits, nullptr, p->seqlens, gate, part_ml, scores,
-                               weights_in, weights_out};
-    e = da::launch_key_weights(w, s);
+    const da::FinishArgs w{p->B, p->h, p->h_kv, p->d, p->L_max, splits, nullptr, p->seqlens, gate, part_o, part_ml,
+                           scores, weights_in, weights_out, p->out};
+    e = da::launch_decode_finish(w, s);
   }
   return cuda_status(e);
 }

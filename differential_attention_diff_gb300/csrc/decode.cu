@@ -17,6 +17,7 @@
 // Stage 2 (merge): grid (h, B); merges the splits of heads 2p and 2p+1 with
 // the log-sum-exp rule and writes out = O_2p - gate * O_2p+1 in bf16.
 #include "common.cuh"
+#include "decode_merge.cuh"
 #include "kernels.h"
 
 namespace da {
@@ -269,34 +270,16 @@ decode_split_kernel(DecodeArgs a) {
 }
 
 // Merge the splits of one pair and apply the gate.  Block = d threads, one
-// feature each; grid (h, B).  kAhead: launched before the split kernel's end.
-template <bool kAhead>
+// feature each; grid (h, B).
 __global__ void __launch_bounds__(128)
 decode_merge_kernel(DecodeArgs a) {
-  if constexpr (kAhead) cudaGridDependencySynchronize();
   const int p = blockIdx.x, b = blockIdx.y, col = threadIdx.x;
   const int H2 = 2 * a.h;
   float res[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int j = 2 * p + e;
-    float mt = -INFINITY;
-    for (int s = 0; s < a.num_splits; ++s)
-      mt = fmaxf(mt, a.part_ml[((static_cast<int64_t>(s) * a.B + b) * H2 + j) * 2]);
-    const float base = mt == -INFINITY ? 0.f : mt;
-    float lt = 0.f, ot = 0.f;
-    for (int s = 0; s < a.num_splits; ++s) {
-      const int64_t pidx = (static_cast<int64_t>(s) * a.B + b) * H2 + j;
-      const float f = exp2f(a.part_ml[pidx * 2] - base);
-      lt += a.part_ml[pidx * 2 + 1] * f;
-      ot += a.part_o[pidx * a.d + col] * f;
-    }
-    res[e] = lt > 0.f ? ot / lt : 0.f;
-  }
-  const float gte = a.gate[static_cast<int64_t>(b) * a.h + p];
-  const float y = __fsub_rn(res[0], __fmul_rn(gte, res[1]));
-  static_cast<__nv_bfloat16*>(a.out)[(static_cast<int64_t>(b) * a.h + p) * a.d + col] =
-      __float2bfloat16_rn(y);
+  for (int e = 0; e < 2; ++e)
+    res[e] = merged_head(a.part_o, a.part_ml, a.num_splits, a.B, H2, a.d, b, 2 * p + e, col);
+  store_pair(a.out, a.gate, static_cast<int64_t>(b) * a.h + p, a.d, col, res[0], res[1]);
 }
 
 template <int D, bool kScores>
@@ -321,10 +304,9 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
     e = a.d == 128 ? launch_split<128, true>(a, s) : launch_split<64, true>(a, s);
   else
     e = a.d == 128 ? launch_split<128, false>(a, s) : launch_split<64, false>(a, s);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.scores) return e;  // with scores the key weights' kernel merges too
   dim3 g2(a.h, a.B);
-  if (a.scores) return launch_ahead(decode_merge_kernel<true>, g2, dim3(a.d), 0, s, true, a);
-  decode_merge_kernel<false><<<g2, a.d, 0, s>>>(a);
+  decode_merge_kernel<<<g2, a.d, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -138,19 +138,21 @@ struct Kv4DecodeArgs {
 };
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 
-// ---- gathered key weights from the scores of a decode -------------------------
-struct KeyWeightsArgs {
-  int B, h, h_kv, L_max;
-  int splits;          // key-range splits, where norm is null
-  const float2* norm;  // [B, 2h] each head's maximum and 1 / sum, or null: taken from part_ml
+// ---- the end of a decode that gathers the keys' weights -----------------------
+struct FinishArgs {
+  int B, h, h_kv, d, L_max;
+  int splits;            // key-range splits, where norm is null
+  const float2* norm;    // [B, 2h] each head's maximum and 1 / sum, or null: taken from part_ml
   const int* seqlens;
   const float* gate;
+  const float* part_o;   // [splits, B, 2h, d]
   const float* part_ml;  // [splits, B, 2h, 2]
   const float* scores;   // [B, h_kv, L_max, G]
   const float* weights_in;
   float* weights_out;
+  void* out;             // bf16 [B, h, d]: merged too, or null
 };
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t s);
+cudaError_t launch_decode_finish(const FinishArgs& a, cudaStream_t s);
 
 // ---- eviction from a cache -----------------------------------------------------
 constexpr int kEvictMaxSlots = 1 << 20;  // of a head: 8 slices whose masks fit shared memory beside their ranks

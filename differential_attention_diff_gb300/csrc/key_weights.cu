@@ -1,41 +1,79 @@
-// key_weights.cu — the weight that each cached key gathers in a V2 decode
-// step: w[j] = sum over the KV head's pairs p of |A_2p[j] - gate_p A_2p+1[j]|.
+// key_weights.cu — the end of a V2 decode step that gathers the keys' weights,
+//   w[j] = sum over the KV head's pairs p of |A_2p[j] - gate_p A_2p+1[j]|.
 //
 // A key's weight needs both maps' normalisers, which exist only after the
 // whole sequence was read.  The decode's split kernel therefore stores its
-// scaled scores t (log2 units, fp32); this kernel merges the partials' maxima
-// and sums and takes A = exp2(t - max) / sum from them.  Scores in fewer bits
-// would not do: an error e in t is an error of 0.7 e in the weight.  4 G bytes
-// of scores per key are fewer than its K row's 2 d of bf16, so keeping them
-// beats a second pass over K.
+// scaled scores t (log2 units, fp32); this kernel takes A = exp2(t - max) / sum
+// from them.  Scores in fewer bits would not do: an error e in t is an error
+// of 0.7 e in the weight.  4 G bytes of scores per key are fewer than its K
+// row's 2 d of bf16, so keeping them beats a second pass over K.
+//
+// Over a bf16 cache the same launch merges the splits, in its first blocks: in
+// two launches that cost 22 us for 8 ragged sequences up to 4096 keys, in one
+// 19.4.  Over a 4-bit cache the merge has left the normalisers.  Bound by the
+// scores' traffic: 32 x 16384 keys of 8 heads, 168 MB, 31 us under the profiler.
 #include "common.cuh"
+#include "decode_merge.cuh"
 #include "kernels.h"
 
 namespace da {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 4;  // per thread, all loaded before the first is used
+constexpr int kBlockKeys = kThreads * kKeys;
 
-// P pairs of heads; block (1024 keys, KV head, sequence).
+// A head's maximum and 1 / sum: from the table, or over the splits by a warp.  A
+// sum of 0 is keys that are all -inf: zero weights; NaN stays.
+__device__ __forceinline__ float2 head_norm(const FinishArgs& a, int64_t head) {
+  if (a.norm) return a.norm[head];
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + head;
+  const int64_t step = static_cast<int64_t>(a.B) * 2 * a.h;
+  const int lane = threadIdx.x & 31;
+  float mt = -INFINITY, lt = 0.f;
+  for (int i = lane; i < a.splits; i += 32) mt = fmaxf(mt, ml[i * step].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+  mt = mt == -INFINITY ? 0.f : mt;
+  for (int i = lane; i < a.splits; i += 32) lt += ml[i * step].y * exp2f(ml[i * step].x - mt);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+  return make_float2(mt, lt == 0.f ? 0.f : 1.f / lt);
+}
+
+// P pairs of heads per KV head.  Blocks: the merge's, then (1024 keys, KV
+// head, sequence).
 template <int P>
-__global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a) {
+__global__ void __launch_bounds__(kThreads) decode_finish_kernel(FinishArgs a, int merge_blocks) {
   constexpr int G = 2 * P;
-  __shared__ float sm[G], sc[G];
   cudaGridDependencySynchronize();  // scores and partials
-  const int g = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x;
+  if (blockIdx.x < static_cast<unsigned>(merge_blocks)) {
+    const int64_t pair = static_cast<int64_t>(blockIdx.x) * (kThreads / a.d) + tid / a.d;
+    if (pair >= static_cast<int64_t>(a.B) * a.h) return;
+    const int b = static_cast<int>(pair / a.h), p = static_cast<int>(pair % a.h), col = tid % a.d;
+    float res[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      res[e] = merged_head(a.part_o, a.part_ml, a.splits, a.B, 2 * a.h, a.d, b, 2 * p + e, col);
+    store_pair(a.out, a.gate, pair, a.d, col, res[0], res[1]);
+    return;
+  }
+  __shared__ float sm[G], sc[G];
+  const unsigned block = blockIdx.x - merge_blocks, per = (a.L_max + kBlockKeys - 1) / kBlockKeys;
+  const int64_t unit = block / per;
+  const int b = static_cast<int>(unit / a.h_kv);
+  const int key0 = static_cast<int>(block % per) * kBlockKeys;
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
-  if (L < 1 || L > a.L_max) return;  // recorded by the split kernel
-  const int key0 = blockIdx.x * (kThreads * kKeys);
-  if (key0 >= L) return;
-  const int64_t unit = static_cast<int64_t>(b) * a.h_kv + g;
+  if (L < 1 || L > a.L_max || key0 >= L) return;  // a bad length is recorded by the split kernel
   const int64_t base = unit * a.L_max;
   // loads first: they do not wait for the normalisers
   float2 t[kKeys][P];
   float w[kKeys];
 #pragma unroll
   for (int k = 0; k < kKeys; ++k) {
-    const int key = key0 + k * kThreads + threadIdx.x;
+    const int key = key0 + k * kThreads + tid;
     if (key < L) {
       const float* s = a.scores + (base + key) * G;
       if constexpr (P % 2 == 0) {
@@ -52,43 +90,17 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a)
       w[k] = a.weights_in ? a.weights_in[base + key] : 0.f;
     }
   }
-  // a warp per head, a lane per partial
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < G; r += kThreads / 32) {
-    const int64_t head = static_cast<int64_t>(b) * 2 * a.h + g * G + r;
-    if (a.norm) {
-      if (lane == 0) {
-        const float2 n = a.norm[head];
-        sm[r] = n.x;
-        sc[r] = (r & 1) ? n.y * a.gate[head / 2] : n.y;
-      }
-      continue;
-    }
-    float mt = -INFINITY, lt = 0.f;
-    for (int i = lane; i < a.splits; i += 32) {
-      const float2 ml = reinterpret_cast<const float2*>(a.part_ml)[i * static_cast<int64_t>(a.B) * 2 * a.h + head];
-      const float top = fmaxf(mt, ml.x), nb = top == -INFINITY ? 0.f : top;
-      lt = lt * exp2f(mt - nb) + ml.y * exp2f(ml.x - nb);
-      mt = top;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, mt, o), l2 = __shfl_xor_sync(0xffffffffu, lt, o);
-      const float top = fmaxf(mt, m2), nb = top == -INFINITY ? 0.f : top;
-      lt = lt * exp2f(mt - nb) + l2 * exp2f(m2 - nb);
-      mt = top;
-    }
-    if (lane == 0) {
-      float c = lt == 0.f ? 0.f : 1.f / lt;
-      if (r & 1) c *= a.gate[head / 2];
-      sm[r] = mt == -INFINITY ? 0.f : mt;
-      sc[r] = c;
+  for (int r = tid >> 5; r < G; r += kWarps) {
+    const float2 n = head_norm(a, unit * G + r);
+    if ((tid & 31) == 0) {
+      sm[r] = n.x;
+      sc[r] = (r & 1) ? n.y * a.gate[unit * P + r / 2] : n.y;
     }
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kKeys; ++k) {
-    const int key = key0 + k * kThreads + threadIdx.x;
+    const int key = key0 + k * kThreads + tid;
     if (key >= L) continue;
     // products rounded before they are subtracted: equal maps cancel to zero
 #pragma unroll
@@ -99,24 +111,24 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(KeyWeightsArgs a)
   }
 }
 
-template <int P>
-cudaError_t launch_pairs(const KeyWeightsArgs& a, cudaStream_t s) {
-  const dim3 grid((a.L_max + kThreads * kKeys - 1) / (kThreads * kKeys), a.h_kv, a.B);
-  return launch_ahead(key_weights_kernel<P>, grid, dim3(kThreads), 0, s, true, a);
-}
-
 }  // namespace
 
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t s) {
+cudaError_t launch_decode_finish(const FinishArgs& a, cudaStream_t s) {
+  const int64_t pairs = static_cast<int64_t>(a.B) * a.h, per = kThreads / a.d;
+  const int64_t merge = a.out ? (pairs + per - 1) / per : 0;
+  const int64_t blocks = merge + static_cast<int64_t>(a.B) * a.h_kv * ((a.L_max + kBlockKeys - 1) / kBlockKeys);
+  if (blocks > 2147483647) return cudaErrorInvalidValue;
+  const int m = static_cast<int>(merge);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   switch (a.h / a.h_kv) {  // pairs per KV head
-    case 1: return launch_pairs<1>(a, s);
-    case 2: return launch_pairs<2>(a, s);
-    case 3: return launch_pairs<3>(a, s);
-    case 4: return launch_pairs<4>(a, s);
-    case 5: return launch_pairs<5>(a, s);
-    case 6: return launch_pairs<6>(a, s);
-    case 7: return launch_pairs<7>(a, s);
-    case 8: return launch_pairs<8>(a, s);
+    case 1: return launch_ahead(decode_finish_kernel<1>, grid, block, 0, s, true, a, m);
+    case 2: return launch_ahead(decode_finish_kernel<2>, grid, block, 0, s, true, a, m);
+    case 3: return launch_ahead(decode_finish_kernel<3>, grid, block, 0, s, true, a, m);
+    case 4: return launch_ahead(decode_finish_kernel<4>, grid, block, 0, s, true, a, m);
+    case 5: return launch_ahead(decode_finish_kernel<5>, grid, block, 0, s, true, a, m);
+    case 6: return launch_ahead(decode_finish_kernel<6>, grid, block, 0, s, true, a, m);
+    case 7: return launch_ahead(decode_finish_kernel<7>, grid, block, 0, s, true, a, m);
+    case 8: return launch_ahead(decode_finish_kernel<8>, grid, block, 0, s, true, a, m);
   }
   return cudaErrorInvalidValue;
 }

@@ -803,9 +803,12 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = a.d == 128 ? launch_merge_for<128>(a, s) : launch_merge_for<64>(a, s);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;
-  const KeyWeightsArgs w{a.B, a.h, a.h_kv, a.L_max, 0, a.norm, a.seqlens, a.gate, a.part_ml, a.scores,
-                         a.weights_in, a.weights_out};
-  return launch_key_weights(w, s);
+  // a launch of its own: merged by the same kernel as a bf16 cache's splits, the
+  // parts took 3 us more (64 x 2048 keys), since that kernel's blocks hold
+  // twice the registers
+  const FinishArgs f{a.B, a.h, a.h_kv, a.d, a.L_max, 0, a.norm, a.seqlens, a.gate, nullptr, nullptr, a.scores,
+                     a.weights_in, a.weights_out, nullptr};
+  return launch_decode_finish(f, s);
 }
 
 }  // namespace da
