@@ -41,10 +41,7 @@ da_status check_rows(int B, int N, int h_kv, int d, int L_max, const da_t4& k, c
 
 // CTAs of the 4-bit decode: one per SM, or as many as the fullest batch has
 // parts.  The lengths are on the device, so this is an upper bound.
-int decode_grid(int B, int h_kv, int L_max) {
-  uint32_t* status;
-  int sms = 152;
-  if (!da::device_handles(&status, &sms)) sms = 152;
+int decode_grid(int B, int h_kv, int L_max, int sms) {
   const int64_t chunks = (static_cast<int64_t>(L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys;
   const int64_t most = sms < da::kKv4MaxGrid ? sms : da::kKv4MaxGrid;
   return static_cast<int>(chunks * h_kv * B < most ? chunks * h_kv * B : most);
@@ -53,9 +50,9 @@ int decode_grid(int B, int h_kv, int L_max) {
 struct DecodeSpace {
   size_t ml, parts, norm, scores, gate, total;  // offsets; the partial O rows are at 0
 };
-DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
+DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights, int grid) {
   const size_t rows =
-      (static_cast<size_t>(decode_grid(B, h_kv, L_max)) * da::kKv4MaxWarps + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
+      (static_cast<size_t>(grid) * da::kKv4MaxWarps + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
   DecodeSpace w;
   w.ml = align256(rows * d * sizeof(float));
   w.parts = w.ml + align256(rows * 2 * sizeof(float));
@@ -121,7 +118,10 @@ da_status diffattn_kv4_read(const da_kv4_read_params* p, void* stream) {
 
 size_t diffattn_v2_decode_kv4_workspace_size(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights) {
   if (B <= 0 || h <= 0 || h_kv <= 0 || d <= 0 || L_max <= 0) return 0;
-  return decode_space(B, h, h_kv, d, L_max, gate_given, weights).total;
+  uint32_t* status;
+  int sms = 152;
+  if (!da::device_handles(&status, &sms)) sms = 152;
+  return decode_space(B, h, h_kv, d, L_max, gate_given, weights, decode_grid(B, h_kv, L_max, sms)).total;
 }
 
 da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream) {
@@ -149,11 +149,15 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
   // sequences and KV heads are grid dimensions; partials are numbered in 32 bits
   if (p->B > 65535 || p->h_kv > 65535 || static_cast<int64_t>(p->B) * p->h_kv > (1 << 28) || p->L_max > (1 << 30))
     return DA_ERR_UNSUPPORTED;
-  const DecodeSpace w = decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr);
-  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   uint32_t* status;
-  int sms;
-  if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
+  int sms = 152;
+  const bool device = da::device_handles(&status, &sms);
+  if (!device) sms = 152;  // the workspace is checked first, as the size query would have it
+  int grid = decode_grid(p->B, p->h_kv, p->L_max, sms);
+  const DecodeSpace w =
+      decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr, grid);
+  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
+  if (!device) return DA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   const float* gate = p->gate;
@@ -167,7 +171,6 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
   // up to 48 chunks a warp the decode leaves them alone (gate from x at 64 x
   // 2048 keys: 51 us on all SMs, 46 on the others; at 64 x 8192, 54 chunks:
   // 121 and 120; at 64 x 32768: 395 and 409).
-  int grid = decode_grid(p->B, p->h_kv, p->L_max);
   const int64_t chunks = (static_cast<int64_t>(p->L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys * p->h_kv * p->B;
   if (p->gate == nullptr && grid > sms - 8 && sms > 16 && chunks <= 48LL * da::kKv4MaxWarps * sms) grid = sms - 8;
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.f / std::sqrt(static_cast<float>(p->d));
