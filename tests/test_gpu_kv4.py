@@ -526,6 +526,77 @@ def test_decode_kv4_other_stream_and_graph():
         assert torch.equal(out, got) and torch.equal(w, gw)
 
 
+def test_decode_kv4_gate_from_x_in_a_graph():
+    """The gate's projection, the decode that runs beside it and the weights,
+    captured: replays follow the inputs, also back to back, where one replay's
+    gate must not start on the workspace before the last one's merge is done."""
+    g, cache, q, _, _ = make(3, 700, 8, 2, 128, [700, 300, 512], 575)
+    x, wl = randn((3, 512), g), randn((512, 8), g, 0.05)
+    sl = torch.tensor([700, 300, 512], dtype=torch.int32, device="cuda")
+    w = torch.zeros((3, 2, 700), device="cuda")
+    ws = torch.empty((bd.diffattn_v2_decode_kv4_workspace_size(3, 8, 2, 128, 700, False, True),), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.empty((3, 8, 128), dtype=BF16, device="cuda")
+
+    def step():
+        bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, x=x, w_lambda=wl, weights_out=w, out=out, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(576, 582):
+        x.copy_(randn((3, 512), gen(seed)))
+        q.copy_(randn((3, 16, 128), gen(seed + 100)))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        got, gw = out.clone(), w.clone()
+        gate = bd.diffattn_v2_gate(x, wl)
+        want_w = torch.zeros_like(w)
+        # the gate given: cut for all SMs, so the fp32 sums may associate otherwise
+        want = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_out=want_w)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got) and torch.equal(w, gw)
+        assert float((got.float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max())
+        assert float((gw - want_w).abs().max()) <= 1e-5 * float(want_w.max())
+
+
+def _sweep(seed):
+    r = np.random.default_rng(seed)
+    d, hkv, G = int(r.choice([64, 128])), int(r.choice([1, 2, 3, 8])), 2 * int(r.integers(1, 9))
+    B, L = int(r.integers(1, 6)), int(np.exp(r.uniform(0, np.log(3000))))
+    lens = [int(x) for x in r.integers(1, L + 1, B)]
+    return dict(B=B, L=L, h=hkv * G // 2, hkv=hkv, d=d, lens=lens, layout=str(r.choice(["head", "token", "padded"])),
+                scale=float(r.choice([0.0, 0.05, 0.4])), k_std=float(r.choice([0.3, 1.0, 2.0])),
+                v_std=float(r.choice([1e-3, 1.0, 50.0])), from_x=bool(r.random() < 0.3), weights=bool(r.random() < 0.7))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_decode_kv4_swept_shapes(seed):
+    c = _sweep(9000 + seed)
+    g, cache, q, gate, sl = make(c["B"], c["L"], c["h"], c["hkv"], c["d"], c["lens"], 9100 + seed, c["layout"],
+                                 c["k_std"], c["v_std"])
+    kw = dict(gate=gate)
+    if c["from_x"] and c["h"] <= 64:
+        kw = dict(x=randn((c["B"], 192), g), w_lambda=randn((192, c["h"]), g, 0.1))
+        gate = bd.diffattn_v2_gate(kw["x"], kw["w_lambda"])
+    w = w_in = before = None
+    if c["weights"]:
+        w_in = torch.rand((c["B"], c["hkv"], c["L"]), generator=g, device="cuda")
+        w = torch.full_like(w_in, -2.0)
+        before = w.clone()
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, softmax_scale=c["scale"], weights_in=w_in, weights_out=w, **kw)
+    kf, vf, rk, rv = ranges(clean(cache, c["lens"]))
+    check_decode(q, kf, vf, rk, rv, c["lens"], f64(gate), out, w, w_in, before, scale=c["scale"] or None)
+
+
 def test_prefix_read_back_feeds_the_forward():
     """A cached prefix read back and attended by diffattn_v2_fwd gives, for the
     last position, the decode's result over the same records."""

@@ -163,6 +163,82 @@ def test_evict_weights_that_tie_or_are_not_numbers(kind):
         run_evict(B, hkv, L, keep, [L], sinks=1 if keep > 1 else 0, weights=w.clone(), seed=keep)
 
 
+@pytest.mark.parametrize("kind", ["equal", "two", "few"])
+def test_evict_ties_across_a_cluster(kind):
+    """Slots that tie spread over the slices of one head's cluster: the lowest
+    of them stay, whichever slice holds them."""
+    L = 70_001
+    r = torch.rand((1, 2, L), generator=gen(722), device="cuda")
+    w = {"equal": torch.full_like(r, 3.0), "two": torch.where(r < 0.5, 1.0, 2.0), "few": (r * 5).floor()}[kind]
+    for keep in (1, 9_000, 35_123, 70_000):
+        run_evict(1, 2, L, keep, [L], sinks=min(keep, 3), recent=min(keep // 2, 500), weights=w.clone(),
+                  widths=((8, BF16),), seed=keep)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_evict_swept(seed):
+    r = np.random.default_rng(9500 + seed)
+    B, hkv, L = int(r.integers(1, 5)), int(r.choice([1, 2, 3, 8])), int(np.exp(r.uniform(0, np.log(12_000))))
+    keep = int(r.integers(1, L + 3))
+    sinks = int(r.integers(0, min(keep, 6) + 1))
+    recent = int(r.integers(0, keep - sinks + 1))
+    lens = [int(x) for x in r.integers(0, L + 1, B)]
+    w = spread((B, hkv, L), 9600 + seed)
+    if r.random() < 0.3:
+        w = w.floor()
+    positions = nxt = None
+    if r.random() < 0.5:
+        seen = L + int(r.integers(0, 50))
+        positions = torch.rand((B, hkv, seen), generator=gen(seed), device="cuda").argsort(-1)[..., :L].int().contiguous()
+        nxt = [seen - int(x) for x in r.integers(0, 10, B)]
+    kinds = [((64, BF16),), ((64, BF16), (64, BF16)), ((80, torch.uint8),), ((8, torch.float32), (16, BF16), (144, torch.uint8))]
+    run_evict(B, hkv, L, keep, lens, sinks=sinks, recent=recent, weights=w, positions=positions, nxt=nxt,
+              widths=kinds[int(r.integers(0, 4))], inplace=bool(r.random() < 0.5), layout=str(r.choice(["head", "token"])),
+              seed=seed)
+
+
+def test_weighted_decode_and_eviction_in_a_graph():
+    """A decode over bf16 caches that gathers weights, with the gate from x, and
+    the eviction that follows, captured together and replayed on new inputs."""
+    t = synth.decode_inputs(2, 600, 4, 2, 128, 256, seed=790, device="cuda")
+    k0, v0 = t["k_cache"].clone(), t["v_cache"].clone()
+    w, sl = torch.zeros((2, 2, 600), device="cuda"), torch.tensor([600, 450], dtype=torch.int32, device="cuda")
+    wo, po, so = torch.zeros_like(w), torch.zeros((2, 2, 600), dtype=torch.int32, device="cuda"), torch.zeros_like(sl)
+    ws = torch.empty((max(bd.diffattn_v2_decode_weighted_workspace_size(2, 4, 2, 128, 600),
+                          bd.diffattn_kv_evict_workspace_size(2, 2, 600, 200)),), dtype=torch.uint8, device="cuda")
+    out = torch.empty((2, 4, 128), dtype=BF16, device="cuda")
+
+    def step():
+        bd.diffattn_v2_decode_weighted(t["q"], t["k_cache"], t["v_cache"], seqlens=sl, x=t["x"], w_lambda=t["w_lambda"],
+                                       weights_out=w, out=out, workspace=ws)
+        bd.diffattn_kv_evict([t["k_cache"], t["v_cache"]], w, 200, sinks=4, recent=32, seqlens=sl, weights_out=wo,
+                             positions_out=po, seqlens_out=so, workspace=ws)
+
+    def restore():
+        t["k_cache"].copy_(k0)
+        t["v_cache"].copy_(v0)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (791, 792):
+        t["q"].copy_(randn((2, 8, 128), gen(seed)))
+        restore()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (out, w, wo, po, so, t["k_cache"], t["v_cache"])]
+        restore()
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, w, wo, po, so, t["k_cache"], t["v_cache"])))
+        for b, n in enumerate((600, 450)):
+            for i in range(2):
+                m, src = kvo.evict(w[b, i, :n].cpu().numpy(), 200, sinks=4, recent=32)
+                assert po[b, i, :m].tolist() == src and torch.equal(t["k_cache"][b, :m, i], k0[b, src, i])
+
+
 def test_evict_without_positions_or_lengths():
     w = spread((1, 2, 64), 730)
     rows = [randn((1, 64, 2, 64), gen(731))]
