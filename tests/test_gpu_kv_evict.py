@@ -265,6 +265,17 @@ def test_evict_bad_length_is_recorded_and_left():
     assert torch.equal(rows[0][:2], before[:2]) and torch.equal(w[:2], w0[:2])
 
 
+def test_evict_many_heads_in_place():
+    """Heads enough for every SM, lengths updated where the other heads of a
+    sequence read them; rows of several kinds."""
+    B, hkv = 44, 8
+    for L, widths in ((97, ((80, torch.uint8),)), (2500, ((64, BF16), (16, BF16)))):
+        lens = [int(x) for x in np.random.default_rng(L).integers(0, L + 1, B)]
+        pos = torch.rand((B, hkv, L + 9), generator=gen(L), device="cuda").argsort(-1)[..., :L].int().contiguous()
+        run_evict(B, hkv, L, L // 2 + 1, lens, sinks=2, recent=L // 9, weights=spread((B, hkv, L), 761), positions=pos,
+                  nxt=[L + 9] * B, widths=widths, inplace=True, layout="token")
+
+
 def test_evict_many_heads():
     B, hkv, L = 40, 8, 130
     lens = [int(x) for x in np.random.default_rng(9).integers(0, L + 1, B)]
