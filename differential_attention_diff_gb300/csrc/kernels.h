@@ -135,6 +135,7 @@ struct Kv4DecodeArgs {
   float* weights_out;
   uint32_t* status;
   bool after_gate;    // the kernel launched just before is this call's gate
+  bool own;           // a block per head, no partials
 };
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 

@@ -43,11 +43,13 @@
 // O) and goes on to the next, and no block-wide barrier stops the loads (warps
 // that shared a head and summed their partials in shared memory took 63 us for
 // 64 sequences of 2048 keys where this takes 46).  A second kernel merges the
-// parts of each head and applies the gate.
+// parts of each head and applies the gate.  Where the heads are few and short, a
+// block takes a whole head instead, merges its warps' partials in shared memory
+// and is done in one launch (the rule and both sides: own_heads in kv_api.cu).
 //
 // Measured (64 query heads, 8 KV heads, d 128): 64 x 32768 keys 405 us with the
 // gate from x, the split kernel 6.2 TB/s of records, 0.91 of a copy; 2 x 131072
-// with the keys' weights 91 us; one sequence of 1000 keys 10 us.  Up to about
+// with the keys' weights 91 us; one sequence of 1000 keys 10 us, in one launch.  Up to about
 // 64 x 8192 keys the instructions bound it (610 a chunk and warp, ALU pipe 60 %
 // busy, tensor pipe 26 %, at 5.4 TB/s), above that the memory nearly does.
 #include "common.cuh"
@@ -55,6 +57,7 @@
 
 #include <type_traits>
 
+#include "decode_merge.cuh"
 #include "kernels.h"
 #include "tma.cuh"
 
@@ -147,14 +150,17 @@ struct Cursor {
 // The reference of a head that has seen no key: any score sends p past 2^8.
 constexpr float kNoMax = -3e38f;
 
-template <int D, int NT, bool kScores>
+// kOwn: a block takes a whole head, shares its chunks out to its warps, merges
+// them and writes the output (and the keys' weights) itself: one launch for
+// short sequences of few heads.
+template <int D, int NT, bool kScores, bool kOwn>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4DecodeArgs a) {
   using C = Cfg<D, NT>;
   constexpr int kW = C::kWarps, kS = C::kStages, kRec = C::kRec, kWords = C::kWords, kGT = C::kGroupTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kW * kS];
-  __shared__ int64_t warp_sum[kW];
-  __shared__ int64_t ends[C::kThreads];  // of a tile of sequences: chunks of one head up to each one's end
+  __shared__ int64_t warp_sum[kOwn ? 1 : kW];
+  __shared__ int64_t ends[kOwn ? 1 : C::kThreads];  // of a tile of sequences: chunks of one head up to each one's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tq = lane & 3;
   const int H2 = 2 * a.h, G = H2 / a.h_kv;
@@ -163,66 +169,85 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   if (tid < kW * kS) mbar_init(smem_u32(&bars[tid]), dense ? 1 : 32);
   fence_mbar_init();
 
-  // ---- this warp's part of the line ----
-  // sequences b0 .. b0 + kThreads - 1 into `ends`; returns the sum up to their end
-  auto sum_tile = [&](int b0, int64_t carry) {
-    const int b = b0 + tid;
-    int64_t x = b < a.B ? seq_chunks(a, b) : 0;
-    if (blockIdx.x == 0 && b < a.B && x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) x += warp_sum[w];
-    x += carry;
-    ends[tid] = x;
-    __syncthreads();
-    return ends[C::kThreads - 1];
-  };
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    if (b0) __syncthreads();
-    sum = sum_tile(b0, sum);
-  }
-  const int64_t total = sum * a.h_kv;
-  const int64_t parts = kv4_parts(total, static_cast<int64_t>(gridDim.x) * kW);
-  // Few parts go to an SM each; as many as there are warps go to each SM side
-  // by side, where they touch fewer pages.
-  const int64_t me = parts < static_cast<int64_t>(gridDim.x) * kW ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
-                                                                  : static_cast<int64_t>(blockIdx.x) * kW + warp;
-  const bool works = me < parts;
-  const int64_t first = works ? me * total / parts : 0, last = works ? (me + 1) * total / parts : 0;
   Cursor at;
-  at.b = -1;
-  int64_t from = 0;  // chunks before the tile, of one head
-  for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
-    if (a.B > C::kThreads) {  // more than one tile: the last one is in `ends` now
-      __syncthreads();
-      sum_tile(b0, from);
+  int64_t me = 0;
+  int take = 0;  // chunks of this warp's part
+  if constexpr (kOwn) {
+    __syncthreads();  // the barriers
+    at.b = blockIdx.x / a.h_kv;
+    at.g = blockIdx.x % a.h_kv;
+    const int n = seq_chunks(a, at.b);
+    if (n == 0) {  // a bad length: recorded, zeros
+      if (tid == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
+      for (int x = tid; x < G / 2 * D; x += C::kThreads)
+        static_cast<__nv_bfloat16*>(a.out)[(static_cast<int64_t>(at.b) * a.h + at.g * (G / 2)) * D + x] = __float2bfloat16_rn(0.f);
+      cudaGridDependencySynchronize();
+      return;
     }
-    if (works && at.b < 0 && first < ends[C::kThreads - 1] * a.h_kv) {
-      // the sequence whose end is the first above `first`
-      for (int i = 0; at.b < 0; i += 32) {
-        const unsigned hit = __ballot_sync(0xffffffffu, ends[i + lane] * a.h_kv > first);
-        if (hit) {
-          const int k = i + __ffs(hit) - 1;
-          at.b = b0 + k;
-          const int64_t before = k ? ends[k - 1] : from;
-          const int n = static_cast<int>(ends[k] - before);
-          const int64_t in = first - before * a.h_kv;
-          at.g = static_cast<int>(in / n);
-          at.chunk = static_cast<int>(in - static_cast<int64_t>(at.g) * n);
+    at.chunk = warp * n / kW;
+    take = (warp + 1) * n / kW - at.chunk;
+  } else {
+    // ---- this warp's part of the line ----
+    // sequences b0 .. b0 + kThreads - 1 into `ends`; returns the sum up to their end
+    auto sum_tile = [&](int b0, int64_t carry) {
+      const int b = b0 + tid;
+      int64_t x = b < a.B ? seq_chunks(a, b) : 0;
+      if (blockIdx.x == 0 && b < a.B && x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) x += warp_sum[w];
+      x += carry;
+      ends[tid] = x;
+      __syncthreads();
+      return ends[C::kThreads - 1];
+    };
+    int64_t sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+      if (b0) __syncthreads();
+      sum = sum_tile(b0, sum);
+    }
+    const int64_t total = sum * a.h_kv;
+    const int64_t parts = kv4_parts(total, static_cast<int64_t>(gridDim.x) * kW);
+    // Few parts go to an SM each; as many as there are warps go to each SM side
+    // by side, where they touch fewer pages.
+    me = parts < static_cast<int64_t>(gridDim.x) * kW ? static_cast<int64_t>(warp) * gridDim.x + blockIdx.x
+                                                                    : static_cast<int64_t>(blockIdx.x) * kW + warp;
+    const bool works = me < parts;
+    const int64_t first = works ? me * total / parts : 0, last = works ? (me + 1) * total / parts : 0;
+    take = static_cast<int>(last - first);
+    at.b = -1;
+    int64_t from = 0;  // chunks before the tile, of one head
+    for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+      if (a.B > C::kThreads) {  // more than one tile: the last one is in `ends` now
+        __syncthreads();
+        sum_tile(b0, from);
+      }
+      if (works && at.b < 0 && first < ends[C::kThreads - 1] * a.h_kv) {
+        // the sequence whose end is the first above `first`
+        for (int i = 0; at.b < 0; i += 32) {
+          const unsigned hit = __ballot_sync(0xffffffffu, ends[i + lane] * a.h_kv > first);
+          if (hit) {
+            const int k = i + __ffs(hit) - 1;
+            at.b = b0 + k;
+            const int64_t before = k ? ends[k - 1] : from;
+            const int n = static_cast<int>(ends[k] - before);
+            const int64_t in = first - before * a.h_kv;
+            at.g = static_cast<int>(in / n);
+            at.chunk = static_cast<int>(in - static_cast<int64_t>(at.g) * n);
+          }
         }
       }
+      from = ends[C::kThreads - 1];
     }
-    from = ends[C::kThreads - 1];
-  }
-  if (!works) {
-    cudaGridDependencySynchronize();  // the gate, where it runs beside this kernel: the merge counts on its end
-    return;
+    if (!works) {
+      cudaGridDependencySynchronize();  // the gate, where it runs beside this kernel: the merge counts on its end
+      return;
+    }
   }
 
   auto enter = [&](Cursor& c, int begin) {  // chunks begin .. of head (c.b, c.g), as far as the part goes
@@ -239,7 +264,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     } while (seq_chunks(a, c.b) == 0);
     enter(c, 0);
   };
-  at.left = static_cast<int>(last - first);
+  at.left = take;
   enter(at, at.chunk);
 
   const uint32_t ring = smem_u32(smem) + warp * kS * C::kSlot;
@@ -601,6 +626,78 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       __syncwarp();  // the slot is read before it is filled again
     }
 
+    if constexpr (kOwn) {
+      // ---- the head's end: all warps' partials, in the ring's place ----
+      __shared__ float2 wml[kW][8 * NT];
+      __shared__ float2 norm[8 * NT];  // maximum and 1 / sum
+      float* park = reinterpret_cast<float*>(smem);  // [warp][head][D]
+      __syncthreads();  // the ring is read (a warp without chunks has m = kNoMax, l = 0, O = 0)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float lt = l[t][e], m0 = mn[t][0][e], m1 = mn[t][1][e];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            lt += __shfl_xor_sync(0xffffffffu, lt, x);
+            m0 += __shfl_xor_sync(0xffffffffu, m0, x);
+            m1 += __shfl_xor_sync(0xffffffffu, m1, x);
+          }
+          const int head = t * 8 + 2 * tq + e;
+          const float f = 1.f / vs[t][e];
+          if (gr == 0) wml[warp][head] = make_float2(mx[t][e], lt);
+#pragma unroll
+          for (int g2 = 0; g2 < 2; ++g2)
+#pragma unroll
+            for (int hw = 0; hw < kWords; ++hw) {
+              const float* x = o[t][g2 * kGT + hw * 2];
+              const float* y = o[t][g2 * kGT + hw * 2 + 1];
+              const float m = g2 ? m1 : m0;
+              *reinterpret_cast<float4*>(park + (warp * 8 * NT + head) * D + g2 * (D / 2) + gr * (D / 16) + hw * 4) =
+                  make_float4(fmaf(x[e] * 0x1p24f, f, m), fmaf(y[e] * 0x1p20f, f, m),
+                              fmaf(x[2 + e] * 0x1p24f, f, m), fmaf(y[2 + e] * 0x1p20f, f, m));
+            }
+        }
+      __syncthreads();
+      if (tid < 8 * NT) {
+        float top = kNoMax, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) top = fmaxf(top, wml[w][tid].x);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) sum += wml[w][tid].y * exp2f(wml[w][tid].x - top);
+        // a sum of 0 is keys that are all -inf: zeros, as in decode.cu; NaN stays
+        norm[tid] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+      }
+      cudaGridDependencySynchronize();  // the gate, where it runs beside this kernel
+      __syncthreads();
+      const int64_t pair0 = static_cast<int64_t>(at.b) * a.h + at.g * (G / 2);
+      for (int x = tid; x < G / 2 * D; x += C::kThreads) {
+        const int p = x / D, f = x % D;
+        float res[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 n = norm[2 * p + e];
+#pragma unroll
+          for (int w = 0; w < kW; ++w)
+            res[e] = fmaf(park[(w * 8 * NT + 2 * p + e) * D + f], exp2f(wml[w][2 * p + e].x - n.x), res[e]);
+          res[e] *= n.y;
+        }
+        store_pair(a.out, a.gate, pair0 + p, D, f, res[0], res[1]);
+      }
+      if constexpr (kScores) {  // written by this block, read after its barriers
+        const float* t0 = a.scores + unit * a.L_max * G;
+        for (int key = tid; key < at.L; key += C::kThreads) {
+          float w = a.weights_in ? a.weights_in[unit * a.L_max + key] : 0.f;
+          for (int p = 0; p < G / 2; ++p) {
+            const float2 t = reinterpret_cast<const float2*>(t0 + static_cast<int64_t>(key) * G)[p];
+            const float2 n0 = norm[2 * p], n1 = norm[2 * p + 1];
+            w += fabsf(__fsub_rn(__fmul_rn(exp2f(t.x - n0.x), n0.y), __fmul_rn(exp2f(t.y - n1.x), n1.y * a.gate[pair0 + p])));
+          }
+          a.weights_out[unit * a.L_max + key] = w;
+        }
+      }
+      break;
+    }
     // ---- the head's end: this warp's partial ----
     const int64_t number = me + unit, row = number * G;
     if (lane == 0) {
@@ -775,31 +872,38 @@ cudaError_t launch_merge_for(const Kv4DecodeArgs& a, cudaStream_t s) {
   return blocks * kThin > a.grid ? launch_merge<D, kThin / 2, 32, true>(a, s) : launch_merge<D, kThin, 64, true>(a, s);
 }
 
-template <int D, int NT, bool kScores>
+template <int D, int NT, bool kScores, bool kOwn>
 cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
   using C = Cfg<D, NT>;
   static_assert(C::kRing <= 220 * 1024, "the ring and the static arrays fit an SM");
   static_assert(C::kWarps <= kKv4MaxWarps, "the workspace has room for every warp's parts");
-  auto* kernel = kv4_split_kernel<D, NT, kScores>;
+  auto* kernel = kv4_split_kernel<D, NT, kScores, kOwn>;
   static OncePerDevice once;
   const cudaError_t e = once.run([&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
   });
   if (e != cudaSuccess) return e;
-  return launch_ahead(kernel, dim3(a.grid), dim3(C::kThreads), C::kRing, s, a.after_gate, a);
+  return launch_ahead(kernel, dim3(kOwn ? a.B * a.h_kv : a.grid), dim3(C::kThreads), C::kRing, s, a.after_gate, a);
+}
+
+template <int D, int NT, bool kOwn>
+cudaError_t launch_scored(const Kv4DecodeArgs& a, cudaStream_t s) {
+  return a.scores ? launch_split<D, NT, true, kOwn>(a, s) : launch_split<D, NT, false, kOwn>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
-  const bool two = 2 * a.h / a.h_kv > 8, sc = a.scores != nullptr;
+  const bool two = 2 * a.h / a.h_kv > 8;
+  if (a.own) {
+    if (a.d == 128) return two ? launch_scored<128, 2, true>(a, s) : launch_scored<128, 1, true>(a, s);
+    return two ? launch_scored<64, 2, true>(a, s) : launch_scored<64, 1, true>(a, s);
+  }
   cudaError_t e;
   if (a.d == 128)
-    e = two ? (sc ? launch_split<128, 2, true>(a, s) : launch_split<128, 2, false>(a, s))
-            : (sc ? launch_split<128, 1, true>(a, s) : launch_split<128, 1, false>(a, s));
+    e = two ? launch_scored<128, 2, false>(a, s) : launch_scored<128, 1, false>(a, s);
   else
-    e = two ? (sc ? launch_split<64, 2, true>(a, s) : launch_split<64, 2, false>(a, s))
-            : (sc ? launch_split<64, 1, true>(a, s) : launch_split<64, 1, false>(a, s));
+    e = two ? launch_scored<64, 2, false>(a, s) : launch_scored<64, 1, false>(a, s);
   if (e != cudaSuccess) return e;
   e = a.d == 128 ? launch_merge_for<128>(a, s) : launch_merge_for<64>(a, s);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;

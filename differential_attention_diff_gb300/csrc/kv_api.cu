@@ -47,6 +47,20 @@ int decode_grid(int B, int h_kv, int L_max, int sms) {
   return static_cast<int>(chunks * h_kv * B < most ? chunks * h_kv * B : most);
 }
 
+// Whether a block takes a whole head and writes its output itself: heads that
+// all find an SM at once, and sequences short enough that 16 warps soon have
+// them, the shorter the fewer heads there are (the other path spreads few heads
+// over all SMs, for two or three launches instead of one).  Replayed, without
+// weights, own block and line: 8 heads of 512 keys 8.5 and 9.7 us, of 1024 10.1
+// and 10.2, of 2048 13.9 and 10.4; 64 of 2048 13.9 and 14.8, of 4096 21.3 and
+// 18.4; 128 of 2048 14.2 and 20.5.  With weights the first is a launch better
+// still (8 of 1024: 11.8 and 12.5 us; called eagerly 14.3 and 17.5).  Lengths
+// below L_max favour the line, which cuts them evenly: hence no more than 2048.
+bool own_heads(int B, int h_kv, int L_max, int sms) {
+  const int64_t heads = static_cast<int64_t>(B) * h_kv;
+  return heads <= sms && (L_max <= 1024 || (L_max <= 2048 && heads >= 64));
+}
+
 struct DecodeSpace {
   size_t ml, parts, norm, scores, gate, total;  // offsets; the partial O rows are at 0
 };
@@ -180,7 +194,8 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
                             reinterpret_cast<da::Kv4Parts*>(ws + w.parts),
                             p->weights_out ? reinterpret_cast<float2*>(ws + w.norm) : nullptr,
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
-                            p->weights_in, p->weights_out, status, p->gate == nullptr};
+                            p->weights_in, p->weights_out, status, p->gate == nullptr,
+                            own_heads(p->B, p->h_kv, p->L_max, sms)};
   return cuda_status(da::launch_kv4_decode(a, s));
 }
 
