@@ -96,7 +96,7 @@ __device__ void move_rows(const EvictArgs& a, int unit, const int* dst, const in
 // CTA's, which also moves the rows (from lists that take the ranks' place) and
 // writes the new length, unless other heads still read it there.
 template <int T, bool kAll, bool kMove>
-__global__ void __launch_bounds__(T, kMove ? 6 : 2048 / T) evict_select_kernel(EvictArgs a, int cached) {
+__global__ void __launch_bounds__(T, kMove ? 1536 / T : 2048 / T) evict_select_kernel(EvictArgs a, int cached) {
   constexpr int kThreads = T, kWarps = T / 32;
   extern __shared__ __align__(16) uint32_t ranks[];  // and behind them the masks
   __shared__ Shared<T> sh;
@@ -427,11 +427,18 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
   // an SM six or more at a time (512 heads of 4352: 32 us, 34 with 512 threads,
   // 41 with 1024; 128 of 8192: 46, 43, 41)
   const bool small = per <= 1024 || (per <= 6144 && static_cast<int64_t>(units) * cs > 2 * a.num_sms);
-  if (small && cs == 1 && units >= a.num_sms) {
-    // heads enough for every SM: each CTA moves its own rows, which saves a
-    // launch and the wait for it (512 heads, 256 of 4352 slots moved: 25.6 us,
-    // 29.4 in two launches)
-    const cudaError_t e = launch_select<256, true, true>(a, cs, cached, smem, s);
+  int64_t chunks = 0;
+  for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
+  // Each CTA moves its own rows, which saves a launch and the wait for it,
+  // unless there are many rows and many SMs without a head to share them with
+  // (512 heads, 256 of 4352 slots moved: 25.6 us, 29.4 in two launches; 8
+  // heads, 1 of 4097: 9.9 and 11.9; 128 heads, 2048 of 8192: 38.2 and 41.6;
+  // but 96 of them 34.2 and 33.0, 16 heads, 1000 of 3000: 16.8 and 12.4)
+  const int64_t idle = units < a.num_sms ? a.num_sms - units : 0;
+  const bool own = small || (per <= 8192 && units <= a.num_sms);
+  if (cs == 1 && own && a.max_moves * chunks * idle <= int64_t{12288} * a.num_sms) {
+    const cudaError_t e = small ? launch_select<256, true, true>(a, cs, cached, smem, s)
+                                : launch_select<1024, true, true>(a, cs, cached, smem, s);
     if (e != cudaSuccess || a.p.seqlens_out != a.p.seqlens) return e;
     return launch_ahead(evict_lengths_kernel, dim3((a.p.B + kMoveThreads - 1) / kMoveThreads), dim3(kMoveThreads), 0, s, true, a);
   }
@@ -440,8 +447,6 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
                                   : launch_select<1024, true>(a, cs, cached, smem, s);
   if (e != cudaSuccess) return e;
   // enough blocks for the most rows that can move, 4 steps of a block each
-  int64_t chunks = 0;
-  for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
   int64_t per_unit = (a.max_moves * chunks + 4 * kMoveThreads - 1) / (4 * kMoveThreads);
   const int64_t most = (16 * a.num_sms + units - 1) / units;  // and no more than fill the GPU twice
   per_unit = per_unit < 1 ? 1 : per_unit > most ? most : per_unit;

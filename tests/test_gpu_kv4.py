@@ -597,6 +597,124 @@ def test_decode_kv4_swept_shapes(seed):
     check_decode(q, kf, vf, rk, rv, c["lens"], f64(gate), out, w, w_in, before, scale=c["scale"] or None)
 
 
+# A cache that can hold more keys than the short path takes sends the same
+# short sequences through the line of chunks and the merge after it; one that
+# cannot gives every head a block.  LINE is past the longest short cache.
+LINE = 2080
+
+
+@pytest.mark.parametrize("layout", ["head", "token", "padded"])
+@pytest.mark.parametrize("d,G", [(d, G) for d in (64, 128) for G in (2, 4, 8, 10, 16)])
+def test_decode_kv4_short_sequences_in_a_long_cache(d, G, layout):
+    lens = [201, 64, 1, 33]
+    g, cache, q, gate, sl = make(4, LINE, G, 2, d, lens, 610 + G + d, layout)
+    w_in = torch.rand((4, 2, LINE), generator=g, device="cuda")
+    w = torch.full_like(w_in, -3.0)
+    before = w.clone()
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_in=w_in, weights_out=w)
+    kf, vf, rk, rv = ranges(clean(cache, lens))
+    check_decode(q, kf, vf, rk, rv, lens, f64(gate), out, w, w_in, before)
+    short = cache[:, :201]  # the same records, a block per head
+    w2 = torch.full((4, 2, 201), -3.0, device="cuda")
+    out2 = bd.diffattn_v2_decode_kv4(q, short, seqlens=sl, gate=gate, weights_in=w_in[..., :201].contiguous(),
+                                     weights_out=w2)
+    check_decode(q, kf, vf, rk, rv, lens, f64(gate), out2, w2, w_in, torch.full_like(w, -3.0)[..., :201])
+
+
+def test_decode_kv4_long_cache_bad_lengths_nan_and_in_place():
+    """The line's own refusals: lengths of 0, below 0 and past the cache beside
+    a good one, a NaN record, weights taken in place."""
+    lens = [0, LINE + 1, -1, 100]
+    g, cache, q, gate, _ = make(4, LINE, 4, 2, 128, [100] * 4, 630)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    w = torch.rand((4, 2, LINE), generator=g, device="cuda")
+    w0 = w.clone()
+    apart = torch.full_like(w, 5.0)
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_in=w, weights_out=apart)
+    assert bd.diffattn_get_device_status() == bd.DA_ERR_BOUNDS
+    again = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_in=w, weights_out=w)
+    assert bd.diffattn_get_device_status() == bd.DA_ERR_BOUNDS
+    assert torch.equal(out, again) and torch.count_nonzero(out[:3]).item() == 0
+    assert torch.equal(w[:3], w0[:3]) and torch.equal(w[3, :, 100:], w0[3, :, 100:])
+    assert torch.equal(w[3, :, :100], apart[3, :, :100]) and float(apart[:3].min()) == float(apart[:3].max()) == 5.0
+    bad = torch.full((1, 1, 2, 128), float("nan"), dtype=BF16, device="cuda")
+    bad[:, :, 1] = 0.5
+    bd.diffattn_kv4_append(bad, bad[:, :, 1:].expand(1, 1, 2, 128).contiguous(), cache[3:],
+                           start=torch.tensor([40], dtype=torch.int32, device="cuda"))
+    out = bd.diffattn_v2_decode_kv4(q[3:], cache[3:], seqlens=sl[3:], gate=gate[3:], weights_out=w[3:])
+    assert bool(torch.isnan(out[0, :2]).all()) and bool(torch.isfinite(out[0, 2:]).all())
+    assert bool(torch.isnan(w[3, 0, :100]).all()) and bool(torch.isfinite(w[3, 1]).all())
+
+
+@pytest.mark.parametrize("case", ["rising", "mixed_v", "sharp"])
+@pytest.mark.parametrize("L", [700, LINE + 120])
+def test_decode_kv4_magnitudes_on_either_path(case, L):
+    """References that must move within a warp's part and between parts, d = 64
+    and two head tiles."""
+    h, hkv, d = 6, 1, 64
+    g = gen(640 + len(case))
+    k, v, q = randn((1, L, hkv, d), g), randn((1, L, hkv, d), g), randn((1, 2 * h, d), g)
+    if case == "rising":
+        k *= torch.linspace(0.05, 6.0, L, device="cuda").to(BF16)[None, :, None, None]
+    elif case == "mixed_v":
+        v *= torch.logspace(-6, 6, L, device="cuda").flip(0).to(BF16)[None, :, None, None]
+    scale = 3.0 if case == "sharp" else 0.0
+    cache = new_cache(1, L, hkv, d)
+    bd.diffattn_kv4_append(k, v, cache)
+    gate = torch.rand((1, h), generator=g, device="cuda")
+    w = torch.zeros((1, hkv, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate, weights_out=w, softmax_scale=scale)
+    kf, vf, rk, rv = ranges(cache.cpu().numpy())
+    check_decode(q, kf, vf, rk, rv, [L], f64(gate), out, w, None, torch.zeros_like(w), scale=scale or None)
+
+
+@pytest.mark.parametrize("more", [-1, 0, 1])
+@pytest.mark.parametrize("L", [1024, 1025, 2048, 2049])
+def test_decode_kv4_where_the_paths_meet(more, L):
+    """As many heads as there are SMs, one more and one fewer, at caches of the
+    lengths where the path changes; most sequences short, the last ones full."""
+    B = torch.cuda.get_device_properties(0).multi_processor_count + more
+    lens = [1 + (7 * b) % 41 for b in range(B)]
+    lens[-1], lens[-2], lens[0] = L, L - 1, 1
+    g, cache, q, gate, sl = make(B, L, 2, 1, 64, lens, 650 + more)
+    w = torch.zeros((B, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_out=w)
+    some = list(range(0, B, 9)) + [B - 2, B - 1]
+    n = [lens[b] for b in some]
+    kf, vf, rk, rv = ranges(clean(cache[some], n))
+    check_decode(q[some], kf, vf, rk, rv, n, f64(gate[some]), out[some], w[some], None, torch.zeros_like(w[some]))
+
+
+@pytest.mark.parametrize("L", [700, LINE])
+def test_decode_kv4_gate_from_x_captured_on_either_path(L):
+    g, cache, q, _, sl = make(2, L, 4, 2, 128, [300, 555], 660)
+    x, wl = randn((2, 256), g), randn((256, 4), g, 0.05)
+    w, w2 = torch.zeros((2, 2, L), device="cuda"), torch.zeros((2, 2, L), device="cuda")
+    ws = torch.empty((bd.diffattn_v2_decode_kv4_workspace_size(2, 4, 2, 128, L, False, True),), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.empty((2, 4, 128), dtype=BF16, device="cuda")
+
+    def step():
+        bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, x=x, w_lambda=wl, weights_out=w, out=out, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (661, 662):
+        x.copy_(randn((2, 256), gen(seed)))
+        q.copy_(randn((2, 8, 128), gen(seed + 10)))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        kf, vf, rk, rv = ranges(clean(cache, [300, 555]))
+        check_decode(q, kf, vf, rk, rv, [300, 555], f64(bd.diffattn_v2_gate(x, wl)), out, w, None, w2)
+
+
 def test_prefix_read_back_feeds_the_forward():
     """A cached prefix read back and attended by diffattn_v2_fwd gives, for the
     last position, the decode's result over the same records."""

@@ -276,6 +276,28 @@ def test_evict_many_heads_in_place():
                   nxt=[L + 9] * B, widths=widths, inplace=True, layout="token")
 
 
+@pytest.mark.parametrize("more", [-1, 0, 1])
+@pytest.mark.parametrize("L,keep,widths", [(1000, 900, ((128, BF16), (256, BF16))), (6200, 6000, ((16, BF16),)),
+                                           (8192, 4096, ((8, BF16),)), (8193, 4097, ((8, BF16),))])
+def test_evict_as_many_heads_as_sms(more, L, keep, widths):
+    """One head per SM, one more, one fewer: rows moved by the head's own block
+    or by a launch of their own."""
+    B = torch.cuda.get_device_properties(0).multi_processor_count + more
+    lens = [L - (b % 5) * (L // 6) for b in range(B)]
+    run_evict(B, 1, L, keep, lens, sinks=4, recent=50, weights=spread((B, 1, L), 765), widths=widths, inplace=True)
+
+
+@pytest.mark.parametrize("keep", [99, 100, 350])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_evict_few_heads_with_few_and_many_rows(keep, inplace):
+    """Three heads whose rows to move are just below and above what their own
+    blocks take; several sequences with the lengths updated in place."""
+    B, hkv, L = 3, 2, 700
+    pos = torch.rand((B, hkv, 900), generator=gen(5), device="cuda").argsort(-1)[..., :L].int().contiguous()
+    run_evict(B, hkv, L, keep, [700, 351, 90], sinks=3, recent=20, weights=spread((B, hkv, L), 766), positions=pos,
+              nxt=[900] * B, widths=((256, BF16), (256, BF16), (512, BF16)), inplace=inplace)
+
+
 def test_evict_many_heads():
     B, hkv, L = 40, 8, 130
     lens = [int(x) for x in np.random.default_rng(9).integers(0, L + 1, B)]
