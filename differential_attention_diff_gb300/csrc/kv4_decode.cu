@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     if constexpr (kOwn) {
       // ---- the head's end: all warps' partials, in the ring's place ----
       __shared__ float2 wml[kW][8 * NT];
-      __shared__ float2 norm[8 * NT];  // maximum and 1 / sum
+      __shared__ float2 norm[8 * NT];      // maximum and 1 / sum
+      __shared__ float factor[kW][8 * NT];  // of each warp's part in its head's sum
       float* park = reinterpret_cast<float*>(smem);  // [warp][head][D]
       __syncthreads();  // the ring is read (a warp without chunks has m = kNoMax, l = 0, O = 0)
 #pragma unroll
@@ -659,14 +660,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             }
         }
       __syncthreads();
-      if (tid < 8 * NT) {
-        float top = kNoMax, sum = 0.f;
+      if (tid < 8 * NT * kW) {  // kW lanes side by side for each head
+        const int w = tid % kW, head = tid / kW;
+        const float2 part = wml[w][head];
+        float top = part.x;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) top = fmaxf(top, wml[w][tid].x);
+        for (int x = 1; x < kW; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float down = exp2f(part.x - top);
+        float sum = part.y * down;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) sum += wml[w][tid].y * exp2f(wml[w][tid].x - top);
+        for (int x = 1; x < kW; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         // a sum of 0 is keys that are all -inf: zeros, as in decode.cu; NaN stays
-        norm[tid] = make_float2(top, sum == 0.f ? 0.f : 1.f / sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        factor[w][head] = down * inv;
+        if (w == 0) norm[head] = make_float2(top, inv);
       }
       cudaGridDependencySynchronize();  // the gate, where it runs beside this kernel
       __syncthreads();
@@ -675,13 +682,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         const int p = x / D, f = x % D;
         float res[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 n = norm[2 * p + e];
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int w = 0; w < kW; ++w)
-            res[e] = fmaf(park[(w * 8 * NT + 2 * p + e) * D + f], exp2f(wml[w][2 * p + e].x - n.x), res[e]);
-          res[e] *= n.y;
-        }
+          for (int w = 0; w < kW; ++w) res[e] = fmaf(park[(w * 8 * NT + 2 * p + e) * D + f], factor[w][2 * p + e], res[e]);
         store_pair(a.out, a.gate, pair0 + p, D, f, res[0], res[1]);
       }
       if constexpr (kScores) {  // written by this block, read after its barriers
