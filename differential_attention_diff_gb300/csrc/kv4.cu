@@ -61,25 +61,66 @@ struct RowWalk {
   }
 };
 
-// Eight codes of bf16 pairs w: rint((x - lo) / s) for (x - lo) in
-// [0, 15.03 s], exactly, without a division.  f is the quotient less a half,
-// rounded, so that the code is f or f + 1 whatever the reciprocal's error, and
-// c = (f + 1/2) s, which fp32 holds exactly (f has 4 bits and s 8), decides; a
-// tie goes to the even one, so for an odd f the comparison is against the
-// number just below c.  f stays in the low bits of 1.5 2^23 + f and the codes
-// are summed with those bits; what the eight constants add to is taken off.
+// Two fp32 numbers in a register pair: one instruction for both.
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit F2(unsigned long long x) : v(x) {}
+  __device__ __forceinline__ uint2 bits() const {
+    uint2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return F2(r);
+}
+
+// x / 15, rounded once; NaN and infinity stay something that is not finite.
+__device__ __forceinline__ float fifteenth(float x) {
+  if (x > 0.f && x < 0x1p-90f) return __fdiv_rn(x, 15.f);  // the residual may not be a normal number
+  const float q = x * (1.f / 15.f);
+  return fmaf(fmaf(q, -15.f, x), 1.f / 15.f, q);
+}
+__device__ __forceinline__ float reciprocal(float x) {  // within an ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight codes of bf16 pairs w: rint(t / s) for t = x - lo in [0, 15.03 s],
+// exactly, without a division.  q = t inv is off by an ulp or two; its residual
+// t - q s fits fp32, and q + residual inv is rounded once, from a value within
+// 2^-21 ulp of t / s: the rounded quotient, but where t / s lies that close to
+// the middle between two numbers.  The rounding to a code could still go wrong
+// where t / s lies within half an ulp of a tie k + 1/2 without being one; but
+// (k + 1/2) s has 13 bits and t 24, so that they differ by more than that (by
+// 2^-24 t (1 + 2^-13) at least, half an ulp of the tie being 2^-24 of it at
+// most), and a true tie comes out exactly.  The code stays in the low bits of
+// 1.5 2^23 + q and is summed with those bits; what the eight constants add to
+// is taken off.
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, float s, float inv) {
   constexpr float kMagic = 12582912.f;  // 0x4b400000
-  const float half_s = 0.5f * s;
+  const F2 inv2(inv, inv), s2(-s, -s), lo2(-lo, -lo), magic(kMagic, kMagic);
   uint32_t sum = 0;
 #pragma unroll
-  for (int e = 7; e >= 0; --e) {
-    const float t = __fsub_rn((e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]), lo);
-    const float r = fmaf(t, inv, -0.5f) + kMagic;
-    const uint32_t bits = __float_as_uint(r);
-    const float c = fmaf(r - kMagic, s, half_s);
-    sum = sum * 16u + bits;
-    if (t > __uint_as_float(__float_as_uint(c) - (bits & 1u))) ++sum;
+  for (int e = 3; e >= 0; --e) {
+    const F2 t = add2(F2(bf16_lo(w[e]), bf16_hi(w[e])), lo2);
+    const F2 q = mul2(t, inv2);
+    const uint2 code = add2(fma2(fma2(q, s2, t), inv2, q), magic).bits();
+    sum = (sum * 16u + code.y) * 16u + code.x;
   }
   return sum - 0x4b400000u * 0x11111111u;
 }
@@ -136,13 +177,13 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4RowsArgs a, int
         }
         float lo = __bfloat162float(__hmin_nan(lo2.x, lo2.y));
         const float hi = __bfloat162float(__hmax_nan(hi2.x, hi2.y));
-        float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
+        float s = __bfloat162float(__float2bfloat16_rn(fifteenth(__fsub_rn(hi, lo))));
         const bool bad = !(fabsf(s) < INFINITY);
         uint2 codes = make_uint2(0, 0);
         if (s >= 0x1p-100f && !bad) {
-          const float inv = __frcp_rn(s);
+          const float inv = reciprocal(s);
           codes = make_uint2(codes_of(w0, lo, s, inv), codes_of(w1, lo, s, inv));
-        } else if (s > 0.f && !bad) {  // the reciprocal or the half step may not be normal numbers
+        } else if (s > 0.f && !bad) {  // the reciprocal or the residual may not be normal numbers
           for (int e = 0; e < 16; ++e) {
             const uint32_t w = (e & 8) ? w1[(e & 7) >> 1] : w0[e >> 1];
             const float x = (e & 1) ? bf16_hi(w) : bf16_lo(w);
