@@ -9,6 +9,7 @@
 // memory alone: with 656 bytes moved per record, an SM has about 28 cycles for
 // one, so what counts is the instructions per feature.
 #include "common.cuh"
+#include "fp32_pair.cuh"
 #include "kernels.h"
 
 namespace da {
@@ -60,33 +61,6 @@ struct RowWalk {
     }
   }
 };
-
-// Two fp32 numbers in a register pair: one instruction for both.
-struct F2 {
-  unsigned long long v;
-  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
-  __device__ __forceinline__ explicit F2(unsigned long long x) : v(x) {}
-  __device__ __forceinline__ uint2 bits() const {
-    uint2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(v));
-    return r;
-  }
-};
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-  return F2(r);
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
-  return F2(r);
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return F2(r);
-}
 
 // x / 15, rounded once; NaN and infinity stay something that is not finite.
 __device__ __forceinline__ float fifteenth(float x) {

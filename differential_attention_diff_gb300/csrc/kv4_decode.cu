@@ -26,7 +26,8 @@
 // tensor cores, whose accumulators are truncated at each step, it lost 2.2e-3
 // of the output (B64 L32768), more than the output's own rounding.  Sums of 32
 // keys, added with rounding, lose nothing that shows, for an addition per
-// accumulator and chunk.
+// accumulator and chunk; at d 128 two accumulators share one (64 x 32768:
+// 398 -> 388.5 us; at d 64 it measured slower, 78.6 -> 83.5 at 64 x 8192).
 //
 // P is fp16 (11 bits, against 8 of a bf16 P).  Its range is kept by a power
 // of two per head, vs, beside the running maximum m of the scores: both are
@@ -58,6 +59,7 @@
 #include <type_traits>
 
 #include "decode_merge.cuh"
+#include "fp32_pair.cuh"
 #include "kernels.h"
 #include "tma.cuh"
 
@@ -104,6 +106,18 @@ __device__ __forceinline__ void mma_f16_16816_first(float* d, uint32_t a0, uint3
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// x[0..1] += y[0..1], in one instruction if kOne.
+template <bool kOne>
+__device__ __forceinline__ void add_pair(float* x, const float* y) {
+  if constexpr (kOne) {
+    const uint2 r = add2(F2(x[0], x[1]), F2(y[0], y[1])).bits();
+    x[0] = __uint_as_float(r.x);
+    x[1] = __uint_as_float(r.y);
+  } else {
+    x[0] += y[0];
+    x[1] += y[1];
+  }
 }
 // 8x8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -612,9 +626,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                o[t][g2 * kGT + hw * 2][i] += even[t][i];
-                o[t][g2 * kGT + hw * 2 + 1][i] += odd[t][i];
+              for (int i = 0; i < 4; i += 2) {
+                add_pair<D == 128>(&o[t][g2 * kGT + hw * 2][i], &even[t][i]);
+                add_pair<D == 128>(&o[t][g2 * kGT + hw * 2 + 1][i], &odd[t][i]);
               }
           }
         }
