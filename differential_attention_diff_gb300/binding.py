@@ -13,6 +13,7 @@ raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import struct
 import threading
@@ -684,8 +685,16 @@ def _new(make, like, shape, dtype, stream):
         return make(shape, dtype=dtype, device=like.device)
 
 
+@functools.lru_cache(maxsize=4096)
+def _need(dev, name, *args):
+    """The workspace_size entry point `name`; a function of its arguments and the (current) device dev."""
+    return getattr(load(), name)(*args)
+
+
 def _space(workspace, dev):
-    """(pointer, bytes) of a workspace."""
+    """(pointer, bytes) of a workspace; None is none."""
+    if workspace is None:
+        return 0, 0
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on device {dev} expected")
     return workspace.data_ptr(), workspace.nbytes
@@ -761,8 +770,10 @@ def diffattn_v2_decode_kv4(q, cache, *, seqlens=None, gate=None, x=None, w_lambd
     if out is None:
         out = _new(torch.empty, q, (B, h, d), bf16, stream)
     if workspace is None:
-        need = diffattn_v2_decode_kv4_workspace_size(B, h, hkv, d, L_max, gate is not None, weights_out is not None)
-        workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
+        need = _need(dev, "diffattn_v2_decode_kv4_workspace_size", B, h, hkv, d, L_max, gate is not None,
+                     weights_out is not None)
+        if need:
+            workspace = _new(torch.empty, q, (need,), torch.uint8, stream)
     gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
     per_slot = (B, hkv, L_max)
     _call("diffattn_v2_decode_kv4", _pack_decode_kv4(
@@ -791,7 +802,8 @@ def diffattn_v2_decode_weighted(q, k_cache, v_cache, *, weights_out, weights_in=
     if out is None:
         out = _new(torch.empty, q, (B, h, d), bf16, stream)
     if workspace is None:
-        need = diffattn_v2_decode_weighted_workspace_size(B, h, hkv, d, L_max, num_splits, gate is not None)
+        need = _need(dev, "diffattn_v2_decode_weighted_workspace_size", B, h, hkv, d, L_max, num_splits,
+                     gate is not None)
         workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
     gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, B, h, dev)
     rows, per_slot = (B, L_max, hkv, d), (B, hkv, L_max)
@@ -829,7 +841,7 @@ def diffattn_kv_evict(rows, key_weights, keep, *, sinks=0, recent=0, seqlens=Non
     if seqlens_out is None:
         seqlens_out = _new(torch.empty, key_weights, (B,), i32, stream) if seqlens is None else seqlens
     if workspace is None:
-        need = diffattn_kv_evict_workspace_size(B, hkv, L_max, keep)
+        need = _need(dev, "diffattn_kv_evict_workspace_size", B, hkv, L_max, keep)
         workspace = _new(torch.empty, key_weights, (max(need, 1),), torch.uint8, stream)
     row_bytes, views = [0] * DIFFATTN_EVICT_MAX_ROWS, [0] * (4 * DIFFATTN_EVICT_MAX_ROWS)
     for i, r in enumerate(rows):

@@ -161,13 +161,15 @@ struct EvictArgs {
   da_kv_evict_params p;
   int* n_moves;  // [B * h_kv]
   int* new_len;  // [B]
-  int* dst;      // [B * h_kv, max_moves]
-  int* src;      // [B * h_kv, max_moves]
+  int* dst;      // [B * h_kv, max_moves], but for evict_moves_unlisted
+  int* src;
   int max_moves;
   uint32_t* status;
   int num_sms;
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
+// Whether every head's own block moves its rows, whatever they are: no lists in memory.
+bool evict_moves_unlisted(int64_t units, int L_max, int sms);
 
 // ---- V1 decode: split-KV partials of both streams, then merge + RMSNorm ----
 struct V1DecodeArgs {

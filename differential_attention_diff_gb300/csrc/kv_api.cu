@@ -61,17 +61,22 @@ bool own_heads(int B, int h_kv, int L_max, int sms) {
   return heads <= sms && (L_max <= 1024 || (L_max <= 2048 && heads >= 64));
 }
 
+// Blocks that take whole heads need room for the scores and the gate only; the
+// others for a part per warp, or per chunk where there are fewer, and head.
 struct DecodeSpace {
   size_t ml, parts, norm, scores, gate, total;  // offsets; the partial O rows are at 0
 };
-DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights, int grid) {
-  const size_t rows =
-      (static_cast<size_t>(grid) * da::kKv4MaxWarps + static_cast<size_t>(B) * h_kv) * (2 * h / h_kv);
+DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights, int sms) {
+  const int64_t heads = static_cast<int64_t>(B) * h_kv;
+  const bool own = own_heads(B, h_kv, L_max, sms);
+  const int64_t chunks = (static_cast<int64_t>(L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys * heads;
+  const int64_t warps = static_cast<int64_t>(decode_grid(B, h_kv, L_max, sms)) * da::kKv4MaxWarps;
+  const size_t rows = own ? 0 : static_cast<size_t>((chunks < warps ? chunks : warps) + heads) * (2 * h / h_kv);
   DecodeSpace w;
   w.ml = align256(rows * d * sizeof(float));
   w.parts = w.ml + align256(rows * 2 * sizeof(float));
-  w.norm = w.parts + align256(static_cast<size_t>(B) * h_kv * sizeof(da::Kv4Parts));
-  w.scores = w.norm + align256(static_cast<size_t>(B) * 2 * h * sizeof(float2));
+  w.norm = w.parts + (own ? 0 : align256(heads * sizeof(da::Kv4Parts)));
+  w.scores = w.norm + (own ? 0 : align256(static_cast<size_t>(B) * 2 * h * sizeof(float2)));
   w.gate = w.scores + (weights ? align256(static_cast<size_t>(B) * 2 * h * L_max * sizeof(float)) : 0);
   w.total = w.gate + (gate_given ? 0 : align256(static_cast<size_t>(B) * h * sizeof(float)));
   return w;
@@ -81,15 +86,16 @@ struct EvictSpace {
   size_t len, dst, src, total;  // offsets; the move counts are at 0
   int max_moves;
 };
-EvictSpace evict_space(int B, int h_kv, int L_max, int keep) {
+EvictSpace evict_space(int B, int h_kv, int L_max, int keep, int sms) {
   const size_t units = static_cast<size_t>(B) * h_kv;
   EvictSpace w;
   // a head moves one row per slot below m that goes: at most min(m, L - m)
   w.max_moves = keep >= L_max ? 0 : (keep < L_max - keep ? keep : L_max - keep);
   w.len = align256(units * sizeof(int));
   w.dst = w.len + align256(static_cast<size_t>(B) * sizeof(int));
-  w.src = w.dst + align256(units * w.max_moves * sizeof(int));
-  w.total = w.src + align256(units * w.max_moves * sizeof(int));
+  const size_t listed = da::evict_moves_unlisted(units, L_max, sms) ? 0 : units * w.max_moves;
+  w.src = w.dst + align256(listed * sizeof(int));
+  w.total = w.src + align256(listed * sizeof(int));
   return w;
 }
 
@@ -135,7 +141,7 @@ size_t diffattn_v2_decode_kv4_workspace_size(int B, int h, int h_kv, int d, int 
   uint32_t* status;
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
-  return decode_space(B, h, h_kv, d, L_max, gate_given, weights, decode_grid(B, h_kv, L_max, sms)).total;
+  return decode_space(B, h, h_kv, d, L_max, gate_given, weights, sms).total;
 }
 
 da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream) {
@@ -169,8 +175,9 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
   if (!device) sms = 152;  // the workspace is checked first, as the size query would have it
   int grid = decode_grid(p->B, p->h_kv, p->L_max, sms);
   const DecodeSpace w =
-      decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr, grid);
-  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
+      decode_space(p->B, p->h, p->h_kv, p->d, p->L_max, p->gate != nullptr, p->weights_out != nullptr, sms);
+  if (w.total > 0 && (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)))
+    return DA_ERR_WORKSPACE;
   if (!device) return DA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
@@ -201,7 +208,10 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
 
 size_t diffattn_kv_evict_workspace_size(int B, int h_kv, int L_max, int keep) {
   if (B <= 0 || h_kv <= 0 || L_max <= 0 || keep <= 0) return 0;
-  return evict_space(B, h_kv, L_max, keep).total;
+  uint32_t* status;
+  int sms = 152;
+  if (!da::device_handles(&status, &sms)) sms = 152;
+  return evict_space(B, h_kv, L_max, keep, sms).total;
 }
 
 da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
@@ -223,11 +233,13 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* stream) {
   if (static_cast<int64_t>(p->B) * p->h_kv > (1 << 24) || p->L_max > da::kEvictMaxSlots) return DA_ERR_UNSUPPORTED;
   for (int k = 0; k < p->n_rows; ++k)
     if (static_cast<int64_t>(p->L_max) * (p->row_bytes[k] / 16) > (1 << 30)) return DA_ERR_UNSUPPORTED;
-  const EvictSpace w = evict_space(p->B, p->h_kv, p->L_max, p->keep);
-  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   uint32_t* status;
-  int sms;
-  if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
+  int sms = 152;
+  const bool device = da::device_handles(&status, &sms);
+  if (!device) sms = 152;  // the workspace is checked first, as the size query would have it
+  const EvictSpace w = evict_space(p->B, p->h_kv, p->L_max, p->keep, sms);
+  if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
+  if (!device) return DA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   const da::EvictArgs a{*p, reinterpret_cast<int*>(ws), reinterpret_cast<int*>(ws + w.len),
                         reinterpret_cast<int*>(ws + w.dst), reinterpret_cast<int*>(ws + w.src), w.max_moves, status, sms};

@@ -409,24 +409,39 @@ cudaError_t launch_select(const EvictArgs& a, int cs, int cached, size_t smem, c
 
 }  // namespace
 
-cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
-  const int units = a.p.B * a.p.h_kv;
+namespace {
+
+struct Plan {
+  int cs, per;  // CTAs per head, slots of each
+  bool small;   // 256 threads instead of 1024
+};
+Plan plan_of(int64_t units, int L_max, int sms) {
   // Spread a head over a cluster while that leaves no SM two CTAs and each
   // still has 8192 slots (64 heads of 33000: 1, 2, 4, 8 CTAs took 32, 27, 33,
   // 68 us; 8 heads of 131072: 231, 112, 35, 31; 8 of 4097: 11.5 and, with 2,
   // 14.0); a slice that would pass kMaxRanks asks for more too.
   int cs = 1;
-  while (cs < kMaxCluster &&
-         ((static_cast<int64_t>(units) * cs * 2 <= a.num_sms && a.p.L_max / cs > 8192) || a.p.L_max / cs > kMaxRanks))
-    cs *= 2;
-  const int per = ((a.p.L_max + cs - 1) / cs + 31) / 32 * 32;
-  const int cached = per < kMaxRanks ? per : kMaxRanks;
-  const size_t smem = (static_cast<size_t>(cached) + per / 32) * sizeof(uint32_t);
-  if (smem > kMaxSelectSmem) return cudaErrorInvalidValue;  // refused by the entry point before
+  while (cs < kMaxCluster && ((units * cs * 2 <= sms && L_max / cs > 8192) || L_max / cs > kMaxRanks)) cs *= 2;
+  const int per = ((L_max + cs - 1) / cs + 31) / 32 * 32;
   // 1024 threads, but 256 for short heads that are many: their CTAs then share
   // an SM six or more at a time (512 heads of 4352: 32 us, 34 with 512 threads,
   // 41 with 1024; 128 of 8192: 46, 43, 41)
-  const bool small = per <= 1024 || (per <= 6144 && static_cast<int64_t>(units) * cs > 2 * a.num_sms);
+  return {cs, per, per <= 1024 || (per <= 6144 && units * cs > 2 * sms)};
+}
+
+}  // namespace
+
+bool evict_moves_unlisted(int64_t units, int L_max, int sms) {
+  const Plan p = plan_of(units, L_max, sms);
+  return p.cs == 1 && p.small && units >= sms;
+}
+
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
+  const int units = a.p.B * a.p.h_kv;
+  const auto [cs, per, small] = plan_of(units, a.p.L_max, a.num_sms);
+  const int cached = per < kMaxRanks ? per : kMaxRanks;
+  const size_t smem = (static_cast<size_t>(cached) + per / 32) * sizeof(uint32_t);
+  if (smem > kMaxSelectSmem) return cudaErrorInvalidValue;  // refused by the entry point before
   int64_t chunks = 0;
   for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
   // Each CTA moves its own rows, which saves a launch and the wait for it,

@@ -528,9 +528,9 @@ da_status diffattn_kv4_read(const da_kv4_read_params* p, void* cuda_stream);
  * for j < seqlens[b]; the other positions are left as they were.  Both fp32
  * [B, h_kv, L_max] contiguous; weights_in NULL = 0, and it may be the same
  * array as weights_out (it may not overlap it otherwise).
- * workspace: diffattn_v2_decode_kv4_workspace_size bytes, 256-byte aligned,
- * contents on entry irrelevant; calls that run at the same time need
- * workspaces of their own.  Results are bitwise reproducible from call to
+ * workspace: diffattn_v2_decode_kv4_workspace_size bytes (which may be 0: then
+ * it is not looked at), 256-byte aligned, contents on entry irrelevant; calls
+ * that run at the same time need workspaces of their own.  Results are bitwise reproducible from call to
  * call.  B, h_kv at most 65535, B * h_kv at most 2^28, L_max at most 2^30. */
 typedef struct {
   int B, h, h_kv, d, L_max, d_model;

@@ -143,13 +143,21 @@ def test_decode_kv4_argument_checks(lib):
     for bad in (dict(d=96), dict(h=128), dict(gate=None, x=FAKE, w_lambda=FAKE, d_model=100), dict(B=65536),
                 dict(L_max=(1 << 30) + 1)):
         assert f(_with(p, **bad), None) == bd.DA_ERR_UNSUPPORTED, bad
-    need = lib.diffattn_v2_decode_kv4_workspace_size(2, 32, 8, 128, 1024, 1, 0)
+    size = lib.diffattn_v2_decode_kv4_workspace_size
+    p.L_max = 4096
+    need = size(2, 32, 8, 128, 4096, 1, 0)
     assert f(_with(p), None) == bd.DA_ERR_WORKSPACE
     assert f(_with(p, workspace=FAKE, workspace_bytes=need - 1), None) == bd.DA_ERR_WORKSPACE
     assert f(_with(p, workspace=FAKE + 128, workspace_bytes=need), None) == bd.DA_ERR_WORKSPACE
     # gathering needs room for a score per query head and key
-    assert (lib.diffattn_v2_decode_kv4_workspace_size(2, 32, 8, 128, 1024, 1, 1) - need) >= 2 * 64 * 1024 * 4
+    assert size(2, 32, 8, 128, 4096, 1, 1) - need >= 2 * 64 * 4096 * 4
     assert f(_with(p, weights_out=FAKE, workspace=FAKE, workspace_bytes=need), None) == bd.DA_ERR_WORKSPACE
+    # few short heads need room for the scores and the gate only
+    assert size(2, 32, 8, 128, 1024, 1, 0) == 0
+    assert size(2, 32, 8, 128, 1024, 0, 0) == 2 * 32 * 4 and size(2, 32, 8, 128, 1024, 1, 1) == 2 * 64 * 1024 * 4
+    p.L_max = 1024
+    assert f(_with(p, weights_out=FAKE), None) == bd.DA_ERR_WORKSPACE
+    assert f(_with(p, gate=None, x=FAKE, w_lambda=FAKE, d_model=64), None) == bd.DA_ERR_WORKSPACE
     assert lib.diffattn_v2_decode_kv4_workspace_size(0, 32, 8, 128, 1024, 1, 0) == 0
 
 
