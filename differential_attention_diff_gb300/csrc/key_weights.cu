@@ -47,7 +47,10 @@ __device__ __forceinline__ float2 head_norm(const FinishArgs& a, int64_t head) {
 template <int P>
 __global__ void __launch_bounds__(kThreads) decode_finish_kernel(FinishArgs a, int merge_blocks) {
   constexpr int G = 2 * P;
-  cudaGridDependencySynchronize();  // scores and partials
+  // Scores and partials.  Over a 4-bit cache they were there before the merge
+  // that runs ahead of this kernel let it start; only the normalisers are
+  // waited for, below.
+  if (!a.norm) cudaGridDependencySynchronize();
   const int tid = threadIdx.x;
   if (blockIdx.x < static_cast<unsigned>(merge_blocks)) {
     const int64_t pair = static_cast<int64_t>(blockIdx.x) * (kThreads / a.d) + tid / a.d;
@@ -66,9 +69,13 @@ __global__ void __launch_bounds__(kThreads) decode_finish_kernel(FinishArgs a, i
   const int b = static_cast<int>(unit / a.h_kv);
   const int key0 = static_cast<int>(block % per) * kBlockKeys;
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
-  if (L < 1 || L > a.L_max || key0 >= L) return;  // a bad length is recorded by the split kernel
+  if (L < 1 || L > a.L_max || key0 >= L) {  // a bad length is recorded by the split kernel
+    if (a.norm) cudaGridDependencySynchronize();
+    return;
+  }
   const int64_t base = unit * a.L_max;
-  // loads first: they do not wait for the normalisers
+  // loads first: they do not wait for the normalisers (and go to L2, as nothing
+  // has been waited for yet that would say what L1 holds)
   float2 t[kKeys][P];
   float w[kKeys];
 #pragma unroll
@@ -79,17 +86,18 @@ __global__ void __launch_bounds__(kThreads) decode_finish_kernel(FinishArgs a, i
       if constexpr (P % 2 == 0) {
 #pragma unroll
         for (int p = 0; p < P; p += 2) {
-          const float4 v = reinterpret_cast<const float4*>(s)[p / 2];
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + p / 2);
           t[k][p] = make_float2(v.x, v.y);
           t[k][p + 1] = make_float2(v.z, v.w);
         }
       } else {
 #pragma unroll
-        for (int p = 0; p < P; ++p) t[k][p] = reinterpret_cast<const float2*>(s)[p];
+        for (int p = 0; p < P; ++p) t[k][p] = __ldcg(reinterpret_cast<const float2*>(s) + p);
       }
-      w[k] = a.weights_in ? a.weights_in[base + key] : 0.f;
+      w[k] = a.weights_in ? __ldcg(a.weights_in + base + key) : 0.f;
     }
   }
+  if (a.norm) cudaGridDependencySynchronize();
   for (int r = tid >> 5; r < G; r += kWarps) {
     const float2 n = head_norm(a, unit * G + r);
     if ((tid & 31) == 0) {

@@ -798,6 +798,8 @@ __global__ void __launch_bounds__(WAYS * D / SLICES / 2) kv4_merge_kernel(Kv4Dec
   const int L = a.seqlens ? a.seqlens[b] : a.L_max;
   const bool bad = L < 1 || L > a.L_max;  // recorded by the split kernel
   cudaGridDependencySynchronize();        // the parts
+  // the weights' kernel may start: its scores are there, it waits for the norms
+  cudaTriggerProgrammaticLaunchCompletion();
   int64_t first = 0;
   int count = 0;
   if (!bad) {
