@@ -136,6 +136,7 @@ struct Kv4DecodeArgs {
   uint32_t* status;
   bool after_gate;    // the kernel launched just before is this call's gate
   bool own;           // a block per head, no partials
+  int late_blocks;    // of the grid's end, which have to wait for the gate's SMs
 };
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 

@@ -188,12 +188,19 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
     if (da::launch_gate(ga, s) != cudaSuccess) return DA_ERR_CUDA;
     gate = g;
   }
-  // The gate projection takes 8 SMs for about 8 us, and the work is cut evenly:
-  // up to 48 chunks a warp the decode leaves them alone (gate from x at 64 x
-  // 2048 keys: 51 us on all SMs, 46 on the others; at 64 x 8192, 54 chunks:
-  // 121 and 120; at 64 x 32768: 395 and 409).
+  // The gate projection takes 8 SMs for about 8 us (more from 65 sequences on).
+  // Short work leaves them alone (64 x 2048 keys: 51 us on all SMs, 46 on the
+  // others); long work takes them too, and the blocks that start there last get
+  // a little less of it (64 x 5120, 34 chunks a warp: 83.5 and 82.4 us; x 7000:
+  // 106.5 and 103.7; x 32768: 409 and 390, 396 with equal parts).
   const int64_t chunks = (static_cast<int64_t>(p->L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys * p->h_kv * p->B;
-  if (p->gate == nullptr && grid > sms - 8 && sms > 16 && chunks <= 48LL * da::kKv4MaxWarps * sms) grid = sms - 8;
+  int late = 0;
+  if (p->gate == nullptr && grid > sms - 8 && sms > 16) {
+    if (chunks <= (p->B <= 64 ? 32LL : 48LL) * da::kKv4MaxWarps * sms)
+      grid = sms - 8;
+    else if (p->B <= 64)  // 8 CTAs of gate.cu, a cluster
+      late = 8;
+  }
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.f / std::sqrt(static_cast<float>(p->d));
   const da::Kv4DecodeArgs a{p->B, p->h, p->h_kv, p->d, p->L_max, grid,
                             scale * kLog2e, p->q, p->cache, p->seqlens, gate, p->out,
@@ -202,7 +209,7 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
                             p->weights_out ? reinterpret_cast<float2*>(ws + w.norm) : nullptr,
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
                             p->weights_in, p->weights_out, status, p->gate == nullptr,
-                            own_heads(p->B, p->h_kv, p->L_max, sms)};
+                            own_heads(p->B, p->h_kv, p->L_max, sms), late};
   return cuda_status(da::launch_kv4_decode(a, s));
 }
 

@@ -715,6 +715,28 @@ def test_decode_kv4_gate_from_x_captured_on_either_path(L):
         check_decode(q, kf, vf, rk, rv, [300, 555], f64(bd.diffattn_v2_gate(x, wl)), out, w, None, w2)
 
 
+@pytest.mark.parametrize("lens,d,G", [([80000] * 4, 64, 2), ([80000, 79999, 70001, 80000], 64, 12),
+                                      ([80000, 1, 33, 64], 64, 4), ([80000, 79000, 80000, 78001], 128, 8)])
+def test_decode_kv4_gate_from_x_over_long_caches(lens, d, G):
+    """Parts of unequal length beside the gate's projection: every key is taken
+    once.  The workspace holds NaN before, so a key that was passed over leaves
+    one in its weight."""
+    B, L, hkv = 4, 80000, 8
+    g, cache, q, _, sl = make(B, L, hkv * G // 2, hkv, d, lens, 670 + G)
+    x, wl = randn((B, 256), g), randn((256, hkv * G // 2), g, 0.05)
+    need = bd.diffattn_v2_decode_kv4_workspace_size(B, hkv * G // 2, hkv, d, L, False, True)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    w, want_w = torch.zeros((B, hkv, L), device="cuda"), torch.zeros((B, hkv, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, x=x, w_lambda=wl, weights_out=w, workspace=ws)
+    want = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=bd.diffattn_v2_gate(x, wl), weights_out=want_w)
+    for b, n in enumerate(lens):
+        assert bool(torch.isfinite(w[b, :, :n]).all()) and torch.count_nonzero(w[b, :, n:]).item() == 0
+        top = float(want[b].float().abs().max())
+        # other cuts: fp32 sums associate otherwise; then one bf16 rounding each
+        assert float((out[b].float() - want[b].float()).abs().max()) <= 2.0 ** -7 * top
+        assert float((w[b] - want_w[b]).abs().max()) <= 1e-5 * float(want_w[b].max())
+
+
 def test_prefix_read_back_feeds_the_forward():
     """A cached prefix read back and attended by diffattn_v2_fwd gives, for the
     last position, the decode's result over the same records."""
