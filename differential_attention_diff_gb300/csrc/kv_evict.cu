@@ -57,6 +57,15 @@ struct Shared {
   int digit, above, in_bin;
 };
 
+// Whether the array that the new lengths go to is read by the heads.
+__host__ __device__ inline bool lengths_read(const EvictArgs& a) {
+  return a.p.seqlens_out == a.p.seqlens || a.p.seqlens_out == a.p.next_position;
+}
+
+// A barrier over the cluster in two halves: all threads arrive, and wait later.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Move n rows of a head from slots src[i] to dst[i], 16 bytes per thread and
 // step, four steps in flight, and the slots' weights and positions with them.
 // Thread x0 of `step`.
@@ -94,14 +103,17 @@ __device__ void move_rows(const EvictArgs& a, int unit, const int* dst, const in
 
 // T threads; kAll: every slice fits in `cached` ranks; kMove: a head is one
 // CTA's, which also moves the rows (from lists that take the ranks' place) and
-// writes the new length, unless other heads still read it there.
+// writes the new length.  Where other heads read that in the same place, the
+// heads of a sequence are a cluster and it is written behind a barrier, if
+// `lengths`, or by a kernel of its own.
 template <int T, bool kAll, bool kMove>
-__global__ void __launch_bounds__(T, kMove ? 1536 / T : 2048 / T) evict_select_kernel(EvictArgs a, int cached) {
+__global__ void __launch_bounds__(T, kMove ? 1536 / T : 2048 / T) evict_select_kernel(EvictArgs a, int cached, bool lengths) {
   constexpr int kThreads = T, kWarps = T / 32;
   extern __shared__ __align__(16) uint32_t ranks[];  // and behind them the masks
   __shared__ Shared<T> sh;
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
+  // with kMove a cluster is the heads of a sequence instead, if `lengths`
+  const int cs = kMove ? 1 : static_cast<int>(cluster.num_blocks()), part = kMove ? 0 : static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / cs, b = unit / a.p.h_kv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t base = static_cast<int64_t>(unit) * a.p.L_max;
   const int L = a.p.seqlens ? a.p.seqlens[b] : a.p.L_max;
@@ -111,7 +123,7 @@ __global__ void __launch_bounds__(T, kMove ? 1536 / T : 2048 / T) evict_select_k
     if (bad) record_status(a.status, DA_ERR_BOUNDS, 0x4B03);
     if (unit % a.p.h_kv == 0) {
       a.new_len[b] = m;
-      if (kMove && a.p.seqlens_out != a.p.seqlens) a.p.seqlens_out[b] = m;
+      if (kMove && !lengths && !lengths_read(a)) a.p.seqlens_out[b] = m;
     }
   }
   const float* w_in = a.p.weights_in + base;
@@ -126,10 +138,17 @@ __global__ void __launch_bounds__(T, kMove ? 1536 / T : 2048 / T) evict_select_k
         if (copy_w) w_out[j] = w_in[j];
         if (copy_p) p_out[j] = p_in ? p_in[j] : j;
       }
+    if (kMove && lengths) {
+      cluster_arrive();
+      cluster_wait();
+      if (tid == 0 && unit % a.p.h_kv == 0) a.p.seqlens_out[b] = m;
+    }
     return;
   }
   const int end = a.p.next_position ? a.p.next_position[b] : L;
   const int recent_from = end >= INT_MIN + a.p.recent ? end - a.p.recent : INT_MIN;
+  // this CTA has read the length (which may be the next position's array too)
+  if (kMove && lengths) cluster_arrive();
   const bool alone = cs == 1;
   auto sync_all = [&]() {
     if (alone)
@@ -364,6 +383,10 @@ __global__ void __launch_bounds__(T, kMove ? 1536 / T : 2048 / T) evict_select_k
   if constexpr (kMove) {
     __syncthreads();
     move_rows(a, unit, dst, src, sh.counts[1], tid, kThreads);
+    if (lengths) {
+      cluster_wait();
+      if (tid == 0 && unit % a.p.h_kv == 0) a.p.seqlens_out[b] = m;
+    }
   } else {
     if (part == 0 && tid == 0) a.n_moves[unit] = slices(1, cs);
     if (!alone) cluster.sync();  // no CTA leaves while another may still read its counts
@@ -387,7 +410,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_lengths_kernel(EvictArgs a
 }
 
 template <int T, bool kAll, bool kMove = false>
-cudaError_t launch_select(const EvictArgs& a, int cs, int cached, size_t smem, cudaStream_t s) {
+cudaError_t launch_select(const EvictArgs& a, int cs, int cached, size_t smem, cudaStream_t s, bool lengths = false) {
   auto* kernel = evict_select_kernel<T, kAll, kMove>;
   static OncePerDevice once;
   const cudaError_t e = once.run(
@@ -400,11 +423,11 @@ cudaError_t launch_select(const EvictArgs& a, int cs, int cached, size_t smem, c
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.x = lengths ? a.p.h_kv : cs;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, cached);
+  return cudaLaunchKernelEx(&cfg, kernel, a, cached, lengths);
 }
 
 }  // namespace
@@ -446,15 +469,18 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
   for (int k = 0; k < a.p.n_rows; ++k) chunks += a.p.row_bytes[k] / 16;
   // Each CTA moves its own rows, which saves a launch and the wait for it,
   // unless there are many rows and many SMs without a head to share them with
-  // (512 heads, 256 of 4352 slots moved: 25.6 us, 29.4 in two launches; 8
-  // heads, 1 of 4097: 9.9 and 11.9; 128 heads, 2048 of 8192: 38.2 and 41.6;
-  // but 96 of them 34.2 and 33.0, 16 heads, 1000 of 3000: 16.8 and 12.4)
+  // (512 heads, 256 of 4352 slots moved: 29.4 us in two launches, 25.6 in one
+  // and one for the lengths, 22.1 in one; 8 heads, 1 of 4097: 11.9 and 9.9; 128
+  // heads, 2048 of 8192: 41.6 and 38.2; but 96 of them 33.0 and 34.2, 16 heads,
+  // 1000 of 3000: 12.4 and 16.8).  Clusters of 1024-thread CTAs, one to an SM,
+  // would leave SMs empty: those lengths get the launch.
   const int64_t idle = units < a.num_sms ? a.num_sms - units : 0;
   const bool own = small || (per <= 8192 && units <= a.num_sms);
   if (cs == 1 && own && a.max_moves * chunks * idle <= int64_t{12288} * a.num_sms) {
-    const cudaError_t e = small ? launch_select<256, true, true>(a, cs, cached, smem, s)
+    const bool in_place = lengths_read(a), lengths = in_place && small && a.p.h_kv <= kMaxCluster;
+    const cudaError_t e = small ? launch_select<256, true, true>(a, cs, cached, smem, s, lengths)
                                 : launch_select<1024, true, true>(a, cs, cached, smem, s);
-    if (e != cudaSuccess || a.p.seqlens_out != a.p.seqlens) return e;
+    if (e != cudaSuccess || !in_place || lengths) return e;
     return launch_ahead(evict_lengths_kernel, dim3((a.p.B + kMoveThreads - 1) / kMoveThreads), dim3(kMoveThreads), 0, s, true, a);
   }
   cudaError_t e = per > kMaxRanks ? launch_select<1024, false>(a, cs, cached, smem, s)

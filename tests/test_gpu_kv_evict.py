@@ -298,6 +298,33 @@ def test_evict_few_heads_with_few_and_many_rows(keep, inplace):
               nxt=[900] * B, widths=((256, BF16), (256, BF16), (512, BF16)), inplace=inplace)
 
 
+@pytest.mark.parametrize("B,hkv,L,keep", [(2, 2, 700, 400), (40, 8, 130, 60), (23, 7, 300, 250), (18, 9, 300, 250),
+                                          (160, 1, 97, 40), (3, 1, 5000, 2500), (70, 2, 3001, 2900)])
+@pytest.mark.parametrize("out", ["lengths", "next", "both", "apart"])
+def test_evict_lengths_that_others_read(B, hkv, L, keep, out):
+    """New lengths written over the array that every head of the sequence reads
+    its length or its newest position from."""
+    lens = [max(1, L - (i * 37) % L) for i in range(B)]
+    w = spread((B, hkv, L), 768)
+    rows = [randn((B, L, hkv, 8), gen(6))]
+    raw = rows[0].cpu().view(torch.uint8).numpy().copy()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    nxt = sl if out == "both" else sl + 5
+    pos = (torch.arange(L, dtype=torch.int32, device="cuda") + (0 if out == "both" else 5)).expand(B, hkv, L).contiguous()
+    so = {"lengths": sl, "both": sl, "next": nxt, "apart": torch.full_like(sl, -9)}[out]
+    w_np, p_np, n_np = w.cpu().numpy().copy(), pos.cpu().numpy().copy(), nxt.tolist()
+    r = bd.diffattn_kv_evict(rows, w, keep, sinks=0, recent=20, seqlens=sl, positions=pos, next_position=nxt,
+                             seqlens_out=so)
+    assert so.tolist() == [min(n, keep) for n in lens]
+    got = rows[0].cpu().view(torch.uint8).numpy()
+    for b in range(B):
+        for h in range(hkv):
+            m, source = kvo.evict(w_np[b, h, :lens[b]], keep, sinks=0, recent=20, positions=p_np[b, h, :lens[b]],
+                                  next_position=n_np[b])
+            assert np.array_equal(r["positions"][b, h, :m].cpu().numpy(), p_np[b, h, source])
+            assert np.array_equal(got[b, :m, h], raw[b, source, h])
+
+
 def test_evict_many_heads():
     B, hkv, L = 40, 8, 130
     lens = [int(x) for x in np.random.default_rng(9).integers(0, L + 1, B)]
