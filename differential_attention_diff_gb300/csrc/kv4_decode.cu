@@ -48,11 +48,12 @@
 // block takes a whole head instead, merges its warps' partials in shared memory
 // and is done in one launch (the rule and both sides: own_heads in kv_api.cu).
 //
-// Measured (64 query heads, 8 KV heads, d 128): 64 x 32768 keys 405 us with the
-// gate from x, the split kernel 6.2 TB/s of records, 0.91 of a copy; 2 x 131072
-// with the keys' weights 91 us; one sequence of 1000 keys 10 us, in one launch.  Up to about
-// 64 x 8192 keys the instructions bound it (610 a chunk and warp, ALU pipe 60 %
-// busy, tensor pipe 26 %, at 5.4 TB/s), above that the memory nearly does.
+// Measured (64 query heads, 8 KV heads, d 128): 64 x 32768 keys 389 us with the
+// gate from x, 6.2 TB/s of records over the whole call, 0.91 of a copy; 2 x
+// 131072 with the keys' weights 86 us; one sequence of 1000 keys 10 us, in one
+// launch.  Up to about 64 x 8192 keys the instructions bound it (580 a chunk and
+// warp, ALU pipe 60 % busy, tensor pipe 27 %, at 5.5 TB/s), above that the
+// memory nearly does.
 #include "common.cuh"
 #include <cuda_fp16.h>
 

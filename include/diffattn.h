@@ -587,8 +587,9 @@ da_status diffattn_v2_decode_weighted(const da_v2_decode_weighted_params* p, voi
  * below m of the outputs are written with what moved there, the others left.
  * Each _out may be the same array as its _in (and may not overlap it
  * otherwise).  next_position: int32 [B], one past the newest token's position
- * (NULL = seqlens; seqlens_out may be that array too).  1 <= keep, 0 <= sinks, 0 <= recent, sinks + recent <=
- * keep; keep may exceed L_max; L_max at most 2^20.
+ * (NULL = seqlens; seqlens_out may be that array too).  1 <= keep, 0 <=
+ * sinks, 0 <= recent, sinks + recent <= keep; keep may exceed L_max; L_max at
+ * most 2^20.
  * A length outside [0, L_max] is recorded as DA_ERR_BOUNDS in the device
  * status word; that sequence is left as it was, with its length copied.
  * workspace: diffattn_kv_evict_workspace_size bytes, 256-byte aligned,
