@@ -284,9 +284,10 @@ decode_merge_kernel(DecodeArgs a) {
 
 template <int D, bool kScores>
 cudaError_t launch_split(const DecodeArgs& a, cudaStream_t s) {
-  // set on every launch: the attribute is per device, and the call is cheap
-  cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemBytes);
+  static OncePerDevice once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(decode_split_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
   if (e != cudaSuccess) return e;
   dim3 g1(a.num_splits, a.h_kv, a.B);
   if constexpr (kScores)
