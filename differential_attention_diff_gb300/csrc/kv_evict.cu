@@ -62,9 +62,10 @@ __host__ __device__ inline bool lengths_read(const EvictArgs& a) {
   return a.p.seqlens_out == a.p.seqlens || a.p.seqlens_out == a.p.next_position;
 }
 
-// A barrier over the cluster in two halves: all threads arrive, and wait later.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A barrier over the cluster in two halves: all threads arrive, and wait later
+// (not as whole warps: the loops before end at different times for each thread).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Move n rows of a head from slots src[i] to dst[i], 16 bytes per thread and
 // step, four steps in flight, and the slots' weights and positions with them.
