@@ -64,20 +64,32 @@ bool device_handles(uint32_t** status, int* num_sms);
 // Launches a kernel that may start before the one launched just before it has
 // ended (programmatic stream serialization): it waits for that one's end itself
 // (cudaGridDependencySynchronize) before it reads what that one writes, or
-// before its own end.
+// before its own end.  With `cluster` blocks to a cluster, along x.
 template <class... P, class... A>
-cudaError_t launch_ahead(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool ahead, A... args) {
+cudaError_t launch_clustered(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool ahead,
+                             unsigned cluster, A... args) {
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = ahead ? 1 : 0;
+  if (ahead) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_ahead(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool ahead, A... args) {
+  return launch_clustered(kernel, grid, block, smem, s, ahead, 1, args...);
 }
 
 // Runs a set-up call (a kernel attribute, say) once on each device: with its
@@ -135,7 +147,7 @@ struct Kv4DecodeArgs {
   float* weights_out;
   uint32_t* status;
   bool after_gate;    // the kernel launched just before is this call's gate
-  bool own;           // a block per head, no partials
+  int own;            // blocks (a cluster) per head, no partials; 0: the work is cut over all heads
   int late_blocks;    // of the grid's end, which have to wait for the gate's SMs
 };
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);

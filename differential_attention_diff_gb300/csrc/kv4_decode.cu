@@ -46,7 +46,7 @@
 // 64 sequences of 2048 keys where this takes 46).  A second kernel merges the
 // parts of each head and applies the gate.  Where the heads are few and short, a
 // block takes a whole head instead, merges its warps' partials in shared memory
-// and is done in one launch (the rule and both sides: own_heads in kv_api.cu).
+// and is done in one launch (the rule and both sides: own_blocks in kv_api.cu).
 //
 // Measured (64 query heads, 8 KV heads, d 128): 64 x 32768 keys 389 us with the
 // gate from x, 6.2 TB/s of records over the whole call, 0.91 of a copy; 2 x
@@ -55,6 +55,7 @@
 // warp, ALU pipe 60 % busy, tensor pipe 27 %, at 5.5 TB/s), above that the
 // memory nearly does.
 #include "common.cuh"
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -63,6 +64,8 @@
 #include "fp32_pair.cuh"
 #include "kernels.h"
 #include "tma.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace da {
 namespace {
@@ -181,10 +184,10 @@ constexpr int kLateChunks = 4;
 // The reference of a head that has seen no key: any score sends p past 2^8.
 constexpr float kNoMax = -3e38f;
 
-// kOwn: a block takes a whole head, shares its chunks out to its warps, merges
-// them and writes the output (and the keys' weights) itself: one launch for
-// short sequences of few heads.
-template <int D, int NT, bool kScores, bool kOwn>
+// kOwn: a block (1), or a cluster of a.own blocks (2), takes a whole head, shares
+// its chunks out to its warps, merges them and writes the output (and the keys'
+// weights) itself: one launch for short sequences of few heads.
+template <int D, int NT, bool kScores, int kOwn>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4DecodeArgs a) {
   using C = Cfg<D, NT>;
   constexpr int kW = C::kWarps, kS = C::kStages, kRec = C::kRec, kWords = C::kWords, kGT = C::kGroupTiles;
@@ -205,18 +208,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
   int take = 0;  // chunks of this warp's part
   if constexpr (kOwn) {
     __syncthreads();  // the barriers
-    at.b = blockIdx.x / a.h_kv;
-    at.g = blockIdx.x % a.h_kv;
+    const int own = kOwn == 1 ? 1 : a.own, unit = blockIdx.x / own, part = blockIdx.x % own;
+    at.b = unit / a.h_kv;
+    at.g = unit % a.h_kv;
     const int n = seq_chunks(a, at.b);
-    if (n == 0) {  // a bad length: recorded, zeros
-      if (tid == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
-      for (int x = tid; x < G / 2 * D; x += C::kThreads)
+    if (n == 0) {  // a bad length: recorded, zeros (and the whole cluster leaves)
+      if (tid == 0 && part == 0) record_status(a.status, DA_ERR_BOUNDS, 0x4B02);
+      for (int x = part * C::kThreads + tid; x < G / 2 * D; x += own * C::kThreads)
         static_cast<__nv_bfloat16*>(a.out)[(static_cast<int64_t>(at.b) * a.h + at.g * (G / 2)) * D + x] = __float2bfloat16_rn(0.f);
       cudaGridDependencySynchronize();
       return;
     }
-    at.chunk = warp * n / kW;
-    take = (warp + 1) * n / kW - at.chunk;
+    const int w = part * kW + warp;
+    at.chunk = w * n / (own * kW);
+    take = (w + 1) * n / (own * kW) - at.chunk;
   } else {
     // ---- this warp's part of the line ----
     // sequences b0 .. b0 + kThreads - 1 into `ends`; returns the sum up to their end
@@ -718,24 +723,66 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         for (int x = 1; x < kW; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         // a sum of 0 is keys that are all -inf: zeros, as in decode.cu; NaN stays
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        factor[w][head] = down * inv;
-        if (w == 0) norm[head] = make_float2(top, inv);
+        factor[w][head] = kOwn == 2 ? down : down * inv;
+        if (w == 0) norm[head] = make_float2(top, kOwn == 2 ? sum : inv);
       }
       cudaGridDependencySynchronize();  // the gate, where it runs beside this kernel
       __syncthreads();
       const int64_t pair0 = static_cast<int64_t>(at.b) * a.h + at.g * (G / 2);
-      for (int x = tid; x < G / 2 * D; x += C::kThreads) {
-        const int p = x / D, f = x % D;
-        float res[2] = {0.f, 0.f};
+      if constexpr (kOwn == 2) {  // this block's sums, then those of the cluster's blocks
+        __shared__ float2 block_norm[8 * NT];
+        cg::cluster_group cluster = cg::this_cluster();
+        float* mine = park + kW * 8 * NT * D;  // [head][D]
+        static_assert((kW + 1) * 8 * NT * D * 4 <= C::kRing, "the blocks' sums lie behind the warps'");
+        for (int x = tid; x < G * D; x += C::kThreads) {
+          const int head = x / D;
+          float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+          for (int w = 0; w < kW; ++w) sum = fmaf(park[(w * 8 * NT + head) * D + x % D], factor[w][head], sum);
+          mine[x] = sum;
+        }
+        if (tid < 8 * NT) block_norm[tid] = norm[tid];
+        cluster.sync();
+        if (tid < 8 * NT) {
+          float top = kNoMax, sum = 0.f;
+          for (int c = 0; c < a.own; ++c) top = fmaxf(top, cluster.map_shared_rank(block_norm, c)[tid].x);
+          for (int c = 0; c < a.own; ++c) {
+            const float2 x = cluster.map_shared_rank(block_norm, c)[tid];
+            sum += x.y * exp2f(x.x - top);
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          norm[tid] = make_float2(top, inv);
+          for (int c = 0; c < a.own; ++c) factor[c][tid] = exp2f(cluster.map_shared_rank(block_norm, c)[tid].x - top) * inv;
+        }
+        __syncthreads();
+        const int part = static_cast<int>(cluster.block_rank());
+        for (int x = part * C::kThreads + tid; x < G / 2 * D; x += a.own * C::kThreads) {
+          const int p = x / D, f = x % D;
+          float res[2] = {0.f, 0.f};
+          for (int c = 0; c < a.own; ++c) {
+            const float* theirs = cluster.map_shared_rank(mine, c);
 #pragma unroll
-          for (int w = 0; w < kW; ++w) res[e] = fmaf(park[(w * 8 * NT + 2 * p + e) * D + f], factor[w][2 * p + e], res[e]);
-        store_pair(a.out, a.gate, pair0 + p, D, f, res[0], res[1]);
+            for (int e = 0; e < 2; ++e) res[e] = fmaf(theirs[(2 * p + e) * D + f], factor[c][2 * p + e], res[e]);
+          }
+          store_pair(a.out, a.gate, pair0 + p, D, f, res[0], res[1]);
+        }
+      } else {
+        for (int x = tid; x < G / 2 * D; x += C::kThreads) {
+          const int p = x / D, f = x % D;
+          float res[2] = {0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < kW; ++w)
+              res[e] = fmaf(park[(w * 8 * NT + 2 * p + e) * D + f], factor[w][2 * p + e], res[e]);
+          store_pair(a.out, a.gate, pair0 + p, D, f, res[0], res[1]);
+        }
       }
       if constexpr (kScores) {  // written by this block, read after its barriers
         const float* t0 = a.scores + unit * a.L_max * G;
-        for (int key = tid; key < at.L; key += C::kThreads) {
+        const int n = (at.L + kChunk - 1) / kChunk, own = kOwn == 1 ? 1 : a.own, part = blockIdx.x % own;
+        const int k0 = part * n / own * kChunk, k1 = min(at.L, (part + 1) * n / own * kChunk);  // this block's keys
+        for (int key = k0 + tid; key < k1; key += C::kThreads) {
           float w = a.weights_in ? a.weights_in[unit * a.L_max + key] : 0.f;
           for (int p = 0; p < G / 2; ++p) {
             const float2 t = reinterpret_cast<const float2*>(t0 + static_cast<int64_t>(key) * G)[p];
@@ -745,6 +792,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
           a.weights_out[unit * a.L_max + key] = w;
         }
       }
+      if constexpr (kOwn == 2) cg::this_cluster().sync();  // no block leaves while another may still read its sums
       break;
     }
     // ---- the head's end: this warp's partial ----
@@ -937,7 +985,7 @@ cudaError_t launch_merge_for(const Kv4DecodeArgs& a, cudaStream_t s) {
   return blocks * kThin > a.grid ? launch_merge<D, kThin / 2, 32, true>(a, s) : launch_merge<D, kThin, 64, true>(a, s);
 }
 
-template <int D, int NT, bool kScores, bool kOwn>
+template <int D, int NT, bool kScores, int kOwn>
 cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
   using C = Cfg<D, NT>;
   static_assert(C::kRing <= 220 * 1024, "the ring and the static arrays fit an SM");
@@ -948,27 +996,27 @@ cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t s) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
   });
   if (e != cudaSuccess) return e;
-  return launch_ahead(kernel, dim3(kOwn ? a.B * a.h_kv : a.grid), dim3(C::kThreads), C::kRing, s, a.after_gate, a);
+  return launch_clustered(kernel, dim3(kOwn ? a.B * a.h_kv * a.own : a.grid), dim3(C::kThreads), C::kRing, s, a.after_gate,
+                          kOwn ? a.own : 1, a);
 }
 
-template <int D, int NT, bool kOwn>
+template <int D, int NT, int kOwn>
 cudaError_t launch_scored(const Kv4DecodeArgs& a, cudaStream_t s) {
   return a.scores ? launch_split<D, NT, true, kOwn>(a, s) : launch_split<D, NT, false, kOwn>(a, s);
+}
+
+template <int kOwn>
+cudaError_t launch_shaped(const Kv4DecodeArgs& a, cudaStream_t s) {
+  const bool two = 2 * a.h / a.h_kv > 8;
+  if (a.d == 128) return two ? launch_scored<128, 2, kOwn>(a, s) : launch_scored<128, 1, kOwn>(a, s);
+  return two ? launch_scored<64, 2, kOwn>(a, s) : launch_scored<64, 1, kOwn>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
-  const bool two = 2 * a.h / a.h_kv > 8;
-  if (a.own) {
-    if (a.d == 128) return two ? launch_scored<128, 2, true>(a, s) : launch_scored<128, 1, true>(a, s);
-    return two ? launch_scored<64, 2, true>(a, s) : launch_scored<64, 1, true>(a, s);
-  }
-  cudaError_t e;
-  if (a.d == 128)
-    e = two ? launch_scored<128, 2, false>(a, s) : launch_scored<128, 1, false>(a, s);
-  else
-    e = two ? launch_scored<64, 2, false>(a, s) : launch_scored<64, 1, false>(a, s);
+  if (a.own) return a.own == 1 ? launch_shaped<1>(a, s) : launch_shaped<2>(a, s);
+  cudaError_t e = launch_shaped<0>(a, s);
   if (e != cudaSuccess) return e;
   e = a.d == 128 ? launch_merge_for<128>(a, s) : launch_merge_for<64>(a, s);
   if (e != cudaSuccess || a.weights_out == nullptr) return e;

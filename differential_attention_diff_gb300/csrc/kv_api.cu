@@ -47,18 +47,25 @@ int decode_grid(int B, int h_kv, int L_max, int sms) {
   return static_cast<int>(chunks * h_kv * B < most ? chunks * h_kv * B : most);
 }
 
-// Whether a block takes a whole head and writes its output itself: heads that
-// all find an SM at once, and sequences short enough that 16 warps soon have
-// them, the shorter the fewer heads there are (the other path spreads few heads
-// over all SMs, for two or three launches instead of one).  Replayed, without
-// weights, own block and line: 8 heads of 512 keys 8.5 and 9.7 us, of 1024 10.1
-// and 10.2, of 2048 13.9 and 10.4; 64 of 2048 13.9 and 14.8, of 4096 21.3 and
-// 18.4; 128 of 2048 14.2 and 20.5.  With weights the first is a launch better
-// still (8 of 1024: 11.8 and 12.5 us; called eagerly 14.3 and 17.5).  Lengths
-// below L_max favour the line, which cuts them evenly: hence no more than 2048.
-bool own_heads(int B, int h_kv, int L_max, int sms) {
+// Blocks (a cluster) that take a whole head and write its output themselves,
+// 0 for the line of chunks that is cut over all warps: heads that all find SMs
+// at once, and sequences short enough that each warp has two chunks at most,
+// one where the SMs allow it (clusters of 8 find room on half of the SMs: 16
+// heads of 8000 keys took 21.7 us so, 14.5 on the line).  One launch instead
+// of two, three with weights, and room for the scores only.  Replayed and
+// called eagerly, own blocks and line: 8 heads of 1000 keys 9.7 / 11.7 and 10.1
+// / 14.3 us, of 2000 11.0 / 12.7 and 10.2 / 17.2, of 8000 13.5 / 16.5 and 13.7 /
+// 16.6; 32 of 4000 12.9 / 14.9 and 14.5 / 17.3; 128 of 2000 14.2 and 20.5
+// (replayed); with weights 8 of 2000 12.1 / 14.7 and 11.5 / 20.1, 32 of 4000
+// 14.6 / 16.6 and 17.1 / 20.4.  64 heads of 4096 are better off on the line
+// (21.3 and 18.4).
+int own_blocks(int B, int h_kv, int L_max, int sms) {
   const int64_t heads = static_cast<int64_t>(B) * h_kv;
-  return heads <= sms && (L_max <= 1024 || (L_max <= 2048 && heads >= 64));
+  if (heads <= sms && (L_max <= 1024 || (L_max <= 2048 && heads >= 64))) return 1;
+  for (int keys = 512; keys <= 1024; keys *= 2)
+    for (int n = 2; n <= 8; n *= 2)
+      if (heads * n <= (n == 8 ? sms / 2 : sms) && L_max <= keys * n) return n;
+  return 0;
 }
 
 // Blocks that take whole heads need room for the scores and the gate only; the
@@ -68,7 +75,7 @@ struct DecodeSpace {
 };
 DecodeSpace decode_space(int B, int h, int h_kv, int d, int L_max, int gate_given, int weights, int sms) {
   const int64_t heads = static_cast<int64_t>(B) * h_kv;
-  const bool own = own_heads(B, h_kv, L_max, sms);
+  const bool own = own_blocks(B, h_kv, L_max, sms) != 0;
   const int64_t chunks = (static_cast<int64_t>(L_max) + da::kKv4ChunkKeys - 1) / da::kKv4ChunkKeys * heads;
   const int64_t warps = static_cast<int64_t>(decode_grid(B, h_kv, L_max, sms)) * da::kKv4MaxWarps;
   const size_t rows = own ? 0 : static_cast<size_t>((chunks < warps ? chunks : warps) + heads) * (2 * h / h_kv);
@@ -209,7 +216,7 @@ da_status diffattn_v2_decode_kv4(const da_v2_decode_kv4_params* p, void* stream)
                             p->weights_out ? reinterpret_cast<float2*>(ws + w.norm) : nullptr,
                             p->weights_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr,
                             p->weights_in, p->weights_out, status, p->gate == nullptr,
-                            own_heads(p->B, p->h_kv, p->L_max, sms), late};
+                            own_blocks(p->B, p->h_kv, p->L_max, sms), late};
   return cuda_status(da::launch_kv4_decode(a, s));
 }
 

@@ -599,8 +599,9 @@ def test_decode_kv4_swept_shapes(seed):
 
 # A cache that can hold more keys than the short path takes sends the same
 # short sequences through the line of chunks and the merge after it; one that
-# cannot gives every head a block.  LINE is past the longest short cache.
-LINE = 2080
+# cannot gives every head a block or a cluster of them.  LINE is past the
+# longest short cache.
+LINE = 8200
 
 
 @pytest.mark.parametrize("layout", ["head", "token", "padded"])
@@ -619,6 +620,45 @@ def test_decode_kv4_short_sequences_in_a_long_cache(d, G, layout):
     out2 = bd.diffattn_v2_decode_kv4(q, short, seqlens=sl, gate=gate, weights_in=w_in[..., :201].contiguous(),
                                      weights_out=w2)
     check_decode(q, kf, vf, rk, rv, lens, f64(gate), out2, w2, w_in, torch.full_like(w, -3.0)[..., :201])
+
+
+@pytest.mark.parametrize("layout", ["head", "padded"])
+@pytest.mark.parametrize("d,G", [(64, 2), (64, 16), (128, 8), (128, 10)])
+@pytest.mark.parametrize("B,hkv,L,lens", [(1, 1, 8192, [8191]), (3, 1, 8000, [1, 4100, 31]), (2, 8, 2048, [2048, 1025]),
+                                          (4, 8, 4096, [33, 4096, 1, 500]), (5, 8, 1100, [1100, 512, 64, 1099, 2]),
+                                          (12, 4, 2048, [2048, 7] * 6), (2, 2, 1025, [1025, 32])])
+def test_decode_kv4_clusters(B, hkv, L, lens, d, G, layout):
+    """A cluster of two, four or eight blocks per head: full heads, heads with
+    fewer chunks than warps or than blocks; a repeated call gives the same bits."""
+    g, cache, q, gate, sl = make(B, L, hkv * G // 2, hkv, d, lens, 680 + G + L, layout)
+    w_in = torch.rand((B, hkv, L), generator=g, device="cuda")
+    w = torch.full_like(w_in, -3.0)
+    before = w.clone()
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_in=w_in, weights_out=w)
+    assert torch.equal(out, bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate))
+    w2 = w_in.clone()
+    assert torch.equal(out, bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_in=w2, weights_out=w2))
+    for b, n in enumerate(lens):
+        assert torch.equal(w2[b, :, :n], w[b, :, :n]) and torch.equal(w2[b, :, n:], w_in[b, :, n:])
+    kf, vf, rk, rv = ranges(clean(cache, lens))
+    check_decode(q, kf, vf, rk, rv, lens, f64(gate), out, w, w_in, before)
+
+
+def test_decode_kv4_clusters_bad_lengths_and_nan():
+    L = 2000
+    g, cache, q, gate, _ = make(4, L, 4, 2, 128, [100, 100, 100, L], 690)
+    sl = torch.tensor([0, L + 1, -5, L], dtype=torch.int32, device="cuda")
+    w = torch.full((4, 2, L), 2.0, device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_out=w)
+    assert bd.diffattn_get_device_status() == bd.DA_ERR_BOUNDS
+    assert torch.count_nonzero(out[:3]).item() == 0 and torch.count_nonzero(out[3]).item() > 0
+    assert float(w[:3].min()) == float(w[:3].max()) == 2.0 and float(w[3].max()) < 2.0
+    bad = torch.full((1, 1, 2, 128), 0.5, dtype=BF16, device="cuda")
+    bad[:, :, 0] = float("nan")
+    bd.diffattn_kv4_append(bad, bad, cache[3:], start=torch.tensor([L - 1], dtype=torch.int32, device="cuda"))
+    out = bd.diffattn_v2_decode_kv4(q[3:], cache[3:], seqlens=sl[3:], gate=gate[3:], weights_out=w[3:])
+    assert bool(torch.isnan(out[0, :2]).all()) and bool(torch.isfinite(out[0, 2:]).all())
+    assert bool(torch.isnan(w[3, 0]).all()) and bool(torch.isfinite(w[3, 1]).all())
 
 
 def test_decode_kv4_long_cache_bad_lengths_nan_and_in_place():
@@ -647,7 +687,7 @@ def test_decode_kv4_long_cache_bad_lengths_nan_and_in_place():
 
 
 @pytest.mark.parametrize("case", ["rising", "mixed_v", "sharp"])
-@pytest.mark.parametrize("L", [700, LINE + 120])
+@pytest.mark.parametrize("L", [700, 2200, LINE + 120])
 def test_decode_kv4_magnitudes_on_either_path(case, L):
     """References that must move within a warp's part and between parts, d = 64
     and two head tiles."""
@@ -685,7 +725,7 @@ def test_decode_kv4_where_the_paths_meet(more, L):
     check_decode(q[some], kf, vf, rk, rv, n, f64(gate[some]), out[some], w[some], None, torch.zeros_like(w[some]))
 
 
-@pytest.mark.parametrize("L", [700, LINE])
+@pytest.mark.parametrize("L", [700, 2000, LINE])
 def test_decode_kv4_gate_from_x_captured_on_either_path(L):
     g, cache, q, _, sl = make(2, L, 4, 2, 128, [300, 555], 660)
     x, wl = randn((2, 256), g), randn((256, 4), g, 0.05)

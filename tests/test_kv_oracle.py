@@ -144,13 +144,13 @@ def test_decode_kv4_argument_checks(lib):
                 dict(L_max=(1 << 30) + 1)):
         assert f(_with(p, **bad), None) == bd.DA_ERR_UNSUPPORTED, bad
     size = lib.diffattn_v2_decode_kv4_workspace_size
-    p.L_max = 4096
-    need = size(2, 32, 8, 128, 4096, 1, 0)
+    p.L_max = 16384
+    need = size(2, 32, 8, 128, 16384, 1, 0)
     assert f(_with(p), None) == bd.DA_ERR_WORKSPACE
     assert f(_with(p, workspace=FAKE, workspace_bytes=need - 1), None) == bd.DA_ERR_WORKSPACE
     assert f(_with(p, workspace=FAKE + 128, workspace_bytes=need), None) == bd.DA_ERR_WORKSPACE
     # gathering needs room for a score per query head and key
-    assert size(2, 32, 8, 128, 4096, 1, 1) - need >= 2 * 64 * 4096 * 4
+    assert size(2, 32, 8, 128, 16384, 1, 1) - need >= 2 * 64 * 16384 * 4
     assert f(_with(p, weights_out=FAKE, workspace=FAKE, workspace_bytes=need), None) == bd.DA_ERR_WORKSPACE
     # few short heads need room for the scores and the gate only
     assert size(2, 32, 8, 128, 1024, 1, 0) == 0
