@@ -50,21 +50,21 @@ int decode_grid(int B, int h_kv, int L_max, int sms) {
 // Blocks (a cluster) that take a whole head and write its output themselves,
 // 0 for the line of chunks that is cut over all warps: heads that all find SMs
 // at once, and sequences short enough that each warp has two chunks at most,
-// one where the SMs allow it (clusters of 8 find room on half of the SMs: 16
-// heads of 8000 keys took 21.7 us so, 14.5 on the line).  One launch instead
-// of two, three with weights, and room for the scores only.  Replayed and
-// called eagerly, own blocks and line: 8 heads of 1000 keys 9.7 / 11.7 and 10.1
-// / 14.3 us, of 2000 11.0 / 12.7 and 10.2 / 17.2, of 8000 13.5 / 16.5 and 13.7 /
-// 16.6; 32 of 4000 12.9 / 14.9 and 14.5 / 17.3; 128 of 2000 14.2 and 20.5
-// (replayed); with weights 8 of 2000 12.1 / 14.7 and 11.5 / 20.1, 32 of 4000
-// 14.6 / 16.6 and 17.1 / 20.4.  64 heads of 4096 are better off on the line
-// (21.3 and 18.4).
+// one where the SMs allow it.  Not all SMs of a GPU are in groups of 4 or 8 that
+// a cluster fits (36 clusters of 4 ran at once, 11.4 us for 2000 keys, and 37 in
+// two turns, 20.9; 16 of 8 took 21.7 us for 8000 keys, 14.5 on the line), hence
+// the shares below.  One launch instead of two, three with weights, and room for
+// the scores only.  Replayed / called eagerly, own blocks and line: 8 heads of
+// 1000 keys 9.7 / 11.7 and 10.1 / 14.3 us, of 2000 11.0 / 12.7 and 10.2 / 17.2,
+// of 8000 13.5 / 16.5 and 13.7 / 16.6; 32 of 4000 12.9 / 14.9 and 14.5 / 17.3;
+// with weights 8 of 2000 12.1 / 14.7 and 11.5 / 20.1, 32 of 4000 14.6 / 16.6 and
+// 17.1 / 20.4.  Replayed, 128 of 2000 14.2 and 20.5; 64 of 4096 21.3 and 18.4.
 int own_blocks(int B, int h_kv, int L_max, int sms) {
   const int64_t heads = static_cast<int64_t>(B) * h_kv;
   if (heads <= sms && (L_max <= 1024 || (L_max <= 2048 && heads >= 64))) return 1;
   for (int keys = 512; keys <= 1024; keys *= 2)
     for (int n = 2; n <= 8; n *= 2)
-      if (heads * n <= (n == 8 ? sms / 2 : sms) && L_max <= keys * n) return n;
+      if (heads * n <= (n == 8 ? sms / 2 : n == 4 ? sms * 7 / 8 : sms) && L_max <= keys * n) return n;
   return 0;
 }
 

@@ -644,6 +644,18 @@ def test_decode_kv4_clusters(B, hkv, L, lens, d, G, layout):
     check_decode(q, kf, vf, rk, rv, lens, f64(gate), out, w, w_in, before)
 
 
+@pytest.mark.parametrize("B,L", [(33, 2048), (34, 2048), (38, 2048), (39, 1025), (76, 1025), (77, 2048), (9, 8192),
+                                 (10, 8192), (33, 4096)])
+def test_decode_kv4_as_many_clusters_as_fit(B, L):
+    lens = [1 + (131 * b) % L for b in range(B)]
+    lens[-1] = L
+    g, cache, q, gate, sl = make(B, L, 2, 1, 64, lens, 695)
+    w = torch.zeros((B, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, seqlens=sl, gate=gate, weights_out=w)
+    kf, vf, rk, rv = ranges(clean(cache, lens))
+    check_decode(q, kf, vf, rk, rv, lens, f64(gate), out, w, None, torch.zeros_like(w))
+
+
 def test_decode_kv4_clusters_bad_lengths_and_nan():
     L = 2000
     g, cache, q, gate, _ = make(4, L, 4, 2, 128, [100, 100, 100, L], 690)
