@@ -29,11 +29,13 @@
 // accumulator and chunk; at d 128 two accumulators share one (64 x 32768:
 // 398 -> 388.5 us; at d 64 it measured slower, 78.6 -> 83.5 at 64 x 8192).
 //
-// P is fp16 (11 bits, against 8 of a bf16 P).  Its range is kept by a power
-// of two per head, vs, beside the running maximum m of the scores: both are
+// P is fp16 (11 bits, against 8 of a bf16 P).  Its range is kept by a factor
+// per head and half row, vs, beside the running maximum m of the scores: they are
 // references that only move when a value would pass 2^8 (p) or 2^14 (p s vs),
 // or is NaN, by a warp vote, so the common path has no reductions.  vs follows p s and
-// not s, so a large value row of a key with no weight costs no precision.
+// not s, so a large value row of a key with no weight costs no precision, and
+// each half has its own, so neither does a half beside a larger one (a factor
+// for both lost a half's codes behind one 2^30 larger).
 // Sums of p, of p m and the score corrections are fp32.
 //
 // Schedule: the batch's work is one line of 32-key chunks in (sequence, KV
@@ -429,7 +431,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       }
     }
     float o[NT][C::kTiles][4];
-    float mx[NT][2], vs[NT][2], l[NT][2], mn[NT][2][2];  // reference max, value factor, sums of p and p m (per group)
+    // reference max, value factors (per group), sums of p and of p m (per group)
+    float mx[NT][2], vs[NT][2][2], l[NT][2], mn[NT][2][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mx[t][e] = kNoMax;
-        vs[t][e] = 0x1p100f;
+        vs[t][0][e] = vs[t][1][e] = 0x1p100f;
         l[t][e] = mn[t][0][e] = mn[t][1][e] = 0.f;
       }
     }
@@ -545,10 +548,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
                 const float y = fast_exp2(fmaf(s[u][t][2 * r + 1], fac[t][1], -mx[t][1]));
                 p[u][t][2 * r] = x;
                 p[u][t][2 * r + 1] = y;
-                const float xv = x * vs[t][0], yv = y * vs[t][1];
-                const float s0 = lo_bf16(par[u][r].z), s1 = hi_bf16(par[u][r].z);
-                pf[u][t][0][r] = pack_f16x2(xv * s0, yv * s0);
-                pf[u][t][1][r] = pack_f16x2(xv * s1, yv * s1);
+                const F2 xy(x, y);
+#pragma unroll
+                for (int g2 = 0; g2 < 2; ++g2) {
+                  const float sg = g2 ? hi_bf16(par[u][r].z) : lo_bf16(par[u][r].z);
+                  const uint2 v = mul2(xy, F2(vs[t][g2][0], vs[t][g2][1])).bits();
+                  pf[u][t][g2][r] = pack_f16x2(__uint_as_float(v.x) * sg, __uint_as_float(v.y) * sg);
+                }
               }
             lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
             lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
@@ -573,30 +579,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
               const float old = mx[t][e], now = fmaxf(old, top);
-              float big = 0.f;
+              float big[2] = {0.f, 0.f};
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                  big = fmaxf(big, fast_exp2(fmaf(s[u][t][2 * r + e], fac[t][e], -now)) *
-                                       fmaxf(lo_bf16(par[u][r].z), hi_bf16(par[u][r].z)));
+                for (int r = 0; r < 2; ++r) {
+                  const float w = fast_exp2(fmaf(s[u][t][2 * r + e], fac[t][e], -now));
+                  big[0] = fmaxf(big[0], w * lo_bf16(par[u][r].z));
+                  big[1] = fmaxf(big[1], w * hi_bf16(par[u][r].z));
+                }
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+              for (int x = 4; x < 32; x <<= 1) {
+                big[0] = fmaxf(big[0], __shfl_xor_sync(0xffffffffu, big[0], x));
+                big[1] = fmaxf(big[1], __shfl_xor_sync(0xffffffffu, big[1], x));
+              }
               const float down = exp2f(old - now);
               l[t][e] *= down;
               mn[t][0][e] *= down;
               mn[t][1][e] *= down;
               mx[t][e] = now;
               // O stands for O / vs: a higher maximum raises vs and leaves O alone
-              const float keep = vs[t][e] * exp2f(now - old);
-              float v = fminf(keep, 0x1p100f);
-              if (big > 0.f) v = fminf(v, exponent_scale(big, 8));
-              const float by = keep == v ? 1.f : v / keep;
-              vs[t][e] = v;
 #pragma unroll
-              for (int i = 0; i < C::kTiles; ++i) {
-                o[t][i][e] *= by;
-                o[t][i][2 + e] *= by;
+              for (int g2 = 0; g2 < 2; ++g2) {
+                const float keep = vs[t][g2][e] * exp2f(now - old);
+                float v = fminf(keep, 0x1p100f);
+                if (big[g2] > 0.f) v = fminf(v, exponent_scale(big[g2], 8));
+                const float by = keep == v ? 1.f : v / keep;
+                vs[t][g2][e] = v;
+#pragma unroll
+                for (int i = g2 * kGT; i < (g2 + 1) * kGT; ++i) {
+                  o[t][i][e] *= by;
+                  o[t][i][2 + e] *= by;
+                }
               }
             }
           weigh();
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             m1 += __shfl_xor_sync(0xffffffffu, m1, x);
           }
           const int head = t * 8 + 2 * tq + e;
-          const float f = 1.f / vs[t][e];
+          const float f[2] = {1.f / vs[t][0][e], 1.f / vs[t][1][e]};
           if (gr == 0) wml[warp][head] = make_float2(mx[t][e], lt);
 #pragma unroll
           for (int g2 = 0; g2 < 2; ++g2)
@@ -706,8 +720,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
               const float* y = o[t][g2 * kGT + hw * 2 + 1];
               const float m = g2 ? m1 : m0;
               *reinterpret_cast<float4*>(park + (warp * 8 * NT + head) * D + g2 * (D / 2) + gr * (D / 16) + hw * 4) =
-                  make_float4(fmaf(x[e] * 0x1p24f, f, m), fmaf(y[e] * 0x1p20f, f, m),
-                              fmaf(x[2 + e] * 0x1p24f, f, m), fmaf(y[2 + e] * 0x1p20f, f, m));
+                  make_float4(fmaf(x[e] * 0x1p24f, f[g2], m), fmaf(y[e] * 0x1p20f, f[g2], m),
+                              fmaf(x[2 + e] * 0x1p24f, f[g2], m), fmaf(y[2 + e] * 0x1p20f, f[g2], m));
             }
         }
       __syncthreads();
@@ -814,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         }
         const int head = t * 8 + 2 * tq + e;
         if (head >= G) continue;
-        const float f = 1.f / vs[t][e];
+        const float f[2] = {1.f / vs[t][0][e], 1.f / vs[t][1][e]};
         float* po = a.part_o + (row + head) * D;
         if (gr == 0) *reinterpret_cast<float2*>(a.part_ml + (row + head) * 2) = make_float2(mx[t][e], lt);
         // four neighbouring features: rows gr and gr + 8 of two tiles.  2^24
@@ -827,8 +841,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             const float* y = o[t][g2 * kGT + hw * 2 + 1];
             const float m = g2 ? m1 : m0;
             *reinterpret_cast<float4*>(po + g2 * (D / 2) + gr * (D / 16) + hw * 4) =
-                make_float4(fmaf(x[e] * 0x1p24f, f, m), fmaf(y[e] * 0x1p20f, f, m),
-                            fmaf(x[2 + e] * 0x1p24f, f, m), fmaf(y[2 + e] * 0x1p20f, f, m));
+                make_float4(fmaf(x[e] * 0x1p24f, f[g2], m), fmaf(y[e] * 0x1p20f, f[g2], m),
+                            fmaf(x[2 + e] * 0x1p24f, f[g2], m), fmaf(y[2 + e] * 0x1p20f, f[g2], m));
           }
       }
     if (at.left == 0) break;
