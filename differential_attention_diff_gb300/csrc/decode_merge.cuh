@@ -9,6 +9,7 @@
 namespace da {
 
 // Feature `col` of query head j of sequence b, over the splits in their order.
+// A sum of 0 is an empty sequence or keys that are all -inf: zeros; NaN stays.
 __device__ __forceinline__ float merged_head(const float* part_o, const float* part_ml, int num_splits, int B, int H2,
                                              int d, int b, int j, int col) {
   float mt = -INFINITY;
@@ -22,7 +23,7 @@ __device__ __forceinline__ float merged_head(const float* part_o, const float* p
     lt += part_ml[pidx * 2 + 1] * f;
     ot += part_o[pidx * d + col] * f;
   }
-  return lt > 0.f ? ot / lt : 0.f;
+  return lt == 0.f ? 0.f : ot / lt;
 }
 
 // Even - gate * odd, the two products rounded apart so that equal heads cancel.
