@@ -5,6 +5,7 @@ and eviction by gathered weight.  Nothing is shared with the GPU path.
 A row of d features has two groups of d/2; a group stores its minimum m, its
 scale s = bf16((max - min) / 15) and codes n = rint((x - m) / s) in 0..15; it
 stands for s n + m.  s = 0: codes 0.  s not finite: s = m = NaN, codes 0.
+max - min and x - m are rounded to fp32, as the definition has it.
 """
 
 from __future__ import annotations
@@ -37,10 +38,10 @@ def kv4_quantise(x):
     g = x.reshape(*x.shape[:-1], 2, x.shape[-1] // 2)
     with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         m = g.min(-1)
-        span = g.max(-1) - m
-        s = round_bf16(np.where(span > np.finfo(np.float32).max, np.inf, span) / 15)
+        s = round_bf16((g.max(-1) - m).astype(np.float32).astype(np.float64) / 15)
         bad = ~np.isfinite(s)
-        n = np.minimum(np.rint((g - m[..., None]) / s[..., None]), 15)
+        above = (g - m[..., None]).astype(np.float32).astype(np.float64)
+        n = np.minimum(np.rint(above / s[..., None]), 15)
         n = np.where((s == 0)[..., None] | bad[..., None], 0, n)
     s, m = np.where(bad, np.nan, s), np.where(bad, np.nan, m)
     return n.reshape(x.shape).astype(np.uint8), s, m

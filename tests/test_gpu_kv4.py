@@ -88,6 +88,25 @@ def test_append_special_values_bit_for_bit():
             assert np.all(np.abs(got - exp)[ok] <= 2.0 ** -8 * (1 + 2.0 ** -12) * np.abs(exp[ok]) + 2.0 ** -134)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_ties_of_rounded_differences(d):
+    """Differences x - m that are ties of two codes in fp32 and not in more
+    bits, in either group, at scales from 2^-115 to 2^120; a minimum of
+    -2^-18 s beside one of -2^-30 s shows in the differences."""
+    x = torch.zeros((1, 16, 1, d), dtype=torch.float64)
+    for i, e in enumerate((0, 40, 100, 120, -40, -99, -101, -115)):
+        for j, low in enumerate((2.0 ** -30, 2.0 ** -18)):
+            for half in (0, 1):
+                part = x[0, 2 * i + j, 0, half * d // 2:]
+                part[:15] = torch.arange(15) + 0.5
+                part[15], part[16 + half] = 15.0, -low
+            x[0, 2 * i + j] *= 2.0 ** e
+    x = x.to(BF16).cuda()
+    cache = new_cache(1, 16, 1, d)
+    bd.diffattn_kv4_append(x, x.flip(1), cache)
+    assert np.array_equal(cache.cpu().numpy(), kvo.kv4_pack(f64(x), f64(x.flip(1))))
+
+
 @pytest.mark.parametrize("layout", ["head", "token", "padded"])
 @pytest.mark.parametrize("B,N,hkv,d,L,ragged", [(1, 1, 1, 64, 1, False), (3, 1, 8, 128, 40, False),
                                                  (2, 37, 3, 128, 64, True), (4, 130, 2, 64, 131, True),

@@ -51,6 +51,18 @@ def test_quantise_special_groups():
     assert v[1, 40] == 15 * kvo.round_bf16(2 / 15)  # the top code, with s rounded to bf16
 
 
+def test_differences_are_rounded_to_fp32():
+    """Over a minimum of -2^-30 and with s = 1, x - m of 0.5, 1.5, .. 14.5 is that
+    number in fp32: a tie, which goes to the even code."""
+    x = np.zeros((2, 64))
+    x[:, :15] = np.arange(15) + 0.5
+    x[:, 15], x[:, 16] = 15.0, [-2.0 ** -30, -2.0 ** -18]  # 15 + 2^-18 is an fp32 number, the scale's bf16 still 1
+    n, s, _ = kvo.kv4_quantise(x)
+    assert np.all(s[:, 0] == 1)
+    assert n[0, :15].tolist() == [0, 2, 2, 4, 4, 6, 6, 8, 8, 10, 10, 12, 12, 14, 14]
+    assert n[1, :15].tolist() == list(range(1, 16))  # 2^-18 shows in all of these differences
+
+
 def test_key_weights_of_equal_maps_vanish_and_of_plain_attention_sum_to_one():
     """gate 1 with equal queries gathers nothing; gate 0 is plain attention,
     whose weights sum to one per pair."""
