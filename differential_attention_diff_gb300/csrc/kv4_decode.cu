@@ -153,13 +153,10 @@ template <class T>
 __device__ __forceinline__ T lds(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
 }
-__device__ __forceinline__ float exponent_scale(float x, int target) {
-  // the power of two that brings x > 0 into [2^target, 2^(target+1)), limited to 2^-126 .. 2^100
-  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 0xffu) - 127;
-  int k = target - e;
-  k = k > 100 ? 100 : k < -126 ? -126 : k;
-  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-}
+// 2^k for k in -126 .. 127, the exponent of a normal number, and 1 / x of a power of two in 2^-126 .. 2^126.
+__device__ __forceinline__ float power(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xffu) - 127; }
+__device__ __forceinline__ float inverse_power(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // 16-byte copies that a barrier counts: each lane's arrival comes when its copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -183,8 +180,12 @@ struct Cursor {
 // 0, 3, 4, 5, 6: 122.4, 117.6, 117.2, 117.0, 119.8 us).
 constexpr int kLateChunks = 4;
 
-// The reference of a head that has seen no key: any score sends p past 2^8.
-constexpr float kNoMax = -3e38f;
+// The reference of a head that has seen no key: any score above it sends p past 2^8.
+constexpr float kNoMax = -0x1.fffffep127f;
+
+// What the products of codes are multiplied by where a query is so large that
+// its score factor is divided by it.
+constexpr float kLift = 0x1p32f;
 
 // kOwn: a block (1), or a cluster of a.own blocks (2), takes a whole head, shares
 // its chunks out to its warps, merges them and writes the output (and the keys'
@@ -376,6 +377,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
     const int64_t unit = static_cast<int64_t>(at.b) * a.h_kv + at.g;
     uint32_t qf[NT][4 * kWords][2];  // B fragments: [2 groups x kWords x 2 MMAs]
     float qs0[NT][2], qs1[NT][2], fac[NT][2];  // of heads 2 tq, 2 tq + 1: group sums of q, score factor
+    unsigned lifted[NT];  // bit 4 j: head j's products take kLift
+    bool careful = false;  // whole chunks go the way of partial ones (see take_chunk)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int head = t * 8 + gr;
@@ -400,8 +403,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // largest query feature in [2^14, 2^15): exact in fp16 down to 2^-29 of it
-      const float up = mx > 0.f ? exponent_scale(mx, 14) : 1.f;
+      // largest query feature in [2^14, 2^15): exact in fp16 down to 2^-31 of it,
+      // 2^-27 where a feature meets upper codes and is divided by 16
+      const float up = mx > 0.f ? power(min(max(14 - exponent(mx), -126), 126)) : 1.f;
+      const bool lift = up < 0x1p-64f;  // 2^24 / up would pass the largest number at 2^-104
+      lifted[t] = __ballot_sync(0xffffffffu, lift);
+      careful |= lifted[t] != 0;
       float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         sum[p] += __shfl_xor_sync(0xffffffffu, sum[p], 2);
         sum[p] *= 0x1p-24f;
       }
-      const float f = 0x1p24f / up * a.scale_log2;
+      const float f = (lift ? 0x1p24f / kLift : 0x1p24f) * inverse_power(up) * a.scale_log2;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         qs0[t][e] = __shfl_sync(0xffffffffu, sum[0], (2 * tq + e) * 4);
@@ -459,9 +466,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       slot = slot == kS - 1 ? 0 : slot + 1;
       const int valid = at.L - at.chunk * kChunk;  // keys of this chunk
 
+      // kPartial: a chunk that is not whole, or a head that asks for care.  In
+      // the others scores are held as their fac-th part, and p = 2^(s fac - m) is
+      // one multiply-add.  Its unrounded product is off from the rounded one by up
+      // to half an ulp, which passes the range of p from scores of about 2^30 on:
+      // there, and wherever a reference moves, s fac is rounded first.
       auto take_chunk = [&](auto partial) {
         constexpr bool kPartial = decltype(partial)::value;
         // ---- scores (of fac log2 units), two 16-key tiles ----
+        float* const score_row = kScores ? a.scores + (unit * a.L_max + at.chunk * kChunk + row_key) * G + 2 * tq : nullptr;
         uint4 par[2][2];  // [tile][row half]: K s0 s1 | K m0 m1 | V s0 s1 | V m0 m1
         float s[2][NT][4];
 #pragma unroll
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
               x = fmaf(lo_bf16(r.y), qs0[t][c], x);
               x = fmaf(lo_bf16(r.x), acc[0][t][e], x);
               x = fmaf(hi_bf16(r.x), acc[1][t][e], x);
-              s[u][t][e] = x;
+              s[u][t][e] = kPartial ? x * fac[t][c] * ((lifted[t] >> (8 * tq + 4 * c)) & 1 ? kLift : 1.f) : x;
             }
           if constexpr (kPartial) {
 #pragma unroll
@@ -527,8 +540,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
               for (int r = 0; r < 2; ++r) {
                 const int k = u * 16 + row_key + r;
                 if ((!kPartial || k < valid) && t * 8 + 2 * tq < G)
-                  *reinterpret_cast<float2*>(a.scores + (unit * a.L_max + at.chunk * kChunk + k) * G + t * 8 + 2 * tq) =
-                      make_float2(s[u][t][2 * r] * fac[t][0], s[u][t][2 * r + 1] * fac[t][1]);
+                  *reinterpret_cast<float2*>(score_row + (u * 16 + r) * G + t * 8) =
+                      kPartial ? make_float2(s[u][t][2 * r], s[u][t][2 * r + 1])
+                               : make_float2(s[u][t][2 * r] * fac[t][0], s[u][t][2 * r + 1] * fac[t][1]);
               }
           }
         }
@@ -536,7 +550,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         // ---- softmax against the references ----
         float p[2][NT][4], lsum[NT][2];
         uint32_t pf[2][NT][2][2];  // [tile][head tile][group][row half], fp16 pairs of heads
-        auto weigh = [&]() {
+        auto weigh = [&](auto rounded) {  // rounded: s is s fac already
+          constexpr bool kRounded = decltype(rounded)::value, kTwo = kRounded || !kScores;
           bool over = false;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -544,17 +559,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const float x = fast_exp2(fmaf(s[u][t][2 * r], fac[t][0], -mx[t][0]));
-                const float y = fast_exp2(fmaf(s[u][t][2 * r + 1], fac[t][1], -mx[t][1]));
+                const float sx = s[u][t][2 * r], sy = s[u][t][2 * r + 1];
+                const float x = fast_exp2(kRounded ? sx - mx[t][0] : fmaf(sx, fac[t][0], -mx[t][0]));
+                const float y = fast_exp2(kRounded ? sy - mx[t][1] : fmaf(sy, fac[t][1], -mx[t][1]));
                 p[u][t][2 * r] = x;
                 p[u][t][2 * r + 1] = y;
+                const float s0 = lo_bf16(par[u][r].z), s1 = hi_bf16(par[u][r].z);
                 const F2 xy(x, y);
-#pragma unroll
-                for (int g2 = 0; g2 < 2; ++g2) {
-                  const float sg = g2 ? hi_bf16(par[u][r].z) : lo_bf16(par[u][r].z);
-                  const uint2 v = mul2(xy, F2(vs[t][g2][0], vs[t][g2][1])).bits();
-                  pf[u][t][g2][r] = pack_f16x2(__uint_as_float(v.x) * sg, __uint_as_float(v.y) * sg);
-                }
+                const uint2 v0 = mul2(xy, F2(vs[t][0][0], vs[t][0][1])).bits();
+                const uint2 v1 = kTwo ? mul2(xy, F2(vs[t][1][0], vs[t][1][1])).bits() : v0;
+                pf[u][t][0][r] = pack_f16x2(__uint_as_float(v0.x) * s0, __uint_as_float(v0.y) * s0);
+                pf[u][t][1][r] = pack_f16x2(__uint_as_float(v1.x) * s1, __uint_as_float(v1.y) * s1);
               }
             lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
             lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
@@ -568,44 +583,69 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
           }
           return over;
         };
-        if (__any_sync(0xffffffffu, weigh())) {
-          // new references from this chunk's keys: the score maximum, then the
-          // largest p s under it
+        if (__any_sync(0xffffffffu, weigh(partial))) {
+          if constexpr (!kPartial) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][t][e] *= fac[t][e & 1];
+          }
+          // new references from this chunk's keys: a whole number at the score
+          // maximum, then powers of two from each half's largest p s under it, so
+          // that what was summed so far is scaled exactly
+          careful = false;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            careful |= lifted[t] != 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e])) * fac[t][e];
+              float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              const float old = mx[t][e], now = fmaxf(old, top);
+              const float old = mx[t][e], now = fmaxf(old, ceilf(top));
               float big[2] = {0.f, 0.f};
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  const float w = fast_exp2(fmaf(s[u][t][2 * r + e], fac[t][e], -now));
+                  const float w = fast_exp2(s[u][t][2 * r + e] - now);
                   big[0] = fmaxf(big[0], w * lo_bf16(par[u][r].z));
                   big[1] = fmaxf(big[1], w * hi_bf16(par[u][r].z));
                 }
+              // the upper halves of both, which order as whole numbers do (without a zero's sign)
+              uint32_t both = __byte_perm(__float_as_uint(big[0]), __float_as_uint(big[1]), 0x7632) & 0x7fff7fffu;
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) {
-                big[0] = fmaxf(big[0], __shfl_xor_sync(0xffffffffu, big[0], x));
-                big[1] = fmaxf(big[1], __shfl_xor_sync(0xffffffffu, big[1], x));
-              }
-              const float down = exp2f(old - now);
-              l[t][e] *= down;
-              mn[t][0][e] *= down;
-              mn[t][1][e] *= down;
-              mx[t][e] = now;
+              for (int x = 4; x < 32; x <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, x));
               // O stands for O / vs: a higher maximum raises vs and leaves O alone
+              const int rise = static_cast<int>(fminf(now - old, 512.f));
+              int had[2], k[2];
 #pragma unroll
               for (int g2 = 0; g2 < 2; ++g2) {
-                const float keep = vs[t][g2][e] * exp2f(now - old);
-                float v = fminf(keep, 0x1p100f);
-                if (big[g2] > 0.f) v = fminf(v, exponent_scale(big[g2], 8));
-                const float by = keep == v ? 1.f : v / keep;
-                vs[t][g2][e] = v;
+                const uint32_t top16 = g2 ? both >> 16 : both & 0xffffu;
+                had[g2] = exponent(vs[t][g2][e]) + rise;
+                k[g2] = min(had[g2], 100);
+                if (top16) k[g2] = max(min(k[g2], 8 + 127 - static_cast<int>(top16 >> 7)), -126);
+              }
+              careful |= fabsf(now) > 0x1p22f;
+              // Where scores are stored, halves of about the same size take one
+              // factor, and others ask for care: fewer multiplications in the
+              // common path (64 x 8192: 169.5 -> 163.7 us, 169.2 for halves 2^10
+              // apart; without scores two factors are as fast, 112.5 and 112.5).
+              if constexpr (kScores) {
+                const int low = min(k[0], k[1]);
+                if (max(k[0], k[1]) <= low + 4) k[0] = k[1] = low;
+                careful |= k[0] != k[1];
+              }
+              const float down = rise > 126 ? 0.f : power(-rise);
+              mx[t][e] = now;
+              l[t][e] *= down;
+#pragma unroll
+              for (int g2 = 0; g2 < 2; ++g2) {
+                mn[t][g2][e] *= down;
+                const float by = k[g2] < had[g2] - 126 ? 0.f : power(k[g2] - had[g2]);
+                vs[t][g2][e] = power(k[g2]);
 #pragma unroll
                 for (int i = g2 * kGT; i < (g2 + 1) * kGT; ++i) {
                   o[t][i][e] *= by;
@@ -613,7 +653,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
                 }
               }
             }
-          weigh();
+          }
+          careful = __any_sync(0xffffffffu, careful);
+          weigh(std::true_type{});
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -684,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
           }
         }
       };
-      if (valid >= kChunk)
+      if (valid >= kChunk && !careful)
         take_chunk(std::false_type{});
       else
         take_chunk(std::true_type{});
@@ -710,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
             m1 += __shfl_xor_sync(0xffffffffu, m1, x);
           }
           const int head = t * 8 + 2 * tq + e;
-          const float f[2] = {1.f / vs[t][0][e], 1.f / vs[t][1][e]};
+          const float f[2] = {inverse_power(vs[t][0][e]), inverse_power(vs[t][1][e])};
           if (gr == 0) wml[warp][head] = make_float2(mx[t][e], lt);
 #pragma unroll
           for (int g2 = 0; g2 < 2; ++g2)
@@ -828,7 +870,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
         }
         const int head = t * 8 + 2 * tq + e;
         if (head >= G) continue;
-        const float f[2] = {1.f / vs[t][0][e], 1.f / vs[t][1][e]};
+        const float f[2] = {inverse_power(vs[t][0][e]), inverse_power(vs[t][1][e])};
         float* po = a.part_o + (row + head) * D;
         if (gr == 0) *reinterpret_cast<float2*>(a.part_ml + (row + head) * 2) = make_float2(mx[t][e], lt);
         // four neighbouring features: rows gr and gr + 8 of two tiles.  2^24

@@ -521,7 +521,7 @@ da_status diffattn_kv4_read(const da_kv4_read_params* p, void* cuda_stream);
  * the supported shapes and the treatment of bad sequence lengths are those of
  * diffattn_v2_decode.  The
  * products A_j s_j of a half row are rounded to 11 bits, those far below the
- * largest of them at its 2^-33: the output is off by 2^-11 of the largest 15 s
+ * largest of them at its 2^-29: the output is off by 2^-11 of the largest 15 s
  * that the half's records hold at most, beside its own rounding.
  * Gathered weights (optional, weights_out NULL = not computed): what each key
  * contributes to the differential maps of its KV head, summed over the head's

@@ -8,8 +8,8 @@ scale and minimum):
   a factor of the weights;
 - p s goes to the value product in fp16, 2^-11 relative at most, on codes up to
   15: 2^-11 of the half's largest 15 s.  What falls below fp16's normal numbers
-  is off by 2^-25 a key, where the half's largest p s is 2^8 or more: less than
-  L 2^-33 of 15 s;
+  is off by 2^-25 a key, where the half's largest p s is 2^4 or more: less than
+  L 2^-29 of 15 s;
 - fp32 steps on s n and m: 64 u (15 s + |m|);
 - the output's bf16 rounding, 2^-8 relative."""
 
@@ -100,3 +100,73 @@ def test_value_halves_of_different_size(L, d, G, ratio, large, keys):
     cache = cache_of(k, v)
     out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate)
     check_halves(q, cache, gate, out)
+
+
+# ------------------------------------------------------ the scores' range ---
+@pytest.mark.parametrize("heads", ["all", "even"])
+@pytest.mark.parametrize("q_size,k_size", [(2.0 ** 119, 2.0 ** -118), (2.0 ** 126, 2.0 ** -126), (2.0 ** -119, 2.0 ** 118),
+                                           (2.0 ** -126, 2.0 ** 122)])
+@pytest.mark.parametrize("d,G", [(64, 12), (128, 4)])
+@pytest.mark.parametrize("L", (33,) + PATHS)
+def test_scores_of_huge_and_tiny_queries(L, d, G, q_size, k_size, heads):
+    """Queries and keys at the ends of bf16's range whose products are ordinary
+    numbers, beside heads (the odd ones, of "even") of ordinary queries."""
+    g = torch.Generator(device="cuda").manual_seed(930 + L + d)
+    k, v = (torch.rand((2, L, 1, d), generator=g, device="cuda") * 2 - 1 for _ in range(2))
+    q = torch.rand((2, G, d), generator=g, device="cuda") * 2 - 1
+    if heads == "all":
+        q *= q_size
+    else:
+        q[:, 0::2] *= q_size
+        if k_size > 1:
+            q[:, 1::2] /= k_size
+    q, gate = q.to(BF16), torch.rand((2, G // 2), generator=g, device="cuda")
+    cache = cache_of(k * k_size, v)
+    w = torch.zeros((2, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate, weights_out=w)
+    check_halves(q, cache, gate, out)
+    assert bool(torch.isfinite(w).all())
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("L", (1, 33) + PATHS)
+def test_equal_scores_at_the_end_of_the_range(L, sign):
+    """Equal keys whose scores are 0.95 of the least or largest number: every
+    weight is 1 / L, as of any equal scores."""
+    d, h = 64, 2
+    g = torch.Generator(device="cuda").manual_seed(950 + L)
+    k, v = torch.full((1, L, 1, d), sign * 2.0 ** 61, device="cuda"), randn((1, L, 1, d), g)
+    q = torch.full((1, 2 * h, d), 2.0 ** 60, device="cuda").to(BF16)  # q . k = 2^127
+    scale = 0.95 * 2 / 1.4426950408889634  # 0.95 * 2^128 in log2 units
+    gate = torch.rand((1, h), generator=g, device="cuda")
+    cache = cache_of(k, v)
+    w = torch.zeros((1, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate, weights_out=w, softmax_scale=scale)
+    check_halves(torch.zeros_like(q), cache, gate, out)  # queries of the same weights
+    want = float((1 - gate.double()).sum()) / L
+    # products rounded before they are subtracted: 64 u of (1 + gate) / L per pair
+    assert float((w.double() - want).abs().max()) <= 64 * U * float((1 + gate.double()).sum()) / L
+
+
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 15, 2.0 ** 30])
+@pytest.mark.parametrize("d,G", [(64, 12), (128, 4)])
+@pytest.mark.parametrize("L", (33,) + PATHS)
+def test_scores_far_apart(L, d, G, size):
+    """Scores of 2^20 to 2^67: the largest key, ahead of the others by more
+    than the scores' error, has all the weight, wherever it stands."""
+    g = torch.Generator(device="cuda").manual_seed(960 + L + d)
+    signs = torch.where(torch.rand((2, 1, 1, d), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    height = 0.5 + 0.4 * torch.rand((2, L, 1, 1), generator=g, device="cuda")
+    best = [L // 3, L - 1]
+    height[0, best[0]] = height[1, best[1]] = 1.0
+    k, v = size * height * signs, randn((2, L, 1, d), g)
+    q = (size * signs[:, 0].expand(2, G, d)).to(BF16)
+    gate = torch.rand((2, G // 2), generator=g, device="cuda")
+    cache = cache_of(k, v)
+    w = torch.zeros((2, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate, weights_out=w)
+    check_halves(q, cache, gate, out, e=0.0)
+    want = torch.zeros_like(w, dtype=torch.float64)
+    for b in range(2):
+        want[b, 0, best[b]] = (1 - gate[b].double()).sum()
+    assert float((w.double() - want).abs().max()) <= 64 * U * 2 * G
