@@ -31,7 +31,7 @@
 //
 // P is fp16 (11 bits, against 8 of a bf16 P).  Its range is kept by a factor
 // per head and half row, vs, beside the running maximum m of the scores: they are
-// references that only move when a value would pass 2^8 (p) or 2^14 (p s vs),
+// references that only move when a value would pass 2^-2 (p) or 2^14 (p s vs),
 // or is NaN, by a warp vote, so the common path has no reductions.  vs follows p s and
 // not s, so a large value row of a key with no weight costs no precision, and
 // each half has its own, so neither does a half beside a larger one (a factor
@@ -180,8 +180,15 @@ struct Cursor {
 // 0, 3, 4, 5, 6: 122.4, 117.6, 117.2, 117.0, 119.8 us).
 constexpr int kLateChunks = 4;
 
-// The reference of a head that has seen no key: any score above it sends p past 2^8.
+// The reference of a head that has seen no key: any score above it sends p past kTop.
 constexpr float kNoMax = -0x1.fffffep127f;
+
+// A moved reference lies kHeadroom above the largest score, and p may grow by
+// 2^8 before it moves again: p stays below 1, so that sums of p m and of p s n
+// of values at the end of their range stay within it (as in a softmax about
+// its true maximum, and with a reference at the maximum they did not).
+constexpr int kHeadroom = 10;
+constexpr float kTop = 0x1p-2f;
 
 // What the products of codes are multiplied by where a query is so large that
 // its score factor is divided by it.
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mx[t][e] = kNoMax;
-        vs[t][0][e] = vs[t][1][e] = 0x1p100f;
+        vs[t][0][e] = vs[t][1][e] = 0x1p126f;
         l[t][e] = mn[t][0][e] = mn[t][1][e] = 0.f;
       }
     }
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
               }
             lsum[t][0] = (p[0][t][0] + p[0][t][2]) + (p[1][t][0] + p[1][t][2]);
             lsum[t][1] = (p[0][t][1] + p[0][t][3]) + (p[1][t][1] + p[1][t][3]);
-            over |= !(lsum[t][0] <= 256.f && lsum[t][1] <= 256.f);
+            over |= !(lsum[t][0] <= kTop && lsum[t][1] <= kTop);
             // none of them is negative: their sum bounds each (and its adds do
             // not take the pipe that the code masks fill)
             __half2 top = *reinterpret_cast<__half2*>(&pf[0][t][0][0]);
@@ -592,8 +599,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[u][t][e] *= fac[t][e & 1];
           }
-          // new references from this chunk's keys: a whole number at the score
-          // maximum, then powers of two from each half's largest p s under it, so
+          // new references from this chunk's keys: a whole number kHeadroom above
+          // the score maximum, then powers of two from each half's largest p s under it, so
           // that what was summed so far is scaled exactly
           careful = false;
 #pragma unroll
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
               float top = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              const float old = mx[t][e], now = fmaxf(old, ceilf(top));
+              const float old = mx[t][e], now = fmaxf(old, ceilf(top) + kHeadroom);
               float big[2] = {0.f, 0.f};
 #pragma unroll
               for (int u = 0; u < 2; ++u)
@@ -625,7 +632,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
               for (int g2 = 0; g2 < 2; ++g2) {
                 const uint32_t top16 = g2 ? both >> 16 : both & 0xffffu;
                 had[g2] = exponent(vs[t][g2][e]) + rise;
-                k[g2] = min(had[g2], 100);
+                k[g2] = min(had[g2], 126);
                 if (top16) k[g2] = max(min(k[g2], 8 + 127 - static_cast<int>(top16 >> 7)), -126);
               }
               careful |= fabsf(now) > 0x1p22f;

@@ -170,3 +170,46 @@ def test_scores_far_apart(L, d, G, size):
     for b in range(2):
         want[b, 0, best[b]] = (1 - gate[b].double()).sum()
     assert float((w.double() - want).abs().max()) <= 64 * U * 2 * G
+
+
+# ------------------------------------------------------ the values' range ---
+@pytest.mark.parametrize("values", ["equal", "spread"])
+@pytest.mark.parametrize("d,G", [(64, 2), (64, 12), (128, 4)])
+@pytest.mark.parametrize("B,L", [(24, 1024), (24, 4096), (48, 8320)])
+def test_values_near_the_end_of_the_range(B, L, d, G, values):
+    """Two chunks or more go to a warp, and every second chunk of 32 keys holds
+    one of a score above those before it (by 2^7, or by 2^5 where the values'
+    scales bound it too), the others far less; the values are so large that a
+    weight of 2^7 or 2^5 of one or two of them passes the largest number, while
+    the sum of weights of at most 1 does not."""
+    g = torch.Generator(device="cuda").manual_seed(970 + L + d)
+    chunks = L // 32
+    k = torch.zeros((B, L, 1, d), device="cuda")
+    k[..., 0] = -40.0
+    for c in range(chunks):
+        k[:, 32 * c + (5 * c) % 32, 0, 0] = (7 if values == "equal" else 5) / 1.4426950408889634 if c % 2 else 0.0
+    v = 0.6 + 0.4 * torch.rand((B, L, 1, d if values == "spread" else 1), generator=g, device="cuda")
+    v = (3.2e38 / (chunks // 2) * v).expand(B, L, 1, d)
+    q = torch.zeros((B, G, d), device="cuda")
+    q[..., 0] = d ** 0.5
+    q[:, 1::2, 0] *= 0.875
+    q, gate = q.to(BF16), torch.rand((B, G // 2), generator=g, device="cuda")
+    cache = cache_of(k, v)
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate)
+    check_halves(q, cache, gate, out)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -105, 2.0 ** -115, 2.0 ** -122])
+@pytest.mark.parametrize("keys", ["flat", "rising"])
+@pytest.mark.parametrize("L", PATHS)
+def test_tiny_values(L, keys, size):
+    """Values whose scales are far below 1, down to bf16's least normal numbers."""
+    d, G = 128, 4
+    g = torch.Generator(device="cuda").manual_seed(990 + L)
+    k, v = randn((2, L, 1, d), g), randn((2, L, 1, d), g, size)
+    if keys == "rising":
+        k *= torch.linspace(0.05, 4.0, L, device="cuda")[None, :, None, None]
+    q, gate = randn((2, G, d), g).to(BF16), torch.rand((2, G // 2), generator=g, device="cuda")
+    cache = cache_of(k, v)
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate)
+    check_halves(q, cache, gate, out)
