@@ -15,12 +15,12 @@ namespace da {
 constexpr int kKv4ChunkKeys = 32;
 constexpr int kKv4MaxGrid = 256;   // CTAs at most (one per SM)
 constexpr int kKv4MaxWarps = 16;   // of each
-constexpr int kKv4MaxParts = kKv4MaxGrid * kKv4MaxWarps;  // and so partials of one head
 
 // Parts of a line of `total` chunks for `warps` warps: a chunk each while half
-// of the warps are enough for that (one sequence of 1000 keys takes 10.0 us so,
-// 11.0 us with two each), else at least two (8 of them: 14.0 and 12.5 us: below
-// it the parts cost more to merge than they save).
+// of the warps are enough for that (one sequence of 1000 keys and 8 KV heads, in
+// a cache too long for blocks of its own, takes 10.8 us so, 11.7 us with two
+// each), else at least two (8 of them: 12.9 and 11.6 us: below it the parts cost
+// more to merge than they save).
 __host__ __device__ inline int64_t kv4_parts(int64_t total, int64_t warps) {
   const int64_t most = total <= warps / 2 ? total : (total + 1) / 2;
   return most < warps ? most : warps;
