@@ -5,8 +5,11 @@
 // whole sequence was read.  The decode's split kernel therefore stores its
 // scaled scores t (log2 units, fp32); this kernel takes A = exp2(t - max) / sum
 // from them.  Scores in fewer bits would not do: an error e in t is an error
-// of 0.7 e in the weight.  4 G bytes of scores per key are fewer than its K
-// row's 2 d of bf16, so keeping them beats a second pass over K.
+// of 0.7 e in the weight.  Stored and read, that is 8 G bytes per key.  A second
+// pass over K instead would read its row's 2 d of bf16 and compute the scores
+// again, which is fewer bytes nowhere (G up to 16; equal at d 64); over a 4-bit
+// cache it would read d/2 + 8, which is fewer from G = 10 on at d 128 and from
+// G = 6 at d 64 (not built).
 //
 // Over a bf16 cache the same launch merges the splits, in its first blocks: in
 // two launches that cost 22 us for 8 ragged sequences up to 4096 keys, in one

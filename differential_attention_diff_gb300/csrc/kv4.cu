@@ -7,9 +7,10 @@
 // 16 features each: two 16-byte accesses on the bf16 side and 8 bytes of codes
 // on the other, so a warp touches whole contiguous rows.  Neither is bound by
 // memory alone: with 656 bytes moved per record, an SM has about 28 cycles for
-// one, so what counts is the instructions per feature.  Measured, 16 x 4096 x 8
-// rows of d 128: append 72.4 us, 4.75 TB/s (issue slots 67 % busy, the ALU pipe
-// 57 %); read 55.4 us, 6.2 TB/s, 0.91 of a copy.
+// one, so the instructions per feature count too.  Measured, 16 x 4096 x 8
+// rows of d 128: append 72.4 us, 4.75 TB/s, with no unit full (issue slots 67 %
+// busy, the ALU pipe 57 %, 45 % of the warps at 62 registers); read 55.4 us, 6.2
+// TB/s, 0.91 of a copy.
 #include "common.cuh"
 #include "fp32_pair.cuh"
 #include "kernels.h"
@@ -64,7 +65,8 @@ struct RowWalk {
   }
 };
 
-// x / 15, rounded once; NaN and infinity stay something that is not finite.
+// x / 15, rounded once, as a quotient corrected by its residual (Markstein's
+// correction); NaN and infinity stay something that is not finite.
 __device__ __forceinline__ float fifteenth(float x) {
   if (x > 0.f && x < 0x1p-90f) return __fdiv_rn(x, 15.f);  // the residual may not be a normal number
   const float q = x * (1.f / 15.f);
@@ -77,7 +79,7 @@ __device__ __forceinline__ float reciprocal(float x) {  // within an ulp
 }
 
 // Eight codes of bf16 pairs w: rint(t / s) for t = x - lo in [0, 15.03 s],
-// exactly, without a division.  q = t inv is off by an ulp or two; its residual
+// exactly, without a division (Markstein's correction again).  q = t inv is off by an ulp or two; its residual
 // t - q s fits fp32, and q + residual inv is rounded once, from a value within
 // 2^-21 ulp of t / s: the rounded quotient, but where t / s lies that close to
 // the middle between two numbers.  The rounding to a code could still go wrong

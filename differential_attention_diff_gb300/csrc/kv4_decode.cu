@@ -50,12 +50,12 @@
 // block takes a whole head instead, merges its warps' partials in shared memory
 // and is done in one launch (the rule and both sides: own_blocks in kv_api.cu).
 //
-// Measured (64 query heads, 8 KV heads, d 128): 64 x 32768 keys 389 us with the
-// gate from x, 6.2 TB/s of records over the whole call, 0.91 of a copy; 2 x
-// 131072 with the keys' weights 86 us; one sequence of 1000 keys 10 us, in one
+// Measured (64 query heads, 8 KV heads, d 128): 64 x 32768 keys 384 us with the
+// gate from x, 6.3 TB/s of records over the whole call, 0.93 of a copy; 2 x
+// 131072 with the keys' weights 88 us; one sequence of 1000 keys 10 us, in one
 // launch.  Up to about 64 x 8192 keys the instructions bound it (580 a chunk and
-// warp, ALU pipe 60 % busy, tensor pipe 27 %, at 5.5 TB/s), above that the
-// memory nearly does.
+// warp, issue slots 64 % busy, ALU pipe 61 %, tensor pipe 28 %, at 5.6 TB/s; at
+// d 64 455, 71 %, 58 % and 20 %, at 4.5 TB/s), above that the memory nearly does.
 #include "common.cuh"
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) kv4_split_kernel(Kv4D
       auto take_chunk = [&](auto partial) {
         constexpr bool kPartial = decltype(partial)::value;
         // ---- scores (of fac log2 units), two 16-key tiles ----
-        float* const score_row = kScores ? a.scores + (unit * a.L_max + at.chunk * kChunk + row_key) * G + 2 * tq : nullptr;
+        [[maybe_unused]] float* const score_row = kScores ? a.scores + (unit * a.L_max + at.chunk * kChunk + row_key) * G + 2 * tq : nullptr;
         uint4 par[2][2];  // [tile][row half]: K s0 s1 | K m0 m1 | V s0 s1 | V m0 m1
         float s[2][NT][4];
 #pragma unroll

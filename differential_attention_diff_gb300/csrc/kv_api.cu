@@ -49,16 +49,23 @@ int decode_grid(int B, int h_kv, int L_max, int sms) {
 
 // Blocks (a cluster) that take a whole head and write its output themselves,
 // 0 for the line of chunks that is cut over all warps: heads that all find SMs
-// at once, and sequences short enough that each warp has two chunks at most,
-// one where the SMs allow it.  Not all SMs of a GPU are in groups of 4 or 8 that
+// at once, and sequences of at most 1024 keys a block (512 where the SMs allow
+// it, 2048 from 64 heads on).  With up to 8 query heads per KV head a block has
+// 16 warps, so that is two chunks a warp (one, four); with more it has 8, and
+// twice the chunks.  Not all SMs of a GPU are in groups of 4 or 8 that
 // a cluster fits (36 clusters of 4 ran at once, 11.4 us for 2000 keys, and 37 in
 // two turns, 20.9; 16 of 8 took 21.7 us for 8000 keys, 14.5 on the line), hence
 // the shares below.  One launch instead of two, three with weights, and room for
-// the scores only.  Replayed / called eagerly, own blocks and line: 8 heads of
-// 1000 keys 9.7 / 11.7 and 10.1 / 14.3 us, of 2000 11.0 / 12.7 and 10.2 / 17.2,
-// of 8000 13.5 / 16.5 and 13.7 / 16.6; 32 of 4000 12.9 / 14.9 and 14.5 / 17.3;
-// with weights 8 of 2000 12.1 / 14.7 and 11.5 / 20.1, 32 of 4000 14.6 / 16.6 and
-// 17.1 / 20.4.  Replayed, 128 of 2000 14.2 and 20.5; 64 of 4096 21.3 and 18.4.
+// the scores only.  Called eagerly, own blocks and line: 8 heads of 1000 keys
+// 11.7 and 14.3 us, of 2000 12.7 and 17.2, of 8000 16.5 and 16.6; 32 of 4000
+// 14.9 and 17.3; with weights 8 of 2000 14.7 and 20.1, 32 of 4000 16.6 and 20.4.
+// Replayed, where a launch less counts for less: 8 of 1000 9.6 and 9.0, of 2000
+// 10.2 and 9.4, of 8000 12.8 and 13.0; 32 of 4000 12.3 and 15.6; 128 of 2000
+// 13.5 and 18.8; 64 of 4096 21.3 and 18.4; with weights 8 of 2000 11.5 and 11.1,
+// 32 of 4000 14.2 and 18.6.  These are for 8 query heads per KV head.  For 16 (d 128, replayed) the limits
+// fit less well: 8 heads of 1000 keys 11.9 and 10.6 us, with weights 15.3 and
+// 12.6; 64 of 2000 17.8 and 17.2, with weights 24.1 and 20.6; but 32 of 2000
+// 11.9 and 16.0 (14.1 and 19.3), 128 of 2000 18.1 and 25.0 (24.4 and 29.9).
 int own_blocks(int B, int h_kv, int L_max, int sms) {
   const int64_t heads = static_cast<int64_t>(B) * h_kv;
   if (heads <= sms && (L_max <= 1024 || (L_max <= 2048 && heads >= 64))) return 1;

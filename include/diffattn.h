@@ -533,8 +533,9 @@ da_status diffattn_kv4_read(const da_kv4_read_params* p, void* cuda_stream);
  * array as weights_out (it may not overlap it otherwise).
  * workspace: diffattn_v2_decode_kv4_workspace_size bytes (which may be 0: then
  * it is not looked at), 256-byte aligned, contents on entry irrelevant; calls
- * that run at the same time need workspaces of their own.  Results are bitwise reproducible from call to
- * call.  B, h_kv at most 65535, B * h_kv at most 2^28, L_max at most 2^30. */
+ * that run at the same time need workspaces of their own.  With weights it holds
+ * a score per query head and position, 8 B h L_max bytes whatever the lengths.
+ * Results are bitwise reproducible from call to call.  B, h_kv at most 65535, B * h_kv at most 2^28, L_max at most 2^30. */
 typedef struct {
   int B, h, h_kv, d, L_max, d_model;
   float softmax_scale;   /* <= 0 selects 1/sqrt(d) */
@@ -583,8 +584,10 @@ da_status diffattn_v2_decode_weighted(const da_v2_decode_weighted_params* p, voi
  * row_bytes[i] bytes each (K and V, or K1, K2 and V, or 4-bit records), with
  * strides in BYTES; pointers, strides and row_bytes multiples of 16; no two
  * rows overlap.  Slots at or above m are left as they were.
- * weights_in / weights_out: fp32 [B, h_kv, L_max] contiguous; positions_in /
- * positions_out: int32, likewise (positions_in NULL: slot j holds token
+ * weights_in / weights_out: fp32 [B, h_kv, L_max] contiguous.  The two V2
+ * decodes above gather them, a decode step at a time; no forward gives those of
+ * a prompt's own queries and no V1 call gathers any, so there they are the
+ * caller's to make.  positions_in / positions_out: int32, likewise (positions_in NULL: slot j holds token
  * position j; positions_out NULL: not written, allowed where positions_in is
  * NULL); seqlens / seqlens_out: int32 [B] (seqlens NULL = all L_max).  Slots
  * below m of the outputs are written with what moved there, the others left.
