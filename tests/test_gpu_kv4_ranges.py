@@ -102,6 +102,31 @@ def test_value_halves_of_different_size(L, d, G, ratio, large, keys):
     check_halves(q, cache, gate, out)
 
 
+@pytest.mark.parametrize("ratio", [2.0 ** 3, 2.0 ** 6, 2.0 ** 30])
+@pytest.mark.parametrize("d,G", [(64, 12), (128, 4)])
+@pytest.mark.parametrize("L", PATHS)
+def test_value_halves_of_different_size_beside_weights(L, d, G, ratio):
+    """The same where the keys' weights are gathered, for halves that may share
+    a factor and halves that may not; the weights do not depend on the values."""
+    g = torch.Generator(device="cuda").manual_seed(920 + L + d)
+    k, v = randn((2, L, 1, d), g), randn((2, L, 1, d), g)
+    v[1:, ..., :d // 2] *= ratio
+    v[:1, ..., d // 2:] *= ratio
+    q, gate = randn((2, G, d), g).to(BF16), torch.rand((2, G // 2), generator=g, device="cuda")
+    cache, other = cache_of(k, v), cache_of(k, v.flip(0).contiguous())
+    w, w2 = torch.zeros((2, 1, L), device="cuda"), torch.zeros((2, 1, L), device="cuda")
+    out = bd.diffattn_v2_decode_kv4(q, cache, gate=gate, weights_out=w)
+    check_halves(q, cache, gate, out)
+    check_halves(q, other, gate, bd.diffattn_v2_decode_kv4(q, other, gate=gate, weights_out=w2))
+    rec = cache.cpu().numpy()
+    kf, mag = kvo.kv4_values(rec)[0], parameters(rec)[1][..., 0, :].max()
+    for b in range(2):
+        ref, total = kvo.key_weights(f64(q[b]), kf[b], f64(gate[b]))
+        e = 64 * U * (2 + d ** -0.5 * np.abs(f64(q[b])).sum(-1).max() * mag)
+        for got in (w, w2):
+            assert np.all(np.abs(f64(got[b]) - ref) <= e * total + 4 * U * ref + 1e-37)
+
+
 # ------------------------------------------------------ the scores' range ---
 @pytest.mark.parametrize("heads", ["all", "even"])
 @pytest.mark.parametrize("q_size,k_size", [(2.0 ** 119, 2.0 ** -118), (2.0 ** 126, 2.0 ** -126), (2.0 ** -119, 2.0 ** 118),
