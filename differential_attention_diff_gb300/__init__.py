@@ -14,6 +14,11 @@ from .binding import (  # noqa: F401
     diffattn_kv_evict,
     diffattn_kv_evict_workspace_size,
     diffattn_lambda_init,
+    diffattn_paged_append,
+    diffattn_qk_rope_bwd,
+    diffattn_qk_rope_bwd_workspace_size,
+    diffattn_qk_rope_fwd,
+    diffattn_rope_inv_freq,
     diffattn_v1_bwd,
     diffattn_v1_fwd,
     diffattn_v2_decode,
@@ -25,5 +30,7 @@ from .binding import (  # noqa: F401
     diffattn_v2_decode_workspace_size,
     diffattn_v2_fwd,
     diffattn_v2_gate,
+    diffattn_v2_paged_fwd,
+    diffattn_v2_paged_fwd_workspace_size,
     load,
 )

@@ -59,6 +59,13 @@ EXPORTS = (
     "diffattn_v2_decode_weighted_workspace_size",
     "diffattn_kv_evict",
     "diffattn_kv_evict_workspace_size",
+    "diffattn_rope_inv_freq",
+    "diffattn_qk_rope_fwd",
+    "diffattn_qk_rope_bwd",
+    "diffattn_qk_rope_bwd_workspace_size",
+    "diffattn_paged_append",
+    "diffattn_v2_paged_fwd",
+    "diffattn_v2_paged_fwd_workspace_size",
     "diffattn_get_device_status",
     "diffattn_debug_inject_fault",
     "diffattn_get_device_status_detail",
@@ -201,6 +208,43 @@ class da_kv_evict_params(C.Structure):
                 ("workspace_bytes", C.c_size_t)]
 
 
+class da_t3(C.Structure):
+    _fields_ = [("ptr", C.c_void_p), ("st", C.c_int64), ("sh", C.c_int64)]
+
+
+class da_qk_rope_fwd_params(C.Structure):
+    _fields_ = [("B", C.c_int), ("N", C.c_int), ("h_q", C.c_int), ("h_k", C.c_int), ("d", C.c_int),
+                ("dtype", C.c_int), ("rot_dim", C.c_int), ("interleaved", C.c_int), ("inv_freq", C.c_void_p),
+                ("rope_scale", C.c_float), ("norm", C.c_int), ("norm_eps", C.c_float), ("q_weight", C.c_void_p),
+                ("k_weight", C.c_void_p), ("positions", C.c_void_p), ("q", da_t4), ("k", da_t4),
+                ("q_out", da_t4), ("k_out", da_t4)]
+
+
+class da_qk_rope_bwd_params(C.Structure):
+    _fields_ = [("fwd", da_qk_rope_fwd_params), ("dq_out", da_t4), ("dk_out", da_t4), ("dq", da_t4), ("dk", da_t4),
+                ("dq_weight", C.c_void_p), ("dk_weight", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t)]
+
+
+class da_paged_cache(C.Structure):
+    _fields_ = [("B", C.c_int), ("T", C.c_int), ("h_kv", C.c_int), ("d", C.c_int), ("page_size", C.c_int),
+                ("n_pages", C.c_int), ("max_pages", C.c_int), ("k_pages", da_t4), ("v_pages", da_t4),
+                ("block_table", C.c_void_p), ("cu_seqlens", C.c_void_p), ("seqlens", C.c_void_p)]
+
+
+class da_paged_append_params(C.Structure):
+    _fields_ = [("cache", da_paged_cache), ("h_q", C.c_int), ("rot_dim", C.c_int), ("interleaved", C.c_int),
+                ("inv_freq", C.c_void_p), ("rope_scale", C.c_float), ("norm", C.c_int), ("norm_eps", C.c_float),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("positions", C.c_void_p), ("k", da_t3),
+                ("v", da_t3), ("q", da_t3), ("q_out", da_t3)]
+
+
+class da_v2_paged_fwd_params(C.Structure):
+    _fields_ = [("cache", da_paged_cache), ("h", C.c_int), ("d_model", C.c_int), ("max_new", C.c_int),
+                ("softmax_scale", C.c_float), ("q", da_t3), ("gate", C.c_void_p), ("x", C.c_void_p),
+                ("w_lambda", C.c_void_p), ("out", da_t3), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -232,7 +276,11 @@ def load(path: str = LIB_PATH):
                          ("diffattn_kv4_read", da_kv4_read_params),
                          ("diffattn_v2_decode_kv4", da_v2_decode_kv4_params),
                          ("diffattn_v2_decode_weighted", da_v2_decode_weighted_params),
-                         ("diffattn_kv_evict", da_kv_evict_params)):
+                         ("diffattn_kv_evict", da_kv_evict_params),
+                         ("diffattn_qk_rope_fwd", da_qk_rope_fwd_params),
+                         ("diffattn_qk_rope_bwd", da_qk_rope_bwd_params),
+                         ("diffattn_paged_append", da_paged_append_params),
+                         ("diffattn_v2_paged_fwd", da_v2_paged_fwd_params)):
             f = getattr(lib, name)
             f.restype = C.c_int
             f.argtypes = [C.POINTER(st), vp]
@@ -260,10 +308,15 @@ def load(path: str = LIB_PATH):
         lib.diffattn_kv4_record_bytes.argtypes = [C.c_int]
         for name, n in (("diffattn_v2_decode_kv4_workspace_size", 7),
                         ("diffattn_v2_decode_weighted_workspace_size", 7),
-                        ("diffattn_kv_evict_workspace_size", 4)):
+                        ("diffattn_kv_evict_workspace_size", 4),
+                        ("diffattn_qk_rope_bwd_workspace_size", 5),
+                        ("diffattn_v2_paged_fwd_workspace_size", 7)):
             f = getattr(lib, name)
             f.restype = C.c_size_t
             f.argtypes = [C.c_int] * n
+        lib.diffattn_rope_inv_freq.restype = C.c_int
+        lib.diffattn_rope_inv_freq.argtypes = [C.c_int, C.c_double, C.c_int, C.c_double, C.c_int,
+                                               C.POINTER(C.c_float), C.POINTER(C.c_float)]
         lib.diffattn_debug_inject_fault.restype = C.c_int
         lib.diffattn_debug_inject_fault.argtypes = [C.c_int]
         lib.diffattn_get_device_status.restype = C.c_int
@@ -628,6 +681,8 @@ def _packer(t):
 _pack_append, _pack_read = _packer(da_kv4_append_params), _packer(da_kv4_read_params)
 _pack_decode_kv4, _pack_weighted = _packer(da_v2_decode_kv4_params), _packer(da_v2_decode_weighted_params)
 _pack_evict = _packer(da_kv_evict_params)
+_pack_rope_fwd, _pack_rope_bwd = _packer(da_qk_rope_fwd_params), _packer(da_qk_rope_bwd_params)
+_pack_paged_append, _pack_paged_fwd = _packer(da_paged_append_params), _packer(da_v2_paged_fwd_params)
 _packed_calls = {}
 
 
@@ -857,6 +912,191 @@ def diffattn_kv_evict(rows, key_weights, keep, *, sinks=0, recent=0, seqlens=Non
         _array(next_position, (B,), i32, dev, "next_position"), len(rows), *row_bytes, *views,
         *_space(workspace, dev)), raw)
     return dict(key_weights=weights_out, positions=positions_out, seqlens=seqlens_out)
+
+
+# ---- positions, paged cache --------------------------------------------------
+
+DA_ROPE_STRETCH = {None: 0, "linear": 1, "base": 2, "ramp": 3}
+
+
+def diffattn_rope_inv_freq(rot_dim, base=10000.0, *, stretch=None, factor=1.0, trained_len=0, device="cuda"):
+    """(inv_freq, rope_scale): fp32 [rot_dim / 2] frequencies in radians per position on `device`, and the scale
+    of the rotated features, for contexts `factor` times as long as trained (stretch: None, "linear", "base" or
+    "ramp", which needs the trained_len in positions)."""
+    if stretch not in DA_ROPE_STRETCH:
+        raise ValueError(f"stretch: one of {list(DA_ROPE_STRETCH)} expected, got {stretch!r}")
+    f, s = (C.c_float * max(rot_dim // 2, 1))(), C.c_float()
+    _check(load().diffattn_rope_inv_freq(rot_dim, base, DA_ROPE_STRETCH[stretch], factor, trained_len, f, C.byref(s)),
+           "diffattn_rope_inv_freq")
+    return torch.tensor(list(f), dtype=torch.float32).to(device), s.value
+
+
+def _rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev):
+    """The rotation's and the norm's fields, from rot_dim to k_weight."""
+    f32 = torch.float32
+    if rot_dim is None:
+        rot_dim = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    return (rot_dim, interleaved, _array(inv_freq, (rot_dim // 2,), f32, dev, "inv_freq"), rope_scale, norm, norm_eps,
+            _array(q_weight, (d,), f32, dev, "q_weight"), _array(k_weight, (d,), f32, dev, "k_weight"))
+
+
+_NO_T4, _NO_T3 = (0, 0, 0, 0), (0, 0, 0)
+
+
+def _qk_fields(q, k, B, N, d, dtype, dev, names):
+    """The da_t4 fields of a tensor of queries and one of keys, either may be None."""
+    out = ()
+    for t, name in ((q, names[0]), (k, names[1])):
+        out += _NO_T4 if t is None else _rows4(t, (B, N, t.shape[2], d), dtype, dev, name)
+    return out
+
+
+def diffattn_qk_rope_fwd(q, k, inv_freq, *, positions=None, rot_dim=None, interleaved=False, rope_scale=1.0, norm=False,
+                         norm_eps=1e-5, q_weight=None, k_weight=None, q_out=None, k_out=None, stream=None):
+    """Queries [B, N, h_q, d] and keys [B, N, h_k, d] (bf16 or fp32; either may be None) normed per head (norm; fp32
+    [d] weights, None = unit) and their first rot_dim (None = all that inv_freq has) features rotated by their
+    positions (int32 [B, N], None = 0 .. N-1).  Returns (q_out, k_out), which may be q and k themselves."""
+    some = q if q is not None else k
+    dev, raw = _device(some, stream)
+    B, N, _, d = some.shape
+    dtype = some.dtype
+    if q is not None and q_out is None:
+        q_out = _new(torch.empty, q, q.shape, dtype, stream)
+    if k is not None and k_out is None:
+        k_out = _new(torch.empty, k, k.shape, dtype, stream)
+    h_q, h_k = 0 if q is None else q.shape[2], 0 if k is None else k.shape[2]
+    _same_heads(q, q_out, "q_out")
+    _same_heads(k, k_out, "k_out")
+    _call("diffattn_qk_rope_fwd", _pack_rope_fwd(
+        B, N, h_q, h_k, d, _dtype_code(some),
+        *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
+        _array(positions, (B, N), torch.int32, dev, "positions"), *_qk_fields(q, k, B, N, d, dtype, dev, ("q", "k")),
+        *_qk_fields(q_out, k_out, B, N, d, dtype, dev, ("q_out", "k_out"))), raw)
+    return q_out, k_out
+
+
+def _same_heads(t, other, name):
+    if (t is None) != (other is None) or t is not None and t.shape != other.shape:
+        raise ValueError(f"{name}: a tensor of {None if t is None else tuple(t.shape)} expected, got "
+                         f"{None if other is None else tuple(other.shape)}")
+
+
+def diffattn_qk_rope_bwd_workspace_size(B, N, h_q, h_k, d) -> int:
+    return int(load().diffattn_qk_rope_bwd_workspace_size(B, N, h_q, h_k, d))
+
+
+def diffattn_qk_rope_bwd(q, k, dq_out, dk_out, inv_freq, *, positions=None, rot_dim=None, interleaved=False,
+                         rope_scale=1.0, norm=False, norm_eps=1e-5, q_weight=None, k_weight=None, dq=None, dk=None,
+                         dq_weight=None, dk_weight=None, want_weights=None, workspace=None, stream=None):
+    """Gradients of diffattn_qk_rope_fwd given those of its outputs: dict(dq, dk) and, with norm (unless want_weights
+    is False), dq_weight and dk_weight, fp32 [d].  q and k are needed with norm only.  dq and dk may be dq_out and
+    dk_out themselves."""
+    some = dq_out if dq_out is not None else dk_out
+    dev, raw = _device(some, stream)
+    B, N, _, d = some.shape
+    dtype = some.dtype
+    if dq_out is not None and dq is None:
+        dq = _new(torch.empty, some, dq_out.shape, dtype, stream)
+    if dk_out is not None and dk is None:
+        dk = _new(torch.empty, some, dk_out.shape, dtype, stream)
+    _same_heads(dq_out, dq, "dq")
+    _same_heads(dk_out, dk, "dk")
+    if norm:
+        _same_heads(dq_out, q, "q")
+        _same_heads(dk_out, k, "k")
+    else:
+        q = k = None
+    if want_weights is None:
+        want_weights = norm
+    h_q, h_k = 0 if dq_out is None else dq_out.shape[2], 0 if dk_out is None else dk_out.shape[2]
+    if want_weights:
+        if dq_weight is None and h_q:
+            dq_weight = _new(torch.empty, some, (d,), torch.float32, stream)
+        if dk_weight is None and h_k:
+            dk_weight = _new(torch.empty, some, (d,), torch.float32, stream)
+    if workspace is None and (dq_weight is not None or dk_weight is not None):
+        need = _need(dev, "diffattn_qk_rope_bwd_workspace_size", B, N, h_q, h_k, d)
+        workspace = _new(torch.empty, some, (max(need, 1),), torch.uint8, stream)
+    _call("diffattn_qk_rope_bwd", _pack_rope_bwd(
+        B, N, h_q, h_k, d, _dtype_code(some),
+        *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
+        _array(positions, (B, N), torch.int32, dev, "positions"), *_qk_fields(q, k, B, N, d, dtype, dev, ("q", "k")),
+        *_NO_T4, *_NO_T4, *_qk_fields(dq_out, dk_out, B, N, d, dtype, dev, ("dq_out", "dk_out")),
+        *_qk_fields(dq, dk, B, N, d, dtype, dev, ("dq", "dk")), _array(dq_weight, (d,), torch.float32, dev, "dq_weight"),
+        _array(dk_weight, (d,), torch.float32, dev, "dk_weight"), *_space(workspace, dev)), raw)
+    return dict(dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight)
+
+
+def _rows3(t, shape, dtype, dev, name):
+    """The da_t3 fields of a packed tensor of the given shape and type on device dev."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+    st, sh, sx = t.stride()
+    if sx != 1:
+        raise ValueError(f"{name}: a contiguous last dimension expected")
+    return t.data_ptr(), st, sh
+
+
+def _paged_fields(T, k_pages, v_pages, block_table, cu_seqlens, seqlens, dev):
+    """The fields of a da_paged_cache."""
+    n_pages, page_size, hkv, d = shape = k_pages.shape
+    B, max_pages = block_table.shape
+    i32 = torch.int32
+    return (B, T, hkv, d, page_size, n_pages, max_pages, *_rows4(k_pages, shape, torch.bfloat16, dev, "k_pages"),
+            *_rows4(v_pages, shape, torch.bfloat16, dev, "v_pages"),
+            _array(block_table, (B, max_pages), i32, dev, "block_table"),
+            _array(cu_seqlens, (B + 1,), i32, dev, "cu_seqlens"), _array(seqlens, (B,), i32, dev, "seqlens"))
+
+
+def diffattn_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, inv_freq, *, q=None, q_out=None,
+                          positions=None, rot_dim=None, interleaved=False, rope_scale=1.0, norm=False, norm_eps=1e-5,
+                          q_weight=None, k_weight=None, stream=None):
+    """Put new tokens' keys (normed and rotated) and values [T, h_kv, d] into a paged cache: k_pages, v_pages
+    [n_pages, page_size, h_kv, d] in any stride order, block_table int32 [B, max_pages].  Sequence b's tokens are
+    rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1, the last of its seqlens[b] positions.  q [T, h_q, d] of the same
+    tokens goes, normed and rotated too, to q_out (None: a new tensor, whose rows without a sequence are zeros).
+    Returns q_out."""
+    dev, raw = _device(k, stream)
+    T, hkv, d = shape = k.shape
+    bf16 = torch.bfloat16
+    if q is not None and q_out is None:
+        q_out = _new(torch.zeros, q, q.shape, bf16, stream)
+    _same_heads(q, q_out, "q_out")
+    h_q = 0 if q is None else q.shape[1]
+    _call("diffattn_paged_append", _pack_paged_append(
+        *_paged_fields(T, k_pages, v_pages, block_table, cu_seqlens, seqlens, dev), h_q,
+        *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
+        _array(positions, (T,), torch.int32, dev, "positions"), *_rows3(k, (T, k_pages.shape[2], k_pages.shape[3]), bf16, dev, "k"),
+        *_rows3(v, shape, bf16, dev, "v"), *(_NO_T3 if q is None else _rows3(q, (T, h_q, d), bf16, dev, "q")),
+        *(_NO_T3 if q is None else _rows3(q_out, (T, h_q, d), bf16, dev, "q_out"))), raw)
+    return q_out
+
+
+def diffattn_v2_paged_fwd_workspace_size(T, B, max_new, h, h_kv, d, gate_given=False) -> int:
+    return int(load().diffattn_v2_paged_fwd_workspace_size(T, B, max_new, h, h_kv, d, int(gate_given)))
+
+
+def diffattn_v2_paged_fwd(q, k_pages, v_pages, block_table, cu_seqlens, seqlens, *, max_new=0, gate=None, x=None,
+                          w_lambda=None, out=None, softmax_scale=0.0, workspace=None, stream=None):
+    """V2 attention of new tokens q [T, 2h, d] over a paged cache (see diffattn_paged_append) that holds their keys:
+    out [T, h, d] (None: a new tensor, whose rows without a sequence are zeros).  max_new: the most new tokens that
+    a sequence is expected to have (0 = T); the kernel is chosen by it."""
+    dev, raw = _device(q, stream)
+    T, H2, d = q.shape
+    h, bf16 = H2 // 2, torch.bfloat16
+    B, hkv = block_table.shape[0], k_pages.shape[2]
+    if out is None:
+        out = _new(torch.zeros, q, (T, h, d), bf16, stream)
+    if workspace is None:
+        need = _need(dev, "diffattn_v2_paged_fwd_workspace_size", T, B, max_new, h, hkv, d, gate is not None)
+        workspace = _new(torch.empty, q, (max(need, 1),), torch.uint8, stream)
+    gate_, x_, w_, d_model = _gate_source(gate, x, w_lambda, T, h, dev)
+    _call("diffattn_v2_paged_fwd", _pack_paged_fwd(
+        *_paged_fields(T, k_pages, v_pages, block_table, cu_seqlens, seqlens, dev), h, d_model, max_new, softmax_scale,
+        *_rows3(q, (T, 2 * h, k_pages.shape[3]), bf16, dev, "q"), gate_, x_, w_, *_rows3(out, (T, h, d), bf16, dev, "out"),
+        *_space(workspace, dev)), raw)
+    return out
 
 
 DA_FAULT_NONE, DA_FAULT_V2_FWD_SKIP_LOAD = 0, 1

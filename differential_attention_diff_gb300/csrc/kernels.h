@@ -184,6 +184,61 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
 // Whether every head's own block moves its rows, whatever they are: no lists in memory.
 bool evict_moves_unlisted(int64_t units, int L_max, int sms);
 
+// ---- queries and keys normed and rotated; append to a paged cache ---------------
+struct RopeArgs {
+  int64_t tokens;
+  int N;                   // tokens are [B, N] (not paged)
+  int h_q, h_k, h_v;       // rows of a token; h_v: copied (paged)
+  int rot, interleaved, norm;
+  float rope_scale, norm_eps;
+  const float *inv_freq, *q_weight, *k_weight;
+  const int* positions;
+  da_t4 q, k, v;           // paged: sb unused, sn the token's stride
+  da_t4 q_out, k_out, v_out;  // paged: k_out, v_out are the pages
+  da_paged_cache cache;    // paged
+  uint32_t* status;
+  int chunks, chunk_passes;  // the warps' shares of a token (set by the launchers)
+  int64_t units;
+};
+struct RopeBwdArgs {
+  RopeArgs a;
+  da_t4 dq_out, dk_out, dq, dk;
+  float* part;             // [blocks, 2, d] sums of the weights' gradients, or null
+  float *dq_weight, *dk_weight;
+};
+constexpr int kRopeBwdBlocksPerSm = 4;
+int64_t rope_bwd_blocks(int64_t units, int sms);  // of the backward's grid, for `units` shares of work
+cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool f32, int sms, cudaStream_t s);
+cudaError_t launch_rope_bwd(const RopeBwdArgs& g, int d, bool f32, int sms, cudaStream_t s);
+// The checks of a paged cache: sizes and types, then pointers and strides (which
+// an empty call need not give).
+da_status check_paged_cache(const da_paged_cache& c);
+bool paged_cache_given(const da_paged_cache& c);
+cudaError_t launch_paged_append(const RopeArgs& a, int d, int sms, cudaStream_t s);
+
+// ---- V2 attention over a paged cache --------------------------------------------
+struct PagedDesc {
+  int flags, b, g, i;  // the item that is begun and not ended (paged.cuh)
+};
+struct PagedArgs {
+  da_paged_cache cache;
+  int h, G;            // output heads, query heads per KV head
+  int tq, tq1;         // tokens of an item, and of one of its MMA tiles
+  int box;             // keys of a page that one TMA copy takes
+  float scale_log2;
+  da_t3 q, out;
+  const float* gate;   // [T, h]
+  float* part_o;       // [2 grid, rows, d] unnormalised outputs of the parts
+  float* part_ml;      // [2 grid, rows, 2] their maxima (log2 units) and sums
+  PagedDesc* desc;     // [grid]
+  int rows;            // of a part: 128 per MMA tile
+  int grid;
+  uint32_t* status;
+  bool after_gate;     // the kernel launched just before is this call's gate
+};
+cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t s);
+
 // ---- V1 decode: split-KV partials of both streams, then merge + RMSNorm ----
 struct V1DecodeArgs {
   int B, H, d_qk, d_v, L_max, num_splits;  // (d_qk, d_v) = (128, 256) or (64, 128)

@@ -1,0 +1,215 @@
+// paged.cuh — how the attention over a paged cache shares its work, for the
+// kernels that do it (paged_fwd.cu) and the one that joins their parts
+// (paged_merge.cu).
+//
+// The unit of work is one tile of 128 keys for one item: up to `tq` new tokens
+// of one sequence with all G query heads of one KV head.  The units of a call
+// form a line, (sequence, KV head, item, key tile) in this order, and CTA c of C
+// takes its c-th equal share, wherever that begins and ends.  So a batch of any
+// lengths loads the SMs evenly, whether it is one long sequence or many short
+// ones, and only the items that a share's end cuts are left to be joined: at
+// most C - 1, whatever the batch.  A CTA has at most two such parts, the rest of
+// an item that an earlier one began (slot 2c) and the beginning of one that a
+// later one ends (slot 2c + 1); an item that runs through whole shares has its
+// middle parts in the slots 2c.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace da {
+
+constexpr int kPagedTile = 128;  // keys
+enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
+
+__device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
+  return t0 >= 0 && t0 <= t1 && t1 <= c.T && L >= t1 - t0 && L <= static_cast<int64_t>(c.max_pages) * c.page_size;
+}
+
+// sum over i < n of floor((a i + b) / m), by the steps of Euclid's algorithm
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// Key tiles of the first i items of a sequence with n new tokens, length L.
+__device__ __forceinline__ int64_t tiles_before(int i, int n, int L, int tq) {
+  return floor_sum(i, kPagedTile, tq, static_cast<int64_t>(L) - n + tq + kPagedTile - 1);
+}
+
+// Units of sequence b for one KV head, 0 if it is out of bounds (then *bad).
+__device__ __forceinline__ int64_t sequence_units(const da_paged_cache& c, int b, int tq, bool* bad) {
+  const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1], L = c.seqlens[b];
+  if (!paged_sequence_ok(c, t0, t1, L)) {
+    *bad = true;
+    return 0;
+  }
+  const int n = t1 - t0;
+  if (n == 0) return 0;
+  const int64_t last = (L + kPagedTile - 1) / kPagedTile;
+  return n <= tq ? last : tiles_before((n - 1) / tq, n, L, tq) + last;
+}
+
+// Where a CTA's share begins and how long it is.
+struct PagedShare {
+  int b, g, i, j;
+  int64_t units;
+  int bad;  // some sequence is out of bounds
+};
+
+// Fills *share (shared memory); called by all kThreads of a block.
+template <int kThreads>
+__device__ void paged_share(const PagedArgs& a, PagedShare* share) {
+  static_assert(kThreads % 32 == 0, "whole warps");
+  constexpr int kW = kThreads / 32;
+  __shared__ int64_t sums[kW];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = a.cache.B;
+  bool bad = false;
+  int64_t mine = 0, first = 0;  // first: of sequence tid, for a batch of at most kThreads
+  for (int b = tid; b < B; b += kThreads) {
+    const int64_t u = sequence_units(a.cache, b, a.tq, &bad) * a.cache.h_kv;
+    if (b == tid) first = u;
+    mine += u;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sums[warp] = mine;
+  const bool any_bad = __syncthreads_or(bad);
+  int64_t total = 0;
+  for (int w = 0; w < kW; ++w) total += sums[w];
+  // shares of less than a tile make no sense
+  const int64_t ctas = total < gridDim.x ? total : gridDim.x;
+  const int64_t c = blockIdx.x;
+  const int64_t u0 = c < ctas ? total * c / ctas : total, u1 = c < ctas ? total * (c + 1) / ctas : total;
+  if (tid == 0) {
+    share->units = u1 - u0;
+    share->bad = any_bad;
+  }
+  int64_t base = 0;
+  for (int r = 0; r < B && base <= u0 && u0 < u1; r += kThreads) {
+    const int b = r + tid;
+    bool ignore = false;
+    const int64_t w = r == 0 ? first : b < B ? sequence_units(a.cache, b, a.tq, &ignore) * a.cache.h_kv : 0;
+    int64_t incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    __syncthreads();  // sums has been read
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t before = base;
+    for (int v = 0; v < kW; ++v) {
+      if (v < warp) before += sums[v];
+      base += sums[v];
+    }
+    before += incl - w;
+    if (u0 >= before && u0 < before + w) {
+      const int n = a.cache.cu_seqlens[b + 1] - a.cache.cu_seqlens[b], L = a.cache.seqlens[b];
+      const int64_t per = w / a.cache.h_kv;
+      int64_t off = u0 - before;
+      const int g = static_cast<int>(off / per);
+      off -= g * per;
+      int lo = 0, hi = (n + a.tq - 1) / a.tq;  // the item: the last that begins at or before off
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (tiles_before(mid, n, L, a.tq) <= off)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      share->b = b;
+      share->g = g;
+      share->i = lo;
+      share->j = static_cast<int>(off - (lo ? tiles_before(lo, n, L, a.tq) : 0));
+    }
+  }
+  __syncthreads();
+}
+
+// A CTA's way along its share, part by part; every warp walks by itself.
+struct PagedWalk {
+  const PagedArgs& a;
+  int b, g, i, j;       // the part's item and first key tile
+  int64_t left;         // units that are left, this part's counted in
+  int t0, n, L;         // the sequence
+  int tokens, tiles, j1;  // the item's tokens and key tiles; the part ends before tile j1
+  __device__ __forceinline__ PagedWalk(const PagedArgs& a_, const PagedShare& s)
+      : a(a_), b(s.b), g(s.g), i(s.i), j(s.j), left(s.units) {
+    if (left > 0) {
+      sequence();
+      item();
+    }
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool begins() const { return j == 0; }
+  __device__ __forceinline__ bool ends() const { return j1 == tiles; }
+  // position of the item's first token
+  __device__ __forceinline__ int first_position() const { return L - n + i * a.tq; }
+  __device__ __forceinline__ void next() {
+    left -= j1 - j;
+    if (left <= 0) return;
+    j = 0;
+    if ((i + 1) * a.tq < n) {
+      ++i;
+    } else {
+      i = 0;
+      if (++g == a.cache.h_kv) {
+        g = 0;
+        ++b;
+        sequence();
+      }
+    }
+    item();
+  }
+
+ private:
+  __device__ __forceinline__ void sequence() {
+    for (;; ++b) {  // there is one with work, since units are left
+      t0 = a.cache.cu_seqlens[b];
+      const int t1 = a.cache.cu_seqlens[b + 1];
+      L = a.cache.seqlens[b];
+      n = t1 - t0;
+      if (b >= a.cache.B - 1 || (n > 0 && paged_sequence_ok(a.cache, t0, t1, L))) break;
+    }
+  }
+  __device__ __forceinline__ void item() {
+    tokens = min(a.tq, n - i * a.tq);
+    tiles = (first_position() + tokens + kPagedTile - 1) / kPagedTile;
+    j1 = left < tiles - j ? j + static_cast<int>(left) : tiles;
+  }
+};
+
+// The outputs of the sequences that are out of bounds, where their rows are
+// within the array: zeros.  All threads of the grid share them.
+__device__ __forceinline__ void paged_zero_bad(const PagedArgs& a) {
+  const da_paged_cache& c = a.cache;
+  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+    const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1];
+    if (paged_sequence_ok(c, t0, t1, c.seqlens[b])) continue;
+    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
+    const int per = a.h * c.d / 8;
+    const int lo = max(t0, 0), hi = min(t1, c.T);
+    for (int64_t x = threadIdx.x; x < static_cast<int64_t>(hi - lo) * per; x += blockDim.x) {
+      const int t = lo + static_cast<int>(x / per), r = static_cast<int>(x % per);
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out.ptr) + t * a.out.st + r / (c.d / 8) * a.out.sh + r % (c.d / 8) * 8;
+      *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+}  // namespace da

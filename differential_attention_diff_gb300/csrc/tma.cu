@@ -49,6 +49,22 @@ bool encode_tmap_bf16_4d(CUtensorMap* map, const da_t4& t, int B, int N, int H, 
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_bf16_box(CUtensorMap* map, void* ptr, const int64_t (&dims)[4], const int64_t (&strides)[3],
+                          const int (&box)[4]) {
+  if (!tma_available()) return false;
+  cuuint64_t ext[4], step[3];
+  cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    ext[i] = static_cast<cuuint64_t>(dims[i]);
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+  }
+  for (int i = 0; i < 3; ++i) step[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(strides[i]) * 2;
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, ext, step, bx, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool encode_tmap_f32_4d(CUtensorMap* map, void* ptr, int B, int N, int H, int D, int rows, int box_d) {
   if (!tma_available()) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),

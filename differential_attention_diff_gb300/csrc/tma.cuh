@@ -18,6 +18,10 @@ namespace da {
 // out-of-range rows read as zero.
 bool encode_tmap_bf16_4d(CUtensorMap* map, const da_t4& t, int B, int N, int H,
                          int D, int rows);
+// A 4-D bf16 tensor map with any extents, element strides of dimensions 1 to 3
+// (not looked at where the extent is 1) and box, 128-byte swizzle, zeros outside.
+bool encode_tmap_bf16_box(CUtensorMap* map, void* ptr, const int64_t (&dims)[4], const int64_t (&strides)[3],
+                          const int (&box)[4]);
 // A 4-D fp32 tensor map over a contiguous [B, N, H, D] tensor, box = {box_d
 // (0: D), 1, rows, 1}, no swizzle (used for reduce-adds of fp32 tiles).
 bool encode_tmap_f32_4d(CUtensorMap* map, void* ptr, int B, int N, int H, int D, int rows, int box_d = 0);

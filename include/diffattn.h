@@ -623,6 +623,178 @@ size_t diffattn_kv_evict_workspace_size(int B, int h_kv, int L_max, int keep);
 da_status diffattn_kv_evict(const da_kv_evict_params* p, void* cuda_stream);
 
 /* ------------------------------------------------------------------------ */
+/* Positions.  The pages leave them to the model around the operator ([P2] §1:
+ * Q and K are projections of the input); these entry points give queries and
+ * keys theirs, by rotation, with the per-head RMSNorm of queries and keys that
+ * a model may have before it, in the same pass.  For a row x of d features:
+ *   z = w x / sqrt(mean_k x_k^2 + norm_eps)   (norm; z = x without it)
+ *   a_i = position * inv_freq[i], i < rot_dim / 2, of the fp32 inv_freq as it
+ *         is: no product is rounded before it is reduced to one turn
+ *   y_u = rope_scale (z_u cos a_i - z_v sin a_i)
+ *   y_v = rope_scale (z_v cos a_i + z_u sin a_i)
+ * with (u, v) = (i, i + rot_dim / 2), or (2i, 2i + 1) where `interleaved`; the
+ * features from rot_dim on are y = z.  Everything is computed in fp32 (the sum
+ * of x_k^2 too: it has to stay within its range) and rounded once.  Stretched contexts are other frequencies and another scale:
+ * diffattn_rope_inv_freq makes both. */
+
+/* A packed [T, H, D] tensor: element (t, h, x) lives at ptr + t*st + h*sh + x
+ * (in elements). */
+typedef struct {
+  void* ptr;
+  int64_t st, sh;
+} da_t3;
+
+/* How frequencies base^(-2i / rot_dim) are stretched for contexts `factor`
+ * times as long as the trained one of `trained_len` positions:
+ *   NONE    not at all (factor is not looked at)
+ *   LINEAR  every frequency / factor
+ *   BASE    base * factor^(rot_dim / (rot_dim - 2)): the highest frequency
+ *           stays, the lowest is divided by factor
+ *   RAMP    frequencies that turn more than 32 times over trained_len stay,
+ *           those that turn less than once are divided by factor, those in
+ *           between are mixed by the number of turns; the rotated features are
+ *           scaled by 0.1 ln(factor) + 1 */
+typedef enum { DA_ROPE_NONE = 0, DA_ROPE_LINEAR = 1, DA_ROPE_BASE = 2, DA_ROPE_RAMP = 3 } da_rope_stretch;
+
+/* Host function: writes rot_dim / 2 frequencies (radians per position, computed
+ * in fp64 and rounded once) to the HOST array inv_freq and the scale of the
+ * rotated features to *rope_scale.  rot_dim a positive multiple of 8 (above 2
+ * for BASE), base > 1, factor >= 1, trained_len > 0 (RAMP). */
+da_status diffattn_rope_inv_freq(int rot_dim, double base, da_rope_stretch stretch, double factor, int trained_len,
+                                 float* inv_freq, float* rope_scale);
+
+/* Queries and keys normed and rotated.  q: [B, N, h_q, d], k: [B, N, h_k, d]
+ * of `dtype` (h_q or h_k may be 0, the tensor is then not looked at); q_out,
+ * k_out of the same shapes, each of them its input itself or apart from it.
+ * positions: int32 [B, N] contiguous (NULL = 0 .. N-1), any value.
+ * q_weight, k_weight: fp32 [d] (NULL = unit; not looked at without norm).
+ * Supported: d = 16, 32, 64 or 128, DA_BF16 or DA_F32, rot_dim a multiple of 8
+ * from 0 (no rotation) to d; bases and strides multiples of 16 bytes. */
+typedef struct {
+  int B, N, h_q, h_k, d;
+  da_dtype dtype;
+  int rot_dim, interleaved;
+  const float* inv_freq;  /* device fp32 [rot_dim / 2] */
+  float rope_scale;
+  int norm;
+  float norm_eps;         /* >= 0 */
+  const float *q_weight, *k_weight;
+  const int* positions;
+  da_t4 q, k;
+  da_t4 q_out, k_out;
+} da_qk_rope_fwd_params;
+
+da_status diffattn_qk_rope_fwd(const da_qk_rope_fwd_params* p, void* cuda_stream);
+
+/* The gradients of diffattn_qk_rope_fwd: with dy the gradient of y and R the
+ * rotation, xh = x / sqrt(mean x^2 + norm_eps),
+ *   dz = R^T dy,  dw = sum over all rows of dz xh,
+ *   dx = (w dz - xh mean(w dz xh)) / sqrt(mean x^2 + norm_eps)   (dz without norm)
+ * `fwd` as given to the forward (q_out and k_out are not looked at; q and k only
+ * with norm); dq_out, dk_out: the gradients of q_out and k_out; dq, dk: those of
+ * q and k, each of them dq_out / dk_out itself or apart from everything else.
+ * dq_weight, dk_weight: fp32 [d] (NULL = not computed; both need norm),
+ * overwritten, summed in a fixed order: bitwise reproducible.  workspace:
+ * diffattn_qk_rope_bwd_workspace_size bytes, 256-byte aligned, looked at where a
+ * weight's gradient is asked for; calls that run at the same time need
+ * workspaces of their own. */
+typedef struct {
+  da_qk_rope_fwd_params fwd;
+  da_t4 dq_out, dk_out;
+  da_t4 dq, dk;
+  float *dq_weight, *dk_weight;
+  void* workspace;
+  size_t workspace_bytes;
+} da_qk_rope_bwd_params;
+
+size_t diffattn_qk_rope_bwd_workspace_size(int B, int N, int h_q, int h_k, int d);
+da_status diffattn_qk_rope_bwd(const da_qk_rope_bwd_params* p, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged cache.  K and V of B sequences in pages of page_size positions that
+ * lie anywhere: position j of sequence b lives in slot j % page_size of page
+ * block_table[b, j / page_size].  k_pages, v_pages: bf16 [n_pages, page_size,
+ * h_kv, d] as da_t4 with sb the page's, sn the slot's and sh the head's stride
+ * (any order); block_table: int32 [B, max_pages] contiguous, looked at up to
+ * the sequence's length; two sequences may share pages.
+ * New tokens are packed: sequence b's are rows cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1 (n of them, 0 allowed) of arrays of T rows; cu_seqlens:
+ * int32 [B + 1], rising.  They are the last n of its seqlens[b] positions (the
+ * new tokens counted in): token i has position seqlens[b] - n + i.  Rows from
+ * cu_seqlens[B] on belong to no sequence: outputs are left as they were there.
+ * A sequence whose rows are not within 0 .. T, or whose length is not within
+ * n .. max_pages * page_size, is recorded as DA_ERR_BOUNDS in the device status
+ * word, and so is a page outside 0 .. n_pages - 1 where one is looked up. */
+typedef struct {
+  int B, T, h_kv, d;
+  int page_size, n_pages, max_pages;
+  da_t4 k_pages, v_pages;
+  const int* block_table;
+  const int* cu_seqlens;
+  const int* seqlens;
+} da_paged_cache;
+
+/* Puts new tokens into the pages: k (normed and rotated as by
+ * diffattn_qk_rope_fwd) and v (as it is), bf16 [T, h_kv, d], and, where h_q >
+ * 0, the same tokens' queries q [T, h_q, d], normed and rotated, to q_out (q
+ * itself, or apart from it).  positions: int32 [T], the rotation's (NULL = the
+ * tokens' positions in their sequences).  d = 64 or 128.  Of a sequence that is
+ * out of bounds nothing is written; of a token whose page is, the queries are.
+ * Two tokens may not go to the same slot. */
+typedef struct {
+  da_paged_cache cache;
+  int h_q;
+  int rot_dim, interleaved;
+  const float* inv_freq;
+  float rope_scale;
+  int norm;
+  float norm_eps;
+  const float *q_weight, *k_weight;
+  const int* positions;
+  da_t3 k, v;
+  da_t3 q, q_out;
+} da_paged_append_params;
+
+da_status diffattn_paged_append(const da_paged_append_params* p, void* cuda_stream);
+
+/* V2 attention ([P2] §1, §2) of new tokens over a paged cache that holds their
+ * keys already: a token sees the positions of its sequence up to its own,
+ *   out[t, p] = O[t, 2p] - gate[t, p] O[t, 2p + 1],
+ * with the heads' grouping and the gate's source as in diffattn_v2_fwd.  One
+ * token per sequence is a decode step, many are a chunk of a prompt, and a call
+ * may mix both.  q: bf16 [T, 2h, d]; gate: fp32 [T, h] contiguous, or x bf16
+ * [T, d_model] and w_lambda bf16 [d_model, h] contiguous; out: bf16 [T, h, d].
+ * max_new: the most new tokens that a sequence may be expected to have (0 = T):
+ * the kernel is chosen by it, the result is right whatever it says.
+ * The rows of a sequence that is out of bounds are zeros (where the rows are
+ * within 0 .. T); keys and values of a page that is out of bounds are read as
+ * zeros.  What lies behind a sequence's end in its last page is not looked at,
+ * whatever it holds; a value row that holds an infinity or a NaN may reach
+ * tokens of its own chunk that come up to 255 positions before it.
+ * Supported: d = 64 or 128; 2h / h_kv even, at most 128; page_size a multiple of
+ * 16; strides of dimensions longer than 1 above 0; d_model % 64 == 0 and h <= 64 where the gate is computed.  T * 2h and
+ * B * max_pages at most 2^31 - 1, h_kv at most 65535, max_pages * page_size at
+ * most 2^30.
+ * workspace: diffattn_v2_paged_fwd_workspace_size bytes, 256-byte aligned,
+ * contents on entry irrelevant; calls that run at the same time need workspaces
+ * of their own.  Results are bitwise reproducible from call to call. */
+typedef struct {
+  da_paged_cache cache;
+  int h, d_model, max_new;
+  float softmax_scale;   /* <= 0 selects 1/sqrt(d) */
+  da_t3 q;
+  const float* gate;
+  const void* x;
+  const void* w_lambda;
+  da_t3 out;
+  void* workspace;
+  size_t workspace_bytes;
+} da_v2_paged_fwd_params;
+
+size_t diffattn_v2_paged_fwd_workspace_size(int T, int B, int max_new, int h, int h_kv, int d, int gate_given);
+da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ */
 /* Device status word.  Kernels record the first error they detect (a bounded
  * wait that expired, a failed index check) in a per-device word instead of
  * trapping.  diffattn_get_device_status synchronises `cuda_stream`, returns
