@@ -192,56 +192,102 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
   } else if (warp == 9) {
     // ------------------------------------------------------- MMA issuer ---
+    // One thread, whose instructions between two MMAs are what bounds the loop
+    // when there are many: descriptors are sums of a base and constants, and
+    // turns are told apart by unrolling.
     if (lane == 0) {
       int kv_it = 0, it = 0;
       uint32_t pc[2] = {0, 0};
       bool ok = true;
-      auto issue_s = [&](int s, int q, int st) {
-        const uint32_t qa = sh.base + kOffQ + q * kNB * kBox;
-        const uint32_t kb = sh.base + kOffK + st * kNB * kBox;
+      const uint32_t q0 = sdesc_lo(sh.base + kOffQ, 16), k0 = sdesc_lo(sh.base + kOffK, 16), v0 = sdesc_lo(sh.base + kOffV, kBox);
+      constexpr uint32_t kTile = kNB * kBox >> 4;  // descriptor units (16 bytes) from one tile to the next
+      auto issue_s = [&](int s, uint32_t q, uint32_t k) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-          tc_mma_ss(tmem + s * 128, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), kIdescS, kk > 0);
+          const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+          tc_mma_ss_lo(tmem + s * 128, q + off, k + off, kIdescS, kk > 0);
         }
         tc_commit(sh.bar(B_SFULL + s));
       };
-      auto issue_pv = [&](int s, int st, bool acc) {
-        const uint32_t vb = sh.base + kOffV + st * kNB * kBox;
+      auto issue_pv = [&](int s, uint32_t v, bool acc) {
 #pragma unroll
         for (int kk = 0; kk < kPagedTile / 16; ++kk)
           // P of keys 0-63 in columns 0-31 of the S buffer, keys 64-127 in 64-95
-          tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8 + (kk >= 4 ? 32 : 0),
-                    sdesc_sw128(vb + kk * 2048, kBox, 1024), kIdescPV, (acc || kk > 0) ? 1u : 0u);
+          tc_mma_ts_lo(tmem + 256 + s * 128, tmem + s * 128 + kk * 8 + (kk >= 4 ? 32 : 0), v + (kk * 2048 >> 4), kIdescPV,
+                       (acc || kk > 0) ? 1u : 0u);
+      };
+      auto full = [&](int bar, int x, uint32_t site) {  // of tile x's stage
+        return wait_bar(sh, sh.bar(bar + (x & 1)), (x >> 1) & 1, a.status, site);
       };
       for (PagedWalk w(a, share); w.more() && ok; w.next(), ++it) {
-        const bool dual = two(w);
-        const int tiles = w.j1 - w.j, steps = dual ? 2 * tiles : tiles;
+        const int tiles = w.j1 - w.j;
         if (!wait_bar(sh, sh.bar(B_QFULL), it & 1, a.status, 0x8101)) break;
+        if (!full(B_KFULL, kv_it, 0x8102)) break;
         tc_fence_after();
-        // step k: turn k & 1, on key tile k / 2 (two Q tiles) or k (one)
-        auto start = [&](int k) {
-          const int x = kv_it + (dual ? k >> 1 : k), st = x & 1;
-          if (!wait_bar(sh, sh.bar(B_KFULL + st), (x >> 1) & 1, a.status, 0x8102)) return false;
-          tc_fence_after();
-          issue_s(k & 1, dual ? k & 1 : 0, st);
-          if (!dual || (k & 1)) tc_commit(sh.bar(B_KEMPTY + st));
-          if (k == steps - 1) tc_commit(sh.bar(B_QEMPTY));
-          return true;
-        };
-        ok = start(0) && (steps < 2 || start(1));
-        for (int k = 0; k < steps && ok; ++k) {
-          const int s = k & 1, x = kv_it + (dual ? k >> 1 : k), st = x & 1;
-          if (!wait_bar(sh, sh.bar(B_PFULL + s), pc[s] & 1, a.status, 0x8103) ||
-              !wait_bar(sh, sh.bar(B_VFULL + st), (x >> 1) & 1, a.status, 0x8104)) {
-            ok = false;
-            break;
+        if (two(w)) {
+          // both turns on every tile
+          const uint32_t kb = k0 + (kv_it & 1) * kTile;
+          issue_s(0, q0, kb);
+          issue_s(1, q0 + kTile, kb);
+          tc_commit(sh.bar(B_KEMPTY + (kv_it & 1)));
+          if (tiles == 1) tc_commit(sh.bar(B_QEMPTY));
+          for (int j = 0; j < tiles; ++j) {
+            const int x = kv_it + j, st = x & 1;
+            const uint32_t v = v0 + st * kTile, k = k0 + (st ^ 1) * kTile;
+            const bool more = j + 1 < tiles;
+            ok = full(B_VFULL, x, 0x8104) && wait_bar(sh, sh.bar(B_PFULL + 0), pc[0] & 1, a.status, 0x8103);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(0, v, j > 0);
+            if (more) {
+              ok = full(B_KFULL, x + 1, 0x8105);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(0, q0, k);
+            }
+            ok = wait_bar(sh, sh.bar(B_PFULL + 1), pc[1] & 1, a.status, 0x8106);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, v, j > 0);
+            tc_commit(sh.bar(B_VEMPTY + st));
+            if (more) {
+              issue_s(1, q0 + kTile, k);
+              tc_commit(sh.bar(B_KEMPTY + (st ^ 1)));
+              if (j + 2 == tiles) tc_commit(sh.bar(B_QEMPTY));
+            }
+            ++pc[0];
+            ++pc[1];
           }
-          ++pc[s];
-          tc_fence_after();
-          issue_pv(s, st, k >= 2);
-          if (!dual || s) tc_commit(sh.bar(B_VEMPTY + st));
-          if (k + 2 < steps) ok = start(k + 2);
+        } else {
+          // turn A on tiles 0, 2, .., turn B on 1, 3, ..: a tile per step
+          auto start = [&](int s, int j) {
+            const int x = kv_it + j;
+            issue_s(s, q0, k0 + (x & 1) * kTile);
+            tc_commit(sh.bar(B_KEMPTY + (x & 1)));
+            if (j + 1 == tiles) tc_commit(sh.bar(B_QEMPTY));
+          };
+          auto step = [&](int s, int j) {
+            const int x = kv_it + j;
+            if (!full(B_VFULL, x, 0x8107) || !wait_bar(sh, sh.bar(B_PFULL + s), pc[s] & 1, a.status, 0x8108)) return false;
+            ++pc[s];
+            tc_fence_after();
+            issue_pv(s, v0 + (x & 1) * kTile, j >= 2);
+            tc_commit(sh.bar(B_VEMPTY + (x & 1)));
+            if (j + 2 < tiles) {
+              if (!full(B_KFULL, x + 2, 0x8109)) return false;
+              tc_fence_after();
+              start(s, j + 2);
+            }
+            return true;
+          };
+          start(0, 0);
+          if (tiles > 1) {
+            ok = full(B_KFULL, kv_it + 1, 0x810a);
+            if (!ok) break;
+            tc_fence_after();
+            start(1, 1);
+          }
+          for (int j = 0; j < tiles && ok; j += 2) ok = step(0, j) && (j + 1 == tiles || step(1, j + 1));
         }
         if (!ok) break;
         tc_commit(sh.bar(B_ORDY));
