@@ -391,6 +391,21 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       kv_it += tiles;
       // ----------------------------------------------------- epilogue ----
+      const bool whole = w.begins() && w.ends();
+      if (whole && !synced) {
+        cudaGridDependencySynchronize();  // the gate
+        synced = true;
+      }
+      // what the row's output is scaled by: 1 (even heads) or the gate, fetched
+      // while the last products run
+      const int pair = w.g * (a.G / 2) + ((row - my_tok * a.G) >> 1);
+      const int64_t t_item = w.t0 + static_cast<int64_t>(w.i) * a.tq;
+      float factor[2] = {1.f, 1.f};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int tok = (s ? a.tq1 : 0) + my_tok;
+        if (whole && (row & 1) && in_tile && tok < w.tokens && (dual || s == 0)) factor[s] = a.gate[(t_item + tok) * a.h + pair];
+      }
       if (!wait_bar(sh, sh.bar(B_ORDY), it & 1, a.status, 0x8202)) ok = false;
       tc_fence_after();
       float* lx = sh.lx();
@@ -399,11 +414,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (named_red_or_256(!ok || *sh.abort_flag())) {
         ok = false;
         break;
-      }
-      const bool whole = w.begins() && w.ends();
-      if (whole && !synced) {
-        cudaGridDependencySynchronize();  // the gate
-        synced = true;
       }
       const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.begins() ? 1 : 0)) * a.rows;
 #pragma unroll 1
@@ -423,12 +433,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           l = l * fa + lb * fb;
           m = mm;
         }
-        const int head = row - my_tok * a.G;  // within the group
-        const int64_t t = w.t0 + w.i * a.tq + tok;
-        const int pair = w.g * (a.G / 2) + (head >> 1);
-        float coef = 0.f;
-        if (whole && valid) coef = (row & 1 ? a.gate[t * a.h + pair] : 1.f) / l;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.ptr) + t * a.out.st + pair * a.out.sh + wg * (D / 2);
+        const float coef = (s ? factor[1] : factor[0]) / l;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.ptr) + (t_item + tok) * a.out.st + pair * a.out.sh + wg * (D / 2);
         float* po = a.part_o + (part + s * 128 + row) * D + wg * (D / 2);
         const uint32_t t_o = tmem + lane_off + 256 + s * 128 + wg * (D / 2);
 #pragma unroll 1

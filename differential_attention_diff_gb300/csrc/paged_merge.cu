@@ -2,11 +2,13 @@
 // (paged.cuh): the softmax rule over each part's maximum and sum, then even -
 // gate * odd.
 //
-// Block c of the grid's rows looks after the item that CTA c of the attention
-// began and did not end, if there is one: its parts are slot 2c + 1 and then the
-// slots 2c', c' = c + 1, ..., up to the CTA that ends it.  The item's pairs are
-// dealt to the blocks (c, y); a block's threads are the head's features times
-// ways that share the parts, and the ways are added in their order.
+// Block (c, y) looks after a share of the pairs of the item that CTA c of the
+// attention began and did not end, if there is one: its parts are slot 2c + 1 and
+// then the slots 2c', c' = c + 1, ..., up to the CTA that ends it.  An item of a
+// prompt has many pairs and few parts (of many key tiles each): a warp takes a
+// pair, d / 32 features of both heads to a lane, and nothing is shared.  One of a
+// decode step has few pairs and may have many parts: the block takes a pair, its
+// threads are the features times ways that share the parts, added in their order.
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.cuh"
@@ -15,7 +17,43 @@ namespace da {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxParts = 1024;  // of an item: CTAs of a grid
+constexpr int kFew = 8;          // parts that a warp joins by itself
+
+template <int D>
+struct Merge {
+  const PagedArgs& a;
+  PagedDesc d;
+  int c, parts, t0;
+  __device__ __forceinline__ int64_t slot(int i, int row) const {
+    return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.rows + row;
+  }
+  __device__ __forceinline__ int row(int pair) const {
+    const int half = a.G / 2, tok = pair / half;
+    return tok / a.tq1 * 128 + tok % a.tq1 * a.G + 2 * (pair % half);
+  }
+  // of the pair, the output's token row and head
+  __device__ __forceinline__ int64_t token(int pair) const { return t0 + static_cast<int64_t>(d.i) * a.tq + pair / (a.G / 2); }
+  __device__ __forceinline__ int head(int pair) const { return d.g * (a.G / 2) + pair % (a.G / 2); }
+  __device__ __forceinline__ __nv_bfloat16* out(int pair, int col) const {
+    return static_cast<__nv_bfloat16*>(a.out.ptr) + token(pair) * a.out.st + head(pair) * a.out.sh + col;
+  }
+};
+
+// The weight of part `lane` of a head's row (lanes from `parts` on: 0), and 1 / sum.
+__device__ __forceinline__ float part_weight(const float* part_ml, int64_t slot, bool there, float* inv) {
+  const float2 ml = there ? *reinterpret_cast<const float2*>(part_ml + slot * 2) : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float f = exp2f(ml.x - (m == -INFINITY ? 0.f : m));
+  float l = ml.y * f;
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+  *inv = 1.f / l;
+  return f;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads)
@@ -24,33 +62,74 @@ paged_merge_kernel(PagedArgs a) {
   __shared__ float weight[2][kMaxParts];
   __shared__ float inv[2];
   __shared__ float sums[kWays][2][D];
+  __shared__ int last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
+  if (tid == 0) last = a.grid - 1;
   cudaGridDependencySynchronize();  // the parts (and, behind them, the gate)
-  const PagedDesc d = a.desc[c];
-  if (!(d.flags & kPagedOpen)) return;
-  int parts = 1;  // and those of the CTAs that follow, up to the one that ends it
-  for (int x = c + 1; x < a.grid; ++x) {
-    ++parts;
-    if (a.desc[x].flags & kPagedEnds) break;
+  Merge<D> mg{a, a.desc[c], c, 0, 0};
+  if (!(mg.d.flags & kPagedOpen)) return;
+  __syncthreads();
+  for (int x = c + 1 + tid; x < a.grid; x += kThreads)
+    if (a.desc[x].flags & kPagedEnds) {
+      atomicMin(&last, x);
+      break;
+    }
+  mg.t0 = a.cache.cu_seqlens[mg.d.b];
+  const int n = a.cache.cu_seqlens[mg.d.b + 1] - mg.t0;
+  const int pairs = min(a.tq, n - mg.d.i * a.tq) * (a.G / 2);
+  __syncthreads();
+  const int parts = mg.parts = last - c + 1;
+  if (parts <= kFew) {
+    constexpr int kPer = D / 32;
+    for (int pair = blockIdx.y * kWarps + warp; pair < pairs; pair += gridDim.y * kWarps) {
+      const int row = mg.row(pair);
+      const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
+      float o[2][kPer], iv[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = part_weight(a.part_ml, mg.slot(lane < parts ? lane : 0, row + e), lane < parts, &iv[e]);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) o[e][q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          if (i >= parts) break;
+          const float w = __shfl_sync(0xffffffffu, f, i);
+          const float* po = a.part_o + mg.slot(i, row + e) * D + lane * kPer;
+          float x[kPer];
+          if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(po);
+          else
+            *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(po);
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) o[e][q] = fmaf(x[q], w, o[e][q]);
+        }
+      }
+      uint32_t y[kPer / 2];
+      const float c0 = iv[0], c1 = iv[1] * g;
+#pragma unroll
+      for (int q = 0; q < kPer / 2; ++q)  // the products rounded apart, so that equal heads cancel with gate 1
+        y[q] = pack_bf16x2(__fsub_rn(__fmul_rn(o[0][2 * q], c0), __fmul_rn(o[1][2 * q], c1)),
+                           __fsub_rn(__fmul_rn(o[0][2 * q + 1], c0), __fmul_rn(o[1][2 * q + 1], c1)));
+      uint32_t* dst = reinterpret_cast<uint32_t*>(mg.out(pair, lane * kPer));
+#pragma unroll
+      for (int q = 0; q < kPer / 2; ++q) dst[q] = y[q];
+    }
+    return;
   }
-  const int t0 = a.cache.cu_seqlens[d.b], n = a.cache.cu_seqlens[d.b + 1] - t0;
-  const int tokens = min(a.tq, n - d.i * a.tq), half = a.G / 2;
   const int col = tid % D, way = tid / D;
-  for (int pair = blockIdx.y; pair < tokens * half; pair += gridDim.y) {
-    const int tok = pair / half, p = pair % half;
-    const int row = tok / a.tq1 * 128 + tok % a.tq1 * a.G + 2 * p;
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.rows + row; };
+  for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
+    const int row = mg.row(pair);
     // the parts' weights: warp e takes head e of the pair
     if (warp < 2) {
       float m = -INFINITY;
-      for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[(slot(i) + warp) * 2]);
+      for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[mg.slot(i, row + warp) * 2]);
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float base = m == -INFINITY ? 0.f : m;
       float l = 0.f;
       for (int i = lane; i < parts; i += 32) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot(i) + warp) * 2);
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + mg.slot(i, row + warp) * 2);
         const float f = exp2f(ml.x - base);
         weight[warp][i] = f;
         l = fmaf(ml.y, f, l);
@@ -63,7 +142,7 @@ paged_merge_kernel(PagedArgs a) {
     float o0 = 0.f, o1 = 0.f;
 #pragma unroll 4
     for (int i = way; i < parts; i += kWays) {
-      const float* o = a.part_o + slot(i) * D + col;
+      const float* o = a.part_o + mg.slot(i, row) * D + col;
       o0 = fmaf(o[0], weight[0][i], o0);
       o1 = fmaf(o[D], weight[1][i], o1);
     }
@@ -75,11 +154,8 @@ paged_merge_kernel(PagedArgs a) {
         o0 += sums[w][0][col];
         o1 += sums[w][1][col];
       }
-      const int64_t t = t0 + d.i * a.tq + tok;
-      const int head = d.g * half + p;
-      // the products rounded apart, so that equal heads cancel with gate 1
-      const float y = __fsub_rn(__fmul_rn(o0, inv[0]), __fmul_rn(o1, inv[1] * a.gate[t * a.h + head]));
-      static_cast<__nv_bfloat16*>(a.out.ptr)[t * a.out.st + head * a.out.sh + col] = __float2bfloat16_rn(y);
+      const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
+      *mg.out(pair, col) = __float2bfloat16_rn(__fsub_rn(__fmul_rn(o0, inv[0]), __fmul_rn(o1, inv[1] * g)));
     }
     __syncthreads();
   }
