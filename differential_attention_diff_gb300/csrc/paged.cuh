@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tma.cuh"
 
 namespace da {
 
@@ -192,6 +193,72 @@ struct PagedWalk {
     tiles = (first_position() + tokens + kPagedTile - 1) / kPagedTile;
     j1 = left < tiles - j ? j + static_cast<int>(left) : tiles;
   }
+};
+
+// ------------------------------------------------------- tiles of pages ----
+// A tile of 128 keys (or values) of a KV head in shared memory: groups of 8 rows,
+// in each group D / 64 atoms of 8 rows x 128 bytes (64 features, 128-byte
+// swizzle).  So any number of rows that is a multiple of 8 is one contiguous
+// piece with all features, and a page's share of a tile is one TMA copy: the
+// tensor map's dimensions are (64 features, 8 rows, blocks of 64 features counted
+// through all heads, groups of 8 rows, pages).  Copies of 4 KB (two of 2 KB each
+// in a layout with a box per 64 features) are what a page of 16 leaves.
+// As an MMA operand with the features along K the groups are (D / 64) KB apart;
+// with the features along M or N so are the groups along K, and the 64-feature
+// blocks 1 KB.
+template <int D>
+struct KeyTile {
+  static constexpr int kNB = D / 64;
+  static constexpr int kGroup = kNB * 1024;
+  static constexpr int kBytes = 16 * kGroup;
+  static constexpr uint32_t kHi = sdesc_hi(kGroup);
+  // descriptor units (16 bytes) to K step kk (16 features or 16 keys)
+  static constexpr __device__ uint32_t feature_step(int kk) { return ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4; }
+  static constexpr __device__ uint32_t key_step(int kk) { return kk * 2 * kGroup >> 4; }
+  static __device__ uint32_t row(int r) { return (r >> 3) * kGroup + (r & 7) * 128; }
+};
+
+inline bool encode_pages(CUtensorMap* map, const da_t4& t, const da_paged_cache& c, int box) {
+  const int64_t dims[5] = {64, 8, c.h_kv > 1 ? (c.h_kv - 1) * (t.sh / 64) + c.d / 64 : c.d / 64, c.page_size / 8, c.n_pages};
+  const int64_t strides[4] = {t.sn, 64, 8 * t.sn, t.sb};
+  const int boxes[5] = {64, 8, c.d / 64, box / 8, 1};
+  return encode_tmap_bf16_box(map, t.ptr, 5, dims, strides, boxes);
+}
+
+// Queries: boxes of 64 features, all heads of a KV head, `tokens` tokens.
+inline bool encode_queries(CUtensorMap* map, const PagedArgs& a, int tokens) {
+  const int64_t dims[3] = {a.cache.d, 2 * a.h, a.cache.T}, strides[2] = {a.q.sh, a.q.st};
+  const int boxes[3] = {64, a.G, tokens};
+  return encode_tmap_bf16_box(map, a.q.ptr, 3, dims, strides, boxes);
+}
+
+// A producer lane's copies: lanes 0 .. 128 / box - 1 each look up and copy `box`
+// rows of every tile, from the page that the block table names.  A page that is
+// none reads as zeros: it is taken to be the one behind the last.
+struct PageCopies {
+  const PagedArgs& a;
+  int row0, k_block, v_block;  // first row of this lane's copies; 64-feature blocks per head
+  bool mine;
+  __device__ __forceinline__ PageCopies(const PagedArgs& a_, int lane) : a(a_) {
+    row0 = lane * a.box;
+    mine = row0 < kPagedTile;
+    k_block = static_cast<int>(a.cache.k_pages.sh / 64);
+    v_block = static_cast<int>(a.cache.v_pages.sh / 64);
+  }
+  // whether tile j's copy holds any of a sequence's L keys
+  __device__ __forceinline__ bool used(int L, int j) const { return mine && j * kPagedTile + row0 < L; }
+  // its entry in the block table (`page` looks at it: what it waits for is the load)
+  __device__ __forceinline__ int entry(int b, int L, int j) const {
+    if (!used(L, j)) return 0;
+    return a.cache.block_table[static_cast<int64_t>(b) * a.cache.max_pages + (j * kPagedTile + row0) / a.cache.page_size];
+  }
+  __device__ __forceinline__ int page(int entry, int L, int j) const {
+    const bool in = entry >= 0 && entry < a.cache.n_pages;
+    if (used(L, j) && in) return entry;
+    if (!in) record_status(a.status, DA_ERR_BOUNDS, 0x0F02);
+    return a.cache.n_pages;
+  }
+  __device__ __forceinline__ int group(int j) const { return (j * kPagedTile + row0) % a.cache.page_size / 8; }
 };
 
 // The outputs of the sequences that are out of bounds, where their rows are

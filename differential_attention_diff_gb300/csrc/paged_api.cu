@@ -73,6 +73,8 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   if (c.n_pages == 0 || c.max_pages == 0 || !da::paged_cache_given(c)) return DA_ERR_INVALID_ARG;
   for (const da_t4* t : {&c.k_pages, &c.v_pages})
     if (!ok_stride(t->sb, c.n_pages) || !ok_stride(t->sn, c.page_size) || !ok_stride(t->sh, c.h_kv)) return DA_ERR_INVALID_ARG;
+  // a head's place in a page is counted in blocks of 64 features
+  if (c.h_kv > 1 && (c.k_pages.sh % 64 || c.v_pages.sh % 64)) return DA_ERR_UNSUPPORTED;
   for (const da_t3* t : {&p->q, &p->out})
     if (t->ptr == nullptr || !aligned(t->ptr, 16) || !ok_stride(t->st, c.T) || !ok_stride(t->sh, 2)) return DA_ERR_INVALID_ARG;
   if (p->gate == nullptr) {

@@ -16,11 +16,10 @@
 //   TMEM (512 columns x 128 lanes, lane = row):
 //     [0, 128) S_A (fp32 scores) / P_A (bf16)    [128, 256) S_B / P_B
 //     [256, 384) O_A    [384, 512) O_B            (the first D columns of each)
-//   Shared memory: Q_A, Q_B, K and V rings of two stages, in 128-byte-swizzled
-//   64-column boxes of 128 rows.  A key tile's box is filled page by page: copies
-//   of `box` rows, the largest power of two that divides the page (at most 128),
-//   each from the page that the block table names; the 32 lanes of the producer
-//   warp look up and issue one each.
+//   Shared memory: Q_A, Q_B in 128-byte-swizzled 64-column boxes of 128 rows, K
+//   and V rings of two stages of tiles of pages (paged.cuh), each filled by copies
+//   of `box` rows, the largest power of two that divides the page (at most 128);
+//   the lanes of the producer warp look up and issue one of K and one of V each.
 //
 //   warp 8: TMA producer; warp 9 (one lane): MMA issuer; warps 0-7: softmax and
 //   epilogue, each warpgroup half of a tile's keys (softmax.cuh).
@@ -93,8 +92,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     sh.base = aligned;
     sh.gen = smem_raw + (aligned - raw);
   }
-  constexpr int kNB = D / 64;  // 64-column boxes per tile row
-  constexpr int kOffQ = 0, kOffK = 2 * kNB * kBox, kOffV = 4 * kNB * kBox;
+  using Tile = KeyTile<D>;
+  constexpr int kNB = D / 64;  // 64-column boxes per Q tile
+  constexpr int kOffQ = 0, kOffK = 2 * kNB * kBox, kOffV = kOffK + 2 * Tile::kBytes;
   constexpr uint32_t kIdescPV = idesc_bf16(128, D, 1);  // P (TMEM) x V (MN-major)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -134,9 +134,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
   if (warp == 8) {
     // ------------------------------------------------------ TMA producer --
-    const int nb = kPagedTile / a.box;             // copies per box of 128 rows
-    const int my_r = lane % nb, my_c = lane / nb % kNB, my_v = lane / (nb * kNB);  // this lane's copy
-    const bool mine = lane < 2 * nb * kNB;
+    const PageCopies copies(a, lane);
     // all lanes wait, and all go on or none
     auto wait_warp = [&](uint32_t bar, uint32_t parity, uint32_t site) {
       return __all_sync(0xffffffffu, wait_bar(sh, bar, parity, a.status, site)) != 0;
@@ -144,44 +142,33 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     int kv_it = 0, it = 0;
     bool ok = true;
     for (PagedWalk w(a, share); w.more() && ok; w.next(), ++it) {
-      // the page of this lane's copy of tile j; one behind all pages reads as zeros
-      auto page_of = [&](int j) {
-        const int pos = j * kPagedTile + my_r * a.box;
-        if (!mine || pos >= w.L) return a.cache.n_pages;
-        const int id = a.cache.block_table[static_cast<int64_t>(w.b) * a.cache.max_pages + pos / a.cache.page_size];
-        if (id >= 0 && id < a.cache.n_pages) return id;
-        record_status(a.status, DA_ERR_BOUNDS, 0x0F02);
-        return a.cache.n_pages;
-      };
-      int page = page_of(w.j);
+      int entry = copies.entry(w.b, w.L, w.j);
       if (it > 0) ok = wait_warp(sh.bar(B_QEMPTY), (it - 1) & 1, 0x8001);
       if (ok && lane == 0) {
         const int tiles = two(w) ? 2 : 1;
         mbar_arrive_expect_tx(sh.bar(B_QFULL), tiles * kNB * a.G * a.tq1 * 128);
         for (int s = 0; s < tiles; ++s)
           for (int box = 0; box < kNB; ++box)
-            tma_load_4d(sh.base + kOffQ + (s * kNB + box) * kBox, &tm_q, sh.bar(B_QFULL), box * 64, w.g * a.G,
-                        w.t0 + w.i * a.tq + s * a.tq1, 0);
+            tma_load_3d(sh.base + kOffQ + (s * kNB + box) * kBox, &tm_q, sh.bar(B_QFULL), box * 64, w.g * a.G,
+                        w.t0 + w.i * a.tq + s * a.tq1);
       }
       for (int j = w.j; j < w.j1 && ok; ++j, ++kv_it) {
         const int st = kv_it & 1, use = kv_it >> 1;
-        const int here = page;
-        if (j + 1 < w.j1) page = page_of(j + 1);  // looked up a tile ahead
-        const int slot = (j * kPagedTile + my_r * a.box) % a.cache.page_size;
+        const int page = copies.page(entry, w.L, j), group = copies.group(j);
+        if (j + 1 < w.j1) entry = copies.entry(w.b, w.L, j + 1);  // looked up a tile ahead
+        const uint32_t to = st * Tile::kBytes + Tile::row(copies.row0);
         if (use > 0) ok = wait_warp(sh.bar(B_KEMPTY + st), (use - 1) & 1, 0x8002);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(sh.bar(B_KFULL + st), kNB * kBox);
+        if (lane == 0) mbar_arrive_expect_tx(sh.bar(B_KFULL + st), Tile::kBytes);
         __syncwarp();
-        if (mine && my_v == 0)
-          tma_load_4d(sh.base + kOffK + (st * kNB + my_c) * kBox + my_r * a.box * 128, &tm_k, sh.bar(B_KFULL + st),
-                      my_c * 64, slot, w.g, here);
+        if (copies.mine)
+          tma_load_5d(sh.base + kOffK + to, &tm_k, sh.bar(B_KFULL + st), 0, 0, w.g * copies.k_block, group, page);
         if (use > 0) ok = wait_warp(sh.bar(B_VEMPTY + st), (use - 1) & 1, 0x8003);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(sh.bar(B_VFULL + st), kNB * kBox);
+        if (lane == 0) mbar_arrive_expect_tx(sh.bar(B_VFULL + st), Tile::kBytes);
         __syncwarp();
-        if (mine && my_v == 1)
-          tma_load_4d(sh.base + kOffV + (st * kNB + my_c) * kBox + my_r * a.box * 128, &tm_v, sh.bar(B_VFULL + st),
-                      my_c * 64, slot, w.g, here);
+        if (copies.mine)
+          tma_load_5d(sh.base + kOffV + to, &tm_v, sh.bar(B_VFULL + st), 0, 0, w.g * copies.v_block, group, page);
       }
     }
     if (!ok) {
@@ -199,22 +186,21 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       int kv_it = 0, it = 0;
       uint32_t pc[2] = {0, 0};
       bool ok = true;
-      const uint32_t q0 = sdesc_lo(sh.base + kOffQ, 16), k0 = sdesc_lo(sh.base + kOffK, 16), v0 = sdesc_lo(sh.base + kOffV, kBox);
-      constexpr uint32_t kTile = kNB * kBox >> 4;  // descriptor units (16 bytes) from one tile to the next
+      const uint32_t q0 = sdesc_lo(sh.base + kOffQ, 16), k0 = sdesc_lo(sh.base + kOffK, 16), v0 = sdesc_lo(sh.base + kOffV, 1024);
+      constexpr uint32_t kTile = Tile::kBytes >> 4;  // descriptor units (16 bytes) from one tile (Q, K or V) to the next
       auto issue_s = [&](int s, uint32_t q, uint32_t k) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-          tc_mma_ss_lo(tmem + s * 128, q + off, k + off, kIdescS, kk > 0);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss_lo(tmem + s * 128, q + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), sdesc_hi(1024), k + Tile::feature_step(kk),
+                       Tile::kHi, kIdescS, kk > 0);
         tc_commit(sh.bar(B_SFULL + s));
       };
       auto issue_pv = [&](int s, uint32_t v, bool acc) {
 #pragma unroll
         for (int kk = 0; kk < kPagedTile / 16; ++kk)
           // P of keys 0-63 in columns 0-31 of the S buffer, keys 64-127 in 64-95
-          tc_mma_ts_lo(tmem + 256 + s * 128, tmem + s * 128 + kk * 8 + (kk >= 4 ? 32 : 0), v + (kk * 2048 >> 4), kIdescPV,
-                       (acc || kk > 0) ? 1u : 0u);
+          tc_mma_ts_lo(tmem + 256 + s * 128, tmem + s * 128 + kk * 8 + (kk >= 4 ? 32 : 0), v + Tile::key_step(kk), Tile::kHi,
+                       kIdescPV, (acc || kk > 0) ? 1u : 0u);
       };
       auto full = [&](int bar, int x, uint32_t site) {  // of tile x's stage
         return wait_bar(sh, sh.bar(bar + (x & 1)), (x >> 1) & 1, a.status, site);
@@ -331,9 +317,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           // values behind the sequence's end: zeros
           const int st = (kv_it + x) & 1, r0 = w.L - key0;
           if (!wait_bar(sh, sh.bar(B_VFULL + st), ((kv_it + x) >> 1) & 1, a.status, 0x8203)) ok = false;
-          uint8_t* v = sh.gen + kOffV + st * kNB * kBox;
+          uint8_t* v = sh.gen + kOffV + st * Tile::kBytes;
           for (int e = threadIdx.x; e < (kPagedTile - r0) * 8 * kNB; e += 256)
-            *reinterpret_cast<uint4*>(v + e / ((kPagedTile - r0) * 8) * kBox + r0 * 128 + e % ((kPagedTile - r0) * 8) * 16) =
+            *reinterpret_cast<uint4*>(v + Tile::row(r0 + e / (8 * kNB)) + e % (8 * kNB) / 8 * 1024 + e % 8 * 16) =
                 make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
@@ -501,11 +487,7 @@ template <int D>
 cudaError_t launch_d(const PagedArgs& a, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   const da_paged_cache& c = a.cache;
-  if (!encode_tmap_bf16_box(&tq, a.q.ptr, {D, 2 * a.h, c.T, 1}, {a.q.sh, a.q.st, 0}, {64, a.G, a.tq1, 1}) ||
-      !encode_tmap_bf16_box(&tk, c.k_pages.ptr, {D, c.page_size, c.h_kv, c.n_pages},
-                            {c.k_pages.sn, c.k_pages.sh, c.k_pages.sb}, {64, a.box, 1, 1}) ||
-      !encode_tmap_bf16_box(&tv, c.v_pages.ptr, {D, c.page_size, c.h_kv, c.n_pages},
-                            {c.v_pages.sn, c.v_pages.sh, c.v_pages.sb}, {64, a.box, 1, 1}))
+  if (!encode_queries(&tq, a, a.tq1) || !encode_pages(&tk, c.k_pages, c, a.box) || !encode_pages(&tv, c.v_pages, c, a.box))
     return cudaErrorInvalidValue;
   static OncePerDevice once;
   const cudaError_t e = once.run([] {

@@ -49,17 +49,17 @@ bool encode_tmap_bf16_4d(CUtensorMap* map, const da_t4& t, int B, int N, int H, 
   return r == CUDA_SUCCESS;
 }
 
-bool encode_tmap_bf16_box(CUtensorMap* map, void* ptr, const int64_t (&dims)[4], const int64_t (&strides)[3],
-                          const int (&box)[4]) {
+bool encode_tmap_bf16_box(CUtensorMap* map, void* ptr, int rank, const int64_t* dims, const int64_t* strides,
+                          const int* box) {
   if (!tma_available()) return false;
-  cuuint64_t ext[4], step[3];
-  cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
-  for (int i = 0; i < 4; ++i) {
+  cuuint64_t ext[5], step[4];
+  cuuint32_t bx[5], estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
     ext[i] = static_cast<cuuint64_t>(dims[i]);
     bx[i] = static_cast<cuuint32_t>(box[i]);
   }
-  for (int i = 0; i < 3; ++i) step[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(strides[i]) * 2;
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, ext, step, bx, estr,
+  for (int i = 0; i + 1 < rank; ++i) step[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(strides[i]) * 2;
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, ptr, ext, step, bx, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;

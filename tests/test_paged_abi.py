@@ -91,7 +91,7 @@ def test_paged_append(lib, kw, want):
 @pytest.mark.parametrize("kw,want", CACHE + [
     (dict(h=0), INV), ({"h": 7, "cache.h_kv": 3}, INV), ({"h": 3, "cache.h_kv": 2}, INV), (dict(h=192), UNS), (dict(max_new=-1), INV),
     ({"cache.page_size": 8}, UNS), ({"cache.page_size": 24}, UNS), ({"cache.T": 1 << 30}, UNS),
-    ({"cache.max_pages": 0}, INV), ({"cache.n_pages": 0}, INV), ({"cache.k_pages": t4(sh=0)}, INV),
+    ({"cache.max_pages": 0}, INV), ({"cache.n_pages": 0}, INV), ({"cache.k_pages": t4(sh=0)}, INV), ({"cache.v_pages": t4(sh=136)}, UNS),
     (dict(q=t3(8)), INV), (dict(q=t3(sh=0)), INV), (dict(out=bd.da_t3(None, 0, 0)), INV), (dict(out=t3(st=4)), INV),
     (dict(gate=FAKE + 2), INV), (dict(gate=None), INV), (dict(gate=None, x=FAKE, w_lambda=FAKE, d_model=100), UNS),
     (dict(gate=None, x=FAKE + 8, w_lambda=FAKE, d_model=128), INV), (dict(), WS),
