@@ -231,12 +231,14 @@ struct PagedArgs {
   float* part_o;       // [2 grid, rows, d] unnormalised outputs of the parts
   float* part_ml;      // [2 grid, rows, 2] their maxima (log2 units) and sums
   PagedDesc* desc;     // [grid]
-  int rows;            // of a part: 128 per MMA tile
+  int rows;            // of a part: 128 per MMA tile, or the columns of the kernel for few tokens
   int grid;
   uint32_t* status;
   bool after_gate;     // the kernel launched just before is this call's gate
 };
+constexpr int kPagedDecodeCols = 32;  // the most (token, query head) columns that the kernel for few tokens has
 cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t s);
 
 // ---- V1 decode: split-KV partials of both streams, then merge + RMSNorm ----

@@ -19,15 +19,25 @@ da_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ERR_
 // Strides that TMA copies can take: 16-byte multiples, above 0 where they are used.
 bool ok_stride(int64_t stride, int64_t extent) { return extent <= 1 || (stride > 0 && stride % 8 == 0); }
 
-// How a call's work is cut (paged.cuh).
+// How a call's work is cut (paged.cuh), and by which kernel: sequences whose new
+// tokens fit the columns of the kernel for few tokens read their keys once there;
+// with more the 128-row tiles pay.
 struct Cut {
   int tq, tq1, rows, grid;
+  bool few;
 };
-Cut cut(int G, int sms) {
+Cut cut(int T, int max_new, int G, int sms) {
   Cut c;
-  c.tq1 = 128 / G;
-  c.tq = 2 * c.tq1;
-  c.rows = 256;
+  const int64_t cols = static_cast<int64_t>(max_new > 0 && max_new < T ? max_new : T) * G;
+  c.few = cols <= da::kPagedDecodeCols;
+  if (c.few) {
+    c.rows = cols <= 8 ? 8 : cols <= 16 ? 16 : 32;
+    c.tq = c.tq1 = c.rows / G;
+  } else {
+    c.tq1 = 128 / G;
+    c.tq = 2 * c.tq1;
+    c.rows = 256;
+  }
   c.grid = sms;
   return c;
 }
@@ -52,11 +62,11 @@ extern "C" {
 size_t diffattn_v2_paged_fwd_workspace_size(int T, int B, int max_new, int h, int h_kv, int d, int gate_given) {
   if (T <= 0 || B <= 0 || h <= 0 || h_kv <= 0 || d <= 0 || (2 * static_cast<int64_t>(h)) % h_kv) return 0;
   const int64_t G = 2 * static_cast<int64_t>(h) / h_kv;
-  if (G > 128) return 0;
+  if (G > 128 || max_new < 0) return 0;
   uint32_t* status;
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
-  return space(cut(static_cast<int>(G), sms), T, h, d, gate_given).total;
+  return space(cut(T, max_new, static_cast<int>(G), sms), T, h, d, gate_given).total;
 }
 
 da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
@@ -87,7 +97,7 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   int sms = 152;
   const bool device = da::device_handles(&status, &sms);
   if (!device) sms = 152;  // the workspace is checked first, as the size query would have it
-  const Cut k = cut(static_cast<int>(G), sms);
+  const Cut k = cut(c.T, p->max_new, static_cast<int>(G), sms);
   const Space w = space(k, c.T, p->h, c.d, p->gate != nullptr);
   if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   if (!device || !da::tma_available()) return DA_ERR_CUDA;
@@ -120,7 +130,7 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   a.grid = k.grid;
   a.status = status;
   a.after_gate = p->gate == nullptr;
-  return cuda_status(da::launch_paged_fwd(a, s));
+  return cuda_status(k.few ? da::launch_paged_decode(a, s) : da::launch_paged_fwd(a, s));
 }
 
 }  // extern "C"
