@@ -218,7 +218,8 @@ cudaError_t launch_paged_append(const RopeArgs& a, int d, int sms, cudaStream_t 
 
 // ---- V2 attention over a paged cache --------------------------------------------
 struct PagedDesc {
-  int flags, b, g, i;  // the item that is begun and not ended (paged.cuh)
+  int flags;             // paged.cuh; the rest: the item that is begun and not ended
+  int token, tokens, g;  // its rows of the packed arrays, its KV head
 };
 struct PagedArgs {
   da_paged_cache cache;

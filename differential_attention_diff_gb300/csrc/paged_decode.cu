@@ -432,7 +432,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             *reinterpret_cast<float2*>(a.part_ml + (part + n) * 2) = make_float2(l[n] == 0.f ? -INFINITY : m[n], l[n]);
         }
         if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
-        if (w.begins()) desc = PagedDesc{kPagedOpen, w.b, w.g, w.i};
+        if (w.begins()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       }
     }
     if (r == 0) {

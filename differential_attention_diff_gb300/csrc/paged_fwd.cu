@@ -467,7 +467,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           *reinterpret_cast<float2*>(a.part_ml + (part + s * 128 + row) * 2) = make_float2(m, l);
       }
       if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
-      if (w.begins() && !w.ends()) desc = PagedDesc{kPagedOpen, w.b, w.g, w.i};
+      if (w.begins() && !w.ends()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       tc_fence_before();
     }
     if (threadIdx.x == 0) {

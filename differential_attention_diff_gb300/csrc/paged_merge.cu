@@ -25,7 +25,7 @@ template <int D>
 struct Merge {
   const PagedArgs& a;
   PagedDesc d;
-  int c, parts, t0;
+  int c, parts;
   __device__ __forceinline__ int64_t slot(int i, int row) const {
     return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.rows + row;
   }
@@ -34,7 +34,7 @@ struct Merge {
     return tok / a.tq1 * 128 + tok % a.tq1 * a.G + 2 * (pair % half);
   }
   // of the pair, the output's token row and head
-  __device__ __forceinline__ int64_t token(int pair) const { return t0 + static_cast<int64_t>(d.i) * a.tq + pair / (a.G / 2); }
+  __device__ __forceinline__ int64_t token(int pair) const { return d.token + pair / (a.G / 2); }
   __device__ __forceinline__ int head(int pair) const { return d.g * (a.G / 2) + pair % (a.G / 2); }
   __device__ __forceinline__ __nv_bfloat16* out(int pair, int col) const {
     return static_cast<__nv_bfloat16*>(a.out.ptr) + token(pair) * a.out.st + head(pair) * a.out.sh + col;
@@ -66,18 +66,17 @@ paged_merge_kernel(PagedArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
   if (tid == 0) last = a.grid - 1;
-  cudaGridDependencySynchronize();  // the parts (and, behind them, the gate)
-  Merge<D> mg{a, a.desc[c], c, 0, 0};
-  if (!(mg.d.flags & kPagedOpen)) return;
   __syncthreads();
-  for (int x = c + 1 + tid; x < a.grid; x += kThreads)
-    if (a.desc[x].flags & kPagedEnds) {
-      atomicMin(&last, x);
-      break;
-    }
-  mg.t0 = a.cache.cu_seqlens[mg.d.b];
-  const int n = a.cache.cu_seqlens[mg.d.b + 1] - mg.t0;
-  const int pairs = min(a.tq, n - mg.d.i * a.tq) * (a.G / 2);
+  cudaGridDependencySynchronize();  // the parts (and, behind them, the gate)
+  // the CTA that ends the item: the first of those that follow that ends one
+  const int next = c + 1 + tid;
+  const bool ends = next < a.grid && (a.desc[next].flags & kPagedEnds);
+  Merge<D> mg{a, a.desc[c], c, 0};
+  if (!(mg.d.flags & kPagedOpen)) return;
+  if (ends) atomicMin(&last, next);
+  for (int x = next + kThreads; x < a.grid; x += kThreads)
+    if (a.desc[x].flags & kPagedEnds) atomicMin(&last, x);
+  const int pairs = mg.d.tokens * (a.G / 2);
   __syncthreads();
   const int parts = mg.parts = last - c + 1;
   if (parts <= kFew) {
@@ -85,7 +84,18 @@ paged_merge_kernel(PagedArgs a) {
     for (int pair = blockIdx.y * kWarps + warp; pair < pairs; pair += gridDim.y * kWarps) {
       const int row = mg.row(pair);
       const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
-      float o[2][kPer], iv[2];
+      float x[2][kFew][kPer], o[2][kPer], iv[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          const float* po = a.part_o + mg.slot(i, row + e) * D + lane * kPer;
+          if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(x[e][i]) = i < parts ? *reinterpret_cast<const float4*>(po) : make_float4(0, 0, 0, 0);
+          else
+            *reinterpret_cast<float2*>(x[e][i]) = i < parts ? *reinterpret_cast<const float2*>(po) : make_float2(0, 0);
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float f = part_weight(a.part_ml, mg.slot(lane < parts ? lane : 0, row + e), lane < parts, &iv[e]);
@@ -93,16 +103,9 @@ paged_merge_kernel(PagedArgs a) {
         for (int q = 0; q < kPer; ++q) o[e][q] = 0.f;
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
-          if (i >= parts) break;
           const float w = __shfl_sync(0xffffffffu, f, i);
-          const float* po = a.part_o + mg.slot(i, row + e) * D + lane * kPer;
-          float x[kPer];
-          if constexpr (kPer == 4)
-            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(po);
-          else
-            *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(po);
 #pragma unroll
-          for (int q = 0; q < kPer; ++q) o[e][q] = fmaf(x[q], w, o[e][q]);
+          for (int q = 0; q < kPer; ++q) o[e][q] = i < parts ? fmaf(x[e][i][q], w, o[e][q]) : o[e][q];
         }
       }
       uint32_t y[kPer / 2];
