@@ -50,17 +50,32 @@ __device__ __forceinline__ int64_t tiles_before(int i, int n, int L, int tq) {
   return floor_sum(i, kPagedTile, tq, static_cast<int64_t>(L) - n + tq + kPagedTile - 1);
 }
 
-// Units of sequence b for one KV head, 0 if it is out of bounds (then *bad).
-__device__ __forceinline__ int64_t sequence_units(const da_paged_cache& c, int b, int tq, bool* bad) {
-  const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1], L = c.seqlens[b];
-  if (!paged_sequence_ok(c, t0, t1, L)) {
+// A sequence of the batch as the arrays have it.
+struct PagedSequence {
+  int t0, t1, L;
+  __device__ __forceinline__ void load(const da_paged_cache& c, int b) {
+    t0 = c.cu_seqlens[b];
+    t1 = c.cu_seqlens[b + 1];
+    L = c.seqlens[b];
+  }
+};
+
+// Its units for one KV head, 0 if it is out of bounds (then *bad).
+__device__ __forceinline__ int64_t sequence_units(const da_paged_cache& c, const PagedSequence& s, int tq, bool* bad) {
+  if (!paged_sequence_ok(c, s.t0, s.t1, s.L)) {
     *bad = true;
     return 0;
   }
-  const int n = t1 - t0;
+  const int n = s.t1 - s.t0;
   if (n == 0) return 0;
-  const int64_t last = (L + kPagedTile - 1) / kPagedTile;
-  return n <= tq ? last : tiles_before((n - 1) / tq, n, L, tq) + last;
+  const int64_t last = (s.L + kPagedTile - 1) / kPagedTile;
+  return n <= tq ? last : tiles_before((n - 1) / tq, n, s.L, tq) + last;
+}
+
+// x / y, in 32 bits where that will do (a 64-bit division takes some 100 instructions)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
 
 // Where a CTA's share begins and how long it is.
@@ -70,41 +85,88 @@ struct PagedShare {
   int bad;  // some sequence is out of bounds
 };
 
-// Fills *share (shared memory); called by all kThreads of a block.
+// Fills *share (shared memory); called by all kThreads of a block, with sequence
+// threadIdx.x (where there is one) in `mine`: fetched at the kernel's start, since
+// the rest waits for it.
 template <int kThreads>
-__device__ void paged_share(const PagedArgs& a, PagedShare* share) {
+__device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, PagedShare* share) {
   static_assert(kThreads % 32 == 0, "whole warps");
   constexpr int kW = kThreads / 32;
   __shared__ int64_t sums[kW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.cache.B;
   bool bad = false;
-  int64_t mine = 0, first = 0;  // first: of sequence tid, for a batch of at most kThreads
-  for (int b = tid; b < B; b += kThreads) {
-    const int64_t u = sequence_units(a.cache, b, a.tq, &bad) * a.cache.h_kv;
-    if (b == tid) first = u;
-    mine += u;
+  // inclusive sums over the warp's sequences, and each round's over the warps:
+  // the first round's stay in registers, which for kThreads sequences are all
+  int64_t per = tid < B ? sequence_units(a.cache, mine, a.tq, &bad) : 0;
+  int64_t incl = per * a.cache.h_kv, rest = 0;
+  for (int b = tid + kThreads; b < B; b += kThreads) {
+    PagedSequence s;
+    s.load(a.cache, b);
+    rest += sequence_units(a.cache, s, a.tq, &bad) * a.cache.h_kv;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sums[warp] = mine;
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (B > kThreads) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  }
+  if (lane == 31) sums[warp] = incl;
   const bool any_bad = __syncthreads_or(bad);
-  int64_t total = 0;
-  for (int w = 0; w < kW; ++w) total += sums[w];
-  // shares of less than a tile make no sense
-  const int64_t ctas = total < gridDim.x ? total : gridDim.x;
-  const int64_t c = blockIdx.x;
-  const int64_t u0 = c < ctas ? total * c / ctas : total, u1 = c < ctas ? total * (c + 1) / ctas : total;
+  int64_t before = incl - per * a.cache.h_kv, total = 0;
+#pragma unroll
+  for (int v = 0; v < kW; ++v) {
+    if (v < warp) before += sums[v];
+    total += sums[v];
+  }
+  int64_t base = total;  // of the first round
+  if (B > kThreads) {
+    __syncthreads();
+    if (lane == 0) sums[warp] = rest;
+    __syncthreads();
+    for (int v = 0; v < kW; ++v) total += sums[v];
+  }
+  // equal shares, the first `more` of them one unit longer; less than a unit makes no sense
+  const int64_t ctas = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
+  const int64_t each = ctas ? quotient(total, ctas) : 0, more = total - each * ctas;
+  const int64_t u0 = c * each + (c < more ? c : more), units = c < ctas ? each + (c < more) : 0;
   if (tid == 0) {
-    share->units = u1 - u0;
+    share->units = units;
     share->bad = any_bad;
   }
-  int64_t base = 0;
-  for (int r = 0; r < B && base <= u0 && u0 < u1; r += kThreads) {
-    const int b = r + tid;
-    bool ignore = false;
-    const int64_t w = r == 0 ? first : b < B ? sequence_units(a.cache, b, a.tq, &ignore) * a.cache.h_kv : 0;
-    int64_t incl = w;
+  PagedSequence s = mine;
+  for (int r = 0;;) {
+    const int64_t w = per * a.cache.h_kv;
+    if (units > 0 && u0 >= before && u0 < before + w) {
+      const int n = s.t1 - s.t0;
+      int64_t off = u0 - before;
+      const int g = static_cast<int>(quotient(off, per));
+      off -= g * per;
+      int lo = 0, hi = (n + a.tq - 1) / a.tq;  // the item: the last that begins at or before off
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (tiles_before(mid, n, s.L, a.tq) <= off)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      share->b = r + tid;
+      share->g = g;
+      share->i = lo;
+      share->j = static_cast<int>(off - (lo ? tiles_before(lo, n, s.L, a.tq) : 0));
+    }
+    r += kThreads;
+    if (r >= B || u0 < base || units == 0) break;
+    // the next kThreads sequences
+    per = 0;
+    if (r + tid < B) {
+      s.load(a.cache, r + tid);
+      per = sequence_units(a.cache, s, a.tq, &bad);
+    }
+    incl = per * a.cache.h_kv;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -113,30 +175,10 @@ __device__ void paged_share(const PagedArgs& a, PagedShare* share) {
     __syncthreads();  // sums has been read
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int64_t before = base;
+    before = base + incl - per * a.cache.h_kv;
     for (int v = 0; v < kW; ++v) {
       if (v < warp) before += sums[v];
       base += sums[v];
-    }
-    before += incl - w;
-    if (u0 >= before && u0 < before + w) {
-      const int n = a.cache.cu_seqlens[b + 1] - a.cache.cu_seqlens[b], L = a.cache.seqlens[b];
-      const int64_t per = w / a.cache.h_kv;
-      int64_t off = u0 - before;
-      const int g = static_cast<int>(off / per);
-      off -= g * per;
-      int lo = 0, hi = (n + a.tq - 1) / a.tq;  // the item: the last that begins at or before off
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (tiles_before(mid, n, L, a.tq) <= off)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      share->b = b;
-      share->g = g;
-      share->i = lo;
-      share->j = static_cast<int>(off - (lo ? tiles_before(lo, n, L, a.tq) : 0));
     }
   }
   __syncthreads();

@@ -16,9 +16,10 @@
 //   check that no weight passes 2^64, and the rare one that does raises m.
 //   Every tile's product starts from zero and is added in fp32.
 //
-//   warps 0-3: softmax, sums, epilogue (thread = key of the tile, then feature)
-//   warp 4: TMA producer (queries; K and V page by page, paged.cuh)
-//   warp 5 (one lane): MMA issuer; S of the next tile, the next item's first
+//   a warpgroup or, for C = 32, two with half of the columns each: softmax, sums,
+//     epilogue (thread = key of the tile, then feature)
+//   a warp: TMA producer (queries; K and V page by page, paged.cuh)
+//   a warp (one lane): MMA issuer; S of the next tile, the next item's first
 //     among them, goes ahead of the product of this one
 //   Shared memory: K and V rings (3 stages of 64 KB for D = 128, 6 of 32 KB for
 //   64: what HBM's latency needs in flight), two query tiles, the P buffers.
@@ -33,8 +34,6 @@
 namespace da {
 namespace {
 
-constexpr int kThreads = 192;
-
 // barrier indices (8 bytes each); up to 6 stages
 enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8, B_KFULL = 10, B_KEMPTY = 16, B_VFULL = 22, B_VEMPTY = 28,
        B_COUNT = 34 };
@@ -45,6 +44,11 @@ template <int D, int C>
 struct Cfg {
   using Tile = KeyTile<D>;
   static constexpr int kStages = D == 128 ? 3 : 6;
+  // 32 columns take a warpgroup longer than the memory takes a tile of D = 64
+  // (32 sequences of 4096, 4 tokens x 8 heads: 55 us, 43 with two)
+  static constexpr int kGroups = C == 32 ? 2 : 1;
+  static constexpr int kCols = C / kGroups;              // of a warpgroup
+  static constexpr int kThreads = kGroups * 128 + 64;
   static constexpr int kCq = C < 16 ? 16 : C;            // an MMA has 16 columns at least
   static constexpr int kQBytes = Tile::kNB * kCq * 128;  // boxes of 64 features x kCq rows
   static constexpr int kPBox = 2 * C * 128;              // 64 keys x (C columns hi, C lo)
@@ -88,13 +92,13 @@ __device__ __forceinline__ bool wait_bar(volatile int* abort_flag, uint32_t bar,
   }
 }
 
-// Named barrier 1 over the 128 softmax threads; the second also says whether any passed `pred`.
-__device__ __forceinline__ void sync_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool any_128(bool pred) {
+// A named barrier (1 and up) over a warpgroup; the second also says whether any passed `pred`.
+__device__ __forceinline__ void sync_128(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool any_128(int id, bool pred) {
   uint32_t r;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
                : "=r"(r)
-               : "r"(static_cast<uint32_t>(pred))
+               : "r"(static_cast<uint32_t>(pred)), "r"(id)
                : "memory");
   return r != 0;
 }
@@ -128,12 +132,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
 }
 
 template <int D, int C>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, C>::kThreads, 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, PagedArgs a) {
   using F = Cfg<D, C>;
   using Tile = typename F::Tile;
   constexpr int kS = F::kStages;
+  constexpr int kProducer = F::kGroups * 4, kIssuer = kProducer + 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PagedShare share;
   __shared__ uint32_t tmem_slot;
@@ -145,12 +150,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   float* red = reinterpret_cast<float*>(gen + F::kOffBar + kBarBytes);  // [2][4][C]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  PagedSequence mine;
+  if (threadIdx.x < a.cache.B) mine.load(a.cache, threadIdx.x);
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_QFULL + i), 1);
       mbar_init(bar(B_QEMPTY + i), 1);
       mbar_init(bar(B_SFULL + i), 1);
-      mbar_init(bar(B_PFULL + i), 128);
+      mbar_init(bar(B_PFULL + i), F::kGroups * 128);
       mbar_init(bar(B_OFULL + i), 1);
     }
     for (int i = 0; i < kS; ++i) {
@@ -162,23 +170,23 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kIssuer) {
     tmem_alloc(smem_u32(&tmem_slot), F::kTmem);
     tmem_relinquish();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kProducer && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<kThreads>(a, &share);
+  paged_share<F::kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == 4) {
+  if (warp == kProducer) {
     // ------------------------------------------------------ TMA producer --
     const PageCopies copies(a, lane);
     auto wait_warp = [&](uint32_t b, uint32_t parity, uint32_t site) {
@@ -222,7 +230,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       while (globaltimer() - t0 < 100000000ull) {
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kIssuer) {
     // ------------------------------------------------------- MMA issuer ---
     if (lane == 0) {
       constexpr uint32_t kTile = Tile::kBytes >> 4;
@@ -274,33 +282,39 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
   } else {
     // --------------------------------------------- softmax + epilogue -----
-    // All four warps reach named barrier 1 in the same order: it depends on the
-    // part, the tile and barrier reductions only, and a failed wait leaves at the
-    // end of a part, for all of them.
-    const int r = threadIdx.x;  // key of the tile; TMEM lane; feature of the output
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    // The four warps of a warpgroup reach its named barrier in the same order: it
+    // depends on the part, the tile and barrier reductions only, and a failed wait
+    // leaves at the end of a part, for all of them.
+    constexpr int kC = F::kCols;
+    const int wg = F::kGroups > 1 ? warp >> 2 : 0, q4 = warp & 3, id = 1 + wg;
+    const int n0 = wg * kC;              // the warpgroup's first column
+    const int r = threadIdx.x & 127;     // key of the tile; TMEM lane; feature of the output
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const float sl2 = a.scale_log2;
     // this key's place in a P row: 64 keys to a box, 16-byte pieces swizzled by the row
-    uint8_t* p_key = gen + F::kOffP + (r >> 6) * F::kPBox + (r & 7) * 2;
+    uint8_t* p_key = gen + F::kOffP + (r >> 6) * F::kPBox + (r & 7) * 2 + n0 * 128;
     const int piece = (r & 63) >> 3;
+    red += wg * 8 * kC;                  // [2][4][kC]
     int x = 0, flags = 0, vs = 0;
     uint32_t v_round = 0;
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = false;
     for (PagedWalk w(a, share); w.more(); w.next()) {
-      const int cols = w.tokens * a.G;  // the item's columns
-      float m[C], l[C], o[C];
+      const int cols = w.tokens * a.G - n0;  // the item's columns, from n0 on
+      float m[kC], l[kC], o[kC];
 #pragma unroll
-      for (int n = 0; n < C; ++n) m[n] = l[n] = o[n] = 0.f;
+      for (int n = 0; n < kC; ++n) m[n] = l[n] = o[n] = 0.f;
       // the product of the tile before: O += hi part + lo part
       auto add_product = [&]() {
         if (!wait_bar(&abort_flag, bar(B_OFULL + ((x - 1) & 1)), ((x - 1) >> 1) & 1, a.status, 0x9202)) ok = false;
         tc_fence_after();
-        uint32_t t[2 * C];
-        tmem_ld<2 * C>(tmem + lane_off + F::kTmemO + ((x - 1) & 1) * 2 * C, t);
+        uint32_t hi[kC], lo[kC];
+        const uint32_t t = tmem + lane_off + F::kTmemO + ((x - 1) & 1) * 2 * C + n0;
+        tmem_ld<kC>(t, hi);
+        tmem_ld<kC>(t + C, lo);
         tmem_ld_wait();
 #pragma unroll
-        for (int n = 0; n < C; ++n) o[n] += __uint_as_float(t[n]) + __uint_as_float(t[C + n]);
+        for (int n = 0; n < kC; ++n) o[n] += __uint_as_float(hi[n]) + __uint_as_float(lo[n]);
         tc_fence_before();
       };
       for (int j = w.j; j < w.j1; ++j, ++x) {
@@ -308,50 +322,50 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const bool masked = j * kPagedTile + kPagedTile - 1 > w.first_position();
         if (!wait_bar(&abort_flag, bar(B_SFULL + (x & 1)), (x >> 1) & 1, a.status, 0x9201)) ok = false;
         tc_fence_after();
-        uint32_t s[F::kCq];
-        tmem_ld<F::kCq>(tmem + lane_off + (x & 1) * F::kCq, s);
+        uint32_t s[kC];
+        tmem_ld<kC>(tmem + lane_off + (x & 1) * F::kCq + n0, s);
         tmem_ld_wait();
-        float p[C];
+        float p[kC];
 #pragma unroll
-        for (int n = 0; n < C; ++n) p[n] = __uint_as_float(s[n]) * sl2;
+        for (int n = 0; n < kC; ++n) p[n] = __uint_as_float(s[n]) * sl2;
         if (masked) {
           // column n is token n / G, which sees the keys up to its position
-          const int from = max(0, key - w.first_position()) * a.G;  // columns from here on see the key
+          const int from = max(0, key - w.first_position()) * a.G - n0;  // columns from here on see the key
 #pragma unroll
-          for (int n = 0; n < C; ++n)
+          for (int n = 0; n < kC; ++n)
             if (n < from) p[n] = -INFINITY;
         }
         // the maximum of every column over the tile's keys (between two of these
         // there is always another barrier, so `red` has been read)
-        auto tile_max = [&](float (&mx)[C]) {
+        auto tile_max = [&](float (&mx)[kC]) {
 #pragma unroll
-          for (int n = 0; n < C; ++n) {
+          for (int n = 0; n < kC; ++n) {
             const float v = warp_max(p[n]);
-            if (lane == (n & 31)) red[warp * C + n] = v;
+            if (lane == (n & 31)) red[q4 * kC + n] = v;
           }
-          sync_128();
+          sync_128(id);
 #pragma unroll
-          for (int n = 0; n < C; ++n) {
-            mx[n] = fmaxf(fmaxf(red[n], red[C + n]), fmaxf(red[2 * C + n], red[3 * C + n]));
+          for (int n = 0; n < kC; ++n) {
+            mx[n] = fmaxf(fmaxf(red[n], red[kC + n]), fmaxf(red[2 * kC + n], red[3 * kC + n]));
           }
         };
-        float e[C], scale[C];
+        float e[kC], scale[kC];
         bool raised = false;
         if (j == w.j) {
           tile_max(m);
 #pragma unroll
-          for (int n = 0; n < C; ++n)
+          for (int n = 0; n < kC; ++n)
             if (m[n] == -INFINITY) m[n] = 0.f;  // a column that sees none of these keys sees none behind them
         } else {
           bool over = false;
 #pragma unroll
-          for (int n = 0; n < C; ++n) over |= n < cols && !(p[n] - m[n] <= 64.f);
-          if (any_128(over)) {
-            float mx[C];
+          for (int n = 0; n < kC; ++n) over |= n < cols && !(p[n] - m[n] <= 64.f);
+          if (any_128(id, over)) {
+            float mx[kC];
             tile_max(mx);
             raised = true;
 #pragma unroll
-            for (int n = 0; n < C; ++n) {
+            for (int n = 0; n < kC; ++n) {
               const float mn = fmaxf(m[n], mx[n]);
               scale[n] = exp2f(m[n] - mn);
               m[n] = mn;
@@ -360,11 +374,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           }
         }
 #pragma unroll
-        for (int n = 0; n < C; ++n) {
+        for (int n = 0; n < kC; ++n) {
           e[n] = fast_exp2(p[n] - m[n]);
           l[n] += e[n];
         }
-        if (key >= w.L) {
+        if (key >= w.L && wg == 0) {
           // a value behind the sequence's end may be a NaN, and 0 times it is not 0
           if (!wait_bar(&abort_flag, bar(B_VFULL + vs), v_round & 1, a.status, 0x9203)) ok = false;
           uint8_t* v = gen + F::kOffV + vs * Tile::kBytes + Tile::row(r);
@@ -375,7 +389,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (F::kPBufs == 1 && x > 0 && j > w.j) add_product();  // the P buffer is free once its product is there
         uint8_t* pk = p_key + (x & (F::kPBufs - 1)) * F::kPBytes;
 #pragma unroll
-        for (int n = 0; n < C; ++n) {
+        for (int n = 0; n < kC; ++n) {
           const __nv_bfloat16 hi = __float2bfloat16_rn(e[n]);
           const __nv_bfloat16 lo = __float2bfloat16_rn(e[n] - __bfloat162float(hi));
           *reinterpret_cast<__nv_bfloat16*>(pk + n * 128 + ((piece ^ (n & 7)) << 4)) = hi;
@@ -387,36 +401,36 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (F::kPBufs > 1 && j > w.j) add_product();
         if (raised) {
 #pragma unroll
-          for (int n = 0; n < C; ++n) o[n] *= scale[n];
+          for (int n = 0; n < kC; ++n) o[n] *= scale[n];
         }
         if (++vs == kS) vs = 0, ++v_round;
       }
       // ----------------------------------------------------- epilogue ----
       add_product();
 #pragma unroll
-      for (int n = 0; n < C; ++n) {
+      for (int n = 0; n < kC; ++n) {
         float v = l[n];
 #pragma unroll
         for (int h = 16; h > 0; h /= 2) v += __shfl_xor_sync(0xffffffffu, v, h);
-        if (lane == (n & 31)) red[4 * C + warp * C + n] = v;
+        if (lane == (n & 31)) red[(4 + q4) * kC + n] = v;
       }
       const bool whole = w.begins() && w.ends();
       if (whole && !synced) {
         cudaGridDependencySynchronize();  // the gate
         synced = true;
       }
-      if (any_128(!ok || abort_flag)) {
+      if (any_128(id, !ok || abort_flag)) {
         ok = false;
         break;
       }
 #pragma unroll
-      for (int n = 0; n < C; ++n) l[n] = (red[4 * C + n] + red[5 * C + n]) + (red[6 * C + n] + red[7 * C + n]);
+      for (int n = 0; n < kC; ++n) l[n] = (red[4 * kC + n] + red[5 * kC + n]) + (red[6 * kC + n] + red[7 * kC + n]);
       if (whole) {
         const int half = a.G / 2;
 #pragma unroll
-        for (int n = 0; n < C; n += 2) {
+        for (int n = 0; n < kC; n += 2) {
           if (n < cols && r < D) {
-            const int tok = n / a.G, pair = w.g * half + (n - tok * a.G) / 2;
+            const int tok = (n0 + n) / a.G, pair = w.g * half + (n0 + n - tok * a.G) / 2;
             const int64_t t = w.t0 + static_cast<int64_t>(w.i) * a.tq + tok;
             // the products rounded apart, so that equal heads cancel with gate 1
             const float y = __fsub_rn(__fmul_rn(o[n], 1.f / l[n]), __fmul_rn(o[n + 1], a.gate[t * a.h + pair] / l[n + 1]));
@@ -426,16 +440,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       } else {
         const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.begins() ? 1 : 0)) * a.rows;
 #pragma unroll
-        for (int n = 0; n < C; ++n) {
-          if (n < cols && r < D) a.part_o[(part + n) * D + r] = o[n];
+        for (int n = 0; n < kC; ++n) {
+          if (n < cols && r < D) a.part_o[(part + n0 + n) * D + r] = o[n];
           if (n < cols && r == n)
-            *reinterpret_cast<float2*>(a.part_ml + (part + n) * 2) = make_float2(l[n] == 0.f ? -INFINITY : m[n], l[n]);
+            *reinterpret_cast<float2*>(a.part_ml + (part + n0 + n) * 2) = make_float2(l[n] == 0.f ? -INFINITY : m[n], l[n]);
         }
         if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
         if (w.begins()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       }
     }
-    if (r == 0) {
+    if (threadIdx.x == 0) {
       desc.flags = ok ? desc.flags | flags : 0;
       a.desc[blockIdx.x] = desc;
     }
@@ -445,7 +459,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, F::kTmem);
+  if (warp == kIssuer) tmem_dealloc(tmem, F::kTmem);
 }
 
 template <int D, int C>
@@ -459,7 +473,7 @@ cudaError_t launch_c(const PagedArgs& a, cudaStream_t s) {
     return cudaFuncSetAttribute(paged_decode_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, C>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_ahead(paged_decode_kernel<D, C>, dim3(a.grid), dim3(kThreads), Cfg<D, C>::kSmem, s, a.after_gate, tq, tk, tv, a);
+  return launch_ahead(paged_decode_kernel<D, C>, dim3(a.grid), dim3(Cfg<D, C>::kThreads), Cfg<D, C>::kSmem, s, a.after_gate, tq, tk, tv, a);
 }
 
 template <int D>

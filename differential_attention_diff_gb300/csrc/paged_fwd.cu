@@ -98,6 +98,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   constexpr uint32_t kIdescPV = idesc_bf16(128, D, 1);  // P (TMEM) x V (MN-major)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  PagedSequence mine;
+  if (threadIdx.x < a.cache.B) mine.load(a.cache, threadIdx.x);
+
   if (threadIdx.x == 0) {
     mbar_init(sh.bar(B_QFULL), 1);
     mbar_init(sh.bar(B_QEMPTY), 1);
@@ -122,7 +125,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<kThreads>(a, &share);
+  paged_share<kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();

@@ -146,6 +146,16 @@ def test_swept_shapes():
         check(t, out, scale=scale or None, tag=str(i))
 
 
+@pytest.mark.parametrize("max_new", [2, 0])
+def test_more_sequences_than_threads(max_new):
+    rng = np.random.default_rng(5)
+    L = [int(x) for x in rng.integers(0, 300, 700)]
+    n = [min(x, int(rng.integers(0, 3))) for x in L]
+    n[650], L[650] = 70, 270
+    t = make(n, L, 16, 2, 1, 64)
+    check(t, call(t, max_new=max_new))
+
+
 def test_scores_that_grow():
     """Scores far above the first tile's: the running maximum is raised, O rescaled; and the reverse."""
     for n, L in (([1], [1500]), ([300], [1500]), ([60], [1500])):
