@@ -31,4 +31,17 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return F2(r);
 }
 
+// The same as a value type: {lo, hi} with operators.
+struct F2Pair {
+  unsigned long long v;
+  __device__ __forceinline__ F2Pair() {}
+  __device__ __forceinline__ F2Pair(float lo, float hi) : v(F2(lo, hi).v) {}
+  __device__ __forceinline__ explicit F2Pair(F2 x) : v(x.v) {}
+  __device__ __forceinline__ float lo() const { return __uint_as_float(F2(v).bits().x); }
+  __device__ __forceinline__ float hi() const { return __uint_as_float(F2(v).bits().y); }
+  __device__ __forceinline__ F2Pair operator-() const { return F2Pair(-lo(), -hi()); }
+};
+__device__ __forceinline__ F2Pair operator*(F2Pair a, F2Pair b) { return F2Pair(mul2(F2(a.v), F2(b.v))); }
+__device__ __forceinline__ F2Pair fma2(F2Pair a, F2Pair b, F2Pair c) { return F2Pair(fma2(F2(a.v), F2(b.v), F2(c.v))); }
+
 }  // namespace da

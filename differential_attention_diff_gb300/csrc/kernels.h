@@ -185,29 +185,34 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
 bool evict_moves_unlisted(int64_t units, int L_max, int sms);
 
 // ---- queries and keys normed and rotated; append to a paged cache ---------------
+// Rows of one kind: queries, keys, or (paged) values, which are copied.
+struct RopeKind {
+  int heads;
+  da_t4 src, dst;          // paged: of the packed rows sb is unused, sn the token's stride; k and v go to the pages
+  const float* weight;
+  // set by the launchers: passes over a token's heads, in how many shares; the kind's blocks
+  int passes, chunk_passes, chunks;
+  int64_t units;           // shares of all tokens
+  unsigned block0, blocks;
+};
 struct RopeArgs {
   int64_t tokens;
   int N;                   // tokens are [B, N] (not paged)
-  int h_q, h_k, h_v;       // rows of a token; h_v: copied (paged)
   int rot, interleaved, norm;
   float rope_scale, norm_eps;
-  const float *inv_freq, *q_weight, *k_weight;
+  const float* inv_freq;
   const int* positions;
-  da_t4 q, k, v;           // paged: sb unused, sn the token's stride
-  da_t4 q_out, k_out, v_out;  // paged: k_out, v_out are the pages
+  RopeKind kind[3];
   da_paged_cache cache;    // paged
   uint32_t* status;
-  int chunks, chunk_passes;  // the warps' shares of a token (set by the launchers)
-  int64_t units;
 };
 struct RopeBwdArgs {
-  RopeArgs a;
-  da_t4 dq_out, dk_out, dq, dk;
-  float* part;             // [blocks, 2, d] sums of the weights' gradients, or null
+  RopeArgs a;              // kind[].dst: the gradients to write
+  da_t4 dq_out, dk_out;
+  float* part;             // [blocks, d] sums of the weights' gradients, or null
   float *dq_weight, *dk_weight;
 };
-constexpr int kRopeBwdBlocksPerSm = 4;
-int64_t rope_bwd_blocks(int64_t units, int sms);  // of the backward's grid, for `units` shares of work
+constexpr int kRopeBlocksPerSm = 2;  // of the grid at most; each kind of rows may have one more
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool f32, int sms, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeBwdArgs& g, int d, bool f32, int sms, cudaStream_t s);
 // The checks of a paged cache: sizes and types, then pointers and strides (which

@@ -3,11 +3,19 @@
 // with both applied on the way.
 //
 // Definitions in diffattn.h.  All three stream rows of d features once and are
-// bound by memory; what they must not do is compute angles per row.  A warp
-// takes a token (or a share of its heads, where there are few tokens), computes
-// the token's cosines and sines once, and passes over its rows: d / 8 lanes to a
-// row, each with four pairs of features, so a row's sums take log2(d / 8)
-// shuffles and the rotation none.
+// bound by memory, as long as little else is done per row and enough of them are
+// on their way.  A block takes rows of one kind (queries, keys, or values to
+// copy), so that weights, and the sums of the weights' gradients, stay in its
+// registers; a warp takes a token, or a share of its heads where there are few
+// tokens, computes the token's cosines and sines once, a frequency to a lane, and
+// passes over its rows.  d / F lanes have a row, F = 16 features each (8 where
+// they are fp32, or where rot_dim is no multiple of 16): two pieces of 16 bytes
+// that hold whole pairs, so a row's sums take log2(d / F) shuffles and the
+// rotation none, and two features go through an instruction.  The pieces come by
+// asynchronous copies, each lane its own, kStages groups of rows ahead and across
+// the warp's tokens: 128 KB per SM in flight (192 in the backward).  With rows in
+// registers instead, the backward of 2 x 8192 tokens of 64 + 8 heads, d 128, norm,
+// took 165 us on a GB300 (now 148, 6.1 TB/s; the forward 100, 6.0 TB/s).
 //
 // The angle: position * inv_freq in turns, as a 64-bit fixed-point fraction that
 // wraps by itself (position times 2^64 inv_freq / 2 pi, modulo 2^64).  It is off
@@ -15,13 +23,18 @@
 // ones, and the quarter of the turn comes out of its top bits exactly; what goes
 // to sincospi is at most an eighth of a turn either way.
 #include "common.cuh"
+#include "fp32_pair.cuh"
 #include "kernels.h"
+#include "paged.cuh"
 
 namespace da {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+
+constexpr int kUnroll = 2;      // passes (of 32 / lanes rows) that are a group
+constexpr int kStagesFwd = 4, kStagesBwd = 3;
 
 // 2^64 inv_freq / 2 pi modulo 2^64.  1 / 2 pi in two doubles (the first is it
 // rounded, the second the rest): their product with a 24-bit number is good to
@@ -45,55 +58,110 @@ __device__ __forceinline__ void sincos_turns(uint64_t t, float scale, float& s, 
   c = ((quarter + 1) & 2) ? -b * scale : b * scale;
 }
 
-// Four neighbouring features, as they are stored.
-template <typename T>
-struct Four;
-template <>
-struct Four<__nv_bfloat16> {
-  uint2 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-  __device__ __forceinline__ void set(const float* x) { v = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])); }
-};
-template <>
-struct Four<float> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
-  __device__ __forceinline__ void get(float* x) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
-  __device__ __forceinline__ void set(const float* x) { v = make_float4(x[0], x[1], x[2], x[3]); }
-};
-
-// The features of lane l of a row: four at `a` and four at `b`.  Half layout:
-// features 4l .. and their partners rot / 2 further on; interleaved, or behind
-// rot: eight in a row.  x[i] and x[4 + i], or x[2i] and x[2i + 1], are pair i.
-template <bool kInter>
+// The features of a lane of a row, F of them: F / 2 at `a` and F / 2 at `b`, half
+// of the rotated features (or of those behind them) further on, so that a row's
+// lanes read on end; as stored, and as F / 4 pairs (fp32) of first and of second
+// features of rotation pairs.  Half layout: a holds first features, b their
+// partners; interleaved: each holds whole pairs.
+template <typename T, int D, int F, bool kInter>
 struct Lane {
+  static constexpr int kHalf = F / 2;                              // features of a piece
+  static constexpr int kWords = kHalf * static_cast<int>(sizeof(T)) / 4;  // 2 or 4
+  static constexpr int kPiece = 4 * kWords;                        // bytes of one
+  static constexpr int kSlot = 64 * kPiece;                        // of a warp's pass: two pieces a lane
   bool rotated;
   int a, b;
-  __device__ __forceinline__ Lane(int l, int rot) {
-    rotated = 8 * l < rot;
-    const bool split = !kInter && rotated;
-    a = split ? 4 * l : 8 * l;
-    b = split ? 4 * l + rot / 2 : 8 * l + 4;
+  // this lane's pieces of row p, to its place in a slot
+  __device__ __forceinline__ void fetch(uint32_t slot, const T* p) const {
+    if constexpr (kPiece == 16) {
+      cp_async_16(slot, p + a, 16);
+      cp_async_16(slot + 32 * kPiece, p + b, 16);
+    } else {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(slot), "l"(p + a));
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(slot + 32 * kPiece), "l"(p + b));
+    }
   }
+  __device__ __forceinline__ Lane(int l, int rot) {
+    rotated = F * l < rot;
+    a = rotated ? kHalf * l : rot + kHalf * (l - rot / F);
+    b = a + (rotated ? rot : D - rot) / 2;
+  }
+  struct Raw {
+    uint32_t w[2][kWords];
+    // from a slot of two pieces per lane (`fetch`)
+    __device__ __forceinline__ void load(const uint8_t* slot) {
+      if constexpr (kWords == 4) {
+        *reinterpret_cast<uint4*>(w[0]) = *reinterpret_cast<const uint4*>(slot);
+        *reinterpret_cast<uint4*>(w[1]) = *reinterpret_cast<const uint4*>(slot + 32 * kPiece);
+      } else {
+        *reinterpret_cast<uint2*>(w[0]) = *reinterpret_cast<const uint2*>(slot);
+        *reinterpret_cast<uint2*>(w[1]) = *reinterpret_cast<const uint2*>(slot + 32 * kPiece);
+      }
+    }
+    __device__ __forceinline__ void store(T* p, const Lane& f) const {
+      if constexpr (kWords == 4) {
+        *reinterpret_cast<uint4*>(p + f.a) = *reinterpret_cast<const uint4*>(w[0]);
+        *reinterpret_cast<uint4*>(p + f.b) = *reinterpret_cast<const uint4*>(w[1]);
+      } else {
+        *reinterpret_cast<uint2*>(p + f.a) = *reinterpret_cast<const uint2*>(w[0]);
+        *reinterpret_cast<uint2*>(p + f.b) = *reinterpret_cast<const uint2*>(w[1]);
+      }
+    }
+    // feature i of the lane's F, from a's first to b's last
+    __device__ __forceinline__ float at(int i) const {
+      if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(w[i / kHalf][i % kHalf]);
+      } else {
+        const uint32_t x = w[i / kHalf][i % kHalf / 2];
+        return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+      }
+    }
+    __device__ __forceinline__ void put(int i, float lo, float hi) {  // features i and i + 1 (i even)
+      if constexpr (sizeof(T) == 4) {
+        w[i / kHalf][i % kHalf] = __float_as_uint(lo);
+        w[i / kHalf][i % kHalf + 1] = __float_as_uint(hi);
+      } else {
+        w[i / kHalf][i % kHalf / 2] = pack_bf16x2(lo, hi);
+      }
+    }
+  };
+  // the lane's index of the first / second feature of its rotation pair i
   __device__ static __forceinline__ constexpr int u(int i) { return kInter ? 2 * i : i; }
-  __device__ static __forceinline__ constexpr int v(int i) { return kInter ? 2 * i + 1 : 4 + i; }
+  __device__ static __forceinline__ constexpr int v(int i) { return kInter ? 2 * i + 1 : kHalf + i; }
+  __device__ static __forceinline__ void get(const Raw& r, F2Pair (&x)[F / 2]) {
+#pragma unroll
+    for (int i = 0; i < F / 4; ++i) {
+      x[i] = {r.at(u(2 * i)), r.at(u(2 * i + 1))};
+      x[F / 4 + i] = {r.at(v(2 * i)), r.at(v(2 * i + 1))};
+    }
+  }
+  __device__ static __forceinline__ void put(Raw& r, const F2Pair (&x)[F / 2]) {
+#pragma unroll
+    for (int i = 0; i < F / 4; ++i) {
+      if constexpr (kInter) {
+        r.put(4 * i, x[i].lo(), x[F / 4 + i].lo());
+        r.put(4 * i + 2, x[i].hi(), x[F / 4 + i].hi());
+      } else {
+        r.put(2 * i, x[i].lo(), x[i].hi());
+        r.put(kHalf + 2 * i, x[F / 4 + i].lo(), x[F / 4 + i].hi());
+      }
+    }
+  }
+  // where pair-array entry e, half h is among the row's features
+  __device__ __forceinline__ int feature(int e, int h) const {
+    const int i = e < F / 4 ? u(2 * e + h) : v(2 * (e - F / 4) + h);
+    return i < kHalf ? a + i : b + i - kHalf;
+  }
 };
 
-template <bool kInter>
-__device__ __forceinline__ void rotate(float* x, const float* c, const float* s) {
+// (u, v) turned: u c - v s, v c + u s
+template <int P>
+__device__ __forceinline__ void rotate(F2Pair (&x)[2 * P], const F2Pair (&c)[P], const F2Pair (&s)[P]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float p = x[Lane<kInter>::u(i)], q = x[Lane<kInter>::v(i)];
-    x[Lane<kInter>::u(i)] = p * c[i] - q * s[i];
-    x[Lane<kInter>::v(i)] = q * c[i] + p * s[i];
+  for (int i = 0; i < P; ++i) {
+    const F2Pair u = x[i], v = x[P + i];
+    x[i] = fma2(-v, s[i], u * c[i]);
+    x[P + i] = fma2(u, s[i], v * c[i]);
   }
 }
 
@@ -104,14 +172,46 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ void load_weight(const float* w, int a, int b, float* out) {
-  if (w == nullptr) {
+template <int P>
+__device__ __forceinline__ float square_sum(const F2Pair (&x)[P]) {
+  F2Pair s = x[0] * x[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = 1.f;
-    return;
+  for (int i = 1; i < P; ++i) s = fma2(x[i], x[i], s);
+  return s.lo() + s.hi();
+}
+
+// A token's cosines and sines, a frequency to a lane, left in shared memory for
+// the lanes that have its pairs.  `sign` turns the other way.
+__device__ __forceinline__ void token_angles(const RopeArgs& a, const uint64_t* freq, int pos, float sign, float* cs, int stride, int lane) {
+  __syncwarp();
+  for (int i = lane; i < a.rot / 2; i += 32) {
+    float s, c;
+    sincos_turns(static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq[i], a.rope_scale, s, c);
+    cs[i] = c;
+    cs[stride + i] = s * sign;
   }
+  __syncwarp();
+}
+
+// The lane's: of its pairs 0 .. 2P - 1, half layout on end from 2P l; interleaved
+// the first P from P l, the others rot / 4 further on.
+template <int P, bool kInter>
+__device__ __forceinline__ void load_angles(const float* cs, int stride, int l, int rot, F2Pair (&c)[P], F2Pair (&s)[P]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = __ldg(w + a + i), out[4 + i] = __ldg(w + b + i);
+  for (int i = 0; i < P; ++i) {
+    const int at = kInter ? P * l + 2 * i + (2 * i >= P ? rot / 4 - P : 0) : 2 * P * l + 2 * i;
+    const float2 x = *reinterpret_cast<const float2*>(cs + at);
+    const float2 y = *reinterpret_cast<const float2*>(cs + stride + at);
+    c[i] = {x.x, x.y};
+    s[i] = {y.x, y.y};
+  }
+}
+
+template <int F, class L>
+__device__ __forceinline__ void load_weight(const float* w, const L& f, F2Pair (&out)[F / 2]) {
+#pragma unroll
+  for (int e = 0; e < F / 2; ++e)
+    out[e] = w == nullptr ? F2Pair{1.f, 1.f} : F2Pair{__ldg(w + f.feature(e, 0)), __ldg(w + f.feature(e, 1))};
 }
 
 template <typename T>
@@ -134,303 +234,379 @@ __device__ __forceinline__ int sequence_of(const int* cu, int B, int t, int lane
   return lo;
 }
 
-// Whether a sequence's rows and length are within bounds (diffattn.h).
-__device__ __forceinline__ bool sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
-  return t0 >= 0 && t0 <= t1 && t1 <= c.T && L >= t1 - t0 && L <= static_cast<int64_t>(c.max_pages) * c.page_size;
+// The kind of rows that this block has.
+__device__ __forceinline__ int block_kind(const RopeArgs& a) {
+  return blockIdx.x < a.kind[1].block0 ? 0 : blockIdx.x < a.kind[2].block0 ? 1 : 2;
 }
 
-template <typename T, int D, bool kInter, bool kPaged>
-__global__ void __launch_bounds__(kThreads)
-rope_rows_kernel(RopeArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes to a row, rows to a warp's pass
-  constexpr int kUnroll = 4;
+// A warp's way through its shares of tokens (units), a group of kUnroll passes at
+// a time.  One runs ahead to fetch, one follows.
+struct Way {
+  const RopeKind& kd;
+  int64_t unit;
+  int t, p, p1;  // token, first pass of the group, end of the share
+  bool fresh;    // the group is a share's first
+  __device__ __forceinline__ Way(const RopeKind& kd_, int warp) : kd(kd_), unit(static_cast<int64_t>(blockIdx.x - kd_.block0) * kWarps + warp) { share(); }
+  __device__ __forceinline__ bool more() const { return unit < kd.units; }
+  __device__ __forceinline__ int64_t stride() const { return static_cast<int64_t>(kd.blocks) * kWarps; }
+  __device__ __forceinline__ int token(int64_t u) const { return static_cast<int>(kd.chunks == 1 ? u : u / kd.chunks); }
+  __device__ __forceinline__ void share() {
+    t = token(unit);
+    p = static_cast<int>(unit - static_cast<int64_t>(t) * kd.chunks) * kd.chunk_passes;
+    p1 = min(kd.passes, p + kd.chunk_passes);
+    fresh = true;
+  }
+  __device__ __forceinline__ void next() {
+    p += kUnroll;
+    fresh = false;
+    if (p < p1) return;
+    unit += stride();
+    if (more()) share();
+  }
+};
+
+// Whether the pass has a row of this lane, and its head.
+template <int kRows>
+__device__ __forceinline__ bool has_row(const Way& w, int u, int sub, int* h) {
+  *h = (w.p + u) * kRows + sub;
+  return w.p + u < w.p1 && *h < w.kd.heads;
+}
+
+// A token's place: its rotation's position and where its rows go, as far as they
+// are loaded and not looked at (a share ahead of their use).
+struct Place {
+  int pos, page, j;  // paged: the entry of the block table and the position; page_ok's and page's
+  bool ok;
+};
+template <bool kPaged>
+__device__ __forceinline__ Place place_of(const RopeArgs& a, int which, int t, int lane) {
+  Place r{0, 0, 0, true};
+  if constexpr (kPaged) {
+    const da_paged_cache& c = a.cache;
+    const int b = sequence_of(c.cu_seqlens, c.B, t, lane);
+    const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1], len = c.seqlens[b];
+    // else padding, or a sequence that is out of bounds
+    r.ok = t >= t0 && t < t1 && paged_sequence_ok(c, t0, t1, len);
+    if (r.ok) {
+      r.j = len - t1 + t;
+      r.pos = a.positions ? a.positions[t] : r.j;
+      if (which > 0) r.page = c.block_table[static_cast<int64_t>(b) * c.max_pages + r.j / c.page_size];
+    }
+  } else {
+    r.pos = a.positions ? a.positions[t] : t % a.N;
+  }
+  return r;
+}
+
+template <typename T, int D, int F, bool kInter, bool kPaged>
+__global__ void __launch_bounds__(kThreads, kRopeBlocksPerSm)
+rope_rows_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = D / F, kRows = 32 / kLanes;  // lanes to a row, rows to a warp's pass
+  using L = Lane<T, D, F, kInter>;
+  extern __shared__ __align__(16) uint8_t ring[];     // [warp][stage][pass][two pieces of every lane]
   __shared__ uint64_t freq[D / 2];
+  __shared__ __align__(16) float angles[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
+  const int which = block_kind(a);
+  const RopeKind& kd = a.kind[which];
+  const bool turned = which < 2;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  const L f(l, a.rot);
+  uint8_t* mine = ring + warp * kStagesFwd * kUnroll * L::kSlot + lane * L::kPiece;
+  const uint32_t mine_s = smem_u32(mine);
+  Way ahead(kd, warp);
+  auto fetch = [&](int st) {
+    if (ahead.more()) {
+      const T* from = kPaged ? at<T>(kd.src, 0, ahead.t) : at<T>(kd.src, ahead.t / a.N, ahead.t % a.N);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        int h;
+        if (has_row<kRows>(ahead, u, sub, &h)) f.fetch(mine_s + (st * kUnroll + u) * L::kSlot, from + h * kd.src.sh);
+      }
+      ahead.next();
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < kStagesFwd - 1; ++st) fetch(st);
+  for (int i = threadIdx.x; turned && i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
   if constexpr (kPaged) {
     const da_paged_cache& c = a.cache;
     for (int b = threadIdx.x; blockIdx.x == 0 && b < c.B; b += kThreads)
-      if (!sequence_ok(c, c.cu_seqlens[b], c.cu_seqlens[b + 1], c.seqlens[b])) record_status(a.status, DA_ERR_BOUNDS, 0x0E01);
+      if (!paged_sequence_ok(c, c.cu_seqlens[b], c.cu_seqlens[b + 1], c.seqlens[b])) record_status(a.status, DA_ERR_BOUNDS, 0x0E01);
   }
   __syncthreads();
-  const int l = lane % kLanes, sub = lane / kLanes;
-  const Lane<kInter> f(l, a.rot);
-  const int passes[3] = {(a.h_q + kRows - 1) / kRows, (a.h_k + kRows - 1) / kRows, (a.h_v + kRows - 1) / kRows};
-  const int heads[3] = {a.h_q, a.h_k, a.h_v};
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < a.units;
-       unit += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int t = static_cast<int>(unit / a.chunks), chunk = static_cast<int>(unit % a.chunks);
-    int64_t sb = 0, sn = t, db = 0, dn = t;  // the rows' place in the sources and in q_out
-    int64_t page = 0, slot = 0;
-    bool paged_ok = true;
-    int pos;
-    if constexpr (kPaged) {
-      const da_paged_cache& c = a.cache;
-      const int b = sequence_of(c.cu_seqlens, c.B, t, lane);
-      const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1], L = c.seqlens[b];
-      // padding, or a sequence that is out of bounds
-      if (t < t0 || t >= t1 || !sequence_ok(c, t0, t1, L)) continue;
-      const int j = L - t1 + t;
-      const int id = c.block_table[static_cast<int64_t>(b) * c.max_pages + j / c.page_size];
-      paged_ok = id >= 0 && id < c.n_pages;
-      if (!paged_ok && lane == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0E02);
-      page = id;
-      slot = j % c.page_size;
-      pos = a.positions ? a.positions[t] : j;
-    } else {
-      sb = db = t / a.N;
-      sn = dn = t % a.N;
-      pos = a.positions ? a.positions[t] : static_cast<int>(sn);
-    }
-    float co[4], si[4];
-    if (f.rotated) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sincos_turns(static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq[4 * l + i], a.rope_scale, si[i], co[i]);
-    }
-    const int p0 = chunk * a.chunk_passes, p1 = p0 + a.chunk_passes;
-    int base = 0;
-#pragma unroll
-    for (int kind = 0; kind < (kPaged ? 3 : 2); ++kind) {
-      const int lo = max(p0, base), hi = min(p1, base + passes[kind]);
-      if (lo < hi && (kind == 0 || paged_ok)) {
-        const da_t4& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-        const da_t4& dst = kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out;
-        const T* from = at<T>(src, sb, sn);
-        T* to = kPaged && kind > 0 ? at<T>(dst, page, slot) : at<T>(dst, db, dn);
-        float w[8];
-        if (a.norm && kind < 2) load_weight(kind == 0 ? a.q_weight : a.k_weight, f.a, f.b, w);
-        for (int p = lo; p < hi; p += kUnroll) {
-          Four<T> xa[kUnroll], xb[kUnroll];
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            const int h = (p + u - base) * kRows + sub;
-            if (p + u < hi && h < heads[kind]) {
-              xa[u].load(from + h * src.sh + f.a);
-              xb[u].load(from + h * src.sh + f.b);
-            } else {
-              xa[u].v = {};
-              xb[u].v = {};
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            if (p + u >= hi) break;
-            const int h = (p + u - base) * kRows + sub;
-            if (kind < 2) {
-              float x[8];
-              xa[u].get(x);
-              xb[u].get(x + 4);
-              if (a.norm) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-                const float r = rsqrtf(row_sum<kLanes>(ss) * (1.f / D) + a.norm_eps);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-              }
-              if (f.rotated) rotate<kInter>(x, co, si);
-              xa[u].set(x);
-              xb[u].set(x + 4);
-            }
-            if (h < heads[kind]) {
-              xa[u].store(to + h * dst.sh + f.a);
-              xb[u].store(to + h * dst.sh + f.b);
-            }
-          }
+  const bool norm = a.norm && turned;
+  F2Pair w[F / 2], co[F / 4], si[F / 4];
+  if (norm) load_weight<F>(kd.weight, f, w);
+  int st = 0;
+  Place place{}, next{};
+  T* to = nullptr;
+  Way way(kd, warp);
+  if (way.more()) next = place_of<kPaged>(a, which, way.t, lane);
+  for (; way.more(); way.next(), st = st + 1 == kStagesFwd ? 0 : st + 1) {
+    fetch(st == 0 ? kStagesFwd - 1 : st - 1);
+    if (way.fresh) {
+      place = next;
+      if (way.unit + way.stride() < kd.units) next = place_of<kPaged>(a, which, way.token(way.unit + way.stride()), lane);
+      if constexpr (kPaged) {
+        if (place.ok && which > 0 && (place.page < 0 || place.page >= a.cache.n_pages)) {
+          if (lane == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0E02);
+          place.ok = false;
         }
+        to = which > 0 ? at<T>(kd.dst, place.page, place.j % a.cache.page_size) : at<T>(kd.dst, 0, way.t);
+      } else {
+        to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
       }
-      base += passes[kind];
+      if (turned && a.rot) {
+        token_angles(a, freq, place.pos, 1.f, angles[warp], D / 2, lane);
+        if (f.rotated) load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
+      }
+    }
+    cp_async_wait<kStagesFwd - 1>();
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (way.p + u >= way.p1) break;
+      int h;
+      const bool row = has_row<kRows>(way, u, sub, &h);
+      typename L::Raw x;
+      x.load(mine + (st * kUnroll + u) * L::kSlot);
+      if (turned) {
+        F2Pair y[F / 2];
+        L::get(x, y);
+        if (norm) {
+          const float r = rsqrtf(row_sum<kLanes>(square_sum(y)) * (1.f / D) + a.norm_eps);
+#pragma unroll
+          for (int e = 0; e < F / 2; ++e) y[e] = y[e] * F2Pair{r, r} * w[e];
+        }
+        if (f.rotated) rotate(y, co, si);
+        L::put(x, y);
+      }
+      if (row && place.ok) x.store(to + h * kd.dst.sh, f);
     }
   }
+  cp_async_wait<0>();
 }
 
 // The gradients.  The weights' are summed by each lane over its rows in fp32
 // (some hundred to a few thousand of them), over a block's lanes and warps in a
 // fixed order, and over the blocks by the kernel below in fp64.
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads)
-rope_bwd_kernel(RopeBwdArgs g) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  constexpr int kUnroll = 2;
+template <typename T, int D, int F, bool kInter>
+__global__ void __launch_bounds__(kThreads, kRopeBlocksPerSm)
+rope_bwd_kernel(const __grid_constant__ RopeBwdArgs g) {
+  constexpr int kLanes = D / F, kRows = 32 / kLanes;
+  using L = Lane<T, D, F, kInter>;
   const RopeArgs& a = g.a;
+  extern __shared__ __align__(16) uint8_t ring[];     // [warp][stage][pass][x, dy][two pieces of every lane]
   __shared__ uint64_t freq[D / 2];
-  __shared__ float sums[kWarps][2][D];
+  __shared__ __align__(16) float angles[kWarps][D];  // and the warps' sums at the end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
-  __syncthreads();
+  const int which = block_kind(a);
+  const RopeKind& kd = a.kind[which];
+  const da_t4& gy = which == 0 ? g.dq_out : g.dk_out;  // (kd.dst: dq or dk)
   const int l = lane % kLanes, sub = lane / kLanes;
-  const Lane<kInter> f(l, a.rot);
-  const int passes[2] = {(a.h_q + kRows - 1) / kRows, (a.h_k + kRows - 1) / kRows};
-  const int heads[2] = {a.h_q, a.h_k};
-  float acc[2][8];
+  const L f(l, a.rot);
+  uint8_t* mine = ring + warp * kStagesBwd * kUnroll * 2 * L::kSlot + lane * L::kPiece;
+  const uint32_t mine_s = smem_u32(mine);
+  Way ahead(kd, warp);
+  auto fetch = [&](int st) {
+    if (ahead.more()) {
+      const int b = ahead.t / a.N, n = ahead.t - b * a.N;
+      const T* xp = at<T>(kd.src, b, n);
+      const T* yp = at<T>(gy, b, n);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < a.units;
-       unit += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int t = static_cast<int>(unit / a.chunks), chunk = static_cast<int>(unit % a.chunks);
-    const int b = t / a.N, n = t % a.N;
-    const int pos = a.positions ? a.positions[t] : n;
-    float co[4], si[4];
-    if (f.rotated) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sincos_turns(static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq[4 * l + i], a.rope_scale, si[i], co[i]);
-        si[i] = -si[i];
-      }
-    }
-    const int p0 = chunk * a.chunk_passes, p1 = p0 + a.chunk_passes;
-    int base = 0;
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const int lo = max(p0, base), hi = min(p1, base + passes[kind]);
-      if (lo < hi) {
-        const da_t4& x_ = kind == 0 ? a.q : a.k;
-        const da_t4& dy_ = kind == 0 ? g.dq_out : g.dk_out;
-        const da_t4& dx_ = kind == 0 ? g.dq : g.dk;
-        const T* xp = a.norm ? at<T>(x_, b, n) : nullptr;
-        const T* dyp = at<T>(dy_, b, n);
-        T* dxp = at<T>(dx_, b, n);
-        float w[8];
-        if (a.norm) load_weight(kind == 0 ? a.q_weight : a.k_weight, f.a, f.b, w);
-        for (int p = lo; p < hi; p += kUnroll) {
-          Four<T> xa[kUnroll], xb[kUnroll], ya[kUnroll], yb[kUnroll];
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            const int h = (p + u - base) * kRows + sub;
-            xa[u].v = xb[u].v = ya[u].v = yb[u].v = {};
-            if (p + u < hi && h < heads[kind]) {
-              ya[u].load(dyp + h * dy_.sh + f.a);
-              yb[u].load(dyp + h * dy_.sh + f.b);
-              if (a.norm) {
-                xa[u].load(xp + h * x_.sh + f.a);
-                xb[u].load(xp + h * x_.sh + f.b);
-              }
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            if (p + u >= hi) break;
-            const int h = (p + u - base) * kRows + sub;
-            float dz[8];
-            ya[u].get(dz);
-            yb[u].get(dz + 4);
-            if (f.rotated) rotate<kInter>(dz, co, si);
-            if (a.norm) {
-              float x[8];
-              xa[u].get(x);
-              xb[u].get(x + 4);
-              float ss = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-              const float r = rsqrtf(row_sum<kLanes>(ss) * (1.f / D) + a.norm_eps);
-              float m = 0.f;
-              const bool row = h < heads[kind];  // a row that is not there is zeros; with norm_eps 0 its r is infinite
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                x[i] *= r;
-                if (row) acc[kind][i] = fmaf(dz[i], x[i], acc[kind][i]);
-                dz[i] *= w[i];
-                m = fmaf(dz[i], x[i], m);
-              }
-              m = row_sum<kLanes>(m) * (1.f / D);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dz[i] = r * (dz[i] - x[i] * m);
-            }
-            if (h < heads[kind]) {
-              xa[u].set(dz);
-              xb[u].set(dz + 4);
-              xa[u].store(dxp + h * dx_.sh + f.a);
-              xb[u].store(dxp + h * dx_.sh + f.b);
-            }
-          }
+      for (int u = 0; u < kUnroll; ++u) {
+        int h;
+        if (has_row<kRows>(ahead, u, sub, &h)) {
+          const uint32_t slot = mine_s + (st * kUnroll + u) * 2 * L::kSlot;
+          f.fetch(slot + L::kSlot, yp + h * gy.sh);
+          if (a.norm) f.fetch(slot, xp + h * kd.src.sh);
         }
       }
-      base += passes[kind];
+      ahead.next();
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < kStagesBwd - 1; ++st) fetch(st);
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
+  __syncthreads();
+  F2Pair w[F / 2], co[F / 4], si[F / 4], acc[F / 2];
+  if (a.norm) load_weight<F>(kd.weight, f, w);
+#pragma unroll
+  for (int e = 0; e < F / 2; ++e) acc[e] = {0.f, 0.f};
+  int st = 0;
+  Place next{};
+  T* to = nullptr;
+  Way way(kd, warp);
+  if (way.more()) next = place_of<false>(a, which, way.t, lane);
+  for (; way.more(); way.next(), st = st + 1 == kStagesBwd ? 0 : st + 1) {
+    fetch(st == 0 ? kStagesBwd - 1 : st - 1);
+    if (way.fresh) {
+      const Place place = next;
+      if (way.unit + way.stride() < kd.units) next = place_of<false>(a, which, way.token(way.unit + way.stride()), lane);
+      to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
+      if (a.rot) {
+        token_angles(a, freq, place.pos, -1.f, angles[warp], D / 2, lane);
+        if (f.rotated) load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
+      }
+    }
+    cp_async_wait<kStagesBwd - 1>();
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (way.p + u >= way.p1) break;
+      int h;
+      const bool row = has_row<kRows>(way, u, sub, &h);
+      const uint8_t* slot = mine + (st * kUnroll + u) * 2 * L::kSlot;
+      typename L::Raw x;
+      x.load(slot + L::kSlot);
+      F2Pair dz[F / 2];
+      L::get(x, dz);
+      if (f.rotated) rotate(dz, co, si);
+      if (a.norm) {
+        F2Pair xh[F / 2];
+        x.load(slot);
+        L::get(x, xh);
+        const float r = rsqrtf(row_sum<kLanes>(square_sum(xh)) * (1.f / D) + a.norm_eps);
+        F2Pair m{0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < F / 2; ++e) {
+          xh[e] = xh[e] * F2Pair{r, r};
+          if (row) acc[e] = fma2(dz[e], xh[e], acc[e]);  // where there is none the slot holds anything
+          dz[e] = dz[e] * w[e];
+          m = fma2(dz[e], xh[e], m);
+        }
+        const float mean = row_sum<kLanes>(m.lo() + m.hi()) * (-1.f / D);
+#pragma unroll
+        for (int e = 0; e < F / 2; ++e) dz[e] = fma2(xh[e], F2Pair{mean, mean}, dz[e]) * F2Pair{r, r};
+      }
+      if (row) {
+        L::put(x, dz);
+        x.store(to + h * kd.dst.sh, f);
+      }
     }
   }
+  cp_async_wait<0>();
   if (g.part == nullptr) return;
+  __syncthreads();
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
+  for (int e = 0; e < F / 2; ++e) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x = acc[kind][i];
+    for (int half = 0; half < 2; ++half) {
+      float x = half ? acc[e].hi() : acc[e].lo();
 #pragma unroll
       for (int o = kLanes; o < 32; o *= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (sub == 0) sums[warp][kind][(i < 4 ? f.a : f.b) + (i & 3)] = x;
+      if (sub == 0) angles[warp][f.feature(e, half)] = x;
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += sums[w][i / D][i % D];
-    g.part[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = x;
+    for (int v = 0; v < kWarps; ++v) x += angles[v][i];
+    g.part[static_cast<int64_t>(blockIdx.x) * D + i] = x;
   }
 }
 
-// dq_weight and dk_weight [d] from the blocks' sums [blocks, 2, d]: a block per 32
-// features, its eight warps a share of the blocks each.
-__global__ void __launch_bounds__(256) rope_dw_kernel(const float* part, int blocks, int d, float* dq_weight, float* dk_weight) {
-  __shared__ double sums[8][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 32 + lane;
+// dq_weight and dk_weight [d] from the blocks' sums [blocks, d], those of the
+// queries' blocks first: a block per 8 features of one of them, an 8-lane group
+// per share of the kind's blocks, added in their order.
+__global__ void __launch_bounds__(256) rope_dw_kernel(const float* part, int q_blocks, int blocks, int d, float* dq_weight, float* dk_weight) {
+  __shared__ double sums[32][8];
+  const int group = threadIdx.x / 8, k = threadIdx.x % 8;
+  const bool keys = static_cast<int>(blockIdx.x) >= d / 8;
+  const int i = (blockIdx.x - (keys ? d / 8 : 0)) * 8 + k;
+  const int lo = keys ? q_blocks : 0, hi = keys ? blocks : q_blocks;
   double x = 0.0;
   cudaGridDependencySynchronize();
 #pragma unroll 4
-  for (int b = warp; b < blocks; b += 8) x += static_cast<double>(part[static_cast<int64_t>(b) * 2 * d + i]);
-  sums[warp][lane] = x;
+  for (int b = lo + group; b < hi; b += 32) x += static_cast<double>(part[static_cast<int64_t>(b) * d + i]);
+  sums[group][k] = x;
   __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < 8; ++w) x += sums[w][lane];
-    float* out = i < d ? dq_weight : dk_weight;
-    if (out) out[i < d ? i : i - d] = static_cast<float>(x);
+  if (group == 0) {
+    for (int v = 1; v < 32; ++v) x += sums[v][k];
+    float* out = keys ? dk_weight : dq_weight;
+    if (out) out[i] = static_cast<float>(x);
   }
 }
 
-// The warps' shares: a token each where there are enough of them to fill the
-// SMs' warps, else some passes of a token's heads (at least one).
-void share(RopeArgs& a, int d, int warps) {
-  const int rows = 256 / d;
-  const int64_t passes = (a.h_q + rows - 1) / rows + (a.h_k + rows - 1) / rows + (a.h_v + rows - 1) / rows;
-  int64_t each = a.tokens * passes / warps;
-  each = each < 1 ? 1 : each > passes ? passes : each;
-  a.chunk_passes = static_cast<int>(each);
-  a.chunks = static_cast<int>((passes + each - 1) / each);
-  a.units = a.tokens * a.chunks;
+// The kinds' blocks, in proportion to what their rows cost, and the warps' shares:
+// a token each where there are enough of them to fill the SMs' warps, else some
+// passes of a token's heads (at least one).  A token costs its passes, its angles
+// about two more, and finding its page one (2 x 8192 tokens of 64 + 8 heads: 133
+// us in proportion to the passes alone, 100 with the angles; six prompts appended:
+// 134 us without the page's, 113 with it).  Returns the grid.
+unsigned share(RopeArgs& a, int rows, int sms) {
+  const bool paged = a.cache.B > 0;
+  const int64_t warps = static_cast<int64_t>(sms) * kRopeBlocksPerSm * kWarps;
+  int64_t passes = 0, cost[3], all = 0;
+  for (int i = 0; i < 3; ++i) {
+    RopeKind& k = a.kind[i];
+    k.passes = (k.heads + rows - 1) / rows;
+    cost[i] = k.passes ? k.passes + (i < 2 ? 2 : 0) + (paged ? 1 : 0) : 0;
+    passes += k.passes;
+    all += cost[i];
+  }
+  int64_t each = a.tokens * passes / warps;  // passes to a warp
+  if (each < 1) each = 1;
+  unsigned grid = 0;
+  for (int i = 0; i < 3; ++i) {
+    RopeKind& k = a.kind[i];
+    k.block0 = grid;
+    k.chunk_passes = static_cast<int>(each < k.passes ? each : k.passes);
+    k.chunks = k.passes ? (k.passes + k.chunk_passes - 1) / k.chunk_passes : 0;
+    k.units = a.tokens * k.chunks;
+    const int64_t want = (k.units + kWarps - 1) / kWarps;
+    int64_t most = all ? static_cast<int64_t>(kRopeBlocksPerSm) * sms * cost[i] / all : 0;
+    if (most < 1) most = 1;
+    k.blocks = static_cast<unsigned>(want < most ? want : most);
+    grid += k.blocks;
+  }
+  return grid;
 }
 
-template <bool kPaged, typename T, int D>
-cudaError_t launch_rows(RopeArgs a, int sms, cudaStream_t s) {
-  share(a, D, sms * 32);
-  const int64_t blocks = (a.units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 4;
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (a.interleaved)
-    rope_rows_kernel<T, D, true, kPaged><<<grid, kThreads, 0, s>>>(a);
-  else
-    rope_rows_kernel<T, D, false, kPaged><<<grid, kThreads, 0, s>>>(a);
+template <class A>
+cudaError_t launch(void (*kernel)(A), OncePerDevice& once, const A& a, unsigned grid, int smem, cudaStream_t s) {
+  const cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t launch_bwd(RopeBwdArgs g, int sms, cudaStream_t s) {
-  share(g.a, D, sms * 32);
-  const unsigned grid = static_cast<unsigned>(rope_bwd_blocks(g.a.units, sms));
-  if (g.a.interleaved)
-    rope_bwd_kernel<T, D, true><<<grid, kThreads, 0, s>>>(g);
-  else
-    rope_bwd_kernel<T, D, false><<<grid, kThreads, 0, s>>>(g);
-  const cudaError_t e = cudaGetLastError();
+template <bool kPaged, typename T, int D, int F>
+cudaError_t launch_rows_f(RopeArgs a, int sms, cudaStream_t s) {
+  constexpr int kSmem = kWarps * kStagesFwd * kUnroll * Lane<T, D, F, false>::kSlot;
+  static OncePerDevice once[2];
+  const unsigned grid = share(a, 32 * F / D, sms);
+  return a.interleaved ? launch(rope_rows_kernel<T, D, F, true, kPaged>, once[1], a, grid, kSmem, s)
+                       : launch(rope_rows_kernel<T, D, F, false, kPaged>, once[0], a, grid, kSmem, s);
+}
+
+template <typename T, int D, int F>
+cudaError_t launch_bwd_f(RopeBwdArgs g, int sms, cudaStream_t s) {
+  constexpr int kSmem = kWarps * kStagesBwd * kUnroll * 2 * Lane<T, D, F, false>::kSlot;
+  static OncePerDevice once[2];
+  const unsigned grid = share(g.a, 32 * F / D, sms);
+  const cudaError_t e = g.a.interleaved ? launch(rope_bwd_kernel<T, D, F, true>, once[1], g, grid, kSmem, s)
+                                        : launch(rope_bwd_kernel<T, D, F, false>, once[0], g, grid, kSmem, s);
   if (e != cudaSuccess || g.part == nullptr) return e;
-  return launch_ahead(rope_dw_kernel, dim3(2 * D / 32), dim3(256), 0, s, true, static_cast<const float*>(g.part),
-                      static_cast<int>(grid), D, g.dq_weight, g.dk_weight);
+  return launch_ahead(rope_dw_kernel, dim3(2 * D / 8), dim3(256), 0, s, true, static_cast<const float*>(g.part),
+                      static_cast<int>(g.a.kind[1].block0), static_cast<int>(grid), D, g.dq_weight, g.dk_weight);
+}
+
+// Features of a lane: what two 16-byte pieces hold, if whole lanes are rotated.
+template <bool kPaged, typename T, int D>
+cudaError_t launch_rows(const RopeArgs& a, int sms, cudaStream_t s) {
+  if (sizeof(T) == 2 && a.rot % 16 == 0) return launch_rows_f<kPaged, T, D, sizeof(T) == 2 ? 16 : 8>(a, sms, s);
+  return launch_rows_f<kPaged, T, D, 8>(a, sms, s);
+}
+
+template <typename T, int D>
+cudaError_t launch_bwd(const RopeBwdArgs& g, int sms, cudaStream_t s) {
+  if (sizeof(T) == 2 && g.a.rot % 16 == 0) return launch_bwd_f<T, D, sizeof(T) == 2 ? 16 : 8>(g, sms, s);
+  return launch_bwd_f<T, D, 8>(g, sms, s);
 }
 
 }  // namespace
-
-int64_t rope_bwd_blocks(int64_t units, int sms) {
-  const int64_t blocks = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * kRopeBwdBlocksPerSm;
-  return blocks < most ? blocks : most;
-}
 
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool f32, int sms, cudaStream_t s) {
   switch (d) {

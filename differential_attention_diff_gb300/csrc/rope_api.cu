@@ -47,25 +47,28 @@ da_status check_qk(const da_qk_rope_fwd_params* p, bool* empty) {
   return DA_OK;
 }
 
-da::RopeArgs rope_args(const da_qk_rope_fwd_params* p) {
+da::RopeKind rows(int heads, const da_t4& src, const da_t4& dst, const float* weight) {
+  da::RopeKind k{};
+  k.heads = heads;
+  k.src = src;
+  k.dst = dst;
+  k.weight = weight;
+  return k;
+}
+
+da::RopeArgs rope_args(const da_qk_rope_fwd_params* p, const da_t4& q_to, const da_t4& k_to) {
   da::RopeArgs a{};
   a.tokens = static_cast<int64_t>(p->B) * p->N;
   a.N = p->N;
-  a.h_q = p->h_q;
-  a.h_k = p->h_k;
   a.rot = p->rot_dim;
   a.interleaved = p->interleaved != 0;
   a.norm = p->norm != 0;
   a.rope_scale = p->rope_scale;
   a.norm_eps = p->norm_eps;
   a.inv_freq = p->inv_freq;
-  a.q_weight = p->q_weight;
-  a.k_weight = p->k_weight;
   a.positions = p->positions;
-  a.q = p->q;
-  a.k = p->k;
-  a.q_out = p->q_out;
-  a.k_out = p->k_out;
+  a.kind[0] = rows(p->h_q, p->q, q_to, p->q_weight);
+  a.kind[1] = rows(p->h_k, p->k, k_to, p->k_weight);
   return a;
 }
 
@@ -108,7 +111,7 @@ da_status diffattn_qk_rope_fwd(const da_qk_rope_fwd_params* p, void* stream) {
   uint32_t* status;
   int sms;
   if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
-  return cuda_status(da::launch_rope_fwd(rope_args(p), p->d, p->dtype == DA_F32, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(da::launch_rope_fwd(rope_args(p, p->q_out, p->k_out), p->d, p->dtype == DA_F32, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t diffattn_qk_rope_bwd_workspace_size(int B, int N, int h_q, int h_k, int d) {
@@ -117,7 +120,7 @@ size_t diffattn_qk_rope_bwd_workspace_size(int B, int N, int h_q, int h_k, int d
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
   // the sums of every block that the grid can have
-  return align256(static_cast<size_t>(sms) * da::kRopeBwdBlocksPerSm * 2 * d * sizeof(float));
+  return align256((static_cast<size_t>(sms) * da::kRopeBlocksPerSm + 2) * d * sizeof(float));
 }
 
 da_status diffattn_qk_rope_bwd(const da_qk_rope_bwd_params* p, void* stream) {
@@ -144,7 +147,7 @@ da_status diffattn_qk_rope_bwd(const da_qk_rope_bwd_params* p, void* stream) {
   uint32_t* status;
   int sms;
   if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
-  const da::RopeBwdArgs g{rope_args(&p->fwd), p->dq_out, p->dk_out, p->dq, p->dk,
+  const da::RopeBwdArgs g{rope_args(&p->fwd, p->dq, p->dk), p->dq_out, p->dk_out,
                           weights ? static_cast<float*>(p->workspace) : nullptr, p->dq_weight, p->dk_weight};
   return cuda_status(da::launch_rope_bwd(g, p->fwd.d, p->fwd.dtype == DA_F32, sms, s));
 }
@@ -166,23 +169,16 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* stream) {
   if (!da::device_handles(&status, &sms)) return DA_ERR_CUDA;
   da::RopeArgs a{};
   a.tokens = p->cache.T;
-  a.h_q = p->h_q;
-  a.h_k = a.h_v = p->cache.h_kv;
   a.rot = p->rot_dim;
   a.interleaved = p->interleaved != 0;
   a.norm = p->norm != 0;
   a.rope_scale = p->rope_scale;
   a.norm_eps = p->norm_eps;
   a.inv_freq = p->inv_freq;
-  a.q_weight = p->q_weight;
-  a.k_weight = p->k_weight;
   a.positions = p->positions;
-  a.q = as_t4(p->q);
-  a.k = as_t4(p->k);
-  a.v = as_t4(p->v);
-  a.q_out = as_t4(p->q_out);
-  a.k_out = p->cache.k_pages;
-  a.v_out = p->cache.v_pages;
+  a.kind[0] = rows(p->h_q, as_t4(p->q), as_t4(p->q_out), p->q_weight);
+  a.kind[1] = rows(p->cache.h_kv, as_t4(p->k), p->cache.k_pages, p->k_weight);
+  a.kind[2] = rows(p->cache.h_kv, as_t4(p->v), p->cache.v_pages, nullptr);
   a.cache = p->cache;
   a.status = status;
   return cuda_status(da::launch_paged_append(a, d, sms, static_cast<cudaStream_t>(stream)));
