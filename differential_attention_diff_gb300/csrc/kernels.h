@@ -190,10 +190,9 @@ struct RopeKind {
   int heads;
   da_t4 src, dst;          // paged: of the packed rows sb is unused, sn the token's stride; k and v go to the pages
   const float* weight;
-  // set by the launchers: passes over a token's heads, in how many shares; the kind's blocks
+  // set by the launchers: passes over a token's heads, and in how many shares (units)
   int passes, chunk_passes, chunks;
-  int64_t units;           // shares of all tokens
-  unsigned block0, blocks;
+  uint32_t unit0;          // the kind's first unit
 };
 struct RopeArgs {
   int64_t tokens;
@@ -203,16 +202,17 @@ struct RopeArgs {
   const float* inv_freq;
   const int* positions;
   RopeKind kind[3];
+  uint32_t units;          // of all kinds (set by the launchers)
   da_paged_cache cache;    // paged
   uint32_t* status;
 };
 struct RopeBwdArgs {
   RopeArgs a;              // kind[].dst: the gradients to write
   da_t4 dq_out, dk_out;
-  float* part;             // [blocks, d] sums of the weights' gradients, or null
+  float* part;             // [blocks, 2, d] sums of the weights' gradients, or null
   float *dq_weight, *dk_weight;
 };
-constexpr int kRopeBlocksPerSm = 2;  // of the grid at most; each kind of rows may have one more
+constexpr int kRopeBlocksPerSm = 2;  // of the grid at most
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool f32, int sms, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeBwdArgs& g, int d, bool f32, int sms, cudaStream_t s);
 // The checks of a paged cache: sizes and types, then pointers and strides (which

@@ -4,24 +4,23 @@
 //
 // Definitions in diffattn.h.  All three stream rows of d features once and are
 // bound by memory, as long as little else is done per row and enough of them are
-// on their way.  A block takes rows of one kind (queries, keys, or values to
-// copy), so that weights, and the sums of the weights' gradients, stay in its
-// registers; a warp takes a token, or a share of its heads where there are few
-// tokens, computes the token's cosines and sines once, a frequency to a lane, and
-// passes over its rows.  d / F lanes have a row, F = 16 features each (8 where
+// on their way.  A warp takes a token's rows of one kind (queries, keys, or values
+// to copy), or a share of them where there are few tokens, computes the token's
+// cosines and sines once, a frequency to a lane, and passes over its rows; all of
+// its queries come first, then its keys, so weights, and the sums of the weights'
+// gradients, stay in registers.  d / F lanes have a row, F = 16 features each (8 where
 // they are fp32, or where rot_dim is no multiple of 16): two pieces of 16 bytes
 // that hold whole pairs, so a row's sums take log2(d / F) shuffles and the
 // rotation none, and two features go through an instruction.  The pieces come by
 // asynchronous copies, each lane its own, kStages groups of rows ahead and across
 // the warp's tokens: 128 KB per SM in flight (192 in the backward).  With rows in
 // registers instead, the backward of 2 x 8192 tokens of 64 + 8 heads, d 128, norm,
-// took 165 us on a GB300 (now 148, 6.1 TB/s; the forward 100, 6.0 TB/s).
+// took 165 us on a GB300 (150 now, 6.1 TB/s; the forward 106, 5.7 TB/s).
 //
 // The angle: position * inv_freq in turns, as a 64-bit fixed-point fraction that
 // wraps by itself (position times 2^64 inv_freq / 2 pi, modulo 2^64).  It is off
 // by 2^-64 turns a position at most, so far positions keep the accuracy of near
-// ones, and the quarter of the turn comes out of its top bits exactly; what goes
-// to sincospi is at most an eighth of a turn either way.
+// ones, and the quarter of the turn comes out of its top bits exactly.
 #include "common.cuh"
 #include "fp32_pair.cuh"
 #include "kernels.h"
@@ -35,6 +34,12 @@ constexpr int kThreads = kWarps * 32;
 
 constexpr int kUnroll = 2;      // passes (of 32 / lanes rows) that are a group
 constexpr int kStagesFwd = 4, kStagesBwd = 3;
+// The passes of a share of work, 1 KB of rows each, where there is plenty.  More
+// spread what the GPU reads at a time, fewer compute more angles: 2 x 8192 tokens of
+// 64 + 8 heads take forward 106, 100, 111, 113 us with 4, 6, 8, 16 (99, 110, 111,
+// 109 without the norm; in fp32, half as many, 94, 113, 109, 107), backward 156,
+// 150, 153, 168 (103, 99, 112, 112).
+constexpr int kSharePasses = 4, kSharePassesBwd = 6;
 
 // 2^64 inv_freq / 2 pi modulo 2^64.  1 / 2 pi in two doubles (the first is it
 // rounded, the second the rest): their product with a 24-bit number is good to
@@ -48,11 +53,23 @@ __device__ __forceinline__ uint64_t turns(float inv_freq) {
   return __double2ull_rn(frac * 18446744073709551616.0) + static_cast<uint64_t>(__double2ll_rn(lo * 18446744073709551616.0));
 }
 
+// Sine and cosine of t / 2^64 turns, times scale.  What is left of the nearest
+// quarter, at most an eighth of a turn, is taken to 2^-34 of a turn; Taylor's
+// series up to x^9 and x^10 are off by 2^-29 and 2^-34 there.
 __device__ __forceinline__ void sincos_turns(uint64_t t, float scale, float& s, float& c) {
   const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
-  const int64_t rest = static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62));  // within 2^61 either way
-  float s0, c0;
-  sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &s0, &c0);  // 2^-63: half turns
+  const int rest = static_cast<int>(static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62)) >> 30);  // 2^-34 turns
+  const float x = static_cast<float>(rest) * 3.6572951982e-10f;                                               // 2 pi 2^-34
+  const float x2 = x * x;
+  float p = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+  p = fmaf(x2, p, 1.f / 120.f);
+  p = fmaf(x2, p, -1.f / 6.f);
+  const float s0 = fmaf(x * x2, p, x);
+  p = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+  p = fmaf(x2, p, -1.f / 720.f);
+  p = fmaf(x2, p, 1.f / 24.f);
+  p = fmaf(x2, p, -0.5f);
+  const float c0 = fmaf(x2, p, 1.f);
   const float a = (quarter & 1) ? c0 : s0, b = (quarter & 1) ? s0 : c0;
   s = (quarter & 2) ? -a * scale : a * scale;
   c = ((quarter + 1) & 2) ? -b * scale : b * scale;
@@ -154,16 +171,38 @@ struct Lane {
   }
 };
 
-// (u, v) turned: u c - v s, v c + u s
+// The rotation of a lane's pairs, with what its features are multiplied by before
+// (w) and which way: u' = u uc + v us, v' = v vc + u vs.
 template <int P>
-__device__ __forceinline__ void rotate(F2Pair (&x)[2 * P], const F2Pair (&c)[P], const F2Pair (&s)[P]) {
+struct Turn {
+  F2Pair uc[P], us[P], vc[P], vs[P];
+  // no rotation
+  __device__ __forceinline__ void set(const F2Pair (&w)[2 * P]) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const F2Pair u = x[i], v = x[P + i];
-    x[i] = fma2(-v, s[i], u * c[i]);
-    x[P + i] = fma2(u, s[i], v * c[i]);
+    for (int i = 0; i < P; ++i) {
+      uc[i] = w[i];
+      vc[i] = w[P + i];
+      us[i] = vs[i] = {0.f, 0.f};
+    }
   }
-}
+  __device__ __forceinline__ void set(const F2Pair (&w)[2 * P], const F2Pair (&c)[P], const F2Pair (&s)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      uc[i] = w[i] * c[i];
+      us[i] = -(w[P + i] * s[i]);
+      vc[i] = w[P + i] * c[i];
+      vs[i] = w[i] * s[i];
+    }
+  }
+  __device__ __forceinline__ void apply(F2Pair (&x)[2 * P]) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const F2Pair u = x[i], v = x[P + i];
+      x[i] = fma2(v, us[i], u * uc[i]);
+      x[P + i] = fma2(u, vs[i], v * vc[i]);
+    }
+  }
+};
 
 template <int kLanes>
 __device__ __forceinline__ float row_sum(float x) {
@@ -182,7 +221,8 @@ __device__ __forceinline__ float square_sum(const F2Pair (&x)[P]) {
 
 // A token's cosines and sines, a frequency to a lane, left in shared memory for
 // the lanes that have its pairs.  `sign` turns the other way.
-__device__ __forceinline__ void token_angles(const RopeArgs& a, const uint64_t* freq, int pos, float sign, float* cs, int stride, int lane) {
+__device__ __forceinline__ void token_angles(const RopeArgs& a, const uint64_t* freq, int pos, float sign, float* cs, int stride,
+                                             int lane) {
   __syncwarp();
   for (int i = lane; i < a.rot / 2; i += 32) {
     float s, c;
@@ -234,43 +274,43 @@ __device__ __forceinline__ int sequence_of(const int* cu, int B, int t, int lane
   return lo;
 }
 
-// The kind of rows that this block has.
-__device__ __forceinline__ int block_kind(const RopeArgs& a) {
-  return blockIdx.x < a.kind[1].block0 ? 0 : blockIdx.x < a.kind[2].block0 ? 1 : 2;
-}
-
-// A warp's way through its shares of tokens (units), a group of kUnroll passes at
-// a time.  One runs ahead to fetch, one follows.
+// A warp's way through its shares of tokens (units), those of the queries, then
+// the keys', then the values', a group of kUnroll passes at a time.  One runs
+// ahead to fetch, one follows.
 struct Way {
-  const RopeKind& kd;
-  int64_t unit;
-  int t, p, p1;  // token, first pass of the group, end of the share
-  bool fresh;    // the group is a share's first
-  __device__ __forceinline__ Way(const RopeKind& kd_, int warp) : kd(kd_), unit(static_cast<int64_t>(blockIdx.x - kd_.block0) * kWarps + warp) { share(); }
-  __device__ __forceinline__ bool more() const { return unit < kd.units; }
-  __device__ __forceinline__ int64_t stride() const { return static_cast<int64_t>(kd.blocks) * kWarps; }
-  __device__ __forceinline__ int token(int64_t u) const { return static_cast<int>(kd.chunks == 1 ? u : u / kd.chunks); }
+  const RopeArgs* args;
+  uint32_t unit;
+  int which;       // kind of rows
+  int t, p, p1;    // token, first pass of the group, end of the share
+  bool fresh;      // the group is a share's first
+  __device__ __forceinline__ Way(const RopeArgs& a_, int warp) : args(&a_), unit(blockIdx.x * kWarps + warp) { share(); }
+  __device__ __forceinline__ bool more() const { return unit < args->units; }
+  __device__ __forceinline__ const RopeKind& kind() const { return args->kind[which]; }
   __device__ __forceinline__ void share() {
-    t = token(unit);
-    p = static_cast<int>(unit - static_cast<int64_t>(t) * kd.chunks) * kd.chunk_passes;
-    p1 = min(kd.passes, p + kd.chunk_passes);
+    which = unit < args->kind[1].unit0 ? 0 : unit < args->kind[2].unit0 ? 1 : 2;
+    const RopeKind& k = kind();
+    const uint32_t u = unit - k.unit0;
+    t = static_cast<int>(k.chunks <= 1 ? u : u / k.chunks);
+    p = k.chunks <= 1 ? 0 : static_cast<int>(u - t * k.chunks) * k.chunk_passes;
+    p1 = min(k.passes, p + k.chunk_passes);
     fresh = true;
+  }
+  __device__ __forceinline__ void step() {  // to the next share
+    unit += gridDim.x * kWarps;
+    if (more()) share();
   }
   __device__ __forceinline__ void next() {
     p += kUnroll;
     fresh = false;
-    if (p < p1) return;
-    unit += stride();
-    if (more()) share();
+    if (p >= p1) step();
+  }
+  // whether pass u of the group has a row of this lane, and its head
+  template <int kRows>
+  __device__ __forceinline__ bool row(int u, int sub, int* h) const {
+    *h = (p + u) * kRows + sub;
+    return p + u < p1 && *h < kind().heads;
   }
 };
-
-// Whether the pass has a row of this lane, and its head.
-template <int kRows>
-__device__ __forceinline__ bool has_row(const Way& w, int u, int sub, int* h) {
-  *h = (w.p + u) * kRows + sub;
-  return w.p + u < w.p1 && *h < w.kd.heads;
-}
 
 // A token's place: its rotation's position and where its rows go, as far as they
 // are loaded and not looked at (a share ahead of their use).
@@ -307,21 +347,20 @@ rope_rows_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ uint64_t freq[D / 2];
   __shared__ __align__(16) float angles[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int which = block_kind(a);
-  const RopeKind& kd = a.kind[which];
-  const bool turned = which < 2;
   const int l = lane % kLanes, sub = lane / kLanes;
   const L f(l, a.rot);
   uint8_t* mine = ring + warp * kStagesFwd * kUnroll * L::kSlot + lane * L::kPiece;
   const uint32_t mine_s = smem_u32(mine);
-  Way ahead(kd, warp);
+  Way ahead(a, warp);
+  const T* from = nullptr;
   auto fetch = [&](int st) {
     if (ahead.more()) {
-      const T* from = kPaged ? at<T>(kd.src, 0, ahead.t) : at<T>(kd.src, ahead.t / a.N, ahead.t % a.N);
+      const da_t4& src = ahead.kind().src;
+      if (ahead.fresh) from = kPaged ? at<T>(src, 0, ahead.t) : at<T>(src, ahead.t / a.N, ahead.t % a.N);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         int h;
-        if (has_row<kRows>(ahead, u, sub, &h)) f.fetch(mine_s + (st * kUnroll + u) * L::kSlot, from + h * kd.src.sh);
+        if (ahead.row<kRows>(u, sub, &h)) f.fetch(mine_s + (st * kUnroll + u) * L::kSlot, from + h * src.sh);
       }
       ahead.next();
     }
@@ -329,61 +368,77 @@ rope_rows_kernel(const __grid_constant__ RopeArgs a) {
   };
 #pragma unroll
   for (int st = 0; st < kStagesFwd - 1; ++st) fetch(st);
-  for (int i = threadIdx.x; turned && i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
   if constexpr (kPaged) {
     const da_paged_cache& c = a.cache;
     for (int b = threadIdx.x; blockIdx.x == 0 && b < c.B; b += kThreads)
       if (!paged_sequence_ok(c, c.cu_seqlens[b], c.cu_seqlens[b + 1], c.seqlens[b])) record_status(a.status, DA_ERR_BOUNDS, 0x0E01);
   }
   __syncthreads();
-  const bool norm = a.norm && turned;
-  F2Pair w[F / 2], co[F / 4], si[F / 4];
-  if (norm) load_weight<F>(kd.weight, f, w);
-  int st = 0;
-  Place place{}, next{};
-  T* to = nullptr;
-  Way way(kd, warp);
-  if (way.more()) next = place_of<kPaged>(a, which, way.t, lane);
-  for (; way.more(); way.next(), st = st + 1 == kStagesFwd ? 0 : st + 1) {
-    fetch(st == 0 ? kStagesFwd - 1 : st - 1);
-    if (way.fresh) {
-      place = next;
-      if (way.unit + way.stride() < kd.units) next = place_of<kPaged>(a, which, way.token(way.unit + way.stride()), lane);
-      if constexpr (kPaged) {
-        if (place.ok && which > 0 && (place.page < 0 || place.page >= a.cache.n_pages)) {
-          if (lane == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0E02);
-          place.ok = false;
-        }
-        to = which > 0 ? at<T>(kd.dst, place.page, place.j % a.cache.page_size) : at<T>(kd.dst, 0, way.t);
+  F2Pair w[F / 2];
+  Turn<F / 4> turn;
+  int st = 0, kind = -1;
+  Way way(a, warp);
+  Place next{};
+  if (way.more()) next = place_of<kPaged>(a, way.which, way.t, lane);
+  while (way.more()) {
+    // a share: where its rows go, and what turns them
+    Place place = next;
+    Way after = way;
+    after.step();
+    if (after.more()) next = place_of<kPaged>(a, after.which, after.t, lane);  // looked up a share ahead
+    const RopeKind& kd = way.kind();
+    if (way.which != kind) {
+      kind = way.which;
+      load_weight<F>(a.norm ? kd.weight : nullptr, f, w);
+    }
+    const bool turned = kind < 2 && (a.norm || a.rot), norm = kind < 2 && a.norm;
+    T* to;
+    if constexpr (kPaged) {
+      if (place.ok && kind > 0 && (place.page < 0 || place.page >= a.cache.n_pages)) {
+        if (lane == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0E02);
+        place.ok = false;
+      }
+      to = kind > 0 ? at<T>(kd.dst, place.page, place.j % a.cache.page_size) : at<T>(kd.dst, 0, way.t);
+    } else {
+      to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
+    }
+    if (turned) {
+      if (a.rot) token_angles(a, freq, place.pos, 1.f, angles[warp], D / 2, lane);
+      if (f.rotated) {
+        F2Pair co[F / 4], si[F / 4];
+        load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
+        turn.set(w, co, si);
       } else {
-        to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
-      }
-      if (turned && a.rot) {
-        token_angles(a, freq, place.pos, 1.f, angles[warp], D / 2, lane);
-        if (f.rotated) load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
+        turn.set(w);
       }
     }
-    cp_async_wait<kStagesFwd - 1>();
+    for (int p = way.p; p < way.p1; p += kUnroll, st = st + 1 == kStagesFwd ? 0 : st + 1) {
+      fetch(st == 0 ? kStagesFwd - 1 : st - 1);
+      cp_async_wait<kStagesFwd - 1>();
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (way.p + u >= way.p1) break;
-      int h;
-      const bool row = has_row<kRows>(way, u, sub, &h);
-      typename L::Raw x;
-      x.load(mine + (st * kUnroll + u) * L::kSlot);
-      if (turned) {
-        F2Pair y[F / 2];
-        L::get(x, y);
-        if (norm) {
-          const float r = rsqrtf(row_sum<kLanes>(square_sum(y)) * (1.f / D) + a.norm_eps);
+      for (int u = 0; u < kUnroll; ++u) {
+        if (p + u >= way.p1) break;
+        const int h = (p + u) * kRows + sub;
+        typename L::Raw x;
+        x.load(mine + (st * kUnroll + u) * L::kSlot);
+        if (turned) {
+          F2Pair y[F / 2];
+          L::get(x, y);
+          if (norm) {
+            const float r = rsqrtf(row_sum<kLanes>(square_sum(y)) * (1.f / D) + a.norm_eps);
+            turn.apply(y);
 #pragma unroll
-          for (int e = 0; e < F / 2; ++e) y[e] = y[e] * F2Pair{r, r} * w[e];
+            for (int e = 0; e < F / 2; ++e) y[e] = y[e] * F2Pair{r, r};
+          } else if (f.rotated) {
+            turn.apply(y);
+          }
+          L::put(x, y);
         }
-        if (f.rotated) rotate(y, co, si);
-        L::put(x, y);
+        if (h < kd.heads && place.ok) x.store(to + h * kd.dst.sh, f);
       }
-      if (row && place.ok) x.store(to + h * kd.dst.sh, f);
     }
+    way = after;
   }
   cp_async_wait<0>();
 }
@@ -399,28 +454,30 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs g) {
   const RopeArgs& a = g.a;
   extern __shared__ __align__(16) uint8_t ring[];     // [warp][stage][pass][x, dy][two pieces of every lane]
   __shared__ uint64_t freq[D / 2];
-  __shared__ __align__(16) float angles[kWarps][D];  // and the warps' sums at the end
+  __shared__ __align__(16) float angles[kWarps][D];
+  __shared__ float sums[kWarps][2][D];                // the warps' sums of the weights' gradients
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int which = block_kind(a);
-  const RopeKind& kd = a.kind[which];
-  const da_t4& gy = which == 0 ? g.dq_out : g.dk_out;  // (kd.dst: dq or dk)
   const int l = lane % kLanes, sub = lane / kLanes;
   const L f(l, a.rot);
   uint8_t* mine = ring + warp * kStagesBwd * kUnroll * 2 * L::kSlot + lane * L::kPiece;
   const uint32_t mine_s = smem_u32(mine);
-  Way ahead(kd, warp);
+  Way ahead(a, warp);
+  const T *xp = nullptr, *yp = nullptr;
   auto fetch = [&](int st) {
     if (ahead.more()) {
-      const int b = ahead.t / a.N, n = ahead.t - b * a.N;
-      const T* xp = at<T>(kd.src, b, n);
-      const T* yp = at<T>(gy, b, n);
+      const da_t4 &src = ahead.kind().src, &gy = ahead.which == 0 ? g.dq_out : g.dk_out;
+      if (ahead.fresh) {
+        const int b = ahead.t / a.N, n = ahead.t - b * a.N;
+        xp = at<T>(src, b, n);
+        yp = at<T>(gy, b, n);
+      }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         int h;
-        if (has_row<kRows>(ahead, u, sub, &h)) {
+        if (ahead.row<kRows>(u, sub, &h)) {
           const uint32_t slot = mine_s + (st * kUnroll + u) * 2 * L::kSlot;
           f.fetch(slot + L::kSlot, yp + h * gy.sh);
-          if (a.norm) f.fetch(slot, xp + h * kd.src.sh);
+          if (a.norm) f.fetch(slot, xp + h * src.sh);
         }
       }
       ahead.next();
@@ -430,138 +487,151 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs g) {
 #pragma unroll
   for (int st = 0; st < kStagesBwd - 1; ++st) fetch(st);
   for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) freq[i] = turns(a.inv_freq[i]);
+  for (int i = lane; i < 2 * D; i += 32) (&sums[warp][0][0])[i] = 0.f;
   __syncthreads();
-  F2Pair w[F / 2], co[F / 4], si[F / 4], acc[F / 2];
-  if (a.norm) load_weight<F>(kd.weight, f, w);
+  F2Pair w[F / 2], acc[F / 2];
+  F2Pair co[F / 4], si[F / 4];
+  auto clear = [&]() {
 #pragma unroll
-  for (int e = 0; e < F / 2; ++e) acc[e] = {0.f, 0.f};
-  int st = 0;
+    for (int e = 0; e < F / 2; ++e) acc[e] = {0.f, 0.f};
+  };
+  // the warp's sums of a kind, once: its rows of that kind come on end
+  auto keep = [&](int kind) {
+#pragma unroll
+    for (int e = 0; e < F / 2; ++e) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x = half ? acc[e].hi() : acc[e].lo();
+#pragma unroll
+        for (int o = kLanes; o < 32; o *= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (sub == 0) sums[warp][kind][f.feature(e, half)] = x;
+      }
+    }
+  };
+  clear();
+  int st = 0, kind = -1;
+  Way way(a, warp);
   Place next{};
-  T* to = nullptr;
-  Way way(kd, warp);
-  if (way.more()) next = place_of<false>(a, which, way.t, lane);
-  for (; way.more(); way.next(), st = st + 1 == kStagesBwd ? 0 : st + 1) {
-    fetch(st == 0 ? kStagesBwd - 1 : st - 1);
-    if (way.fresh) {
-      const Place place = next;
-      if (way.unit + way.stride() < kd.units) next = place_of<false>(a, which, way.token(way.unit + way.stride()), lane);
-      to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
-      if (a.rot) {
-        token_angles(a, freq, place.pos, -1.f, angles[warp], D / 2, lane);
-        if (f.rotated) load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
+  if (way.more()) next = place_of<false>(a, way.which, way.t, lane);
+  while (way.more()) {
+    const Place place = next;
+    Way after = way;
+    after.step();
+    if (after.more()) next = place_of<false>(a, after.which, after.t, lane);
+    const RopeKind& kd = way.kind();  // (kd.dst: dq or dk)
+    if (way.which != kind) {
+      if (kind >= 0 && g.part) {
+        keep(kind);
+        clear();
       }
+      kind = way.which;
+      if (a.norm) load_weight<F>(kd.weight, f, w);
     }
-    cp_async_wait<kStagesBwd - 1>();
+    T* to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
+    if (a.rot) {
+      token_angles(a, freq, place.pos, 1.f, angles[warp], D / 2, lane);
+      if (f.rotated) load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
+    }
+    for (int p = way.p; p < way.p1; p += kUnroll, st = st + 1 == kStagesBwd ? 0 : st + 1) {
+      fetch(st == 0 ? kStagesBwd - 1 : st - 1);
+      cp_async_wait<kStagesBwd - 1>();
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (way.p + u >= way.p1) break;
-      int h;
-      const bool row = has_row<kRows>(way, u, sub, &h);
-      const uint8_t* slot = mine + (st * kUnroll + u) * 2 * L::kSlot;
-      typename L::Raw x;
-      x.load(slot + L::kSlot);
-      F2Pair dz[F / 2];
-      L::get(x, dz);
-      if (f.rotated) rotate(dz, co, si);
-      if (a.norm) {
-        F2Pair xh[F / 2];
-        x.load(slot);
-        L::get(x, xh);
-        const float r = rsqrtf(row_sum<kLanes>(square_sum(xh)) * (1.f / D) + a.norm_eps);
-        F2Pair m{0.f, 0.f};
+      for (int u = 0; u < kUnroll; ++u) {
+        if (p + u >= way.p1) break;
+        const int h = (p + u) * kRows + sub;
+        const bool row = h < kd.heads;
+        const uint8_t* slot = mine + (st * kUnroll + u) * 2 * L::kSlot;
+        typename L::Raw x;
+        x.load(slot + L::kSlot);
+        F2Pair dz[F / 2];
+        L::get(x, dz);
+        if (f.rotated) {  // the other way: u c + v s, v c - u s
 #pragma unroll
-        for (int e = 0; e < F / 2; ++e) {
-          xh[e] = xh[e] * F2Pair{r, r};
-          if (row) acc[e] = fma2(dz[e], xh[e], acc[e]);  // where there is none the slot holds anything
-          dz[e] = dz[e] * w[e];
-          m = fma2(dz[e], xh[e], m);
+          for (int i = 0; i < F / 4; ++i) {
+            const F2Pair du = dz[i], dv = dz[F / 4 + i];
+            dz[i] = fma2(dv, si[i], du * co[i]);
+            dz[F / 4 + i] = fma2(-du, si[i], dv * co[i]);
+          }
         }
-        const float mean = row_sum<kLanes>(m.lo() + m.hi()) * (-1.f / D);
+        if (a.norm) {
+          F2Pair xh[F / 2];
+          x.load(slot);
+          L::get(x, xh);
+          const float r = rsqrtf(row_sum<kLanes>(square_sum(xh)) * (1.f / D) + a.norm_eps);
+          F2Pair m{0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < F / 2; ++e) dz[e] = fma2(xh[e], F2Pair{mean, mean}, dz[e]) * F2Pair{r, r};
-      }
-      if (row) {
-        L::put(x, dz);
-        x.store(to + h * kd.dst.sh, f);
+          for (int e = 0; e < F / 2; ++e) {
+            xh[e] = xh[e] * F2Pair{r, r};
+            if (row) acc[e] = fma2(dz[e], xh[e], acc[e]);  // where there is none the slot holds anything
+            dz[e] = dz[e] * w[e];
+            m = fma2(dz[e], xh[e], m);
+          }
+          const float mean = row_sum<kLanes>(m.lo() + m.hi()) * (-1.f / D);
+#pragma unroll
+          for (int e = 0; e < F / 2; ++e) dz[e] = fma2(xh[e], F2Pair{mean, mean}, dz[e]) * F2Pair{r, r};
+        }
+        if (row) {
+          L::put(x, dz);
+          x.store(to + h * kd.dst.sh, f);
+        }
       }
     }
+    way = after;
   }
   cp_async_wait<0>();
   if (g.part == nullptr) return;
+  if (kind >= 0) keep(kind);
   __syncthreads();
-#pragma unroll
-  for (int e = 0; e < F / 2; ++e) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float x = half ? acc[e].hi() : acc[e].lo();
-#pragma unroll
-      for (int o = kLanes; o < 32; o *= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (sub == 0) angles[warp][f.feature(e, half)] = x;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < D; i += kThreads) {
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     float x = 0.f;
-    for (int v = 0; v < kWarps; ++v) x += angles[v][i];
-    g.part[static_cast<int64_t>(blockIdx.x) * D + i] = x;
+    for (int v = 0; v < kWarps; ++v) x += sums[v][i / D][i % D];
+    g.part[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = x;
   }
 }
 
-// dq_weight and dk_weight [d] from the blocks' sums [blocks, d], those of the
-// queries' blocks first: a block per 8 features of one of them, an 8-lane group
-// per share of the kind's blocks, added in their order.
-__global__ void __launch_bounds__(256) rope_dw_kernel(const float* part, int q_blocks, int blocks, int d, float* dq_weight, float* dk_weight) {
+// dq_weight and dk_weight [d] from the blocks' sums [blocks, 2, d]: a block per 8
+// features of one of them, an 8-lane group per share of the blocks, the groups
+// added in their order.
+__global__ void __launch_bounds__(256) rope_dw_kernel(const float* part, int blocks, int d, float* dq_weight, float* dk_weight) {
   __shared__ double sums[32][8];
   const int group = threadIdx.x / 8, k = threadIdx.x % 8;
-  const bool keys = static_cast<int>(blockIdx.x) >= d / 8;
-  const int i = (blockIdx.x - (keys ? d / 8 : 0)) * 8 + k;
-  const int lo = keys ? q_blocks : 0, hi = keys ? blocks : q_blocks;
+  const int i = blockIdx.x * 8 + k;
   double x = 0.0;
   cudaGridDependencySynchronize();
 #pragma unroll 4
-  for (int b = lo + group; b < hi; b += 32) x += static_cast<double>(part[static_cast<int64_t>(b) * d + i]);
+  for (int b = group; b < blocks; b += 32) x += static_cast<double>(part[static_cast<int64_t>(b) * 2 * d + i]);
   sums[group][k] = x;
   __syncthreads();
   if (group == 0) {
     for (int v = 1; v < 32; ++v) x += sums[v][k];
-    float* out = keys ? dk_weight : dq_weight;
-    if (out) out[i] = static_cast<float>(x);
+    float* out = i < d ? dq_weight : dk_weight;
+    if (out) out[i < d ? i : i - d] = static_cast<float>(x);
   }
 }
 
-// The kinds' blocks, in proportion to what their rows cost, and the warps' shares:
-// a token each where there are enough of them to fill the SMs' warps, else some
-// passes of a token's heads (at least one).  A token costs its passes, its angles
-// about two more, and finding its page one (2 x 8192 tokens of 64 + 8 heads: 133
-// us in proportion to the passes alone, 100 with the angles; six prompts appended:
-// 134 us without the page's, 113 with it).  Returns the grid.
-unsigned share(RopeArgs& a, int rows, int sms) {
-  const bool paged = a.cache.B > 0;
+// The warps' shares: up to most_passes passes over a token's rows of a kind where
+// there are enough of them to fill the SMs' warps, else fewer (at least one).
+// They are dealt to the warps in one row: what the GPU reads at a time lies close
+// together, and the kinds need not cost the same.  Returns the grid.
+unsigned share(RopeArgs& a, int rows, int sms, int most_passes) {
   const int64_t warps = static_cast<int64_t>(sms) * kRopeBlocksPerSm * kWarps;
-  int64_t passes = 0, cost[3], all = 0;
-  for (int i = 0; i < 3; ++i) {
-    RopeKind& k = a.kind[i];
+  int64_t passes = 0, units = 0;
+  for (RopeKind& k : a.kind) {
     k.passes = (k.heads + rows - 1) / rows;
-    cost[i] = k.passes ? k.passes + (i < 2 ? 2 : 0) + (paged ? 1 : 0) : 0;
     passes += k.passes;
-    all += cost[i];
   }
   int64_t each = a.tokens * passes / warps;  // passes to a warp
+  if (each > most_passes && a.tokens < (1 << 20)) each = most_passes;  // (units are counted in 32 bits)
   if (each < 1) each = 1;
-  unsigned grid = 0;
-  for (int i = 0; i < 3; ++i) {
-    RopeKind& k = a.kind[i];
-    k.block0 = grid;
+  for (RopeKind& k : a.kind) {
+    k.unit0 = static_cast<uint32_t>(units);
     k.chunk_passes = static_cast<int>(each < k.passes ? each : k.passes);
     k.chunks = k.passes ? (k.passes + k.chunk_passes - 1) / k.chunk_passes : 0;
-    k.units = a.tokens * k.chunks;
-    const int64_t want = (k.units + kWarps - 1) / kWarps;
-    int64_t most = all ? static_cast<int64_t>(kRopeBlocksPerSm) * sms * cost[i] / all : 0;
-    if (most < 1) most = 1;
-    k.blocks = static_cast<unsigned>(want < most ? want : most);
-    grid += k.blocks;
+    units += a.tokens * k.chunks;
   }
-  return grid;
+  a.units = static_cast<uint32_t>(units);
+  const int64_t want = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * kRopeBlocksPerSm;
+  return static_cast<unsigned>(want < most ? want : most);
 }
 
 template <class A>
@@ -576,7 +646,7 @@ template <bool kPaged, typename T, int D, int F>
 cudaError_t launch_rows_f(RopeArgs a, int sms, cudaStream_t s) {
   constexpr int kSmem = kWarps * kStagesFwd * kUnroll * Lane<T, D, F, false>::kSlot;
   static OncePerDevice once[2];
-  const unsigned grid = share(a, 32 * F / D, sms);
+  const unsigned grid = share(a, 32 * F / D, sms, kSharePasses);
   return a.interleaved ? launch(rope_rows_kernel<T, D, F, true, kPaged>, once[1], a, grid, kSmem, s)
                        : launch(rope_rows_kernel<T, D, F, false, kPaged>, once[0], a, grid, kSmem, s);
 }
@@ -585,12 +655,12 @@ template <typename T, int D, int F>
 cudaError_t launch_bwd_f(RopeBwdArgs g, int sms, cudaStream_t s) {
   constexpr int kSmem = kWarps * kStagesBwd * kUnroll * 2 * Lane<T, D, F, false>::kSlot;
   static OncePerDevice once[2];
-  const unsigned grid = share(g.a, 32 * F / D, sms);
+  const unsigned grid = share(g.a, 32 * F / D, sms, kSharePassesBwd);
   const cudaError_t e = g.a.interleaved ? launch(rope_bwd_kernel<T, D, F, true>, once[1], g, grid, kSmem, s)
                                         : launch(rope_bwd_kernel<T, D, F, false>, once[0], g, grid, kSmem, s);
   if (e != cudaSuccess || g.part == nullptr) return e;
   return launch_ahead(rope_dw_kernel, dim3(2 * D / 8), dim3(256), 0, s, true, static_cast<const float*>(g.part),
-                      static_cast<int>(g.a.kind[1].block0), static_cast<int>(grid), D, g.dq_weight, g.dk_weight);
+                      static_cast<int>(grid), D, g.dq_weight, g.dk_weight);
 }
 
 // Features of a lane: what two 16-byte pieces hold, if whole lanes are rotated.

@@ -120,7 +120,7 @@ size_t diffattn_qk_rope_bwd_workspace_size(int B, int N, int h_q, int h_k, int d
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
   // the sums of every block that the grid can have
-  return align256((static_cast<size_t>(sms) * da::kRopeBlocksPerSm + 2) * d * sizeof(float));
+  return align256(static_cast<size_t>(sms) * da::kRopeBlocksPerSm * 2 * d * sizeof(float));
 }
 
 da_status diffattn_qk_rope_bwd(const da_qk_rope_bwd_params* p, void* stream) {
