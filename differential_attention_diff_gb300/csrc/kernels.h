@@ -234,9 +234,11 @@ struct PagedArgs {
   float scale_log2;
   da_t3 q, out;
   const float* gate;   // [T, h]
-  float* part_o;       // [2 grid, rows, d] unnormalised outputs of the parts
+  float* part_o;       // [2 grid, rows, d] unnormalised outputs of the parts, d in
+                       // groups of four: row r's group q at r * part_row + q * part_group
   float* part_ml;      // [2 grid, rows, 2] their maxima (log2 units) and sums
   PagedDesc* desc;     // [grid]
+  int part_row, part_group;
   int rows;            // of a part: 128 per MMA tile, or the columns of the kernel for few tokens
   int grid;
   uint32_t* status;

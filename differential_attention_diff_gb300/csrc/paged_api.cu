@@ -127,6 +127,8 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   a.part_ml = reinterpret_cast<float*>(ws + w.ml);
   a.desc = reinterpret_cast<da::PagedDesc*>(ws + w.desc);
   a.rows = k.rows;
+  a.part_row = k.few ? c.d : 4;
+  a.part_group = k.few ? 4 : 4 * k.rows;
   a.grid = k.grid;
   a.status = status;
   a.after_gate = p->gate == nullptr;

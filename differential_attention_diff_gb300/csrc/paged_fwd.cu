@@ -424,7 +424,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         const float coef = (s ? factor[1] : factor[0]) / l;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.ptr) + (t_item + tok) * a.out.st + pair * a.out.sh + wg * (D / 2);
-        float* po = a.part_o + (part + s * 128 + row) * D + wg * (D / 2);
+        // the parts' rows lie side by side, four features each: a warp writes 512 bytes on end
+        float* po = a.part_o + part * D + (s * 128 + row) * a.part_row + wg * (D / 8) * a.part_group;
         const uint32_t t_o = tmem + lane_off + 256 + s * 128 + wg * (D / 2);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
@@ -463,7 +464,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           } else if (valid) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(po + c * 32)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              *reinterpret_cast<uint4*>(po + (c * 8 + e) * a.part_group) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         if (!whole && valid && wg == 0)

@@ -33,6 +33,9 @@ struct Merge {
     const int half = a.G / 2, tok = pair / half;
     return tok / a.tq1 * 128 + tok % a.tq1 * a.G + 2 * (pair % half);
   }
+  __device__ __forceinline__ const float* part(int i, int row, int col) const {
+    return a.part_o + slot(i, 0) * D + static_cast<int64_t>(row) * a.part_row + (col >> 2) * a.part_group + (col & 3);
+  }
   // of the pair, the output's token row and head
   __device__ __forceinline__ int64_t token(int pair) const { return d.token + pair / (a.G / 2); }
   __device__ __forceinline__ int head(int pair) const { return d.g * (a.G / 2) + pair % (a.G / 2); }
@@ -89,7 +92,7 @@ paged_merge_kernel(PagedArgs a) {
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
-          const float* po = a.part_o + mg.slot(i, row + e) * D + lane * kPer;
+          const float* po = mg.part(i, row + e, lane * kPer);
           if constexpr (kPer == 4)
             *reinterpret_cast<float4*>(x[e][i]) = i < parts ? *reinterpret_cast<const float4*>(po) : make_float4(0, 0, 0, 0);
           else
@@ -145,9 +148,9 @@ paged_merge_kernel(PagedArgs a) {
     float o0 = 0.f, o1 = 0.f;
 #pragma unroll 4
     for (int i = way; i < parts; i += kWays) {
-      const float* o = a.part_o + mg.slot(i, row) * D + col;
+      const float* o = mg.part(i, row, col);
       o0 = fmaf(o[0], weight[0][i], o0);
-      o1 = fmaf(o[D], weight[1][i], o1);
+      o1 = fmaf(o[a.part_row], weight[1][i], o1);
     }
     sums[way][0][col] = o0;
     sums[way][1][col] = o1;
