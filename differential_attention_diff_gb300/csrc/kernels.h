@@ -222,6 +222,7 @@ bool paged_cache_given(const da_paged_cache& c);
 cudaError_t launch_paged_append(const RopeArgs& a, int d, int sms, cudaStream_t s);
 
 // ---- V2 attention over a paged cache --------------------------------------------
+constexpr int kPagedMaxTurns = 4;  // shares of a CTA (paged.cuh)
 struct PagedDesc {
   int flags;             // paged.cuh; the rest: the item that is begun and not ended
   int token, tokens, g;  // its rows of the packed arrays, its KV head
@@ -234,11 +235,12 @@ struct PagedArgs {
   float scale_log2;
   da_t3 q, out;
   const float* gate;   // [T, h]
-  float* part_o;       // [2 grid, rows, d] unnormalised outputs of the parts, d in
+  float* part_o;       // [2 grid turns, rows, d] unnormalised outputs of the parts, d in
                        // groups of four: row r's group q at r * part_row + q * part_group
-  float* part_ml;      // [2 grid, rows, 2] their maxima (log2 units) and sums
-  PagedDesc* desc;     // [grid]
+  float* part_ml;      // [2 grid turns, rows, 2] their maxima (log2 units) and sums
+  PagedDesc* desc;     // [grid turns]
   int part_row, part_group;
+  int turns;           // the most shares that a CTA may have
   int rows;            // of a part: 128 per MMA tile, or the columns of the kernel for few tokens
   int grid;
   uint32_t* status;

@@ -4,14 +4,19 @@
 //
 // The unit of work is one tile of 128 keys for one item: up to `tq` new tokens
 // of one sequence with all G query heads of one KV head.  The units of a call
-// form a line, (sequence, KV head, item, key tile) in this order, and CTA c of C
-// takes its c-th equal share, wherever that begins and ends.  So a batch of any
+// form a line, (sequence, KV head, item, key tile) in this order, and share c of C
+// is its c-th equal piece, wherever that begins and ends.  So a batch of any
 // lengths loads the SMs evenly, whether it is one long sequence or many short
-// ones, and only the items that a share's end cuts are left to be joined: at
-// most C - 1, whatever the batch.  A CTA has at most two such parts, the rest of
-// an item that an earlier one began (slot 2c) and the beginning of one that a
-// later one ends (slot 2c + 1); an item that runs through whole shares has its
-// middle parts in the slots 2c.
+// ones, and only the items that a share's end cuts are left to be joined: at most
+// C - 1, whatever the batch.  A share has at most two such parts, the rest of an
+// item that an earlier one began (slot 2c) and the beginning of one that a later
+// one ends (slot 2c + 1); an item that runs through whole shares has its middle
+// parts in the slots 2c.
+// There are as many shares as CTAs, or a few times as many where a prompt's keys
+// and values do not fit L2 and are read for many items: the CTAs then take the
+// first shares of all, the next ones, and so on, so that what is read at a time is
+// a stretch of the line that fits (4 x 2048 tokens of 16384, 64 query and 8 KV
+// heads: 2977 us with one share to a CTA, 2768 with six).
 #pragma once
 
 #include "common.cuh"
@@ -21,6 +26,8 @@
 namespace da {
 
 constexpr int kPagedTile = 128;  // keys
+constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
+constexpr int kTurnUnits = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
 
 __device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
@@ -78,49 +85,65 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
   return x / y;
 }
 
-// Where a CTA's share begins and how long it is.
+// A CTA's shares: where each begins and how long it is.
 struct PagedShare {
   int b, g, i, j;
   int64_t units;
-  int bad;  // some sequence is out of bounds
+};
+template <int kTurns>  // the most that a CTA may have
+struct PagedShares {
+  int count;  // of this CTA; its k-th is share k * gridDim.x + blockIdx.x
+  int bad;    // some sequence is out of bounds
+  PagedShare share[kTurns];
 };
 
-// Fills *share (shared memory); called by all kThreads of a block, with sequence
+// Fills *out (shared memory); called by all kThreads of a block, with sequence
 // threadIdx.x (where there is one) in `mine`: fetched at the kernel's start, since
 // the rest waits for it.
-template <int kThreads>
-__device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, PagedShare* share) {
+template <int kThreads, int kTurns>
+__device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, PagedShares<kTurns>* out) {
   static_assert(kThreads % 32 == 0, "whole warps");
   constexpr int kW = kThreads / 32;
-  __shared__ int64_t sums[kW];
+  __shared__ int64_t sums[kW], lengths[kW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.cache.B;
   bool bad = false;
   // inclusive sums over the warp's sequences, and each round's over the warps:
   // the first round's stay in registers, which for kThreads sequences are all
   int64_t per = tid < B ? sequence_units(a.cache, mine, a.tq, &bad) : 0;
-  int64_t incl = per * a.cache.h_kv, rest = 0;
+  int64_t incl = per * a.cache.h_kv, rest = 0, keys = per ? mine.L : 0;
   for (int b = tid + kThreads; b < B; b += kThreads) {
     PagedSequence s;
     s.load(a.cache, b);
-    rest += sequence_units(a.cache, s, a.tq, &bad) * a.cache.h_kv;
+    const int64_t u = sequence_units(a.cache, s, a.tq, &bad);
+    rest += u * a.cache.h_kv;
+    keys += u ? s.L : 0;
   }
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
+  if constexpr (kTurns > 1) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+  }
   if (B > kThreads) {
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) rest += __shfl_xor_sync(0xffffffffu, rest, o);
   }
-  if (lane == 31) sums[warp] = incl;
+  if (lane == 31) {
+    sums[warp] = incl;
+    if constexpr (kTurns > 1) lengths[warp] = keys;
+  }
   const bool any_bad = __syncthreads_or(bad);
   int64_t before = incl - per * a.cache.h_kv, total = 0;
+  keys = 0;
 #pragma unroll
   for (int v = 0; v < kW; ++v) {
     if (v < warp) before += sums[v];
     total += sums[v];
+    if constexpr (kTurns > 1) keys += lengths[v];
   }
   int64_t base = total;  // of the first round
   if (B > kThreads) {
@@ -129,18 +152,30 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     __syncthreads();
     for (int v = 0; v < kW; ++v) total += sums[v];
   }
+  // turns of the CTAs: a stretch of the line reads about kTurnBytes of keys and
+  // values, and a share is long enough to outweigh its two cut items
+  int turns = 1;
+  if constexpr (kTurns > 1) {
+    const int64_t by_bytes = (keys * a.cache.h_kv * a.cache.d * 4) / kTurnBytes, by_units = quotient(total, gridDim.x) / kTurnUnits;
+    const int64_t t = by_bytes < by_units ? by_bytes : by_units;
+    turns = static_cast<int>(t < 1 ? 1 : t < kTurns ? t : kTurns);
+  }
   // equal shares, the first `more` of them one unit longer; less than a unit makes no sense
-  const int64_t ctas = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
-  const int64_t each = ctas ? quotient(total, ctas) : 0, more = total - each * ctas;
-  const int64_t u0 = c * each + (c < more ? c : more), units = c < ctas ? each + (c < more) : 0;
+  const int64_t all = static_cast<int64_t>(turns) * gridDim.x, shares = total < all ? total : all;
+  const int64_t each = shares ? quotient(total, shares) : 0, more = total - each * shares;
+  auto begin = [&](int64_t c) { return c * each + (c < more ? c : more); };
+  auto length = [&](int64_t c) { return c < shares ? each + (c < more) : 0; };
   if (tid == 0) {
-    share->units = units;
-    share->bad = any_bad;
+    out->count = turns;
+    out->bad = any_bad;
+    for (int k = 0; k < turns; ++k) out->share[k].units = length(static_cast<int64_t>(k) * gridDim.x + blockIdx.x);
   }
   PagedSequence s = mine;
   for (int r = 0;;) {
     const int64_t w = per * a.cache.h_kv;
-    if (units > 0 && u0 >= before && u0 < before + w) {
+    for (int k = 0; k < turns; ++k) {
+      const int64_t c = static_cast<int64_t>(k) * gridDim.x + blockIdx.x, u0 = begin(c);
+      if (length(c) == 0 || u0 < before || u0 >= before + w) continue;
       const int n = s.t1 - s.t0;
       int64_t off = u0 - before;
       const int g = static_cast<int>(quotient(off, per));
@@ -153,13 +188,13 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
         else
           hi = mid;
       }
-      share->b = r + tid;
-      share->g = g;
-      share->i = lo;
-      share->j = static_cast<int>(off - (lo ? tiles_before(lo, n, s.L, a.tq) : 0));
+      out->share[k].b = r + tid;
+      out->share[k].g = g;
+      out->share[k].i = lo;
+      out->share[k].j = static_cast<int>(off - (lo ? tiles_before(lo, n, s.L, a.tq) : 0));
     }
     r += kThreads;
-    if (r >= B || u0 < base || units == 0) break;
+    if (r >= B || begin(static_cast<int64_t>(turns - 1) * gridDim.x + blockIdx.x) < base) break;
     // the next kThreads sequences
     per = 0;
     if (r + tid < B) {
@@ -184,20 +219,20 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   __syncthreads();
 }
 
-// A CTA's way along its share, part by part; every warp walks by itself.
+// A CTA's way along its shares, part by part; every warp walks by itself.
+template <int kTurns>
 struct PagedWalk {
   const PagedArgs& a;
+  const PagedShares<kTurns>& s;
+  int k;                // the share, of this CTA's
   int b, g, i, j;       // the part's item and first key tile
-  int64_t left;         // units that are left, this part's counted in
+  int64_t left;         // units that are left of the share, this part's counted in
   int t0, n, L;         // the sequence
   int tokens, tiles, j1;  // the item's tokens and key tiles; the part ends before tile j1
-  __device__ __forceinline__ PagedWalk(const PagedArgs& a_, const PagedShare& s)
-      : a(a_), b(s.b), g(s.g), i(s.i), j(s.j), left(s.units) {
-    if (left > 0) {
-      sequence();
-      item();
-    }
-  }
+  __device__ __forceinline__ PagedWalk(const PagedArgs& a_, const PagedShares<kTurns>& s_) : a(a_), s(s_), k(0) { share(); }
+  // the share's number, of all
+  __device__ __forceinline__ int number() const { return (kTurns > 1 ? k * static_cast<int>(gridDim.x) : 0) + static_cast<int>(blockIdx.x); }
+  __device__ __forceinline__ bool last() const { return left <= j1 - j; }  // of the share
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ bool begins() const { return j == 0; }
   __device__ __forceinline__ bool ends() const { return j1 == tiles; }
@@ -205,7 +240,10 @@ struct PagedWalk {
   __device__ __forceinline__ int first_position() const { return L - n + i * a.tq; }
   __device__ __forceinline__ void next() {
     left -= j1 - j;
-    if (left <= 0) return;
+    if (left <= 0) {
+      if (kTurns > 1 && ++k < s.count) share();
+      return;
+    }
     j = 0;
     if ((i + 1) * a.tq < n) {
       ++i;
@@ -221,6 +259,17 @@ struct PagedWalk {
   }
 
  private:
+  __device__ __forceinline__ void share() {
+    const PagedShare& x = s.share[k];
+    left = x.units;
+    if (left <= 0) return;
+    b = x.b;
+    g = x.g;
+    i = x.i;
+    j = x.j;
+    sequence();
+    item();
+  }
   __device__ __forceinline__ void sequence() {
     for (;; ++b) {  // there is one with work, since units are left
       t0 = a.cache.cu_seqlens[b];

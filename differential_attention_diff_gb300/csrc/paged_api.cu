@@ -23,11 +23,12 @@ bool ok_stride(int64_t stride, int64_t extent) { return extent <= 1 || (stride >
 // tokens fit the columns of the kernel for few tokens read their keys once there;
 // with more the 128-row tiles pay.
 struct Cut {
-  int tq, tq1, rows, grid;
+  int tq, tq1, rows, grid, turns;
   bool few;
 };
-Cut cut(int T, int max_new, int G, int sms) {
+Cut cut(int T, int max_new, int G, int h_kv, int sms) {
   Cut c;
+  c.turns = 1;
   const int64_t cols = static_cast<int64_t>(max_new > 0 && max_new < T ? max_new : T) * G;
   c.few = cols <= da::kPagedDecodeCols;
   if (c.few) {
@@ -37,6 +38,9 @@ Cut cut(int T, int max_new, int G, int sms) {
     c.tq1 = 128 / G;
     c.tq = 2 * c.tq1;
     c.rows = 256;
+    // a long prompt's chunk reads its keys for many items, four and more to a CTA:
+    // room for finer shares, which the lengths, on the device, decide on
+    if (static_cast<int64_t>(T) / c.tq * h_kv >= 4 * static_cast<int64_t>(sms)) c.turns = da::kPagedMaxTurns;
   }
   c.grid = sms;
   return c;
@@ -47,10 +51,10 @@ struct Space {
 };
 Space space(const Cut& c, int T, int h, int d, int gate_given) {
   Space w;
-  const size_t rows = static_cast<size_t>(2) * c.grid * c.rows;
+  const size_t rows = static_cast<size_t>(2) * c.grid * c.turns * c.rows;
   w.ml = align256(rows * d * sizeof(float));
   w.desc = w.ml + align256(rows * 2 * sizeof(float));
-  w.gate = w.desc + align256(c.grid * sizeof(da::PagedDesc));
+  w.gate = w.desc + align256(static_cast<size_t>(c.grid) * c.turns * sizeof(da::PagedDesc));
   w.total = w.gate + (gate_given ? 0 : align256(static_cast<size_t>(T) * h * sizeof(float)));
   return w;
 }
@@ -66,7 +70,7 @@ size_t diffattn_v2_paged_fwd_workspace_size(int T, int B, int max_new, int h, in
   uint32_t* status;
   int sms = 152;
   if (!da::device_handles(&status, &sms)) sms = 152;
-  return space(cut(T, max_new, static_cast<int>(G), sms), T, h, d, gate_given).total;
+  return space(cut(T, max_new, static_cast<int>(G), h_kv, sms), T, h, d, gate_given).total;
 }
 
 da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
@@ -97,7 +101,7 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   int sms = 152;
   const bool device = da::device_handles(&status, &sms);
   if (!device) sms = 152;  // the workspace is checked first, as the size query would have it
-  const Cut k = cut(c.T, p->max_new, static_cast<int>(G), sms);
+  const Cut k = cut(c.T, p->max_new, static_cast<int>(G), c.h_kv, sms);
   const Space w = space(k, c.T, p->h, c.d, p->gate != nullptr);
   if (p->workspace == nullptr || p->workspace_bytes < w.total || !aligned(p->workspace, 256)) return DA_ERR_WORKSPACE;
   if (!device || !da::tma_available()) return DA_ERR_CUDA;
@@ -129,6 +133,9 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   a.rows = k.rows;
   a.part_row = k.few ? c.d : 4;
   a.part_group = k.few ? 4 : 4 * k.rows;
+  // finer shares only where the keys and values that there can be do not fit L2
+  const int64_t bytes = static_cast<int64_t>(c.B) * c.max_pages * c.page_size * c.h_kv * c.d * 4;
+  a.turns = bytes >= (int64_t(96) << 20) ? k.turns : 1;
   a.grid = k.grid;
   a.status = status;
   a.after_gate = p->gate == nullptr;

@@ -140,7 +140,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   constexpr int kS = F::kStages;
   constexpr int kProducer = F::kGroups * 4, kIssuer = kProducer + 1;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ PagedShare share;
+  __shared__ PagedShares<1> share;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   const uint32_t raw = smem_u32(smem_raw);
@@ -195,7 +195,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int it = 0, st = 0;
     uint32_t round = 0;  // of the rings
     bool ok = true;
-    for (PagedWalk w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<1> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
       if (!ok) break;
@@ -239,7 +239,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const uint32_t v0 = sdesc_lo(base + F::kOffV, 1024), p0 = sdesc_lo(base + F::kOffP, 16);
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) { return wait_bar(&abort_flag, b, parity, a.status, site); };
       // S of tile x (of the CTA's share) for the item that a walk of its own is at
-      PagedWalk ahead(a, share);
+      PagedWalk<1> ahead(a, share);
       int it = 0, j = ahead.j, ks = 0;
       uint32_t k_round = 0;
       auto start = [&](int x) {
@@ -262,7 +262,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         return true;
       };
-      const int total = static_cast<int>(share.units);
+      const int total = static_cast<int>(share.share[0].units);  // (one share to a CTA here)
       int vs = 0;
       uint32_t v_round = 0;
       bool ok = total == 0 || start(0);
@@ -299,7 +299,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint32_t v_round = 0;
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = false;
-    for (PagedWalk w(a, share); w.more(); w.next()) {
+    for (PagedWalk<1> w(a, share); w.more(); w.next()) {
       const int cols = w.tokens * a.G - n0;  // the item's columns, from n0 on
       float m[kC], l[kC], o[kC];
 #pragma unroll
@@ -438,7 +438,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           }
         }
       } else {
-        const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.begins() ? 1 : 0)) * a.rows;
+        const int64_t part = static_cast<int64_t>(2 * w.number() + (w.begins() ? 1 : 0)) * a.rows;
 #pragma unroll
         for (int n = 0; n < kC; ++n) {
           if (n < cols && r < D) a.part_o[(part + n0 + n) * D + r] = o[n];

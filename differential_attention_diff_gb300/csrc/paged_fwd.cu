@@ -79,12 +79,12 @@ __device__ __forceinline__ bool wait_bar(const Shared& sh, uint32_t bar, uint32_
   }
 }
 
-template <int D>
+template <int D, int kTurns>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ PagedShare share;
+  __shared__ PagedShares<kTurns> share;
   Shared sh;
   {
     const uint32_t raw = smem_u32(smem_raw);
@@ -133,7 +133,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = *sh.tmem_slot();
   // the item's tokens have two Q tiles (A and B over the same key tiles), or one
   // (A and B over every other key tile)
-  auto two = [&](const PagedWalk& w) { return w.tokens > a.tq1; };
+  auto two = [&](const PagedWalk<kTurns>& w) { return w.tokens > a.tq1; };
 
   if (warp == 8) {
     // ------------------------------------------------------ TMA producer --
@@ -144,7 +144,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     int kv_it = 0, it = 0;
     bool ok = true;
-    for (PagedWalk w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 0) ok = wait_warp(sh.bar(B_QEMPTY), (it - 1) & 1, 0x8001);
       if (ok && lane == 0) {
@@ -208,7 +208,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       auto full = [&](int bar, int x, uint32_t site) {  // of tile x's stage
         return wait_bar(sh, sh.bar(bar + (x & 1)), (x >> 1) & 1, a.status, site);
       };
-      for (PagedWalk w(a, share); w.more() && ok; w.next(), ++it) {
+      for (PagedWalk<kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
         const int tiles = w.j1 - w.j;
         if (!wait_bar(sh, sh.bar(B_QFULL), it & 1, a.status, 0x8101)) break;
         if (!full(B_KFULL, kv_it, 0x8102)) break;
@@ -300,11 +300,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int my_tok = row / a.G;
     const bool in_tile = row < a.tq1 * a.G;  // 128 need not be a multiple of G
     float* xm = sh.xm();
-    int it = 0, kv_it = 0, flags = 0;
+    int it = 0, kv_it = 0, flags = 0, done = 0;
     uint32_t sc[2] = {0, 0};
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = false;
-    for (PagedWalk w(a, share); w.more(); w.next(), ++it) {
+    for (PagedWalk<kTurns> w(a, share); w.more(); w.next(), ++it) {
       const bool dual = two(w);
       const int tiles = w.j1 - w.j, steps = dual ? 2 * tiles : tiles;
       float m_run[2] = {0.f, 0.f}, l_half[2] = {0.f, 0.f};
@@ -404,7 +404,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ok = false;
         break;
       }
-      const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (w.begins() ? 1 : 0)) * a.rows;
+      const int64_t part = static_cast<int64_t>(2 * w.number() + (w.begins() ? 1 : 0)) * a.rows;
 #pragma unroll 1
       for (int s = 0; s < (dual ? 2 : 1); ++s) {
         const int tok = (s ? a.tq1 : 0) + my_tok;
@@ -472,12 +472,16 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
       if (w.begins() && !w.ends()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
+      if (w.last()) {
+        desc.flags |= flags;
+        if (threadIdx.x == 0) a.desc[w.number()] = desc;
+        desc.flags = flags = 0;
+        done = w.k + 1;
+      }
       tc_fence_before();
     }
-    if (threadIdx.x == 0) {
-      desc.flags = ok ? desc.flags | flags : 0;
-      a.desc[blockIdx.x] = desc;
-    }
+    // shares that there are not, or that were given up
+    for (int k = done; threadIdx.x == 0 && k < kTurns; ++k) a.desc[k * gridDim.x + blockIdx.x] = PagedDesc{0, 0, 0, 0};
     if (!synced) cudaGridDependencySynchronize();  // the merge counts on the gate's end
   }
 
@@ -487,7 +491,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, int kTurns>
 cudaError_t launch_d(const PagedArgs& a, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   const da_paged_cache& c = a.cache;
@@ -495,16 +499,20 @@ cudaError_t launch_d(const PagedArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   static OncePerDevice once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(paged_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return cudaFuncSetAttribute(paged_fwd_kernel<D, kTurns>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch_ahead(paged_fwd_kernel<D>, dim3(a.grid), dim3(kThreads), kSmemBytes, s, a.after_gate, tq, tk, tv, a);
+  return launch_ahead(paged_fwd_kernel<D, kTurns>, dim3(a.grid), dim3(kThreads), kSmemBytes, s, a.after_gate, tq, tk, tv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_fwd(const PagedArgs& a, cudaStream_t s) {
-  const cudaError_t e = a.cache.d == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+  cudaError_t e;
+  if (a.turns > 1)
+    e = a.cache.d == 128 ? launch_d<128, kPagedMaxTurns>(a, s) : launch_d<64, kPagedMaxTurns>(a, s);
+  else
+    e = a.cache.d == 128 ? launch_d<128, 1>(a, s) : launch_d<64, 1>(a, s);
   return e == cudaSuccess ? launch_paged_merge(a, s) : e;
 }
 

@@ -2,9 +2,9 @@
 // (paged.cuh): the softmax rule over each part's maximum and sum, then even -
 // gate * odd.
 //
-// Block (c, y) looks after a share of the pairs of the item that CTA c of the
-// attention began and did not end, if there is one: its parts are slot 2c + 1 and
-// then the slots 2c', c' = c + 1, ..., up to the CTA that ends it.  An item of a
+// Block (x, y) looks after some pairs of the items that CTA x of the attention
+// began and did not end in one of its shares: for share c the parts are slot 2c + 1
+// and then the slots 2c', c' = c + 1, ..., up to the share that ends it.  An item of a
 // prompt has many pairs and few parts (of many key tiles each): a warp takes a
 // pair, d / 32 features of both heads to a lane, and nothing is shared.  One of a
 // decode step has few pairs and may have many parts: the block takes a pair, its
@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 1024;  // of an item: CTAs of a grid
+constexpr int kMaxParts = 2048;  // of an item: shares
 constexpr int kFew = 8;          // parts that a warp joins by itself
 
 template <int D>
@@ -65,115 +65,125 @@ paged_merge_kernel(PagedArgs a) {
   __shared__ float weight[2][kMaxParts];
   __shared__ float inv[2];
   __shared__ float sums[kWays][2][D];
+  __shared__ uint32_t open;
   __shared__ int last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = blockIdx.x;
-  if (tid == 0) last = a.grid - 1;
-  __syncthreads();
+  const int shares = a.grid * a.turns;
   cudaGridDependencySynchronize();  // the parts (and, behind them, the gate)
-  // the CTA that ends the item: the first of those that follow that ends one
-  const int next = c + 1 + tid;
-  const bool ends = next < a.grid && (a.desc[next].flags & kPagedEnds);
-  Merge<D> mg{a, a.desc[c], c, 0};
-  if (!(mg.d.flags & kPagedOpen)) return;
-  if (ends) atomicMin(&last, next);
-  for (int x = next + kThreads; x < a.grid; x += kThreads)
-    if (a.desc[x].flags & kPagedEnds) atomicMin(&last, x);
-  const int pairs = mg.d.tokens * (a.G / 2);
-  __syncthreads();
-  const int parts = mg.parts = last - c + 1;
-  if (parts <= kFew) {
-    constexpr int kPer = D / 32;
-    for (int pair = blockIdx.y * kWarps + warp; pair < pairs; pair += gridDim.y * kWarps) {
-      const int row = mg.row(pair);
-      const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
-      float x[2][kFew][kPer], o[2][kPer], iv[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-          const float* po = mg.part(i, row + e, lane * kPer);
-          if constexpr (kPer == 4)
-            *reinterpret_cast<float4*>(x[e][i]) = i < parts ? *reinterpret_cast<const float4*>(po) : make_float4(0, 0, 0, 0);
-          else
-            *reinterpret_cast<float2*>(x[e][i]) = i < parts ? *reinterpret_cast<const float2*>(po) : make_float2(0, 0);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float f = part_weight(a.part_ml, mg.slot(lane < parts ? lane : 0, row + e), lane < parts, &iv[e]);
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) o[e][q] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-          const float w = __shfl_sync(0xffffffffu, f, i);
-#pragma unroll
-          for (int q = 0; q < kPer; ++q) o[e][q] = i < parts ? fmaf(x[e][i][q], w, o[e][q]) : o[e][q];
-        }
-      }
-      uint32_t y[kPer / 2];
-      const float c0 = iv[0], c1 = iv[1] * g;
-#pragma unroll
-      for (int q = 0; q < kPer / 2; ++q)  // the products rounded apart, so that equal heads cancel with gate 1
-        y[q] = pack_bf16x2(__fsub_rn(__fmul_rn(o[0][2 * q], c0), __fmul_rn(o[1][2 * q], c1)),
-                           __fsub_rn(__fmul_rn(o[0][2 * q + 1], c0), __fmul_rn(o[1][2 * q + 1], c1)));
-      uint32_t* dst = reinterpret_cast<uint32_t*>(mg.out(pair, lane * kPer));
-#pragma unroll
-      for (int q = 0; q < kPer / 2; ++q) dst[q] = y[q];
-    }
-    return;
+  if (warp == 0) {
+    static_assert(kPagedMaxTurns <= 32, "a lane a turn");
+    const uint32_t x = __ballot_sync(0xffffffffu, lane < a.turns && (a.desc[lane * a.grid + blockIdx.x].flags & kPagedOpen));
+    if (lane == 0) open = x;
   }
-  const int col = tid % D, way = tid / D;
-  for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
-    const int row = mg.row(pair);
-    // the parts' weights: warp e takes head e of the pair
-    if (warp < 2) {
-      float m = -INFINITY;
-      for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[mg.slot(i, row + warp) * 2]);
-#pragma unroll
-      for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float base = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
-      for (int i = lane; i < parts; i += 32) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + mg.slot(i, row + warp) * 2);
-        const float f = exp2f(ml.x - base);
-        weight[warp][i] = f;
-        l = fmaf(ml.y, f, l);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) inv[warp] = 1.f / l;
-    }
+  __syncthreads();
+  for (uint32_t todo = open; todo; todo &= todo - 1) {
+    const int c = (__ffs(todo) - 1) * a.grid + blockIdx.x;
+    __syncthreads();  // `last` of the item before has been read
+    if (tid == 0) last = shares - 1;
+    // the share that ends the item: the first of those that follow that ends one
+    const int next = c + 1 + tid;
+    const bool ends = next < shares && (a.desc[next].flags & kPagedEnds);
+    Merge<D> mg{a, a.desc[c], c, 0};
     __syncthreads();
-    float o0 = 0.f, o1 = 0.f;
+    if (ends) atomicMin(&last, next);
+    for (int x = next + kThreads; x < shares; x += kThreads)
+      if (a.desc[x].flags & kPagedEnds) atomicMin(&last, x);
+    const int pairs = mg.d.tokens * (a.G / 2);
+    __syncthreads();
+    const int parts = mg.parts = last - c + 1;
+    if (parts <= kFew) {
+      constexpr int kPer = D / 32;
+      for (int pair = blockIdx.y * kWarps + warp; pair < pairs; pair += gridDim.y * kWarps) {
+        const int row = mg.row(pair);
+        const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
+        float x[2][kFew][kPer], o[2][kPer], iv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int i = 0; i < kFew; ++i) {
+            const float* po = mg.part(i, row + e, lane * kPer);
+            if constexpr (kPer == 4)
+              *reinterpret_cast<float4*>(x[e][i]) = i < parts ? *reinterpret_cast<const float4*>(po) : make_float4(0, 0, 0, 0);
+            else
+              *reinterpret_cast<float2*>(x[e][i]) = i < parts ? *reinterpret_cast<const float2*>(po) : make_float2(0, 0);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = part_weight(a.part_ml, mg.slot(lane < parts ? lane : 0, row + e), lane < parts, &iv[e]);
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) o[e][q] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kFew; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) o[e][q] = i < parts ? fmaf(x[e][i][q], w, o[e][q]) : o[e][q];
+          }
+        }
+        uint32_t y[kPer / 2];
+        const float c0 = iv[0], c1 = iv[1] * g;
+#pragma unroll
+        for (int q = 0; q < kPer / 2; ++q)  // the products rounded apart, so that equal heads cancel with gate 1
+          y[q] = pack_bf16x2(__fsub_rn(__fmul_rn(o[0][2 * q], c0), __fmul_rn(o[1][2 * q], c1)),
+                             __fsub_rn(__fmul_rn(o[0][2 * q + 1], c0), __fmul_rn(o[1][2 * q + 1], c1)));
+        uint32_t* dst = reinterpret_cast<uint32_t*>(mg.out(pair, lane * kPer));
+#pragma unroll
+        for (int q = 0; q < kPer / 2; ++q) dst[q] = y[q];
+      }
+      continue;
+    }
+    const int col = tid % D, way = tid / D;
+    for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
+      const int row = mg.row(pair);
+      // the parts' weights: warp e takes head e of the pair
+      if (warp < 2) {
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[mg.slot(i, row + warp) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+          const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + mg.slot(i, row + warp) * 2);
+          const float f = exp2f(ml.x - base);
+          weight[warp][i] = f;
+          l = fmaf(ml.y, f, l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) inv[warp] = 1.f / l;
+      }
+      __syncthreads();
+      float o0 = 0.f, o1 = 0.f;
 #pragma unroll 4
-    for (int i = way; i < parts; i += kWays) {
-      const float* o = mg.part(i, row, col);
-      o0 = fmaf(o[0], weight[0][i], o0);
-      o1 = fmaf(o[a.part_row], weight[1][i], o1);
-    }
-    sums[way][0][col] = o0;
-    sums[way][1][col] = o1;
-    __syncthreads();
-    if (way == 0) {
-      for (int w = 1; w < kWays; ++w) {
-        o0 += sums[w][0][col];
-        o1 += sums[w][1][col];
+      for (int i = way; i < parts; i += kWays) {
+        const float* o = mg.part(i, row, col);
+        o0 = fmaf(o[0], weight[0][i], o0);
+        o1 = fmaf(o[a.part_row], weight[1][i], o1);
       }
-      const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
-      *mg.out(pair, col) = __float2bfloat16_rn(__fsub_rn(__fmul_rn(o0, inv[0]), __fmul_rn(o1, inv[1] * g)));
+      sums[way][0][col] = o0;
+      sums[way][1][col] = o1;
+      __syncthreads();
+      if (way == 0) {
+        for (int w = 1; w < kWays; ++w) {
+          o0 += sums[w][0][col];
+          o1 += sums[w][1][col];
+        }
+        const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
+        *mg.out(pair, col) = __float2bfloat16_rn(__fsub_rn(__fmul_rn(o0, inv[0]), __fmul_rn(o1, inv[1] * g)));
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t s) {
-  if (a.grid > kMaxParts) return cudaErrorInvalidValue;
-  if (a.grid < 2) return cudaSuccess;  // one CTA cuts nothing
+  if (a.grid * a.turns > kMaxParts) return cudaErrorInvalidValue;
+  if (a.grid * a.turns < 2) return cudaSuccess;  // one share cuts nothing
   const int pairs = a.tq * a.G / 2;
-  const dim3 grid(a.grid - 1, pairs < 16 ? pairs : 16);
+  const dim3 grid(a.grid, pairs < 16 ? pairs : 16);
   if (a.cache.d == 128) return launch_ahead(paged_merge_kernel<128>, grid, dim3(kThreads), 0, s, true, a);
   return launch_ahead(paged_merge_kernel<64>, grid, dim3(kThreads), 0, s, true, a);
 }
