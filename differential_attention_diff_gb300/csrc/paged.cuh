@@ -2,10 +2,14 @@
 // kernels that do it (paged_fwd.cu) and the one that joins their parts
 // (paged_merge.cu).
 //
-// The unit of work is one tile of 128 keys for one item: up to `tq` new tokens
-// of one sequence with all G query heads of one KV head.  The units of a call
-// form a line, (sequence, KV head, item, key tile) in this order, and share c of C
-// is its c-th equal piece, wherever that begins and ends.  So a batch of any
+// The work is tiles of 128 keys for items: up to `tq` new tokens of one sequence
+// with all G query heads of one KV head.  A tile costs some units of time, and so
+// does an item by itself (its queries, its end), before its first tile: without
+// that the CTA with the first items of a long prompt, of one tile each, would be
+// the last (8192 of 8192 tokens, 64 query heads: 843 us, 724 with it).  The units of a call form a
+// line, (sequence, KV head, item, key tile) in this order, and share c of C is its
+// c-th equal piece, wherever that begins and ends; a tile belongs to the share in
+// which it begins.  So a batch of any
 // lengths loads the SMs evenly, whether it is one long sequence or many short
 // ones, and only the items that a share's end cuts are left to be joined: at most
 // C - 1, whatever the batch.  A share has at most two such parts, the rest of an
@@ -16,7 +20,7 @@
 // and values do not fit L2 and are read for many items: the CTAs then take the
 // first shares of all, the next ones, and so on, so that what is read at a time is
 // a stretch of the line that fits (4 x 2048 tokens of 16384, 64 query and 8 KV
-// heads: 2977 us with one share to a CTA, 2768 with six).
+// heads: 2870 us with one share to a CTA, 2715 with four).
 #pragma once
 
 #include "common.cuh"
@@ -26,8 +30,17 @@
 namespace da {
 
 constexpr int kPagedTile = 128;  // keys
+// What a tile costs (one of an item with two MMA tiles, with one), and an item
+// beside its tiles: 1.5 and 1 us and about 4 us.  With few tokens the memory does
+// not wait for an item's end.
+struct PagedCostFwd {
+  static constexpr int kTile = 3, kTileOne = 2, kItem = 8;
+};
+struct PagedCostFew {
+  static constexpr int kTile = 1, kTileOne = 1, kItem = 0;
+};
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
-constexpr int kTurnUnits = 128;           // of a share, where there are several turns
+constexpr int kTurnTiles = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
 
 __device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
@@ -52,9 +65,17 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
   return s;
 }
 
-// Key tiles of the first i items of a sequence with n new tokens, length L.
-__device__ __forceinline__ int64_t tiles_before(int i, int n, int L, int tq) {
-  return floor_sum(i, kPagedTile, tq, static_cast<int64_t>(L) - n + tq + kPagedTile - 1);
+// Units of the first i items of a sequence with n new tokens, length L; all but its
+// last item are whole.
+template <class Cost>
+__device__ __forceinline__ int64_t units_before(const PagedArgs& a, int i, int n, int L) {
+  return Cost::kTile * floor_sum(i, kPagedTile, a.tq, static_cast<int64_t>(L) - n + a.tq + kPagedTile - 1) +
+         static_cast<int64_t>(Cost::kItem) * i;
+}
+// A tile's cost for an item of so many tokens.
+template <class Cost>
+__device__ __forceinline__ int tile_cost(const PagedArgs& a, int tokens) {
+  return Cost::kTile == Cost::kTileOne || tokens > a.tq1 ? Cost::kTile : Cost::kTileOne;
 }
 
 // A sequence of the batch as the arrays have it.
@@ -68,15 +89,17 @@ struct PagedSequence {
 };
 
 // Its units for one KV head, 0 if it is out of bounds (then *bad).
-__device__ __forceinline__ int64_t sequence_units(const da_paged_cache& c, const PagedSequence& s, int tq, bool* bad) {
-  if (!paged_sequence_ok(c, s.t0, s.t1, s.L)) {
+template <class Cost>
+__device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, bool* bad) {
+  if (!paged_sequence_ok(a.cache, s.t0, s.t1, s.L)) {
     *bad = true;
     return 0;
   }
   const int n = s.t1 - s.t0;
   if (n == 0) return 0;
-  const int64_t last = (s.L + kPagedTile - 1) / kPagedTile;
-  return n <= tq ? last : tiles_before((n - 1) / tq, n, s.L, tq) + last;
+  const int before = n <= a.tq ? 0 : (n - 1) / a.tq;  // items before the last
+  const int64_t last = static_cast<int64_t>((s.L + kPagedTile - 1) / kPagedTile) * tile_cost<Cost>(a, n - before * a.tq) + Cost::kItem;
+  return before ? units_before<Cost>(a, before, n, s.L) + last : last;
 }
 
 // x / y, in 32 bits where that will do (a 64-bit division takes some 100 instructions)
@@ -87,7 +110,8 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 
 // A CTA's shares: where each begins and how long it is.
 struct PagedShare {
-  int b, g, i, j;
+  int b, g, i;
+  int from;       // its first unit in that item
   int64_t units;
 };
 template <int kTurns>  // the most that a CTA may have
@@ -100,7 +124,7 @@ struct PagedShares {
 // Fills *out (shared memory); called by all kThreads of a block, with sequence
 // threadIdx.x (where there is one) in `mine`: fetched at the kernel's start, since
 // the rest waits for it.
-template <int kThreads, int kTurns>
+template <class Cost, int kThreads, int kTurns>
 __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, PagedShares<kTurns>* out) {
   static_assert(kThreads % 32 == 0, "whole warps");
   constexpr int kW = kThreads / 32;
@@ -110,12 +134,12 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   bool bad = false;
   // inclusive sums over the warp's sequences, and each round's over the warps:
   // the first round's stay in registers, which for kThreads sequences are all
-  int64_t per = tid < B ? sequence_units(a.cache, mine, a.tq, &bad) : 0;
+  int64_t per = tid < B ? sequence_units<Cost>(a, mine, &bad) : 0;
   int64_t incl = per * a.cache.h_kv, rest = 0, keys = per ? mine.L : 0;
   for (int b = tid + kThreads; b < B; b += kThreads) {
     PagedSequence s;
     s.load(a.cache, b);
-    const int64_t u = sequence_units(a.cache, s, a.tq, &bad);
+    const int64_t u = sequence_units<Cost>(a, s, &bad);
     rest += u * a.cache.h_kv;
     keys += u ? s.L : 0;
   }
@@ -156,13 +180,15 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   // values, and a share is long enough to outweigh its two cut items
   int turns = 1;
   if constexpr (kTurns > 1) {
-    const int64_t by_bytes = (keys * a.cache.h_kv * a.cache.d * 4) / kTurnBytes, by_units = quotient(total, gridDim.x) / kTurnUnits;
+    const int64_t by_bytes = (keys * a.cache.h_kv * a.cache.d * 4) / kTurnBytes, by_units = quotient(total, static_cast<int64_t>(gridDim.x) * Cost::kTile * kTurnTiles);
     const int64_t t = by_bytes < by_units ? by_bytes : by_units;
     turns = static_cast<int>(t < 1 ? 1 : t < kTurns ? t : kTurns);
   }
-  // equal shares, the first `more` of them one unit longer; less than a unit makes no sense
-  const int64_t all = static_cast<int64_t>(turns) * gridDim.x, shares = total < all ? total : all;
-  const int64_t each = shares ? quotient(total, shares) : 0, more = total - each * shares;
+  // equal shares, the first `more` of them one unit longer; none shorter than a
+  // tile, so that an item's parts follow each other without a gap
+  const int64_t all = static_cast<int64_t>(turns) * gridDim.x, most = Cost::kTile == 1 ? total : quotient(total, Cost::kTile);
+  const int64_t shares = most < 1 ? 1 : most < all ? most : all;
+  const int64_t each = quotient(total, shares), more = total - each * shares;
   auto begin = [&](int64_t c) { return c * each + (c < more ? c : more); };
   auto length = [&](int64_t c) { return c < shares ? each + (c < more) : 0; };
   if (tid == 0) {
@@ -183,7 +209,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
       int lo = 0, hi = (n + a.tq - 1) / a.tq;  // the item: the last that begins at or before off
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (tiles_before(mid, n, s.L, a.tq) <= off)
+        if (units_before<Cost>(a, mid, n, s.L) <= off)
           lo = mid;
         else
           hi = mid;
@@ -191,7 +217,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
       out->share[k].b = r + tid;
       out->share[k].g = g;
       out->share[k].i = lo;
-      out->share[k].j = static_cast<int>(off - (lo ? tiles_before(lo, n, s.L, a.tq) : 0));
+      out->share[k].from = static_cast<int>(off - (lo ? units_before<Cost>(a, lo, n, s.L) : 0));
     }
     r += kThreads;
     if (r >= B || begin(static_cast<int64_t>(turns - 1) * gridDim.x + blockIdx.x) < base) break;
@@ -199,7 +225,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     per = 0;
     if (r + tid < B) {
       s.load(a.cache, r + tid);
-      per = sequence_units(a.cache, s, a.tq, &bad);
+      per = sequence_units<Cost>(a, s, &bad);
     }
     incl = per * a.cache.h_kv;
 #pragma unroll
@@ -220,31 +246,51 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
 }
 
 // A CTA's way along its shares, part by part; every warp walks by itself.
-template <int kTurns>
+template <class Cost, int kTurns>
 struct PagedWalk {
   const PagedArgs& a;
   const PagedShares<kTurns>& s;
   int k;                // the share, of this CTA's
   int b, g, i, j;       // the part's item and first key tile
-  int64_t left;         // units that are left of the share, this part's counted in
   int t0, n, L;         // the sequence
   int tokens, tiles, j1;  // the item's tokens and key tiles; the part ends before tile j1
   __device__ __forceinline__ PagedWalk(const PagedArgs& a_, const PagedShares<kTurns>& s_) : a(a_), s(s_), k(0) { share(); }
   // the share's number, of all
   __device__ __forceinline__ int number() const { return (kTurns > 1 ? k * static_cast<int>(gridDim.x) : 0) + static_cast<int>(blockIdx.x); }
-  __device__ __forceinline__ bool last() const { return left <= j1 - j; }  // of the share
-  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool more() const { return j < j1; }
   __device__ __forceinline__ bool begins() const { return j == 0; }
   __device__ __forceinline__ bool ends() const { return j1 == tiles; }
   // position of the item's first token
   __device__ __forceinline__ int first_position() const { return L - n + i * a.tq; }
   __device__ __forceinline__ void next() {
-    left -= j1 - j;
-    if (left <= 0) {
-      if (kTurns > 1 && ++k < s.count) share();
-      return;
+    advance();
+    find();
+  }
+
+ private:
+  int64_t left;  // units that are left of the share, this part's counted in
+  int from, end;  // this part's units in the item (at most 2^23 tiles)
+  // to the first part with a tile, in this share or the next; none: j = j1
+  __device__ __forceinline__ void find() {
+    while (true) {
+      if (left <= 0) {
+        if (kTurns == 1 || k + 1 >= s.count) {
+          j = j1 = 0;
+          return;
+        }
+        ++k;
+        start();
+        continue;
+      }
+      item();
+      if (j < j1) return;
+      advance();
     }
-    j = 0;
+  }
+  __device__ __forceinline__ void advance() {
+    left -= end - from;
+    from = 0;
+    if (left <= 0) return;
     if ((i + 1) * a.tq < n) {
       ++i;
     } else {
@@ -255,20 +301,21 @@ struct PagedWalk {
         sequence();
       }
     }
-    item();
   }
-
- private:
   __device__ __forceinline__ void share() {
+    j = j1 = 0;
+    start();
+    find();
+  }
+  __device__ __forceinline__ void start() {
     const PagedShare& x = s.share[k];
     left = x.units;
     if (left <= 0) return;
     b = x.b;
     g = x.g;
     i = x.i;
-    j = x.j;
+    from = x.from;
     sequence();
-    item();
   }
   __device__ __forceinline__ void sequence() {
     for (;; ++b) {  // there is one with work, since units are left
@@ -282,7 +329,16 @@ struct PagedWalk {
   __device__ __forceinline__ void item() {
     tokens = min(a.tq, n - i * a.tq);
     tiles = (first_position() + tokens + kPagedTile - 1) / kPagedTile;
-    j1 = left < tiles - j ? j + static_cast<int>(left) : tiles;
+    const int cost = tile_cost<Cost>(a, tokens), all = tiles * cost + Cost::kItem;
+    const bool cut = left < all - from;
+    end = cut ? from + static_cast<int>(left) : all;
+    j = from == 0 ? 0 : tile_at(from, cost);
+    j1 = cut ? tile_at(end, cost) : tiles;
+  }
+  // the tiles that begin before unit u of the item
+  __device__ __forceinline__ int tile_at(int u, int cost) const {
+    if (Cost::kTile == 1) return u - Cost::kItem;
+    return u <= Cost::kItem ? 0 : static_cast<int>(static_cast<uint32_t>(u - Cost::kItem + cost - 1) / static_cast<uint32_t>(cost));
   }
 };
 

@@ -179,7 +179,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<F::kThreads>(a, mine, &share);
+  paged_share<PagedCostFew, F::kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
@@ -195,7 +195,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int it = 0, st = 0;
     uint32_t round = 0;  // of the rings
     bool ok = true;
-    for (PagedWalk<1> w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<PagedCostFew, 1> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
       if (!ok) break;
@@ -239,7 +239,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const uint32_t v0 = sdesc_lo(base + F::kOffV, 1024), p0 = sdesc_lo(base + F::kOffP, 16);
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) { return wait_bar(&abort_flag, b, parity, a.status, site); };
       // S of tile x (of the CTA's share) for the item that a walk of its own is at
-      PagedWalk<1> ahead(a, share);
+      PagedWalk<PagedCostFew, 1> ahead(a, share);
       int it = 0, j = ahead.j, ks = 0;
       uint32_t k_round = 0;
       auto start = [&](int x) {
@@ -262,12 +262,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         return true;
       };
-      const int total = static_cast<int>(share.share[0].units);  // (one share to a CTA here)
       int vs = 0;
       uint32_t v_round = 0;
-      bool ok = total == 0 || start(0);
-      for (int x = 0; x < total && ok; ++x) {
-        if (x + 1 < total && !start(x + 1)) break;
+      bool more = ahead.more() && start(0);
+      for (int x = 0; more; ++x) {
+        more = ahead.more();
+        if (more && !start(x + 1)) break;
         if (!wait(bar(B_VFULL + vs), v_round & 1, 0x9103) || !wait(bar(B_PFULL + (x & 1)), (x >> 1) & 1, 0x9104)) break;
         tc_fence_after();
         const uint32_t v = v0 + vs * kTile, p = p0 + (x & (F::kPBufs - 1)) * (F::kPBytes >> 4);
@@ -299,7 +299,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint32_t v_round = 0;
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = false;
-    for (PagedWalk<1> w(a, share); w.more(); w.next()) {
+    for (PagedWalk<PagedCostFew, 1> w(a, share); w.more(); w.next()) {
       const int cols = w.tokens * a.G - n0;  // the item's columns, from n0 on
       float m[kC], l[kC], o[kC];
 #pragma unroll

@@ -125,7 +125,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<kThreads>(a, mine, &share);
+  paged_share<PagedCostFwd, kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
@@ -133,7 +133,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = *sh.tmem_slot();
   // the item's tokens have two Q tiles (A and B over the same key tiles), or one
   // (A and B over every other key tile)
-  auto two = [&](const PagedWalk<kTurns>& w) { return w.tokens > a.tq1; };
+  auto two = [&](const PagedWalk<PagedCostFwd, kTurns>& w) { return w.tokens > a.tq1; };
 
   if (warp == 8) {
     // ------------------------------------------------------ TMA producer --
@@ -144,7 +144,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     int kv_it = 0, it = 0;
     bool ok = true;
-    for (PagedWalk<kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<PagedCostFwd, kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 0) ok = wait_warp(sh.bar(B_QEMPTY), (it - 1) & 1, 0x8001);
       if (ok && lane == 0) {
@@ -208,7 +208,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       auto full = [&](int bar, int x, uint32_t site) {  // of tile x's stage
         return wait_bar(sh, sh.bar(bar + (x & 1)), (x >> 1) & 1, a.status, site);
       };
-      for (PagedWalk<kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
+      for (PagedWalk<PagedCostFwd, kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
         const int tiles = w.j1 - w.j;
         if (!wait_bar(sh, sh.bar(B_QFULL), it & 1, a.status, 0x8101)) break;
         if (!full(B_KFULL, kv_it, 0x8102)) break;
@@ -300,11 +300,15 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int my_tok = row / a.G;
     const bool in_tile = row < a.tq1 * a.G;  // 128 need not be a multiple of G
     float* xm = sh.xm();
-    int it = 0, kv_it = 0, flags = 0, done = 0;
+    int it = 0, kv_it = 0, done = 0;  // done: shares whose parts are all described
     uint32_t sc[2] = {0, 0};
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = false;
-    for (PagedWalk<kTurns> w(a, share); w.more(); w.next(), ++it) {
+    for (PagedWalk<PagedCostFwd, kTurns> w(a, share); w.more(); w.next(), ++it) {
+      for (; kTurns > 1 && done < w.k; ++done) {
+        if (threadIdx.x == 0) a.desc[done * gridDim.x + blockIdx.x] = desc;
+        desc = PagedDesc{0, 0, 0, 0};
+      }
       const bool dual = two(w);
       const int tiles = w.j1 - w.j, steps = dual ? 2 * tiles : tiles;
       float m_run[2] = {0.f, 0.f}, l_half[2] = {0.f, 0.f};
@@ -470,18 +474,14 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (!whole && valid && wg == 0)
           *reinterpret_cast<float2*>(a.part_ml + (part + s * 128 + row) * 2) = make_float2(m, l);
       }
-      if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
-      if (w.begins() && !w.ends()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
-      if (w.last()) {
-        desc.flags |= flags;
-        if (threadIdx.x == 0) a.desc[w.number()] = desc;
-        desc.flags = flags = 0;
-        done = w.k + 1;
-      }
+      if (!w.begins()) desc.flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
+      if (w.begins() && !w.ends()) desc = PagedDesc{desc.flags | kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       tc_fence_before();
     }
-    // shares that there are not, or that were given up
-    for (int k = done; threadIdx.x == 0 && k < kTurns; ++k) a.desc[k * gridDim.x + blockIdx.x] = PagedDesc{0, 0, 0, 0};
+    for (; done < kTurns; ++done) {
+      if (threadIdx.x == 0) a.desc[done * gridDim.x + blockIdx.x] = ok ? desc : PagedDesc{0, 0, 0, 0};
+      desc = PagedDesc{0, 0, 0, 0};
+    }
     if (!synced) cudaGridDependencySynchronize();  // the merge counts on the gate's end
   }
 
