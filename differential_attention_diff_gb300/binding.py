@@ -933,22 +933,32 @@ def diffattn_rope_inv_freq(rot_dim, base=10000.0, *, stretch=None, factor=1.0, t
 
 def _rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev):
     """The rotation's and the norm's fields, from rot_dim to k_weight."""
-    f32 = torch.float32
     if rot_dim is None:
         rot_dim = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    f32 = torch.float32
     return (rot_dim, interleaved, _array(inv_freq, (rot_dim // 2,), f32, dev, "inv_freq"), rope_scale, norm, norm_eps,
-            _array(q_weight, (d,), f32, dev, "q_weight"), _array(k_weight, (d,), f32, dev, "k_weight"))
+            0 if q_weight is None else _array(q_weight, (d,), f32, dev, "q_weight"),
+            0 if k_weight is None else _array(k_weight, (d,), f32, dev, "k_weight"))
 
 
 _NO_T4, _NO_T3 = (0, 0, 0, 0), (0, 0, 0)
 
 
-def _qk_fields(q, k, B, N, d, dtype, dev, names):
-    """The da_t4 fields of a tensor of queries and one of keys, either may be None."""
-    out = ()
-    for t, name in ((q, names[0]), (k, names[1])):
-        out += _NO_T4 if t is None else _rows4(t, (B, N, t.shape[2], d), dtype, dev, name)
-    return out
+def _out(like, stream):
+    """A new tensor of the shape and type of `like`, on the stream that the call launches on."""
+    if stream is None:
+        return like.new_empty(like.shape)
+    with torch.cuda.stream(stream):
+        return like.new_empty(like.shape)
+
+
+def _heads4(t, B, N, d, dtype, dev, name, heads=None):
+    """The da_t4 fields of a tensor [B, N, heads, d], of any heads where None; none of a tensor that is None."""
+    if t is None:
+        if heads:
+            raise ValueError(f"{name}: a tensor of {heads} heads expected, got None")
+        return _NO_T4
+    return _rows4(t, (B, N, t.shape[2] if heads is None else heads, d), dtype, dev, name)
 
 
 def diffattn_qk_rope_fwd(q, k, inv_freq, *, positions=None, rot_dim=None, interleaved=False, rope_scale=1.0, norm=False,
@@ -956,29 +966,26 @@ def diffattn_qk_rope_fwd(q, k, inv_freq, *, positions=None, rot_dim=None, interl
     """Queries [B, N, h_q, d] and keys [B, N, h_k, d] (bf16 or fp32; either may be None) normed per head (norm; fp32
     [d] weights, None = unit) and their first rot_dim (None = all that inv_freq has) features rotated by their
     positions (int32 [B, N], None = 0 .. N-1).  Returns (q_out, k_out), which may be q and k themselves."""
-    some = q if q is not None else k
+    some = k if q is None else q
     dev, raw = _device(some, stream)
     B, N, _, d = some.shape
     dtype = some.dtype
-    if q is not None and q_out is None:
-        q_out = _new(torch.empty, q, q.shape, dtype, stream)
-    if k is not None and k_out is None:
-        k_out = _new(torch.empty, k, k.shape, dtype, stream)
-    h_q, h_k = 0 if q is None else q.shape[2], 0 if k is None else k.shape[2]
-    _same_heads(q, q_out, "q_out")
-    _same_heads(k, k_out, "k_out")
+    h_q = h_k = 0
+    if q is not None:
+        h_q = q.shape[2]
+        if q_out is None:
+            q_out = _out(q, stream)
+    if k is not None:
+        h_k = k.shape[2]
+        if k_out is None:
+            k_out = _out(k, stream)
     _call("diffattn_qk_rope_fwd", _pack_rope_fwd(
         B, N, h_q, h_k, d, _dtype_code(some),
         *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
-        _array(positions, (B, N), torch.int32, dev, "positions"), *_qk_fields(q, k, B, N, d, dtype, dev, ("q", "k")),
-        *_qk_fields(q_out, k_out, B, N, d, dtype, dev, ("q_out", "k_out"))), raw)
+        0 if positions is None else _array(positions, (B, N), torch.int32, dev, "positions"),
+        *_heads4(q, B, N, d, dtype, dev, "q"), *_heads4(k, B, N, d, dtype, dev, "k"),
+        *_heads4(q_out, B, N, d, dtype, dev, "q_out", h_q), *_heads4(k_out, B, N, d, dtype, dev, "k_out", h_k)), raw)
     return q_out, k_out
-
-
-def _same_heads(t, other, name):
-    if (t is None) != (other is None) or t is not None and t.shape != other.shape:
-        raise ValueError(f"{name}: a tensor of {None if t is None else tuple(t.shape)} expected, got "
-                         f"{None if other is None else tuple(other.shape)}")
 
 
 def diffattn_qk_rope_bwd_workspace_size(B, N, h_q, h_k, d) -> int:
@@ -991,39 +998,37 @@ def diffattn_qk_rope_bwd(q, k, dq_out, dk_out, inv_freq, *, positions=None, rot_
     """Gradients of diffattn_qk_rope_fwd given those of its outputs: dict(dq, dk) and, with norm (unless want_weights
     is False), dq_weight and dk_weight, fp32 [d].  q and k are needed with norm only.  dq and dk may be dq_out and
     dk_out themselves."""
-    some = dq_out if dq_out is not None else dk_out
+    some = dk_out if dq_out is None else dq_out
     dev, raw = _device(some, stream)
     B, N, _, d = some.shape
-    dtype = some.dtype
-    if dq_out is not None and dq is None:
-        dq = _new(torch.empty, some, dq_out.shape, dtype, stream)
-    if dk_out is not None and dk is None:
-        dk = _new(torch.empty, some, dk_out.shape, dtype, stream)
-    _same_heads(dq_out, dq, "dq")
-    _same_heads(dk_out, dk, "dk")
-    if norm:
-        _same_heads(dq_out, q, "q")
-        _same_heads(dk_out, k, "k")
-    else:
-        q = k = None
-    if want_weights is None:
-        want_weights = norm
-    h_q, h_k = 0 if dq_out is None else dq_out.shape[2], 0 if dk_out is None else dk_out.shape[2]
-    if want_weights:
-        if dq_weight is None and h_q:
-            dq_weight = _new(torch.empty, some, (d,), torch.float32, stream)
-        if dk_weight is None and h_k:
-            dk_weight = _new(torch.empty, some, (d,), torch.float32, stream)
+    dtype, f32 = some.dtype, torch.float32
+    h_q = h_k = 0
+    want = norm if want_weights is None else want_weights
+    if dq_out is not None:
+        h_q = dq_out.shape[2]
+        if dq is None:
+            dq = _out(dq_out, stream)
+        if want and dq_weight is None:
+            dq_weight = _new(torch.empty, some, (d,), f32, stream)
+    if dk_out is not None:
+        h_k = dk_out.shape[2]
+        if dk is None:
+            dk = _out(dk_out, stream)
+        if want and dk_weight is None:
+            dk_weight = _new(torch.empty, some, (d,), f32, stream)
     if workspace is None and (dq_weight is not None or dk_weight is not None):
         need = _need(dev, "diffattn_qk_rope_bwd_workspace_size", B, N, h_q, h_k, d)
         workspace = _new(torch.empty, some, (max(need, 1),), torch.uint8, stream)
     _call("diffattn_qk_rope_bwd", _pack_rope_bwd(
         B, N, h_q, h_k, d, _dtype_code(some),
         *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
-        _array(positions, (B, N), torch.int32, dev, "positions"), *_qk_fields(q, k, B, N, d, dtype, dev, ("q", "k")),
-        *_NO_T4, *_NO_T4, *_qk_fields(dq_out, dk_out, B, N, d, dtype, dev, ("dq_out", "dk_out")),
-        *_qk_fields(dq, dk, B, N, d, dtype, dev, ("dq", "dk")), _array(dq_weight, (d,), torch.float32, dev, "dq_weight"),
-        _array(dk_weight, (d,), torch.float32, dev, "dk_weight"), *_space(workspace, dev)), raw)
+        0 if positions is None else _array(positions, (B, N), torch.int32, dev, "positions"),
+        *(_heads4(q, B, N, d, dtype, dev, "q", h_q) if norm else _NO_T4),
+        *(_heads4(k, B, N, d, dtype, dev, "k", h_k) if norm else _NO_T4), *_NO_T4, *_NO_T4,
+        *_heads4(dq_out, B, N, d, dtype, dev, "dq_out"), *_heads4(dk_out, B, N, d, dtype, dev, "dk_out"),
+        *_heads4(dq, B, N, d, dtype, dev, "dq", h_q), *_heads4(dk, B, N, d, dtype, dev, "dk", h_k),
+        0 if dq_weight is None else _array(dq_weight, (d,), f32, dev, "dq_weight"),
+        0 if dk_weight is None else _array(dk_weight, (d,), f32, dev, "dk_weight"), *_space(workspace, dev)), raw)
     return dict(dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight)
 
 
@@ -1060,14 +1065,15 @@ def diffattn_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqle
     dev, raw = _device(k, stream)
     T, hkv, d = shape = k.shape
     bf16 = torch.bfloat16
-    if q is not None and q_out is None:
-        q_out = _new(torch.zeros, q, q.shape, bf16, stream)
-    _same_heads(q, q_out, "q_out")
-    h_q = 0 if q is None else q.shape[1]
+    h_q = 0
+    if q is not None:
+        h_q = q.shape[1]
+        if q_out is None:
+            q_out = _new(torch.zeros, q, q.shape, bf16, stream)
     _call("diffattn_paged_append", _pack_paged_append(
         *_paged_fields(T, k_pages, v_pages, block_table, cu_seqlens, seqlens, dev), h_q,
         *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
-        _array(positions, (T,), torch.int32, dev, "positions"), *_rows3(k, (T, k_pages.shape[2], k_pages.shape[3]), bf16, dev, "k"),
+        0 if positions is None else _array(positions, (T,), torch.int32, dev, "positions"), *_rows3(k, (T, k_pages.shape[2], k_pages.shape[3]), bf16, dev, "k"),
         *_rows3(v, shape, bf16, dev, "v"), *(_NO_T3 if q is None else _rows3(q, (T, h_q, d), bf16, dev, "q")),
         *(_NO_T3 if q is None else _rows3(q_out, (T, h_q, d), bf16, dev, "q_out"))), raw)
     return q_out

@@ -156,6 +156,28 @@ def test_more_sequences_than_threads(max_new):
     check(t, call(t, max_new=max_new))
 
 
+def test_turns_of_the_shares():
+    """Keys that do not fit L2, read for many items: the CTAs take several shares each, whose parts are joined."""
+    t = make([260, 150, 300], [9000, 12000, 10000], 128, 16, 8, 128, layout="head", seed=4)
+    P = 400  # room for 51200 positions a sequence: 3.7 GB of keys and values at most
+    table = torch.full((3, P), -1, dtype=torch.int32, device="cuda")
+    table[:, :t["table"].shape[1]] = t["table"]
+    t["table"] = table
+    out = call(t)
+    t0 = 0
+    for n, L in zip(t["n"], t["L"]):  # one sequence by itself, its first and last tokens
+        one = dict(t, q=t["q"][t0:t0 + n], gate=t["gate"][t0:t0 + n], n=[n], L=[L], cu=i32([0, n]), sl=i32([L]),
+                   table=t["table"][t["L"].index(L)][None].contiguous())
+        alone = call(one)
+        assert float((alone.float() - out[t0:t0 + n].float()).abs().max()) <= 2.0 ** -6 * float(alone.float().abs().max())
+        few = [0, 1, n // 2, n - 1]
+        k, v = (f64(one[x][one["table"][0, :-(-L // 128)].long()].flatten(0, 1)[:L]) for x in ("k", "v"))
+        ref, size = po.attend(f64(one["q"][few]), k, v, f64(one["gate"][few]), np.array(few) + L - n + 1, sizes=True)
+        got = f64(out[t0:t0 + n][few])
+        assert np.all(np.abs(got - ref) <= (2.0 ** -8 + 2.0 ** -10) * size + 2.0 ** -8 * np.abs(ref))
+        t0 += n
+
+
 def test_scores_that_grow():
     """Scores far above the first tile's: the running maximum is raised, O rescaled; and the reverse."""
     for n, L in (([1], [1500]), ([300], [1500]), ([60], [1500])):
@@ -201,6 +223,29 @@ def test_shared_pages():
     t["table"][1, :8] = t["table"][0, :8]
     t["table"][2, :8] = t["table"][0, :8]
     check(t, call(t))
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_far_pages(n):
+    """Pages that lie more than 2^32 elements and bytes behind the first."""
+    page, hkv, d = 64, 8, 128
+    count = 2 ** 32 // (page * hkv * d) + 5  # 8.6 GB each of K and V
+    t = make([n], [200], page, 16, hkv, d)
+    far = torch.tensor([count - 1, 3, count - 4, count - 2], device="cuda")
+    pages = []
+    for x in ("k", "v"):
+        big = torch.empty((count, page, hkv, d), dtype=BF16, device="cuda")
+        big[far] = t[x][t["table"][0].long()]
+        pages.append(big)
+    near = call(t)
+    t.update(k=pages[0], v=pages[1], table=far.int()[None])
+    assert torch.equal(call(t), near)
+    check(t, near)
+    # and appended to
+    k, v = randn((n, hkv, d), gen(1)), randn((n, hkv, d), gen(2))
+    bd.diffattn_paged_append(k, v, *pages, t["table"], t["cu"], t["sl"], None)
+    j = torch.arange(200 - n, 200, device="cuda")
+    assert torch.equal(pages[0][far[j // page], j % page], k) and torch.equal(pages[1][far[j // page], j % page], v)
 
 
 @pytest.mark.parametrize("n", [[1, 1, 1], [100, 70, 90]])

@@ -305,3 +305,46 @@ def test_paged_append_out_of_bounds(what):
     assert int(torch.isnan(kp[..., 0, 0]).logical_not().sum()) == 4
     if what == "page":
         assert torch.equal(q_out, q)
+
+
+# ------------------------------------------------------------- a training step ---
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_training_step_with_the_v2_attention(interleaved):
+    """Raw queries and keys normed, rotated, attended, and all the way back: gradients of the raw rows, of the values
+    and of the norms' weights against the 64-bit chain, with the attention's own bars (1.5e-2 of a tensor's norm for
+    its backward, as much again for the bf16 rows in between)."""
+    g = gen(31)
+    B, N, h, hkv, d = 2, 130, 4, 2, 64
+    q, k, v = randn((B, N, 2 * h, d), g), randn((B, N, hkv, d), g), randn((B, N, hkv, d), g)
+    dout, gate = randn((B, N, h, d), g), torch.rand((B, N, h), generator=g, device="cuda")
+    w = [1 + randn((d,), g, F32, 0.2) for _ in range(2)]
+    f, _ = bd.diffattn_rope_inv_freq(32)
+    kw = dict(interleaved=interleaved, norm=True, q_weight=w[0], k_weight=w[1])
+    qr, kr = bd.diffattn_qk_rope_fwd(q, k, f, **kw)
+    _, saves = bd.diffattn_v2_fwd(qr, kr, v, gate=gate, save=True)
+    a = bd.diffattn_v2_bwd(qr, kr, v, dout, saves, gate=gate)
+    r = bd.diffattn_qk_rope_bwd(q, k, a["dq"], a["dk"], f, **kw)
+
+    pos = np.broadcast_to(np.arange(N), (B, N))
+    rk = dict(rot=32, interleaved=interleaved, do_norm=True)
+    q64, k64, w64 = f64(q), f64(k), [f64(x) for x in w]
+    q1, k1 = po.qk_rope(q64, f64(f), pos, w=w64[0], **rk), po.qk_rope(k64, f64(f), pos, w=w64[1], **rk)
+    gz = f64(gate)
+    dq1, dk1, dv1 = np.zeros_like(q1), np.zeros_like(k1), np.zeros_like(k1)
+    for b in range(B):  # the chain rule of the attention, head by head
+        for j in range(2 * h):
+            c = j // (2 * h // hkv)
+            t = q1[b, :, j] @ k1[b, :, c].T * d ** -0.5
+            t[np.triu_indices(N, 1)] = -np.inf
+            A = np.exp(t - t.max(-1, keepdims=True))
+            A /= A.sum(-1, keepdims=True)
+            do = f64(dout)[b, :, j // 2] * (1.0 if j % 2 == 0 else -gz[b, :, j // 2, None])
+            dP = do @ f64(v)[b, :, c].T
+            dS = A * (dP - (A * dP).sum(-1, keepdims=True)) * d ** -0.5
+            dq1[b, :, j] += dS @ k1[b, :, c]
+            dk1[b, :, c] += dS.T @ q1[b, :, j]
+            dv1[b, :, c] += A.T @ do
+    dq, dqw = po.qk_rope_bwd(q64, dq1, f64(f), pos, w=w64[0], **rk)
+    dk, dkw = po.qk_rope_bwd(k64, dk1, f64(f), pos, w=w64[1], **rk)
+    for got, exp in ((r["dq"], dq), (r["dk"], dk), (a["dv"], dv1), (r["dq_weight"], dqw), (r["dk_weight"], dkw)):
+        assert np.linalg.norm(f64(got) - exp) <= 3e-2 * np.linalg.norm(exp)
