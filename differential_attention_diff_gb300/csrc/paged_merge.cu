@@ -2,9 +2,12 @@
 // (paged.cuh): the softmax rule over each part's maximum and sum, then even -
 // gate * odd.
 //
-// Block (x, y) looks after some pairs of the items that CTA x of the attention
-// began and did not end in one of its shares: for share c the parts are slot 2c + 1
-// and then the slots 2c', c' = c + 1, ..., up to the share that ends it.  An item of a
+// Share c of the attention describes the item that it began and did not end, if
+// there is one: the item's parts are slot 2c + 1 and then the slots 2c', c' = c + 1,
+// ..., up to the share that ends it.  Every block reads all descriptions, and the
+// items' pairs are dealt to the blocks; no more of them than run at once, since a
+// block that finds nothing to do costs as much as one that does (32 sequences of
+// 4096, d 64, 4 tokens: 7 us for 152 x 16 blocks, 3 for these).  An item of a
 // prompt has many pairs and few parts (of many key tiles each): a warp takes a
 // pair, d / 32 features of both heads to a lane, and nothing is shared.  One of a
 // decode step has few pairs and may have many parts: the block takes a pair, its
@@ -18,7 +21,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 2048;  // of an item: shares
+constexpr int kBlocksPerSm = 2;
+constexpr int kMaxShares = 1024;
 constexpr int kFew = 8;          // parts that a warp joins by itself
 
 template <int D>
@@ -59,41 +63,55 @@ __device__ __forceinline__ float part_weight(const float* part_ml, int64_t slot,
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 paged_merge_kernel(PagedArgs a) {
   constexpr int kWays = kThreads / D;
-  __shared__ float weight[2][kMaxParts];
+  __shared__ float weight[2][kMaxShares];
   __shared__ float inv[2];
   __shared__ float sums[kWays][2][D];
-  __shared__ uint32_t open;
+  __shared__ uint8_t flags[kMaxShares];
+  __shared__ int16_t open[kMaxShares];  // the shares that left an item open, in order
+  __shared__ int counts[kWarps];
   __shared__ int last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int shares = a.grid * a.turns;
   cudaGridDependencySynchronize();  // the parts (and, behind them, the gate)
-  if (warp == 0) {
-    static_assert(kPagedMaxTurns <= 32, "a lane a turn");
-    const uint32_t x = __ballot_sync(0xffffffffu, lane < a.turns && (a.desc[lane * a.grid + blockIdx.x].flags & kPagedOpen));
-    if (lane == 0) open = x;
-  }
-  __syncthreads();
-  for (uint32_t todo = open; todo; todo &= todo - 1) {
-    const int c = (__ffs(todo) - 1) * a.grid + blockIdx.x;
-    __syncthreads();  // `last` of the item before has been read
-    if (tid == 0) last = shares - 1;
-    // the share that ends the item: the first of those that follow that ends one
-    const int next = c + 1 + tid;
-    const bool ends = next < shares && (a.desc[next].flags & kPagedEnds);
-    Merge<D> mg{a, a.desc[c], c, 0};
+  int n_open = 0;
+  for (int c0 = 0; c0 < shares; c0 += kThreads) {
+    const int c = c0 + tid, f = c < shares ? a.desc[c].flags : 0;
+    if (c < shares) flags[c] = static_cast<uint8_t>(f);
+    const uint32_t mask = __ballot_sync(0xffffffffu, f & kPagedOpen);
+    if (lane == 0) counts[warp] = __popc(mask);
     __syncthreads();
-    if (ends) atomicMin(&last, next);
-    for (int x = next + kThreads; x < shares; x += kThreads)
-      if (a.desc[x].flags & kPagedEnds) atomicMin(&last, x);
-    const int pairs = mg.d.tokens * (a.G / 2);
+    int before = n_open;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += counts[w];
+      n_open += counts[w];
+    }
+    if (f & kPagedOpen) open[before + __popc(mask & ((1u << lane) - 1))] = static_cast<int16_t>(c);
+    __syncthreads();
+  }
+  // a unit of work: the block's eight warps' pairs, or one pair where that fills fewer blocks
+  const int most = a.tq * (a.G / 2), per = n_open * most <= static_cast<int>(gridDim.x) ? 1 : kWarps;
+  const int groups = (most + per - 1) / per;
+  for (int unit = blockIdx.x; unit < n_open * groups; unit += gridDim.x) {
+    const int c = open[unit / groups], first = unit % groups * per;
+    if (tid == 0) last = shares - 1;
+    __syncthreads();
+    // the share that ends the item: the first of those that follow that ends one
+    for (int x = c + 1 + tid; x < shares; x += kThreads)
+      if (flags[x] & kPagedEnds) {
+        atomicMin(&last, x);
+        break;
+      }
+    Merge<D> mg{a, a.desc[c], c, 0};
+    const int pairs = min(mg.d.tokens * (a.G / 2), first + per);
     __syncthreads();
     const int parts = mg.parts = last - c + 1;
+    __syncthreads();
     if (parts <= kFew) {
       constexpr int kPer = D / 32;
-      for (int pair = blockIdx.y * kWarps + warp; pair < pairs; pair += gridDim.y * kWarps) {
+      if (const int pair = first + warp; pair < pairs) {
         const int row = mg.row(pair);
         const float g = a.gate[mg.token(pair) * a.h + mg.head(pair)];
         float x[2][kFew][kPer], o[2][kPer], iv[2];
@@ -133,7 +151,7 @@ paged_merge_kernel(PagedArgs a) {
       continue;
     }
     const int col = tid % D, way = tid / D;
-    for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
+    for (int pair = first; pair < pairs; ++pair) {
       const int row = mg.row(pair);
       // the parts' weights: warp e takes head e of the pair
       if (warp < 2) {
@@ -180,10 +198,9 @@ paged_merge_kernel(PagedArgs a) {
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t s) {
-  if (a.grid * a.turns > kMaxParts) return cudaErrorInvalidValue;
+  if (a.grid * a.turns > kMaxShares) return cudaErrorInvalidValue;
   if (a.grid * a.turns < 2) return cudaSuccess;  // one share cuts nothing
-  const int pairs = a.tq * a.G / 2;
-  const dim3 grid(a.grid, pairs < 16 ? pairs : 16);
+  const dim3 grid(a.grid * kBlocksPerSm);
   if (a.cache.d == 128) return launch_ahead(paged_merge_kernel<128>, grid, dim3(kThreads), 0, s, true, a);
   return launch_ahead(paged_merge_kernel<64>, grid, dim3(kThreads), 0, s, true, a);
 }
