@@ -31,13 +31,14 @@ namespace da {
 
 constexpr int kPagedTile = 128;  // keys
 // What a tile costs (one of an item with two MMA tiles, with one), and an item
-// beside its tiles: 1.5 and 1 us and about 4 us.  With few tokens the memory does
-// not wait for an item's end.
+// beside its tiles: 1.5 and 1 us and about 4 us; with few tokens the time of about
+// two tiles of d 128, three of 64, or four with two warpgroups.
 struct PagedCostFwd {
   static constexpr int kTile = 3, kTileOne = 2, kItem = 8;
 };
+template <int D, int C>
 struct PagedCostFew {
-  static constexpr int kTile = 1, kTileOne = 1, kItem = 0;
+  static constexpr int kTile = 2, kTileOne = 2, kItem = D == 128 ? 4 : C == 32 ? 8 : 6;
 };
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns

@@ -179,7 +179,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<PagedCostFew, F::kThreads>(a, mine, &share);
+  paged_share<PagedCostFew<D, C>, F::kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
@@ -195,7 +195,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int it = 0, st = 0;
     uint32_t round = 0;  // of the rings
     bool ok = true;
-    for (PagedWalk<PagedCostFew, 1> w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<PagedCostFew<D, C>, 1> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
       if (!ok) break;
@@ -239,7 +239,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const uint32_t v0 = sdesc_lo(base + F::kOffV, 1024), p0 = sdesc_lo(base + F::kOffP, 16);
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) { return wait_bar(&abort_flag, b, parity, a.status, site); };
       // S of tile x (of the CTA's share) for the item that a walk of its own is at
-      PagedWalk<PagedCostFew, 1> ahead(a, share);
+      PagedWalk<PagedCostFew<D, C>, 1> ahead(a, share);
       int it = 0, j = ahead.j, ks = 0;
       uint32_t k_round = 0;
       auto start = [&](int x) {
@@ -298,9 +298,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int x = 0, flags = 0, vs = 0;
     uint32_t v_round = 0;
     PagedDesc desc{0, 0, 0, 0};
-    bool ok = true, synced = false;
-    for (PagedWalk<PagedCostFew, 1> w(a, share); w.more(); w.next()) {
+    bool ok = true, synced = !a.after_gate;
+    for (PagedWalk<PagedCostFew<D, C>, 1> w(a, share); w.more(); w.next()) {
       const int cols = w.tokens * a.G - n0;  // the item's columns, from n0 on
+      const bool whole = w.begins() && w.ends();
+      const int64_t part = static_cast<int64_t>(2 * w.number() + (w.begins() ? 1 : 0)) * a.rows;
+      // what thread n's column n is scaled by: 1 (even heads) or the gate
+      auto gate_of = [&]() {
+        const int tok = (n0 + r) / a.G;
+        return (r & 1) && r < cols && r < kC
+                   ? a.gate[(w.t0 + static_cast<int64_t>(w.i) * a.tq + tok) * a.h + w.g * (a.G / 2) + (n0 + r - tok * a.G) / 2]
+                   : 1.f;
+      };
+      float gate = whole && synced ? gate_of() : 1.f;
       float m[kC], l[kC], o[kC];
 #pragma unroll
       for (int n = 0; n < kC; ++n) m[n] = l[n] = o[n] = 0.f;
@@ -407,44 +417,60 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       }
       // ----------------------------------------------------- epilogue ----
       add_product();
+      // each column's sum over the warp's keys: the columns are halved with every
+      // exchange, until a lane has one
+      int col = 0, off = 16;
 #pragma unroll
-      for (int n = 0; n < kC; ++n) {
-        float v = l[n];
+      for (int half = kC / 2; half > 0; half /= 2, off /= 2) {
+        const bool upper = lane & off;
 #pragma unroll
-        for (int h = 16; h > 0; h /= 2) v += __shfl_xor_sync(0xffffffffu, v, h);
-        if (lane == (n & 31)) red[(4 + q4) * kC + n] = v;
+        for (int n = 0; n < half; ++n) {
+          const float send = upper ? l[n] : l[n + half];
+          l[n] = (upper ? l[n + half] : l[n]) + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+        col += upper ? half : 0;
       }
-      const bool whole = w.begins() && w.ends();
+      float lw = l[0];
+      for (; off > 0; off /= 2) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+      if ((lane & (32 / kC - 1)) == 0) red[(4 + q4) * kC + col] = lw;
       if (whole && !synced) {
         cudaGridDependencySynchronize();  // the gate
         synced = true;
+        gate = gate_of();
       }
       if (any_128(id, !ok || abort_flag)) {
         ok = false;
         break;
       }
+      if (r < kC) {  // thread n has column n's sum
+        const float sum = (red[4 * kC + r] + red[5 * kC + r]) + (red[6 * kC + r] + red[7 * kC + r]);
+        if (whole) {
+          red[4 * kC + r] = gate / sum;
+        } else if (r < cols) {
+          float mr = m[0];
 #pragma unroll
-      for (int n = 0; n < kC; ++n) l[n] = (red[4 * kC + n] + red[5 * kC + n]) + (red[6 * kC + n] + red[7 * kC + n]);
+          for (int n = 1; n < kC; ++n) mr = r == n ? m[n] : mr;
+          *reinterpret_cast<float2*>(a.part_ml + (part + n0 + r) * 2) = make_float2(sum == 0.f ? -INFINITY : mr, sum);
+        }
+      }
       if (whole) {
+        sync_128(id);
         const int half = a.G / 2;
+        int tok = n0 / a.G, p = (n0 - tok * a.G) / 2;
 #pragma unroll
         for (int n = 0; n < kC; n += 2) {
           if (n < cols && r < D) {
-            const int tok = (n0 + n) / a.G, pair = w.g * half + (n0 + n - tok * a.G) / 2;
             const int64_t t = w.t0 + static_cast<int64_t>(w.i) * a.tq + tok;
             // the products rounded apart, so that equal heads cancel with gate 1
-            const float y = __fsub_rn(__fmul_rn(o[n], 1.f / l[n]), __fmul_rn(o[n + 1], a.gate[t * a.h + pair] / l[n + 1]));
-            static_cast<__nv_bfloat16*>(a.out.ptr)[t * a.out.st + pair * a.out.sh + r] = __float2bfloat16_rn(y);
+            const float y = __fsub_rn(__fmul_rn(o[n], red[4 * kC + n]), __fmul_rn(o[n + 1], red[4 * kC + n + 1]));
+            static_cast<__nv_bfloat16*>(a.out.ptr)[t * a.out.st + (w.g * half + p) * a.out.sh + r] = __float2bfloat16_rn(y);
           }
+          if (++p == half) p = 0, ++tok;
         }
       } else {
-        const int64_t part = static_cast<int64_t>(2 * w.number() + (w.begins() ? 1 : 0)) * a.rows;
 #pragma unroll
-        for (int n = 0; n < kC; ++n) {
+        for (int n = 0; n < kC; ++n)
           if (n < cols && r < D) a.part_o[(part + n0 + n) * D + r] = o[n];
-          if (n < cols && r == n)
-            *reinterpret_cast<float2*>(a.part_ml + (part + n0 + n) * 2) = make_float2(l[n] == 0.f ? -INFINITY : m[n], l[n]);
-        }
         if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
         if (w.begins()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       }
