@@ -10,6 +10,8 @@
 
 namespace {
 
+constexpr int kMostTokens = 1 << 29;
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 da_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ERR_CUDA; }
@@ -40,9 +42,8 @@ da_status check_qk(const da_qk_rope_fwd_params* p, bool* empty) {
   const da_status chk = check_rope(p->d, p->rot_dim, p->inv_freq, p->rope_scale, p->norm, p->norm_eps, p->q_weight,
                                    p->k_weight, p->positions);
   if (chk != DA_OK) return chk;
-  // tokens and a token's heads are counted in 32 bits
-  if (static_cast<int64_t>(p->B) * p->N > (int64_t(1) << 31) - 1 || p->h_q > (1 << 24) || p->h_k > (1 << 24))
-    return DA_ERR_UNSUPPORTED;
+  // tokens, a token's heads and the shares of them are counted in 32 bits
+  if (static_cast<int64_t>(p->B) * p->N > kMostTokens || p->h_q > (1 << 24) || p->h_k > (1 << 24)) return DA_ERR_UNSUPPORTED;
   *empty = p->B == 0 || p->N == 0 || (p->h_q == 0 && p->h_k == 0);
   return DA_OK;
 }
@@ -160,7 +161,7 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* stream) {
   chk = check_rope(d, p->rot_dim, p->inv_freq, p->rope_scale, p->norm, p->norm_eps, p->q_weight, p->k_weight, p->positions);
   if (chk != DA_OK) return chk;
   if (p->h_q < 0) return DA_ERR_INVALID_ARG;
-  if (p->h_q > (1 << 24) || p->cache.h_kv > (1 << 24)) return DA_ERR_UNSUPPORTED;
+  if (p->h_q > (1 << 24) || p->cache.h_kv > (1 << 24) || p->cache.T > kMostTokens) return DA_ERR_UNSUPPORTED;
   if (p->cache.T == 0 || p->cache.B == 0) return DA_OK;
   if (!da::paged_cache_given(p->cache) || !ok_t3(p->k) || !ok_t3(p->v)) return DA_ERR_INVALID_ARG;
   if (p->h_q > 0 && (!ok_t3(p->q) || !ok_t3(p->q_out))) return DA_ERR_INVALID_ARG;

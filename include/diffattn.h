@@ -669,7 +669,8 @@ da_status diffattn_rope_inv_freq(int rot_dim, double base, da_rope_stretch stret
  * positions: int32 [B, N] contiguous (NULL = 0 .. N-1), any value.
  * q_weight, k_weight: fp32 [d] (NULL = unit; not looked at without norm).
  * Supported: d = 16, 32, 64 or 128, DA_BF16 or DA_F32, rot_dim a multiple of 8
- * from 0 (no rotation) to d; bases and strides multiples of 16 bytes. */
+ * from 0 (no rotation) to d; bases and strides multiples of 16 bytes; B * N at
+ * most 2^29. */
 typedef struct {
   int B, N, h_q, h_k, d;
   da_dtype dtype;
@@ -738,9 +739,9 @@ typedef struct {
  * diffattn_qk_rope_fwd) and v (as it is), bf16 [T, h_kv, d], and, where h_q >
  * 0, the same tokens' queries q [T, h_q, d], normed and rotated, to q_out (q
  * itself, or apart from it).  positions: int32 [T], the rotation's (NULL = the
- * tokens' positions in their sequences).  d = 64 or 128.  Of a sequence that is
- * out of bounds nothing is written; of a token whose page is, the queries are.
- * Two tokens may not go to the same slot. */
+ * tokens' positions in their sequences).  d = 64 or 128, T at most 2^29.  Of a
+ * sequence that is out of bounds nothing is written; of a token whose page is,
+ * the queries are.  Two tokens may not go to the same slot. */
 typedef struct {
   da_paged_cache cache;
   int h_q;

@@ -324,6 +324,32 @@ def test_graph_and_streams():
         assert all(torch.equal(r[0], y) for y in r)
 
 
+@pytest.mark.parametrize("n", [[1, 1, 2], [150, 1, 40]])
+def test_graph_with_the_gate_from_x(n):
+    """The gate's kernel, the attention that starts beside it and the join, captured and replayed after x changed; and
+    a step of append and attention."""
+    t = make(n, [200, 700, 333], 32, 8, 2, 64, seed=9)
+    g, T = gen(10), sum(n)
+    x, w = randn((T, 512), g), randn((512, 8), g, 0.05)
+    k, v, q = randn((T, 2, 64), g), randn((T, 2, 64), g), randn((T, 16, 64), g)
+    f, _ = bd.diffattn_rope_inv_freq(64)
+    out = torch.zeros((T, 8, 64), dtype=BF16, device="cuda")
+    ws = torch.empty(bd.diffattn_v2_paged_fwd_workspace_size(T, 3, max(n), 8, 2, 64), dtype=torch.uint8, device="cuda")
+
+    def step():
+        bd.diffattn_paged_append(k, v, t["k"], t["v"], t["table"], t["cu"], t["sl"], f, q=q, q_out=t["q"])
+        call(t, x=x, w_lambda=w, out=out, workspace=ws, max_new=max(n))
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        x.copy_(randn(x.shape, g))
+        k.copy_(randn(k.shape, g))
+        graph.replay()
+        check(t, out, gate=1 / (1 + np.exp(-(f64(x) @ f64(w)))))
+
+
 def test_serving_steps():
     """A run as a serving loop makes it: prompts in chunks, then single tokens, each appended (normed, rotated) and
     attended; against the definition over everything that was appended."""

@@ -43,6 +43,7 @@ ROPE = [(dict(B=-1), INV), (dict(h_q=-1), INV), (dict(dtype=5), INV), (dict(d=96
         (dict(rot_dim=-8), INV), (dict(rot_dim=12), UNS), (dict(inv_freq=None), INV), (dict(inv_freq=FAKE + 2), INV),
         (dict(rope_scale=float("inf")), INV), (dict(norm_eps=-1.0), INV), (dict(norm_eps=float("nan")), INV),
         (dict(q_weight=FAKE + 2), INV), (dict(positions=FAKE + 1), INV), (dict(B=1 << 16, N=1 << 16), UNS),
+        (dict(B=1 << 15, N=(1 << 14) + 1), UNS),
         (dict(B=0), OK), (dict(N=0), OK), (dict(h_q=0, h_k=0), OK)]
 
 
@@ -79,9 +80,10 @@ CACHE = [({"cache.B": -1}, INV), ({"cache.T": -1}, INV), ({"cache.h_kv": 0}, INV
 
 
 @pytest.mark.parametrize("kw,want", CACHE + [
-    (dict(h_q=-1), INV), (dict(rot_dim=12), UNS), (dict(inv_freq=None), INV), (dict(norm_eps=-1.0), INV),
-    (dict(positions=FAKE + 2), INV), (dict(k=t3(8)), INV), (dict(v=bd.da_t3(None, 0, 0)), INV), (dict(q=t3(8)), INV),
-    (dict(q_out=bd.da_t3(None, 0, 0)), INV), (dict(v=t3(sh=4)), INV)])
+    (dict(h_q=-1), INV), (dict(h_q=1 << 25), UNS), ({"cache.T": (1 << 29) + 1}, UNS), (dict(rot_dim=12), UNS),
+    (dict(inv_freq=None), INV), (dict(norm_eps=-1.0), INV), (dict(positions=FAKE + 2), INV),
+    (dict(k=t3(8)), INV), (dict(v=bd.da_t3(None, 0, 0)), INV), (dict(q=t3(8)), INV), (dict(q_out=bd.da_t3(None, 0, 0)), INV),
+    (dict(v=t3(sh=4)), INV)])
 def test_paged_append(lib, kw, want):
     p = bd.da_paged_append_params(cache(), 8, 128, 0, FAKE, 1.0, 1, 1e-5, FAKE, FAKE, None, t3(), t3(), t3(), t3())
     assert lib.diffattn_paged_append(with_(p, kw), None) == want
