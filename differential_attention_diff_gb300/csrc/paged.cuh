@@ -3,13 +3,12 @@
 // (paged_merge.cu).
 //
 // The work is tiles of 128 keys for items: up to `tq` new tokens of one sequence
-// with all G query heads of one KV head.  A tile costs some units of time, and so
-// does an item by itself (its queries, its end), before its first tile: without
-// that the CTA with the first items of a long prompt, of one tile each, would be
-// the last (8192 of 8192 tokens, 64 query heads: 843 us, 724 with it).  The units of a call form a
-// line, (sequence, KV head, item, key tile) in this order, and share c of C is its
-// c-th equal piece, wherever that begins and ends; a tile belongs to the share in
-// which it begins.  So a batch of any
+// with all G query heads of one KV head.  A tile is a unit of work, and an item by
+// itself (its queries, its end) is a few more, before its first tile: without that
+// the CTA with the first items of a long prompt, of one tile each, would be the
+// last (8192 of 8192 tokens, 64 query heads: 843 us, 724 with it).  The units of a
+// call form a line, (sequence, KV head, item, key tile) in this order, and share c
+// of C is its c-th equal piece, wherever that begins and ends.  So a batch of any
 // lengths loads the SMs evenly, whether it is one long sequence or many short
 // ones, and only the items that a share's end cuts are left to be joined: at most
 // C - 1, whatever the batch.  A share has at most two such parts, the rest of an
@@ -30,16 +29,15 @@
 namespace da {
 
 constexpr int kPagedTile = 128;  // keys
-// What a tile costs (one of an item with two MMA tiles, with one), and an item
-// beside its tiles: 1.5 and 1 us and about 4 us; with few tokens the time of about
-// two tiles of d 128, three of 64, or four with two warpgroups.
-struct PagedCostFwd {
-  static constexpr int kTile = 3, kTileOne = 2, kItem = 8;
-};
+// What an item costs beside its tiles, in tiles' time: about 4 us of 1.3 to 1.5 in
+// the kernel for chunks (an item with one MMA tile waits longer for each of its
+// steps than one with two has to compute, and its tiles count no less: 8 chunks of
+// 1000 tokens among 40 single ones, up to 6000 keys: 242 us with two thirds, 215 so,
+// 229 with four); with few tokens the time of two tiles of d 128, three of 64, or
+// four with two warpgroups.
+constexpr int kItemFwd = 3;
 template <int D, int C>
-struct PagedCostFew {
-  static constexpr int kTile = 2, kTileOne = 2, kItem = D == 128 ? 4 : C == 32 ? 8 : 6;
-};
+constexpr int kItemFew = D == 128 ? 2 : C == 32 ? 4 : 3;
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
@@ -68,15 +66,9 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 
 // Units of the first i items of a sequence with n new tokens, length L; all but its
 // last item are whole.
-template <class Cost>
+template <int kItem>
 __device__ __forceinline__ int64_t units_before(const PagedArgs& a, int i, int n, int L) {
-  return Cost::kTile * floor_sum(i, kPagedTile, a.tq, static_cast<int64_t>(L) - n + a.tq + kPagedTile - 1) +
-         static_cast<int64_t>(Cost::kItem) * i;
-}
-// A tile's cost for an item of so many tokens.
-template <class Cost>
-__device__ __forceinline__ int tile_cost(const PagedArgs& a, int tokens) {
-  return Cost::kTile == Cost::kTileOne || tokens > a.tq1 ? Cost::kTile : Cost::kTileOne;
+  return floor_sum(i, kPagedTile, a.tq, static_cast<int64_t>(L) - n + a.tq + kPagedTile - 1) + static_cast<int64_t>(kItem) * i;
 }
 
 // A sequence of the batch as the arrays have it.
@@ -90,7 +82,7 @@ struct PagedSequence {
 };
 
 // Its units for one KV head, 0 if it is out of bounds (then *bad).
-template <class Cost>
+template <int kItem>
 __device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, bool* bad) {
   if (!paged_sequence_ok(a.cache, s.t0, s.t1, s.L)) {
     *bad = true;
@@ -99,8 +91,8 @@ __device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const Page
   const int n = s.t1 - s.t0;
   if (n == 0) return 0;
   const int before = n <= a.tq ? 0 : (n - 1) / a.tq;  // items before the last
-  const int64_t last = static_cast<int64_t>((s.L + kPagedTile - 1) / kPagedTile) * tile_cost<Cost>(a, n - before * a.tq) + Cost::kItem;
-  return before ? units_before<Cost>(a, before, n, s.L) + last : last;
+  const int64_t last = (static_cast<int64_t>(s.L) + kPagedTile - 1) / kPagedTile + kItem;
+  return before ? units_before<kItem>(a, before, n, s.L) + last : last;
 }
 
 // x / y, in 32 bits where that will do (a 64-bit division takes some 100 instructions)
@@ -125,7 +117,7 @@ struct PagedShares {
 // Fills *out (shared memory); called by all kThreads of a block, with sequence
 // threadIdx.x (where there is one) in `mine`: fetched at the kernel's start, since
 // the rest waits for it.
-template <class Cost, int kThreads, int kTurns>
+template <int kItem, int kThreads, int kTurns>
 __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, PagedShares<kTurns>* out) {
   static_assert(kThreads % 32 == 0, "whole warps");
   constexpr int kW = kThreads / 32;
@@ -135,12 +127,12 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   bool bad = false;
   // inclusive sums over the warp's sequences, and each round's over the warps:
   // the first round's stay in registers, which for kThreads sequences are all
-  int64_t per = tid < B ? sequence_units<Cost>(a, mine, &bad) : 0;
+  int64_t per = tid < B ? sequence_units<kItem>(a, mine, &bad) : 0;
   int64_t incl = per * a.cache.h_kv, rest = 0, keys = per ? mine.L : 0;
   for (int b = tid + kThreads; b < B; b += kThreads) {
     PagedSequence s;
     s.load(a.cache, b);
-    const int64_t u = sequence_units<Cost>(a, s, &bad);
+    const int64_t u = sequence_units<kItem>(a, s, &bad);
     rest += u * a.cache.h_kv;
     keys += u ? s.L : 0;
   }
@@ -181,14 +173,14 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   // values, and a share is long enough to outweigh its two cut items
   int turns = 1;
   if constexpr (kTurns > 1) {
-    const int64_t by_bytes = (keys * a.cache.h_kv * a.cache.d * 4) / kTurnBytes, by_units = quotient(total, static_cast<int64_t>(gridDim.x) * Cost::kTile * kTurnTiles);
+    const int64_t by_bytes = (keys * a.cache.h_kv * a.cache.d * 4) / kTurnBytes;
+    const int64_t by_units = quotient(total, static_cast<int64_t>(gridDim.x) * kTurnTiles);
     const int64_t t = by_bytes < by_units ? by_bytes : by_units;
     turns = static_cast<int>(t < 1 ? 1 : t < kTurns ? t : kTurns);
   }
-  // equal shares, the first `more` of them one unit longer; none shorter than a
-  // tile, so that an item's parts follow each other without a gap
-  const int64_t all = static_cast<int64_t>(turns) * gridDim.x, most = Cost::kTile == 1 ? total : quotient(total, Cost::kTile);
-  const int64_t shares = most < 1 ? 1 : most < all ? most : all;
+  // equal shares, the first `more` of them one unit longer; none is empty between
+  // others, so that an item's parts follow each other without a gap
+  const int64_t all = static_cast<int64_t>(turns) * gridDim.x, shares = total < 1 ? 1 : total < all ? total : all;
   const int64_t each = quotient(total, shares), more = total - each * shares;
   auto begin = [&](int64_t c) { return c * each + (c < more ? c : more); };
   auto length = [&](int64_t c) { return c < shares ? each + (c < more) : 0; };
@@ -210,7 +202,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
       int lo = 0, hi = (n + a.tq - 1) / a.tq;  // the item: the last that begins at or before off
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (units_before<Cost>(a, mid, n, s.L) <= off)
+        if (units_before<kItem>(a, mid, n, s.L) <= off)
           lo = mid;
         else
           hi = mid;
@@ -218,7 +210,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
       out->share[k].b = r + tid;
       out->share[k].g = g;
       out->share[k].i = lo;
-      out->share[k].from = static_cast<int>(off - (lo ? units_before<Cost>(a, lo, n, s.L) : 0));
+      out->share[k].from = static_cast<int>(off - (lo ? units_before<kItem>(a, lo, n, s.L) : 0));
     }
     r += kThreads;
     if (r >= B || begin(static_cast<int64_t>(turns - 1) * gridDim.x + blockIdx.x) < base) break;
@@ -226,7 +218,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     per = 0;
     if (r + tid < B) {
       s.load(a.cache, r + tid);
-      per = sequence_units<Cost>(a, s, &bad);
+      per = sequence_units<kItem>(a, s, &bad);
     }
     incl = per * a.cache.h_kv;
 #pragma unroll
@@ -247,7 +239,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
 }
 
 // A CTA's way along its shares, part by part; every warp walks by itself.
-template <class Cost, int kTurns>
+template <int kItem, int kTurns>
 struct PagedWalk {
   const PagedArgs& a;
   const PagedShares<kTurns>& s;
@@ -330,16 +322,10 @@ struct PagedWalk {
   __device__ __forceinline__ void item() {
     tokens = min(a.tq, n - i * a.tq);
     tiles = (first_position() + tokens + kPagedTile - 1) / kPagedTile;
-    const int cost = tile_cost<Cost>(a, tokens), all = tiles * cost + Cost::kItem;
-    const bool cut = left < all - from;
-    end = cut ? from + static_cast<int>(left) : all;
-    j = from == 0 ? 0 : tile_at(from, cost);
-    j1 = cut ? tile_at(end, cost) : tiles;
-  }
-  // the tiles that begin before unit u of the item
-  __device__ __forceinline__ int tile_at(int u, int cost) const {
-    if (Cost::kTile == 1) return u - Cost::kItem;
-    return u <= Cost::kItem ? 0 : static_cast<int>(static_cast<uint32_t>(u - Cost::kItem + cost - 1) / static_cast<uint32_t>(cost));
+    const int all = tiles + kItem;
+    end = left < all - from ? from + static_cast<int>(left) : all;
+    j = max(from - kItem, 0);
+    j1 = max(end - kItem, 0);
   }
 };
 

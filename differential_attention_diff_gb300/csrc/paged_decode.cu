@@ -115,19 +115,14 @@ __device__ __forceinline__ float warp_max(float x) {
 // N consecutive TMEM columns of this thread's lane.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 64) {
-    tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-    tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-  } else if constexpr (N == 32) {
-    tmem_ld32(addr, r);
-  } else if constexpr (N == 16) {
+  if constexpr (N == 16) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
   } else {
-    static_assert(N == 8, "8, 16, 32 or 64 columns");
+    static_assert(N == 8, "8 or 16 columns");
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(addr));
@@ -182,7 +177,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<PagedCostFew<D, C>, F::kThreads>(a, mine, &share);
+  paged_share<kItemFew<D, C>, F::kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
@@ -198,7 +193,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int it = 0, st = 0;
     uint32_t round = 0;  // of the rings
     bool ok = true;
-    for (PagedWalk<PagedCostFew<D, C>, 1> w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<kItemFew<D, C>, 1> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
       if (!ok) break;
@@ -242,7 +237,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const uint32_t v0 = sdesc_lo(base + F::kOffV, 1024), p0 = sdesc_lo(base + F::kOffP, 16);
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) { return wait_bar(&abort_flag, b, parity, a.status, site); };
       // S of tile x (of the CTA's share) for the item that a walk of its own is at
-      PagedWalk<PagedCostFew<D, C>, 1> ahead(a, share);
+      PagedWalk<kItemFew<D, C>, 1> ahead(a, share);
       int it = 0, j = ahead.j, ks = 0;
       uint32_t k_round = 0;
       auto start = [&](int x) {
@@ -302,7 +297,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint32_t v_round = 0;
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = !a.after_gate;
-    for (PagedWalk<PagedCostFew<D, C>, 1> w(a, share); w.more(); w.next()) {
+    for (PagedWalk<kItemFew<D, C>, 1> w(a, share); w.more(); w.next()) {
       const int cols = w.tokens * a.G - n0;  // the item's columns, from n0 on
       const bool whole = w.begins() && w.ends();
       const int64_t part = static_cast<int64_t>(2 * w.number() + (w.begins() ? 1 : 0)) * a.rows;
