@@ -945,11 +945,12 @@ _NO_T4, _NO_T3 = (0, 0, 0, 0), (0, 0, 0)
 
 
 def _out(like, stream):
-    """A new tensor of the shape and type of `like`, on the stream that the call launches on."""
+    """A new contiguous tensor of the shape and type of `like`, on the stream that the call launches on (empty_like:
+    1.4 us on the host, new_empty 3.8)."""
     if stream is None:
-        return like.new_empty(like.shape)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
-        return like.new_empty(like.shape)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _heads4(t, B, N, d, dtype, dev, name, heads=None):
@@ -1073,7 +1074,8 @@ def diffattn_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqle
     _call("diffattn_paged_append", _pack_paged_append(
         *_paged_fields(T, k_pages, v_pages, block_table, cu_seqlens, seqlens, dev), h_q,
         *_rope_fields(d, inv_freq, rot_dim, interleaved, rope_scale, norm, norm_eps, q_weight, k_weight, dev),
-        0 if positions is None else _array(positions, (T,), torch.int32, dev, "positions"), *_rows3(k, (T, k_pages.shape[2], k_pages.shape[3]), bf16, dev, "k"),
+        0 if positions is None else _array(positions, (T,), torch.int32, dev, "positions"),
+        *_rows3(k, (T, k_pages.shape[2], k_pages.shape[3]), bf16, dev, "k"),
         *_rows3(v, shape, bf16, dev, "v"), *(_NO_T3 if q is None else _rows3(q, (T, h_q, d), bf16, dev, "q")),
         *(_NO_T3 if q is None else _rows3(q_out, (T, h_q, d), bf16, dev, "q_out"))), raw)
     return q_out
