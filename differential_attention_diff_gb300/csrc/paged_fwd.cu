@@ -329,16 +329,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool masked = key0 + kPagedTile - 1 > pos0;
         const int lim = pos0 + my_tok - key0;                     // the last key column that the row sees
         const bool valid = in_tile && first_tok + my_tok < w.tokens;
-        if (key0 + kPagedTile > w.L && (!dual || s == 0)) {
-          // values behind the sequence's end: zeros
-          const int st = (kv_it + x) & 1, r0 = w.L - key0;
-          if (!wait_bar(sh, sh.bar(B_VFULL + st), ((kv_it + x) >> 1) & 1, a.status, 0x8203)) ok = false;
-          uint8_t* v = sh.gen + kOffV + st * Tile::kBytes;
-          for (int e = threadIdx.x; e < (kPagedTile - r0) * 8 * kNB; e += 256)
-            *reinterpret_cast<uint4*>(v + Tile::row(r0 + e / (8 * kNB)) + e % (8 * kNB) / 8 * 1024 + e % 8 * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
         if (!wait_bar(sh, sh.bar(B_SFULL + s), sc[s] & 1, a.status, 0x8201)) ok = false;
         ++sc[s];
         tc_fence_after();
@@ -386,6 +376,17 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           } else {
             l_half[s] += lsum;
           }
+        }
+        if (key0 + kPagedTile > w.L && (!dual || s == 0)) {
+          // values behind the sequence's end: zeros.  These scores were issued behind
+          // the product of the tile that had the stage before, so the parity is this one's.
+          const int st = (kv_it + x) & 1, r0 = w.L - key0;
+          if (!wait_bar(sh, sh.bar(B_VFULL + st), ((kv_it + x) >> 1) & 1, a.status, 0x8203)) ok = false;
+          uint8_t* v = sh.gen + kOffV + st * Tile::kBytes;
+          for (int e = threadIdx.x; e < (kPagedTile - r0) * 8 * kNB; e += 256)
+            *reinterpret_cast<uint4*>(v + Tile::row(r0 + e / (8 * kNB)) + e % (8 * kNB) / 8 * 1024 + e % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
         }
         tmem_st_wait();
         tc_fence_before();

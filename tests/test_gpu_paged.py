@@ -191,6 +191,21 @@ def test_scores_that_grow():
             check(t, call(t), tag=str((n, up)))
 
 
+def test_partial_last_tiles_call_after_call():
+    """Many sequences of few tokens, each with a last tile that ends inside a page, on the kernel for chunks: the stage
+    whose values are zeroed behind the end may hold nothing of the tile before, whatever the copies' order."""
+    for n, L, h, hkv, page in (([1, 9, 3, 15, 5, 12, 1, 2] * 5, list(range(1203, 9203, 200)), 16, 8, 256),
+                               ([1, 2, 3, 1] * 8, list(range(333, 8333, 250)), 64, 4, 128)):
+        t = make(n, L, page, h, hkv, 128, layout="head")
+        out = call(t, max_new=1000)
+        check(t, out, only=(0, 7, 20, len(n) - 1))
+        other = torch.randn(1 << 25, device="cuda")
+        for i in range(150):
+            if i % 3 == 0:
+                other.add_(1.0)  # the caches' contents differ from call to call
+            assert torch.equal(call(t, max_new=1000), out), i
+
+
 def test_equal_heads_cancel():
     """Heads 2p and 2p + 1 alike and gate 1: exactly nothing is left, whole or joined."""
     for n, L in (([1], [5000]), ([200], [900]), ([1] * 30, [300] * 30)):
