@@ -33,11 +33,11 @@ constexpr int kPagedTile = 128;  // keys
 // the kernel for chunks (an item with one MMA tile waits longer for each of its
 // steps than one with two has to compute, and its tiles count no less: 8 chunks of
 // 1000 tokens among 40 single ones, up to 6000 keys: 242 us with two thirds, 215 so,
-// 229 with four); with few tokens the time of two tiles of d 128, three of 64, or
-// four with two warpgroups.
-constexpr int kItemFwd = 3;
-template <int D, int C>
-constexpr int kItemFew = D == 128 ? 2 : C == 32 ? 4 : 3;
+// 229 with four); in the one for few tokens 1 to 2 us of 0.8 to 1.1 at d 64 and 1.5
+// at d 128, and as much again where a cut makes one item two (300 ragged sequences
+// up to 500, d 128, 4 tokens: 115, 104, 102 us with 1, 2, 3; up to 1000, 128 of
+// them, d 64: 62, 60, 62 with 2, 3, 4, single tokens 51, 45, 47 with 1, 3, 4).
+constexpr int kItem = 3;
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
@@ -66,7 +66,6 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 
 // Units of the first i items of a sequence with n new tokens, length L; all but its
 // last item are whole.
-template <int kItem>
 __device__ __forceinline__ int64_t units_before(const PagedArgs& a, int i, int n, int L) {
   return floor_sum(i, kPagedTile, a.tq, static_cast<int64_t>(L) - n + a.tq + kPagedTile - 1) + static_cast<int64_t>(kItem) * i;
 }
@@ -82,7 +81,6 @@ struct PagedSequence {
 };
 
 // Its units for one KV head, 0 if it is out of bounds (then *bad).
-template <int kItem>
 __device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, bool* bad) {
   if (!paged_sequence_ok(a.cache, s.t0, s.t1, s.L)) {
     *bad = true;
@@ -92,7 +90,7 @@ __device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const Page
   if (n == 0) return 0;
   const int before = n <= a.tq ? 0 : (n - 1) / a.tq;  // items before the last
   const int64_t last = (static_cast<int64_t>(s.L) + kPagedTile - 1) / kPagedTile + kItem;
-  return before ? units_before<kItem>(a, before, n, s.L) + last : last;
+  return before ? units_before(a, before, n, s.L) + last : last;
 }
 
 // x / y, in 32 bits where that will do (a 64-bit division takes some 100 instructions)
@@ -117,7 +115,7 @@ struct PagedShares {
 // Fills *out (shared memory); called by all kThreads of a block, with sequence
 // threadIdx.x (where there is one) in `mine`: fetched at the kernel's start, since
 // the rest waits for it.
-template <int kItem, int kThreads, int kTurns>
+template <int kThreads, int kTurns>
 __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, PagedShares<kTurns>* out) {
   static_assert(kThreads % 32 == 0, "whole warps");
   constexpr int kW = kThreads / 32;
@@ -127,12 +125,12 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   bool bad = false;
   // inclusive sums over the warp's sequences, and each round's over the warps:
   // the first round's stay in registers, which for kThreads sequences are all
-  int64_t per = tid < B ? sequence_units<kItem>(a, mine, &bad) : 0;
+  int64_t per = tid < B ? sequence_units(a, mine, &bad) : 0;
   int64_t incl = per * a.cache.h_kv, rest = 0, keys = per ? mine.L : 0;
   for (int b = tid + kThreads; b < B; b += kThreads) {
     PagedSequence s;
     s.load(a.cache, b);
-    const int64_t u = sequence_units<kItem>(a, s, &bad);
+    const int64_t u = sequence_units(a, s, &bad);
     rest += u * a.cache.h_kv;
     keys += u ? s.L : 0;
   }
@@ -202,7 +200,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
       int lo = 0, hi = (n + a.tq - 1) / a.tq;  // the item: the last that begins at or before off
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (units_before<kItem>(a, mid, n, s.L) <= off)
+        if (units_before(a, mid, n, s.L) <= off)
           lo = mid;
         else
           hi = mid;
@@ -210,7 +208,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
       out->share[k].b = r + tid;
       out->share[k].g = g;
       out->share[k].i = lo;
-      out->share[k].from = static_cast<int>(off - (lo ? units_before<kItem>(a, lo, n, s.L) : 0));
+      out->share[k].from = static_cast<int>(off - (lo ? units_before(a, lo, n, s.L) : 0));
     }
     r += kThreads;
     if (r >= B || begin(static_cast<int64_t>(turns - 1) * gridDim.x + blockIdx.x) < base) break;
@@ -218,7 +216,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     per = 0;
     if (r + tid < B) {
       s.load(a.cache, r + tid);
-      per = sequence_units<kItem>(a, s, &bad);
+      per = sequence_units(a, s, &bad);
     }
     incl = per * a.cache.h_kv;
 #pragma unroll
@@ -239,7 +237,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
 }
 
 // A CTA's way along its shares, part by part; every warp walks by itself.
-template <int kItem, int kTurns>
+template <int kTurns>
 struct PagedWalk {
   const PagedArgs& a;
   const PagedShares<kTurns>& s;

@@ -177,7 +177,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<kItemFew<D, C>, F::kThreads>(a, mine, &share);
+  paged_share<F::kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
@@ -193,7 +193,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int it = 0, st = 0;
     uint32_t round = 0;  // of the rings
     bool ok = true;
-    for (PagedWalk<kItemFew<D, C>, 1> w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<1> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
       if (!ok) break;
@@ -237,7 +237,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const uint32_t v0 = sdesc_lo(base + F::kOffV, 1024), p0 = sdesc_lo(base + F::kOffP, 16);
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) { return wait_bar(&abort_flag, b, parity, a.status, site); };
       // S of tile x (of the CTA's share) for the item that a walk of its own is at
-      PagedWalk<kItemFew<D, C>, 1> ahead(a, share);
+      PagedWalk<1> ahead(a, share);
       int it = 0, j = ahead.j, ks = 0;
       uint32_t k_round = 0;
       auto start = [&](int x) {
@@ -297,7 +297,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint32_t v_round = 0;
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = !a.after_gate;
-    for (PagedWalk<kItemFew<D, C>, 1> w(a, share); w.more(); w.next()) {
+    for (PagedWalk<1> w(a, share); w.more(); w.next()) {
       const int cols = w.tokens * a.G - n0;  // the item's columns, from n0 on
       const bool whole = w.begins() && w.ends();
       const int64_t part = static_cast<int64_t>(2 * w.number() + (w.begins() ? 1 : 0)) * a.rows;

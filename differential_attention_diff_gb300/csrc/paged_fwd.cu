@@ -134,7 +134,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  paged_share<kItemFwd, kThreads>(a, mine, &share);
+  paged_share<kThreads>(a, mine, &share);
   if (share.bad) paged_zero_bad(a);
   tc_fence_before();
   __syncthreads();
@@ -142,7 +142,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = *sh.tmem_slot();
   // the item's tokens have two Q tiles (A and B over the same key tiles), or one
   // (A and B over every other key tile)
-  auto two = [&](const PagedWalk<kItemFwd, kTurns>& w) { return w.tokens > a.tq1; };
+  auto two = [&](const PagedWalk<kTurns>& w) { return w.tokens > a.tq1; };
 
   if (warp == 8) {
     // ------------------------------------------------------ TMA producer --
@@ -153,7 +153,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     int kv_it = 0, it = 0;
     bool ok = true;
-    for (PagedWalk<kItemFwd, kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
+    for (PagedWalk<kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
       if (it > 0) ok = wait_warp(sh.bar(B_QEMPTY), (it - 1) & 1, 0x8001);
       if (ok && lane == 0) {
@@ -217,7 +217,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       auto full = [&](int bar, int x, uint32_t site) {  // of tile x's stage
         return wait_bar(sh, sh.bar(bar + (x & 1)), (x >> 1) & 1, a.status, site);
       };
-      for (PagedWalk<kItemFwd, kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
+      for (PagedWalk<kTurns> w(a, share); w.more() && ok; w.next(), ++it) {
         const int tiles = w.j1 - w.j;
         if (!wait_bar(sh, sh.bar(B_QFULL), it & 1, a.status, 0x8101)) break;
         if (!full(B_KFULL, kv_it, 0x8102)) break;
@@ -313,7 +313,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t sc[2] = {0, 0};
     PagedDesc desc{0, 0, 0, 0};
     bool ok = true, synced = false;
-    for (PagedWalk<kItemFwd, kTurns> w(a, share); w.more(); w.next(), ++it) {
+    for (PagedWalk<kTurns> w(a, share); w.more(); w.next(), ++it) {
       for (; kTurns > 1 && done < w.k; ++done) {
         if (threadIdx.x == 0) a.desc[done * gridDim.x + blockIdx.x] = desc;
         desc = PagedDesc{0, 0, 0, 0};
