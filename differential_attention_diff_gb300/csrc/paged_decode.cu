@@ -18,7 +18,8 @@
 //
 //   a warpgroup or, for C = 32, two with half of the columns each: softmax, sums,
 //     epilogue (thread = key of the tile, then feature)
-//   a warp: TMA producer (queries; K and V page by page, paged.cuh)
+//   a warp, with pages of 16 and D = 64 two: TMA producer (queries; K and V page by
+//     page, paged.cuh)
 //   a warp (one lane): MMA issuer; S of the next tile, the next item's first
 //     among them, goes ahead of the product of this one
 //   Shared memory: K and V rings (3 stages of 64 KB for D = 128, 6 of 32 KB for
@@ -30,6 +31,8 @@
 // us, 7.2 TB/s, every byte of the cache read once (ncu: 537 MB for 537 of 16 x
 // 8192); 16 x 8192: 90 us, of which 6 are the shares and the first tile's way from
 // memory, 4 the joining of cut items; 1 x 1000: 12 us, all of it latency.
+#include <type_traits>
+
 #include "paged.cuh"
 #include "softmax.cuh"
 #include "tma.cuh"
@@ -43,7 +46,7 @@ enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8, B_KFULL
 constexpr int kBarBytes = 320;
 static_assert(B_COUNT * 8 <= kBarBytes, "barrier area");
 
-template <int D, int C>
+template <int D, int C, int P>  // P: producer warps
 struct Cfg {
   using Tile = KeyTile<D>;
   static constexpr int kStages = D == 128 ? 3 : 6;
@@ -51,7 +54,7 @@ struct Cfg {
   // (32 sequences of 4096, 4 tokens x 8 heads: 55 us, 43 with two)
   static constexpr int kGroups = C == 32 ? 2 : 1;
   static constexpr int kCols = C / kGroups;              // of a warpgroup
-  static constexpr int kThreads = kGroups * 128 + 64;
+  static constexpr int kThreads = kGroups * 128 + P * 32 + 32;
   static constexpr int kCq = C < 16 ? 16 : C;            // an MMA has 16 columns at least
   static constexpr int kQBytes = Tile::kNB * kCq * 128;  // boxes of 64 features x kCq rows
   static constexpr int kPBox = 2 * C * 128;              // 64 keys x (C columns hi, C lo)
@@ -129,14 +132,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
   }
 }
 
-template <int D, int C>
-__global__ void __launch_bounds__(Cfg<D, C>::kThreads, 1)
+template <int D, int C, int P>
+__global__ void __launch_bounds__(Cfg<D, C, P>::kThreads, 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, PagedArgs a) {
-  using F = Cfg<D, C>;
+  using F = Cfg<D, C, P>;
   using Tile = typename F::Tile;
   constexpr int kS = F::kStages;
-  constexpr int kProducer = F::kGroups * 4, kIssuer = kProducer + 1;
+  constexpr int kProducer = F::kGroups * 4, kIssuer = kProducer + P;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PagedShares<1> share;
   __shared__ uint32_t tmem_slot;
@@ -184,8 +187,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------ TMA producer --
+  // A producer warp's copies of the queries and keys, of the values, or of all.
+  auto produce = [&](auto keys, auto values) {
+    constexpr bool kKeys = decltype(keys)::value, kValues = decltype(values)::value;
     const PageCopies copies(a, lane);
     auto wait_warp = [&](uint32_t b, uint32_t parity, uint32_t site) {
       return __all_sync(0xffffffffu, wait_bar(&abort_flag, b, parity, a.status, site)) != 0;
@@ -195,9 +199,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     bool ok = true;
     for (PagedWalk<1> w(a, share); w.more() && ok; w.next(), ++it) {
       int entry = copies.entry(w.b, w.L, w.j);
-      if (it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
+      if (kKeys && it > 1) ok = wait_warp(bar(B_QEMPTY + (it & 1)), ((it >> 1) - 1) & 1, 0x9001);
       if (!ok) break;
-      if (lane == 0) {
+      if (kKeys && lane == 0) {
         mbar_arrive_expect_tx(bar(B_QFULL + (it & 1)), Tile::kNB * a.G * a.tq * 128);
         for (int box = 0; box < Tile::kNB; ++box)
           tma_load_3d(base + F::kOffQ + (it & 1) * F::kQBytes + box * F::kCq * 128, &tm_q, bar(B_QFULL + (it & 1)), box * 64,
@@ -207,18 +211,22 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int page = copies.page(entry, w.L, j), group = copies.group(j);
         if (j + 1 < w.j1) entry = copies.entry(w.b, w.L, j + 1);  // looked up a tile ahead
         const uint32_t to = st * Tile::kBytes + Tile::row(copies.row0);
-        if (round > 0) ok = wait_warp(bar(B_KEMPTY + st), (round - 1) & 1, 0x9002);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_KFULL + st), Tile::kBytes);
-        __syncwarp();
-        if (copies.mine)
-          tma_load_5d(base + F::kOffK + to, &tm_k, bar(B_KFULL + st), 0, 0, w.g * copies.k_block, group, page);
-        if (round > 0) ok = wait_warp(bar(B_VEMPTY + st), (round - 1) & 1, 0x9003);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_VFULL + st), Tile::kBytes);
-        __syncwarp();
-        if (copies.mine)
-          tma_load_5d(base + F::kOffV + to, &tm_v, bar(B_VFULL + st), 0, 0, w.g * copies.v_block, group, page);
+        if constexpr (kKeys) {
+          if (round > 0) ok = wait_warp(bar(B_KEMPTY + st), (round - 1) & 1, 0x9002);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(B_KFULL + st), Tile::kBytes);
+          __syncwarp();
+          if (copies.mine)
+            tma_load_5d(base + F::kOffK + to, &tm_k, bar(B_KFULL + st), 0, 0, w.g * copies.k_block, group, page);
+        }
+        if constexpr (kValues) {
+          if (round > 0) ok = wait_warp(bar(B_VEMPTY + st), (round - 1) & 1, 0x9003);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(B_VFULL + st), Tile::kBytes);
+          __syncwarp();
+          if (copies.mine)
+            tma_load_5d(base + F::kOffV + to, &tm_v, bar(B_VFULL + st), 0, 0, w.g * copies.v_block, group, page);
+        }
         if (++st == kS) st = 0, ++round;
       }
     }
@@ -228,6 +236,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       while (globaltimer() - t0 < 100000000ull) {
       }
     }
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------ TMA producer --
+    if constexpr (P > 1)
+      produce(yes, no);
+    else
+      produce(yes, yes);
+  } else if (P > 1 && warp == kProducer + 1) {
+    produce(no, yes);
   } else if (warp == kIssuer) {
     // ------------------------------------------------------- MMA issuer ---
     if (lane == 0) {
@@ -486,18 +506,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   if (warp == kIssuer) tmem_dealloc(tmem, F::kTmem);
 }
 
-template <int D, int C>
-cudaError_t launch_c(const PagedArgs& a, cudaStream_t s) {
+template <int D, int C, int P>
+cudaError_t launch_p(const PagedArgs& a, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   const da_paged_cache& c = a.cache;
   if (!encode_queries(&tq, a, a.tq) || !encode_pages(&tk, c.k_pages, c, a.box) || !encode_pages(&tv, c.v_pages, c, a.box))
     return cudaErrorInvalidValue;
   static OncePerDevice once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(paged_decode_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, C>::kSmem);
+    return cudaFuncSetAttribute(paged_decode_kernel<D, C, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, C, P>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_ahead(paged_decode_kernel<D, C>, dim3(a.grid), dim3(Cfg<D, C>::kThreads), Cfg<D, C>::kSmem, s, a.after_gate, tq, tk, tv, a);
+  return launch_ahead(paged_decode_kernel<D, C, P>, dim3(a.grid), dim3(Cfg<D, C, P>::kThreads), Cfg<D, C, P>::kSmem, s, a.after_gate, tq, tk, tv, a);
+}
+
+// A warp issues its lanes' copies one after the other: with 16 to a tile of 32 KB the
+// values' are a second warp's (pages of 16, d 64, 24 ragged sequences up to 20000: 131
+// us with one warp, 109 with two; with fewer or longer copies two warps are 2 to 4 %
+// slower, pages of 64: 112 and 114).
+template <int D, int C>
+cudaError_t launch_c(const PagedArgs& a, cudaStream_t s) {
+  if constexpr (D == 64) {
+    if (a.box == 16) return launch_p<D, C, 2>(a, s);
+  }
+  return launch_p<D, C, 1>(a, s);
 }
 
 template <int D>
