@@ -517,7 +517,8 @@ cudaError_t launch_p(const PagedArgs& a, cudaStream_t s) {
     return cudaFuncSetAttribute(paged_decode_kernel<D, C, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, C, P>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_ahead(paged_decode_kernel<D, C, P>, dim3(a.grid), dim3(Cfg<D, C, P>::kThreads), Cfg<D, C, P>::kSmem, s, a.after_gate, tq, tk, tv, a);
+  return launch_ahead(paged_decode_kernel<D, C, P>, dim3(a.grid), dim3(Cfg<D, C, P>::kThreads), Cfg<D, C, P>::kSmem, s,
+                      a.after_gate, tq, tk, tv, a);
 }
 
 // A warp issues its lanes' copies one after the other: with 16 to a tile of 32 KB the
