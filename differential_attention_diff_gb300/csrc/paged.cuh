@@ -402,9 +402,10 @@ __device__ __forceinline__ void paged_zero_bad(const PagedArgs& a) {
     if (paged_sequence_ok(c, t0, t1, c.seqlens[b])) continue;
     if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
     const int per = a.h * c.d / 8;
-    const int lo = max(t0, 0), hi = min(t1, c.T);
-    for (int64_t x = threadIdx.x; x < static_cast<int64_t>(hi - lo) * per; x += blockDim.x) {
-      const int t = lo + static_cast<int>(x / per), r = static_cast<int>(x % per);
+    const int64_t lo = max(t0, 0), rows = min(t1, c.T) - lo;  // (in 64 bits: t1 may be any number)
+    for (int64_t x = threadIdx.x; x < rows * per; x += blockDim.x) {
+      const int64_t t = lo + x / per;
+      const int r = static_cast<int>(x % per);
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out.ptr) + t * a.out.st + r / (c.d / 8) * a.out.sh + r % (c.d / 8) * 8;
       *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
     }
