@@ -41,6 +41,9 @@ constexpr int kItem = 3;
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
+// What is out of bounds: some sequence, and the offsets of all of them, which fall
+// somewhere.  The rows of two sequences could then be the same, so none is taken.
+enum { kBadSequence = 1, kBadOffsets = 2 };
 
 __device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
   return t0 >= 0 && t0 <= t1 && t1 <= c.T && L >= t1 - t0 && L <= static_cast<int64_t>(c.max_pages) * c.page_size;
@@ -80,10 +83,10 @@ struct PagedSequence {
   }
 };
 
-// Its units for one KV head, 0 if it is out of bounds (then *bad).
-__device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, bool* bad) {
+// Its units for one KV head, 0 if it is out of bounds (then *bad says how).
+__device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, int* bad) {
   if (!paged_sequence_ok(a.cache, s.t0, s.t1, s.L)) {
-    *bad = true;
+    *bad |= s.t1 < s.t0 ? kBadSequence | kBadOffsets : kBadSequence;
     return 0;
   }
   const int n = s.t1 - s.t0;
@@ -108,7 +111,7 @@ struct PagedShare {
 template <int kTurns>  // the most that a CTA may have
 struct PagedShares {
   int count;  // of this CTA; its k-th is share k * gridDim.x + blockIdx.x
-  int bad;    // some sequence is out of bounds
+  int bad;    // kBadSequence, kBadOffsets
   PagedShare share[kTurns];
 };
 
@@ -122,7 +125,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   __shared__ int64_t sums[kW], lengths[kW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.cache.B;
-  bool bad = false;
+  int bad = 0;
   // inclusive sums over the warp's sequences, and each round's over the warps:
   // the first round's stay in registers, which for kThreads sequences are all
   int64_t per = tid < B ? sequence_units(a, mine, &bad) : 0;
@@ -151,7 +154,8 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     sums[warp] = incl;
     if constexpr (kTurns > 1) lengths[warp] = keys;
   }
-  const bool any_bad = __syncthreads_or(bad);
+  int any_bad = __syncthreads_or(bad) ? kBadSequence : 0;
+  if (any_bad && __syncthreads_or(bad & kBadOffsets)) any_bad |= kBadOffsets;
   int64_t before = incl - per * a.cache.h_kv, total = 0;
   keys = 0;
 #pragma unroll
@@ -167,6 +171,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     __syncthreads();
     for (int v = 0; v < kW; ++v) total += sums[v];
   }
+  if (any_bad & kBadOffsets) total = 0;
   // turns of the CTAs: a stretch of the line reads about kTurnBytes of keys and
   // values, and a share is long enough to outweigh its two cut items
   int turns = 1;
@@ -393,22 +398,30 @@ struct PageCopies {
   __device__ __forceinline__ int group(int j) const { return (j * kPagedTile + row0) % a.cache.page_size / 8; }
 };
 
-// The outputs of the sequences that are out of bounds, where their rows are
-// within the array: zeros.  All threads of the grid share them.
-__device__ __forceinline__ void paged_zero_bad(const PagedArgs& a) {
+// The outputs of the sequences that are out of bounds (`bad`: PagedShares), where
+// their rows are within the array: zeros.  All threads of the grid share them.
+__device__ __forceinline__ void paged_zero_bad(const PagedArgs& a, int bad) {
   const da_paged_cache& c = a.cache;
-  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
-    const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1];
-    if (paged_sequence_ok(c, t0, t1, c.seqlens[b])) continue;
-    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
-    const int per = a.h * c.d / 8;
-    const int64_t lo = max(t0, 0), rows = min(t1, c.T) - lo;  // (in 64 bits: t1 may be any number)
-    for (int64_t x = threadIdx.x; x < rows * per; x += blockDim.x) {
-      const int64_t t = lo + x / per;
+  const int per = a.h * c.d / 8;
+  auto zero = [&](int64_t row, int64_t rows, int64_t first, int64_t step) {
+    for (int64_t x = first; x < rows * per; x += step) {
+      const int64_t t = row + x / per;
       const int r = static_cast<int>(x % per);
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out.ptr) + t * a.out.st + r / (c.d / 8) * a.out.sh + r % (c.d / 8) * 8;
       *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
     }
+  };
+  if (bad & kBadOffsets) {
+    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
+    zero(0, c.T, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, static_cast<int64_t>(gridDim.x) * blockDim.x);
+    return;
+  }
+  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+    const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1];
+    if (paged_sequence_ok(c, t0, t1, c.seqlens[b])) continue;
+    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
+    const int64_t lo = max(t0, 0);  // (in 64 bits: t1 may be any number)
+    zero(lo, min(t1, c.T) - lo, threadIdx.x, blockDim.x);
   }
 }
 
