@@ -192,7 +192,8 @@ da_status da::check_paged_cache(const da_paged_cache& c) {
   if (c.B < 0 || c.T < 0 || c.h_kv <= 0 || c.d <= 0 || c.page_size <= 0 || c.n_pages < 0 || c.max_pages < 0)
     return DA_ERR_INVALID_ARG;
   if (c.d != 64 && c.d != 128) return DA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(c.max_pages) * c.page_size > (1 << 30) ||
+  // sequences are counted in 32 bits, a block's threads of them a step
+  if (c.B > (1 << 30) || static_cast<int64_t>(c.max_pages) * c.page_size > (1 << 30) ||
       static_cast<int64_t>(c.B) * c.max_pages > (int64_t(1) << 31) - 1)
     return DA_ERR_UNSUPPORTED;
   return DA_OK;

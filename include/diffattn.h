@@ -723,6 +723,7 @@ da_status diffattn_qk_rope_bwd(const da_qk_rope_bwd_params* p, void* cuda_stream
  * int32 [B + 1], rising.  They are the last n of its seqlens[b] positions (the
  * new tokens counted in): token i has position seqlens[b] - n + i.  Rows from
  * cu_seqlens[B] on belong to no sequence: outputs are left as they were there.
+ * At most 2^30 sequences.
  * A sequence whose rows are not within 0 .. T, or whose length is not within
  * n .. max_pages * page_size, is recorded as DA_ERR_BOUNDS in the device status
  * word, and so is a page outside 0 .. n_pages - 1 where one is looked up. */
