@@ -777,9 +777,9 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* cuda_stre
  * tokens of its own chunk that come up to 255 positions before it.
  * Supported: d = 64 or 128; 2h / h_kv even, at most 128; page_size a multiple of
  * 16; strides of dimensions longer than 1 above 0, the heads' in the pages
- * multiples of 64; d_model % 64 == 0 and h <= 64 where the gate is computed.  T * 2h and
- * B * max_pages at most 2^31 - 1, h_kv at most 65535, max_pages * page_size at
- * most 2^30.
+ * multiples of 64; d_model % 64 == 0 and h <= 64 where the gate is computed.  B at
+ * most 2^20, T * 2h and B * max_pages at most 2^31 - 1, h_kv at most 65535,
+ * max_pages * page_size at most 2^30.
  * workspace: diffattn_v2_paged_fwd_workspace_size bytes, 256-byte aligned,
  * contents on entry irrelevant; calls that run at the same time need workspaces
  * of their own.  Results are bitwise reproducible from call to call. */

@@ -69,3 +69,18 @@ def test_sequence_before_the_array(n):
     assert bd.diffattn_get_device_status() == bd.DA_ERR_BOUNDS
     check(dict(t, q=t["q"][:n[2]], gate=t["gate"][:n[2]], n=n[2:], L=[300], table=t["table"][2:]), out)
     assert bool((out[n[2]:] == 7).all())
+
+
+@pytest.mark.parametrize("max_new", [0, 1])
+def test_most_sequences_are_empty(max_new):
+    """2^20 sequences of which the first, one in between and the last have tokens."""
+    B = 2 ** 20
+    t = make([2, 3, 1], [300, 150, 90], 16, 4, 2, 128)
+    n = torch.zeros(B, dtype=torch.int32, device="cuda")
+    sl, table = torch.zeros_like(n), torch.zeros((B, t["table"].shape[1]), dtype=torch.int32, device="cuda")
+    for i, b in enumerate((0, 12345, B - 1)):
+        n[b], sl[b], table[b] = t["n"][i], t["L"][i], t["table"][i]
+    cu = torch.cat([n[:1] * 0, n.cumsum(0)]).int()
+    out = call(dict(t, cu=cu, sl=sl, table=table), max_new=max_new)
+    assert bd.diffattn_get_device_status() == bd.DA_OK
+    check(t, out)

@@ -7,9 +7,10 @@ from differential_attention_diff_gb300 import binding as bd
 from test_paged_abi import FAKE, OK, UNS, WS, cache, t3, with_
 
 
-@pytest.mark.parametrize("B,attend,append", [(2 ** 30, WS, OK), (2 ** 30 + 1, UNS, UNS), (2 ** 31 - 1, UNS, UNS)])
+@pytest.mark.parametrize("B,attend,append", [(2 ** 20, WS, OK), (2 ** 20 + 1, UNS, OK), (2 ** 30, UNS, OK),
+                                             (2 ** 30 + 1, UNS, UNS), (2 ** 31 - 1, UNS, UNS)])
 def test_sequences(lib, B, attend, append):
-    """2^30 sequences pass (the attention is refused for the lack of a workspace, the append has no tokens), more do not."""
+    """2^20 sequences may attend (what is left is refused for the lack of a workspace), 2^30 be appended to (nothing, here)."""
     kw = {"cache.B": B, "cache.max_pages": 1}
     p = bd.da_v2_paged_fwd_params(cache(), 4, 0, 0, 0.0, t3(), FAKE, None, None, t3(), None, 0)
     assert lib.diffattn_v2_paged_fwd(with_(p, kw), None) == attend
