@@ -19,7 +19,7 @@
 //
 // The angle: position * inv_freq in turns, as a 64-bit fixed-point fraction that
 // wraps by itself (position times 2^64 inv_freq / 2 pi, modulo 2^64).  It is off
-// by 2^-64 turns a position at most, so far positions keep the accuracy of near
+// by 2^-63 turns a position at most, so far positions keep the accuracy of near
 // ones, and the quarter of the turn comes out of its top bits exactly.
 #include "common.cuh"
 #include "fp32_pair.cuh"
@@ -41,16 +41,18 @@ constexpr int kStagesFwd = 4, kStagesBwd = 3;
 // 150, 153, 168 (103, 99, 112, 112).
 constexpr int kSharePasses = 4, kSharePassesBwd = 6;
 
-// 2^64 inv_freq / 2 pi modulo 2^64.  1 / 2 pi in two doubles (the first is it
+// 2^64 inv_freq / 2 pi modulo 2^64, to an even number, for frequencies below 2^32;
+// 1 for any other, an infinity or a NaN.  1 / 2 pi in two doubles (the first is it
 // rounded, the second the rest): their product with a 24-bit number is good to
-// 2^-77 of itself.
+// 2^-105 of itself, and below 2^32 to 2^-75.
 __device__ __forceinline__ uint64_t turns(float inv_freq) {
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
   const double f = inv_freq;
   const double hi = f * kHi;
   const double lo = fma(f, kHi, -hi) + f * kLo;
   const double frac = hi - floor(hi);
-  return __double2ull_rn(frac * 18446744073709551616.0) + static_cast<uint64_t>(__double2ll_rn(lo * 18446744073709551616.0));
+  const uint64_t t = __double2ull_rn(frac * 18446744073709551616.0) + static_cast<uint64_t>(__double2ll_rn(lo * 18446744073709551616.0));
+  return fabsf(inv_freq) < 4294967296.0f ? t & ~1ull : 1;
 }
 
 // Sine and cosine of t / 2^64 turns, times scale.  What is left of the nearest
@@ -220,15 +222,15 @@ __device__ __forceinline__ float square_sum(const F2Pair (&x)[P]) {
 }
 
 // A token's cosines and sines, a frequency to a lane, left in shared memory for
-// the lanes that have its pairs.  `sign` turns the other way.
-__device__ __forceinline__ void token_angles(const RopeArgs& a, const uint64_t* freq, int pos, float sign, float* cs, int stride,
-                                             int lane) {
+// the lanes that have its pairs; NaN for a frequency that is none.
+__device__ __forceinline__ void token_angles(const RopeArgs& a, const uint64_t* freq, int pos, float* cs, int stride, int lane) {
   __syncwarp();
   for (int i = lane; i < a.rot / 2; i += 32) {
     float s, c;
-    sincos_turns(static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq[i], a.rope_scale, s, c);
+    const uint64_t f = freq[i];
+    sincos_turns(static_cast<uint64_t>(static_cast<int64_t>(pos)) * f, f & 1 ? __int_as_float(0x7fffffff) : a.rope_scale, s, c);
     cs[i] = c;
-    cs[stride + i] = s * sign;
+    cs[stride + i] = s;
   }
   __syncwarp();
 }
@@ -404,7 +406,7 @@ rope_rows_kernel(const __grid_constant__ RopeArgs a) {
       to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
     }
     if (turned) {
-      if (a.rot) token_angles(a, freq, place.pos, 1.f, angles[warp], D / 2, lane);
+      if (a.rot) token_angles(a, freq, place.pos, angles[warp], D / 2, lane);
       if (f.rotated) {
         F2Pair co[F / 4], si[F / 4];
         load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
@@ -529,7 +531,7 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs g) {
     }
     T* to = at<T>(kd.dst, way.t / a.N, way.t % a.N);
     if (a.rot) {
-      token_angles(a, freq, place.pos, 1.f, angles[warp], D / 2, lane);
+      token_angles(a, freq, place.pos, angles[warp], D / 2, lane);
       if (f.rotated) load_angles<F / 4, kInter>(angles[warp], D / 2, l, a.rot, co, si);
     }
     for (int p = way.p; p < way.p1; p += kUnroll, st = st + 1 == kStagesBwd ? 0 : st + 1) {

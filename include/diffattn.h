@@ -630,6 +630,7 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* cuda_stream);
  *   z = w x / sqrt(mean_k x_k^2 + norm_eps)   (norm; z = x without it)
  *   a_i = position * inv_freq[i], i < rot_dim / 2, of the fp32 inv_freq as it
  *         is: no product is rounded before it is reduced to one turn
+ *         (below 2^32 in magnitude; any other, an infinity or a NaN gives NaN)
  *   y_u = rope_scale (z_u cos a_i - z_v sin a_i)
  *   y_v = rope_scale (z_v cos a_i + z_u sin a_i)
  * with (u, v) = (i, i + rot_dim / 2), or (2i, 2i + 1) where `interleaved`; the
