@@ -204,6 +204,14 @@ struct Turn {
       x[P + i] = fma2(u, vs[i], v * vc[i]);
     }
   }
+  // what `apply` is without rotation, where it may not multiply by 0
+  __device__ __forceinline__ void scale(F2Pair (&x)[2 * P]) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      x[i] = x[i] * uc[i];
+      x[P + i] = x[P + i] * vc[i];
+    }
+  }
 };
 
 template <int kLanes>
@@ -340,7 +348,9 @@ __device__ __forceinline__ Place place_of(const RopeArgs& a, int which, int t, i
   return r;
 }
 
-template <typename T, int D, int F, bool kInter, bool kPaged>
+// kRest: rows with a norm of which not all features are rotated (an instance of
+// its own, since its check would cost the others 2 %).
+template <typename T, int D, int F, bool kInter, bool kPaged, bool kRest>
 __global__ void __launch_bounds__(kThreads, kRopeBlocksPerSm)
 rope_rows_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / F, kRows = 32 / kLanes;  // lanes to a row, rows to a warp's pass
@@ -418,6 +428,7 @@ rope_rows_kernel(const __grid_constant__ RopeArgs a) {
     for (int p = way.p; p < way.p1; p += kUnroll, st = st + 1 == kStagesFwd ? 0 : st + 1) {
       fetch(st == 0 ? kStagesFwd - 1 : st - 1);
       cp_async_wait<kStagesFwd - 1>();
+      [[maybe_unused]] float squares = 0.f;  // of the group's rows
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (p + u >= way.p1) break;
@@ -428,7 +439,9 @@ rope_rows_kernel(const __grid_constant__ RopeArgs a) {
           F2Pair y[F / 2];
           L::get(x, y);
           if (norm) {
-            const float r = rsqrtf(row_sum<kLanes>(square_sum(y)) * (1.f / D) + a.norm_eps);
+            const float sum = row_sum<kLanes>(square_sum(y));
+            const float r = rsqrtf(sum * (1.f / D) + a.norm_eps);
+            if (kRest && h < kd.heads) squares += sum;
             turn.apply(y);
 #pragma unroll
             for (int e = 0; e < F / 2; ++e) y[e] = y[e] * F2Pair{r, r};
@@ -438,6 +451,26 @@ rope_rows_kernel(const __grid_constant__ RopeArgs a) {
           L::put(x, y);
         }
         if (h < kd.heads && place.ok) x.store(to + h * kd.dst.sh, f);
+      }
+      if constexpr (kRest) {
+        // 0 times an infinity is NaN, which its partner is not where they are not
+        // rotated: such rows' rest again
+        if (__any_sync(0xffffffffu, norm && !(squares < INFINITY))) {
+#pragma unroll 1
+          for (int u = 0; u < kUnroll && p + u < way.p1; ++u) {
+            const int h = (p + u) * kRows + sub;
+            typename L::Raw x;
+            x.load(mine + (st * kUnroll + u) * L::kSlot);
+            F2Pair y[F / 2];
+            L::get(x, y);
+            const float r = rsqrtf(row_sum<kLanes>(square_sum(y)) * (1.f / D) + a.norm_eps);
+            turn.scale(y);
+#pragma unroll
+            for (int e = 0; e < F / 2; ++e) y[e] = y[e] * F2Pair{r, r};
+            L::put(x, y);
+            if (!f.rotated && h < kd.heads && place.ok) x.store(to + h * kd.dst.sh, f);
+          }
+        }
       }
     }
     way = after;
@@ -647,10 +680,13 @@ cudaError_t launch(void (*kernel)(A), OncePerDevice& once, const A& a, unsigned 
 template <bool kPaged, typename T, int D, int F>
 cudaError_t launch_rows_f(RopeArgs a, int sms, cudaStream_t s) {
   constexpr int kSmem = kWarps * kStagesFwd * kUnroll * Lane<T, D, F, false>::kSlot;
-  static OncePerDevice once[2];
+  static OncePerDevice once[4];
   const unsigned grid = share(a, 32 * F / D, sms, kSharePasses);
-  return a.interleaved ? launch(rope_rows_kernel<T, D, F, true, kPaged>, once[1], a, grid, kSmem, s)
-                       : launch(rope_rows_kernel<T, D, F, false, kPaged>, once[0], a, grid, kSmem, s);
+  if (a.norm && a.rot < D)
+    return a.interleaved ? launch(rope_rows_kernel<T, D, F, true, kPaged, true>, once[3], a, grid, kSmem, s)
+                         : launch(rope_rows_kernel<T, D, F, false, kPaged, true>, once[2], a, grid, kSmem, s);
+  return a.interleaved ? launch(rope_rows_kernel<T, D, F, true, kPaged, false>, once[1], a, grid, kSmem, s)
+                       : launch(rope_rows_kernel<T, D, F, false, kPaged, false>, once[0], a, grid, kSmem, s);
 }
 
 template <typename T, int D, int F>

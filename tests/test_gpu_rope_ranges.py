@@ -93,3 +93,19 @@ def test_frequencies_of_an_append():
     bd.diffattn_paged_append(k, k, kp, vp, i32([[0]]), i32([0, 2]), i32([2]), f)
     nan = torch.isnan(kp[0, :2, 0])
     assert nan[:, [1, 3, 5, 7]].all() and int(nan.sum()) == 8 and torch.equal(vp[0, :2], k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d,rot", [(64, 0), (64, 16), (128, 8), (128, 64), (16, 8), (64, 64)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinity_under_the_norm(interleaved, d, rot, dtype):
+    """x / inf: the infinity itself is NaN, and so is its pair's other feature where it is rotated; the rest is 0."""
+    x = torch.ones((1, d, 1, d), dtype=dtype, device="cuda")
+    x[0, range(d), 0, range(d)] = torch.where(torch.arange(d, device="cuda") % 3 == 0, -torch.inf, torch.inf).to(dtype)
+    f = torch.tensor(10000.0 ** (-np.arange(rot // 2) / max(rot // 2, 1)), dtype=F32, device="cuda")
+    y = bd.diffattn_qk_rope_fwd(x, None, f, norm=True, interleaved=interleaved, rot_dim=rot)[0]
+    with np.errstate(all="ignore"):
+        ref = po.qk_rope(x.double().cpu().numpy(), f.cpu().numpy(), np.arange(d)[None], rot, interleaved, do_norm=True)
+    got = y.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.isnan(ref).sum() == d + rot
+    assert not got[~np.isnan(ref)].any()
