@@ -41,9 +41,6 @@ constexpr int kItem = 3;
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
-// What is out of bounds: some sequence, and the offsets of all of them, which fall
-// somewhere.  The rows of two sequences could then be the same, so none is taken.
-enum { kBadSequence = 1, kBadOffsets = 2 };
 
 __device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
   return t0 >= 0 && t0 <= t1 && t1 <= c.T && L >= t1 - t0 && L <= static_cast<int64_t>(c.max_pages) * c.page_size;
@@ -83,10 +80,10 @@ struct PagedSequence {
   }
 };
 
-// Its units for one KV head, 0 if it is out of bounds (then *bad says how).
-__device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, int* bad) {
+// Its units for one KV head, 0 if it is out of bounds (then *bad).
+__device__ __forceinline__ int64_t sequence_units(const PagedArgs& a, const PagedSequence& s, bool* bad) {
   if (!paged_sequence_ok(a.cache, s.t0, s.t1, s.L)) {
-    *bad |= s.t1 < s.t0 ? kBadSequence | kBadOffsets : kBadSequence;
+    *bad = true;
     return 0;
   }
   const int n = s.t1 - s.t0;
@@ -111,7 +108,7 @@ struct PagedShare {
 template <int kTurns>  // the most that a CTA may have
 struct PagedShares {
   int count;  // of this CTA; its k-th is share k * gridDim.x + blockIdx.x
-  int bad;    // kBadSequence, kBadOffsets
+  int bad;    // some sequence is out of bounds
   PagedShare share[kTurns];
 };
 
@@ -125,7 +122,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
   __shared__ int64_t sums[kW], lengths[kW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.cache.B;
-  int bad = 0;
+  bool bad = false;
   // inclusive sums over the warp's sequences, and each round's over the warps:
   // the first round's stay in registers, which for kThreads sequences are all
   int64_t per = tid < B ? sequence_units(a, mine, &bad) : 0;
@@ -154,8 +151,7 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     sums[warp] = incl;
     if constexpr (kTurns > 1) lengths[warp] = keys;
   }
-  int any_bad = __syncthreads_or(bad) ? kBadSequence : 0;
-  if (any_bad && __syncthreads_or(bad & kBadOffsets)) any_bad |= kBadOffsets;
+  const bool any_bad = __syncthreads_or(bad);
   int64_t before = incl - per * a.cache.h_kv, total = 0;
   keys = 0;
 #pragma unroll
@@ -171,7 +167,6 @@ __device__ void paged_share(const PagedArgs& a, const PagedSequence& mine, Paged
     __syncthreads();
     for (int v = 0; v < kW; ++v) total += sums[v];
   }
-  if (any_bad & kBadOffsets) total = 0;
   // turns of the CTAs: a stretch of the line reads about kTurnBytes of keys and
   // values, and a share is long enough to outweigh its two cut items
   int turns = 1;
@@ -398,9 +393,13 @@ struct PageCopies {
   __device__ __forceinline__ int group(int j) const { return (j * kPagedTile + row0) % a.cache.page_size / 8; }
 };
 
-// The outputs of the sequences that are out of bounds (`bad`: PagedShares), where
-// their rows are within the array: zeros.  All threads of the grid share them.
-__device__ __forceinline__ void paged_zero_bad(const PagedArgs& a, int bad) {
+// A block's way where some sequence is out of bounds: the outputs of those, where
+// their rows are within the array, are zeros, all threads of the grid sharing them.
+// Where the offsets fall somewhere the rows of two sequences could be the same: no
+// sequence is taken then, and all rows are zeros.  A call, since its registers would
+// be the kernels' (8192 of 8192 tokens: 716 us, 744 with it in line).
+template <int kTurns>
+__device__ __noinline__ void paged_out_of_bounds(const PagedArgs& a, PagedShares<kTurns>* shares) {
   const da_paged_cache& c = a.cache;
   const int per = a.h * c.d / 8;
   auto zero = [&](int64_t row, int64_t rows, int64_t first, int64_t step) {
@@ -411,15 +410,17 @@ __device__ __forceinline__ void paged_zero_bad(const PagedArgs& a, int bad) {
       *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
     }
   };
-  if (bad & kBadOffsets) {
-    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
+  if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
+  bool falls = false;
+  for (int b = threadIdx.x; b < c.B; b += blockDim.x) falls |= c.cu_seqlens[b + 1] < c.cu_seqlens[b];
+  if (__syncthreads_or(falls)) {
+    for (int k = threadIdx.x; k < kTurns; k += blockDim.x) shares->share[k].units = 0;
     zero(0, c.T, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, static_cast<int64_t>(gridDim.x) * blockDim.x);
     return;
   }
   for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
     const int t0 = c.cu_seqlens[b], t1 = c.cu_seqlens[b + 1];
     if (paged_sequence_ok(c, t0, t1, c.seqlens[b])) continue;
-    if (threadIdx.x == 0) record_status(a.status, DA_ERR_BOUNDS, 0x0F01);
     const int64_t lo = max(t0, 0);  // (in 64 bits: t1 may be any number)
     zero(lo, min(t1, c.T) - lo, threadIdx.x, blockDim.x);
   }

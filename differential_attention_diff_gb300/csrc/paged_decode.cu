@@ -181,7 +181,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     prefetch_tmap(&tm_v);
   }
   paged_share<F::kThreads>(a, mine, &share);
-  if (share.bad) paged_zero_bad(a, share.bad);
+  if (share.bad) paged_out_of_bounds(a, &share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -135,7 +135,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     prefetch_tmap(&tm_v);
   }
   paged_share<kThreads>(a, mine, &share);
-  if (share.bad) paged_zero_bad(a, share.bad);
+  if (share.bad) paged_out_of_bounds(a, &share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
