@@ -38,6 +38,11 @@ constexpr int kPagedTile = 128;  // keys
 // up to 500, d 128, 4 tokens: 115, 104, 102 us with 1, 2, 3; up to 1000, 128 of
 // them, d 64: 62, 60, 62 with 2, 3, 4, single tokens 51, 45, 47 with 1, 3, 4).
 constexpr int kItem = 3;
+// A row's maximum is taken on a part's first tile and raised where a later tile's
+// weights pass 2^kRaise: so 2^30 keys' sum to 2^54 at most, and values of up to 2^73
+// stay within fp32 (2^64, as in the V2 forward, would leave 2^33).
+constexpr int kRaise = 24;
+constexpr float kPagedSumGuard = 1 << kRaise;
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns
 enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags

@@ -13,7 +13,7 @@
 //   bounds the kernel (bf16 alone: 0.0026 of the output's norm off, with lo 0.0017,
 //   the output's own rounding, 64 sequences of 32768).
 //   The first tile of a part gives each column's maximum m; later tiles only
-//   check that no weight passes 2^64, and the rare one that does raises m.
+//   check that no weight passes 2^24, and the rare one that does raises m.
 //   Every tile's product starts from zero and is added in fp32.
 //
 //   a warpgroup or, for C = 32, two with half of the columns each: softmax, sums,
@@ -387,7 +387,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         } else {
           bool over = false;
 #pragma unroll
-          for (int n = 0; n < kC; ++n) over |= n < cols && !(p[n] - m[n] <= 64.f);
+          for (int n = 0; n < kC; ++n) over |= n < cols && !(p[n] - m[n] <= static_cast<float>(kRaise));
           if (any_128(id, over)) {
             float mx[kC];
             tile_max(mx);

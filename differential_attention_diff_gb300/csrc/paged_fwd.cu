@@ -354,7 +354,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           l_half[s] = exps(m_run[s]);
         } else {
           float lsum = exps(m_run[s]);
-          if (named_red_or_256(valid && !(lsum <= kSumGuard))) {
+          if (named_red_or_256(valid && !(lsum <= kPagedSumGuard))) {
             // O is at rest: the commit that signalled these scores covers the turn's last product
             const float m_new = fmaxf(m_run[s], tile_max());
             const float alpha = fast_exp2(m_run[s] - m_new);
