@@ -45,7 +45,7 @@ constexpr int kRaise = 24;
 constexpr float kPagedSumGuard = 1 << kRaise;
 constexpr int64_t kTurnBytes = 48 << 20;  // of keys and values that one turn of the CTAs reads
 constexpr int kTurnTiles = 128;           // of a share, where there are several turns
-enum { kPagedOpen = 1, kPagedRest = 2, kPagedEnds = 4 };  // PagedDesc::flags
+enum { kPagedOpen = 1, kPagedEnds = 2 };  // PagedDesc::flags
 
 __device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t0, int t1, int L) {
   return t0 >= 0 && t0 <= t1 && t1 <= c.T && L >= t1 - t0 && L <= static_cast<int64_t>(c.max_pages) * c.page_size;

@@ -489,7 +489,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll
         for (int n = 0; n < kC; ++n)
           if (n < cols && r < D) a.part_o[(part + n0 + n) * D + r] = o[n];
-        if (!w.begins()) flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
+        if (!w.begins() && w.ends()) flags |= kPagedEnds;
         if (w.begins()) desc = PagedDesc{kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       }
     }

@@ -484,7 +484,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (!whole && valid && wg == 0)
           *reinterpret_cast<float2*>(a.part_ml + (part + s * 128 + row) * 2) = make_float2(m, l);
       }
-      if (!w.begins()) desc.flags |= kPagedRest | (w.ends() ? kPagedEnds : 0);
+      if (!w.begins() && w.ends()) desc.flags |= kPagedEnds;
       if (w.begins() && !w.ends()) desc = PagedDesc{desc.flags | kPagedOpen, w.t0 + w.i * a.tq, w.tokens, w.g};
       tc_fence_before();
     }
