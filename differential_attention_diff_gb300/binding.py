@@ -1089,7 +1089,7 @@ def diffattn_v2_paged_fwd(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
                           w_lambda=None, out=None, softmax_scale=0.0, workspace=None, stream=None):
     """V2 attention of new tokens q [T, 2h, d] over a paged cache (see diffattn_paged_append) that holds their keys:
     out [T, h, d] (None: a new tensor, whose rows without a sequence are zeros).  max_new: the most new tokens that
-    a sequence is expected to have (0 = T); the kernel is chosen by it."""
+    a sequence is expected to have (0 = T); the kernel is chosen by it: say 1 for a batch of decode steps."""
     dev, raw = _device(q, stream)
     T, H2, d = q.shape
     h, bf16 = H2 // 2, torch.bfloat16

@@ -51,7 +51,10 @@ __device__ __forceinline__ bool paged_sequence_ok(const da_paged_cache& c, int t
   return t0 >= 0 && t0 <= t1 && t1 <= c.T && L >= t1 - t0 && L <= static_cast<int64_t>(c.max_pages) * c.page_size;
 }
 
-// sum over i < n of floor((a i + b) / m), by the steps of Euclid's algorithm
+// sum over i < n of floor((a i + b) / m): the points of a lattice below a line.
+// Whole parts of a / m and b / m are summed directly; what is left is counted along
+// the other axis, which turns (a, m) into (m, a mod m), as in Euclid's algorithm
+// (Graham, Knuth and Patashnik, Concrete Mathematics, 3.5: sums of floors).
 __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t s = 0;
   while (n > 0) {

@@ -30,8 +30,8 @@
 // products again, which are what bounds the kernel: a tile pair (256 rows x 128
 // keys, d 128) takes 1.55 us where cuBLAS's rate is 1.32, and an item about 4 us
 // beside its tiles.  64 query and 8 KV heads, d 128: 2048 tokens of 32768 in 1307 us
-// (1.63 PFLOP/s, 0.84 of measured), 8192 of 8192 in 716 us (1.54), 2048 of 8192 in
-// 324 us (1.49), the joining of parts among them; tensor pipe 65 % active.
+// (1.63 PFLOP/s, 0.84 of measured), 8192 of 8192 in 722 us (1.52), 2048 of 8192 in
+// 325 us (1.48), the joining of parts among them; tensor pipe 65 % active.
 //
 // A tile that reaches past the sequence's end holds what the page holds there:
 // the scores are masked, and the values' rows are zeroed in shared memory before

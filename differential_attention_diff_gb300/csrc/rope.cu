@@ -34,11 +34,23 @@ constexpr int kThreads = kWarps * 32;
 
 constexpr int kUnroll = 2;      // passes (of 32 / lanes rows) that are a group
 constexpr int kStagesFwd = 4, kStagesBwd = 3;
-// The passes of a share of work, 1 KB of rows each, where there is plenty.  More
-// spread what the GPU reads at a time, fewer compute more angles: 2 x 8192 tokens of
-// 64 + 8 heads take forward 106, 100, 111, 113 us with 4, 6, 8, 16 (99, 110, 111,
-// 109 without the norm; in fp32, half as many, 94, 113, 109, 107), backward 156,
-// 150, 153, 168 (103, 99, 112, 112).
+// The passes of a share of work, 1 KB of rows each, where there is plenty.  Fewer
+// compute more angles, more spread what the GPU reads at a time; beyond that times
+// go up and down with the shape, and no number is best for all.  Forward, us, for 3,
+// 4, 5, 6, 8 (norm unless said otherwise, bf16, all of the head rotated):
+//   2 x 8192 tokens, 64 + 8 heads, d 128     123, 105, 117, 100, 111
+//   the same without norm                    113,  98, 106, 110, 111
+//   the same, half of the head rotated       121, 106, 115,  97, 108
+//   the same in fp32, 2 x 4096               109,  94, 106, 112, 109
+//   4 x 4096, 32 + 8                          70,  64,  66,  69,  63
+//   1 x 16384, 40 + 10, interleaved           97,  80,  76,  76,  83
+//   4 x 8192, 24 + 2                         102, 106, 115,  88,  88
+//   8 x 2048, 16 + 16, d 64                   33,  33,  33,  33,  33
+//   six prompts appended, 64 + 8 and values  142, 119, 133, 111, 124
+//   the same without norm                    131, 111, 121, 125, 128
+// 4 and 6 have the lowest sums, 1 % apart, and each is up to 20 % behind the other
+// somewhere; the backward of the first takes 156, 150, 153, 168 with 4, 6, 8, 16 (103, 99, 112, 112
+// without norm).
 constexpr int kSharePasses = 4, kSharePassesBwd = 6;
 
 // 2^64 inv_freq / 2 pi modulo 2^64, to an even number, for frequencies below 2^32;
@@ -57,7 +69,7 @@ __device__ __forceinline__ uint64_t turns(float inv_freq) {
 
 // Sine and cosine of t / 2^64 turns, times scale.  What is left of the nearest
 // quarter, at most an eighth of a turn, is taken to 2^-34 of a turn; Taylor's
-// series up to x^9 and x^10 are off by 2^-29 and 2^-34 there.
+// series up to x^9 and x^10 are off by 2^-29 and 2^-33 there.
 __device__ __forceinline__ void sincos_turns(uint64_t t, float scale, float& s, float& c) {
   const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
   const int rest = static_cast<int>(static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62)) >> 30);  // 2^-34 turns
@@ -325,8 +337,9 @@ struct Way {
 // A token's place: its rotation's position and where its rows go, as far as they
 // are loaded and not looked at (a share ahead of their use).
 struct Place {
-  int pos, page, j;  // paged: the entry of the block table and the position; page_ok's and page's
-  bool ok;
+  int pos;      // the rotation's
+  int page, j;  // paged: the entry of the block table (keys and values), the position in the sequence
+  bool ok;      // the rows are written
 };
 template <bool kPaged>
 __device__ __forceinline__ Place place_of(const RopeArgs& a, int which, int t, int lane) {

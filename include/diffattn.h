@@ -635,8 +635,9 @@ da_status diffattn_kv_evict(const da_kv_evict_params* p, void* cuda_stream);
  *   y_v = rope_scale (z_v cos a_i + z_u sin a_i)
  * with (u, v) = (i, i + rot_dim / 2), or (2i, 2i + 1) where `interleaved`; the
  * features from rot_dim on are y = z.  Everything is computed in fp32 (the sum
- * of x_k^2 too: it has to stay within its range) and rounded once.  Stretched contexts are other frequencies and another scale:
- * diffattn_rope_inv_freq makes both. */
+ * of x_k^2 too: it has to stay within its range) and rounded once.  Stretched
+ * contexts are other frequencies and another scale: diffattn_rope_inv_freq makes
+ * both. */
 
 /* A packed [T, H, D] tensor: element (t, h, x) lives at ptr + t*st + h*sh + x
  * (in elements). */
@@ -769,7 +770,12 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* cuda_stre
  * may mix both.  q: bf16 [T, 2h, d]; gate: fp32 [T, h] contiguous, or x bf16
  * [T, d_model] and w_lambda bf16 [d_model, h] contiguous; out: bf16 [T, h, d].
  * max_new: the most new tokens that a sequence may be expected to have (0 = T):
- * the kernel is chosen by it, the result is right whatever it says.
+ * the kernel is chosen by it, for the whole call.  The result is right whatever
+ * it says, but not bit for bit the same: with max_new * 2h / h_kv up to 32 the
+ * softmax weights have 16 bits in their product with the values, and outputs are
+ * 0.0017 of their norm off (their own rounding); with more they are bf16, as in
+ * diffattn_v2_fwd, and outputs are 0.0023 to 0.0026 off, those of single tokens
+ * in the same call too.  So a batch of decode steps should say max_new = 1.
  * The rows of a sequence that is out of bounds are zeros (where the rows are
  * within 0 .. T); where the offsets fall anywhere no row has a certain sequence,
  * and all T rows are zeros.  Keys and values of a page that is out of bounds are
@@ -785,8 +791,10 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* cuda_stre
  * most 2^20, T * 2h and B * max_pages at most 2^31 - 1, h_kv at most 65535,
  * max_pages * page_size at most 2^30.
  * workspace: diffattn_v2_paged_fwd_workspace_size bytes, 256-byte aligned,
- * contents on entry irrelevant; calls that run at the same time need workspaces
- * of their own.  Results are bitwise reproducible from call to call. */
+ * contents on entry irrelevant (40 MB for chunks at d = 128, 160 MB where T is
+ * large enough for parts of several turns, whether the cache then needs them or
+ * not); calls that run at the same time need workspaces of their own.  Results
+ * are bitwise reproducible from call to call. */
 typedef struct {
   da_paged_cache cache;
   int h, d_model, max_new;
