@@ -783,8 +783,8 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* cuda_stre
  * whatever it holds; a value row that holds an infinity or a NaN may reach
  * tokens of its own chunk that come up to 255 positions before it.
  * Values of up to 2^73 (9.4e21) in magnitude give finite sums, whatever their
- * number and the scores; the products q k are summed in fp32 and have to stay
- * within its range.
+ * number and the scores; the products q k are summed in fp32, and they and the
+ * scores have to stay within its range.
  * Supported: d = 64 or 128; 2h / h_kv even, at most 128; page_size a multiple of
  * 16; strides of dimensions longer than 1 above 0, the heads' in the pages
  * multiples of 64; d_model % 64 == 0 and h <= 64 where the gate is computed.  B at
