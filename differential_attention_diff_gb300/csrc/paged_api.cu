@@ -83,7 +83,8 @@ da_status diffattn_v2_paged_fwd(const da_v2_paged_fwd_params* p, void* stream) {
   if (G % 2) return DA_ERR_INVALID_ARG;  // a pair must sit in one K/V group
   // a CTA passes over empty sequences one at a time while others of its warps wait
   // for the next tile: 2^20 of them stay well within those waits' limit
-  if (G > 128 || c.B > (1 << 20) || c.page_size % 16 || c.h_kv > 65535 || static_cast<int64_t>(c.T) * 2 * p->h > (int64_t(1) << 31) - 1)
+  if (c.B > (1 << 20)) return DA_ERR_UNSUPPORTED;
+  if (G > 128 || c.page_size % 16 || c.h_kv > 65535 || static_cast<int64_t>(c.T) * 2 * p->h > (int64_t(1) << 31) - 1)
     return DA_ERR_UNSUPPORTED;
   if (c.T == 0 || c.B == 0) return DA_OK;
   if (c.n_pages == 0 || c.max_pages == 0 || !da::paged_cache_given(c)) return DA_ERR_INVALID_ARG;

@@ -49,8 +49,8 @@ constexpr int kStagesFwd = 4, kStagesBwd = 3;
 //   six prompts appended, 64 + 8 and values  142, 119, 133, 111, 124
 //   the same without norm                    131, 111, 121, 125, 128
 // 4 and 6 have the lowest sums, 1 % apart, and each is up to 20 % behind the other
-// somewhere; the backward of the first takes 156, 150, 153, 168 with 4, 6, 8, 16 (103, 99, 112, 112
-// without norm).
+// somewhere.  The backward of the first takes 156, 150, 153, 168 with 4, 6, 8, 16
+// (103, 99, 112, 112 without norm).
 constexpr int kSharePasses = 4, kSharePassesBwd = 6;
 
 // 2^64 inv_freq / 2 pi modulo 2^64, to an even number, for frequencies below 2^32;
@@ -63,7 +63,8 @@ __device__ __forceinline__ uint64_t turns(float inv_freq) {
   const double hi = f * kHi;
   const double lo = fma(f, kHi, -hi) + f * kLo;
   const double frac = hi - floor(hi);
-  const uint64_t t = __double2ull_rn(frac * 18446744073709551616.0) + static_cast<uint64_t>(__double2ll_rn(lo * 18446744073709551616.0));
+  constexpr double k64 = 18446744073709551616.0;  // 2^64
+  const uint64_t t = __double2ull_rn(frac * k64) + static_cast<uint64_t>(__double2ll_rn(lo * k64));
   return fabsf(inv_freq) < 4294967296.0f ? t & ~1ull : 1;
 }
 
@@ -247,8 +248,8 @@ __device__ __forceinline__ void token_angles(const RopeArgs& a, const uint64_t* 
   __syncwarp();
   for (int i = lane; i < a.rot / 2; i += 32) {
     float s, c;
-    const uint64_t f = freq[i];
-    sincos_turns(static_cast<uint64_t>(static_cast<int64_t>(pos)) * f, f & 1 ? __int_as_float(0x7fffffff) : a.rope_scale, s, c);
+    const uint64_t f = freq[i], t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * f;
+    sincos_turns(t, f & 1 ? __int_as_float(0x7fffffff) : a.rope_scale, s, c);
     cs[i] = c;
     cs[stride + i] = s;
   }

@@ -745,7 +745,8 @@ typedef struct {
  * tokens' positions in their sequences).  d = 64 or 128, T at most 2^29.  Of a
  * sequence that is out of bounds nothing is written; of a token whose page is,
  * the queries are.  A token's sequence is looked for among rising offsets: where
- * they fall, tokens may be taken for none's.  Two tokens may not go to the same slot. */
+ * they fall, tokens may be taken for none's.  Two tokens may not go to the same
+ * slot. */
 typedef struct {
   da_paged_cache cache;
   int h_q;
@@ -779,9 +780,9 @@ da_status diffattn_paged_append(const da_paged_append_params* p, void* cuda_stre
  * The rows of a sequence that is out of bounds are zeros (where the rows are
  * within 0 .. T); where the offsets fall anywhere no row has a certain sequence,
  * and all T rows are zeros.  Keys and values of a page that is out of bounds are
- * read as zeros.  What lies behind a sequence's end in its last page is not looked at,
- * whatever it holds; a value row that holds an infinity or a NaN may reach
- * tokens of its own chunk that come up to 255 positions before it.
+ * read as zeros.  What lies behind a sequence's end in its last page is not
+ * looked at, whatever it holds; a value row that holds an infinity or a NaN may
+ * reach tokens of its own chunk that come up to 255 positions before it.
  * Values of up to 2^73 (9.4e21) in magnitude give finite sums, whatever their
  * number and the scores; the products q k are summed in fp32, and they and the
  * scores have to stay within its range.
